@@ -210,7 +210,7 @@ def prepare(c, seed):
                 o[k] = torch.empty(cap, dtype=torch.int32, device=DEV)
             o["mask"] = torch.empty(cap, dtype=torch.int64, device=DEV) if c["tree"] else None
             s["plan"] = lib.make_tree_tables(s["ctx"], s["new"], s["page_table"], s["free"], s["free_count"], parent=s["parent"], P=P, **o)
-            s["ws"] = lib.alloc_state(lib.tree_tables_workspace_size())
+            s["ws"] = lib.alloc_state(lib.tree_tables_state_size())
         return s
 
     s["row_start"] = _i32(start)
@@ -239,7 +239,7 @@ def prepare(c, seed):
             s["plan"] = lib.make_tree_problem(s["q"], s["cache"], s["page_table"], s["ctx"], s["row_start"], s["mask"], s["max_ctx"], s["max_new"], c["D"] ** -0.5)
             s["out"] = torch.empty(R, c["Hq"], c["D"], dtype=torch.bfloat16, device=DEV)
             s["lse"] = torch.empty(R, c["Hq"], dtype=torch.float32, device=DEV)
-            s["ws"] = lib.alloc_state(lib.tree_workspace_size(s["plan"], c.get("K", 0)))
+            s["ws"] = lib.alloc_state(lib.tree_state_size(s["plan"], c.get("K", 0)))
     return s
 
 
