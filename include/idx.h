@@ -285,6 +285,147 @@ idx_status idx_top1(const float *logits, int64_t ld, int32_t R, int64_t V, int32
 idx_status idx_topk_noalloc(const float *scores, int64_t ld, const int32_t *row_bound, int32_t R,
                             int32_t max_bound, int32_t K, int32_t *out_idx, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The tree-verify decode step around the indexer: page tables and slot maps for a
+ * step's new tokens (idx_tree_tables), their keys and values into the paged cache
+ * (idx_write_kv), and the attention of each request's drafted tokens over that
+ * cache, whole (idx_tree_attention) or at the positions that idx_launch selected
+ * (idx_tree_attention_selected).
+ *
+ * A step gives request i new_len[i] tokens at logical positions ctx_len[i] ..
+ * ctx_len[i] + new_len[i] - 1 of its pages; they are the rows row_start[i] ..
+ * row_start[i + 1] - 1 of every per-row array.  In a tree of drafted tokens, token
+ * t stands at the storage position ctx_len[i] + t whatever its depth.
+ *
+ * The state buffer of these calls is device memory, 1024-byte aligned, all zero
+ * before its first use.  Its first word is a status word that errors found on the
+ * device are or-ed into; idx_last_device_status reads and clears it.  Calls that
+ * overlap in time need a state each. */
+#define IDX_MAX_REQS 4096     /* requests of a step */
+#define IDX_MAX_TREE 64       /* drafted tokens of one request (bits of a mask) */
+
+/* Page tables, slot maps and tree masks of a step, from request lengths.
+ * Request i holds ceil(ctx_len[i] / 64) pages already and gets the pages that its
+ * new tokens need, in request order, from the top of the free stack:
+ * free_pages[free_count - 1], free_pages[free_count - 2], ...  A prompt is a
+ * request with ctx_len 0. */
+typedef struct {
+    const int32_t *ctx_len;    /* device int32 [Q]: tokens each request has cached (< 0 reads as 0) */
+    const int32_t *new_len;    /* device int32 [Q]: new tokens of each request (< 0 reads as 0) */
+    const int32_t *parent;     /* device int32 [cap] or NULL (a chain): the parent of row r as a token number
+                                  of its request, below the row's own number; -1 for a root */
+    const int32_t *free_pages; /* device int32 [free_count]: page ids in [0, P) */
+    const int32_t *free_count; /* device int32 [1] */
+    int32_t *page_table;       /* device int32 [Q][pt_stride]: held pages are read, new entries written */
+    int32_t *row_start;        /* out, device int32 [Q + 1]: exclusive prefix sums of new_len, at most cap */
+    int32_t *free_left;        /* out, device int32 [1]: pages left on the free stack (not free_count itself) */
+    int32_t *row_req;          /* out, device int32 [cap]: the row's request */
+    int32_t *row_bound;        /* out, device int32 [cap]: its storage position + 1 (idx_patch_new_keys's bound) */
+    int32_t *row_pos;          /* out, device int32 [cap]: ctx_len + depth in the tree (the rotary position) */
+    int32_t *slot;             /* out, device int32 [cap]: page * 64 + position % 64, or -1 without a page */
+    uint64_t *mask;            /* out, device [cap] or NULL: bit u set iff token u is the row's token or one of
+                                  its ancestors */
+    int64_t P;                 /* pages of the cache, 1 .. INT32_MAX / 64 */
+    int32_t Q;                 /* requests, 1 .. IDX_MAX_REQS */
+    int32_t pt_stride;         /* page-table row length, >= 1 */
+    int32_t cap;               /* rows that the per-row arrays hold, >= 0 (0: only tables and row_start) */
+} idx_tree_tables_args;
+
+/* Bytes of state that idx_tree_tables needs. */
+size_t idx_tree_tables_state_size(void);
+
+/* One launch.  Rows from row_start[Q] to cap - 1 are padding: request 0, bound 0,
+ * position 0, slot -1, mask 0.  Found on the device and recorded as IDX_EDEVICE:
+ * fewer free pages than needed or a table row too short (the rows without a page
+ * get slot -1, their table entries -1), more new tokens than cap (the rest have no
+ * row), a page id outside [0, P) (slot -1), a parent that is not an earlier token
+ * (read as a root), a request of more than IDX_MAX_TREE new tokens with parents or
+ * masks asked for (those past the 64th: mask 0, depth counted as in a chain).  IDX_EINVAL for a NULL or bad
+ * argument, IDX_EUNSUPPORTED for Q or P above the limits; launches nothing then. */
+idx_status idx_tree_tables(const idx_tree_tables_args *args, void *state, size_t state_bytes, void *stream);
+
+/* A paged key/value cache.  Element (page p, token s, head h, dim d) of K and of V
+ * is at p * page_stride + s * token_stride + h * head_stride + d elements: any order
+ * of tokens and heads, and K and V interleaved in one allocation. */
+typedef struct {
+    void *k, *v;               /* device, E4M3 bytes or bf16, 16-byte aligned */
+    float *k_scale, *v_scale;  /* device fp32 [P][Hkv][64] for E4M3, 16-byte aligned; NULL for bf16 */
+    int64_t P;                 /* pages, 1 .. INT32_MAX / 64 */
+    int64_t page_stride, token_stride, head_stride;  /* elements; multiples of 16 bytes, positive */
+    int32_t Hkv;               /* key/value heads, 1 .. 1024 */
+    int32_t D;                 /* dimensions per head: 64 or 128 */
+    int32_t kv_dtype;          /* idx_kv_dtype */
+} idx_kv_cache;
+
+/* Writes R tokens' keys and values into the cache.
+ *   k_new, v_new  device bf16: row r's head h at r * row_stride + h * D elements, 16-byte
+ *                 aligned, row_stride >= Hkv * D and a multiple of 8 (a slice of a fused
+ *                 projection's output fits).
+ *   slot          device int32 [R]: page * 64 + token (idx_tree_tables writes it); a
+ *                 slot outside [0, P * 64) writes nothing.  Slots >= 0 must differ.
+ * bf16 cache: the values as given.  E4M3 cache: per token and head scale = amax / 448
+ * in fp32 (1 for an all-zero vector), each value divided by it in fp32 and rounded to
+ * the nearest E4M3 code (ties to even), saturating at +-448.  R = 0 does nothing.
+ * Asynchronous on `stream`; allocates nothing. */
+idx_status idx_write_kv(const idx_kv_cache *cache, const void *k_new, const void *v_new, int64_t row_stride,
+                        const int32_t *slot, int64_t R, void *stream);
+
+/* The drafted tokens of Q requests and the cache they attend to. */
+typedef struct {
+    const void *q;             /* device bf16: row r's head h at r * q_row_stride + h * D elements, 16-byte aligned */
+    int64_t q_row_stride;      /* elements, >= Hq * D, a multiple of 8 */
+    idx_kv_cache cache;        /* read only here */
+    const int32_t *page_table; /* device int32 [Q][pt_stride] */
+    const int32_t *ctx_len;    /* device int32 [Q] */
+    const int32_t *row_start;  /* device int32 [Q + 1]: ascending, within 0 .. R */
+    const uint64_t *mask;      /* device [R]: bit u set iff the row sees its request's drafted token u;
+                                  NULL: a chain (token t sees 0 .. t) */
+    int32_t R;                 /* rows that q and the outputs hold, 1 .. IDX_MAX_ROWS */
+    int32_t Q;                 /* requests, 1 .. IDX_MAX_REQS */
+    int32_t pt_stride;
+    int32_t max_ctx;           /* host upper bound on every ctx_len, 0 .. pt_stride * 64 */
+    int32_t max_new;           /* host upper bound on every request's rows, 1 .. IDX_MAX_TREE */
+    int32_t Hq;                /* query heads, a multiple of cache.Hkv; head h reads key/value head h / (Hq / Hkv) */
+    float scale;               /* of the scores, finite */
+} idx_tree_problem;
+
+/* Bytes of state for the attention calls on this problem; sel_k: 0 for
+ * idx_tree_attention, the selection's K for idx_tree_attention_selected.  0 if the
+ * problem is invalid. */
+size_t idx_tree_state_size(const idx_tree_problem *problem, int32_t sel_k);
+
+/* Attention of every drafted token over its request's cached tokens and the drafted
+ * tokens that its mask shows (their K and V already in the cache, see idx_write_kv).
+ * For row r of request i and head h, with k_j and v_j the cache's values (code times
+ * scale) at logical position j,
+ *     V(r)  = { j < ctx_len[i] } + { ctx_len[i] + u : u < rows of i, bit u of mask[r] }
+ *     s_j   = scale * <q[r][h], k_j>
+ *     out   = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)   over j in V(r);
+ * a row that sees nothing gets zeros and lse -inf.  Masked positions contribute
+ * nothing, whatever the cache holds there (NaN and infinities included).
+ *   out  device bf16 [R][Hq][D], 16-byte aligned.
+ *   lse  device fp32 [R][Hq] or NULL.
+ * Rows outside every request are not written.  Sums and softmax statistics are fp32;
+ * the probabilities are rounded to bf16 for the product with V.  The result does not
+ * depend on how the work was split in a way that changes between equal calls.
+ * Device-detected (IDX_EDEVICE): a page id outside [0, P) (its tokens are left out),
+ * ctx_len outside 0 .. max_ctx, more rows than max_new or positions past the page
+ * table (clamped), row_start outside 0 .. R.  IDX_ETIMEOUT: a wait ran out.
+ * Asynchronous on `stream`; allocates nothing. */
+idx_status idx_tree_attention(const idx_tree_problem *problem, void *out, float *lse, void *state,
+                              size_t state_bytes, void *stream);
+
+/* The same over selected positions: V(r) = { sel[r][n] : 0 <= sel[r][n] < ctx_len[i] } +
+ * { ctx_len[i] + u : bit u of mask[r] }.
+ *   sel    device int32 [R][sel_k]: idx_launch's out_idx on rows bounded by ctx_len (any
+ *          order; entries outside 0 .. ctx_len - 1, such as its -1 padding, are skipped).
+ *          A row's entries must differ.
+ *   sel_k  1 .. IDX_MAX_K.
+ * Hq / Hkv at most 128.  Other arguments, outputs and errors as for
+ * idx_tree_attention. */
+idx_status idx_tree_attention_selected(const idx_tree_problem *problem, const int32_t *sel, int32_t sel_k, void *out,
+                                       float *lse, void *state, size_t state_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,6 +10,9 @@ not been built, importing this package raises; there is no other code path.
     idx_launch_host  idx_launch on host inputs, copies included
     idx_launch_scored, idx_merge_topk  the key-sharded indexer (shard.py splits
                      a problem and exchanges the shards' lists)
+    idx_tree_tables, idx_write_kv, idx_tree_attention,
+    idx_tree_attention_selected  the tree-verify step around the indexer: page
+                     tables and slots, K/V writes, attention over the paged cache
 """
 from __future__ import annotations
 
@@ -22,12 +25,15 @@ LIB_PATH = os.path.join(_HERE, "_build", "libidx.so")
 IDX_OK, IDX_EINVAL, IDX_EUNSUPPORTED, IDX_ECUDA, IDX_ETIMEOUT, IDX_EDEVICE = range(6)
 IDX_KV_E4M3, IDX_KV_BF16 = 0, 1
 IDX_HEADS, IDX_DIM, IDX_PAGE, IDX_MAX_K = 64, 128, 64, 2048
+IDX_MAX_REQS, IDX_MAX_TREE = 4096, 64
 IDX_DEBUG_WAIT_LIMIT_NS, IDX_DEBUG_STALL_SCORE_MMA = 1, 2
 
 EXPORTS = ["idx_workspace_size", "idx_score", "idx_topk", "idx_launch", "idx_host_arena_size",
            "idx_launch_host", "idx_last_device_status", "idx_status_string", "idx_version",
            "idx_debug_set", "idx_profile_events", "idx_top1_state_size", "idx_top1", "idx_topk_noalloc",
-           "idx_patch_new_keys", "idx_launch_scored", "idx_merge_topk", "idx_launch_new_keys"]
+           "idx_patch_new_keys", "idx_launch_scored", "idx_merge_topk", "idx_launch_new_keys",
+           "idx_tree_tables_state_size", "idx_tree_tables", "idx_write_kv", "idx_tree_state_size",
+           "idx_tree_attention", "idx_tree_attention_selected"]
 
 
 class IdxError(RuntimeError):
@@ -44,6 +50,33 @@ class Problem(ctypes.Structure):
         ("row_bound", ctypes.c_void_p), ("R", ctypes.c_int32), ("Q", ctypes.c_int32),
         ("P", ctypes.c_int64), ("pt_stride", ctypes.c_int32), ("max_bound", ctypes.c_int32),
         ("kv_dtype", ctypes.c_int32), ("rows_hint", ctypes.c_int32),
+    ]
+
+
+class TreeTables(ctypes.Structure):
+    """Mirror of idx_tree_tables_args."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "ctx_len", "new_len", "parent", "free_pages", "free_count", "page_table", "row_start", "free_left",
+        "row_req", "row_bound", "row_pos", "slot", "mask")] + [
+        ("P", ctypes.c_int64), ("Q", ctypes.c_int32), ("pt_stride", ctypes.c_int32), ("cap", ctypes.c_int32)]
+
+
+class KvCache(ctypes.Structure):
+    """Mirror of idx_kv_cache."""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("P", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
+    ]
+
+
+class TreeProblem(ctypes.Structure):
+    """Mirror of idx_tree_problem."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_row_stride", ctypes.c_int64), ("cache", KvCache), ("page_table", ctypes.c_void_p),
+        ("ctx_len", ctypes.c_void_p), ("row_start", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("R", ctypes.c_int32),
+        ("Q", ctypes.c_int32), ("pt_stride", ctypes.c_int32), ("max_ctx", ctypes.c_int32), ("max_new", ctypes.c_int32),
+        ("Hq", ctypes.c_int32), ("scale", ctypes.c_float),
     ]
 
 
@@ -90,6 +123,19 @@ def _load():
     lib.idx_merge_topk.restype = ctypes.c_int
     lib.idx_launch_new_keys.argtypes = [P, vp, i32, vp, vp, sz, vp]
     lib.idx_launch_new_keys.restype = ctypes.c_int
+    T, C, A = ctypes.POINTER(TreeTables), ctypes.POINTER(KvCache), ctypes.POINTER(TreeProblem)
+    lib.idx_tree_tables_state_size.argtypes = []
+    lib.idx_tree_tables_state_size.restype = sz
+    lib.idx_tree_tables.argtypes = [T, vp, sz, vp]
+    lib.idx_tree_tables.restype = ctypes.c_int
+    lib.idx_write_kv.argtypes = [C, vp, vp, i64, vp, i64, vp]
+    lib.idx_write_kv.restype = ctypes.c_int
+    lib.idx_tree_state_size.argtypes = [A, i32]
+    lib.idx_tree_state_size.restype = sz
+    lib.idx_tree_attention.argtypes = [A, vp, vp, vp, sz, vp]
+    lib.idx_tree_attention.restype = ctypes.c_int
+    lib.idx_tree_attention_selected.argtypes = [A, vp, i32, vp, vp, vp, sz, vp]
+    lib.idx_tree_attention_selected.restype = ctypes.c_int
     return lib
 
 
@@ -209,6 +255,144 @@ def idx_launch_host(host_problem: Problem, K: int, host_out, arena, stream=None)
            "idx_launch_host")
 
 
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _int32(name, t, numel=None):
+    import torch
+    _need(t.dtype == torch.int32 and t.is_contiguous(), f"{name}: a contiguous int32 tensor is wanted")
+    _need(numel is None or t.numel() >= numel, f"{name}: at least {numel} values are wanted")
+
+
+def make_tree_tables(ctx_len, new_len, page_table, free_pages, free_count, *, P: int, row_start, free_left, row_req,
+                     row_bound, row_pos, slot, mask=None, parent=None) -> TreeTables:
+    """idx_tree_tables_args from device tensors (see idx.h): ctx_len and new_len [Q],
+    page_table [Q][stride] (written), free_pages [F] with free_count [1] of them free,
+    P the cache's pages; outputs row_start [Q + 1], free_left [1], row_req, row_bound,
+    row_pos and slot [cap], mask [cap] int64 or None; parent [cap] or None (chains)."""
+    import torch
+    Q, cap = int(ctx_len.shape[0]), int(slot.shape[0])
+    for name, t, n in (("ctx_len", ctx_len, Q), ("new_len", new_len, Q), ("page_table", page_table, None),
+                       ("free_pages", free_pages, None), ("free_count", free_count, 1), ("row_start", row_start, Q + 1),
+                       ("free_left", free_left, 1), ("row_req", row_req, cap), ("row_bound", row_bound, cap),
+                       ("row_pos", row_pos, cap), ("slot", slot, cap)):
+        _int32(name, t, n)
+    if parent is not None:
+        _int32("parent", parent, cap)
+    _need(page_table.dim() == 2 and page_table.shape[0] == Q, "page_table: [Q][stride] is wanted")
+    _need(mask is None or (mask.dtype == torch.int64 and mask.is_contiguous() and mask.numel() >= cap),
+          "mask: a contiguous int64 tensor of a value per row is wanted")
+    return TreeTables(ctx_len=_ptr(ctx_len), new_len=_ptr(new_len), parent=_ptr(parent), free_pages=_ptr(free_pages),
+                      free_count=_ptr(free_count), page_table=_ptr(page_table), row_start=_ptr(row_start),
+                      free_left=_ptr(free_left), row_req=_ptr(row_req), row_bound=_ptr(row_bound),
+                      row_pos=_ptr(row_pos), slot=_ptr(slot), mask=_ptr(mask), P=int(P), Q=Q,
+                      pt_stride=int(page_table.shape[1]), cap=cap)
+
+
+def tree_tables_state_size() -> int:
+    return int(lib.idx_tree_tables_state_size())
+
+
+def idx_tree_tables(tables: TreeTables, state, stream=None):
+    """Page tables, slots and masks of a step (see idx.h); `state` from
+    alloc_state(tree_tables_state_size())."""
+    _check(lib.idx_tree_tables(ctypes.byref(tables), _ptr(state), state.numel() * state.element_size(),
+                               _stream(stream)), "idx_tree_tables")
+
+
+def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
+    """idx_kv_cache from device tensors: k and v [P][64][Hkv][D] (any strides but a
+    contiguous last dimension, the same for both), bf16, or E4M3 (float8_e4m3fn or
+    uint8) with contiguous fp32 scales [P][Hkv][64]."""
+    import torch
+    P, page, Hkv, D = (int(x) for x in k.shape)
+    _need(page == IDX_PAGE and v.shape == k.shape and v.dtype == k.dtype, "k, v: two [P][64][Hkv][D] tensors are wanted")
+    _need(k.dtype in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8), "k, v: bf16 or E4M3 is wanted")
+    f8 = k.dtype != torch.bfloat16
+    # a dimension of one element is never stepped over: any stride will do
+    st = [[s if n > 1 else page * Hkv * D for n, s in zip(x.shape, x.stride())] for x in (k, v)]
+    _need(st[0] == st[1] and k.stride(3) == 1 and v.stride(3) == 1,
+          "k, v: equal strides and contiguous dimensions are wanted")
+    for s in (k_scale, v_scale):
+        _need((s is not None) == f8, "k_scale, v_scale: wanted for an E4M3 cache only")
+        _need(s is None or (s.dtype == torch.float32 and s.is_contiguous() and tuple(s.shape) == (P, Hkv, page)),
+              "k_scale, v_scale: contiguous fp32 [P][Hkv][64] is wanted")
+    return KvCache(k=_ptr(k), v=_ptr(v), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale), P=P, page_stride=st[0][0],
+                   token_stride=st[0][1], head_stride=st[0][2], Hkv=Hkv, D=D,
+                   kv_dtype=IDX_KV_E4M3 if f8 else IDX_KV_BF16)
+
+
+def idx_write_kv(cache: KvCache, k_new, v_new, slot, stream=None):
+    """Writes k_new and v_new (bf16 [R][Hkv][D], rows of equal stride) into the cache
+    at slot [R] (see idx.h)."""
+    import torch
+    R = int(slot.shape[0])
+    for name, x in (("k_new", k_new), ("v_new", v_new)):
+        _need(x.dtype == torch.bfloat16 and tuple(x.shape) == (R, cache.Hkv, cache.D), f"{name}: bf16 [R][Hkv][D] is wanted")
+        _need(x.stride(2) == 1 and (cache.Hkv == 1 or x.stride(1) == cache.D), f"{name}: contiguous heads are wanted")
+    _int32("slot", slot)
+    stride = k_new.stride(0) if R > 1 else cache.Hkv * cache.D
+    _need(R <= 1 or v_new.stride(0) == stride, "k_new, v_new: equal row strides are wanted")
+    _check(lib.idx_write_kv(ctypes.byref(cache), _ptr(k_new), _ptr(v_new), int(stride), _ptr(slot), R,
+                            _stream(stream)), "idx_write_kv")
+
+
+def make_tree_problem(q, cache: KvCache, page_table, ctx_len, row_start, mask, max_ctx: int, max_new: int,
+                      scale: float) -> TreeProblem:
+    """idx_tree_problem from device tensors: q bf16 [R][Hq][D] (rows of any stride),
+    page_table [Q][stride], ctx_len [Q], row_start [Q + 1], mask [R] int64 or None
+    (chains); max_ctx and max_new bound every request's cached and drafted tokens."""
+    import torch
+    R, Hq, D = (int(x) for x in q.shape)
+    Q = int(ctx_len.shape[0])
+    _need(q.dtype == torch.bfloat16 and D == cache.D and q.stride(2) == 1 and (Hq == 1 or q.stride(1) == D),
+          "q: bf16 [R][Hq][D] with contiguous heads is wanted")
+    for name, t, n in (("page_table", page_table, None), ("ctx_len", ctx_len, Q), ("row_start", row_start, Q + 1)):
+        _int32(name, t, n)
+    _need(page_table.dim() == 2 and page_table.shape[0] == Q, "page_table: [Q][stride] is wanted")
+    _need(mask is None or (mask.dtype == torch.int64 and mask.is_contiguous() and mask.numel() >= R),
+          "mask: a contiguous int64 tensor of a value per row is wanted")
+    return TreeProblem(q=_ptr(q), q_row_stride=int(q.stride(0)) if R > 1 else Hq * D, cache=cache,
+                       page_table=_ptr(page_table), ctx_len=_ptr(ctx_len), row_start=_ptr(row_start), mask=_ptr(mask),
+                       R=R, Q=Q, pt_stride=int(page_table.shape[1]), max_ctx=int(max_ctx), max_new=int(max_new), Hq=Hq,
+                       scale=float(scale))
+
+
+def tree_state_size(problem: TreeProblem, sel_k: int = 0) -> int:
+    return int(lib.idx_tree_state_size(ctypes.byref(problem), int(sel_k)))
+
+
+def _attn_outputs(problem, out, lse):
+    import torch
+    R, Hq, D = problem.R, problem.Hq, problem.cache.D
+    _need(out.dtype == torch.bfloat16 and out.is_contiguous() and tuple(out.shape) == (R, Hq, D),
+          "out: contiguous bf16 [R][Hq][D] is wanted")
+    _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (R, Hq)),
+          "lse: contiguous fp32 [R][Hq] is wanted")
+
+
+def idx_tree_attention(problem: TreeProblem, out, state, lse=None, stream=None):
+    """Attention of the drafted tokens over their requests' caches into out (bf16
+    [R][Hq][D]) and lse (fp32 [R][Hq] or None); `state` from
+    alloc_state(tree_state_size(problem))."""
+    _attn_outputs(problem, out, lse)
+    _check(lib.idx_tree_attention(ctypes.byref(problem), _ptr(out), _ptr(lse), _ptr(state),
+                                  state.numel() * state.element_size(), _stream(stream)), "idx_tree_attention")
+
+
+def idx_tree_attention_selected(problem: TreeProblem, sel, out, state, lse=None, stream=None):
+    """The same over the cached positions sel (int32 [R][K], as idx_launch writes
+    them); `state` from alloc_state(tree_state_size(problem, K))."""
+    _attn_outputs(problem, out, lse)
+    _int32("sel", sel)
+    _need(sel.dim() == 2 and sel.shape[0] == problem.R, "sel: [R][K] is wanted")
+    _check(lib.idx_tree_attention_selected(ctypes.byref(problem), _ptr(sel), int(sel.shape[1]), _ptr(out), _ptr(lse),
+                                           _ptr(state), state.numel() * state.element_size(), _stream(stream)),
+           "idx_tree_attention_selected")
+
+
 def last_device_status(ws, stream=None) -> int:
     return int(lib.idx_last_device_status(_ptr(ws), _stream(stream)))
 
@@ -233,6 +417,14 @@ def alloc_bytes(nbytes: int, device="cuda"):
     raw = torch.empty(int(nbytes) + 1024, dtype=torch.uint8, device=device)
     off = (-raw.data_ptr()) % 1024
     return raw[off:off + int(nbytes)]
+
+
+def alloc_state(nbytes: int, device="cuda"):
+    """alloc_bytes, zeroed: the state of the calls that want one all zero before its
+    first use."""
+    state = alloc_bytes(nbytes, device)
+    state.zero_()
+    return state
 
 
 class DeviceProblem:

@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libidx.so")
-SOURCES = ["api.cu", "prep.cu", "score.cu", "select.cu", "top1.cu", "patch.cu", "merge.cu"]
+SOURCES = ["api.cu", "prep.cu", "score.cu", "select.cu", "top1.cu", "patch.cu", "merge.cu", "tree_api.cu",
+           "tree_tables.cu", "write_kv.cu", "tree_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", INCLUDE, "-I", CSRC]

@@ -111,7 +111,11 @@ idx_status check_problem(const idx_problem *p) {
   return IDX_OK;
 }
 
+}  // namespace
+
 // ---------------------------------------------------------------------------- device info
+namespace idx {
+
 std::atomic<int> g_num_sms[128];   // filled on first use per device (concurrent callers store the same value)
 
 idx_status device_sms(int *out) {
@@ -131,28 +135,41 @@ idx_status device_sms(int *out) {
   return IDX_OK;
 }
 
-// ---------------------------------------------------------------------------- TMA descriptor
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+static std::mutex g_encode_mu;
 
-idx_status key_tensor_map(const idx_problem *p, CUtensorMap *map) {
-  {
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (g_encode == nullptr) {
-      void *fn = nullptr;
-      cudaDriverEntryPointQueryResult q;
-      if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-              cudaSuccess ||
-          q != cudaDriverEntryPointSuccess || fn == nullptr)
-        return IDX_ECUDA;
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    }
+idx_status tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000 *out) {
+  std::lock_guard<std::mutex> lk(g_encode_mu);
+  if (g_encode == nullptr) {
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || fn == nullptr)
+      return IDX_ECUDA;
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
+  *out = g_encode;
+  return IDX_OK;
+}
+
+}  // namespace idx
+
+namespace {
+
+using idx::device_sms;
+
+// ---------------------------------------------------------------------------- TMA descriptor
+idx_status key_tensor_map(const idx_problem *p, CUtensorMap *map) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  const idx_status st = idx::tensor_map_encoder(&encode);
+  if (st != IDX_OK) return st;
   const bool f8 = p->kv_dtype == IDX_KV_E4M3;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(IDX_DIM), static_cast<cuuint64_t>(p->P) * IDX_PAGE};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(f8 ? IDX_DIM : IDX_DIM * 2)};
   cuuint32_t box[2] = {static_cast<cuuint32_t>(f8 ? 128 : 64), static_cast<cuuint32_t>(IDX_PAGE)};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+  CUresult r = encode(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                         const_cast<void *>(p->k_cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <mutex>
@@ -25,6 +26,11 @@ inline cudaError_t once_per_device(std::mutex &mu, bool (&done)[128], F setup) {
   else (void)cudaGetLastError();   // a failed setup must not be reported again by a later launch
   return e;
 }
+
+// SMs of the current device (IDX_EUNSUPPORTED unless it is compute capability 10.3).
+idx_status device_sms(int *out);
+// The driver's tiled tensor-map encoder, looked up once.
+idx_status tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000 *out);
 
 struct PatchArgs {
   const uint16_t *k_new;   // bf16 [R][128]
@@ -105,6 +111,32 @@ struct MergeArgs {
   int32_t *out_idx;          // [R][K]
   float *out_score;          // [R][K] or null
 };
+
+struct TreeTablesArgs {
+  idx_tree_tables_args t;
+  uint32_t *status;
+  int32_t vec4;            // the per-row arrays allow 16-byte stores
+};
+
+struct WriteKvArgs {
+  idx_kv_cache c;
+  const uint16_t *k_new, *v_new;   // bf16
+  int64_t row_stride, R;
+  const int32_t *slot;
+};
+
+struct TreeAttnArgs {
+  idx_tree_problem p;
+  const int32_t *sel;      // [R][sel_k] or null: every cached position
+  int32_t sel_k;
+  uint16_t *out;           // bf16 [R][Hq][D]
+  float *lse;              // [R][Hq] or null
+  uint32_t *status;
+};
+
+cudaError_t launch_tree_tables(const TreeTablesArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_write_kv(const WriteKvArgs &a, cudaStream_t stream);
+cudaError_t launch_tree_attention(const TreeAttnArgs &a, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_prep(const PrepArgs &a, cudaStream_t stream);
 cudaError_t launch_score(const CUtensorMap &kmap, const ScoreArgs &a, int kv_dtype, bool batched, int num_ctas,

@@ -1,0 +1,147 @@
+// The C ABI of the tree-verify step (include/idx.h): argument checks and launches.
+#include <cmath>
+
+#include "idx.h"
+#include "idx_device.cuh"
+#include "launch.h"
+
+namespace {
+
+constexpr size_t kStateAlign = 1024;
+constexpr size_t kStatusBytes = 1024;   // the status word's block at the start of every state
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+idx_status cuda_ok(cudaError_t e) { return e == cudaSuccess ? IDX_OK : IDX_ECUDA; }
+
+bool state_ok(const void *state, size_t bytes, size_t need) {
+  return state != nullptr && aligned(state, kStateAlign) && bytes >= need;
+}
+
+idx_status check_cache(const idx_kv_cache *c) {
+  if (c->k == nullptr || c->v == nullptr || !aligned(c->k, 16) || !aligned(c->v, 16)) return IDX_EINVAL;
+  if (c->P < 1 || c->Hkv < 1) return IDX_EINVAL;
+  if (c->P > INT32_MAX / IDX_PAGE || c->Hkv > 1024) return IDX_EUNSUPPORTED;
+  if (c->D != 64 && c->D != 128) return IDX_EUNSUPPORTED;
+  int64_t bytes;
+  if (c->kv_dtype == IDX_KV_E4M3) {
+    bytes = 1;
+    if (c->k_scale == nullptr || c->v_scale == nullptr || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+      return IDX_EINVAL;
+  } else if (c->kv_dtype == IDX_KV_BF16) {
+    bytes = 2;
+    if (c->k_scale != nullptr || c->v_scale != nullptr) return IDX_EINVAL;
+  } else {
+    return IDX_EINVAL;
+  }
+  for (const int64_t s : {c->page_stride, c->token_stride, c->head_stride}) {
+    if (s < 1 || s % (16 / bytes) != 0) return IDX_EINVAL;
+    if (s >= (int64_t{1} << 40) / bytes) return IDX_EUNSUPPORTED;   // a tensor map's strides have 40 bits
+  }
+  return IDX_OK;
+}
+
+idx_status check_problem(const idx_tree_problem *p, int32_t sel_k) {
+  if (p == nullptr) return IDX_EINVAL;
+  if (p->q == nullptr || !aligned(p->q, 16) || p->page_table == nullptr || p->ctx_len == nullptr ||
+      p->row_start == nullptr)
+    return IDX_EINVAL;
+  const idx_status st = check_cache(&p->cache);
+  if (st != IDX_OK) return st;
+  if (p->R < 1 || p->Q < 1 || p->pt_stride < 1 || p->max_ctx < 0 || p->max_new < 1 || p->Hq < 1) return IDX_EINVAL;
+  if (static_cast<int64_t>(p->max_ctx) > static_cast<int64_t>(p->pt_stride) * IDX_PAGE) return IDX_EINVAL;
+  if (p->Hq % p->cache.Hkv != 0 || !std::isfinite(p->scale)) return IDX_EINVAL;
+  if (p->q_row_stride < static_cast<int64_t>(p->Hq) * p->cache.D || p->q_row_stride % 8 != 0) return IDX_EINVAL;
+  if (p->R > IDX_MAX_ROWS || p->Q > IDX_MAX_REQS || p->max_new > IDX_MAX_TREE || p->Hq > 1024) return IDX_EUNSUPPORTED;
+  if (sel_k < 0 || sel_k > IDX_MAX_K) return IDX_EINVAL;
+  if (sel_k > 0 && p->Hq / p->cache.Hkv > 128) return IDX_EUNSUPPORTED;
+  return IDX_OK;
+}
+
+size_t state_bytes_of(const idx_tree_problem *, int32_t) { return kStatusBytes; }
+
+idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, void *out, float *lse, void *state,
+                  size_t state_bytes, void *stream) {
+  idx_status st = check_problem(p, sel_k);
+  if (st != IDX_OK) return st;
+  if (out == nullptr || !aligned(out, 16) || !state_ok(state, state_bytes, state_bytes_of(p, sel_k))) return IDX_EINVAL;
+  int sms = 0;
+  st = idx::device_sms(&sms);
+  if (st != IDX_OK) return st;
+  idx::TreeAttnArgs a{};
+  a.p = *p;
+  a.sel = sel;
+  a.sel_k = sel_k;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  a.status = static_cast<uint32_t *>(state);
+  return cuda_ok(idx::launch_tree_attention(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t idx_tree_tables_state_size(void) { return kStatusBytes; }
+
+idx_status idx_tree_tables(const idx_tree_tables_args *t, void *state, size_t state_bytes, void *stream) {
+  if (t == nullptr || t->ctx_len == nullptr || t->new_len == nullptr || t->free_pages == nullptr ||
+      t->free_count == nullptr || t->page_table == nullptr || t->row_start == nullptr || t->free_left == nullptr)
+    return IDX_EINVAL;
+  if (t->Q < 1 || t->P < 1 || t->pt_stride < 1 || t->cap < 0) return IDX_EINVAL;
+  if (t->cap > 0 && (t->row_req == nullptr || t->row_bound == nullptr || t->row_pos == nullptr || t->slot == nullptr))
+    return IDX_EINVAL;
+  if (t->free_left == t->free_count || !aligned(t->mask, 8)) return IDX_EINVAL;
+  if (t->Q > IDX_MAX_REQS || t->P > INT32_MAX / IDX_PAGE) return IDX_EUNSUPPORTED;
+  if (!state_ok(state, state_bytes, kStatusBytes)) return IDX_EINVAL;
+  int sms = 0;
+  const idx_status st = idx::device_sms(&sms);
+  if (st != IDX_OK) return st;
+  idx::TreeTablesArgs a{};
+  a.t = *t;
+  a.status = static_cast<uint32_t *>(state);
+  a.vec4 = aligned(t->row_req, 16) && aligned(t->row_bound, 16) && aligned(t->row_pos, 16) && aligned(t->slot, 16) &&
+           aligned(t->mask, 16);
+  return cuda_ok(idx::launch_tree_tables(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+idx_status idx_write_kv(const idx_kv_cache *cache, const void *k_new, const void *v_new, int64_t row_stride,
+                        const int32_t *slot, int64_t R, void *stream) {
+  if (cache == nullptr || R < 0) return IDX_EINVAL;
+  idx_status st = check_cache(cache);
+  if (st != IDX_OK) return st;
+  if (R == 0) return IDX_OK;
+  if (k_new == nullptr || v_new == nullptr || slot == nullptr || !aligned(k_new, 16) || !aligned(v_new, 16))
+    return IDX_EINVAL;
+  if (row_stride < static_cast<int64_t>(cache->Hkv) * cache->D || row_stride % 8 != 0) return IDX_EINVAL;
+  if (R > INT32_MAX) return IDX_EUNSUPPORTED;   // the grid: at least 64 vectors a CTA, at most 2,048 a row
+  int sms = 0;
+  st = idx::device_sms(&sms);   // the device check
+  if (st != IDX_OK) return st;
+  idx::WriteKvArgs a{};
+  a.c = *cache;
+  a.k_new = static_cast<const uint16_t *>(k_new);
+  a.v_new = static_cast<const uint16_t *>(v_new);
+  a.row_stride = row_stride;
+  a.R = R;
+  a.slot = slot;
+  return cuda_ok(idx::launch_write_kv(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t idx_tree_state_size(const idx_tree_problem *problem, int32_t sel_k) {
+  if (check_problem(problem, sel_k) != IDX_OK) return 0;
+  return state_bytes_of(problem, sel_k);
+}
+
+idx_status idx_tree_attention(const idx_tree_problem *problem, void *out, float *lse, void *state, size_t state_bytes,
+                              void *stream) {
+  return attend(problem, nullptr, 0, out, lse, state, state_bytes, stream);
+}
+
+idx_status idx_tree_attention_selected(const idx_tree_problem *problem, const int32_t *sel, int32_t sel_k, void *out,
+                                       float *lse, void *state, size_t state_bytes, void *stream) {
+  if (sel == nullptr || sel_k < 1) return IDX_EINVAL;
+  return attend(problem, sel, sel_k, out, lse, state, state_bytes, stream);
+}
+
+}  // extern "C"
