@@ -385,8 +385,9 @@ typedef struct {
     int32_t pt_stride;
     int32_t max_ctx;           /* host upper bound on every ctx_len, 0 .. pt_stride * 64 */
     int32_t max_new;           /* host upper bound on every request's rows, 1 .. IDX_MAX_TREE */
-    int32_t Hq;                /* query heads, a multiple of cache.Hkv; head h reads key/value head h / (Hq / Hkv) */
-    float scale;               /* of the scores, finite */
+    int32_t Hq;                /* query heads, a multiple of cache.Hkv; head h reads key/value head h / (Hq / Hkv);
+                                  Hq / Hkv at most 128 */
+    float scale;               /* of the scores, finite and >= 0 */
 } idx_tree_problem;
 
 /* Bytes of state for the attention calls on this problem; sel_k: 0 for
@@ -406,7 +407,8 @@ size_t idx_tree_state_size(const idx_tree_problem *problem, int32_t sel_k);
  *   out  device bf16 [R][Hq][D], 16-byte aligned.
  *   lse  device fp32 [R][Hq] or NULL.
  * Rows outside every request are not written.  Sums and softmax statistics are fp32;
- * the probabilities are rounded to bf16 for the product with V.  The result does not
+ * the probabilities are rounded to bf16 for the product with V (to two bf16 terms where
+ * fewer than 128 keys of a 128-key tile are visible to all).  The result does not
  * depend on how the work was split in a way that changes between equal calls.
  * Device-detected (IDX_EDEVICE): a page id outside [0, P) (its tokens are left out),
  * ctx_len outside 0 .. max_ctx, more rows than max_new or positions past the page
@@ -421,8 +423,7 @@ idx_status idx_tree_attention(const idx_tree_problem *problem, void *out, float 
  *          order; entries outside 0 .. ctx_len - 1, such as its -1 padding, are skipped).
  *          A row's entries must differ.
  *   sel_k  1 .. IDX_MAX_K.
- * Hq / Hkv at most 128.  Other arguments, outputs and errors as for
- * idx_tree_attention. */
+ * Other arguments, outputs and errors as for idx_tree_attention. */
 idx_status idx_tree_attention_selected(const idx_tree_problem *problem, const int32_t *sel, int32_t sel_k, void *out,
                                        float *lse, void *state, size_t state_bytes, void *stream);
 

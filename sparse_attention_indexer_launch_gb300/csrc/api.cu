@@ -135,6 +135,8 @@ idx_status device_sms(int *out) {
   return IDX_OK;
 }
 
+uint64_t device_wait_limit_ns() { return wait_limit(); }
+
 static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 static std::mutex g_encode_mu;
 

@@ -29,6 +29,8 @@ inline cudaError_t once_per_device(std::mutex &mu, bool (&done)[128], F setup) {
 
 // SMs of the current device (IDX_EUNSUPPORTED unless it is compute capability 10.3).
 idx_status device_sms(int *out);
+// The time limit of device-side waits (idx_debug_set).
+uint64_t device_wait_limit_ns();
 // The driver's tiled tensor-map encoder, looked up once.
 idx_status tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000 *out);
 
@@ -132,11 +134,21 @@ struct TreeAttnArgs {
   uint16_t *out;           // bf16 [R][Hq][D]
   float *lse;              // [R][Hq] or null
   uint32_t *status;
+  int64_t *prefix;         // [Q + 1] tiles before each request
+  float2 *part_ml;         // [2 * CTAs][rows] (maximum in log2, sum) of shares of split items
+  float *part_o;           // [2 * CTAs][rows][D] their outputs before the division
+  uint64_t wait_limit_ns;
+  int32_t item_tokens;     // drafted tokens of an item
+  int32_t pair;            // its rows are two blocks of item_tokens / 2 tokens
 };
+constexpr int kTreeMaxCtas = 160;   // shares of an attention launch, at most
 
 cudaError_t launch_tree_tables(const TreeTablesArgs &a, int num_sms, cudaStream_t stream);
 cudaError_t launch_write_kv(const WriteKvArgs &a, cudaStream_t stream);
-cudaError_t launch_tree_attention(const TreeAttnArgs &a, int num_sms, cudaStream_t stream);
+// qm: q as [R][Hq][D], box 64 x heads per key/value head x tokens of a row block; km, vm:
+// the cache as [P][Hkv][64][D], box one head's page (64 dimensions of it for bf16).
+cudaError_t launch_tree_attention(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km,
+                                  const CUtensorMap &vm, int num_ctas, cudaStream_t stream);
 
 cudaError_t launch_prep(const PrepArgs &a, cudaStream_t stream);
 cudaError_t launch_score(const CUtensorMap &kmap, const ScoreArgs &a, int kv_dtype, bool batched, int num_ctas,

@@ -1,4 +1,6 @@
 // The C ABI of the tree-verify step (include/idx.h): argument checks and launches.
+#include <cuda.h>
+
 #include <cmath>
 
 #include "idx.h"
@@ -8,6 +10,7 @@
 namespace {
 
 constexpr size_t kStateAlign = 1024;
+constexpr int kMaxGroup = 128;          // query heads per key/value head: the rows of a tensor-core tile
 constexpr size_t kStatusBytes = 1024;   // the status word's block at the start of every state
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -50,24 +53,96 @@ idx_status check_problem(const idx_tree_problem *p, int32_t sel_k) {
   if (st != IDX_OK) return st;
   if (p->R < 1 || p->Q < 1 || p->pt_stride < 1 || p->max_ctx < 0 || p->max_new < 1 || p->Hq < 1) return IDX_EINVAL;
   if (static_cast<int64_t>(p->max_ctx) > static_cast<int64_t>(p->pt_stride) * IDX_PAGE) return IDX_EINVAL;
-  if (p->Hq % p->cache.Hkv != 0 || !std::isfinite(p->scale)) return IDX_EINVAL;
+  if (p->Hq % p->cache.Hkv != 0 || !std::isfinite(p->scale) || p->scale < 0.0f) return IDX_EINVAL;
   if (p->q_row_stride < static_cast<int64_t>(p->Hq) * p->cache.D || p->q_row_stride % 8 != 0) return IDX_EINVAL;
   if (p->R > IDX_MAX_ROWS || p->Q > IDX_MAX_REQS || p->max_new > IDX_MAX_TREE || p->Hq > 1024) return IDX_EUNSUPPORTED;
   if (sel_k < 0 || sel_k > IDX_MAX_K) return IDX_EINVAL;
-  if (sel_k > 0 && p->Hq / p->cache.Hkv > 128) return IDX_EUNSUPPORTED;
+  if (p->Hq / p->cache.Hkv > kMaxGroup) return IDX_EUNSUPPORTED;
+  if (p->q_row_stride >= int64_t{1} << 39) return IDX_EUNSUPPORTED;   // a tensor map's strides have 40 bits
   return IDX_OK;
 }
 
-size_t state_bytes_of(const idx_tree_problem *, int32_t) { return kStatusBytes; }
+size_t round_up(size_t x) { return (x + kStateAlign - 1) / kStateAlign * kStateAlign; }
+
+// The launch's shape: tokens of a 128-row block, and whether a CTA takes two blocks.
+// Two blocks share every K and V tile in shared memory and pay where one block does
+// not hold a request's rows; otherwise the two streams split one block's tiles.
+struct Shape {
+  int block_tokens;
+  bool pair;
+  int rows;   // rows of a CTA's item
+};
+Shape shape_of(const idx_tree_problem *p, int32_t sel_k) {
+  Shape s{};
+  const int G = p->Hq / p->cache.Hkv;
+  s.block_tokens = sel_k > 0 ? 1 : kMaxGroup / G;
+  s.pair = sel_k == 0 && p->max_new > s.block_tokens;
+  s.rows = s.pair ? 2 * kMaxGroup : kMaxGroup;
+  return s;
+}
+
+struct StateLayout {
+  size_t prefix, ml, o, total;
+};
+StateLayout state_layout(const idx_tree_problem *p, int32_t sel_k) {
+  const Shape s = shape_of(p, sel_k);
+  const size_t slots = 2 * static_cast<size_t>(idx::kTreeMaxCtas) * s.rows;
+  StateLayout L{};
+  L.prefix = kStatusBytes;
+  L.ml = L.prefix + round_up((static_cast<size_t>(p->Q) + 1) * sizeof(int64_t));
+  L.o = L.ml + round_up(slots * sizeof(float2));
+  L.total = L.o + round_up(slots * p->cache.D * sizeof(float));
+  return L;
+}
+
+// K or V as a 4-D tensor [P][Hkv][64][D].  bf16: boxes of 64 dimensions in the 128-byte
+// swizzle the tensor core reads; E4M3: whole rows, converted in shared memory.
+idx_status cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const idx_kv_cache *c, void *base, CUtensorMap *map) {
+  const bool f8 = c->kv_dtype == IDX_KV_E4M3;
+  const cuuint64_t e = f8 ? 1 : 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->D), IDX_PAGE, static_cast<cuuint64_t>(c->Hkv),
+                              static_cast<cuuint64_t>(c->P)};
+  const cuuint64_t strides[3] = {c->token_stride * e, c->head_stride * e, c->page_stride * e};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(f8 ? c->D : 64), IDX_PAGE, 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims,
+                            strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? IDX_OK : IDX_ECUDA;
+}
 
 idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, void *out, float *lse, void *state,
                   size_t state_bytes, void *stream) {
   idx_status st = check_problem(p, sel_k);
   if (st != IDX_OK) return st;
-  if (out == nullptr || !aligned(out, 16) || !state_ok(state, state_bytes, state_bytes_of(p, sel_k))) return IDX_EINVAL;
+  const StateLayout L = state_layout(p, sel_k);
+  if (out == nullptr || !aligned(out, 16) || !state_ok(state, state_bytes, L.total)) return IDX_EINVAL;
   int sms = 0;
   st = idx::device_sms(&sms);
   if (st != IDX_OK) return st;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  st = idx::tensor_map_encoder(&encode);
+  if (st != IDX_OK) return st;
+  const Shape s = shape_of(p, sel_k);
+  const int D = p->cache.D, G = p->Hq / p->cache.Hkv;
+  CUtensorMap qm, km{}, vm{};
+  {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p->Hq), static_cast<cuuint64_t>(p->R)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(p->q_row_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(s.block_tokens)};
+    const cuuint32_t one[3] = {1, 1, 1};
+    if (encode(&qm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p->q), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return IDX_ECUDA;
+  }
+  if (sel == nullptr) {   // selected positions are gathered by plain loads
+    st = cache_map(encode, &p->cache, p->cache.k, &km);
+    if (st == IDX_OK) st = cache_map(encode, &p->cache, p->cache.v, &vm);
+    if (st != IDX_OK) return st;
+  }
+  uint8_t *const b = static_cast<uint8_t *>(state);
   idx::TreeAttnArgs a{};
   a.p = *p;
   a.sel = sel;
@@ -75,7 +150,14 @@ idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, 
   a.out = static_cast<uint16_t *>(out);
   a.lse = lse;
   a.status = static_cast<uint32_t *>(state);
-  return cuda_ok(idx::launch_tree_attention(a, sms, static_cast<cudaStream_t>(stream)));
+  a.prefix = reinterpret_cast<int64_t *>(b + L.prefix);
+  a.part_ml = reinterpret_cast<float2 *>(b + L.ml);
+  a.part_o = reinterpret_cast<float *>(b + L.o);
+  a.wait_limit_ns = idx::device_wait_limit_ns();
+  a.pair = s.pair;
+  a.item_tokens = s.pair ? 2 * s.block_tokens : s.block_tokens;
+  const int ctas = sms < idx::kTreeMaxCtas ? sms : idx::kTreeMaxCtas;
+  return cuda_ok(idx::launch_tree_attention(a, qm, km, vm, ctas, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -130,7 +212,7 @@ idx_status idx_write_kv(const idx_kv_cache *cache, const void *k_new, const void
 
 size_t idx_tree_state_size(const idx_tree_problem *problem, int32_t sel_k) {
   if (check_problem(problem, sel_k) != IDX_OK) return 0;
-  return state_bytes_of(problem, sel_k);
+  return state_layout(problem, sel_k).total;
 }
 
 idx_status idx_tree_attention(const idx_tree_problem *problem, void *out, float *lse, void *state, size_t state_bytes,
