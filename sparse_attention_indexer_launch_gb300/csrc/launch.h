@@ -134,12 +134,12 @@ struct TreeAttnArgs {
   uint16_t *out;           // bf16 [R][Hq][D]
   float *lse;              // [R][Hq] or null
   uint32_t *status;
-  int64_t *prefix;         // [Q + 1] tiles before each request
   float2 *part_ml;         // [2 * CTAs][rows] (maximum in log2, sum) of shares of split items
   float *part_o;           // [2 * CTAs][rows][D] their outputs before the division
   uint64_t wait_limit_ns;
   int32_t item_tokens;     // drafted tokens of an item
   int32_t pair;            // its rows are two blocks of item_tokens / 2 tokens
+  int32_t copies;          // of an item's rows in the tile's 128
 };
 constexpr int kTreeMaxCtas = 160;   // shares of an attention launch, at most
 
@@ -147,8 +147,10 @@ cudaError_t launch_tree_tables(const TreeTablesArgs &a, int num_sms, cudaStream_
 cudaError_t launch_write_kv(const WriteKvArgs &a, cudaStream_t stream);
 // qm: q as [R][Hq][D], box 64 x heads per key/value head x tokens of a row block; km, vm:
 // the cache as [P][Hkv][64][D], box one head's page (64 dimensions of it for bf16).
-cudaError_t launch_tree_attention(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km,
-                                  const CUtensorMap &vm, int num_ctas, cudaStream_t stream);
+using TreeAttnLaunch = cudaError_t(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km,
+                                   const CUtensorMap &vm, int num_ctas, cudaStream_t stream);
+TreeAttnLaunch launch_tree_attention_bf16_64, launch_tree_attention_bf16_128, launch_tree_attention_e4m3_64,
+    launch_tree_attention_e4m3_128;
 
 cudaError_t launch_prep(const PrepArgs &a, cudaStream_t stream);
 cudaError_t launch_score(const CUtensorMap &kmap, const ScoreArgs &a, int kv_dtype, bool batched, int num_ctas,

@@ -44,6 +44,34 @@ idx_status check_cache(const idx_kv_cache *c) {
   return IDX_OK;
 }
 
+// The launch's shape.  Few rows are copied to fill the tensor-core tile, so that every
+// softmax warp has work (tree_attention.cuh); more than 128 rows go through a CTA in
+// pairs of blocks that share every K and V tile.
+struct Shape {
+  int block_tokens;   // tokens of a row block
+  int copies;
+  bool pair;
+};
+Shape shape_of(const idx_tree_problem *p, int32_t sel_k) {
+  Shape s{};
+  const int G = p->Hq / p->cache.Hkv;
+  const int rows = (sel_k > 0 ? 1 : p->max_new) * G;   // of a request and key/value head (selected: of a token)
+  s.pair = rows > kMaxGroup / G * G;
+  s.copies = s.pair ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+  s.block_tokens = sel_k > 0 ? 1 : kMaxGroup / s.copies / G;
+  return s;
+}
+
+// Tiles of the launch, at most: the kernels count them in 31 bits.
+bool tiles_fit(const idx_tree_problem *p, int32_t sel_k) {
+  const Shape s = shape_of(p, sel_k);
+  const int64_t item = s.pair ? 2 * s.block_tokens : s.block_tokens;
+  const int64_t tiles = ((sel_k > 0 ? sel_k : p->max_ctx) + static_cast<int64_t>(p->max_new) + 127) / 128;
+  const int64_t blocks = (p->max_new + item - 1) / item;
+  const int64_t items = (static_cast<int64_t>(p->Q) * blocks < p->R ? static_cast<int64_t>(p->Q) * blocks : p->R) * p->cache.Hkv;
+  return items * tiles <= INT32_MAX;
+}
+
 idx_status check_problem(const idx_tree_problem *p, int32_t sel_k) {
   if (p == nullptr) return IDX_EINVAL;
   if (p->q == nullptr || !aligned(p->q, 16) || p->page_table == nullptr || p->ctx_len == nullptr ||
@@ -58,38 +86,21 @@ idx_status check_problem(const idx_tree_problem *p, int32_t sel_k) {
   if (p->R > IDX_MAX_ROWS || p->Q > IDX_MAX_REQS || p->max_new > IDX_MAX_TREE || p->Hq > 1024) return IDX_EUNSUPPORTED;
   if (sel_k < 0 || sel_k > IDX_MAX_K) return IDX_EINVAL;
   if (p->Hq / p->cache.Hkv > kMaxGroup) return IDX_EUNSUPPORTED;
+  if (!tiles_fit(p, sel_k)) return IDX_EUNSUPPORTED;
   if (p->q_row_stride >= int64_t{1} << 39) return IDX_EUNSUPPORTED;   // a tensor map's strides have 40 bits
   return IDX_OK;
 }
 
 size_t round_up(size_t x) { return (x + kStateAlign - 1) / kStateAlign * kStateAlign; }
 
-// The launch's shape: tokens of a 128-row block, and whether a CTA takes two blocks.
-// Two blocks share every K and V tile in shared memory and pay where one block does
-// not hold a request's rows; otherwise the two streams split one block's tiles.
-struct Shape {
-  int block_tokens;
-  bool pair;
-  int rows;   // rows of a CTA's item
-};
-Shape shape_of(const idx_tree_problem *p, int32_t sel_k) {
-  Shape s{};
-  const int G = p->Hq / p->cache.Hkv;
-  s.block_tokens = sel_k > 0 ? 1 : kMaxGroup / G;
-  s.pair = sel_k == 0 && p->max_new > s.block_tokens;
-  s.rows = s.pair ? 2 * kMaxGroup : kMaxGroup;
-  return s;
-}
-
 struct StateLayout {
-  size_t prefix, ml, o, total;
+  size_t ml, o, total;
 };
 StateLayout state_layout(const idx_tree_problem *p, int32_t sel_k) {
   const Shape s = shape_of(p, sel_k);
-  const size_t slots = 2 * static_cast<size_t>(idx::kTreeMaxCtas) * s.rows;
+  const size_t slots = 2 * static_cast<size_t>(idx::kTreeMaxCtas) * (s.pair ? 256 : 128);
   StateLayout L{};
-  L.prefix = kStatusBytes;
-  L.ml = L.prefix + round_up((static_cast<size_t>(p->Q) + 1) * sizeof(int64_t));
+  L.ml = kStatusBytes;
   L.o = L.ml + round_up(slots * sizeof(float2));
   L.total = L.o + round_up(slots * p->cache.D * sizeof(float));
   return L;
@@ -150,14 +161,17 @@ idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, 
   a.out = static_cast<uint16_t *>(out);
   a.lse = lse;
   a.status = static_cast<uint32_t *>(state);
-  a.prefix = reinterpret_cast<int64_t *>(b + L.prefix);
   a.part_ml = reinterpret_cast<float2 *>(b + L.ml);
   a.part_o = reinterpret_cast<float *>(b + L.o);
   a.wait_limit_ns = idx::device_wait_limit_ns();
   a.pair = s.pair;
+  a.copies = s.copies;
   a.item_tokens = s.pair ? 2 * s.block_tokens : s.block_tokens;
   const int ctas = sms < idx::kTreeMaxCtas ? sms : idx::kTreeMaxCtas;
-  return cuda_ok(idx::launch_tree_attention(a, qm, km, vm, ctas, static_cast<cudaStream_t>(stream)));
+  const bool f8 = p->cache.kv_dtype == IDX_KV_E4M3;
+  idx::TreeAttnLaunch &launch = f8 ? (D == 64 ? idx::launch_tree_attention_e4m3_64 : idx::launch_tree_attention_e4m3_128)
+                                   : (D == 64 ? idx::launch_tree_attention_bf16_64 : idx::launch_tree_attention_bf16_128);
+  return cuda_ok(launch(a, qm, km, vm, ctas, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
