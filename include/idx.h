@@ -408,7 +408,7 @@ size_t idx_tree_state_size(const idx_tree_problem *problem, int32_t sel_k);
  *   lse  device fp32 [R][Hq] or NULL.
  * Rows outside every request are not written.  Sums and softmax statistics are fp32;
  * the probabilities are rounded to bf16 for the product with V (to two bf16 terms where
- * fewer than 128 keys of a 128-key tile are visible to all).  The result does not
+ * fewer than 64 keys of a 64-key tile are visible to all).  The result does not
  * depend on how the work was split in a way that changes between equal calls.
  * Device-detected (IDX_EDEVICE): a page id outside [0, P) (its tokens are left out),
  * ctx_len outside 0 .. max_ctx, more rows than max_new or positions past the page

@@ -66,7 +66,7 @@ Shape shape_of(const idx_tree_problem *p, int32_t sel_k) {
 bool tiles_fit(const idx_tree_problem *p, int32_t sel_k) {
   const Shape s = shape_of(p, sel_k);
   const int64_t item = s.pair ? 2 * s.block_tokens : s.block_tokens;
-  const int64_t tiles = ((sel_k > 0 ? sel_k : p->max_ctx) + static_cast<int64_t>(p->max_new) + 127) / 128;
+  const int64_t tiles = ((sel_k > 0 ? sel_k : p->max_ctx) + static_cast<int64_t>(p->max_new) + IDX_PAGE - 1) / IDX_PAGE;
   const int64_t blocks = (p->max_new + item - 1) / item;
   const int64_t items = (static_cast<int64_t>(p->Q) * blocks < p->R ? static_cast<int64_t>(p->Q) * blocks : p->R) * p->cache.Hkv;
   return items * tiles <= INT32_MAX;

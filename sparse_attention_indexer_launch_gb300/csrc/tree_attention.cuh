@@ -1,8 +1,8 @@
 // Attention of drafted tokens over a paged cache, whole or at selected positions.
 //
 // For a key/value head the query vectors that read it (tokens x query heads per
-// key/value head) are the M = 128 rows of a tensor-core tile, and 128 cache
-// positions (two pages) its columns:
+// key/value head) are the M = 128 rows of a tensor-core tile, and the 64 positions of
+// a cache page its columns:
 //
 //     S = Q K^T (TMEM)  ->  P = exp2(c S - m), rows' running maximum m and sum l
 //                       ->  O += P V (TMEM, P read back from TMEM as operand A)
@@ -16,17 +16,17 @@
 // its output; shares of an item go to the state as (O, m, l) and the combine kernel
 // joins them in CTA order, so equal calls give equal bits.
 //
-// Two streams hide the softmax behind the tensor core: the streams are either the
-// even and odd tiles of one row block (up to 128 rows, joined in TMEM at the end of
-// the item: more bytes in flight for the few-row, memory-bound calls) or two row
-// blocks over the same tiles (more rows: each K and V tile is read from shared
-// memory for 256 rows).  Each has S and O in 2 x 128 of TMEM's 512 columns, its own
-// MMA-issuing thread and its own four softmax warps, one thread per row.
+// Two streams fill the tensor core: the even and odd tiles of one row block (up to 128
+// rows, joined in TMEM at the end of the item: more bytes in flight for the few-row,
+// memory-bound calls) or two row blocks over the same tiles (more rows: each K and V
+// tile is read from shared memory for 256 rows).  Each has O and two S buffers of 64
+// columns in TMEM, so that the scores of a tile are computed while its four softmax
+// warps, one thread per row, work on the tile before; P takes its S's place.
 //
 // A block of at most 32 (64) rows fills the 128 of the tile four (two) times over: Q
 // is loaded that often, and each copy of the rows takes a quarter (half) of a tile's
 // keys, with zeros in its P for the others.  All four softmax warps then work on
-// every tile, 32 (64) keys each, and the copies' O are summed at the end of the item.
+// every tile, 16 (32) keys each, and the copies' O are summed at the end of the item.
 // The tensor core computes nothing that it would not have computed for the empty
 // rows.
 #pragma once
@@ -41,11 +41,11 @@
 namespace idx {
 namespace {
 
-constexpr int kTile = 128;               // keys per tile
+constexpr int kTile = kPage;             // keys per tile
 constexpr int kRows = 128;               // rows of a stream
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;   // + 128 * stream
-constexpr int kMinTiles = 2;             // tiles per CTA, at least (fewer CTAs otherwise)
+constexpr uint32_t kColS = 0, kColO = 256;   // + 128 * stream (S: + 64 * buffer)
+constexpr int kMinTiles = 4;             // tiles per CTA, at least (fewer CTAs otherwise)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A row's maximum moves only when a score passes it by 2^8: until then the sums run
@@ -55,8 +55,10 @@ constexpr float kLazy = 8.0f;
 // ---------------------------------------------------------------------------- roles
 // warps 0-3 and 4-7: softmax of streams 0 and 1; 8: TMA producer; 9 and 10: MMA
 // issuers of streams 0 and 1; 11: idle, or with 8 the gatherers of selected positions;
-// 12-15 with an E4M3 cache: conversion to bf16.
+// 12-19 with an E4M3 cache: conversion to bf16, two teams of four on alternate loads.
 constexpr int kProducerWarp = 8, kIssuerWarp = 9, kGatherWarp = 11, kConvertWarp = 12;
+
+constexpr int kMaxStages = 16;
 
 // COPIES: copies of the row block in the tile's rows (4, 2 or 1); PAIR: two row blocks.
 template <int D, bool F8, int COPIES, bool PAIR, bool SEL>
@@ -67,38 +69,39 @@ struct Cfg {
   static constexpr int kQBufs = PAIR || F8 ? 1 : 2;
   static constexpr int kQTotal = kQBytes * (PAIR ? 2 : kQBufs);
   // bf16: 128 KB of tiles; E4M3: raw tiles as memory allows and 96 KB of converted ones
-  static constexpr int kStages = F8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
-  static constexpr int kRawStages = !F8 ? 0 : D == 64 ? 6 : PAIR ? 3 : COPIES > 1 ? 4 : 5;
-  static constexpr int kScaleStages = F8 ? 8 : 0;
+  static constexpr int kStages = F8 ? (D == 128 ? 6 : 12) : (D == 128 ? 8 : 16);
+  static constexpr int kRawStages = !F8 ? 0 : D == 64 ? 16 : PAIR ? 6 : COPIES > 1 ? 8 : 10;
+  static constexpr int kScaleStages = F8 ? 16 : 0;
   static constexpr int kRedBytes = COPIES > 1 ? 2 * kRows * 16 * 4 : 0;   // the copies' sum: 16 columns a stream
-  static constexpr int kThreads = 32 * (F8 ? kConvertWarp + 4 : kConvertWarp);
-  // Registers per thread after the roles part, where a softmax thread holds 128 scores.
-  // The shares add up to no more than the launch's threads x registers.
-  static constexpr bool kShareRegs = COPIES == 1 || (F8 && COPIES == 2);
-  static constexpr int kRegsLaunch = kThreads == 384 ? 168 : 128;
-  static constexpr int kRegsSoftmax = kThreads == 384 ? 208 : 176;
-  static constexpr int kRegsOther = kThreads == 384 ? 88 : 80;
-  static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch, "register shares");
+  static constexpr int kThreads = 32 * (F8 ? kConvertWarp + 8 : kConvertWarp);
+  // K tiles loaded ahead of the first V: two per stream
+  static constexpr int kAhead = PAIR ? 2 : 4;
+  static_assert(kStages >= kAhead + 2 && kStages <= kMaxStages && kRawStages <= kMaxStages, "rings");
+  // Registers per thread after the roles part, where a softmax thread holds up to 64
+  // scores.  The shares add up to no more than the launch's threads x registers.
+  static constexpr bool kShareRegs = F8;
+  static constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsOther = 64;
+  static_assert(!F8 || 256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch, "register shares");
   static constexpr int kDynamic = 1024 + kQTotal + kStages * kTileBytes + kRawStages * kRawBytes +
                                   kScaleStages * 2 * kTile * 4 + kRedBytes;
 };
 
 struct Barriers {
-  uint64_t kv_full[8], kv_empty[8];
-  uint64_t raw_full[6], raw_empty[6];
-  uint64_t sc_full[8], sc_empty[8];
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t raw_full[kMaxStages], raw_empty[kMaxStages];
+  uint64_t sc_full[16], sc_empty[16];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_ready[2], pv_done[2], o_free[2], drain[2], stats[2], red_full[2], red_free[2];
-  uint64_t scrubbed, stagger;
+  uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];   // [stream][buffer]
+  uint64_t o_free[2], drain[2], stats[2], red_full[2], red_free[2], scrubbed[2];
   uint32_t tmem_base;
   int abort;
-  int32_t two_terms[2];            // the stream's P has a low term
+  int32_t two_terms[2][2];         // P of [stream][buffer] has a low term
   int32_t start_req, start_base;   // the share's first request, and the tiles before it
-  uint32_t pages_ok[16];           // dense: bit h: page h of the CTA's tile k % 16 was loaded
-  uint32_t keys_ok[16][4];         // selected: bit per key of tile k % 16
-  int32_t nonfinite[8];            // segment number + 1 whose drafted tokens' V held NaN or infinity
+  uint32_t page_ok[32];            // dense: the page of the CTA's tile k % 32 was loaded
+  uint32_t keys_ok[32][2];         // selected: bit per key of tile k % 32
+  int32_t nonfinite[32];           // segment number + 1 whose drafted tokens' V held NaN or infinity
   float row_m[2][2][kRows], row_l[2][2][kRows];   // [segment parity][stream][row]
-  int32_t warp_sums[16];
+  int32_t warp_sums[20];
 };
 
 // ---------------------------------------------------------------------------- TMEM
@@ -117,17 +120,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 __device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
-      "%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -185,6 +177,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
@@ -308,22 +305,39 @@ struct Walk {
   }
 };
 
-// Place of tile j's K and V in the order K0 K1 V0 K2 V1 ... of a segment of n tiles.
-__device__ __forceinline__ int pos_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ int pos_v(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * n - 1; }
+// The loads of a segment of n tiles: K of the first `ahead` tiles, then V0, K, V1, K ...
+// Their places in that order, and the load at place x.
+__device__ __forceinline__ int pos_k(int j, int ahead) { return j < ahead ? j : 2 * j - ahead + 1; }
+__device__ __forceinline__ int pos_v(int j, int n, int ahead) { return min(n, j + ahead) + j; }
+__device__ __forceinline__ bool load_at(int x, int n, int ahead, int &j) {   // true: V of tile j, false: K
+  const int lead = min(n, ahead);
+  if (x < lead) {
+    j = x;
+    return false;
+  }
+  const int y = x - lead, both = 2 * (n - lead);
+  if (y >= both) {
+    j = n - lead + (y - both);
+    return true;
+  }
+  j = (y >> 1) + (y & 1 ? lead : 0);
+  return (y & 1) == 0;
+}
 
 // ---------------------------------------------------------------------------- softmax
 // Moves the row's maximum to `top` where that passes it by more than kLazy, and scales l
-// and O (D columns at to) along; whole warps together.
-template <int D>
-__device__ __forceinline__ void raise_maximum(uint32_t to, float top, bool has_o, float &m, float &l) {
+// and O (D columns at to, once settled() says that the product before has completed)
+// along; whole warps together.
+template <int D, typename F>
+__device__ __forceinline__ bool raise_maximum(uint32_t to, float top, bool has_o, float &m, float &l, F settled) {
   const bool grow = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
-  if (!__any_sync(0xffffffffu, grow)) return;
+  if (!__any_sync(0xffffffffu, grow)) return true;
   const float nm = fmaxf(m, top);
   const float f = m == -INFINITY ? 0.0f : ex2(m - nm);
   m = nm;
   l *= f;
-  if (!has_o) return;
+  if (!has_o) return true;
+  if (!settled()) return false;
 #pragma unroll 1
   for (int w = 0; w < D / 16; ++w) {
     uint32_t x[16];
@@ -334,34 +348,43 @@ __device__ __forceinline__ void raise_maximum(uint32_t to, float top, bool has_o
     for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(__uint_as_float(x[y]) * f);
     tmem_st16(to + 16 * w, x);
   }
+  return true;
 }
 
-// One row's keys of a tile (N of the 128, from column n0): S (columns at ts) to P in the
+// One row's keys of a tile (N of the 64, from column n0): S (columns at ts) to P in the
 // same columns, the row's maximum m and sum l, and O (D columns at to) when the maximum
 // moves.  special: only the keys of ok (a bit per key) are visible.  sc: the tile's K
 // scales, then its V scales.
 //
-// P is rounded to bf16 for the product with V.  Over the 128 or more keys of a full tile
+// P is rounded to bf16 for the product with V.  Over the 64 or more keys of a full tile
 // the roundings average out below the output's own; the few keys of a special tile do
-// not, so there P is kept in two bf16 terms, high in columns 0-63 and low in 64-127, and
+// not, so there P is kept in two bf16 terms, high in columns 0-31 and low in 32-63, and
 // the product runs over both.
-template <int D, bool F8, int N>
-__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, const float4 *sc, float c, int n0, bool special,
-                                             const uint32_t (&ok)[N / 32], bool has_o, float &m, float &l) {
-  uint32_t x[N / 32][32];
+template <int D, bool F8, int N, typename F>
+__device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const float *sc, float c, int n0, bool special,
+                                             uint64_t ok, bool has_o, float &m, float &l, F settled) {
+  constexpr int kW = N < 32 ? N : 32;        // columns per register group
+  uint32_t x[N / kW][kW];
 #pragma unroll
-  for (int w = 0; w < N / 32; ++w) tmem_ld32(ts + n0 + 32 * w, x[w]);
-  const float4 *const ks = sc + n0 / 4, *const vs = ks + kTile / 4;
+  for (int w = 0; w < N / kW; ++w) {
+    if constexpr (kW == 32) tmem_ld32(ts + n0 + 32 * w, x[w]);
+    else tmem_ld16(ts + n0, x[w]);
+  }
+  const float4 *const ks = reinterpret_cast<const float4 *>(sc + n0);
+  const float2 *const vs = reinterpret_cast<const float2 *>(sc + kTile + n0);
   tmem_wait_ld();
 #pragma unroll
-  for (int w = 0; w < N / 32; ++w) reg_fence32(x[w]);
+  for (int w = 0; w < N / kW; ++w) {
+    if constexpr (kW == 32) reg_fence32(x[w]);
+    else reg_fence16(x[w]);
+  }
   if (F8) {
 #pragma unroll
-    for (int w = 0; w < N / 32; ++w)
+    for (int w = 0; w < N / kW; ++w)
 #pragma unroll
-      for (int y = 0; y < 32; y += 4) {
+      for (int y = 0; y < kW; y += 4) {
         if (y % 16 == 0) asm volatile("" ::: "memory");   // at most four of the loads ahead
-        const float4 k = ks[8 * w + y / 4];
+        const float4 k = ks[kW / 4 * w + y / 4];
         x[w][y] = __float_as_uint(__uint_as_float(x[w][y]) * k.x);
         x[w][y + 1] = __float_as_uint(__uint_as_float(x[w][y + 1]) * k.y);
         x[w][y + 2] = __float_as_uint(__uint_as_float(x[w][y + 2]) * k.z);
@@ -370,38 +393,40 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, const flo
   }
   if (special) {
 #pragma unroll
-    for (int w = 0; w < N / 32; ++w)
+    for (int w = 0; w < N / kW; ++w)
 #pragma unroll
-      for (int y = 0; y < 32; ++y) x[w][y] = (ok[w] >> y) & 1u ? x[w][y] : 0xFF800000u;   // -infinity
+      for (int y = 0; y < kW; ++y)
+        x[w][y] = (static_cast<uint32_t>(ok >> (32 * w)) >> y) & 1u ? x[w][y] : 0xFF800000u;   // -infinity
   }
   float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int w = 0; w < N / 32; ++w)
+  for (int w = 0; w < N / kW; ++w)
 #pragma unroll
-    for (int y = 0; y < 32; y += 8)
+    for (int y = 0; y < kW; y += 8)
 #pragma unroll
       for (int z = 0; z < 4; ++z)
         t4[z] = max3(t4[z], __uint_as_float(x[w][y + 2 * z]), __uint_as_float(x[w][y + 2 * z + 1]));
   float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c;   // in units of log2
   if (top != top) top = 0.0f;   // scale 0: 0 x -inf moves no maximum
-  raise_maximum<D>(to, top, has_o, m, l);
+  if (!raise_maximum<D>(to, top, has_o, m, l, settled)) return false;
   const float base = m == -INFINITY ? 0.0f : m;
   const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
   float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-  for (int w = 0; w < N / 32; ++w) {
-    uint32_t hi[16];
+  for (int w = 0; w < N / kW; ++w) {
+    uint32_t hi[kW / 2];
 #pragma unroll
-    for (int y = 0; y < 32; y += 2) {
+    for (int y = 0; y < kW; y += 2) {
       const float2 e2 = __ffma2_rn(make_float2(__uint_as_float(x[w][y]), __uint_as_float(x[w][y + 1])), c2, b2);
       float2 e = make_float2(ex2(e2.x), ex2(e2.y));
       l2[(y >> 1) & 1] = __fadd2_rn(l2[(y >> 1) & 1], e);
       if (F8) {
         if (y % 16 == 0) asm volatile("" ::: "memory");
-        const float2 v = reinterpret_cast<const float2 *>(vs)[16 * w + y / 2];
+        const float2 v = vs[kW / 2 * w + y / 2];
         if (special) {   // a stale scale may be NaN
-          e.x = (ok[w] >> y) & 1u ? e.x * v.x : 0.0f;
-          e.y = (ok[w] >> (y + 1)) & 1u ? e.y * v.y : 0.0f;
+          const uint32_t seen = static_cast<uint32_t>(ok >> (32 * w)) >> y;
+          e.x = seen & 1u ? e.x * v.x : 0.0f;
+          e.y = seen & 2u ? e.y * v.y : 0.0f;
         } else {
           e.x *= v.x;
           e.y *= v.y;
@@ -411,30 +436,33 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, const flo
       x[w][y] = __float_as_uint(e.x);
       x[w][y + 1] = __float_as_uint(e.y);
     }
-    tmem_st16(ts + n0 / 2 + 16 * w, hi);
+    if constexpr (kW == 32) tmem_st16(ts + n0 / 2 + 16 * w, hi);
+    else tmem_st8(ts + n0 / 2, hi);
     if (special) {
-      uint32_t lo[16];
+      uint32_t lo[kW / 2];
 #pragma unroll
-      for (int y = 0; y < 16; ++y) {
+      for (int y = 0; y < kW / 2; ++y) {
         // an infinity (a scale's) has no low term
         const float r0 = __uint_as_float(x[w][2 * y]) - __uint_as_float(hi[y] << 16);
         const float r1 = __uint_as_float(x[w][2 * y + 1]) - __uint_as_float(hi[y] & 0xFFFF0000u);
         lo[y] = pack_bf16(r0 == r0 ? r0 : 0.0f, r1 == r1 ? r1 : 0.0f);
       }
-      tmem_st16(ts + 64 + n0 / 2 + 16 * w, lo);
+      if constexpr (kW == 32) tmem_st16(ts + 32 + n0 / 2 + 16 * w, lo);
+      else tmem_st8(ts + 32 + n0 / 2, lo);
     }
   }
   if constexpr (N < kTile) {   // the other copies' keys
-    uint32_t zero[16] = {};
+    uint32_t zero[8] = {};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (16 * w >= n0 / 2 && 16 * w < (n0 + N) / 2) continue;
-      tmem_st16(ts + 16 * w, zero);
-      if (special) tmem_st16(ts + 64 + 16 * w, zero);
+    for (int w = 0; w < kTile / 2; w += 8) {
+      if (w >= n0 / 2 && w < (n0 + N) / 2) continue;
+      tmem_st8(ts + w, zero);
+      if (special) tmem_st8(ts + 32 + w, zero);
     }
   }
   l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
   tmem_wait_st();
+  return true;
 }
 
 // ---------------------------------------------------------------------------- kernel
@@ -449,7 +477,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
   uint8_t *const sq = smem;
   uint8_t *const skv = sq + C::kQTotal;
   uint8_t *const sraw = skv + C::kStages * C::kTileBytes;
-  float *const ssc = reinterpret_cast<float *>(sraw + C::kRawStages * C::kRawBytes);   // [stage][K 128, V 128]
+  float *const ssc = reinterpret_cast<float *>(sraw + C::kRawStages * C::kRawBytes);   // [stage][K 64, V 64]
   float *const sred = ssc + C::kScaleStages * 2 * kTile;                                // [stream][row][16]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const idx_tree_problem &p = a.p;
@@ -457,37 +485,36 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
   const int G = p.Hq / Hkv;
   const int tb = PAIR ? a.item_tokens / 2 : a.item_tokens;   // tokens of a row block
   constexpr int kBlocks = D / 64;            // 64-dimension blocks of an operand tile
-  constexpr int kBlockBytes = kTile * 128;
+  constexpr int kBlockBytes = kTile * 128, kQBlockBytes = kRows * 128;
   grid_dependency_trigger();                 // the combine kernel's CTAs may take free SMs
 
   if (tid == 0) {
-    for (int s = 0; s < 8; ++s) {
-      // filled by the four converting warps, the two gathering ones or one TMA thread
+    for (int s = 0; s < kMaxStages; ++s) {
+      // filled by four converting warps, the two gathering ones or one TMA thread
       mbar_init(&bars.kv_full[s], F8 ? 4 : SEL ? 2 : 1);
       mbar_init(&bars.kv_empty[s], PAIR ? 2 : 1);
-      mbar_init(&bars.sc_full[s], SEL ? 2 : 1);
-      mbar_init(&bars.sc_empty[s], PAIR ? 8 : 4);
-    }
-    for (int s = 0; s < 6; ++s) {
       mbar_init(&bars.raw_full[s], SEL ? 2 : 1);
       mbar_init(&bars.raw_empty[s], 4);
+      mbar_init(&bars.sc_full[s], SEL ? 2 : 1);
+      mbar_init(&bars.sc_empty[s], PAIR ? 8 : 4);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.q_full[s], 1);
       mbar_init(&bars.q_empty[s], 2);
-      mbar_init(&bars.s_full[s], 1);
-      mbar_init(&bars.p_ready[s], 4);
-      mbar_init(&bars.pv_done[s], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars.s_full[s][b], 1);
+        mbar_init(&bars.p_ready[s][b], 4);
+        mbar_init(&bars.pv_done[s][b], 1);
+      }
       mbar_init(&bars.o_free[s], PAIR ? 4 : 8);
       mbar_init(&bars.drain[s], 1);
       mbar_init(&bars.stats[s], 4);
       mbar_init(&bars.red_full[s], 4);
       mbar_init(&bars.red_free[s], 4);
+      mbar_init(&bars.scrubbed[s], 4);
     }
-    mbar_init(&bars.scrubbed, 4);
-    mbar_init(&bars.stagger, 1);
     bars.abort = 0;
-    for (int s = 0; s < 8; ++s) bars.nonfinite[s] = 0;
+    for (int s = 0; s < 32; ++s) bars.nonfinite[s] = 0;
     fence_barrier_init();
   }
   if (warp == kIssuerWarp) {
@@ -602,7 +629,6 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
     const int row = lrow % kBlockRows;     // row of the block
     const int copy = lrow / kBlockRows;    // the same for a whole warp
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // first TMEM lane of the warp << 16
-    const uint32_t ts = tmem + kColS + 128 * s + lanes;
     const uint32_t to = tmem + kColO + 128 * s + lanes;
     const float c = p.scale * kLog2e;
     const int step = PAIR ? 1 : 2, j0 = PAIR ? 0 : s;
@@ -625,56 +651,50 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       for (int j = j0; live && j < walk.count; j += step, ++n, ++mine) {
         const int k = tiles + j;
         const int key0 = (walk.tile0 + j) * kTile;
-        if (F8 && !warp_wait_all(&bars.sc_full[k % 8], (k / 8) & 1)) {
-          ok = false;
-          break;
-        }
-        if (!warp_wait_all(&bars.s_full[s], n & 1)) {
+        const int buf = n & 1;
+        if ((F8 && !warp_wait_all(&bars.sc_full[k % 16], (k / 16) & 1)) ||
+            !warp_wait_all(&bars.s_full[s][buf], (n >> 1) & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t okbits[kKeys / 32];   // keys of the tile that the row sees
+        uint64_t okbits = ~0ull;   // the copy's keys of the tile that the row sees
         bool special;
         if (SEL) {
-          special = (bars.keys_ok[k & 15][0] & bars.keys_ok[k & 15][1] & bars.keys_ok[k & 15][2] &
-                     bars.keys_ok[k & 15][3]) != ~0u;
-#pragma unroll
-          for (int w = 0; w < kKeys / 32; ++w) okbits[w] = bars.keys_ok[k & 15][copy * (kKeys / 32) + w];
+          const uint32_t k0 = bars.keys_ok[k & 31][0], k1 = bars.keys_ok[k & 31][1];
+          special = (k0 & k1) != ~0u;
+          if (special) okbits = (static_cast<uint64_t>(k1) << 32 | k0) >> (copy * kKeys);
         } else {
-          const uint32_t flags = bars.pages_ok[k & 15];
-          special = key0 + kTile > ctx || flags != 3u;
-          const int lim = walk.q.keys - ctx;      // drafted tokens within the page table
-          const uint64_t vm = lim >= 64 ? mask : mask & ((1ull << lim) - 1ull);
-#pragma unroll
-          for (int w = 0; w < kKeys / 32; ++w) {
-            const int word = copy * (kKeys / 32) + w;
-            const int before = ctx - (key0 + 32 * word);   // cached keys from the word's first on
-            uint32_t bits = ~0u;
-            if (before < 32) {
-              if (before > 0) bits = ((1u << before) - 1u) | static_cast<uint32_t>(vm << before);
-              else bits = before > -64 ? static_cast<uint32_t>(vm >> -before) : 0u;
+          const uint32_t page = bars.page_ok[k & 31];
+          special = key0 + kTile > ctx || page == 0u;
+          if (special) {
+            const int lim = walk.q.keys - ctx;      // drafted tokens within the page table
+            const uint64_t vm = lim >= 64 ? mask : mask & ((1ull << lim) - 1ull);
+            const int before = ctx - key0;          // cached keys from the tile's first on
+            if (before < 64) {
+              if (before > 0) okbits = ((1ull << before) - 1ull) | (vm << before);
+              else okbits = before > -64 ? vm >> -before : 0ull;
             }
-            okbits[w] = (flags >> (word >> 1)) & 1u ? bits : 0u;
+            okbits = page != 0u ? okbits >> (copy * kKeys) : 0ull;
           }
         }
         if (!SEL && !F8 && special) {
           // V of tokens that some rows do not see has to be finite (0 x NaN is NaN): zero
           // what no row sees, and what is not finite among the drafted tokens (rows that
-          // see it get it back at the end)
-          const int lv = 2 * tiles + pos_v(j, walk.count);
+          // see it get it back at the end).  Two threads share a key.
+          const int lv = 2 * tiles + pos_v(j, walk.count, C::kAhead);
           const int sv = lv % C::kStages;
           if (!warp_wait_all(&bars.kv_full[sv], (lv / C::kStages) & 1)) {
             ok = false;
             break;
           }
-          const int pos = key0 + lrow;
-          const bool dead = pos >= walk.q.keys || !((bars.pages_ok[k & 15] >> (lrow >> 6)) & 1u);
+          const int key = lrow & 63, pos = key0 + key;
+          const bool dead = pos >= walk.q.keys || bars.page_ok[k & 31] == 0u;
           if (dead || pos >= ctx) {
 #pragma unroll 4
-            for (int x = 0; x < kBlocks * 8; ++x) {
-              uint4 *const at = reinterpret_cast<uint4 *>(skv + sv * C::kTileBytes + (x >> 3) * kBlockBytes + lrow * 128 +
-                                                          ((x + lrow) & 7) * 16);
+            for (int x = (lrow >> 6) * kBlocks * 4; x < (lrow >> 6) * kBlocks * 4 + kBlocks * 4; ++x) {
+              uint4 *const at = reinterpret_cast<uint4 *>(skv + sv * C::kTileBytes + (x >> 3) * kBlockBytes + key * 128 +
+                                                          ((x + key) & 7) * 16);
               uint4 v = dead ? make_uint4(0, 0, 0, 0) : *at;
               if (!dead) {
                 uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -691,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
                   }
                 }
                 if (!changed) continue;
-                bars.nonfinite[walk.seg & 7] = walk.seg + 1;
+                bars.nonfinite[walk.seg & 31] = walk.seg + 1;
                 v = make_uint4(w[0], w[1], w[2], w[3]);
               }
               *at = v;
@@ -700,29 +720,37 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           fence_proxy_async_shared();
           __syncwarp();
         }
-        if (active)
-          softmax_tile<D, F8, kKeys>(ts, to, reinterpret_cast<const float4 *>(ssc + (k % 8) * 2 * kTile), c,
-                                     copy * kKeys, special, okbits, mine > 0, m, l);
-        if (lrow == 0) bars.two_terms[s] = special;
+        if (active) {
+          // O may be touched once the product of the tile before has completed
+          auto settled = [&]() { return warp_wait_all(&bars.pv_done[s][buf ^ 1], ((n - 1) >> 1) & 1); };
+          if (!softmax_tile<D, F8, kKeys>(tmem + kColS + 128 * s + 64 * buf + lanes, to, ssc + (k % 16) * 2 * kTile, c,
+                                          copy * kKeys, special, okbits, mine > 0, m, l, settled)) {
+            ok = false;
+            break;
+          }
+        }
+        if (lrow == 0) bars.two_terms[s][buf] = special;
         tc_fence_before();
-        warp_arrive(&bars.p_ready[s]);
-        if (F8 && lane == 0) mbar_arrive(&bars.sc_empty[k % 8]);
+        warp_arrive(&bars.p_ready[s][buf]);
+        if (F8 && lane == 0) mbar_arrive(&bars.sc_empty[k % 16]);
       }
       if (!ok) break;
       if (F8 && PAIR && !live)   // hand the scales of the tiles on
         for (int j = 0; j < walk.count; ++j) {
           const int k = tiles + j;
-          if (!warp_wait_all(&bars.sc_full[k % 8], (k / 8) & 1)) {
+          if (!warp_wait_all(&bars.sc_full[k % 16], (k / 16) & 1)) {
             ok = false;
             break;
           }
-          warp_arrive(&bars.sc_empty[k % 8]);
+          warp_arrive(&bars.sc_empty[k % 16]);
         }
       if (!ok) break;
       tiles += walk.count;
 
       // -------------------------------------------------------------- end of the segment
-      if (mine > 0 && !warp_wait_all(&bars.pv_done[s], (n - 1) & 1)) {
+      // its last two products may still be under way
+      if ((mine > 1 && !warp_wait_all(&bars.pv_done[s][n & 1], ((n - 2) >> 1) & 1)) ||
+          (mine > 0 && !warp_wait_all(&bars.pv_done[s][(n - 1) & 1], ((n - 1) >> 1) & 1))) {
         ok = false;
         break;
       }
@@ -757,7 +785,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
         m = mm;
       }
       const bool two = !PAIR && walk.count > 1;    // stream 1 has tiles
-      const bool poison = *reinterpret_cast<volatile int32_t *>(&bars.nonfinite[walk.seg & 7]) == walk.seg + 1;
+      const bool poison = *reinterpret_cast<volatile int32_t *>(&bars.nonfinite[walk.seg & 31]) == walk.seg + 1;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int hq = walk.head * G + row % G;
       const int slot = (walk.first ? 0 : 1) + 2 * static_cast<int>(blockIdx.x);
@@ -880,9 +908,10 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
         if (lane == 0) r = mbar_wait(bar, parity, limit, abort);
         return __shfl_sync(0xffffffffu, r, 0) != 0;
       };
-      // Gathering: copies of up to three tiles stay in flight while the next is issued;
+      // Gathering: copies of up to kPend tiles stay in flight while the next is issued;
       // their barriers are arrived on once the warp's copies have landed.
-      uint64_t *pend[3] = {nullptr, nullptr, nullptr}, *pend_sc[3] = {nullptr, nullptr, nullptr};
+      constexpr int kPend = 4;
+      uint64_t *pend[kPend] = {}, *pend_sc[kPend] = {};
       auto landed = [&](int x) {
         if (pend[x] == nullptr) return;
         fence_proxy_async_shared();
@@ -895,9 +924,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       };
       auto flush = [&]() {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        landed(0);
-        landed(1);
-        landed(2);
+#pragma unroll
+        for (int x = 0; x < kPend; ++x) landed(x);
       };
       // A wait that never holds back copies that have landed: the wait's end may need them.
       auto wait_flushed = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -918,7 +946,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
             for (int s = 0; s < nhalf; ++s)
               for (int b = 0; b < kBlocks; ++b)
                 for (int x = 0; x < COPIES; ++x)
-                  tma_load_3d(sq + (PAIR ? s : qb) * C::kQBytes + b * kBlockBytes + x * (kBlockBytes / COPIES), &qmap,
+                  tma_load_3d(sq + (PAIR ? s : qb) * C::kQBytes + b * kQBlockBytes + x * (kQBlockBytes / COPIES), &qmap,
                               b * 64, walk.head * G, walk.q.row0 + walk.tok0 + s * tb, &bars.q_full[qb]);
           }
           ++nq;
@@ -929,16 +957,16 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           const uint64_t mask = p.mask != nullptr ? p.mask[r] : (2ull << walk.tok0) - 1ull;
           const int32_t *const sel = a.sel + static_cast<int64_t>(r) * a.sel_k;
           const int32_t *const table = p.page_table + static_cast<int64_t>(walk.i) * p.pt_stride;
-          const int part = warp == kProducerWarp ? 0 : 64;   // the warp's keys of a tile: part + lane, part + 32 + lane
+          const int part = warp == kProducerWarp ? 0 : 32;   // the warp's keys of a tile: part + lane
           const int n0 = walk.tile0 * kTile + part + lane;
-          // A key's way: its entry of the selection (raw), its page, its slot; each step's
-          // load is issued a tile ahead of the next step, so that none is waited for.
-          auto entry = [&](int j, int x) -> int32_t {
-            const int n = n0 + j * kTile + 32 * x;
+          // A key's way: its entry of the selection, its page, its slot; each step's load is
+          // issued a tile or more ahead of the next step, so that none is waited for.
+          auto entry = [&](int j) -> int32_t {
+            const int n = n0 + j * kTile;
             return j < walk.count && n < a.sel_k ? sel[n] : -1;
           };
-          auto position = [&](int j, int x, int32_t e) -> int32_t {   // logical position, -1 for none
-            const int n = n0 + j * kTile + 32 * x;
+          auto position = [&](int j, int32_t e) -> int32_t {   // logical position, -1 for none
+            const int n = n0 + j * kTile;
             if (j >= walk.count) return -1;
             if (n < a.sel_k) return e >= 0 && e < walk.q.ctx ? e : -1;
             const int u = n - a.sel_k;
@@ -953,57 +981,44 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
             }
             return pg * kPage + pos % kPage;
           };
-          int32_t e0[2], e1[2], e2[2], pos1[2], pg1[2], pos2[2], pg2[2], cur[2], old[2] = {-1, -1}, next[2], raw3[2];
+          int32_t e[8];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            e0[x] = entry(0, x);
-            e1[x] = entry(1, x);
-            e2[x] = entry(2, x);
-            raw3[x] = entry(3, x);
+          for (int x = 0; x < 8; ++x) e[x] = entry(x);
+          int32_t pos[4], pg[4];   // tiles j .. j + 3
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            pos[x] = position(x, e[x]);
+            pg[x] = page_of(pos[x]);
           }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int32_t ps = position(0, x, e0[x]);
-            pos1[x] = position(1, x, e1[x]);
-            pos2[x] = position(2, x, e2[x]);
-            const int32_t pg0 = page_of(ps);
-            pg1[x] = page_of(pos1[x]);
-            pg2[x] = page_of(pos2[x]);
-            cur[x] = slot_of(ps, pg0);
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) next[x] = slot_of(pos1[x], pg1[x]);
-          for (int j = 0; ok && j <= walk.count; ++j) {
-            for (int what = 0; what < 2; ++what) {
-              if (what == 0 ? j >= walk.count : j == 0) continue;
+          int32_t old[C::kAhead] = {};     // slots of tiles j - 1, j - 2 ..
+          for (int j = 0; ok && j < walk.count + C::kAhead; ++j) {
+            const int32_t cur = slot_of(pos[0], pg[0]);
+            // V of tile j - kAhead, then K of tile j
+            for (int what = 1; what >= 0; --what) {
+              if (what == 0 ? j >= walk.count : j < C::kAhead) continue;
               constexpr int ring = F8 ? C::kRawStages : C::kStages;
               const int s = nload % ring;
               if (!wait_flushed(F8 ? &bars.raw_empty[s] : &bars.kv_empty[s], ((nload / ring) & 1) ^ 1)) {
                 ok = false;
                 break;
               }
+              const int32_t slot = what == 0 ? cur : old[C::kAhead - 1];
               if (what == 0) {
-                const uint32_t b0 = __ballot_sync(0xffffffffu, cur[0] >= 0), b1 = __ballot_sync(0xffffffffu, cur[1] >= 0);
-                if (lane == 0) {
-                  bars.keys_ok[nscale & 15][part / 32] = b0;
-                  bars.keys_ok[nscale & 15][part / 32 + 1] = b1;
-                }
+                const uint32_t bits = __ballot_sync(0xffffffffu, slot >= 0);
+                if (lane == 0) bars.keys_ok[nscale & 31][part / 32] = bits;
                 if constexpr (F8) {
-                  if (!wait_flushed(&bars.sc_empty[nscale % 8], ((nscale / 8) & 1) ^ 1)) {
+                  if (!wait_flushed(&bars.sc_empty[nscale % 16], ((nscale / 16) & 1) ^ 1)) {
                     ok = false;
                     break;
                   }
-                  float *const d = ssc + (nscale % 8) * 2 * kTile + part + lane;
+                  const int64_t at = slot < 0 ? 0
+                                              : (static_cast<int64_t>(slot / kPage) * Hkv + walk.head) * kPage + slot % kPage;
+                  float *const d = ssc + (nscale % 16) * 2 * kTile + part + lane;
 #pragma unroll
-                  for (int x = 0; x < 4; ++x) {   // K's and V's scales of the two keys
-                    const int32_t slot = cur[x & 1];
-                    const int64_t at = slot < 0 ? 0
-                                                : (static_cast<int64_t>(slot / kPage) * Hkv + walk.head) * kPage + slot % kPage;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                                     smem_u32(d + (x >> 1) * kTile + 32 * (x & 1))),
-                                 "l"((x < 2 ? p.cache.k_scale : p.cache.v_scale) + at), "r"(slot < 0 ? 0 : 4)
+                  for (int x = 0; x < 2; ++x)   // the key's K and V scales
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(d + x * kTile)),
+                                 "l"((x == 0 ? p.cache.k_scale : p.cache.v_scale) + at), "r"(slot < 0 ? 0 : 4)
                                  : "memory");
-                  }
                 }
               }
               // 16 bytes per lane: D / 16 or D / 8 lanes bring one key
@@ -1012,84 +1027,67 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
               const uint8_t *const cache = static_cast<const uint8_t *>(what == 0 ? p.cache.k : p.cache.v);
               uint8_t *const dst = F8 ? sraw + s * C::kRawBytes : skv + s * C::kTileBytes;
               const int ch = lane % kLanes;
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int32_t slot = what == 0 ? cur[x] : old[x];
-                const int64_t off = slot < 0 ? -1
-                                             : (static_cast<int64_t>(slot / kPage) * p.cache.page_stride +
-                                                (slot % kPage) * p.cache.token_stride +
-                                                walk.head * p.cache.head_stride) *
-                                                   (F8 ? 1 : 2);
-#pragma unroll 4
-                for (int y = 0; y < kLanes; ++y) {
-                  const int from = y * kKeysAtOnce + lane / kLanes;
-                  const int64_t o = __shfl_sync(0xffffffffu, off, from);
-                  const int key = part + 32 * x + from;
-                  uint8_t *const at = F8 ? dst + key * D + ch * 16
-                                         : dst + (ch >> 3) * kBlockBytes + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
-                  const uint8_t *const src = cache + (o < 0 ? 0 : o) + ch * 16;
-                  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at)), "l"(src),
-                               "r"(o < 0 ? 0 : 16)
-                               : "memory");
-                }
+              const int64_t off = slot < 0 ? -1
+                                           : (static_cast<int64_t>(slot / kPage) * p.cache.page_stride +
+                                              (slot % kPage) * p.cache.token_stride + walk.head * p.cache.head_stride) *
+                                                 (F8 ? 1 : 2);
+#pragma unroll 8
+              for (int y = 0; y < kLanes; ++y) {
+                const int from = y * kKeysAtOnce + lane / kLanes;
+                const int64_t o = __shfl_sync(0xffffffffu, off, from);
+                const int key = part + from;
+                uint8_t *const at = F8 ? dst + key * D + ch * 16
+                                       : dst + (ch >> 3) * kBlockBytes + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
+                const uint8_t *const src = cache + (o < 0 ? 0 : o) + ch * 16;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at)), "l"(src),
+                             "r"(o < 0 ? 0 : 16)
+                             : "memory");
               }
               asm volatile("cp.async.commit_group;" ::: "memory");
-              asm volatile("cp.async.wait_group 3;" ::: "memory");
+              asm volatile("cp.async.wait_group %0;" ::"n"(kPend) : "memory");
               landed(0);
-              pend[0] = pend[1];
-              pend_sc[0] = pend_sc[1];
-              pend[1] = pend[2];
-              pend_sc[1] = pend_sc[2];
-              pend[2] = F8 ? &bars.raw_full[s] : &bars.kv_full[s];
-              pend_sc[2] = F8 && what == 0 ? &bars.sc_full[nscale % 8] : nullptr;
+#pragma unroll
+              for (int x = 0; x + 1 < kPend; ++x) {
+                pend[x] = pend[x + 1];
+                pend_sc[x] = pend_sc[x + 1];
+              }
+              pend[kPend - 1] = F8 ? &bars.raw_full[s] : &bars.kv_full[s];
+              pend_sc[kPend - 1] = F8 && what == 0 ? &bars.sc_full[nscale % 16] : nullptr;
               ++nload;
               if (what == 0) ++nscale;
             }
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              old[x] = cur[x];
-              cur[x] = next[x];
-              next[x] = slot_of(pos2[x], pg2[x]);
-              pos2[x] = position(j + 3, x, raw3[x]);
-              pg2[x] = page_of(pos2[x]);
-              raw3[x] = entry(j + 4, x);
+            for (int x = C::kAhead - 1; x > 0; --x) old[x] = old[x - 1];
+            old[0] = cur;
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+              pos[x] = pos[x + 1];
+              pg[x] = pg[x + 1];
             }
+            pos[3] = position(j + 4, e[4]);
+            pg[3] = page_of(pos[3]);
+#pragma unroll
+            for (int x = 4; x < 7; ++x) e[x] = e[x + 1];
+            e[7] = entry(j + 8);
           }
         } else {
           // ---------------------------------------------------------- pages by TMA
-          const int npages = (walk.q.keys + kPage - 1) / kPage;
-          const int32_t *const table = p.page_table + static_cast<int64_t>(walk.i) * p.pt_stride;
-          auto fetch = [&](int j) -> int32_t {   // page ids of tiles j .. j + 15 of the segment (-2: none)
-            const int pg = (walk.tile0 + j) * 2 + lane;
-            return pg < npages ? table[pg] : -2;
-          };
-          int32_t ids = fetch(0), ids_next = -2;
-          int32_t vids0 = -1, vids1 = -1;   // pages of tile j - 1, whose V follows K of tile j
-          for (int j = 0; ok && j <= walk.count; ++j) {
-            int32_t pg[2] = {-1, -1};
-            if (j < walk.count) {
-              if ((j & 15) == 0) {
-                if (j > 0) ids = ids_next;
-                ids_next = fetch(j + 16);
-              }
-              pg[0] = __shfl_sync(0xffffffffu, ids, (j & 15) * 2);
-              pg[1] = __shfl_sync(0xffffffffu, ids, (j & 15) * 2 + 1);
-              uint32_t flags = 0;
-              for (int h = 0; h < 2; ++h) {
-                if (pg[h] >= 0 && pg[h] < p.cache.P) {
-                  flags |= 1u << h;
-                } else {
-                  if (pg[h] != -2 && lane == 0) flag_status(a.status, kStatusBadPage);
-                  pg[h] = -1;
-                }
-              }
-              if (lane == 0) bars.pages_ok[nscale & 15] = flags;
+          const int32_t *const table = p.page_table + static_cast<int64_t>(walk.i) * p.pt_stride + walk.tile0;
+          // page ids of 32 tiles of the segment at a time (tiles are pages)
+          auto fetch = [&](int j) -> int32_t { return j + lane < walk.count ? table[j + lane] : -1; };
+          int32_t ids = fetch(0), ids_next = fetch(32), ids_old = -1;
+          for (int j = 0; ok && j < walk.count + C::kAhead; ++j) {
+            if (j > 0 && (j & 31) == 0) {
+              ids_old = ids;
+              ids = ids_next;
+              ids_next = fetch(j + 32);
             }
-            // K of tile j, then V of tile j - 1
-            for (int what = 0; what < 2; ++what) {
-              if (what == 0 ? j >= walk.count : j == 0) continue;
-              const int32_t g0 = what == 0 ? pg[0] : vids0, g1 = what == 0 ? pg[1] : vids1;
-              const uint32_t npg = (g0 >= 0) + (g1 >= 0);
+            // V of tile j - kAhead, then K of tile j
+            for (int what = 1; what >= 0; --what) {
+              if (what == 0 ? j >= walk.count : j < C::kAhead) continue;
+              const int tile = what == 0 ? j : j - C::kAhead;
+              const int32_t pg = __shfl_sync(0xffffffffu, (tile >> 5) == (j >> 5) ? ids : ids_old, tile & 31);
+              const bool good = pg >= 0 && pg < p.cache.P;
               constexpr int ring = F8 ? C::kRawStages : C::kStages;
               const int s = nload % ring;
               if (!warp_wait(F8 ? &bars.raw_empty[s] : &bars.kv_empty[s], ((nload / ring) & 1) ^ 1)) {
@@ -1098,42 +1096,42 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
               }
               uint8_t *const dst = F8 ? sraw + s * C::kRawBytes : skv + s * C::kTileBytes;
               uint64_t *const full = F8 ? &bars.raw_full[s] : &bars.kv_full[s];
-              if (F8 && what == 0) {
-                const int ss = nscale % 8;
-                if (!warp_wait(&bars.sc_empty[ss], ((nscale / 8) & 1) ^ 1)) {
-                  ok = false;
-                  break;
-                }
+              if (what == 0) {
                 if (lane == 0) {
-                  mbar_arrive_expect_tx(&bars.sc_full[ss], npg * 512u);
-                  float *const d = ssc + ss * 2 * kTile;
-                  for (int h = 0; h < 2; ++h) {
-                    if (pg[h] < 0) continue;
-                    const int64_t at = (static_cast<int64_t>(pg[h]) * Hkv + walk.head) * kPage;
-                    bulk_load(d + h * kPage, p.cache.k_scale + at, 256u, &bars.sc_full[ss]);
-                    bulk_load(d + kTile + h * kPage, p.cache.v_scale + at, 256u, &bars.sc_full[ss]);
+                  bars.page_ok[nscale & 31] = good;
+                  if (!good) flag_status(a.status, kStatusBadPage);
+                }
+                if constexpr (F8) {
+                  const int ss = nscale % 16;
+                  if (!warp_wait(&bars.sc_empty[ss], ((nscale / 16) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                  }
+                  if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars.sc_full[ss], good ? 512u : 0u);
+                    if (good) {
+                      const int64_t at = (static_cast<int64_t>(pg) * Hkv + walk.head) * kPage;
+                      bulk_load(ssc + ss * 2 * kTile, p.cache.k_scale + at, 256u, &bars.sc_full[ss]);
+                      bulk_load(ssc + ss * 2 * kTile + kTile, p.cache.v_scale + at, 256u, &bars.sc_full[ss]);
+                    }
                   }
                 }
               }
               if (lane == 0) {
                 const void *const map = what == 0 ? &kmap : &vmap;
-                mbar_arrive_expect_tx(full, npg * static_cast<uint32_t>(F8 ? kPage * D : kPage * D * 2));
-                for (int h = 0; h < 2; ++h) {
-                  const int32_t g = h == 0 ? g0 : g1;
-                  if (g < 0) continue;
+                mbar_arrive_expect_tx(full, good ? static_cast<uint32_t>(F8 ? C::kRawBytes : C::kTileBytes) : 0u);
+                if (good) {
                   if constexpr (F8) {
-                    tma_load_4d(dst + h * kPage * D, map, 0, 0, walk.head, g, full);
+                    tma_load_4d(dst, map, 0, 0, walk.head, pg, full);
                   } else {
                     for (int b = 0; b < kBlocks; ++b)
-                      tma_load_4d(dst + b * kBlockBytes + h * kPage * 128, map, b * 64, 0, walk.head, g, full);
+                      tma_load_4d(dst + b * kBlockBytes, map, b * 64, 0, walk.head, pg, full);
                   }
                 }
               }
               ++nload;
               if (what == 0) ++nscale;
             }
-            vids0 = pg[0];
-            vids1 = pg[1];
           }
         }
       }
@@ -1152,85 +1150,88 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
         if (!SEL) {
           if constexpr (F8) land(bars.raw_full, C::kRawStages, nload);
           else land(bars.kv_full, C::kStages, nload);
-          if (F8) land(bars.sc_full, 8, nscale);
+          if (F8) land(bars.sc_full, 16, nscale);
         }
       }
     } else if (warp == kIssuerWarp || warp == kIssuerWarp + 1) {
       // -------------------------------------------------------------- MMA issuers
-      // Per stream: S of a tile, then (its P ready) O += P V, then the next S once that
-      // has completed, since P lies in S's columns; the other stream's MMAs fill the gap.
-      // Two row blocks over the same tiles would run in step, softmax with softmax: stream
-      // 1 starts each segment once stream 0's first softmax is done.
+      // Per stream: S of two tiles; then, tile by tile, O += P V once its P is ready, and S
+      // of the second next tile once that has completed, since it takes P's columns.
       if (lane == 0) {
         const int s = warp - kIssuerWarp;
         const uint32_t ts = tmem + kColS + 128 * s, to = tmem + kColO + 128 * s;
         const uint32_t idesc_s = umma_idesc(1u, kTile), idesc_o = umma_idesc(1u, D) | kIdescBMn;
         int loads = 0;      // K and V tiles of earlier segments
-        uint32_t n = 0;     // this stream's tiles so far
+        uint32_t ns = 0;    // this stream's S so far
+        uint32_t n = 0;     // this stream's products with V so far
         bool ok = true, any = false;
         while (ok && walk.next()) {
           const int qb = walk.seg % C::kQBufs;
           const bool live = !PAIR || s == 0 || walk.tokens > tb;   // this stream has rows
-          if (!mbar_wait(&bars.q_full[qb], (walk.seg / C::kQBufs) & 1, limit, abort) ||
-              (PAIR && s == 1 && !mbar_wait(&bars.stagger, walk.seg & 1, limit, abort))) {
+          if (!mbar_wait(&bars.q_full[qb], (walk.seg / C::kQBufs) & 1, limit, abort)) {
             ok = false;
             break;
           }
           const uint64_t qdesc = umma_desc_sw128(smem_u32(sq + (PAIR ? s : qb) * C::kQBytes));
           const int step = PAIR ? 1 : 2, j0 = PAIR ? 0 : s;
           if (j0 >= walk.count) mbar_arrive(&bars.q_empty[qb]);
-          for (int j = j0; j < walk.count; j += step) {
-            const int lk = loads + pos_k(j), lv = loads + pos_v(j, walk.count);
-            const int sk = lk % C::kStages, sv = lv % C::kStages;
-            if (!mbar_wait(&bars.kv_full[sk], (lk / C::kStages) & 1, limit, abort)) {
-              ok = false;
-              break;
-            }
-            if (!live) {   // no rows: only pass the tiles on
+          auto scores = [&](int j) -> bool {   // S of tile j
+            const int lk = loads + pos_k(j, C::kAhead);
+            const int sk = lk % C::kStages;
+            if (!mbar_wait(&bars.kv_full[sk], (lk / C::kStages) & 1, limit, abort)) return false;
+            const bool last = j + step >= walk.count;
+            if (!live) {   // no rows: only pass the tile on
               mbar_arrive(&bars.kv_empty[sk]);
-              if (j + step >= walk.count) mbar_arrive(&bars.q_empty[qb]);
-              if (!mbar_wait(&bars.kv_full[sv], (lv / C::kStages) & 1, limit, abort)) {
-                ok = false;
-                break;
-              }
-              mbar_arrive(&bars.kv_empty[sv]);
-              continue;
+              if (last) mbar_arrive(&bars.q_empty[qb]);
+              return true;
             }
             tc_fence_after();
             const uint64_t kdesc = umma_desc_sw128(smem_u32(skv + sk * C::kTileBytes));
+            const uint32_t d = ts + 64 * (ns & 1);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4;
-              umma_f16(ts, qdesc + off, kdesc + off, idesc_s, kk > 0);
-            }
-            umma_commit(&bars.s_full[s]);
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_f16(d, qdesc + (((kk >> 2) * kQBlockBytes + (kk & 3) * 32) >> 4),
+                       kdesc + (((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+            umma_commit(&bars.s_full[s][ns & 1]);
             umma_commit(&bars.kv_empty[sk]);
-            if (j + step >= walk.count) umma_commit(&bars.q_empty[qb]);
+            if (last) umma_commit(&bars.q_empty[qb]);
             any = true;
-            if (!mbar_wait(&bars.p_ready[s], n & 1, limit, abort) ||
-                (j == j0 && !mbar_wait(&bars.o_free[s], (walk.seg & 1) ^ 1, limit, abort)) ||
-                !mbar_wait(&bars.kv_full[sv], (lv / C::kStages) & 1, limit, abort)) {
-              ok = false;
-              break;
-            }
-            if (PAIR && s == 0 && j == 0) mbar_arrive(&bars.stagger);
-            tc_fence_after();
-            const uint64_t vdesc = umma_desc_mn(smem_u32(skv + sv * C::kTileBytes), kBlockBytes);
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              umma_f16_ta(to, ts + kk * 8, vdesc + ((kk * 2048) >> 4), idesc_o, j > j0 || kk > 0);
-            if (*reinterpret_cast<volatile int32_t *>(&bars.two_terms[s])) {
+            ++ns;
+            return true;
+          };
+          for (int j = j0; ok && j < walk.count && j < j0 + 2 * step; j += step) ok = scores(j);
+          for (int j = j0; ok && j < walk.count; j += step) {
+            const int lv = loads + pos_v(j, walk.count, C::kAhead);
+            const int sv = lv % C::kStages, buf = n & 1;
+            if (!live) {
+              ok = mbar_wait(&bars.kv_full[sv], (lv / C::kStages) & 1, limit, abort);
+              if (!ok) break;
+              mbar_arrive(&bars.kv_empty[sv]);
+            } else {
+              if (!mbar_wait(&bars.p_ready[s][buf], (n >> 1) & 1, limit, abort) ||
+                  (j == j0 && !mbar_wait(&bars.o_free[s], (walk.seg & 1) ^ 1, limit, abort)) ||
+                  !mbar_wait(&bars.kv_full[sv], (lv / C::kStages) & 1, limit, abort)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint64_t vdesc = umma_desc_mn(smem_u32(skv + sv * C::kTileBytes), kBlockBytes);
+              const uint32_t ta = ts + 64 * buf;
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
-                umma_f16_ta(to, ts + 64 + kk * 8, vdesc + ((kk * 2048) >> 4), idesc_o, 1u);
+                umma_f16_ta(to, ta + kk * 8, vdesc + ((kk * 2048) >> 4), idesc_o, j > j0 || kk > 0);
+              if (*reinterpret_cast<volatile int32_t *>(&bars.two_terms[s][buf])) {
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                  umma_f16_ta(to, ta + 32 + kk * 8, vdesc + ((kk * 2048) >> 4), idesc_o, 1u);
+              }
+              umma_commit(&bars.pv_done[s][buf]);
+              umma_commit(&bars.kv_empty[sv]);
+              ok = mbar_wait(&bars.pv_done[s][buf], (n >> 1) & 1, limit, abort);
+              if (!ok) break;
+              ++n;
             }
-            umma_commit(&bars.pv_done[s]);
-            umma_commit(&bars.kv_empty[sv]);
-            if (!mbar_wait(&bars.pv_done[s], n & 1, limit, abort)) {
-              ok = false;
-              break;
-            }
-            ++n;
+            if (j + 2 * step < walk.count) ok = scores(j + 2 * step);
           }
           loads += 2 * walk.count;
         }
@@ -1247,17 +1248,17 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
     if constexpr (F8) {
       // -------------------------------------------------------------- E4M3 to bf16
       if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
-      const int t = tid - kConvertWarp * 32;
-      int loads = 0, tiles = 0;
+      const int team = (warp - kConvertWarp) >> 2, t = (tid - kConvertWarp * 32) & 127;
+      int loads = 0, tiles = 0;     // of earlier segments
       uint32_t scrubs = 0;
       bool ok = true;
       while (ok && walk.next()) {
-        for (int x = 0; ok && x < 2 * walk.count; ++x, ++loads) {
-          // place x of the segment is K of tile (x + 1) / 2 or V of tile x / 2 - 1
-          const bool is_v = x == 2 * walk.count - 1 || (x > 0 && (x & 1) == 0);
-          const int j = x == 2 * walk.count - 1 ? walk.count - 1 : is_v ? x / 2 - 1 : (x + 1) / 2;
-          const int sr = loads % C::kRawStages, sk = loads % C::kStages;
-          if (!warp_wait_all(&bars.raw_full[sr], (loads / C::kRawStages) & 1)) {
+        for (int x = (loads ^ team) & 1; ok && x < 2 * walk.count; x += 2) {   // the team's loads: every second one
+          int j;
+          const bool is_v = load_at(x, walk.count, C::kAhead, j);
+          const int load = loads + x;
+          const int sr = load % C::kRawStages, sk = load % C::kStages;
+          if (!warp_wait_all(&bars.raw_full[sr], (load / C::kRawStages) & 1)) {
             ok = false;
             break;
           }
@@ -1265,58 +1266,53 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           uint8_t *const dst = skv + sk * C::kTileBytes;
           if (!SEL && is_v) {
             const int key0 = (walk.tile0 + j) * kTile;
-            const uint32_t flags = bars.pages_ok[(tiles + j) & 15];
-            if (key0 + kTile > walk.q.ctx || flags != 3u) {
+            const bool page = bars.page_ok[(tiles + j) & 31] != 0u;
+            if (key0 + kTile > walk.q.ctx || !page) {
               // V of tokens that some rows do not see has to be finite (0 x NaN is NaN): zero
               // what no row sees, and the NaN codes among the drafted tokens (rows that see
-              // them get them back at the end).  Thread t has key t.
-              const int pos = key0 + t;
-              const bool dead = pos >= walk.q.keys || !((flags >> (t >> 6)) & 1u);
+              // them get them back at the end).  Two threads share a key.
+              const int key = t & 63, pos = key0 + key;
+              const bool dead = pos >= walk.q.keys || !page;
               if (dead || pos >= walk.q.ctx) {
 #pragma unroll 4
-                for (int y = 0; y < D / 4; ++y) {
-                  uint32_t *const at = reinterpret_cast<uint32_t *>(src + t * D) + (y + t) % (D / 4);
+                for (int y = 0; y < D / 8; ++y) {
+                  uint32_t *const at = reinterpret_cast<uint32_t *>(src + key * D) + (t >> 6) * (D / 8) + (y + t) % (D / 8);
                   uint32_t w = dead ? 0u : *at;
 #pragma unroll
                   for (int z = 0; z < 32; z += 8)
                     if (((w >> z) & 0x7Fu) == 0x7Fu) {
                       w &= ~(0xFFu << z);
-                      bars.nonfinite[walk.seg & 7] = walk.seg + 1;
+                      bars.nonfinite[walk.seg & 31] = walk.seg + 1;
                     }
                   *at = w;
                 }
               }
-              warp_arrive(&bars.scrubbed);
-              if (!warp_wait_all(&bars.scrubbed, scrubs & 1)) {
+              warp_arrive(&bars.scrubbed[team]);
+              if (!warp_wait_all(&bars.scrubbed[team], scrubs & 1)) {
                 ok = false;
                 break;
               }
               ++scrubs;
             }
           }
-          constexpr int kChunks = D / 16;     // 16-byte chunks of codes per key
-          constexpr int kBatch = 4;           // chunks in flight per thread
+          constexpr int kChunks = D / 16;             // 16-byte chunks of codes per key
+          constexpr int kBatch = kTile * kChunks / 128;   // chunks per thread
           uint4 v[kBatch];
 #pragma unroll
           for (int y = 0; y < kBatch; ++y) v[y] = *reinterpret_cast<const uint4 *>(src + (y * 128 + t) * 16);
-          if (!warp_wait_all(&bars.kv_empty[sk], ((loads / C::kStages) & 1) ^ 1)) {
+          if (!warp_wait_all(&bars.kv_empty[sk], ((load / C::kStages) & 1) ^ 1)) {
             ok = false;
             break;
           }
 #pragma unroll
-          for (int y0 = 0; y0 < kChunks; y0 += kBatch) {
-#pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-              const int key = ((y0 + y) * 128 + t) / kChunks, ch = t % kChunks;
-              const uint2 a0 = e4m3x4_to_bf16(v[y].x), a1 = e4m3x4_to_bf16(v[y].y), a2 = e4m3x4_to_bf16(v[y].z),
-                          a3 = e4m3x4_to_bf16(v[y].w);
-              if (y0 + kBatch < kChunks)   // the next batch's load takes the freed registers
-                v[y] = *reinterpret_cast<const uint4 *>(src + ((y0 + kBatch + y) * 128 + t) * 16);
-              uint8_t *const row = dst + (ch >> 2) * kBlockBytes + key * 128;
-              const int c0 = (ch & 3) * 2;
-              *reinterpret_cast<uint4 *>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-              *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
-            }
+          for (int y = 0; y < kBatch; ++y) {
+            const int key = (y * 128 + t) / kChunks, ch = t % kChunks;
+            const uint2 a0 = e4m3x4_to_bf16(v[y].x), a1 = e4m3x4_to_bf16(v[y].y), a2 = e4m3x4_to_bf16(v[y].z),
+                        a3 = e4m3x4_to_bf16(v[y].w);
+            uint8_t *const row = dst + (ch >> 2) * kBlockBytes + key * 128;
+            const int c0 = (ch & 3) * 2;
+            *reinterpret_cast<uint4 *>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+            *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
           }
           fence_proxy_async_shared();
           __syncwarp();
@@ -1325,6 +1321,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
             mbar_arrive(&bars.raw_empty[sr]);
           }
         }
+        loads += 2 * walk.count;
         tiles += walk.count;
       }
       if (!ok) give_up();
