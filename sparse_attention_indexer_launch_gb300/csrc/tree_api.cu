@@ -106,9 +106,12 @@ StateLayout state_layout(const idx_tree_problem *p, int32_t sel_k) {
   return L;
 }
 
-// K or V as a 4-D tensor [P][Hkv][64][D].  bf16: boxes of 64 dimensions in the 128-byte
-// swizzle the tensor core reads; E4M3: whole rows, converted in shared memory.
-idx_status cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const idx_kv_cache *c, void *base, CUtensorMap *map) {
+// K or V as a 4-D tensor [P][Hkv][64][D].  What the tensor core reads is swizzled by rows
+// of 128 bytes (bf16: boxes of 64 dimensions; E4M3 K of 128 dimensions) or 64 bytes (E4M3 K
+// of 64 dimensions); E4M3 V is converted in shared memory and comes as it is.  L2 fetches
+// no more around a head's row than the row, unless its tokens lie next to each other.
+idx_status cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const idx_kv_cache *c, bool is_v, CUtensorMap *map) {
+  void *const base = is_v ? c->v : c->k;
   const bool f8 = c->kv_dtype == IDX_KV_E4M3;
   const cuuint64_t e = f8 ? 1 : 2;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->D), IDX_PAGE, static_cast<cuuint64_t>(c->Hkv),
@@ -116,10 +119,16 @@ idx_status cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const idx_kv_cach
   const cuuint64_t strides[3] = {c->token_stride * e, c->head_stride * e, c->page_stride * e};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(f8 ? c->D : 64), IDX_PAGE, 1, 1};
   const cuuint32_t one[4] = {1, 1, 1, 1};
+  const CUtensorMapSwizzle swizzle = !f8 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : is_v ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                     : c->D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const cuuint64_t run = c->token_stride == c->D ? 256 : c->D * e;   // bytes of a head next to each other
+  const CUtensorMapL2promotion promote = run >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                         : run >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                      : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   const CUresult r = encode(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims,
                             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                            swizzle, promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? IDX_OK : IDX_ECUDA;
 }
 
@@ -137,8 +146,8 @@ idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, 
   if (st != IDX_OK) return st;
   const Shape s = shape_of(p, sel_k);
   const int D = p->cache.D, G = p->Hq / p->cache.Hkv;
-  CUtensorMap qm, km{}, vm{};
-  {
+  CUtensorMap qm{}, km{}, vm{};
+  if (p->cache.kv_dtype == IDX_KV_BF16) {   // beside an E4M3 cache Q is split as it is loaded
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p->Hq), static_cast<cuuint64_t>(p->R)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(p->q_row_stride) * 2};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(s.block_tokens)};
@@ -149,8 +158,8 @@ idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, 
       return IDX_ECUDA;
   }
   if (sel == nullptr) {   // selected positions are gathered by plain loads
-    st = cache_map(encode, &p->cache, p->cache.k, &km);
-    if (st == IDX_OK) st = cache_map(encode, &p->cache, p->cache.v, &vm);
+    st = cache_map(encode, &p->cache, false, &km);
+    if (st == IDX_OK) st = cache_map(encode, &p->cache, true, &vm);
     if (st != IDX_OK) return st;
   }
   uint8_t *const b = static_cast<uint8_t *>(state);

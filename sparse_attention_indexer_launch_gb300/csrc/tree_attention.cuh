@@ -10,6 +10,13 @@
 // K comes from shared memory with its dimensions contiguous, V as the transposed
 // (MN-major) operand straight from the same page layout, so neither is rearranged.
 //
+// E4M3 keys feed the tensor core as they are: a row of Q, scaled by a power of two to
+// at most 448, is split into two E4M3 terms whose sum it is (exactly, for elements down
+// to 2^-9 of the row's largest; to 2^-17 of that below), and S is the sum of both
+// terms' products.  P needs bf16's range (two E4M3 terms would drop what lies below
+// 2^-18 of the largest, which adds up over a long cache), so V is converted to bf16 in
+// shared memory, exactly.
+//
 // Work: an item is (request, key/value head, block of tokens) with its tiles in
 // position order; the launch's tiles, in item order, are dealt out as one even,
 // contiguous share per CTA (one CTA per SM).  A CTA that holds a whole item writes
@@ -53,43 +60,49 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;
 
 // ---------------------------------------------------------------------------- roles
-// warps 0-3 and 4-7: softmax of streams 0 and 1; 8: TMA producer; 9 and 10: MMA
-// issuers of streams 0 and 1; 11: idle, or with 8 the gatherers of selected positions;
-// 12-19 with an E4M3 cache: conversion to bf16, two teams of four on alternate loads.
-constexpr int kProducerWarp = 8, kIssuerWarp = 9, kGatherWarp = 11, kConvertWarp = 12;
-
-constexpr int kMaxStages = 16;
+// warps 0-3 and 4-7: softmax of streams 0 and 1; 8 and 11: loads of K and of V (by TMA,
+// or gathering selected positions); 9 and 10: MMA issuers of streams 0 and 1; 12-19 with
+// an E4M3 cache: the split of Q, and V to bf16, two teams of four on alternate loads.
+constexpr int kKWarp = 8, kIssuerWarp = 9, kVWarp = 11, kConvertWarp = 12;
+constexpr int kMaxStages = 8;
 
 // COPIES: copies of the row block in the tile's rows (4, 2 or 1); PAIR: two row blocks.
 template <int D, bool F8, int COPIES, bool PAIR, bool SEL>
 struct Cfg {
-  static constexpr int kTileBytes = kTile * D * 2;       // a K or V tile as bf16
-  static constexpr int kRawBytes = kTile * D;            // ... as E4M3 bytes
+  static constexpr int kLoad = 128 / D;                  // pages per load of K or V
+  static constexpr int kLoadBytes = kLoad * kTile * D * 2;   // as bf16
+  static constexpr int kRawBytes = kLoad * kTile * D;        // as E4M3 bytes
+  static constexpr int kKBytes = F8 ? kRawBytes : kLoadBytes;
+  // Q of a row block: bf16, or the two E4M3 terms
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kQBufs = PAIR || F8 ? 1 : 2;
+  static constexpr int kQBufs = PAIR ? 1 : 2;
   static constexpr int kQTotal = kQBytes * (PAIR ? 2 : kQBufs);
-  // bf16: 128 KB of tiles; E4M3: raw tiles as memory allows and 96 KB of converted ones
-  static constexpr int kStages = F8 ? (D == 128 ? 6 : 12) : (D == 128 ? 8 : 16);
-  static constexpr int kRawStages = !F8 ? 0 : D == 64 ? 16 : PAIR ? 6 : COPIES > 1 ? 8 : 10;
-  static constexpr int kScaleStages = F8 ? 16 : 0;
+  static constexpr int kKStages = F8 ? (D == 128 && COPIES > 1 ? 4 : 6) : (D == 128 ? 4 : 5);
+  static constexpr int kVStages = F8 ? 4 : (D == 128 ? 4 : 5);    // as bf16
+  static constexpr int kRawStages = F8 ? (D == 128 ? 4 : 6) : 0;  // V as E4M3
+  // A stage always belongs to the same team: were its loads to alternate, a team could
+  // come to it again before the other team's load in between, and the parity of its
+  // barrier would pass for the one it waits for.
+  static_assert(!F8 || (kVStages % 2 == 0 && kRawStages % 2 == 0), "stages per converting team");
+  static constexpr int kScaleStages = F8 ? 8 : 0;
+  static constexpr int kScaleFloats = 2 * kLoad * kTile;   // of a load: K's, then V's
   static constexpr int kRedBytes = COPIES > 1 ? 2 * kRows * 16 * 4 : 0;   // the copies' sum: 16 columns a stream
   static constexpr int kThreads = 32 * (F8 ? kConvertWarp + 8 : kConvertWarp);
-  // K tiles loaded ahead of the first V: two per stream
-  static constexpr int kAhead = PAIR ? 2 : 4;
-  static_assert(kStages >= kAhead + 2 && kStages <= kMaxStages && kRawStages <= kMaxStages, "rings");
   // Registers per thread after the roles part, where a softmax thread holds up to 64
   // scores.  The shares add up to no more than the launch's threads x registers.
   static constexpr bool kShareRegs = F8;
   static constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsOther = 64;
   static_assert(!F8 || 256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch, "register shares");
-  static constexpr int kDynamic = 1024 + kQTotal + kStages * kTileBytes + kRawStages * kRawBytes +
-                                  kScaleStages * 2 * kTile * 4 + kRedBytes;
+  static constexpr int kDynamic = 1024 + kQTotal + kKStages * kKBytes + kVStages * kLoadBytes + kRawStages * kRawBytes +
+                                  kScaleStages * kScaleFloats * 4 + kRedBytes;
 };
 
+template <bool PAIR>
 struct Barriers {
-  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages];
+  uint64_t v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t raw_full[kMaxStages], raw_empty[kMaxStages];
-  uint64_t sc_full[16], sc_empty[16];
+  uint64_t sc_full[kMaxStages], sc_empty[kMaxStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];   // [stream][buffer]
   uint64_t o_free[2], drain[2], stats[2], red_full[2], red_free[2], scrubbed[2];
@@ -97,10 +110,14 @@ struct Barriers {
   int abort;
   int32_t two_terms[2][2];         // P of [stream][buffer] has a low term
   int32_t start_req, start_base;   // the share's first request, and the tiles before it
-  uint32_t page_ok[32];            // dense: the page of the CTA's tile k % 32 was loaded
-  uint32_t keys_ok[32][2];         // selected: bit per key of tile k % 32
+  uint32_t page_ok[64], vpage_ok[64];   // dense: the page of tile k % 64 of the CTA was loaded (K, V)
+  uint32_t keys_ok[64][2];         // selected: bit per key of tile k % 64
   int32_t nonfinite[32];           // segment number + 1 whose drafted tokens' V held NaN or infinity
-  float row_m[2][2][kRows], row_l[2][2][kRows];   // [segment parity][stream][row]
+  float row_m[PAIR ? 1 : 2][2][PAIR ? 1 : kRows], row_l[PAIR ? 1 : 2][2][PAIR ? 1 : kRows];   // [segment parity][stream][row]
+  // E4M3: 1 / the row's power of two, [segment % 4][row block][row].  Q of a segment is split
+  // at most three segments before the softmax has begun with it: S of the second next one
+  // takes the place of P of this one.
+  float q_scale[4][PAIR ? 2 : 1][kRows];
   int32_t warp_sums[20];
 };
 
@@ -152,6 +169,16 @@ __device__ __forceinline__ uint64_t umma_desc_mn(uint32_t smem_addr, uint32_t bl
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
 }
+// Descriptor of a K-major operand with rows of 64 bytes in the 64-byte swizzle.
+__device__ __forceinline__ uint64_t umma_desc_sw64(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>(512u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(4u) << 61;
+  return d;
+}
 constexpr uint32_t kIdescBMn = 1u << 16;   // operand B is MN-major
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, int y, int z, uint64_t *bar) {
@@ -197,6 +224,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// Two floats to their nearest E4M3 codes (low byte: a).
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
+}
+__device__ __forceinline__ float2 e4m3x2_value(uint32_t x) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x), __NV_E4M3)));
 }
 // Four E4M3 codes to four bf16 values (exact: every E4M3 value is one).
 __device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t x) {
@@ -305,25 +339,6 @@ struct Walk {
   }
 };
 
-// The loads of a segment of n tiles: K of the first `ahead` tiles, then V0, K, V1, K ...
-// Their places in that order, and the load at place x.
-__device__ __forceinline__ int pos_k(int j, int ahead) { return j < ahead ? j : 2 * j - ahead + 1; }
-__device__ __forceinline__ int pos_v(int j, int n, int ahead) { return min(n, j + ahead) + j; }
-__device__ __forceinline__ bool load_at(int x, int n, int ahead, int &j) {   // true: V of tile j, false: K
-  const int lead = min(n, ahead);
-  if (x < lead) {
-    j = x;
-    return false;
-  }
-  const int y = x - lead, both = 2 * (n - lead);
-  if (y >= both) {
-    j = n - lead + (y - both);
-    return true;
-  }
-  j = (y >> 1) + (y & 1 ? lead : 0);
-  return (y & 1) == 0;
-}
-
 // ---------------------------------------------------------------------------- softmax
 // Moves the row's maximum to `top` where that passes it by more than kLazy, and scales l
 // and O (D columns at to, once settled() says that the product before has completed)
@@ -353,15 +368,15 @@ __device__ __forceinline__ bool raise_maximum(uint32_t to, float top, bool has_o
 
 // One row's keys of a tile (N of the 64, from column n0): S (columns at ts) to P in the
 // same columns, the row's maximum m and sum l, and O (D columns at to) when the maximum
-// moves.  special: only the keys of ok (a bit per key) are visible.  sc: the tile's K
-// scales, then its V scales.
+// moves.  special: only the keys of ok (a bit per key) are visible.  ks: the tile's K
+// scales; vs: its V scales.
 //
 // P is rounded to bf16 for the product with V.  Over the 64 or more keys of a full tile
 // the roundings average out below the output's own; the few keys of a special tile do
 // not, so there P is kept in two bf16 terms, high in columns 0-31 and low in 32-63, and
 // the product runs over both.
 template <int D, bool F8, int N, typename F>
-__device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const float *sc, float c, int n0, bool special,
+__device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const float *sk, const float *sv, float c, int n0, bool special,
                                              uint64_t ok, bool has_o, float &m, float &l, F settled) {
   constexpr int kW = N < 32 ? N : 32;        // columns per register group
   uint32_t x[N / kW][kW];
@@ -370,8 +385,8 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const flo
     if constexpr (kW == 32) tmem_ld32(ts + n0 + 32 * w, x[w]);
     else tmem_ld16(ts + n0, x[w]);
   }
-  const float4 *const ks = reinterpret_cast<const float4 *>(sc + n0);
-  const float2 *const vs = reinterpret_cast<const float2 *>(sc + kTile + n0);
+  const float4 *const ks = reinterpret_cast<const float4 *>(sk + n0);
+  const float2 *const vs = reinterpret_cast<const float2 *>(sv + n0);
   tmem_wait_ld();
 #pragma unroll
   for (int w = 0; w < N / kW; ++w) {
@@ -472,34 +487,37 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
                           const __grid_constant__ CUtensorMap vmap, const TreeAttnArgs a) {
   using C = Cfg<D, F8, COPIES, PAIR, SEL>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ Barriers bars;
+  __shared__ Barriers<PAIR> bars;
   uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
   uint8_t *const sq = smem;
-  uint8_t *const skv = sq + C::kQTotal;
-  uint8_t *const sraw = skv + C::kStages * C::kTileBytes;
-  float *const ssc = reinterpret_cast<float *>(sraw + C::kRawStages * C::kRawBytes);   // [stage][K 64, V 64]
-  float *const sred = ssc + C::kScaleStages * 2 * kTile;                                // [stream][row][16]
+  uint8_t *const sk = sq + C::kQTotal;
+  uint8_t *const sv = sk + C::kKStages * C::kKBytes;
+  uint8_t *const sraw = sv + C::kVStages * C::kLoadBytes;
+  float *const ssc = reinterpret_cast<float *>(sraw + C::kRawStages * C::kRawBytes);   // [stage][K, V]
+  float *const sred = ssc + C::kScaleStages * C::kScaleFloats;                          // [stream][row][16]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const idx_tree_problem &p = a.p;
   const int Hkv = p.cache.Hkv;
   const int G = p.Hq / Hkv;
   const int tb = PAIR ? a.item_tokens / 2 : a.item_tokens;   // tokens of a row block
-  constexpr int kBlocks = D / 64;            // 64-dimension blocks of an operand tile
-  constexpr int kBlockBytes = kTile * 128, kQBlockBytes = kRows * 128;
+  constexpr int kBlocks = D / 64;            // 64-dimension blocks of a bf16 operand
+  constexpr int kLoad = C::kLoad;            // tiles per load
+  constexpr int kBlockBytes = kLoad * kTile * 128, kQBlockBytes = kRows * 128;
   grid_dependency_trigger();                 // the combine kernel's CTAs may take free SMs
 
   if (tid == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
-      // filled by four converting warps, the two gathering ones or one TMA thread
-      mbar_init(&bars.kv_full[s], F8 ? 4 : SEL ? 2 : 1);
-      mbar_init(&bars.kv_empty[s], PAIR ? 2 : 1);
-      mbar_init(&bars.raw_full[s], SEL ? 2 : 1);
+      mbar_init(&bars.k_full[s], 1);
+      mbar_init(&bars.k_empty[s], PAIR ? 2 : 1);
+      mbar_init(&bars.v_full[s], F8 ? 4 : 1);    // by a team's four warps, or the loading one
+      mbar_init(&bars.v_empty[s], PAIR ? 2 : 1);
+      mbar_init(&bars.raw_full[s], 1);
       mbar_init(&bars.raw_empty[s], 4);
-      mbar_init(&bars.sc_full[s], SEL ? 2 : 1);
+      mbar_init(&bars.sc_full[s], 2);            // K's and V's scales
       mbar_init(&bars.sc_empty[s], PAIR ? 8 : 4);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars.q_full[s], 1);
+      mbar_init(&bars.q_full[s], F8 ? 8 : 1);
       mbar_init(&bars.q_empty[s], 2);
       for (int b = 0; b < 2; ++b) {
         mbar_init(&bars.s_full[s][b], 1);
@@ -521,8 +539,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
     tmem_alloc(&bars.tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if (tid == kProducerWarp * 32) {
-    prefetch_tensormap(&qmap);
+  if (tid == kKWarp * 32) {
+    if (!F8) prefetch_tensormap(&qmap);
     if (!SEL) {
       prefetch_tensormap(&kmap);
       prefetch_tensormap(&vmap);
@@ -633,6 +651,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
     const float c = p.scale * kLog2e;
     const int step = PAIR ? 1 : 2, j0 = PAIR ? 0 : s;
     int tiles = 0;      // tiles of earlier segments
+    int loads = 0;      // loads of earlier segments
     uint32_t n = 0;     // this stream's tiles so far
     uint32_t nred = 0;  // sums of copies so far
     bool ok = true;
@@ -648,24 +667,27 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       const int ctx = walk.q.ctx;
       float m = -INFINITY, l = 0.0f;
       int mine = 0;      // this stream's tiles in the segment
-      for (int j = j0; live && j < walk.count; j += step, ++n, ++mine) {
-        const int k = tiles + j;
+      float cs = c;      // of the row's scores
+      for (int jj = j0; ok && live && jj * kLoad < walk.count; jj += step)
+      for (int j = jj * kLoad; j < min(walk.count, (jj + 1) * kLoad); ++j, ++n, ++mine) {
+        const int k = tiles + j, ld = loads + jj, sub = j - jj * kLoad;
         const int key0 = (walk.tile0 + j) * kTile;
         const int buf = n & 1;
-        if ((F8 && !warp_wait_all(&bars.sc_full[k % 16], (k / 16) & 1)) ||
+        if ((F8 && sub == 0 && !warp_wait_all(&bars.sc_full[ld % 8], (ld / 8) & 1)) ||
             !warp_wait_all(&bars.s_full[s][buf], (n >> 1) & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        if (F8 && mine == 0) cs = c * bars.q_scale[walk.seg & 3][PAIR ? s : 0][row];
         uint64_t okbits = ~0ull;   // the copy's keys of the tile that the row sees
         bool special;
         if (SEL) {
-          const uint32_t k0 = bars.keys_ok[k & 31][0], k1 = bars.keys_ok[k & 31][1];
+          const uint32_t k0 = bars.keys_ok[k & 63][0], k1 = bars.keys_ok[k & 63][1];
           special = (k0 & k1) != ~0u;
           if (special) okbits = (static_cast<uint64_t>(k1) << 32 | k0) >> (copy * kKeys);
         } else {
-          const uint32_t page = bars.page_ok[k & 31];
+          const uint32_t page = bars.page_ok[k & 63];
           special = key0 + kTile > ctx || page == 0u;
           if (special) {
             const int lim = walk.q.keys - ctx;      // drafted tokens within the page table
@@ -682,19 +704,18 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           // V of tokens that some rows do not see has to be finite (0 x NaN is NaN): zero
           // what no row sees, and what is not finite among the drafted tokens (rows that
           // see it get it back at the end).  Two threads share a key.
-          const int lv = 2 * tiles + pos_v(j, walk.count, C::kAhead);
-          const int sv = lv % C::kStages;
-          if (!warp_wait_all(&bars.kv_full[sv], (lv / C::kStages) & 1)) {
+          const int sl = ld % C::kVStages;
+          if (!warp_wait_all(&bars.v_full[sl], (ld / C::kVStages) & 1)) {
             ok = false;
             break;
           }
           const int key = lrow & 63, pos = key0 + key;
-          const bool dead = pos >= walk.q.keys || bars.page_ok[k & 31] == 0u;
+          const bool dead = pos >= walk.q.keys || bars.page_ok[k & 63] == 0u;
           if (dead || pos >= ctx) {
 #pragma unroll 4
             for (int x = (lrow >> 6) * kBlocks * 4; x < (lrow >> 6) * kBlocks * 4 + kBlocks * 4; ++x) {
-              uint4 *const at = reinterpret_cast<uint4 *>(skv + sv * C::kTileBytes + (x >> 3) * kBlockBytes + key * 128 +
-                                                          ((x + key) & 7) * 16);
+              uint4 *const at = reinterpret_cast<uint4 *>(sv + sl * C::kLoadBytes + (x >> 3) * kBlockBytes +
+                                                          (sub * kTile + key) * 128 + ((x + key) & 7) * 16);
               uint4 v = dead ? make_uint4(0, 0, 0, 0) : *at;
               if (!dead) {
                 uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -723,7 +744,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
         if (active) {
           // O may be touched once the product of the tile before has completed
           auto settled = [&]() { return warp_wait_all(&bars.pv_done[s][buf ^ 1], ((n - 1) >> 1) & 1); };
-          if (!softmax_tile<D, F8, kKeys>(tmem + kColS + 128 * s + 64 * buf + lanes, to, ssc + (k % 16) * 2 * kTile, c,
+          const float *const ks = ssc + (ld % 8) * C::kScaleFloats + sub * kTile;
+          if (!softmax_tile<D, F8, kKeys>(tmem + kColS + 128 * s + 64 * buf + lanes, to, ks, ks + kLoad * kTile, cs,
                                           copy * kKeys, special, okbits, mine > 0, m, l, settled)) {
             ok = false;
             break;
@@ -732,20 +754,21 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
         if (lrow == 0) bars.two_terms[s][buf] = special;
         tc_fence_before();
         warp_arrive(&bars.p_ready[s][buf]);
-        if (F8 && lane == 0) mbar_arrive(&bars.sc_empty[k % 16]);
+        if (F8 && lane == 0 && (sub == kLoad - 1 || j + 1 == walk.count)) mbar_arrive(&bars.sc_empty[ld % 8]);
       }
       if (!ok) break;
       if (F8 && PAIR && !live)   // hand the scales of the tiles on
-        for (int j = 0; j < walk.count; ++j) {
-          const int k = tiles + j;
-          if (!warp_wait_all(&bars.sc_full[k % 16], (k / 16) & 1)) {
+        for (int jj = 0; jj * kLoad < walk.count; ++jj) {
+          const int ld = loads + jj;
+          if (!warp_wait_all(&bars.sc_full[ld % 8], (ld / 8) & 1)) {
             ok = false;
             break;
           }
-          warp_arrive(&bars.sc_empty[k % 16]);
+          warp_arrive(&bars.sc_empty[ld % 8]);
         }
       if (!ok) break;
       tiles += walk.count;
+      loads += (walk.count + kLoad - 1) / kLoad;
 
       // -------------------------------------------------------------- end of the segment
       // its last two products may still be under way
@@ -757,7 +780,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       tc_fence_after();
       if (l != l) m = INFINITY;   // a NaN among the visible scores takes the whole row, in every join
       float f0 = 1.0f, f1 = 0.0f;
-      if (!PAIR) {
+      if constexpr (!PAIR) {
         // the row's maximum and sum over both streams and all copies; this thread's O
         // (of stream 0 and of stream 1) scales by f0 and f1
         const int sp = walk.seg & 1;
@@ -897,18 +920,29 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
     if (!ok) give_up();
   } else if (warp < kConvertWarp) {
     if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
-    if (warp == kProducerWarp || (SEL && warp == kGatherWarp)) {
-      // -------------------------------------------------------------- producer
-      int nload = 0;      // K and V tiles so far
-      int nscale = 0;     // tiles with scales so far
-      int nq = 0;         // Q loads so far
+    if (warp == kKWarp || warp == kVWarp) {
+      // -------------------------------------------------------------- loads
+      // K's warp also brings a bf16 Q; each brings its own scales.
+      const bool is_v = warp == kVWarp;
+      const int stages = is_v ? (F8 ? C::kRawStages : C::kVStages) : C::kKStages;
+      const int bytes = is_v ? (F8 ? C::kRawBytes : C::kLoadBytes) : C::kKBytes;
+      uint64_t *const full = is_v ? (F8 ? bars.raw_full : bars.v_full) : bars.k_full;
+      uint64_t *const empty = is_v ? (F8 ? bars.raw_empty : bars.v_empty) : bars.k_empty;
+      uint8_t *const ring = is_v ? (F8 ? sraw : sv) : sk;
+      const float *const scales = is_v ? p.cache.v_scale : p.cache.k_scale;
+      float *const sscale = ssc + (is_v ? kLoad * kTile : 0);
+      int stage = 0;          // of the next load
+      uint32_t phase = 1;     // its empty barrier's
+      int nload = 0;          // loads so far
+      int tiles = 0;          // tiles of earlier segments
+      int nq = 0;             // Q loads so far
       bool ok = true;
       auto warp_wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         int r = 1;
         if (lane == 0) r = mbar_wait(bar, parity, limit, abort);
         return __shfl_sync(0xffffffffu, r, 0) != 0;
       };
-      // Gathering: copies of up to kPend tiles stay in flight while the next is issued;
+      // Gathering: copies of up to kPend loads stay in flight while the next is issued;
       // their barriers are arrived on once the warp's copies have landed.
       constexpr int kPend = 4;
       uint64_t *pend[kPend] = {}, *pend_sc[kPend] = {};
@@ -933,9 +967,10 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
         return warp_wait(bar, parity);
       };
       while (ok && walk.next()) {
-        // Q of the segment, once for every copy
-        const int qb = walk.seg % C::kQBufs;
-        if (warp == kProducerWarp) {
+        const int nloads = (walk.count + kLoad - 1) / kLoad;
+        if (!F8 && !is_v) {
+          // Q of the segment, once for every copy
+          const int qb = walk.seg % C::kQBufs;
           if (!wait_flushed(&bars.q_empty[qb], ((walk.seg / C::kQBufs) & 1) ^ 1)) {
             ok = false;
             break;
@@ -951,189 +986,181 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           }
           ++nq;
         }
+        const int32_t *const table = p.page_table + static_cast<int64_t>(walk.i) * p.pt_stride;
         if constexpr (SEL) {
           // ---------------------------------------------------------- gathering
           const int r = walk.q.row0 + walk.tok0;
           const uint64_t mask = p.mask != nullptr ? p.mask[r] : (2ull << walk.tok0) - 1ull;
           const int32_t *const sel = a.sel + static_cast<int64_t>(r) * a.sel_k;
-          const int32_t *const table = p.page_table + static_cast<int64_t>(walk.i) * p.pt_stride;
-          const int part = warp == kProducerWarp ? 0 : 32;   // the warp's keys of a tile: part + lane
-          const int n0 = walk.tile0 * kTile + part + lane;
+          const int n0 = walk.tile0 * kTile + lane, nend = n0 - lane + walk.count * kTile;
+          constexpr int kPer = 2 * kLoad;      // keys of a load per lane: lane, lane + 32 ..
           // A key's way: its entry of the selection, its page, its slot; each step's load is
-          // issued a tile or more ahead of the next step, so that none is waited for.
-          auto entry = [&](int j) -> int32_t {
-            const int n = n0 + j * kTile;
-            return j < walk.count && n < a.sel_k ? sel[n] : -1;
+          // issued a load or more ahead of the next step, so that none is waited for.
+          auto entry = [&](int jj, int x) -> int32_t {
+            const int n = n0 + (jj * kPer + x) * 32;
+            return n < nend && n < a.sel_k ? sel[n] : -1;
           };
-          auto position = [&](int j, int32_t e) -> int32_t {   // logical position, -1 for none
-            const int n = n0 + j * kTile;
-            if (j >= walk.count) return -1;
+          auto position = [&](int jj, int x, int32_t e) -> int32_t {   // logical position, -1 for none
+            const int n = n0 + (jj * kPer + x) * 32;
+            if (n >= nend) return -1;
             if (n < a.sel_k) return e >= 0 && e < walk.q.ctx ? e : -1;
             const int u = n - a.sel_k;
             return u < walk.q.tokens && ((mask >> u) & 1ull) && walk.q.ctx + u < walk.q.keys ? walk.q.ctx + u : -1;
           };
           auto page_of = [&](int32_t pos) -> int32_t { return pos >= 0 ? table[pos / kPage] : -1; };
-          auto slot_of = [&](int32_t pos, int32_t pg) -> int32_t {    // page * 64 + token, -1 for none
-            if (pos < 0) return -1;
-            if (pg < 0 || pg >= p.cache.P) {
-              flag_status(a.status, kStatusBadPage);
-              return -1;
-            }
-            return pg * kPage + pos % kPage;
-          };
-          int32_t e[8];
+          int32_t pos[2][kPer], pg[2][kPer], e[3][kPer];   // loads jj, jj + 1; jj + 2 .. jj + 4
 #pragma unroll
-          for (int x = 0; x < 8; ++x) e[x] = entry(x);
-          int32_t pos[4], pg[4];   // tiles j .. j + 3
+          for (int x = 0; x < kPer; ++x) {
+            pos[0][x] = entry(0, x);
+            pos[1][x] = entry(1, x);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            pos[x] = position(x, e[x]);
-            pg[x] = page_of(pos[x]);
+            for (int y = 0; y < 3; ++y) e[y][x] = entry(2 + y, x);
           }
-          int32_t old[C::kAhead] = {};     // slots of tiles j - 1, j - 2 ..
-          for (int j = 0; ok && j < walk.count + C::kAhead; ++j) {
-            const int32_t cur = slot_of(pos[0], pg[0]);
-            // V of tile j - kAhead, then K of tile j
-            for (int what = 1; what >= 0; --what) {
-              if (what == 0 ? j >= walk.count : j < C::kAhead) continue;
-              constexpr int ring = F8 ? C::kRawStages : C::kStages;
-              const int s = nload % ring;
-              if (!wait_flushed(F8 ? &bars.raw_empty[s] : &bars.kv_empty[s], ((nload / ring) & 1) ^ 1)) {
-                ok = false;
-                break;
-              }
-              const int32_t slot = what == 0 ? cur : old[C::kAhead - 1];
-              if (what == 0) {
-                const uint32_t bits = __ballot_sync(0xffffffffu, slot >= 0);
-                if (lane == 0) bars.keys_ok[nscale & 31][part / 32] = bits;
-                if constexpr (F8) {
-                  if (!wait_flushed(&bars.sc_empty[nscale % 16], ((nscale / 16) & 1) ^ 1)) {
-                    ok = false;
-                    break;
-                  }
-                  const int64_t at = slot < 0 ? 0
-                                              : (static_cast<int64_t>(slot / kPage) * Hkv + walk.head) * kPage + slot % kPage;
-                  float *const d = ssc + (nscale % 16) * 2 * kTile + part + lane;
 #pragma unroll
-                  for (int x = 0; x < 2; ++x)   // the key's K and V scales
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(d + x * kTile)),
-                                 "l"((x == 0 ? p.cache.k_scale : p.cache.v_scale) + at), "r"(slot < 0 ? 0 : 4)
-                                 : "memory");
-                }
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+              pos[y][x] = position(y, x, pos[y][x]);
+              pg[y][x] = page_of(pos[y][x]);
+            }
+          for (int jj = 0; jj < nloads; ++jj) {
+            if (!wait_flushed(&empty[stage], phase)) {
+              ok = false;
+              break;
+            }
+            if (F8 && !wait_flushed(&bars.sc_empty[nload % 8], ((nload / 8) & 1) ^ 1)) {
+              ok = false;
+              break;
+            }
+            uint8_t *const dst = ring + stage * bytes;
+            float *const dsc = sscale + (nload % 8) * C::kScaleFloats;
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+              int32_t slot = -1;           // page * 64 + token
+              if (pos[0][x] >= 0) {
+                if (pg[0][x] >= 0 && pg[0][x] < p.cache.P) slot = pg[0][x] * kPage + pos[0][x] % kPage;
+                else flag_status(a.status, kStatusBadPage);
               }
-              // 16 bytes per lane: D / 16 or D / 8 lanes bring one key
-              constexpr int kLanes = F8 ? D / 16 : D / 8;
-              constexpr int kKeysAtOnce = 32 / kLanes;
-              const uint8_t *const cache = static_cast<const uint8_t *>(what == 0 ? p.cache.k : p.cache.v);
-              uint8_t *const dst = F8 ? sraw + s * C::kRawBytes : skv + s * C::kTileBytes;
-              const int ch = lane % kLanes;
+              const uint32_t bits = __ballot_sync(0xffffffffu, slot >= 0);
+              if (!is_v && lane == 0) bars.keys_ok[(tiles + jj * kLoad + x / 2) & 63][x & 1] = bits;
               const int64_t off = slot < 0 ? -1
                                            : (static_cast<int64_t>(slot / kPage) * p.cache.page_stride +
                                               (slot % kPage) * p.cache.token_stride + walk.head * p.cache.head_stride) *
                                                  (F8 ? 1 : 2);
-#pragma unroll 8
+              if constexpr (F8) {
+                const int64_t at = slot < 0 ? 0
+                                            : (static_cast<int64_t>(slot / kPage) * Hkv + walk.head) * kPage + slot % kPage;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dsc + x * 32 + lane)),
+                             "l"(scales + at), "r"(slot < 0 ? 0 : 4)
+                             : "memory");
+              }
+              // 16 bytes per lane: D / 16 or D / 8 lanes bring one key
+              constexpr int kLanes = F8 ? D / 16 : D / 8;
+              constexpr int kKeysAtOnce = 32 / kLanes;
+              const uint8_t *const cache = static_cast<const uint8_t *>(is_v ? p.cache.v : p.cache.k);
+              const int ch = lane % kLanes;
+#pragma unroll
               for (int y = 0; y < kLanes; ++y) {
                 const int from = y * kKeysAtOnce + lane / kLanes;
                 const int64_t o = __shfl_sync(0xffffffffu, off, from);
-                const int key = part + from;
-                uint8_t *const at = F8 ? dst + key * D + ch * 16
-                                       : dst + (ch >> 3) * kBlockBytes + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
+                const int key = x * 32 + from;
+                uint32_t at;   // bf16: blocks of 128-byte rows, swizzled; E4M3 K: rows of D, swizzled; V: rows of D
+                if (!F8) at = (ch >> 3) * kBlockBytes + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
+                else if (is_v) at = key * D + ch * 16;
+                else at = key * D + ((D == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4);
                 const uint8_t *const src = cache + (o < 0 ? 0 : o) + ch * 16;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at)), "l"(src),
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst) + at), "l"(src),
                              "r"(o < 0 ? 0 : 16)
                              : "memory");
               }
-              asm volatile("cp.async.commit_group;" ::: "memory");
-              asm volatile("cp.async.wait_group %0;" ::"n"(kPend) : "memory");
-              landed(0);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(kPend) : "memory");
+            landed(0);
 #pragma unroll
-              for (int x = 0; x + 1 < kPend; ++x) {
-                pend[x] = pend[x + 1];
-                pend_sc[x] = pend_sc[x + 1];
-              }
-              pend[kPend - 1] = F8 ? &bars.raw_full[s] : &bars.kv_full[s];
-              pend_sc[kPend - 1] = F8 && what == 0 ? &bars.sc_full[nscale % 16] : nullptr;
-              ++nload;
-              if (what == 0) ++nscale;
+            for (int x = 0; x + 1 < kPend; ++x) {
+              pend[x] = pend[x + 1];
+              pend_sc[x] = pend_sc[x + 1];
+            }
+            pend[kPend - 1] = &full[stage];
+            pend_sc[kPend - 1] = F8 ? &bars.sc_full[nload % 8] : nullptr;
+            ++nload;
+            if (++stage == stages) {
+              stage = 0;
+              phase ^= 1u;
             }
 #pragma unroll
-            for (int x = C::kAhead - 1; x > 0; --x) old[x] = old[x - 1];
-            old[0] = cur;
-#pragma unroll
-            for (int x = 0; x < 3; ++x) {
-              pos[x] = pos[x + 1];
-              pg[x] = pg[x + 1];
+            for (int x = 0; x < kPer; ++x) {
+              pos[0][x] = pos[1][x];
+              pg[0][x] = pg[1][x];
+              pos[1][x] = position(jj + 2, x, e[0][x]);
+              pg[1][x] = page_of(pos[1][x]);
+              e[0][x] = e[1][x];
+              e[1][x] = e[2][x];
+              e[2][x] = entry(jj + 5, x);
             }
-            pos[3] = position(j + 4, e[4]);
-            pg[3] = page_of(pos[3]);
-#pragma unroll
-            for (int x = 4; x < 7; ++x) e[x] = e[x + 1];
-            e[7] = entry(j + 8);
           }
         } else {
           // ---------------------------------------------------------- pages by TMA
-          const int32_t *const table = p.page_table + static_cast<int64_t>(walk.i) * p.pt_stride + walk.tile0;
+          const void *const map = is_v ? &vmap : &kmap;
+          uint32_t *const oks = is_v ? bars.vpage_ok : bars.page_ok;
           // page ids of 32 tiles of the segment at a time (tiles are pages)
-          auto fetch = [&](int j) -> int32_t { return j + lane < walk.count ? table[j + lane] : -1; };
-          int32_t ids = fetch(0), ids_next = fetch(32), ids_old = -1;
-          for (int j = 0; ok && j < walk.count + C::kAhead; ++j) {
+          auto fetch = [&](int j) -> int32_t { return j + lane < walk.count ? table[walk.tile0 + j + lane] : -2; };
+          int32_t ids = fetch(0), ids_next = fetch(32);
+          for (int jj = 0; jj < nloads; ++jj) {
+            const int j = jj * kLoad;
             if (j > 0 && (j & 31) == 0) {
-              ids_old = ids;
               ids = ids_next;
               ids_next = fetch(j + 32);
             }
-            // V of tile j - kAhead, then K of tile j
-            for (int what = 1; what >= 0; --what) {
-              if (what == 0 ? j >= walk.count : j < C::kAhead) continue;
-              const int tile = what == 0 ? j : j - C::kAhead;
-              const int32_t pg = __shfl_sync(0xffffffffu, (tile >> 5) == (j >> 5) ? ids : ids_old, tile & 31);
-              const bool good = pg >= 0 && pg < p.cache.P;
-              constexpr int ring = F8 ? C::kRawStages : C::kStages;
-              const int s = nload % ring;
-              if (!warp_wait(F8 ? &bars.raw_empty[s] : &bars.kv_empty[s], ((nload / ring) & 1) ^ 1)) {
-                ok = false;
-                break;
+            int32_t pg[kLoad];
+            uint32_t good = 0;
+#pragma unroll
+            for (int x = 0; x < kLoad; ++x) {
+              pg[x] = __shfl_sync(0xffffffffu, ids, (j + x) & 31);
+              good += pg[x] >= 0 && pg[x] < p.cache.P;
+            }
+            if (!warp_wait(&empty[stage], phase) ||
+                (F8 && !warp_wait(&bars.sc_empty[nload % 8], ((nload / 8) & 1) ^ 1))) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              uint8_t *const dst = ring + stage * bytes;
+              if (good == kLoad) {
+                mbar_arrive_expect_tx(&full[stage], bytes);
+              } else {
+                mbar_arrive_expect_tx(&full[stage], good * static_cast<uint32_t>(bytes / kLoad));
               }
-              uint8_t *const dst = F8 ? sraw + s * C::kRawBytes : skv + s * C::kTileBytes;
-              uint64_t *const full = F8 ? &bars.raw_full[s] : &bars.kv_full[s];
-              if (what == 0) {
-                if (lane == 0) {
-                  bars.page_ok[nscale & 31] = good;
-                  if (!good) flag_status(a.status, kStatusBadPage);
+              if (F8) mbar_arrive_expect_tx(&bars.sc_full[nload % 8], good * 256u);
+#pragma unroll
+              for (int x = 0; x < kLoad; ++x) {
+                const bool there = pg[x] >= 0 && pg[x] < p.cache.P;
+                oks[(tiles + j + x) & 63] = there;
+                if (!there) {
+                  if (pg[x] != -2) flag_status(a.status, kStatusBadPage);
+                  continue;
                 }
                 if constexpr (F8) {
-                  const int ss = nscale % 16;
-                  if (!warp_wait(&bars.sc_empty[ss], ((nscale / 16) & 1) ^ 1)) {
-                    ok = false;
-                    break;
-                  }
-                  if (lane == 0) {
-                    mbar_arrive_expect_tx(&bars.sc_full[ss], good ? 512u : 0u);
-                    if (good) {
-                      const int64_t at = (static_cast<int64_t>(pg) * Hkv + walk.head) * kPage;
-                      bulk_load(ssc + ss * 2 * kTile, p.cache.k_scale + at, 256u, &bars.sc_full[ss]);
-                      bulk_load(ssc + ss * 2 * kTile + kTile, p.cache.v_scale + at, 256u, &bars.sc_full[ss]);
-                    }
-                  }
+                  tma_load_4d(dst + x * (kTile * D), map, 0, 0, walk.head, pg[x], &full[stage]);
+                  bulk_load(sscale + (nload % 8) * C::kScaleFloats + x * kTile,
+                            scales + (static_cast<int64_t>(pg[x]) * Hkv + walk.head) * kPage, 256u,
+                            &bars.sc_full[nload % 8]);
+                } else {
+#pragma unroll
+                  for (int b = 0; b < kBlocks; ++b)
+                    tma_load_4d(dst + b * kBlockBytes + x * (kTile * 128), map, b * 64, 0, walk.head, pg[x], &full[stage]);
                 }
               }
-              if (lane == 0) {
-                const void *const map = what == 0 ? &kmap : &vmap;
-                mbar_arrive_expect_tx(full, good ? static_cast<uint32_t>(F8 ? C::kRawBytes : C::kTileBytes) : 0u);
-                if (good) {
-                  if constexpr (F8) {
-                    tma_load_4d(dst, map, 0, 0, walk.head, pg, full);
-                  } else {
-                    for (int b = 0; b < kBlocks; ++b)
-                      tma_load_4d(dst + b * kBlockBytes, map, b * 64, 0, walk.head, pg, full);
-                  }
-                }
-              }
-              ++nload;
-              if (what == 0) ++nscale;
+            }
+            ++nload;
+            if (++stage == stages) {
+              stage = 0;
+              phase ^= 1u;
             }
           }
         }
+        tiles += walk.count;
       }
       if (SEL) flush();
       if (!ok && lane == 0) give_up();
@@ -1146,11 +1173,10 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
             if (!mbar_wait(&bar[s], (last / n) & 1, limit, &never)) flag_status(a.status, kStatusTimeout);
           }
         };
-        if (warp == kProducerWarp) land(bars.q_full, C::kQBufs, nq);
+        land(bars.q_full, C::kQBufs, nq);
         if (!SEL) {
-          if constexpr (F8) land(bars.raw_full, C::kRawStages, nload);
-          else land(bars.kv_full, C::kStages, nload);
-          if (F8) land(bars.sc_full, 16, nscale);
+          land(full, stages, nload);
+          if (F8) land(bars.sc_full, 8, nload);
         }
       }
     } else if (warp == kIssuerWarp || warp == kIssuerWarp + 1) {
@@ -1160,80 +1186,118 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       if (lane == 0) {
         const int s = warp - kIssuerWarp;
         const uint32_t ts = tmem + kColS + 128 * s, to = tmem + kColO + 128 * s;
-        const uint32_t idesc_s = umma_idesc(1u, kTile), idesc_o = umma_idesc(1u, D) | kIdescBMn;
-        int loads = 0;      // K and V tiles of earlier segments
+        const uint32_t idesc_s = umma_idesc(F8 ? 0u : 1u, kTile), idesc_o = umma_idesc(1u, D) | kIdescBMn;
+        int kstage = 0, vstage = 0;          // of the next load of K and of V
+        uint32_t kphase = 0, vphase = 0;
         uint32_t ns = 0;    // this stream's S so far
         uint32_t n = 0;     // this stream's products with V so far
         bool ok = true, any = false;
+        auto skip = [&](int &stage, uint32_t &phase, int stages, int by) {
+          stage += by;
+          while (stage >= stages) {
+            stage -= stages;
+            phase ^= 1u;
+          }
+        };
+        const int step = PAIR ? 1 : 2, j0 = PAIR ? 0 : s;
         while (ok && walk.next()) {
           const int qb = walk.seg % C::kQBufs;
+          const int nloads = (walk.count + kLoad - 1) / kLoad;
           const bool live = !PAIR || s == 0 || walk.tokens > tb;   // this stream has rows
           if (!mbar_wait(&bars.q_full[qb], (walk.seg / C::kQBufs) & 1, limit, abort)) {
             ok = false;
             break;
           }
-          const uint64_t qdesc = umma_desc_sw128(smem_u32(sq + (PAIR ? s : qb) * C::kQBytes));
-          const int step = PAIR ? 1 : 2, j0 = PAIR ? 0 : s;
-          if (j0 >= walk.count) mbar_arrive(&bars.q_empty[qb]);
-          auto scores = [&](int j) -> bool {   // S of tile j
-            const int lk = loads + pos_k(j, C::kAhead);
-            const int sk = lk % C::kStages;
-            if (!mbar_wait(&bars.kv_full[sk], (lk / C::kStages) & 1, limit, abort)) return false;
-            const bool last = j + step >= walk.count;
-            if (!live) {   // no rows: only pass the tile on
-              mbar_arrive(&bars.kv_empty[sk]);
-              if (last) mbar_arrive(&bars.q_empty[qb]);
-              return true;
+          if (j0 >= nloads) mbar_arrive(&bars.q_empty[qb]);
+          // the stream's first load, and what lies before the next segment's
+          skip(kstage, kphase, C::kKStages, j0);
+          skip(vstage, vphase, C::kVStages, j0);
+          if (!live) {   // no rows: only pass the loads on
+            for (int jj = 0; ok && jj < nloads; ++jj) {
+              ok = mbar_wait(&bars.k_full[kstage], kphase, limit, abort) &&
+                   mbar_wait(&bars.v_full[vstage], vphase, limit, abort);
+              if (!ok) break;
+              mbar_arrive(&bars.k_empty[kstage]);
+              mbar_arrive(&bars.v_empty[vstage]);
+              skip(kstage, kphase, C::kKStages, 1);
+              skip(vstage, vphase, C::kVStages, 1);
             }
+            if (ok) mbar_arrive(&bars.q_empty[qb]);
+            continue;
+          }
+          const uint32_t qaddr = smem_u32(sq + (PAIR ? s : qb) * C::kQBytes);
+          int jk = j0, subk = 0;               // the next S
+          auto scores = [&]() -> bool {
+            if (subk == 0 && !mbar_wait(&bars.k_full[kstage], kphase, limit, abort)) return false;
             tc_fence_after();
-            const uint64_t kdesc = umma_desc_sw128(smem_u32(skv + sk * C::kTileBytes));
             const uint32_t d = ts + 64 * (ns & 1);
+            const uint32_t kaddr = smem_u32(sk + kstage * C::kKBytes);
+            if constexpr (F8) {
+              // both terms of Q over the same keys: D = 128: 128-byte rows, the terms 16 KB
+              // apart; D = 64: the terms side by side in 128-byte rows, keys in 64-byte rows
+              const uint64_t qdesc = umma_desc_sw128(qaddr);
+              const uint64_t kdesc = D == 128 ? umma_desc_sw128(kaddr) : umma_desc_sw64(kaddr + subk * kTile * 64);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_f16(d, qdesc + (((kk >> 2) * kQBlockBytes + (kk & 3) * 32) >> 4),
-                       kdesc + (((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+              for (int kk = 0; kk < 2 * D / 32; ++kk) {
+                const int term = kk / (D / 32), x = kk % (D / 32);
+                umma_f8(d, qdesc + ((term * (D == 128 ? kQBlockBytes : 64) + x * 32) >> 4), kdesc + ((x * 32) >> 4),
+                        idesc_s, kk > 0);
+              }
+            } else {
+              const uint64_t qdesc = umma_desc_sw128(qaddr), kdesc = umma_desc_sw128(kaddr + subk * kTile * 128);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma_f16(d, qdesc + (((kk >> 2) * kQBlockBytes + (kk & 3) * 32) >> 4),
+                         kdesc + (((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+            }
             umma_commit(&bars.s_full[s][ns & 1]);
-            umma_commit(&bars.kv_empty[sk]);
-            if (last) umma_commit(&bars.q_empty[qb]);
             any = true;
             ++ns;
+            if (++subk == kLoad || jk * kLoad + subk == walk.count) {   // the load's last tile
+              umma_commit(&bars.k_empty[kstage]);
+              subk = 0;
+              jk += step;
+              skip(kstage, kphase, C::kKStages, jk < nloads ? step : 0);
+              if (jk >= nloads) umma_commit(&bars.q_empty[qb]);
+            }
             return true;
           };
-          for (int j = j0; ok && j < walk.count && j < j0 + 2 * step; j += step) ok = scores(j);
-          for (int j = j0; ok && j < walk.count; j += step) {
-            const int lv = loads + pos_v(j, walk.count, C::kAhead);
-            const int sv = lv % C::kStages, buf = n & 1;
-            if (!live) {
-              ok = mbar_wait(&bars.kv_full[sv], (lv / C::kStages) & 1, limit, abort);
-              if (!ok) break;
-              mbar_arrive(&bars.kv_empty[sv]);
-            } else {
+          if (jk < nloads) ok = scores();
+          if (ok && jk < nloads) ok = scores();
+          for (int jj = j0; ok && jj < nloads; jj += step) {
+            const int end = min(walk.count, (jj + 1) * kLoad);
+            for (int j = jj * kLoad; j < end; ++j, ++n) {
+              const int buf = n & 1, sub = j - jj * kLoad;
               if (!mbar_wait(&bars.p_ready[s][buf], (n >> 1) & 1, limit, abort) ||
-                  (j == j0 && !mbar_wait(&bars.o_free[s], (walk.seg & 1) ^ 1, limit, abort)) ||
-                  !mbar_wait(&bars.kv_full[sv], (lv / C::kStages) & 1, limit, abort)) {
+                  (j == j0 * kLoad && !mbar_wait(&bars.o_free[s], (walk.seg & 1) ^ 1, limit, abort)) ||
+                  (sub == 0 && !mbar_wait(&bars.v_full[vstage], vphase, limit, abort))) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-              const uint64_t vdesc = umma_desc_mn(smem_u32(skv + sv * C::kTileBytes), kBlockBytes);
+              const uint64_t vdesc = umma_desc_mn(smem_u32(sv + vstage * C::kLoadBytes + sub * kTile * 128), kBlockBytes);
               const uint32_t ta = ts + 64 * buf;
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
-                umma_f16_ta(to, ta + kk * 8, vdesc + ((kk * 2048) >> 4), idesc_o, j > j0 || kk > 0);
+                umma_f16_ta(to, ta + kk * 8, vdesc + ((kk * 2048) >> 4), idesc_o, j > j0 * kLoad || kk > 0);
               if (*reinterpret_cast<volatile int32_t *>(&bars.two_terms[s][buf])) {
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
                   umma_f16_ta(to, ta + 32 + kk * 8, vdesc + ((kk * 2048) >> 4), idesc_o, 1u);
               }
               umma_commit(&bars.pv_done[s][buf]);
-              umma_commit(&bars.kv_empty[sv]);
-              ok = mbar_wait(&bars.pv_done[s][buf], (n >> 1) & 1, limit, abort);
+              if (j + 1 == end) {
+                umma_commit(&bars.v_empty[vstage]);
+                skip(vstage, vphase, C::kVStages, jj + step < nloads ? step : 0);
+              }
+              ok = mbar_wait(&bars.pv_done[s][buf], (n >> 1) & 1, limit, abort) && (jk >= nloads || scores());
               if (!ok) break;
-              ++n;
             }
-            if (j + 2 * step < walk.count) ok = scores(j + 2 * step);
           }
-          loads += 2 * walk.count;
+          // to the next segment's first load
+          const int left = j0 < nloads ? (nloads - j0 - 1) % step + 1 : 0;
+          skip(kstage, kphase, C::kKStages, left);
+          skip(vstage, vphase, C::kVStages, left);
         }
         if (!ok) {
           give_up();
@@ -1246,37 +1310,125 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
     }
   } else {
     if constexpr (F8) {
-      // -------------------------------------------------------------- E4M3 to bf16
+      // -------------------------------------------------------------- E4M3: Q split, V to bf16
       if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
       const int team = (warp - kConvertWarp) >> 2, t = (tid - kConvertWarp * 32) & 127;
-      int loads = 0, tiles = 0;     // of earlier segments
+      Walk qwalk(a, t0, t1, req0, base0);     // the segment whose Q is next
+      // Q of qwalk's segment: two threads per row (of every row block), each with half of
+      // its dimensions.  The copies and both terms go to shared memory, rows without a
+      // token as zeros.
+      auto split_q = [&]() -> bool {
+        constexpr int kBlockRows = kRows / COPIES;
+        const int qb = qwalk.seg % C::kQBufs;
+        if (!warp_wait_all(&bars.q_empty[qb], ((qwalk.seg / C::kQBufs) & 1) ^ 1)) return false;
+        const int id = tid - kConvertWarp * 32, row = id >> 1, half = id & 1;
+#pragma unroll 1
+        for (int blk = 0; blk < (PAIR && qwalk.tokens > tb ? 2 : 1); ++blk) {
+          if (row >= kBlockRows) break;
+          const int nrow = min(tb, qwalk.tokens - blk * tb) * G;
+          uint4 v[D / 16];
+          const uint16_t *const src = static_cast<const uint16_t *>(p.q) +
+                                      static_cast<int64_t>(qwalk.q.row0 + qwalk.tok0 + blk * tb + row / G) * p.q_row_stride +
+                                      static_cast<int64_t>(qwalk.head * G + row % G) * D + half * (D / 2);
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            v[x] = row < nrow ? __ldg(reinterpret_cast<const uint4 *>(src) + x) : make_uint4(0, 0, 0, 0);
+          // the row's largest exponent (of the finite elements: NaN and infinity stay what they are)
+          uint32_t top = 0;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t lo = w[y] & 0x7FFFu, hi = (w[y] >> 16) & 0x7FFFu;
+              if (lo < 0x7F80u) top = max(top, lo);
+              if (hi < 0x7F80u) top = max(top, hi);
+            }
+          }
+          top = max(top, __shfl_xor_sync(__activemask(), top, 1));
+          // 2^e takes it to (224, 448]; rows below 2^-112 stop at 2^120
+          const int e = min(((top & 0x7Fu) <= 0x60u ? 8 : 7) - (static_cast<int>(top >> 7) - 127), 120);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          if (half == 0)
+#pragma unroll
+            for (int x = 0; x < COPIES; ++x)
+              bars.q_scale[qwalk.seg & 3][PAIR ? blk : 0][row + x * kBlockRows] =
+                  __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          uint8_t *const dst = sq + (PAIR ? blk : qb) * C::kQBytes;
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {       // 16 elements: 16 bytes of each term
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t a0 = y < 2 ? (y == 0 ? v[2 * x].x : v[2 * x].z) : (y == 2 ? v[2 * x + 1].x : v[2 * x + 1].z);
+              const uint32_t a1 = y < 2 ? (y == 0 ? v[2 * x].y : v[2 * x].w) : (y == 2 ? v[2 * x + 1].y : v[2 * x + 1].w);
+              const float f0 = __uint_as_float(a0 << 16) * up, f1 = __uint_as_float(a0 & 0xFFFF0000u) * up;
+              const float f2 = __uint_as_float(a1 << 16) * up, f3 = __uint_as_float(a1 & 0xFFFF0000u) * up;
+              const uint32_t h0 = e4m3x2(f0, f1), h1 = e4m3x2(f2, f3);
+              const float2 g0 = e4m3x2_value(h0), g1 = e4m3x2_value(h1);
+              hi[y] = h0 | h1 << 16;
+              // (an infinity, which the first term cuts to 448, becomes NaN here)
+              lo[y] = e4m3x2(fmaf(f0, 0.0f, f0 - g0.x), fmaf(f1, 0.0f, f1 - g0.y)) |
+                      e4m3x2(fmaf(f2, 0.0f, f2 - g1.x), fmaf(f3, 0.0f, f3 - g1.y)) << 16;
+            }
+            const int ch = half * (D / 32) + x;    // 16-byte chunk of the term's row
+#pragma unroll
+            for (int z = 0; z < COPIES; ++z) {
+              const int rr = row + z * kBlockRows;
+              uint8_t *const at = dst + rr * 128;
+              if constexpr (D == 128) {
+                *reinterpret_cast<uint4 *>(at + ((ch ^ (rr & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(at + kQBlockBytes + ((ch ^ (rr & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              } else {
+                *reinterpret_cast<uint4 *>(at + ((ch ^ (rr & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(at + (((ch + 4) ^ (rr & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              }
+            }
+          }
+        }
+        fence_proxy_async_shared();
+        warp_arrive(&bars.q_full[qb]);
+        return true;
+      };
+      int nload = 0, tiles = 0;     // of earlier segments
       uint32_t scrubs = 0;
-      bool ok = true;
+      bool ok = true, more = qwalk.next();
+      if (more) {
+        ok = split_q();
+        more = qwalk.next();
+      }
       while (ok && walk.next()) {
-        for (int x = (loads ^ team) & 1; ok && x < 2 * walk.count; x += 2) {   // the team's loads: every second one
-          int j;
-          const bool is_v = load_at(x, walk.count, C::kAhead, j);
-          const int load = loads + x;
-          const int sr = load % C::kRawStages, sk = load % C::kStages;
-          if (!warp_wait_all(&bars.raw_full[sr], (load / C::kRawStages) & 1)) {
+        const int nloads = (walk.count + kLoad - 1) / kLoad;
+        if (!PAIR && more) {       // the next segment's, while this one runs
+          ok = split_q();
+          more = ok && qwalk.next();
+        }
+        for (int jj = (nload ^ team) & 1; ok && jj < nloads; jj += 2) {   // the team's loads: every second one
+          const int ld = nload + jj;
+          const int sr = ld % C::kRawStages, sl = ld % C::kVStages;
+          if (!warp_wait_all(&bars.raw_full[sr], (ld / C::kRawStages) & 1)) {
             ok = false;
             break;
           }
           uint8_t *const src = sraw + sr * C::kRawBytes;
-          uint8_t *const dst = skv + sk * C::kTileBytes;
-          if (!SEL && is_v) {
-            const int key0 = (walk.tile0 + j) * kTile;
-            const bool page = bars.page_ok[(tiles + j) & 31] != 0u;
-            if (key0 + kTile > walk.q.ctx || !page) {
+          uint8_t *const dst = sv + sl * C::kLoadBytes;
+          if (!SEL) {
+            bool special = (walk.tile0 + (jj + 1) * kLoad) * kTile > walk.q.ctx;
+#pragma unroll
+            for (int x = 0; x < kLoad; ++x) special |= bars.vpage_ok[(tiles + jj * kLoad + x) & 63] == 0u;
+            if (special) {
               // V of tokens that some rows do not see has to be finite (0 x NaN is NaN): zero
               // what no row sees, and the NaN codes among the drafted tokens (rows that see
-              // them get them back at the end).  Two threads share a key.
-              const int key = t & 63, pos = key0 + key;
-              const bool dead = pos >= walk.q.keys || !page;
+              // them get them back at the end).  128 / kLoad / 64 threads share a key.
+              constexpr int kShare = 2 / kLoad, kWords = D / 4 / kShare;
+              const int key = t % (kLoad * kTile), part = t / (kLoad * kTile);
+              const int pos = (walk.tile0 + jj * kLoad) * kTile + key;
+              const int tile = jj * kLoad + key / kTile;
+              const bool dead = pos >= walk.q.keys || tile >= walk.count || bars.vpage_ok[(tiles + tile) & 63] == 0u;
               if (dead || pos >= walk.q.ctx) {
 #pragma unroll 4
-                for (int y = 0; y < D / 8; ++y) {
-                  uint32_t *const at = reinterpret_cast<uint32_t *>(src + key * D) + (t >> 6) * (D / 8) + (y + t) % (D / 8);
+                for (int y = 0; y < kWords; ++y) {
+                  uint32_t *const at = reinterpret_cast<uint32_t *>(src + key * D) + part * kWords + (y + t) % kWords;
                   uint32_t w = dead ? 0u : *at;
 #pragma unroll
                   for (int z = 0; z < 32; z += 8)
@@ -1296,16 +1448,15 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
             }
           }
           constexpr int kChunks = D / 16;             // 16-byte chunks of codes per key
-          constexpr int kBatch = kTile * kChunks / 128;   // chunks per thread
-          uint4 v[kBatch];
+          uint4 v[4];
 #pragma unroll
-          for (int y = 0; y < kBatch; ++y) v[y] = *reinterpret_cast<const uint4 *>(src + (y * 128 + t) * 16);
-          if (!warp_wait_all(&bars.kv_empty[sk], ((load / C::kStages) & 1) ^ 1)) {
+          for (int y = 0; y < 4; ++y) v[y] = *reinterpret_cast<const uint4 *>(src + (y * 128 + t) * 16);
+          if (!warp_wait_all(&bars.v_empty[sl], ((ld / C::kVStages) & 1) ^ 1)) {
             ok = false;
             break;
           }
 #pragma unroll
-          for (int y = 0; y < kBatch; ++y) {
+          for (int y = 0; y < 4; ++y) {
             const int key = (y * 128 + t) / kChunks, ch = t % kChunks;
             const uint2 a0 = e4m3x4_to_bf16(v[y].x), a1 = e4m3x4_to_bf16(v[y].y), a2 = e4m3x4_to_bf16(v[y].z),
                         a3 = e4m3x4_to_bf16(v[y].w);
@@ -1317,12 +1468,16 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&bars.kv_full[sk]);
+            mbar_arrive(&bars.v_full[sl]);
             mbar_arrive(&bars.raw_empty[sr]);
           }
         }
-        loads += 2 * walk.count;
+        nload += nloads;
         tiles += walk.count;
+        if (PAIR && ok && more) {   // one buffer: once this segment's scores are done
+          ok = split_q();
+          more = ok && qwalk.next();
+        }
       }
       if (!ok) give_up();
     }
