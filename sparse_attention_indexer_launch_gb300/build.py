@@ -17,8 +17,9 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libidx.so")
 SOURCES = ["api.cu", "prep.cu", "score.cu", "select.cu", "top1.cu", "patch.cu", "merge.cu", "tree_api.cu",
-           "tree_tables.cu", "write_kv.cu", "tree_attention_bf16_64.cu", "tree_attention_bf16_128.cu",
-           "tree_attention_e4m3_64.cu", "tree_attention_e4m3_128.cu"]
+           "tree_tables.cu", "write_kv.cu", "tree_few_bf16_64.cu", "tree_few_bf16_128.cu", "tree_few_e4m3_64.cu",
+           "tree_few_e4m3_128.cu", "tree_many_bf16_64.cu", "tree_many_bf16_128.cu", "tree_many_e4m3_64.cu",
+           "tree_many_e4m3_128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", INCLUDE, "-I", CSRC]

@@ -139,7 +139,8 @@ struct TreeAttnArgs {
   uint64_t wait_limit_ns;
   int32_t item_tokens;     // drafted tokens of an item
   int32_t pair;            // its rows are two blocks of item_tokens / 2 tokens
-  int32_t copies;          // of an item's rows in the tile's 128
+  int32_t tile;            // keys per tile
+  int32_t rows;            // rows that the few-row kernel provides for, 0: the many-row kernel
 };
 constexpr int kTreeMaxCtas = 160;   // shares of an attention launch, at most
 
@@ -149,8 +150,8 @@ cudaError_t launch_write_kv(const WriteKvArgs &a, cudaStream_t stream);
 // the cache as [P][Hkv][64][D], box one head's page (64 dimensions of it for bf16).
 using TreeAttnLaunch = cudaError_t(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km,
                                    const CUtensorMap &vm, int num_ctas, cudaStream_t stream);
-TreeAttnLaunch launch_tree_attention_bf16_64, launch_tree_attention_bf16_128, launch_tree_attention_e4m3_64,
-    launch_tree_attention_e4m3_128;
+TreeAttnLaunch launch_tree_few_bf16_64, launch_tree_few_bf16_128, launch_tree_few_e4m3_64, launch_tree_few_e4m3_128,
+    launch_tree_many_bf16_64, launch_tree_many_bf16_128, launch_tree_many_e4m3_64, launch_tree_many_e4m3_128;
 
 cudaError_t launch_prep(const PrepArgs &a, cudaStream_t stream);
 cudaError_t launch_score(const CUtensorMap &kmap, const ScoreArgs &a, int kv_dtype, bool batched, int num_ctas,

@@ -44,21 +44,28 @@ idx_status check_cache(const idx_kv_cache *c) {
   return IDX_OK;
 }
 
-// The launch's shape.  Few rows are copied to fill the tensor-core tile, so that every
-// softmax warp has work (tree_attention.cuh); more than 128 rows go through a CTA in
-// pairs of blocks that share every K and V tile.
+// The launch's shape: up to 64 rows of a request and key/value head (selected: of a token)
+// go to the few-row kernel, up to 128 to the many-row kernel in one block, more in pairs of
+// blocks that share every K and V tile.
 struct Shape {
+  int rows;           // the few-row kernel's N, or 0
+  int tile;           // keys
   int block_tokens;   // tokens of a row block
-  int copies;
   bool pair;
 };
 Shape shape_of(const idx_tree_problem *p, int32_t sel_k) {
   Shape s{};
   const int G = p->Hq / p->cache.Hkv;
-  const int rows = (sel_k > 0 ? 1 : p->max_new) * G;   // of a request and key/value head (selected: of a token)
-  s.pair = rows > kMaxGroup / G * G;
-  s.copies = s.pair ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
-  s.block_tokens = sel_k > 0 ? 1 : kMaxGroup / s.copies / G;
+  const int rows = (sel_k > 0 ? 1 : p->max_new) * G;
+  if (rows <= 64) {
+    s.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    s.tile = 128;
+    s.block_tokens = sel_k > 0 ? 1 : s.rows / G;
+  } else {
+    s.tile = IDX_PAGE;
+    s.block_tokens = sel_k > 0 ? 1 : kMaxGroup / G;
+    s.pair = rows > s.block_tokens * G;
+  }
   return s;
 }
 
@@ -66,7 +73,7 @@ Shape shape_of(const idx_tree_problem *p, int32_t sel_k) {
 bool tiles_fit(const idx_tree_problem *p, int32_t sel_k) {
   const Shape s = shape_of(p, sel_k);
   const int64_t item = s.pair ? 2 * s.block_tokens : s.block_tokens;
-  const int64_t tiles = ((sel_k > 0 ? sel_k : p->max_ctx) + static_cast<int64_t>(p->max_new) + IDX_PAGE - 1) / IDX_PAGE;
+  const int64_t tiles = ((sel_k > 0 ? sel_k : p->max_ctx) + static_cast<int64_t>(p->max_new) + s.tile - 1) / s.tile;
   const int64_t blocks = (p->max_new + item - 1) / item;
   const int64_t items = (static_cast<int64_t>(p->Q) * blocks < p->R ? static_cast<int64_t>(p->Q) * blocks : p->R) * p->cache.Hkv;
   return items * tiles <= INT32_MAX;
@@ -174,12 +181,16 @@ idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, 
   a.part_o = reinterpret_cast<float *>(b + L.o);
   a.wait_limit_ns = idx::device_wait_limit_ns();
   a.pair = s.pair;
-  a.copies = s.copies;
+  a.tile = s.tile;
+  a.rows = s.rows;
   a.item_tokens = s.pair ? 2 * s.block_tokens : s.block_tokens;
   const int ctas = sms < idx::kTreeMaxCtas ? sms : idx::kTreeMaxCtas;
   const bool f8 = p->cache.kv_dtype == IDX_KV_E4M3;
-  idx::TreeAttnLaunch &launch = f8 ? (D == 64 ? idx::launch_tree_attention_e4m3_64 : idx::launch_tree_attention_e4m3_128)
-                                   : (D == 64 ? idx::launch_tree_attention_bf16_64 : idx::launch_tree_attention_bf16_128);
+  idx::TreeAttnLaunch *const launches[2][2][2] = {   // [many][E4M3][D = 128]
+      {{idx::launch_tree_few_bf16_64, idx::launch_tree_few_bf16_128}, {idx::launch_tree_few_e4m3_64, idx::launch_tree_few_e4m3_128}},
+      {{idx::launch_tree_many_bf16_64, idx::launch_tree_many_bf16_128},
+       {idx::launch_tree_many_e4m3_64, idx::launch_tree_many_e4m3_128}}};
+  idx::TreeAttnLaunch *const launch = launches[s.rows == 0][f8][D == 128];
   return cuda_ok(launch(a, qm, km, vm, ctas, static_cast<cudaStream_t>(stream)));
 }
 

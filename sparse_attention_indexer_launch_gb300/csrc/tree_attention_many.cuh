@@ -38,26 +38,14 @@
 // rows.
 #pragma once
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
-#include "idx_device.cuh"
-#include "launch.h"
+#include "tree_attention_common.cuh"
 
 namespace idx {
 namespace {
 
 constexpr int kTile = kPage;             // keys per tile
 constexpr int kRows = 128;               // rows of a stream
-constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // + 128 * stream (S: + 64 * buffer)
-constexpr int kMinTiles = 4;             // tiles per CTA, at least (fewer CTAs otherwise)
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-// A row's maximum moves only when a score passes it by 2^8: until then the sums run
-// on the old one, below 2^8 * 2^19 in fp32, and O needs no pass through registers.
-constexpr float kLazy = 8.0f;
 
 // ---------------------------------------------------------------------------- roles
 // warps 0-3 and 4-7: softmax of streams 0 and 1; 8 and 11: loads of K and of V (by TMA,
@@ -77,13 +65,14 @@ struct Cfg {
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kQBufs = PAIR ? 1 : 2;
   static constexpr int kQTotal = kQBytes * (PAIR ? 2 : kQBufs);
-  static constexpr int kKStages = F8 ? (D == 128 && COPIES > 1 ? 4 : 6) : (D == 128 ? 4 : 5);
-  static constexpr int kVStages = F8 ? 4 : (D == 128 ? 4 : 5);    // as bf16
+  // The streams (and the converting teams) take alternate loads, so the counts are even: a
+  // stage then always has the same waiter.  Were they odd, a waiter could come to a stage
+  // again before the other's load in between, and the parity of the barrier would pass for
+  // the one that it waits for.
+  static constexpr int kKStages = F8 ? (D == 128 && COPIES > 1 ? 4 : 6) : 4;
+  static constexpr int kVStages = F8 ? 4 : D == 128 ? 4 : 6;      // as bf16
   static constexpr int kRawStages = F8 ? (D == 128 ? 4 : 6) : 0;  // V as E4M3
-  // A stage always belongs to the same team: were its loads to alternate, a team could
-  // come to it again before the other team's load in between, and the parity of its
-  // barrier would pass for the one it waits for.
-  static_assert(!F8 || (kVStages % 2 == 0 && kRawStages % 2 == 0), "stages per converting team");
+  static_assert(kKStages % 2 == 0 && kVStages % 2 == 0 && kRawStages % 2 == 0, "one waiter per stage");
   static constexpr int kScaleStages = F8 ? 8 : 0;
   static constexpr int kScaleFloats = 2 * kLoad * kTile;   // of a load: K's, then V's
   static constexpr int kRedBytes = COPIES > 1 ? 2 * kRows * 16 * 4 : 0;   // the copies' sum: 16 columns a stream
@@ -109,7 +98,7 @@ struct Barriers {
   uint32_t tmem_base;
   int abort;
   int32_t two_terms[2][2];         // P of [stream][buffer] has a low term
-  int32_t start_req, start_base;   // the share's first request, and the tiles before it
+  int2 found;                      // the share's first request, and the tiles before it
   uint32_t page_ok[64], vpage_ok[64];   // dense: the page of tile k % 64 of the CTA was loaded (K, V)
   uint32_t keys_ok[64][2];         // selected: bit per key of tile k % 64
   int32_t nonfinite[32];           // segment number + 1 whose drafted tokens' V held NaN or infinity
@@ -118,225 +107,7 @@ struct Barriers {
   // at most three segments before the softmax has begun with it: S of the second next one
   // takes the place of P of this one.
   float q_scale[4][PAIR ? 2 : 1][kRows];
-  int32_t warp_sums[20];
-};
-
-// ---------------------------------------------------------------------------- TMEM
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-      "%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// D += A B with A in TMEM (one 32-bit column holds two consecutive K elements of a row).
-__device__ __forceinline__ void umma_f16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
-}
-
-// Descriptor of an MN-major operand in the 128-byte swizzle: 64 elements of the M or N
-// dimension contiguous, groups of eight K rows 1024 bytes apart, the next 64 elements
-// `block` bytes on.
-__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t smem_addr, uint32_t block) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((block >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
-// Descriptor of a K-major operand with rows of 64 bytes in the 64-byte swizzle.
-__device__ __forceinline__ uint64_t umma_desc_sw64(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(1u) << 16;
-  d |= static_cast<uint64_t>(512u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(4u) << 61;
-  return d;
-}
-constexpr uint32_t kIdescBMn = 1u << 16;   // operand B is MN-major
-
-__device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, int y, int z, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Two floats to their nearest E4M3 codes (low byte: a).
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
-}
-__device__ __forceinline__ float2 e4m3x2_value(uint32_t x) {
-  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x), __NV_E4M3)));
-}
-// Four E4M3 codes to four bf16 values (exact: every E4M3 value is one).
-__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t x) {
-  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x & 0xFFFFu), __NV_E4M3);
-  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x >> 16), __NV_E4M3);
-  const float2 fa = __half22float2(__half2(a)), fb = __half22float2(__half2(b));
-  return make_uint2(pack_bf16(fa.x, fa.y), pack_bf16(fb.x, fb.y));
-}
-
-// ---------------------------------------------------------------------------- plan
-// A request as the launch reads it, clamped to the host's bounds.
-struct Req {
-  int32_t row0;    // first row
-  int32_t tokens;  // drafted tokens
-  int32_t ctx;     // cached tokens
-  int32_t keys;    // ctx + tokens, within the page table
-  int32_t tiles;   // of one item
-  int32_t blocks;  // items per key/value head
-  uint32_t bad;
-};
-
-__device__ __forceinline__ Req load_req(const TreeAttnArgs &a, int i) {
-  const idx_tree_problem &p = a.p;
-  Req q;
-  q.bad = 0;
-  const int32_t r0 = p.row_start[i], r1 = p.row_start[i + 1];
-  int32_t ctx = p.ctx_len[i];
-  q.row0 = r0;
-  q.tokens = 0;
-  if (r0 < 0 || r1 > p.R || r1 < r0) q.bad = kStatusBadBound;
-  else q.tokens = r1 - r0;
-  if (q.tokens > p.max_new) {
-    q.bad = kStatusBadBound;
-    q.tokens = p.max_new;
-  }
-  if (ctx < 0 || ctx > p.max_ctx) q.bad = kStatusBadBound;
-  ctx = max(0, min(ctx, p.max_ctx));
-  q.ctx = ctx;
-  q.keys = ctx + q.tokens;       // both far below 2^30
-  const int64_t room = static_cast<int64_t>(p.pt_stride) * kPage;
-  if (q.keys > room) {
-    q.bad = kStatusBadBound;
-    q.keys = static_cast<int32_t>(room);
-  }
-  const int n = a.sel != nullptr ? a.sel_k + q.tokens : q.keys;
-  q.tiles = q.tokens > 0 ? (n + kTile - 1) / kTile : 0;
-  q.blocks = (q.tokens + a.item_tokens - 1) / a.item_tokens;
-  return q;
-}
-// Tiles of a request: with the host's bounds the launch's sum fits 31 bits.
-__device__ __forceinline__ int req_tiles(const Req &q, int hkv) { return q.tiles * q.blocks * hkv; }
-
-// Shares: W tiles over n CTAs, the first W % n of them with one more.
-struct Shares {
-  int W, n, per, rest;
-  __device__ __forceinline__ Shares(int tiles, int ctas) : W(tiles) {
-    n = max(1, min((tiles + kMinTiles - 1) / kMinTiles, ctas));
-    per = W / n;
-    rest = W - per * n;
-  }
-  __device__ __forceinline__ int begin(int c) const { return c * per + min(c, rest); }
-  __device__ __forceinline__ int owner(int t) const {   // the CTA of tile t
-    const int big = rest * (per + 1);
-    return t < big ? t / (per + 1) : rest + (t - big) / per;
-  }
-};
-
-// Walks the segments of a share: the tiles of one item that fall into it.
-struct Walk {
-  const TreeAttnArgs &a;
-  int t, end, base;       // next tile, end of the share, tiles before request i
-  int i;
-  Req q;
-  // the segment
-  int seg = -1;           // its number
-  int head, tok0, tokens; // key/value head; first token and token count of the item's block
-  int tile0, count;       // first tile within the item, tiles
-  bool whole;             // the segment is the whole item
-  bool first;             // it is the share's first segment (its partial goes to slot 0)
-  int share0;
-
-  __device__ __forceinline__ Walk(const TreeAttnArgs &args, int t0, int t1, int req, int req_base)
-      : a(args), t(t0), end(t1), base(req_base), i(req), share0(t0) {
-    if (t < end) q = load_req(a, i);
-  }
-  __device__ __forceinline__ bool next() {
-    if (t >= end) return false;
-    int mine = req_tiles(q, a.p.cache.Hkv);
-    while (t >= base + mine) {
-      base += mine;
-      q = load_req(a, ++i);
-      mine = req_tiles(q, a.p.cache.Hkv);
-    }
-    const int off = t - base;
-    const int item = off / q.tiles;
-    tile0 = off - item * q.tiles;
-    head = item / q.blocks;
-    tok0 = (item - head * q.blocks) * a.item_tokens;
-    tokens = min(a.item_tokens, q.tokens - tok0);
-    count = min(end - t, q.tiles - tile0);
-    whole = count == q.tiles;
-    first = t == share0;
-    t += count;
-    ++seg;
-    return true;
-  }
+  int warp_sums[20];
 };
 
 // ---------------------------------------------------------------------------- softmax
@@ -547,77 +318,15 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
     }
   }
 
-  // ------------------------------------------------------------------ the share
-  // Every CTA sums the requests' tiles itself: a warp at a time for few requests, else
-  // the whole CTA in chunks.
-  constexpr int kWarps = C::kThreads / 32;
-  int W = 0, req0 = 0, base0 = 0;
-  uint32_t bad = 0;
-  auto scan32 = [&](int i) -> int2 {   // (tiles of request i, inclusive sum over the warp)
-    int mine = 0;
-    if (i < p.Q) {
-      const Req q = load_req(a, i);
-      bad |= q.bad;
-      mine = req_tiles(q, Hkv);
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
-    }
-    return make_int2(mine, incl);
-  };
-  if (p.Q <= 32) {
-    const int2 s = scan32(lane);
-    W = __shfl_sync(0xffffffffu, s.y, 31);
-    const Shares sh(W, gridDim.x);
-    const int t0 = sh.begin(min(static_cast<int>(blockIdx.x), sh.n));
-    const uint32_t at = __ballot_sync(0xffffffffu, t0 >= s.y - s.x && t0 < s.y);
-    if (at != 0u) {
-      req0 = __ffs(at) - 1;
-      base0 = __shfl_sync(0xffffffffu, s.y - s.x, req0);
-    }
-    if (blockIdx.x == 0 && warp == 0 && bad) flag_status(a.status, bad);
-  } else {
-    auto scan = [&](int i0, int before, int2 &s) -> int {   // sums of one chunk, returns its total
-      s = scan32(i0 + tid);
-      if (lane == 31) bars.warp_sums[warp] = s.y;
-      __syncthreads();
-      int total = 0;
-      s.y += before;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) s.y += bars.warp_sums[w];
-        total += bars.warp_sums[w];
-      }
-      __syncthreads();
-      return total;
-    };
-    int2 s = make_int2(0, 0);
-    for (int i0 = 0; i0 < p.Q; i0 += C::kThreads) W += scan(i0, W, s);
-    if (blockIdx.x == 0 && bad) flag_status(a.status, bad);
-    const Shares sh(W, gridDim.x);
-    const int t0 = sh.begin(min(static_cast<int>(blockIdx.x), sh.n));
-    int before = 0;
-    for (int i0 = 0; i0 < p.Q; i0 += C::kThreads) {
-      if (p.Q > C::kThreads) before += scan(i0, before, s);   // one chunk: the sums are still in registers
-      if (i0 + tid < p.Q && t0 >= s.y - s.x && t0 < s.y) {
-        bars.start_req = i0 + tid;
-        bars.start_base = s.y - s.x;
-      }
-    }
-  }
+  const Start start = find_share<C::kThreads>(a, &bars.found, bars.warp_sums);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
-  const Shares share(W, gridDim.x);
-  const bool idle = static_cast<int>(blockIdx.x) >= share.n || W == 0;
+  const Shares share(start.W, a.tile, gridDim.x);
+  const bool idle = static_cast<int>(blockIdx.x) >= share.n || start.W == 0;
   const int t0 = idle ? 0 : share.begin(blockIdx.x), t1 = idle ? 0 : share.begin(blockIdx.x + 1);
-  if (!idle && p.Q > 32) {
-    req0 = bars.start_req;
-    base0 = bars.start_base;
-  }
+  const int req0 = p.Q > 32 && !idle ? bars.found.x : start.req, base0 = p.Q > 32 && !idle ? bars.found.y : start.base;
   Walk walk(a, t0, t1, req0, base0);
 
   const uint64_t limit = a.wait_limit_ns;
@@ -649,7 +358,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // first TMEM lane of the warp << 16
     const uint32_t to = tmem + kColO + 128 * s + lanes;
     const float c = p.scale * kLog2e;
-    const int step = PAIR ? 1 : 2, j0 = PAIR ? 0 : s;
+    const int step = PAIR ? 1 : 2;
     int tiles = 0;      // tiles of earlier segments
     int loads = 0;      // loads of earlier segments
     uint32_t n = 0;     // this stream's tiles so far
@@ -667,6 +376,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       const int ctx = walk.q.ctx;
       float m = -INFINITY, l = 0.0f;
       int mine = 0;      // this stream's tiles in the segment
+      const int j0 = PAIR ? 0 : (s ^ loads) & 1;   // the stream's first load: the CTA's even or odd ones
       float cs = c;      // of the row's scores
       for (int jj = j0; ok && live && jj * kLoad < walk.count; jj += step)
       for (int j = jj * kLoad; j < min(walk.count, (jj + 1) * kLoad); ++j, ++n, ++mine) {
@@ -767,8 +477,10 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           warp_arrive(&bars.sc_empty[ld % 8]);
         }
       if (!ok) break;
+      const int odd = loads & 1, nloads = (walk.count + kLoad - 1) / kLoad;
+      const bool has0 = PAIR || odd < nloads, has1 = !PAIR && (odd ^ 1) < nloads;   // the streams that had tiles
       tiles += walk.count;
-      loads += (walk.count + kLoad - 1) / kLoad;
+      loads += nloads;
 
       // -------------------------------------------------------------- end of the segment
       // its last two products may still be under way
@@ -807,7 +519,6 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
         }
         m = mm;
       }
-      const bool two = !PAIR && walk.count > 1;    // stream 1 has tiles
       const bool poison = *reinterpret_cast<volatile int32_t *>(&bars.nonfinite[walk.seg & 31]) == walk.seg + 1;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int hq = walk.head * G + row % G;
@@ -857,15 +568,15 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
         if (active) {
           __syncwarp();
           uint32_t x[16], x1[16];
-          tmem_ld16(o0 + d, x);
-          if (two) tmem_ld16(o0 + 128 + d, x1);
+          if (has0) tmem_ld16(o0 + d, x);
+          if (has1) tmem_ld16(o0 + 128 + d, x1);
           tmem_wait_ld();
           reg_fence16(x);
           reg_fence16(x1);
 #pragma unroll
           for (int y = 0; y < 16; ++y) {
-            o[y] = PAIR ? __uint_as_float(x[y]) : f0 == 0.0f ? 0.0f : __uint_as_float(x[y]) * f0;
-            if (two) o[y] += f1 == 0.0f ? 0.0f : __uint_as_float(x1[y]) * f1;
+            o[y] = PAIR ? __uint_as_float(x[y]) : f0 == 0.0f || !has0 ? 0.0f : __uint_as_float(x[y]) * f0;
+            if (has1) o[y] += f1 == 0.0f ? 0.0f : __uint_as_float(x1[y]) * f1;
           }
         }
         if constexpr (COPIES == 1) {
@@ -1199,7 +910,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
             phase ^= 1u;
           }
         };
-        const int step = PAIR ? 1 : 2, j0 = PAIR ? 0 : s;
+        const int step = PAIR ? 1 : 2;
+        int loads = 0;      // of earlier segments
         while (ok && walk.next()) {
           const int qb = walk.seg % C::kQBufs;
           const int nloads = (walk.count + kLoad - 1) / kLoad;
@@ -1208,6 +920,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
             ok = false;
             break;
           }
+          const int j0 = PAIR ? 0 : (s ^ loads) & 1;   // the stream's first load
+          loads += nloads;
           if (j0 >= nloads) mbar_arrive(&bars.q_empty[qb]);
           // the stream's first load, and what lies before the next segment's
           skip(kstage, kphase, C::kKStages, j0);
@@ -1491,91 +1205,6 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
   }
 }
 
-// ---------------------------------------------------------------------------- combine
-// Joins the shares of split items: one warp per (row, query head), lanes across the
-// dimensions, the shares in CTA order.  All that depends on the inputs alone is worked
-// out while the attention kernel still runs.
-template <int D>
-__global__ void __launch_bounds__(256) combine_kernel(const TreeAttnArgs a, int ctas) {
-  constexpr int E = D / 32;
-  const idx_tree_problem &p = a.p;
-  const int slot_rows = a.pair ? 2 * kRows : kRows;
-  const int lane = threadIdx.x & 31;
-  const int w = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (w >= p.R * p.Hq) return;
-  const int r = w / p.Hq, hq = w - r * p.Hq;
-  const int Hkv = p.cache.Hkv;
-  int i = -1, W = 0, upto = 0;   // the row's request: the last one that starts at or before it
-  for (int i0 = 0; i0 < p.Q; i0 += 32) {
-    int tiles = 0;
-    bool at = false;
-    if (i0 + lane < p.Q) {
-      tiles = req_tiles(load_req(a, i0 + lane), Hkv);
-      at = p.row_start[i0 + lane] <= r;
-    }
-    i += __popc(__ballot_sync(0xffffffffu, at));
-    W += __reduce_add_sync(0xffffffffu, tiles);
-    upto += __reduce_add_sync(0xffffffffu, at ? tiles : 0);
-  }
-  if (i < 0 || W == 0) return;
-  const Req q = load_req(a, i);
-  const int t = r - q.row0;
-  if (t < 0 || t >= q.tokens) return;
-  const int G = p.Hq / Hkv;
-  const int head = hq / G, block = t / a.item_tokens;
-  const int b = upto - req_tiles(q, Hkv) + (head * q.blocks + block) * q.tiles, e = b + q.tiles;
-  const Shares sh(W, ctas);
-  const int c0 = sh.owner(b), c1 = sh.owner(e - 1);
-  if (c0 == c1) return;   // written whole
-  const int tb = a.pair ? a.item_tokens / 2 : a.item_tokens;
-  const int u = t - block * a.item_tokens;
-  const int prow = (u >= tb ? kRows + (u - tb) * G : u * G) + hq - head * G;
-  // CTA c's share of the item is its first segment (slot 0) unless the item begins inside it
-  const int slot0 = 2 * c0 + (sh.begin(c0) < b ? 1 : 0);
-  auto slot_of = [&](int c) { return c == c0 ? slot0 : 2 * c; };
-  grid_dependency_wait();
-  float m = -INFINITY, l = 0.0f, acc[E];
-#pragma unroll
-  for (int x = 0; x < E; ++x) acc[x] = 0.0f;
-  for (int cb = c0; cb <= c1; cb += 32) {
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (cb + lane <= c1) ml = a.part_ml[static_cast<int64_t>(slot_of(cb + lane)) * slot_rows + prow];
-    // the maximum so far, and what was summed up on the old one
-    float nm = ml.x;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
-    nm = fmaxf(nm, m);
-    const float keep = m == -INFINITY ? 0.0f : ex2(m - nm);
-    m = nm;
-    l *= keep;
-#pragma unroll
-    for (int x = 0; x < E; ++x) acc[x] *= keep;
-    const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - nm);
-    const int nc = min(32, c1 - cb + 1);
-#pragma unroll 8
-    for (int x = 0; x < nc; ++x) {
-      const float fx = __shfl_sync(0xffffffffu, f, x), lx = __shfl_sync(0xffffffffu, ml.y, x);
-      const float *const o = a.part_o + (static_cast<int64_t>(slot_of(cb + x)) * slot_rows + prow) * D + lane * E;
-      float v[E];
-      if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(o);
-      else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
-      if (fx != 0.0f) {
-        l += fx * lx;
-#pragma unroll
-        for (int y = 0; y < E; ++y) acc[y] += fx * v[y];
-      }
-    }
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t *const out = a.out + (static_cast<int64_t>(r) * p.Hq + hq) * D + lane * E;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t *>(out) = pack_bf16(acc[0] * inv, acc[1] * inv);
-  if (lane == 0 && a.lse != nullptr)
-    a.lse[static_cast<int64_t>(r) * p.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
 // ---------------------------------------------------------------------------- launch
 template <int D, bool F8, int COPIES, bool PAIR, bool SEL>
 cudaError_t launch(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm,
@@ -1598,26 +1227,7 @@ cudaError_t launch(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorM
   tree_attention_kernel<D, F8, COPIES, PAIR, SEL><<<num_ctas, C::kThreads, C::kDynamic, stream>>>(qm, km, vm, a);
   cudaError_t st = cudaGetLastError();
   if (st != cudaSuccess) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.p.R * a.p.Hq + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D>, a, num_ctas);
-}
-
-template <int D, bool F8, bool SEL>
-cudaError_t launch_shape(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm,
-                         int num_ctas, cudaStream_t stream) {
-  if constexpr (!SEL)
-    if (a.pair) return launch<D, F8, 1, true, SEL>(a, qm, km, vm, num_ctas, stream);
-  if (a.copies == 4) return launch<D, F8, 4, false, SEL>(a, qm, km, vm, num_ctas, stream);
-  if (a.copies == 2) return launch<D, F8, 2, false, SEL>(a, qm, km, vm, num_ctas, stream);
-  return launch<D, F8, 1, false, SEL>(a, qm, km, vm, num_ctas, stream);
+  return launch_combine<D>(a, num_ctas, stream);
 }
 
 }  // namespace

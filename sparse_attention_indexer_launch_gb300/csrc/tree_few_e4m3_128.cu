@@ -1,0 +1,19 @@
+// Attention over the paged cache with few rows (tree_attention_few.cuh): E4M3, 128 dimensions.
+#include "tree_attention_few.cuh"
+
+namespace idx {
+
+cudaError_t launch_tree_few_e4m3_128(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km,
+                                 const CUtensorMap &vm, int num_ctas, cudaStream_t stream) {
+  const bool sel = a.sel != nullptr;
+  if (a.rows == 16)
+    return sel ? launch_few_rows<128, true, 16, true>(a, qm, km, vm, num_ctas, stream)
+               : launch_few_rows<128, true, 16, false>(a, qm, km, vm, num_ctas, stream);
+  if (a.rows == 32)
+    return sel ? launch_few_rows<128, true, 32, true>(a, qm, km, vm, num_ctas, stream)
+               : launch_few_rows<128, true, 32, false>(a, qm, km, vm, num_ctas, stream);
+  return sel ? launch_few_rows<128, true, 64, true>(a, qm, km, vm, num_ctas, stream)
+             : launch_few_rows<128, true, 64, false>(a, qm, km, vm, num_ctas, stream);
+}
+
+}  // namespace idx
