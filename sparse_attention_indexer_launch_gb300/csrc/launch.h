@@ -136,6 +136,7 @@ struct TreeAttnArgs {
   uint32_t *status;
   float2 *part_ml;         // [2 * CTAs][rows] (maximum in log2, sum) of shares of split items
   float *part_o;           // [2 * CTAs][rows][D] their outputs before the division
+  uint2 *joins;            // [CTAs] counters of the items that begin in a CTA and go on in others, zero between calls
   uint64_t wait_limit_ns;
   int32_t item_tokens;     // drafted tokens of an item
   int32_t pair;            // its rows are two blocks of item_tokens / 2 tokens

@@ -101,13 +101,14 @@ idx_status check_problem(const idx_tree_problem *p, int32_t sel_k) {
 size_t round_up(size_t x) { return (x + kStateAlign - 1) / kStateAlign * kStateAlign; }
 
 struct StateLayout {
-  size_t ml, o, total;
+  size_t joins, ml, o, total;
 };
 StateLayout state_layout(const idx_tree_problem *p, int32_t sel_k) {
   const Shape s = shape_of(p, sel_k);
   const size_t slots = 2 * static_cast<size_t>(idx::kTreeMaxCtas) * (s.pair ? 256 : 128);
   StateLayout L{};
-  L.ml = kStatusBytes;
+  L.joins = kStatusBytes;
+  L.ml = L.joins + round_up(idx::kTreeMaxCtas * sizeof(uint2));
   L.o = L.ml + round_up(slots * sizeof(float2));
   L.total = L.o + round_up(slots * p->cache.D * sizeof(float));
   return L;
@@ -177,6 +178,7 @@ idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, 
   a.out = static_cast<uint16_t *>(out);
   a.lse = lse;
   a.status = static_cast<uint32_t *>(state);
+  a.joins = reinterpret_cast<uint2 *>(b + L.joins);
   a.part_ml = reinterpret_cast<float2 *>(b + L.ml);
   a.part_o = reinterpret_cast<float *>(b + L.o);
   a.wait_limit_ns = idx::device_wait_limit_ns();

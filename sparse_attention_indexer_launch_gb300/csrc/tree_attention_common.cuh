@@ -1,5 +1,5 @@
 // What the attention kernels share: tensor-memory and tensor-map helpers, the plan that
-// deals a launch's tiles out to the CTAs, and the kernel that joins split items.
+// deals a launch's tiles out to the CTAs, and the join of split items.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -214,10 +214,8 @@ struct Walk {
   bool first;             // it is the share's first segment (its partial goes to slot 0)
   int share0;
 
-  __device__ __forceinline__ Walk(const TreeAttnArgs &args, int t0, int t1, int req, int req_base)
-      : a(args), t(t0), end(t1), base(req_base), i(req), share0(t0) {
-    if (t < end) q = load_req(a, i);
-  }
+  __device__ __forceinline__ Walk(const TreeAttnArgs &args, int t0, int t1, int req, int req_base, const Req &first)
+      : a(args), t(t0), end(t1), base(req_base), i(req), q(first), share0(t0) {}
   __device__ __forceinline__ bool next() {
     if (t >= end) return false;
     int mine = req_tiles(q, a.p.cache.Hkv);
@@ -247,19 +245,21 @@ struct Walk {
 struct Start {
   int W;            // tiles of the launch
   int req, base;    // the share's first request, and the tiles before it
+  Req q;            // that request
 };
 template <int kThreads>
-__device__ __forceinline__ Start find_share(const TreeAttnArgs &a, int2 *found, int *warp_sums) {
+__device__ __forceinline__ Start find_share(const TreeAttnArgs &a, Start *found, int *warp_sums) {
   const idx_tree_problem &p = a.p;
   const int Hkv = p.cache.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kWarps = kThreads / 32;
-  Start st{0, 0, 0};
+  Start st{};
+  Req q{};
   uint32_t bad = 0;
   auto scan32 = [&](int i) -> int2 {   // (tiles of request i, inclusive sum over the warp)
     int mine = 0;
     if (i < p.Q) {
-      const Req q = load_req(a, i);
+      q = load_req(a, i);
       bad |= q.bad;
       mine = req_tiles(q, Hkv);
     }
@@ -277,10 +277,14 @@ __device__ __forceinline__ Start find_share(const TreeAttnArgs &a, int2 *found, 
     const Shares sh(st.W, a.tile, gridDim.x);
     const int t0 = sh.begin(min(static_cast<int>(blockIdx.x), sh.n));
     const uint32_t at = __ballot_sync(0xffffffffu, t0 >= s.y - s.x && t0 < s.y);
-    if (at != 0u) {
-      st.req = __ffs(at) - 1;
-      st.base = __shfl_sync(0xffffffffu, s.y - s.x, st.req);
-    }
+    st.req = at != 0u ? __ffs(at) - 1 : 0;
+    st.base = __shfl_sync(0xffffffffu, s.y - s.x, st.req);
+    st.q.row0 = __shfl_sync(0xffffffffu, q.row0, st.req);
+    st.q.tokens = __shfl_sync(0xffffffffu, q.tokens, st.req);
+    st.q.ctx = __shfl_sync(0xffffffffu, q.ctx, st.req);
+    st.q.keys = __shfl_sync(0xffffffffu, q.keys, st.req);
+    st.q.tiles = __shfl_sync(0xffffffffu, q.tiles, st.req);
+    st.q.blocks = __shfl_sync(0xffffffffu, q.blocks, st.req);
     if (blockIdx.x == 0 && warp == 0 && bad) flag_status(a.status, bad);
     return st;
   }
@@ -305,108 +309,159 @@ __device__ __forceinline__ Start find_share(const TreeAttnArgs &a, int2 *found, 
   int before = 0;
   for (int i0 = 0; i0 < p.Q; i0 += kThreads) {
     if (p.Q > kThreads) before += scan(i0, before, s);   // one chunk: the sums are still in registers
-    if (i0 + tid < p.Q && t0 >= s.y - s.x && t0 < s.y) *found = make_int2(i0 + tid, s.y - s.x);
+    if (i0 + tid < p.Q && t0 >= s.y - s.x && t0 < s.y) {
+      found->req = i0 + tid;
+      found->base = s.y - s.x;
+      found->q = q;
+    }
   }
   return st;
 }
 
-// ---------------------------------------------------------------------------- combine
-// Joins the shares of split items: one warp per (row, query head), lanes across the
-// dimensions, the shares in CTA order.  All that depends on the inputs alone is worked
-// out while the attention kernel still runs.
+// ---------------------------------------------------------------------------- join
+// A split item is joined by the CTAs that share it.  Each leaves its share (O before the
+// division, the rows' references and sums) in its slot of the state and counts itself in;
+// once all are in, each joins its part of the item's outputs, four values at a time.  The launch is cooperative: the CTAs that wait for each other run at
+// the same time.
+struct Share {
+  int row0, head, nrow;   // the item's first row of q, key/value head, rows
+  int c0, count;          // its first CTA, and how many there are
+  int slot0;              // the first CTA's slot (the others': 2 * CTA)
+};
+
+// The segment's part in a join; begin: the item's first tile in the launch's order.
+__device__ __forceinline__ Share share_of(const Walk &w, const Shares &sh, int G) {
+  Share s;
+  const int begin = w.t - w.count - w.tile0;
+  s.row0 = w.q.row0 + w.tok0;
+  s.head = w.head;
+  s.nrow = w.tokens * G;
+  s.c0 = sh.owner(begin);
+  s.count = sh.owner(begin + w.q.tiles - 1) - s.c0 + 1;
+  s.slot0 = 2 * s.c0 + (sh.begin(s.c0) < begin ? 1 : 0);
+  return s;
+}
+
+// Called by the 256 softmax threads of a CTA once its shares are written (thread 0's list).
 template <int D>
-__global__ void __launch_bounds__(256) combine_kernel(const TreeAttnArgs a, int ctas) {
-  constexpr int E = D / 32;
+__device__ __forceinline__ void join_items(const TreeAttnArgs &a, const Share *shares, const int *count, bool ok) {
   const idx_tree_problem &p = a.p;
-  const int slot_rows = a.pair ? 256 : 128;
   const int lane = threadIdx.x & 31;
-  const int w = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (w >= p.R * p.Hq) return;
-  const int r = w / p.Hq, hq = w - r * p.Hq;
-  const int Hkv = p.cache.Hkv;
-  int i = -1, W = 0, upto = 0;   // the row's request: the last one that starts at or before it
-  for (int i0 = 0; i0 < p.Q; i0 += 32) {
-    int tiles = 0;
-    bool at = false;
-    if (i0 + lane < p.Q) {
-      tiles = req_tiles(load_req(a, i0 + lane), Hkv);
-      at = p.row_start[i0 + lane] <= r;
-    }
-    i += __popc(__ballot_sync(0xffffffffu, at));
-    W += __reduce_add_sync(0xffffffffu, tiles);
-    upto += __reduce_add_sync(0xffffffffu, at ? tiles : 0);
-  }
-  if (i < 0 || W == 0) return;
-  const Req q = load_req(a, i);
-  const int t = r - q.row0;
-  if (t < 0 || t >= q.tokens) return;
-  const int G = p.Hq / Hkv;
-  const int head = hq / G, block = t / a.item_tokens;
-  const int b = upto - req_tiles(q, Hkv) + (head * q.blocks + block) * q.tiles, e = b + q.tiles;
-  const Shares sh(W, a.tile, ctas);
-  const int c0 = sh.owner(b), c1 = sh.owner(e - 1);
-  if (c0 == c1) return;   // written whole
+  const int G = p.Hq / p.cache.Hkv;
+  const int slot_rows = a.pair ? 256 : 128;
   const int tb = a.pair ? a.item_tokens / 2 : a.item_tokens;
-  const int u = t - block * a.item_tokens;
-  const int prow = (u >= tb ? 128 + (u - tb) * G : u * G) + hq - head * G;
-  // CTA c's share of the item is its first segment (slot 0) unless the item begins inside it
-  const int slot0 = 2 * c0 + (sh.begin(c0) < b ? 1 : 0);
-  auto slot_of = [&](int c) { return c == c0 ? slot0 : 2 * c; };
-  grid_dependency_wait();
-  float m = -INFINITY, l = 0.0f, acc[E];
+  asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
+  const int n = *count;
+  if (n == 0) return;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    for (int x = 0; x < n; ++x) atomicAdd(&a.joins[shares[x].c0].x, 1u);
+    const uint64_t t0 = global_ns();
+    for (int x = 0; x < n && ok; ++x) {
+      volatile uint32_t *const in = &a.joins[shares[x].c0].x;
+      while (*in < static_cast<uint32_t>(shares[x].count)) {
+        if (global_ns() - t0 > a.wait_limit_ns) {
+          flag_status(a.status, kStatusTimeout);
+          break;
+        }
+      }
+    }
+    __threadfence();
+  }
+  asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
+  for (int x = 0; x < n; ++x) {
+    const Share s = shares[x];
+    const int k = static_cast<int>(blockIdx.x) - s.c0;
+    const int units = s.nrow * (D / 4);       // of four values
+    const int begin = static_cast<int>(static_cast<int64_t>(units) * k / s.count);
+    const int end = static_cast<int>(static_cast<int64_t>(units) * (k + 1) / s.count);
+    // lanes per unit, over the shares: as many as the units leave of the 256 threads
+    int lanes = 1;
+    while (lanes < 32 && 2 * lanes * (end - begin) <= 256) lanes *= 2;
+    const int sub = lane & (lanes - 1);
+    for (int u0 = begin; u0 < end; u0 += 256 / lanes) {
+      const int u = u0 + static_cast<int>(threadIdx.x) / lanes;
+      const bool live = u < end;
+      const int row = live ? u / (D / 4) : 0, d = live ? (u - row * (D / 4)) * 4 : 0;
+      const int tok = row / G;
+      const int prow = a.pair && tok >= tb ? 128 + row - tb * G : row;
+      float m = -INFINITY, l = 0.0f;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int c0 = live ? sub : s.count; c0 < s.count; c0 += 4 * lanes) {
+        float2 ml[4];
+        float4 o[4];
 #pragma unroll
-  for (int x = 0; x < E; ++x) acc[x] = 0.0f;
-  for (int cb = c0; cb <= c1; cb += 32) {
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (cb + lane <= c1) ml = a.part_ml[static_cast<int64_t>(slot_of(cb + lane)) * slot_rows + prow];
-    // the maximum so far, and what was summed up on the old one
-    float nm = ml.x;
+        for (int y = 0; y < 4; ++y) {
+          const int c = c0 + y * lanes;
+          ml[y] = make_float2(-INFINITY, 0.0f);
+          o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (c >= s.count) continue;
+          const int64_t at = static_cast<int64_t>(c == 0 ? s.slot0 : 2 * (s.c0 + c)) * slot_rows + prow;
+          ml[y] = __ldcg(&a.part_ml[at]);
+          o[y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D + d));
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
-    nm = fmaxf(nm, m);
-    const float keep = m == -INFINITY ? 0.0f : ex2(m - nm);
-    m = nm;
-    l *= keep;
+        for (int y = 0; y < 4; ++y) {
+          const float nm = fmaxf(m, ml[y].x);
+          const float f = ml[y].x == -INFINITY ? 0.0f : ex2(ml[y].x - nm), keep = m == -INFINITY ? 0.0f : ex2(m - nm);
+          m = nm;
+          if (keep != 1.0f) {
+            l = keep == 0.0f ? 0.0f : l * keep;
+            acc.x = keep == 0.0f ? 0.0f : acc.x * keep;
+            acc.y = keep == 0.0f ? 0.0f : acc.y * keep;
+            acc.z = keep == 0.0f ? 0.0f : acc.z * keep;
+            acc.w = keep == 0.0f ? 0.0f : acc.w * keep;
+          }
+          if (f != 0.0f) {
+            l += f * ml[y].y;
+            acc.x += f * o[y].x;
+            acc.y += f * o[y].y;
+            acc.z += f * o[y].z;
+            acc.w += f * o[y].w;
+          }
+        }
+      }
+      float top = m;
+      for (int o = lanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float f = m == -INFINITY ? 0.0f : ex2(m - top);
+      float v[5] = {l, acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-    for (int x = 0; x < E; ++x) acc[x] *= keep;
-    const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - nm);
-    const int nc = min(32, c1 - cb + 1);
-#pragma unroll 8
-    for (int x = 0; x < nc; ++x) {
-      const float fx = __shfl_sync(0xffffffffu, f, x), lx = __shfl_sync(0xffffffffu, ml.y, x);
-      const float *const o = a.part_o + (static_cast<int64_t>(slot_of(cb + x)) * slot_rows + prow) * D + lane * E;
-      float v[E];
-      if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(o);
-      else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
-      if (fx != 0.0f) {
-        l += fx * lx;
+      for (int y = 0; y < 5; ++y) v[y] = f == 0.0f ? 0.0f : v[y] * f;
+      for (int o = lanes / 2; o > 0; o >>= 1)
 #pragma unroll
-        for (int y = 0; y < E; ++y) acc[y] += fx * v[y];
+        for (int y = 0; y < 5; ++y) v[y] += __shfl_xor_sync(0xffffffffu, v[y], o);
+      if (live && sub == 0) {
+        const float inv = v[0] == 0.0f ? 0.0f : 1.0f / v[0];
+        const int64_t at = static_cast<int64_t>(s.row0 + tok) * p.Hq + s.head * G + row - tok * G;
+        *reinterpret_cast<uint2 *>(a.out + at * D + d) =
+            make_uint2(pack_bf16(v[1] * inv, v[2] * inv), pack_bf16(v[3] * inv, v[4] * inv));
+        if (d == 0 && a.lse != nullptr) a.lse[at] = v[0] == 0.0f ? -INFINITY : (top + log2f(v[0])) * kLn2;
       }
     }
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t *const out = a.out + (static_cast<int64_t>(r) * p.Hq + hq) * D + lane * E;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t *>(out) = pack_bf16(acc[0] * inv, acc[1] * inv);
-  if (lane == 0 && a.lse != nullptr)
-    a.lse[static_cast<int64_t>(r) * p.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  // the last CTA out leaves the counters at zero for the next launch
+  if (threadIdx.x == 0)
+    for (int x = 0; x < n; ++x)
+      if (atomicAdd(&a.joins[shares[x].c0].y, 1u) + 1u == static_cast<uint32_t>(shares[x].count)) {
+        a.joins[shares[x].c0].x = 0u;
+        a.joins[shares[x].c0].y = 0u;
+      }
 }
 
-template <int D>
-cudaError_t launch_combine(const TreeAttnArgs &a, int num_ctas, cudaStream_t stream) {
+template <typename... Params, typename... Args>
+cudaError_t launch_cooperative(void (*kernel)(Params...), int ctas, int threads, int smem, cudaStream_t stream,
+                               Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.p.R * a.p.Hq + 7) / 8));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D>, a, num_ctas);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace

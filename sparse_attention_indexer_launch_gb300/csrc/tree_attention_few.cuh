@@ -35,7 +35,7 @@ namespace {
 
 // Warps 0-3 and 4-7: softmax of streams 0 and 1; 8 and 11: loads of K and of V (by TMA,
 // or gathering selected positions); 9 and 10: MMA issuers of streams 0 and 1; 12-19 with
-// an E4M3 cache: the split of Q, and V to bf16, in teams of four on alternate tiles.
+// an E4M3 cache: the split of Q, and V to bf16, in teams of four on a part of every tile.
 constexpr int kFewKWarp = 8, kFewIssuerWarp = 9, kFewVWarp = 11, kFewConvertWarp = 12;
 constexpr int kFewTile = 128;
 
@@ -49,8 +49,7 @@ struct FewCfg {
   static constexpr int kPBufs = N == 64 ? 1 : 2;           // per stream
   static constexpr int kQBufs = F8 && N == 64 ? 1 : 2;
   static constexpr int kFixed = kQBufs * kQBytes + 2 * kPBufs * kPBytes;
-  // Tiles in flight, as shared memory allows.  The streams (and the converting teams) take
-  // alternate tiles, so the counts are even: a stage then always has the same waiter.  Were
+  // Tiles in flight, as shared memory allows.  The streams take alternate tiles, so the counts are even: a stage then always has the same waiter.  Were
   // they odd, a waiter could come to a stage again before the other's tile in between, and
   // the parity of the barrier would pass for the one that it waits for.
   static constexpr int kKStages = F8 ? (D == 64 ? 6 : N == 16 ? 4 : 2) : D == 64 ? (N == 16 ? 6 : 4) : 2;
@@ -83,17 +82,20 @@ struct FewBarriers {
   uint32_t tmem_base;
   int abort;
   int32_t two_terms[2][2];         // [stream][P buffer]: a low term follows
-  int2 found;                      // the share's first request, and the tiles before it
+  Start found;                     // the share's first request
+  Share shares[2];                 // of split items
+  int nshare;                      // how many there are
   int warp_sums[20];
   uint32_t pages_ok[32], vpages_ok[32];   // dense: a bit per page of tile k % 32 that was loaded (K, V)
   uint32_t keys_ok[32][4];                // selected: a bit per key of tile k % 32
   int32_t nonfinite[32];                  // segment number + 1 whose drafted tokens' V held NaN or infinity
-  float ref[2][N], neg_ref[2][N];         // [stream][row]: the reference (-inf: none yet), and what is added to a score
+  alignas(16) float neg_ref[2][N];        // (read four at a time, as q_scale is)
+  alignas(16) float q_scale[4][N];        // E4M3: 1 / the row's power of two, [segment % 4]
+  float ref[2][N];                        // [stream][row]: the reference (-inf: none yet); neg_ref is what is added to a score
   float keep[2][N];                       // what a raised reference leaves of a row's sums
   float warp_max[2][4][N];
   float row_ref[2][2][N], row_l[2][2][4][N];   // [segment parity][stream], and by warp
   float join[2][3][N];                    // [stream]: factors of both streams' O, 1 / sum
-  float q_scale[4][N];                    // E4M3: 1 / the row's power of two, [segment % 4]
 };
 
 // The or of `p` over the 128 threads of a softmax team, which all meet here.
@@ -160,20 +162,18 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
   constexpr int kBlocks = D / 64;            // 64-dimension blocks of a bf16 operand
   constexpr int kBlockBytes = kFewTile * 128, kQBlockBytes = N * 128;
   constexpr uint32_t kColO = 4 * N;          // S: [stream][buffer] x N columns, then O: [stream] x N
-  grid_dependency_trigger();                 // the combine kernel's CTAs may take free SMs
 
-  if (tid == 0) {
-    for (int s = 0; s < 8; ++s) {
-      mbar_init(&bars.k_full[s], SEL ? 33 : 1);   // (33: and the word of keys_ok)
-      mbar_init(&bars.k_empty[s], 1);
-      mbar_init(&bars.v_full[s], F8 ? 4 : SEL ? 32 : 1);
-      mbar_init(&bars.v_empty[s], 1);
-      mbar_init(&bars.raw_full[s], SEL ? 32 : 1);
-      mbar_init(&bars.raw_empty[s], 4);
-      mbar_init(&bars.sc_full[s], SEL ? 64 : 2);   // K's and V's scales
-      mbar_init(&bars.sc_empty[s], 4);
-    }
-    for (int s = 0; s < 2; ++s) {
+  if (tid < 8) {
+    const int s = tid;
+    mbar_init(&bars.k_full[s], SEL ? 33 : 1);   // (33: and the word of keys_ok)
+    mbar_init(&bars.k_empty[s], 1);
+    mbar_init(&bars.v_full[s], F8 ? 4 * C::kTeams : SEL ? 32 : 1);
+    mbar_init(&bars.v_empty[s], 1);
+    mbar_init(&bars.raw_full[s], SEL ? 32 : 1);
+    mbar_init(&bars.raw_empty[s], 4 * C::kTeams);
+    mbar_init(&bars.sc_full[s], SEL ? 64 : 2);   // K's and V's scales
+    mbar_init(&bars.sc_empty[s], 4);
+    if (s < 2) {
       mbar_init(&bars.q_full[s], F8 ? 4 * C::kTeams : 1);
       mbar_init(&bars.q_empty[s], 2);
       for (int b = 0; b < 2; ++b) {
@@ -186,9 +186,12 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
       mbar_init(&bars.stats[s], 4);
       mbar_init(&bars.scrubbed[s], 4);
     }
-    bars.abort = 0;
-    for (int s = 0; s < 32; ++s) bars.nonfinite[s] = 0;
     fence_barrier_init();
+  }
+  if (tid < 32) bars.nonfinite[tid] = 0;
+  if (tid == 0) {
+    bars.abort = 0;
+    bars.nshare = 0;
   }
   if (warp == kFewIssuerWarp) {
     tmem_alloc(&bars.tmem_base, kTmemCols);
@@ -212,8 +215,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
   const Shares share(start.W, a.tile, gridDim.x);
   const bool idle = static_cast<int>(blockIdx.x) >= share.n || start.W == 0;
   const int t0 = idle ? 0 : share.begin(blockIdx.x), t1 = idle ? 0 : share.begin(blockIdx.x + 1);
-  const int req0 = p.Q > 32 && !idle ? bars.found.x : start.req, base0 = p.Q > 32 && !idle ? bars.found.y : start.base;
-  Walk walk(a, t0, t1, req0, base0);
+  const Start &first = p.Q > 32 && !idle ? bars.found : start;
+  Walk walk(a, t0, t1, first.req, first.base, first.q);
 
   const uint64_t limit = a.wait_limit_ns;
   volatile int *abort = &bars.abort;
@@ -315,8 +318,25 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int r = 0; r < N; ++r) asm volatile("" : "+r"(x[r]));
-        // scores relative to the references, in units of log2
-        auto relative = [&](float (&e)[N]) -> float {
+        // Scores relative to the references, in units of log2.  Pass 0 finds whether any
+        // passes its reference by too much; if so pass 1 takes the scores themselves, for
+        // the rows' maxima, and pass 2 the scores relative to the raised references.
+        float e[N];
+        if (h == h0 && !special) {
+          // a full first tile: the references are its first key's scores
+          if (key == 0) {
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+              const float m = __uint_as_float(x[r]) * ck * (F8 ? qs[r] : 1.0f);
+              const bool fine = m - m == 0.0f;    // else the row's maximum is taken below
+              bars.ref[s][r] = fine ? m : -INFINITY;
+              neg[r] = fine ? -m : INFINITY;
+            }
+          }
+          team_sync(s);
+        }
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
           float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int r = 0; r < N; r += 4) {
@@ -342,36 +362,23 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
             for (int r = 0; r < N; ++r)
               if (!((static_cast<uint32_t>(seen >> (r & 32)) >> (r & 31)) & 1u)) e[r] = -INFINITY;
           }
+          if (pass == 2) break;
+          if (pass == 0) {
 #pragma unroll
-          for (int r = 0; r < N; r += 8)
+            for (int r = 0; r < N; r += 8)
 #pragma unroll
-            for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], e[r + 2 * z], e[r + 2 * z + 1]);
-          return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-        };
-        float e[N];
-        if (h == h0 && !special) {
-          // a full first tile: the references are its first key's scores
-          if (key == 0) {
-#pragma unroll
-            for (int r = 0; r < N; ++r) {
-              const float m = __uint_as_float(x[r]) * ck * (F8 ? qs[r] : 1.0f);
-              const bool fine = m - m == 0.0f;    // else the row's maximum is taken below
-              bars.ref[s][r] = fine ? m : -INFINITY;
-              neg[r] = fine ? -m : INFINITY;
+              for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], e[r + 2 * z], e[r + 2 * z + 1]);
+            const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+            if (!team_any(s, !ok || top > kLazy)) break;
+            if (team_any(s, !ok)) {
+              left = true;
+              break;
             }
-          }
-          team_sync(s);
-        }
-        const float top = relative(e);
-        if (team_any(s, !ok || top > kLazy)) {
-          if (team_any(s, !ok)) {
-            left = true;
-            break;
+            if (key < N) neg[key] = 0.0f;
+            team_sync(s);
+            continue;
           }
           // the rows' maxima over the tile, and the references that they raise
-          if (key < N) neg[key] = 0.0f;
-          team_sync(s);
-          (void)relative(e);
           float mine[(N + 31) / 32] = {};
 #pragma unroll
           for (int r = 0; r < N; ++r) {
@@ -419,8 +426,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
             }
             tc_fence_before();
           }
-          (void)relative(e);
         }
+        if (left) break;
         // V of tokens that some rows do not see has to be finite (0 x NaN is NaN): zero
         // what no row sees, and what is not finite among the drafted tokens (rows that
         // see it get it back at the end)
@@ -470,7 +477,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
             if (special && !((static_cast<uint32_t>(seen >> (r & 32)) >> (r & 31)) & 1u)) e[r] = 0.0f;   // a stale scale may be NaN
           }
         }
-        auto hand_over = [&](bool more) {
+#pragma unroll 1
+        for (int more = special; more >= 0; --more) {
           // the buffer's product before has to have completed
           if (h - h0 >= C::kPBufs) ok = ok && settled(h - C::kPBufs);
           uint8_t *const row = sp + (s * C::kPBufs + h % C::kPBufs) * C::kPBytes + key * (2 * N);
@@ -478,16 +486,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
           for (int r = 0; r < N; r += 8) {
             uint32_t w[4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              w[z] = pack_bf16(e[r + 2 * z], e[r + 2 * z + 1]);
-              // what the rounding leaves (an infinity, of a scale, leaves nothing)
-              const float d0 = e[r + 2 * z] - __uint_as_float(w[z] << 16);
-              const float d1 = e[r + 2 * z + 1] - __uint_as_float(w[z] & 0xFFFF0000u);
-              if (more) {
-                e[r + 2 * z] = d0 == d0 ? d0 : 0.0f;
-                e[r + 2 * z + 1] = d1 == d1 ? d1 : 0.0f;
-              }
-            }
+            for (int z = 0; z < 4; ++z) w[z] = pack_bf16(e[r + 2 * z], e[r + 2 * z + 1]);
             const int sw = N == 64 ? key & 7 : N == 32 ? (key >> 1) & 3 : (key >> 2) & 1;
             *reinterpret_cast<uint4 *>(row + (((r >> 3) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
@@ -496,9 +495,14 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
           tc_fence_before();
           warp_arrive(&bars.p_ready[s][h % C::kPBufs]);
           ++h;
-        };
-        hand_over(special);
-        if (special) hand_over(false);
+          if (more) {   // what the rounding left (an infinity, of a scale, leaves nothing)
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+              const float rest = e[r] - __bfloat162float(__float2bfloat16_rn(e[r]));
+              e[r] = rest == rest ? rest : 0.0f;
+            }
+          }
+        }
         if (F8 && lane == 0) mbar_arrive(&bars.sc_empty[k % C::kScaleStages]);
       }
       if (left) break;
@@ -609,8 +613,10 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
         mbar_arrive(&bars.o_free[1]);
       }
       tiles += walk.count;
+      if (!walk.whole && tid == 0) bars.shares[bars.nshare++] = share_of(walk, share, G);
     }
     if (!ok) give_up();
+    join_items<D>(a, bars.shares, &bars.nshare, ok);
   } else if (warp < kFewConvertWarp) {
     if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kFewKWarp || warp == kFewVWarp) {
@@ -937,7 +943,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
       // -------------------------------------------------------------- E4M3: Q split, V to bf16
       if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
       const int team = (warp - kFewConvertWarp) >> 2, t = (tid - kFewConvertWarp * 32) & 127;
-      Walk qwalk(a, t0, t1, req0, base0);     // the segment whose Q is next
+      Walk qwalk(a, t0, t1, first.req, first.base, first.q);     // the segment whose Q is next
       // Q of qwalk's segment: D / 16 lanes per row with 16 elements each; rows without a
       // token are zero.
       auto split_q = [&]() -> bool {
@@ -1006,28 +1012,31 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
           ok = split_q();
           more = ok && qwalk.next();
         }
-        for (int j = (team + C::kTeams - tiles % C::kTeams) % C::kTeams; ok && j < walk.count; j += C::kTeams) {   // the team's tiles
+        for (int j = 0; j < walk.count; ++j) {   // each team a half of every tile
           const int k = tiles + j;
           const int sr = k % C::kRawStages, sl = k % C::kVStages;
           if (!warp_wait_all(&bars.raw_full[sr], (k / C::kRawStages) & 1)) {
             ok = false;
             break;
           }
-          uint8_t *const src = sraw + sr * C::kRawBytes;
-          uint8_t *const dst = sv + sl * C::kTileBytes;
+          constexpr int kKeys = kFewTile / C::kTeams;      // of a team
+          uint8_t *const src = sraw + sr * C::kRawBytes + team * kKeys * D;
+          uint8_t *const dst = sv + sl * C::kTileBytes + team * kKeys * 128;
           if (!SEL) {
             const int key0 = (walk.tile0 + j) * kFewTile;
             const uint32_t pages = bars.vpages_ok[k & 31];
             if (key0 + kFewTile > walk.q.ctx || pages != 3u) {
               // V of tokens that some rows do not see has to be finite (0 x NaN is NaN): zero
               // what no row sees, and the NaN codes among the drafted tokens (rows that see
-              // them get them back at the end).  Thread t has key t.
-              const int pos = key0 + t;
-              const bool dead = pos >= walk.q.keys || !((pages >> (t >> 6)) & 1u);
+              // them get them back at the end).  One or two threads per key.
+              constexpr int kShare = 128 / kKeys, kWords = D / 4 / kShare;
+              const int key = t % kKeys, at_key = team * kKeys + key, pos = key0 + at_key;
+              const bool dead = pos >= walk.q.keys || !((pages >> (at_key >> 6)) & 1u);
               if (dead || pos >= walk.q.ctx) {
 #pragma unroll 4
-                for (int y = 0; y < D / 4; ++y) {
-                  uint32_t *const at = reinterpret_cast<uint32_t *>(src + t * D) + (y + t) % (D / 4);
+                for (int y = 0; y < kWords; ++y) {
+                  uint32_t *const at =
+                      reinterpret_cast<uint32_t *>(src + key * D) + (t / kKeys) * kWords + (y + t) % kWords;
                   uint32_t w = dead ? 0u : *at;
 #pragma unroll
                   for (int z = 0; z < 32; z += 8)
@@ -1046,20 +1055,23 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
               ++scrubs;
             }
           }
-          constexpr int kChunks = D / 16;             // 16-byte chunks of codes per key
-          uint4 v[4];
+          constexpr int kChunks = D / 16;                   // 16-byte chunks of codes per key
+          constexpr int kMine = kKeys * kChunks / 128;      // a thread's chunks
+          constexpr int kBatch = kMine < 4 ? kMine : 4;
+          uint4 v[kBatch];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) v[y] = *reinterpret_cast<const uint4 *>(src + (y * 128 + t) * 16);
+          for (int y = 0; y < kBatch; ++y) v[y] = *reinterpret_cast<const uint4 *>(src + (y * 128 + t) * 16);
           if (!warp_wait_all(&bars.v_empty[sl], ((k / C::kVStages) & 1) ^ 1)) {
             ok = false;
             break;
           }
 #pragma unroll
-          for (int y = 0; y < kChunks; ++y) {
+          for (int y = 0; y < kMine; ++y) {
             const int key = (y * 128 + t) / kChunks, ch = t % kChunks;
-            const uint2 a0 = e4m3x4_to_bf16(v[y & 3].x), a1 = e4m3x4_to_bf16(v[y & 3].y),
-                        a2 = e4m3x4_to_bf16(v[y & 3].z), a3 = e4m3x4_to_bf16(v[y & 3].w);
-            if (y + 4 < kChunks) v[y & 3] = *reinterpret_cast<const uint4 *>(src + ((y + 4) * 128 + t) * 16);
+            uint4 &w = v[y % kBatch];
+            const uint2 a0 = e4m3x4_to_bf16(w.x), a1 = e4m3x4_to_bf16(w.y), a2 = e4m3x4_to_bf16(w.z),
+                        a3 = e4m3x4_to_bf16(w.w);
+            if (y + kBatch < kMine) w = *reinterpret_cast<const uint4 *>(src + ((y + kBatch) * 128 + t) * 16);
             uint8_t *const row = dst + (ch >> 2) * kBlockBytes + key * 128;
             const int c0 = (ch & 3) * 2;
             *reinterpret_cast<uint4 *>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
@@ -1107,9 +1119,7 @@ cudaError_t launch_few_rows(const TreeAttnArgs &a, const CUtensorMap &qm, const 
     return cudaFuncSetAttribute(few_rows_kernel<D, F8, N, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kDynamic);
   });
   if (e != cudaSuccess) return e;
-  few_rows_kernel<D, F8, N, SEL><<<num_ctas, C::kThreads, C::kDynamic, stream>>>(qm, km, vm, a);
-  const cudaError_t st = cudaGetLastError();
-  return st != cudaSuccess ? st : launch_combine<D>(a, num_ctas, stream);
+  return launch_cooperative(few_rows_kernel<D, F8, N, SEL>, num_ctas, C::kThreads, C::kDynamic, stream, qm, km, vm, a);
 }
 
 }  // namespace

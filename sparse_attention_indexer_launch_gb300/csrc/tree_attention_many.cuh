@@ -98,7 +98,9 @@ struct Barriers {
   uint32_t tmem_base;
   int abort;
   int32_t two_terms[2][2];         // P of [stream][buffer] has a low term
-  int2 found;                      // the share's first request, and the tiles before it
+  Start found;                     // the share's first request
+  Share shares[2];                 // of split items
+  int nshare;                      // how many there are
   uint32_t page_ok[64], vpage_ok[64];   // dense: the page of tile k % 64 of the CTA was loaded (K, V)
   uint32_t keys_ok[64][2];         // selected: bit per key of tile k % 64
   int32_t nonfinite[32];           // segment number + 1 whose drafted tokens' V held NaN or infinity
@@ -274,7 +276,6 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
   constexpr int kBlocks = D / 64;            // 64-dimension blocks of a bf16 operand
   constexpr int kLoad = C::kLoad;            // tiles per load
   constexpr int kBlockBytes = kLoad * kTile * 128, kQBlockBytes = kRows * 128;
-  grid_dependency_trigger();                 // the combine kernel's CTAs may take free SMs
 
   if (tid == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       mbar_init(&bars.scrubbed[s], 4);
     }
     bars.abort = 0;
+    bars.nshare = 0;
     for (int s = 0; s < 32; ++s) bars.nonfinite[s] = 0;
     fence_barrier_init();
   }
@@ -326,8 +328,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
   const Shares share(start.W, a.tile, gridDim.x);
   const bool idle = static_cast<int>(blockIdx.x) >= share.n || start.W == 0;
   const int t0 = idle ? 0 : share.begin(blockIdx.x), t1 = idle ? 0 : share.begin(blockIdx.x + 1);
-  const int req0 = p.Q > 32 && !idle ? bars.found.x : start.req, base0 = p.Q > 32 && !idle ? bars.found.y : start.base;
-  Walk walk(a, t0, t1, req0, base0);
+  const Start &first = p.Q > 32 && !idle ? bars.found : start;
+  Walk walk(a, t0, t1, first.req, first.base, first.q);
 
   const uint64_t limit = a.wait_limit_ns;
   volatile int *abort = &bars.abort;
@@ -627,8 +629,10 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
         mbar_arrive(&bars.o_free[PAIR ? s : 0]);
         if (!PAIR) mbar_arrive(&bars.o_free[1]);
       }
+      if (!walk.whole && tid == 0) bars.shares[bars.nshare++] = share_of(walk, share, G);
     }
     if (!ok) give_up();
+    join_items<D>(a, bars.shares, &bars.nshare, ok);
   } else if (warp < kConvertWarp) {
     if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kKWarp || warp == kVWarp) {
@@ -1027,7 +1031,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       // -------------------------------------------------------------- E4M3: Q split, V to bf16
       if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
       const int team = (warp - kConvertWarp) >> 2, t = (tid - kConvertWarp * 32) & 127;
-      Walk qwalk(a, t0, t1, req0, base0);     // the segment whose Q is next
+      Walk qwalk(a, t0, t1, first.req, first.base, first.q);     // the segment whose Q is next
       // Q of qwalk's segment: two threads per row (of every row block), each with half of
       // its dimensions.  The copies and both terms go to shared memory, rows without a
       // token as zeros.
@@ -1224,10 +1228,8 @@ cudaError_t launch(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorM
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kDynamic);
   });
   if (e != cudaSuccess) return e;
-  tree_attention_kernel<D, F8, COPIES, PAIR, SEL><<<num_ctas, C::kThreads, C::kDynamic, stream>>>(qm, km, vm, a);
-  cudaError_t st = cudaGetLastError();
-  if (st != cudaSuccess) return st;
-  return launch_combine<D>(a, num_ctas, stream);
+  return launch_cooperative(tree_attention_kernel<D, F8, COPIES, PAIR, SEL>, num_ctas, C::kThreads, C::kDynamic, stream,
+                            qm, km, vm, a);
 }
 
 }  // namespace
