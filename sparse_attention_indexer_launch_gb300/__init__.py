@@ -298,8 +298,8 @@ def tree_tables_state_size() -> int:
 def idx_tree_tables(tables: TreeTables, state, stream=None):
     """Page tables, slots and masks of a step (see idx.h); `state` from
     alloc_state(tree_tables_state_size())."""
-    _check(lib.idx_tree_tables(ctypes.byref(tables), _ptr(state), state.numel() * state.element_size(),
-                               _stream(stream)), "idx_tree_tables")
+    _check(lib.idx_tree_tables(ctypes.byref(tables), state.data_ptr(), state.nbytes, _stream(stream)),
+           "idx_tree_tables")
 
 
 def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
@@ -328,14 +328,17 @@ def idx_write_kv(cache: KvCache, k_new, v_new, slot, stream=None):
     """Writes k_new and v_new (bf16 [R][Hkv][D], rows of equal stride) into the cache
     at slot [R] (see idx.h)."""
     import torch
-    R = int(slot.shape[0])
-    for name, x in (("k_new", k_new), ("v_new", v_new)):
-        _need(x.dtype == torch.bfloat16 and tuple(x.shape) == (R, cache.Hkv, cache.D), f"{name}: bf16 [R][Hkv][D] is wanted")
-        _need(x.stride(2) == 1 and (cache.Hkv == 1 or x.stride(1) == cache.D), f"{name}: contiguous heads are wanted")
-    _int32("slot", slot)
+    R, shape = slot.shape[0], (slot.shape[0], cache.Hkv, cache.D)
+    for x in (k_new, v_new):
+        st = x.stride()
+        if x.dtype != torch.bfloat16 or x.shape != shape or st[2] != 1 or (st[1] != cache.D and cache.Hkv > 1):
+            raise ValueError("k_new, v_new: bf16 [R][Hkv][D] with contiguous heads is wanted")
+    if slot.dtype != torch.int32 or not slot.is_contiguous():
+        raise ValueError("slot: a contiguous int32 tensor is wanted")
     stride = k_new.stride(0) if R > 1 else cache.Hkv * cache.D
-    _need(R <= 1 or v_new.stride(0) == stride, "k_new, v_new: equal row strides are wanted")
-    _check(lib.idx_write_kv(ctypes.byref(cache), _ptr(k_new), _ptr(v_new), int(stride), _ptr(slot), R,
+    if R > 1 and v_new.stride(0) != stride:
+        raise ValueError("k_new, v_new: equal row strides are wanted")
+    _check(lib.idx_write_kv(ctypes.byref(cache), k_new.data_ptr(), v_new.data_ptr(), stride, slot.data_ptr(), R,
                             _stream(stream)), "idx_write_kv")
 
 
@@ -366,11 +369,11 @@ def tree_state_size(problem: TreeProblem, sel_k: int = 0) -> int:
 
 def _attn_outputs(problem, out, lse):
     import torch
-    R, Hq, D = problem.R, problem.Hq, problem.cache.D
-    _need(out.dtype == torch.bfloat16 and out.is_contiguous() and tuple(out.shape) == (R, Hq, D),
-          "out: contiguous bf16 [R][Hq][D] is wanted")
-    _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (R, Hq)),
-          "lse: contiguous fp32 [R][Hq] is wanted")
+    rows, heads = problem.R, problem.Hq
+    if out.dtype != torch.bfloat16 or out.shape != (rows, heads, problem.cache.D) or not out.is_contiguous():
+        raise ValueError("out: contiguous bf16 [R][Hq][D] is wanted")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (rows, heads) or not lse.is_contiguous()):
+        raise ValueError("lse: contiguous fp32 [R][Hq] is wanted")
 
 
 def idx_tree_attention(problem: TreeProblem, out, state, lse=None, stream=None):
@@ -378,19 +381,20 @@ def idx_tree_attention(problem: TreeProblem, out, state, lse=None, stream=None):
     [R][Hq][D]) and lse (fp32 [R][Hq] or None); `state` from
     alloc_state(tree_state_size(problem))."""
     _attn_outputs(problem, out, lse)
-    _check(lib.idx_tree_attention(ctypes.byref(problem), _ptr(out), _ptr(lse), _ptr(state),
-                                  state.numel() * state.element_size(), _stream(stream)), "idx_tree_attention")
+    _check(lib.idx_tree_attention(ctypes.byref(problem), out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                  state.data_ptr(), state.nbytes, _stream(stream)), "idx_tree_attention")
 
 
 def idx_tree_attention_selected(problem: TreeProblem, sel, out, state, lse=None, stream=None):
     """The same over the cached positions sel (int32 [R][K], as idx_launch writes
     them); `state` from alloc_state(tree_state_size(problem, K))."""
+    import torch
     _attn_outputs(problem, out, lse)
-    _int32("sel", sel)
-    _need(sel.dim() == 2 and sel.shape[0] == problem.R, "sel: [R][K] is wanted")
-    _check(lib.idx_tree_attention_selected(ctypes.byref(problem), _ptr(sel), int(sel.shape[1]), _ptr(out), _ptr(lse),
-                                           _ptr(state), state.numel() * state.element_size(), _stream(stream)),
-           "idx_tree_attention_selected")
+    if sel.dtype != torch.int32 or sel.dim() != 2 or sel.shape[0] != problem.R or not sel.is_contiguous():
+        raise ValueError("sel: a contiguous int32 [R][K] tensor is wanted")
+    _check(lib.idx_tree_attention_selected(ctypes.byref(problem), sel.data_ptr(), sel.shape[1], out.data_ptr(),
+                                           None if lse is None else lse.data_ptr(), state.data_ptr(), state.nbytes,
+                                           _stream(stream)), "idx_tree_attention_selected")
 
 
 def last_device_status(ws, stream=None) -> int:

@@ -18,8 +18,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowsPerThread = 4;   // consecutive rows, so that a warp stores 512 bytes per array
 
+// Lengths are the caller's data: cut to 2^30, which no cache holds, positions fit 31 bits.
+constexpr int32_t kMaxLen = 1 << 30;
+__device__ __forceinline__ int32_t length_of(int32_t n) { return min(max(n, 0), kMaxLen - kPage); }
 // Pages that hold `tokens` tokens.
-__device__ __forceinline__ int64_t pages_of(int64_t tokens) { return (tokens + kPage - 1) / kPage; }
+__device__ __forceinline__ int32_t pages_of(int32_t tokens) {
+  return static_cast<int32_t>(static_cast<uint32_t>(tokens + kPage - 1) / kPage);
+}
 
 // Largest i in [0, n) with v[i] <= x (v ascending, v[0] <= x).
 __device__ __forceinline__ int find_last(const int32_t *v, int n, int32_t x) {
@@ -48,11 +53,11 @@ __global__ void __launch_bounds__(kThreads) tree_tables_kernel(const TreeTablesA
     const int i = i0 + tid;
     int64_t rows = 0, pages = 0;
     if (i < Q) {
-      const int64_t c = max(a.t.ctx_len[i], 0), n = max(a.t.new_len[i], 0);
-      const int64_t held = pages_of(c), all = pages_of(c + n);
+      const int32_t c = length_of(a.t.ctx_len[i]), n = length_of(a.t.new_len[i]);
+      const int32_t held = pages_of(c), all = pages_of(c + n);
       if (all > a.t.pt_stride && n > 0) bad |= kStatusBadBound;
       rows = n;
-      pages = max(min(all, static_cast<int64_t>(a.t.pt_stride)) - held, static_cast<int64_t>(0));
+      pages = max(min(all, a.t.pt_stride) - held, 0);
     }
     int64_t sr = rows, sp = pages;
 #pragma unroll
@@ -101,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) tree_tables_kernel(const TreeTablesA
   // new table entries
   for (int64_t n = first; n < pages; n += step) {
     const int i = find_last(taken, Q, static_cast<int32_t>(n));
-    const int64_t held = pages_of(max(a.t.ctx_len[i], 0));
+    const int32_t held = pages_of(length_of(a.t.ctx_len[i]));
     int32_t page = -1;
     if (n < free_count) {
       page = a.t.free_pages[free_count - 1 - n];
@@ -111,57 +116,60 @@ __global__ void __launch_bounds__(kThreads) tree_tables_kernel(const TreeTablesA
   }
 
   // rows: four consecutive ones per thread
-  for (int64_t r0 = first * kRowsPerThread; r0 < a.t.cap; r0 += step * kRowsPerThread) {
+  for (int64_t r0l = first * kRowsPerThread; r0l < a.t.cap; r0l += step * kRowsPerThread) {
+    const int32_t r0 = static_cast<int32_t>(r0l);
     int32_t req[kRowsPerThread], bound[kRowsPerThread], pos[kRowsPerThread], slot[kRowsPerThread];
     uint64_t mask[kRowsPerThread];
     int i = 0;
-    int64_t c = 0, held = 0, page_seen = -1;
-    int32_t page = -1;
+    int32_t at = 0, t = 0, end = 0, page_seen = -1, base = -1;   // base: the page's first slot, -1 without one
     if (r0 < rows) {
-      i = find_last(start, Q, static_cast<int32_t>(r0));
-      c = max(a.t.ctx_len[i], 0);
-      held = pages_of(c);
+      i = find_last(start, Q, r0);
+      t = r0 - start[i];
+      end = start[i + 1];
+      at = length_of(a.t.ctx_len[i]) + t;
     }
 #pragma unroll
-    for (int k = 0; k < kRowsPerThread; ++k) {
-      const int64_t r = r0 + k;
+    for (int k = 0; k < kRowsPerThread; ++k, ++t, ++at) {
+      const int32_t r = r0 + k;
       req[k] = 0;
       bound[k] = 0;
       pos[k] = 0;
       slot[k] = -1;
       mask[k] = 0;
       if (r >= rows) continue;
-      if (r >= start[i + 1]) {   // the next request with rows
+      if (r >= end) {   // the next request with rows
         do ++i;
         while (r >= start[i + 1]);
-        c = max(a.t.ctx_len[i], 0);
-        held = pages_of(c);
+        t = 0;
+        end = start[i + 1];
+        at = length_of(a.t.ctx_len[i]);
         page_seen = -1;
       }
-      const int64_t t = r - start[i], at = c + t;
-      if (at / kPage != page_seen) {
-        page_seen = at / kPage;
-        page = -1;
-        if (page_seen < held) {
-          if (page_seen < a.t.pt_stride) page = a.t.page_table[static_cast<int64_t>(i) * a.t.pt_stride + page_seen];
-        } else if (page_seen < a.t.pt_stride) {
-          const int64_t n = taken[i] + (page_seen - held);
-          if (n < free_count) page = a.t.free_pages[free_count - 1 - n];
+      const int32_t pg = static_cast<int32_t>(static_cast<uint32_t>(at) / kPage);
+      if (pg != page_seen) {
+        page_seen = pg;
+        int32_t page = -1;
+        const int32_t held = pages_of(at - t);
+        if (pg < a.t.pt_stride) {
+          if (pg < held) {
+            page = a.t.page_table[static_cast<int64_t>(i) * a.t.pt_stride + pg];
+          } else {
+            const int32_t n = taken[i] + (pg - held);
+            if (n < free_count) page = a.t.free_pages[free_count - 1 - n];
+          }
         }
-        if (page < 0 || page >= a.t.P) {
-          page = -1;
-          bad |= kStatusBadPage;
-        }
+        if (page < 0 || page >= a.t.P) bad |= kStatusBadPage;
+        base = page < 0 || page >= a.t.P ? -1 : page * kPage;
       }
       // walk up the tree: parents are earlier tokens, so it ends within 64 steps
-      int64_t depth = t;
+      int32_t depth = t;
       uint64_t m = 0;
       if (a.t.parent != nullptr && t < IDX_MAX_TREE) {
         depth = 0;
-        int64_t u = t;
+        int32_t u = t;
         for (;;) {
           m |= 1ull << u;
-          const int64_t p = a.t.parent[start[i] + u];
+          const int32_t p = a.t.parent[start[i] + u];
           if (p < 0 || p >= u) {
             if (p != -1) bad |= kStatusBadBound;
             break;
@@ -174,9 +182,9 @@ __global__ void __launch_bounds__(kThreads) tree_tables_kernel(const TreeTablesA
       }
       if (t >= IDX_MAX_TREE && (a.t.mask != nullptr || a.t.parent != nullptr)) bad |= kStatusBadBound;
       req[k] = i;
-      bound[k] = static_cast<int32_t>(min(at + 1, static_cast<int64_t>(INT32_MAX)));
-      pos[k] = static_cast<int32_t>(min(c + depth, static_cast<int64_t>(INT32_MAX)));
-      slot[k] = page < 0 ? -1 : page * kPage + static_cast<int32_t>(at % kPage);
+      bound[k] = at + 1;
+      pos[k] = at - t + depth;
+      slot[k] = base < 0 ? -1 : base + at % kPage;
       mask[k] = m;
     }
     if (a.vec4 && r0 + kRowsPerThread <= a.t.cap) {

@@ -15,6 +15,32 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVectors = 4;   // vectors per group and pass
 
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {   // nearest codes, low byte a
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
+}
+
+// E4M3 codes of the fp32 quotients f / sc.  x * (1 / sc) is within 3 * 2^-24 of the rounded
+// quotient, so where the codes of that value times 1 - 2^-22 and 1 + 2^-22 agree they are
+// the quotient's.  They disagree next to a tie only; those vectors, and scales out of the
+// range where the reciprocal is exact to 2^-24, are divided.
+__device__ __forceinline__ void quantize(const float (&f)[8], float sc, uint32_t &lo, uint32_t &hi) {
+  const float inv = __frcp_rn(sc);
+  const float down = inv * (1.0f - 0x1p-22f), up = inv * (1.0f + 0x1p-22f);
+  uint32_t a[4], b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = e4m3x2(f[2 * i] * down, f[2 * i + 1] * down);
+    b[i] = e4m3x2(f[2 * i] * up, f[2 * i + 1] * up);
+  }
+  const bool same = a[0] == b[0] && a[1] == b[1] && a[2] == b[2] && a[3] == b[3];
+  if (!(same && sc > 0x1p-100f && sc < 0x1p100f)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = e4m3x2(__fdiv_rn(f[2 * i], sc), __fdiv_rn(f[2 * i + 1], sc));
+  }
+  lo = a[0] | a[1] << 16;
+  hi = a[2] | a[3] << 16;
+}
+
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads) write_kv_kernel(const WriteKvArgs a) {
   constexpr int kLanes = D / 8;               // lanes per vector
@@ -65,12 +91,8 @@ __global__ void __launch_bounds__(kThreads) write_kv_kernel(const WriteKvArgs a)
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const float sc = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-      uint32_t lo = 0, hi = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(__fdiv_rn(f[i], sc), __NV_SATFINITE, __NV_E4M3)) << (8 * i);
-        hi |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(__fdiv_rn(f[4 + i], sc), __NV_SATFINITE, __NV_E4M3)) << (8 * i);
-      }
+      uint32_t lo, hi;
+      quantize(f, sc, lo, hi);
       if (live) {
         reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_v ? a.c.v : a.c.k) + at)[lane] = make_uint2(lo, hi);
         if (lane == 0) (is_v ? a.c.v_scale : a.c.k_scale)[(page * a.c.Hkv + h) * kPage + tok] = sc;
