@@ -118,6 +118,7 @@ struct TreeTablesArgs {
   idx_tree_tables_args t;
   uint32_t *status;
   int32_t vec4;            // the per-row arrays allow 16-byte stores
+  int32_t groups_per_cta;  // set by the launcher
 };
 
 struct WriteKvArgs {
@@ -145,8 +146,8 @@ struct TreeAttnArgs {
 };
 constexpr int kTreeMaxCtas = 160;   // shares of an attention launch, at most
 
-cudaError_t launch_tree_tables(const TreeTablesArgs &a, int num_sms, cudaStream_t stream);
-cudaError_t launch_write_kv(const WriteKvArgs &a, cudaStream_t stream);
+cudaError_t launch_tree_tables(TreeTablesArgs a, int num_sms, cudaStream_t stream);
+cudaError_t launch_write_kv(const WriteKvArgs &a, int num_sms, cudaStream_t stream);
 // qm: q as [R][Hq][D], box 64 x heads per key/value head x tokens of a row block; km, vm:
 // the cache as [P][Hkv][64][D], box one head's page (64 dimensions of it for bf16).
 using TreeAttnLaunch = cudaError_t(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km,

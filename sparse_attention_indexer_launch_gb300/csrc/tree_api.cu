@@ -232,7 +232,7 @@ idx_status idx_write_kv(const idx_kv_cache *cache, const void *k_new, const void
   if (k_new == nullptr || v_new == nullptr || slot == nullptr || !aligned(k_new, 16) || !aligned(v_new, 16))
     return IDX_EINVAL;
   if (row_stride < static_cast<int64_t>(cache->Hkv) * cache->D || row_stride % 8 != 0) return IDX_EINVAL;
-  if (R > INT32_MAX) return IDX_EUNSUPPORTED;   // the grid: at least 64 vectors a CTA, at most 2,048 a row
+  if (R > INT32_MAX) return IDX_EUNSUPPORTED;   // the grid: a row is at most 128 CTAs of vectors
   int sms = 0;
   st = idx::device_sms(&sms);   // the device check
   if (st != IDX_OK) return st;
@@ -243,7 +243,7 @@ idx_status idx_write_kv(const idx_kv_cache *cache, const void *k_new, const void
   a.row_stride = row_stride;
   a.R = R;
   a.slot = slot;
-  return cuda_ok(idx::launch_write_kv(a, static_cast<cudaStream_t>(stream)));
+  return cuda_ok(idx::launch_write_kv(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t idx_tree_state_size(const idx_tree_problem *problem, int32_t sel_k) {

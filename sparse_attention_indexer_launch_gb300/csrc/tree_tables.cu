@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kThreads) tree_tables_kernel(const TreeTablesA
   }
   __syncthreads();
   const int32_t rows = start[Q], pages = taken[Q];
+  const bool simple = a.t.mask == nullptr && a.t.parent == nullptr;
   const int32_t free_count = max(*a.t.free_count, 0);
   if (tid == 0 && pages > free_count) bad |= kStatusBadPage;
   if (blockIdx.x == 0 && tid == 0) *a.t.free_left = max(free_count - pages, 0);
@@ -115,77 +116,106 @@ __global__ void __launch_bounds__(kThreads) tree_tables_kernel(const TreeTablesA
     a.t.page_table[static_cast<int64_t>(i) * a.t.pt_stride + held + (n - taken[i])] = page;
   }
 
-  // rows: four consecutive ones per thread
-  for (int64_t r0l = first * kRowsPerThread; r0l < a.t.cap; r0l += step * kRowsPerThread) {
+  // The first slot of request i's page pg, -1 without one.  ctx: the request's cached tokens.
+  const auto base_of = [&](int i, int32_t ctx, int32_t pg) {
+    int32_t page = -1;
+    const int32_t held = pages_of(ctx);
+    if (pg < a.t.pt_stride) {
+      if (pg < held) {
+        page = a.t.page_table[static_cast<int64_t>(i) * a.t.pt_stride + pg];
+      } else {
+        const int32_t n = taken[i] + (pg - held);
+        if (n < free_count) page = a.t.free_pages[free_count - 1 - n];
+      }
+    }
+    if (page >= 0 && page < a.t.P) return page * kPage;
+    bad |= kStatusBadPage;
+    return -1;
+  };
+
+  // rows: four consecutive ones per thread, a run of groups per CTA, so that a thread
+  // looks its request up again only where the last one ended
+  const int64_t run = static_cast<int64_t>(a.groups_per_cta) * kThreads * kRowsPerThread;
+  const int64_t run_end = min((blockIdx.x + 1) * run, static_cast<int64_t>(a.t.cap));
+  int i = 0;
+  int32_t end = 0, ctx = 0, begin = 0;   // request i: its rows [begin, end), its cached tokens
+  for (int64_t r0l = blockIdx.x * run + tid * kRowsPerThread; r0l < run_end; r0l += kThreads * kRowsPerThread) {
     const int32_t r0 = static_cast<int32_t>(r0l);
     int32_t req[kRowsPerThread], bound[kRowsPerThread], pos[kRowsPerThread], slot[kRowsPerThread];
     uint64_t mask[kRowsPerThread];
-    int i = 0;
-    int32_t at = 0, t = 0, end = 0, page_seen = -1, base = -1;   // base: the page's first slot, -1 without one
-    if (r0 < rows) {
+    if (r0 < rows && r0 >= end) {
       i = find_last(start, Q, r0);
-      t = r0 - start[i];
+      begin = start[i];
       end = start[i + 1];
-      at = length_of(a.t.ctx_len[i]) + t;
+      ctx = length_of(a.t.ctx_len[i]);
     }
+    if (simple && r0 + kRowsPerThread <= min(rows, end)) {
+      // all four in one request, no tree: consecutive positions on one page or two
+      const int32_t at = ctx + (r0 - begin);
+      const int32_t pg = static_cast<int32_t>(static_cast<uint32_t>(at) / kPage), tok = at % kPage;
+      const int32_t base = base_of(i, ctx, pg);
+      const int32_t next = tok + kRowsPerThread > kPage ? base_of(i, ctx, pg + 1) : -1;
 #pragma unroll
-    for (int k = 0; k < kRowsPerThread; ++k, ++t, ++at) {
-      const int32_t r = r0 + k;
-      req[k] = 0;
-      bound[k] = 0;
-      pos[k] = 0;
-      slot[k] = -1;
-      mask[k] = 0;
-      if (r >= rows) continue;
-      if (r >= end) {   // the next request with rows
-        do ++i;
-        while (r >= start[i + 1]);
-        t = 0;
-        end = start[i + 1];
-        at = length_of(a.t.ctx_len[i]);
-        page_seen = -1;
+      for (int k = 0; k < kRowsPerThread; ++k) {
+        const bool here = tok + k < kPage;
+        const int32_t b = here ? base : next;
+        req[k] = i;
+        bound[k] = at + k + 1;
+        pos[k] = at + k;
+        slot[k] = b < 0 ? -1 : b + (here ? tok + k : tok + k - kPage);
+        mask[k] = 0;
       }
-      const int32_t pg = static_cast<int32_t>(static_cast<uint32_t>(at) / kPage);
-      if (pg != page_seen) {
-        page_seen = pg;
-        int32_t page = -1;
-        const int32_t held = pages_of(at - t);
-        if (pg < a.t.pt_stride) {
-          if (pg < held) {
-            page = a.t.page_table[static_cast<int64_t>(i) * a.t.pt_stride + pg];
-          } else {
-            const int32_t n = taken[i] + (pg - held);
-            if (n < free_count) page = a.t.free_pages[free_count - 1 - n];
-          }
+    } else {
+      int32_t t = r0 < rows ? r0 - begin : 0, at = ctx + t, page_seen = -1, base = -1;
+#pragma unroll
+      for (int k = 0; k < kRowsPerThread; ++k, ++t, ++at) {
+        const int32_t r = r0 + k;
+        req[k] = 0;
+        bound[k] = 0;
+        pos[k] = 0;
+        slot[k] = -1;
+        mask[k] = 0;
+        if (r >= rows) continue;
+        if (r >= end) {   // the next request with rows
+          do ++i;
+          while (r >= start[i + 1]);
+          t = 0;
+          begin = r;
+          end = start[i + 1];
+          at = ctx = length_of(a.t.ctx_len[i]);
+          page_seen = -1;
         }
-        if (page < 0 || page >= a.t.P) bad |= kStatusBadPage;
-        base = page < 0 || page >= a.t.P ? -1 : page * kPage;
-      }
-      // walk up the tree: parents are earlier tokens, so it ends within 64 steps
-      int32_t depth = t;
-      uint64_t m = 0;
-      if (a.t.parent != nullptr && t < IDX_MAX_TREE) {
-        depth = 0;
-        int32_t u = t;
-        for (;;) {
-          m |= 1ull << u;
-          const int32_t p = a.t.parent[start[i] + u];
-          if (p < 0 || p >= u) {
-            if (p != -1) bad |= kStatusBadBound;
-            break;
-          }
-          u = p;
-          ++depth;
+        const int32_t pg = static_cast<int32_t>(static_cast<uint32_t>(at) / kPage);
+        if (pg != page_seen) {
+          page_seen = pg;
+          base = base_of(i, at - t, pg);
         }
-      } else if (t < IDX_MAX_TREE) {
-        m = (2ull << t) - 1ull;   // bits 0 .. t (t = 63: the shift leaves 0, minus 1 sets all)
+        // walk up the tree: parents are earlier tokens, so it ends within 64 steps
+        int32_t depth = t;
+        uint64_t m = 0;
+        if (a.t.parent != nullptr && t < IDX_MAX_TREE) {
+          depth = 0;
+          int32_t u = t;
+          for (;;) {
+            m |= 1ull << u;
+            const int32_t p = a.t.parent[start[i] + u];
+            if (p < 0 || p >= u) {
+              if (p != -1) bad |= kStatusBadBound;
+              break;
+            }
+            u = p;
+            ++depth;
+          }
+        } else if (t < IDX_MAX_TREE) {
+          m = (2ull << t) - 1ull;   // bits 0 .. t (t = 63: the shift leaves 0, minus 1 sets all)
+        }
+        if (t >= IDX_MAX_TREE && (a.t.mask != nullptr || a.t.parent != nullptr)) bad |= kStatusBadBound;
+        req[k] = i;
+        bound[k] = at + 1;
+        pos[k] = at - t + depth;
+        slot[k] = base < 0 ? -1 : base + at % kPage;
+        mask[k] = m;
       }
-      if (t >= IDX_MAX_TREE && (a.t.mask != nullptr || a.t.parent != nullptr)) bad |= kStatusBadBound;
-      req[k] = i;
-      bound[k] = at + 1;
-      pos[k] = at - t + depth;
-      slot[k] = base < 0 ? -1 : base + at % kPage;
-      mask[k] = m;
     }
     if (a.vec4 && r0 + kRowsPerThread <= a.t.cap) {
       *reinterpret_cast<int4 *>(a.t.row_req + r0) = make_int4(req[0], req[1], req[2], req[3]);
@@ -211,12 +241,13 @@ __global__ void __launch_bounds__(kThreads) tree_tables_kernel(const TreeTablesA
 
 }  // namespace
 
-cudaError_t launch_tree_tables(const TreeTablesArgs &a, int num_sms, cudaStream_t stream) {
-  // enough CTAs for one row group per thread, at most eight per SM (the sums are
-  // repeated by every CTA)
+cudaError_t launch_tree_tables(TreeTablesArgs a, int num_sms, cudaStream_t stream) {
+  // enough CTAs for one row group per thread, at most about eight per SM (the sums
+  // are repeated by every CTA)
   const int64_t groups = (static_cast<int64_t>(a.t.cap) + kThreads * kRowsPerThread - 1) / (kThreads * kRowsPerThread);
   const int64_t most = 8 * static_cast<int64_t>(num_sms);
-  const int64_t grid = groups < 1 ? 1 : groups > most ? most : groups;
+  a.groups_per_cta = groups <= most ? 1 : static_cast<int32_t>((groups + most - 1) / most);
+  const int64_t grid = groups < 1 ? 1 : (groups + a.groups_per_cta - 1) / a.groups_per_cta;
   const size_t smem = 2 * (static_cast<size_t>(a.t.Q) + 1) * sizeof(int32_t);
   tree_tables_kernel<<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(a);
   return cudaGetLastError();
