@@ -7,7 +7,7 @@
 // whole call and an address costs it two multiplications by the slot's page and
 // token; kVectors loads are in flight before the first is needed.  In E4M3 the call
 // is bound by instructions as much as by memory: what a vector costs beyond its loads
-// is kept small (amax in packed bf16, quotients by a checked reciprocal).
+// is kept small (amax in packed bf16, quotients by a two-term reciprocal).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -27,35 +27,51 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {   // nearest code
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
 }
 
-// E4M3 codes of the fp32 quotients f / sc.  x times an approximate reciprocal (within
-// 2^-23) is within 2^-22 of the rounded quotient, so where the codes of that value
-// times 1 - 2^-21 and 1 + 2^-21 agree they are the quotient's.  They disagree next to a
-// tie only; those vectors, and scales near the ends of the range, are divided.
-__device__ __forceinline__ void quantize(const uint32_t (&w)[4], float sc, uint32_t &lo, uint32_t &hi) {
-  const float inv = __fdividef(1.0f, sc);
-  const float down = inv * (1.0f - 0x1p-21f), up = inv * (1.0f + 0x1p-21f);
-  uint32_t a[4], b[4];
-  float f[8];
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  return static_cast<uint64_t>(__float_as_uint(y)) << 32 | __float_as_uint(x);
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t z;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+  return z;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t w) {
+  uint64_t z;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(z) : "l"(x), "l"(y), "l"(w));
+  return z;
+}
+
+// The scale amax / 448 and the E4M3 codes of the quotients x / scale, both as fp32
+// division rounds them.  A divisor's reciprocal in two terms, hi + lo, gives
+// x / d = fma(x, hi, x * lo) correctly rounded (Brisebarre and Muller's multiplication by
+// a constant of higher precision): bf16 significands have 8 bits, and all 128 x 128 pairs
+// of amax and x were compared with the division, for every hi within 3 units of the last
+// place.  A single product would not do: 3/4 of the amax, for one, lies on a tie between
+// two codes.  Amaxes near the ends of the range, zero and infinity take the division.
+__device__ __forceinline__ float quantize(const uint32_t (&w)[4], float amax, uint32_t &lo, uint32_t &hi) {
+  float sc;
+  uint32_t c[4];
+  if (amax > 0x1p-100f && amax < 0x1p100f) {
+    constexpr float kHi = 0x1.24924ap-9f, kLo = -0x1.b6db6ep-34f;   // 1 / 448
+    sc = fmaf(amax, kHi, amax * kLo);
+    const float r = __fdividef(1.0f, sc);
+    const float e = fmaf(-r, sc, 1.0f) * r;
+    const uint64_t r2 = pack2(r, r), e2 = pack2(e, e);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    a[i] = e4m3x2(f[2 * i] * down, f[2 * i + 1] * down);
-    b[i] = e4m3x2(f[2 * i] * up, f[2 * i + 1] * up);
-  }
-  lo = a[0] | a[1] << 16;
-  hi = a[2] | a[3] << 16;
-  const bool same = lo == (b[0] | b[1] << 16) && hi == (b[2] | b[3] << 16);
-  if (!(same && sc > 0x1p-100f && sc < 0x1p100f)) {
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {   // rare: kept small
-      const float *const g = f + 4 * i;
-      const uint32_t c = e4m3x2(__fdiv_rn(g[0], sc), __fdiv_rn(g[1], sc)) |
-                         e4m3x2(__fdiv_rn(g[2], sc), __fdiv_rn(g[3], sc)) << 16;
-      if (i == 0) lo = c;
-      else hi = c;
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t f = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+      const uint64_t q = fma2(f, r2, mul2(f, e2));
+      c[i] = e4m3x2(__uint_as_float(static_cast<uint32_t>(q)), __uint_as_float(static_cast<uint32_t>(q >> 32)));
     }
+  } else {
+    sc = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = e4m3x2(__fdiv_rn(__uint_as_float(w[i] << 16), sc), __fdiv_rn(__uint_as_float(w[i] & 0xFFFF0000u), sc));
   }
+  lo = c[0] | c[1] << 16;
+  hi = c[2] | c[3] << 16;
+  return sc;
 }
 
 template <int D, bool F8>
@@ -109,9 +125,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) write_kv_kernel(const Wr
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float amax = fmaxf(__low2float(m), __high2float(m));
-        const float sc = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
         uint32_t lo, hi;
-        quantize(w, sc, lo, hi);
+        const float sc = quantize(w, amax, lo, hi);
         if (live) {
           *reinterpret_cast<uint2 *>(to) = make_uint2(lo, hi);
           if (lane == 0) scale[static_cast<int64_t>(page) * a.c.Hkv * kPage + tok] = sc;
