@@ -2,6 +2,7 @@
 #include <cuda.h>
 
 #include <cmath>
+#include <numeric>
 
 #include "idx.h"
 #include "idx_device.cuh"
@@ -114,10 +115,17 @@ StateLayout state_layout(const idx_tree_problem *p, int32_t sel_k) {
   return L;
 }
 
-// K or V as a 4-D tensor [P][Hkv][64][D].  What the tensor core reads is swizzled by rows
-// of 128 bytes (bf16: boxes of 64 dimensions; E4M3 K of 128 dimensions) or 64 bytes (E4M3 K
-// of 64 dimensions); E4M3 V is converted in shared memory and comes as it is.  L2 fetches
-// no more around a head's row than the row, unless its tokens lie next to each other.
+// What the tensor core reads is swizzled by rows of 128 bytes (bf16: boxes of 64 dimensions;
+// E4M3 K of 128 dimensions) or 64 bytes (E4M3 K of 64 dimensions); E4M3 V is converted in
+// shared memory and comes as it is.
+CUtensorMapSwizzle cache_swizzle(const idx_kv_cache *c, bool is_v) {
+  if (c->kv_dtype == IDX_KV_BF16) return CU_TENSOR_MAP_SWIZZLE_128B;
+  if (is_v) return CU_TENSOR_MAP_SWIZZLE_NONE;
+  return c->D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+}
+
+// K or V as a 4-D tensor [P][Hkv][64][D].  L2 fetches no more around a head's row than the
+// row, unless its tokens lie next to each other.
 idx_status cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const idx_kv_cache *c, bool is_v, CUtensorMap *map) {
   void *const base = is_v ? c->v : c->k;
   const bool f8 = c->kv_dtype == IDX_KV_E4M3;
@@ -127,17 +135,56 @@ idx_status cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const idx_kv_cach
   const cuuint64_t strides[3] = {c->token_stride * e, c->head_stride * e, c->page_stride * e};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(f8 ? c->D : 64), IDX_PAGE, 1, 1};
   const cuuint32_t one[4] = {1, 1, 1, 1};
-  const CUtensorMapSwizzle swizzle = !f8 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                     : is_v ? CU_TENSOR_MAP_SWIZZLE_NONE
-                                     : c->D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   const cuuint64_t run = c->token_stride == c->D ? 256 : c->D * e;   // bytes of a head next to each other
   const CUtensorMapL2promotion promote = run >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                          : run >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
                                                       : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   const CUresult r = encode(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims,
                             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            swizzle, promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                            cache_swizzle(c, is_v), promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? IDX_OK : IDX_ECUDA;
+}
+
+// The cache as rows of equal pitch, where its strides allow: a slot's row, or its row of one
+// head, then is one row of a 2-D tensor, and four of them come with one load.  Measured with
+// 64 requests, 2,048 selected positions, E4M3: @@ us by rows, @@ us by threads' copies.
+void row_layout(const idx_kv_cache *c, idx::TreeAttnArgs *a) {
+  int64_t pitch = std::gcd(c->page_stride, c->token_stride), rows = 0;
+  int64_t row_head = 0, row_x = c->head_stride;
+  if ((c->Hkv - 1) * c->head_stride + c->D > pitch) {   // heads are rows of their own
+    pitch = std::gcd(pitch, c->head_stride);
+    row_head = c->head_stride / pitch;
+    row_x = 0;
+  }
+  const int64_t row_page = c->page_stride / pitch, row_token = c->token_stride / pitch;
+  constexpr int64_t kMost = INT32_MAX;
+  if (pitch >= c->D && row_page <= kMost / c->P && row_token <= kMost / IDX_PAGE && row_head <= kMost / c->Hkv &&
+      row_x <= kMost / c->Hkv)
+    rows = (c->P - 1) * row_page + (IDX_PAGE - 1) * row_token + (c->Hkv - 1) * row_head + 1;
+  if (rows < 1 || rows >= kMost) return;
+  a->cache_rows = rows;
+  a->row_page = static_cast<int32_t>(row_page);
+  a->row_token = static_cast<int32_t>(row_token);
+  a->row_head = static_cast<int32_t>(row_head);
+  a->row_x = static_cast<int32_t>(row_x);
+  a->row_pitch = pitch;
+}
+idx_status row_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const idx_kv_cache *c, const idx::TreeAttnArgs &a, bool is_v,
+                   CUtensorMap *map) {
+  const bool f8 = c->kv_dtype == IDX_KV_E4M3;
+  const cuuint64_t e = f8 ? 1 : 2;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>((c->Hkv - 1) * static_cast<int64_t>(a.row_x) + c->D),
+                              static_cast<cuuint64_t>(a.cache_rows)};
+  const cuuint64_t strides[1] = {a.row_pitch * e};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(f8 ? c->D : 64), 1}, one[2] = {1, 1};
+  const CUtensorMapL2promotion promote = c->D * e >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                         : c->D * e >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                           : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+  return encode(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, is_v ? c->v : c->k, dims,
+                strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, cache_swizzle(c, is_v), promote,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? IDX_OK
+             : IDX_ECUDA;
 }
 
 idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, void *out, float *lse, void *state,
@@ -165,13 +212,17 @@ idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return IDX_ECUDA;
   }
-  if (sel == nullptr) {   // selected positions are gathered by plain loads
-    st = cache_map(encode, &p->cache, false, &km);
-    if (st == IDX_OK) st = cache_map(encode, &p->cache, true, &vm);
-    if (st != IDX_OK) return st;
-  }
   uint8_t *const b = static_cast<uint8_t *>(state);
   idx::TreeAttnArgs a{};
+  if (sel == nullptr) {
+    st = cache_map(encode, &p->cache, false, &km);
+    if (st == IDX_OK) st = cache_map(encode, &p->cache, true, &vm);
+  } else if (s.rows > 0) {
+    row_layout(&p->cache, &a);
+    if (a.cache_rows > 0) st = row_map(encode, &p->cache, a, false, &km);
+    if (a.cache_rows > 0 && st == IDX_OK) st = row_map(encode, &p->cache, a, true, &vm);
+  }
+  if (st != IDX_OK) return st;
   a.p = *p;
   a.sel = sel;
   a.sel_k = sel_k;

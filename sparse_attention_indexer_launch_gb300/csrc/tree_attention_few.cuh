@@ -39,7 +39,7 @@ namespace {
 constexpr int kFewKWarp = 8, kFewIssuerWarp = 9, kFewVWarp = 11, kFewConvertWarp = 12;
 constexpr int kFewTile = 128;
 
-template <int D, bool F8, int N>
+template <int D, bool F8, int N, bool SEL>
 struct FewCfg {
   static constexpr int kTileBytes = kFewTile * D * 2;      // K or V of a tile as bf16
   static constexpr int kRawBytes = kFewTile * D;           // ... as E4M3
@@ -56,14 +56,16 @@ struct FewCfg {
   static constexpr int kVStages = F8 ? (D == 64 ? 4 : 2) : D == 64 ? 6 : N == 16 ? 4 : 2;   // as bf16
   static constexpr int kRawStages = F8 ? 4 : 0;                                             // V as E4M3
   static_assert(kKStages % 2 == 0 && kVStages % 2 == 0 && kRawStages % 2 == 0, "one waiter per stage");
-  // converting teams of four warps (64 rows leave registers for one)
-  static constexpr int kTeams = F8 && N < 64 ? 2 : 1;
+  // converting teams of four warps (64 rows leave registers for one), and the team that
+  // looks selected positions up
+  static constexpr int kTeams = !F8 ? 0 : N < 64 && !SEL ? 2 : 1;
+  static constexpr int kLookupWarp = kFewConvertWarp + 4 * kTeams;
   static constexpr int kScaleStages = F8 && D == 64 ? 8 : 4;
   static constexpr int kScaleBytes = F8 ? kScaleStages * 2 * kFewTile * 4 : 0;
-  static constexpr int kThreads = 32 * (F8 ? kFewConvertWarp + 4 * kTeams : kFewConvertWarp);
+  static constexpr int kThreads = 32 * (kLookupWarp + (SEL ? 4 : 0));
   // Registers per thread after the roles part, where a softmax thread holds a key's scores
   // and row sums; the shares add up to no more than the launch's threads x registers.
-  static constexpr bool kShareRegs = F8 || N == 64;
+  static constexpr bool kShareRegs = kThreads > 384 || N == 64;
   static constexpr int kRegsLaunch = kThreads == 384 ? 168 : kThreads == 512 ? 128 : 96;
   static constexpr int kRegsSoftmax = kThreads == 384 ? 208 : kThreads == 512 ? 176 : 144;
   static constexpr int kRegsOther = kThreads == 384 ? 88 : kThreads == 512 ? 80 : 64;
@@ -141,10 +143,10 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 }
 
 template <int D, bool F8, int N, bool SEL>
-__global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
+__global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
     few_rows_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap, const TreeAttnArgs a) {
-  using C = FewCfg<D, F8, N>;
+  using C = FewCfg<D, F8, N, SEL>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ FewBarriers<N> bars;
   uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
@@ -165,13 +167,15 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
 
   if (tid < 8) {
     const int s = tid;
-    mbar_init(&bars.k_full[s], SEL ? 33 : 1);   // (33: and the word of keys_ok)
+    // selected: four warps bring a tile, with bulk loads or each thread with its copies
+    const int loaders = !SEL ? 1 : a.cache_rows > 0 ? 4 : 128;
+    mbar_init(&bars.k_full[s], loaders);
     mbar_init(&bars.k_empty[s], 1);
-    mbar_init(&bars.v_full[s], F8 ? 4 * C::kTeams : SEL ? 32 : 1);
+    mbar_init(&bars.v_full[s], F8 ? 4 * C::kTeams : loaders);
     mbar_init(&bars.v_empty[s], 1);
-    mbar_init(&bars.raw_full[s], SEL ? 32 : 1);
-    mbar_init(&bars.raw_empty[s], 4 * C::kTeams);
-    mbar_init(&bars.sc_full[s], SEL ? 64 : 2);   // K's and V's scales
+    mbar_init(&bars.raw_full[s], loaders);
+    mbar_init(&bars.raw_empty[s], F8 ? 4 * C::kTeams : 1);
+    mbar_init(&bars.sc_full[s], SEL ? 128 : 2);   // dense: K's and V's scales
     mbar_init(&bars.sc_empty[s], 4);
     if (s < 2) {
       mbar_init(&bars.q_full[s], F8 ? 4 * C::kTeams : 1);
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
     for (int x = tid; x < C::kQBufs * C::kQBytes / 16; x += C::kThreads) reinterpret_cast<uint4 *>(sq)[x] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_shared();
   }
-  if (!SEL && tid == kFewKWarp * 32) {
+  if ((!SEL || a.cache_rows > 0) && tid == kFewKWarp * 32) {
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
   }
@@ -235,6 +239,15 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
   auto warp_arrive = [&](uint64_t *bar) {   // one arrival for the warp's threads
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
+  };
+  // The copies in flight of `used` loads through a ring of n stages land before the CTA may
+  // exit (also after giving up).
+  auto land = [&](uint64_t *bar, int n, int used) {
+    for (int s = 0; s < n; ++s) {
+      if (used <= s) continue;
+      const int last = used - 1 - (used - 1 - s) % n;
+      if (!mbar_wait(&bar[s], (last / n) & 1, limit, &never)) flag_status(a.status, kStatusTimeout);
+    }
   };
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
@@ -619,9 +632,10 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
     join_items<D>(a, bars.shares, &bars.nshare, ok);
   } else if (warp < kFewConvertWarp) {
     if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
-    if (warp == kFewKWarp || warp == kFewVWarp) {
+    if (warp == kFewKWarp || (!SEL && warp == kFewVWarp)) {
       // -------------------------------------------------------------- loads
-      // K's warp also brings a bf16 Q; each brings its own scales.
+      // K's warp also brings a bf16 Q; each brings its own scales.  Selected positions are
+      // brought by a team of their own.
       const bool is_v = warp == kFewVWarp;
       const int stages = is_v ? (F8 ? C::kRawStages : C::kVStages) : C::kKStages;
       constexpr int kBytes = C::kKBytes;       // of a load: E4M3 or bf16, K or V
@@ -656,115 +670,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
           ++nq;
         }
         const int32_t *const table = p.page_table + static_cast<int64_t>(walk.i) * p.pt_stride;
-        if constexpr (SEL) {
-          // ---------------------------------------------------------- gathering
-          const int r = walk.q.row0 + walk.tok0;
-          const uint64_t mask = p.mask != nullptr ? p.mask[r] : (2ull << walk.tok0) - 1ull;
-          const int32_t *const sel = a.sel + static_cast<int64_t>(r) * a.sel_k;
-          const int n0 = walk.tile0 * kFewTile + lane, nend = n0 - lane + walk.count * kFewTile;
-          constexpr int kPer = 4;      // keys of a tile per lane: lane, lane + 32 ..
-          // A key's way: its entry of the selection, its page, its slot; each step's load is
-          // issued a tile or more ahead of the next step, so that none is waited for.
-          auto entry = [&](int j, int x) -> int32_t {
-            const int n = n0 + (j * kPer + x) * 32;
-            return n < nend && n < a.sel_k ? sel[n] : -1;
-          };
-          auto position = [&](int j, int x, int32_t e) -> int32_t {   // logical position, -1 for none
-            const int n = n0 + (j * kPer + x) * 32;
-            if (n >= nend) return -1;
-            if (n < a.sel_k) return e >= 0 && e < walk.q.ctx ? e : -1;
-            const int u = n - a.sel_k;
-            return u < walk.q.tokens && ((mask >> u) & 1ull) && walk.q.ctx + u < walk.q.keys ? walk.q.ctx + u : -1;
-          };
-          auto page_of = [&](int32_t pos) -> int32_t { return pos >= 0 ? table[pos / kPage] : -1; };
-          int32_t pos[2][kPer], pg[2][kPer], e[2][kPer];   // tiles j, j + 1; j + 2, j + 3
-#pragma unroll
-          for (int x = 0; x < kPer; ++x) {
-            pos[0][x] = entry(0, x);
-            pos[1][x] = entry(1, x);
-            e[0][x] = entry(2, x);
-            e[1][x] = entry(3, x);
-          }
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int x = 0; x < kPer; ++x) {
-              pos[y][x] = position(y, x, pos[y][x]);
-              pg[y][x] = page_of(pos[y][x]);
-            }
-          for (int j = 0; j < walk.count; ++j) {
-            if (!warp_wait(&empty[stage], phase) ||
-                (F8 && !warp_wait(&bars.sc_empty[nload % C::kScaleStages], ((nload / C::kScaleStages) & 1) ^ 1))) {
-              ok = false;
-              break;
-            }
-            const uint32_t dst = smem_u32(ring + stage * kBytes);
-            float *const dsc = sscale + (nload % C::kScaleStages) * 2 * kFewTile;
-#pragma unroll
-            for (int x = 0; x < kPer; ++x) {
-              int32_t slot = -1;           // page * 64 + token
-              if (pos[0][x] >= 0) {
-                if (pg[0][x] >= 0 && pg[0][x] < p.cache.P) slot = pg[0][x] * kPage + pos[0][x] % kPage;
-                else flag_status(a.status, kStatusBadPage);
-              }
-              const uint32_t bits = __ballot_sync(0xffffffffu, slot >= 0);
-              if (!is_v && lane == 0) bars.keys_ok[nload & 31][x] = bits;
-              const int64_t off = slot < 0 ? -1
-                                           : (static_cast<int64_t>(slot / kPage) * p.cache.page_stride +
-                                              (slot % kPage) * p.cache.token_stride + walk.head * p.cache.head_stride) *
-                                                 (F8 ? 1 : 2);
-              if constexpr (F8) {
-                const int64_t at = slot < 0 ? 0
-                                            : (static_cast<int64_t>(slot / kPage) * Hkv + walk.head) * kPage + slot % kPage;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dsc + x * 32 + lane)),
-                             "l"(scales + at), "r"(slot < 0 ? 0 : 4)
-                             : "memory");
-              }
-              // 16 bytes per lane: D / 16 or D / 8 lanes bring one key
-              constexpr int kLanes = F8 ? D / 16 : D / 8;
-              constexpr int kKeysAtOnce = 32 / kLanes, kBatch = kLanes < 8 ? kLanes : 8;
-              const uint8_t *const cache = static_cast<const uint8_t *>(is_v ? p.cache.v : p.cache.k);
-              const int ch = lane % kLanes;
-#pragma unroll
-              for (int y0 = 0; y0 < kLanes; y0 += kBatch) {
-              int64_t offs[kBatch];      // looked up together, for the shuffles to overlap
-#pragma unroll
-              for (int y = 0; y < kBatch; ++y)
-                offs[y] = __shfl_sync(0xffffffffu, off, (y0 + y) * kKeysAtOnce + lane / kLanes);
-#pragma unroll
-              for (int y = 0; y < kBatch; ++y) {
-                const int from = (y0 + y) * kKeysAtOnce + lane / kLanes;
-                const int64_t o = offs[y];
-                const int key = x * 32 + from;
-                uint32_t at;   // bf16: blocks of 128-byte rows, swizzled; E4M3 K: rows of D, swizzled; V: rows of D
-                if (!F8) at = (ch >> 3) * kBlockBytes + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
-                else if (is_v) at = key * D + ch * 16;
-                else at = key * D + ((D == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4);
-                const uint8_t *const src = cache + (o < 0 ? 0 : o) + ch * 16;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + at), "l"(src), "r"(o < 0 ? 0 : 16)
-                             : "memory");
-              }
-              }
-            }
-            if (F8) cp_async_arrive(&bars.sc_full[nload % C::kScaleStages]);
-            cp_async_arrive(&full[stage]);
-            if (!is_v && lane == 0) mbar_arrive(&full[stage]);
-            ++nload;
-            if (++stage == stages) {
-              stage = 0;
-              phase ^= 1u;
-            }
-#pragma unroll
-            for (int x = 0; x < kPer; ++x) {
-              pos[0][x] = pos[1][x];
-              pg[0][x] = pg[1][x];
-              pos[1][x] = position(j + 2, x, e[0][x]);
-              pg[1][x] = page_of(pos[1][x]);
-              e[0][x] = e[1][x];
-              e[1][x] = entry(j + 4, x);
-            }
-          }
-        } else {
+        if constexpr (!SEL) {
           // ---------------------------------------------------------- pages by TMA
           const void *const map = is_v ? &vmap : &kmap;
           uint32_t *const oks = is_v ? bars.vpages_ok : bars.pages_ok;
@@ -821,24 +727,13 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
           }
         }
       }
-      if (SEL) asm volatile("cp.async.wait_all;" ::: "memory");
       if (!ok && lane == 0) give_up();
-      // every copy still in flight lands before the CTA may exit (also after giving up)
       if (lane == 0) {
-        auto land = [&](uint64_t *bar, int n, int used) {
-          for (int s = 0; s < n; ++s) {
-            if (used <= s) continue;
-            const int last = used - 1 - (used - 1 - s) % n;
-            if (!mbar_wait(&bar[s], (last / n) & 1, limit, &never)) flag_status(a.status, kStatusTimeout);
-          }
-        };
         land(bars.q_full, C::kQBufs, nq);
-        if (!SEL) {
-          land(full, stages, nload);
-          if (F8) land(bars.sc_full, C::kScaleStages, nload);
-        }
+        land(full, stages, nload);
+        if (F8) land(bars.sc_full, C::kScaleStages, nload);
       }
-    } else if (lane == 0) {
+    } else if (warp != kFewVWarp && lane == 0) {
       // -------------------------------------------------------------- MMA issuers
       // Per stream: S of two tiles; then, tile by tile, O += P V for each term of its P, and
       // S of the second next tile (the S it replaces has been read: its P is there).
@@ -936,6 +831,119 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
           umma_commit(&bars.drain[s]);
           if (!mbar_wait(&bars.drain[s], 0, limit, &never)) flag_status(a.status, kStatusTimeout);
         }
+      }
+    }
+  } else if (SEL && warp >= C::kLookupWarp) {
+    if constexpr (SEL) {
+      // -------------------------------------------------------------- selected positions
+      // A thread looks one key of every tile up: its entry of the selection, the page, the
+      // slot.  Each step's load is issued a tile ahead of the next step.  A warp then brings
+      // its 32 keys' K, V and scales.
+      if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
+      const int key = tid - C::kLookupWarp * 32, w4 = key >> 5;
+      constexpr int kVRing = F8 ? C::kRawStages : C::kVStages;
+      uint64_t *const vfull = F8 ? bars.raw_full : bars.v_full;
+      int k = 0;     // tiles so far
+      bool ok = true;
+      while (ok && walk.next()) {
+        const int32_t *const table = p.page_table + static_cast<int64_t>(walk.i) * p.pt_stride;
+        const int r = walk.q.row0 + walk.tok0;
+        const uint64_t mask = p.mask != nullptr ? p.mask[r] : (2ull << walk.tok0) - 1ull;
+        const int32_t *const sel = a.sel + static_cast<int64_t>(r) * a.sel_k;
+        int n = walk.tile0 * kFewTile + key;
+        const int nend = (walk.tile0 + walk.count) * kFewTile;
+        auto entry = [&](int m) -> int32_t { return m < nend && m < a.sel_k ? sel[m] : -1; };
+        auto position = [&](int m, int32_t e) -> int32_t {   // logical position, -1 for none
+          if (m < a.sel_k) return e >= 0 && e < walk.q.ctx ? e : -1;
+          const int u = m - a.sel_k;
+          return u < walk.q.tokens && ((mask >> u) & 1ull) && walk.q.ctx + u < walk.q.keys ? walk.q.ctx + u : -1;
+        };
+        int32_t pos = position(n, entry(n));
+        int32_t page = pos >= 0 ? table[pos / kPage] : -1;
+        int32_t e = entry(n + kFewTile);
+        for (; n < nend; n += kFewTile, ++k) {
+          int32_t slot = -1;           // page * 64 + token
+          if (pos >= 0) {
+            if (page >= 0 && page < p.cache.P) slot = page * kPage + pos % kPage;
+            else flag_status(a.status, kStatusBadPage);
+          }
+          pos = n + kFewTile < nend ? position(n + kFewTile, e) : -1;
+          page = pos >= 0 ? table[pos / kPage] : -1;
+          e = entry(n + 2 * kFewTile);
+          const uint32_t bits = __ballot_sync(0xffffffffu, slot >= 0);
+          const int ks = k % C::kKStages, vs = k % kVRing, ss = k % C::kScaleStages;
+          if (!warp_wait_all(&bars.k_empty[ks], ((k / C::kKStages) & 1) ^ 1) ||
+              !warp_wait_all(&(F8 ? bars.raw_empty : bars.v_empty)[vs], ((k / kVRing) & 1) ^ 1) ||
+              (F8 && !warp_wait_all(&bars.sc_empty[ss], ((k / C::kScaleStages) & 1) ^ 1))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) bars.keys_ok[k & 31][w4] = bits;
+          if constexpr (F8) {
+            const int64_t at = slot < 0 ? 0 : (static_cast<int64_t>(slot / kPage) * Hkv + walk.head) * kPage + slot % kPage;
+            const uint32_t to = smem_u32(ssc + ss * 2 * kFewTile + key);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(p.cache.k_scale + at), "r"(slot < 0 ? 0 : 4)
+                         : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + kFewTile * 4), "l"(p.cache.v_scale + at),
+                         "r"(slot < 0 ? 0 : 4)
+                         : "memory");
+            cp_async_arrive(&bars.sc_full[ss]);
+          }
+          uint8_t *const kdst = sk + ks * C::kKBytes, *const vdst = (F8 ? sraw : sv) + vs * C::kKBytes;
+          if (a.cache_rows > 0) {
+            // Four rows at a time, K by the warp's first lanes and V by the next (bf16: twice,
+            // for both blocks of 64 dimensions).  A row outside the cache reads as zero.
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&bars.k_full[ks], C::kKBytes / 4);
+              mbar_arrive_expect_tx(&vfull[vs], C::kKBytes / 4);
+            }
+            const int32_t row = slot < 0 ? static_cast<int32_t>(a.cache_rows)
+                                         : slot / kPage * a.row_page + slot % kPage * a.row_token + walk.head * a.row_head;
+            int32_t rows[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) rows[x] = __shfl_sync(0xffffffffu, row, (lane & 7) * 4 + x);
+            constexpr int kBoxes = F8 ? 1 : kBlocks, kBoxBytes = F8 ? D : 128;   // of a row
+            const int x = lane >> 3, b = x % kBoxes;
+            const bool is_v = x >= kBoxes;
+            if (x < 2 * kBoxes)
+              tma_gather4((is_v ? vdst : kdst) + b * kBlockBytes + (w4 * 32 + (lane & 7) * 4) * kBoxBytes, is_v ? &vmap : &kmap,
+                          walk.head * a.row_x + b * 64, rows[0], rows[1], rows[2], rows[3], is_v ? &vfull[vs] : &bars.k_full[ks]);
+            __syncwarp();
+          } else {
+            // 16 bytes per thread: D / 16 or D / 8 lanes bring one key
+            constexpr int kLanes = F8 ? D / 16 : D / 8, kKeysAtOnce = 32 / kLanes;
+            const int ch = lane % kLanes;
+            const int64_t off = slot < 0 ? -1
+                                         : (slot / kPage * p.cache.page_stride + slot % kPage * p.cache.token_stride +
+                                            walk.head * p.cache.head_stride) *
+                                               (F8 ? 1 : 2);
+#pragma unroll 4
+            for (int y = 0; y < kLanes; ++y) {
+              const int from = y * kKeysAtOnce + lane / kLanes, at_key = w4 * 32 + from;
+              const int64_t o = __shfl_sync(0xffffffffu, off, from);
+              // bf16: blocks of 128-byte rows, swizzled; E4M3 K: rows of D, swizzled; V: rows of D
+              const uint32_t kat = !F8 ? (ch >> 3) * kBlockBytes + at_key * 128 + (((ch & 7) ^ (at_key & 7)) << 4)
+                                       : at_key * D + ((D == 128 ? ch ^ (at_key & 7) : ch ^ ((at_key >> 1) & 3)) << 4);
+              const uint32_t vat = !F8 ? kat : at_key * D + ch * 16;
+              const int64_t src = (o < 0 ? 0 : o) + ch * 16;
+              const int bytes = o < 0 ? 0 : 16;
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(kdst + kat)),
+                           "l"(static_cast<const uint8_t *>(p.cache.k) + src), "r"(bytes)
+                           : "memory");
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(vdst + vat)),
+                           "l"(static_cast<const uint8_t *>(p.cache.v) + src), "r"(bytes)
+                           : "memory");
+            }
+            cp_async_arrive(&bars.k_full[ks]);
+            cp_async_arrive(&vfull[vs]);
+          }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!ok && lane == 0) give_up();
+      if (lane == 0 && a.cache_rows > 0) {
+        land(bars.k_full, C::kKStages, k);
+        land(vfull, kVRing, k);
       }
     }
   } else {
@@ -1105,7 +1113,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N>::kThreads, 1)
 template <int D, bool F8, int N, bool SEL>
 cudaError_t launch_few_rows(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm,
                             int num_ctas, cudaStream_t stream) {
-  using C = FewCfg<D, F8, N>;
+  using C = FewCfg<D, F8, N, SEL>;
   static std::mutex mu;
   static bool done[128] = {};
   const cudaError_t e = once_per_device(mu, done, [] {
