@@ -198,7 +198,7 @@ constexpr int kMinKeys = 256;   // keys of a CTA's share, at least (fewer CTAs o
 struct Shares {
   int W, n, per, rest;
   __device__ __forceinline__ Shares(int tiles, int tile, int ctas) : W(tiles) {
-    const int least = kMinKeys / tile;
+    const int least = tiles <= ctas ? 1 : kMinKeys / tile;
     n = max(1, min((tiles + least - 1) / least, ctas));
     per = W / n;
     rest = W - per * n;
@@ -356,6 +356,7 @@ __device__ __forceinline__ Share share_of(const Walk &w, const Shares &sh, int G
 template <int D>
 __device__ __forceinline__ void join_items(const TreeAttnArgs &a, const Share *shares, const int *count, bool ok) {
   const idx_tree_problem &p = a.p;
+  constexpr int kBatch = 8;   // shares whose loads are in flight together
   const int lane = threadIdx.x & 31;
   const int G = p.Hq / p.cache.Hkv;
   const int slot_rows = a.pair ? 256 : 128;
@@ -397,11 +398,11 @@ __device__ __forceinline__ void join_items(const TreeAttnArgs &a, const Share *s
       const int prow = a.pair && tok >= tb ? 128 + row - tb * G : row;
       float m = -INFINITY, l = 0.0f;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int c0 = live ? sub : s.count; c0 < s.count; c0 += 4 * lanes) {
-        float2 ml[4];
-        float4 o[4];
+      for (int c0 = live ? sub : s.count; c0 < s.count; c0 += kBatch * lanes) {
+        float2 ml[kBatch];
+        float4 o[kBatch];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int y = 0; y < kBatch; ++y) {
           const int c = c0 + y * lanes;
           ml[y] = make_float2(-INFINITY, 0.0f);
           o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -411,7 +412,7 @@ __device__ __forceinline__ void join_items(const TreeAttnArgs &a, const Share *s
           o[y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D + d));
         }
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int y = 0; y < kBatch; ++y) {
           const float nm = fmaxf(m, ml[y].x);
           const float f = ml[y].x == -INFINITY ? 0.0f : ex2(ml[y].x - nm), keep = m == -INFINITY ? 0.0f : ex2(m - nm);
           m = nm;

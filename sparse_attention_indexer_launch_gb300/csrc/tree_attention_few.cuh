@@ -306,14 +306,16 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
         }
         // rows that see the key
         uint64_t seen = ~0ull;
-        bool special;
+        bool special, open;     // open: every row sees the tile's first key
         if (SEL) {
           const uint32_t *const w = bars.keys_ok[k & 31];
           special = (w[0] & w[1] & w[2] & w[3]) != ~0u;
+          open = w[0] & 1u;
           if (!((w[w4] >> lane) & 1u)) seen = 0ull;
         } else {
           const uint32_t pages = bars.pages_ok[k & 31];
           special = key0 + kFewTile > ctx || pages != 3u;
+          open = key0 < ctx && (pages & 1u);
           if (special) {
             const int pos = key0 + key;
             if (pos >= walk.q.keys || !((pages >> (key >> 6)) & 1u)) {
@@ -321,6 +323,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
             } else if (pos >= ctx) {
               const int u = pos - ctx;
               seen = 0ull;
+#pragma unroll 4
               for (int t = 0; t < walk.tokens; ++t) {
                 const bool sees = p.mask != nullptr ? (p.mask[row0 + t] >> u) & 1ull : u <= walk.tok0 + t;
                 if (sees) seen |= (G == 64 ? ~0ull : (1ull << G) - 1ull) << (t * G);
@@ -335,13 +338,13 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
         // passes its reference by too much; if so pass 1 takes the scores themselves, for
         // the rows' maxima, and pass 2 the scores relative to the raised references.
         float e[N];
-        if (h == h0 && !special) {
-          // a full first tile: the references are its first key's scores
+        if (h == h0 && open) {
+          // the first tile: the references are its first key's scores
           if (key == 0) {
 #pragma unroll
             for (int r = 0; r < N; ++r) {
               const float m = __uint_as_float(x[r]) * ck * (F8 ? qs[r] : 1.0f);
-              const bool fine = m - m == 0.0f;    // else the row's maximum is taken below
+              const bool fine = m - m == 0.0f;    // else the row's maximum is taken below (+INFINITY asks for it)
               bars.ref[s][r] = fine ? m : -INFINITY;
               neg[r] = fine ? -m : INFINITY;
             }
@@ -450,30 +453,40 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
           const int pos = key0 + key;
           const bool dead = pos >= walk.q.keys || !((bars.pages_ok[k & 31] >> (key >> 6)) & 1u);
           if (ok && (dead || pos >= ctx)) {
+            auto chunk = [&](int y) -> uint4 * {
+              return reinterpret_cast<uint4 *>(sv + sl * C::kTileBytes + (y >> 3) * kBlockBytes + key * 128 +
+                                               ((y + key) & 7) * 16);
+            };
+            bool bad = false;
+            if (!dead) {   // 0 x a value is NaN where it is not finite
+              __nv_bfloat162 z = __float2bfloat162_rn(0.0f);
 #pragma unroll 4
-            for (int y = 0; y < kBlocks * 8; ++y) {
-              uint4 *const at = reinterpret_cast<uint4 *>(sv + sl * C::kTileBytes + (y >> 3) * kBlockBytes + key * 128 +
-                                                          ((y + key) & 7) * 16);
-              uint4 v = dead ? make_uint4(0, 0, 0, 0) : *at;
-              if (!dead) {
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                bool changed = false;
+              for (int y = 0; y < kBlocks * 8; ++y) {
+                const uint4 v = *chunk(y);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  if ((w[z] & 0x7F80u) == 0x7F80u) {
-                    w[z] &= 0xFFFF0000u;
-                    changed = true;
-                  }
-                  if ((w[z] & 0x7F800000u) == 0x7F800000u) {
-                    w[z] &= 0xFFFFu;
-                    changed = true;
+                for (int x = 0; x < 4; ++x)
+                  z = __hfma2(reinterpret_cast<const __nv_bfloat162 &>(w[x]), __float2bfloat162_rn(0.0f), z);
+              }
+              bad = __hisnan(__low2bfloat16(z)) || __hisnan(__high2bfloat16(z));
+            }
+            if (dead || bad) {
+#pragma unroll 1
+              for (int y = 0; y < kBlocks * 8; ++y) {
+                uint4 *const at = chunk(y);
+                uint32_t w[4] = {};
+                if (bad) {
+                  const uint4 v = *at;
+                  w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    if ((w[x] & 0x7F80u) == 0x7F80u) w[x] &= 0xFFFF0000u;
+                    if ((w[x] & 0x7F800000u) == 0x7F800000u) w[x] &= 0xFFFFu;
                   }
                 }
-                if (!changed) continue;
-                bars.nonfinite[walk.seg & 31] = walk.seg + 1;
-                v = make_uint4(w[0], w[1], w[2], w[3]);
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
               }
-              *at = v;
+              if (bad) bars.nonfinite[walk.seg & 31] = walk.seg + 1;
             }
           }
           __syncwarp();
@@ -572,6 +585,17 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       const uint32_t o0 = tmem + kColO + lanes;
       const int odd = tiles & 1;      // (of the segment's first tile)
       const bool has0 = odd < walk.count, has1 = (odd ^ 1) < walk.count;   // the streams that had tiles
+      // an item's rows are G heads of consecutive tokens
+      uint16_t *const out = a.out + (static_cast<int64_t>(row0) * p.Hq + walk.head * G) * D + d;
+      float *const part = a.part_o + static_cast<int64_t>(slot) * 128 * D + d;
+      auto put = [&](int row, float o) {
+        if (!walk.whole) {
+          part[row * D] = o;
+        } else {
+          const int tok = row / G;
+          out[static_cast<int64_t>(tok * p.Hq + row - tok * G) * D] = static_cast<uint16_t>(pack_bf16(o * bars.join[s][2][row], 0.0f));
+        }
+      };
 #pragma unroll 1
       for (int g = s * (N / 2); g < (s + 1) * (N / 2); g += 8) {
         if (g >= nrow) break;
@@ -590,12 +614,16 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
           if (D == 64 && ((r >> 2) != (key >> 6))) continue;
           const int row = g + r;
           if (row >= nrow || !ok) continue;
-          const float f0 = bars.join[s][0][row], f1 = bars.join[s][1][row], inv = bars.join[s][2][row];
+          const float f0 = bars.join[s][0][row], f1 = bars.join[s][1][row];
           float o = f0 == 0.0f || !has0 ? 0.0f : __uint_as_float(x0[r]) * f0;
           if (has1) o += f1 == 0.0f ? 0.0f : __uint_as_float(x1[r]) * f1;
-          if (inv == 0.0f) o = 0.0f;
-          const int tok = row / G, hq = walk.head * G + row - tok * G;
-          if (poison) {   // what was zeroed for the rows that do not see it
+          if (bars.join[s][2][row] == 0.0f) o = 0.0f;
+          if (!poison) {
+            put(row, o);
+            continue;
+          }
+          const int tok = row / G;
+          {   // what was zeroed for the rows that do not see it
             const int t = walk.tok0 + tok;
             const uint64_t mask = p.mask != nullptr ? p.mask[row0 + tok] : (2ull << t) - 1ull;
             for (int u = 0; u < walk.q.tokens; ++u) {
@@ -613,10 +641,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
               if (!isfinite(v)) o += v;
             }
           }
-          if (walk.whole)
-            a.out[(static_cast<int64_t>(row0 + tok) * p.Hq + hq) * D + d] = static_cast<uint16_t>(pack_bf16(o * inv, 0.0f));
-          else
-            a.part_o[(static_cast<int64_t>(slot) * 128 + row) * D + d] = o;
+          put(row, o);
         }
       }
       tc_fence_before();
