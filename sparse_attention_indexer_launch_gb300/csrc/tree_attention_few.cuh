@@ -46,13 +46,7 @@ struct FewCfg {
   static constexpr int kKBytes = F8 ? kRawBytes : kTileBytes;
   static constexpr int kQBytes = N * D * 2;                // bf16, or the two E4M3 terms
   static constexpr int kPBytes = kFewTile * N * 2;         // P^T of a tile
-  // Tiles of a stream that a softmax thread takes at a time: one tile's chain of waits and
-  // barriers leaves the issue slots idle, two overlap (64 rows leave no registers for it).
-  // Not so for selected positions: K and V come together there, and S of that many tiles
-  // ahead would wait for a V that waits for the products before.
-  static constexpr int kHalves = 1;
-  static constexpr int kSBufs = 2 * kHalves;               // per stream, as P's
-  static constexpr int kPBufs = N == 64 ? 1 : 2;
+  static constexpr int kPBufs = N == 64 ? 1 : 2;           // per stream
   static constexpr int kQBufs = F8 && N == 64 ? 1 : 2;
   static constexpr int kFixed = kQBufs * kQBytes + 2 * kPBufs * kPBytes;
   // Tiles in flight, as shared memory allows.  The streams take alternate tiles, so the counts are even: a stage then always has the same waiter.  Were
@@ -84,7 +78,7 @@ template <int N>
 struct FewBarriers {
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], raw_full[8], raw_empty[8], sc_full[8], sc_empty[8];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2][4];                    // [stream][S buffer]
+  uint64_t s_full[2][2];                    // [stream][S buffer]
   uint64_t p_ready[2][2], pv_done[2][2];    // [stream][P buffer]
   uint64_t o_free[2], drain[2], stats[2], scrubbed[2];
   uint32_t tmem_base;
@@ -169,7 +163,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
   const int tb = a.item_tokens;              // tokens of an item, tb * G <= N rows
   constexpr int kBlocks = D / 64;            // 64-dimension blocks of a bf16 operand
   constexpr int kBlockBytes = kFewTile * 128, kQBlockBytes = N * 128;
-  constexpr uint32_t kColO = 2 * C::kSBufs * N;   // S: [stream][buffer] x N columns, then O: [stream] x N
+  constexpr uint32_t kColO = 4 * N;          // S: [stream][buffer] x N columns, then O: [stream] x N
 
   if (tid < 8) {
     const int s = tid;
@@ -186,8 +180,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
     if (s < 2) {
       mbar_init(&bars.q_full[s], F8 ? 4 * C::kTeams : 1);
       mbar_init(&bars.q_empty[s], 2);
-      for (int b = 0; b < 4; ++b) mbar_init(&bars.s_full[s][b], 1);
       for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars.s_full[s][b], 1);
         mbar_init(&bars.p_ready[s][b], 4);
         mbar_init(&bars.pv_done[s][b], 1);
       }
@@ -290,51 +284,39 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       for (int r = 0; r < N; ++r) l[r] = 0.0f;
       const uint32_t h0 = h;
       bool left = false;
-      for (int j = (s ^ tiles) & 1; j < walk.count; j += 2 * C::kHalves) {   // the CTA's even or odd tiles
-        constexpr int kH = C::kHalves;
-        const int nhalf = min(kH, (walk.count - j + 1) / 2);
-        float ck[kH], vs[kH];
-        uint64_t seen[kH];             // rows that see the key
-        bool special[kH];
-        bool open = false;             // every row sees the first tile's first key
-#pragma unroll
-        for (int hf = 0; hf < kH; ++hf) {
-          const int k = tiles + j + 2 * hf;
-          const int key0 = (walk.tile0 + j + 2 * hf) * kFewTile;
-          ck[hf] = c;
-          vs[hf] = 1.0f;
-          seen[hf] = 0ull;
-          special[hf] = true;
-          if (hf >= nhalf) continue;
-          if (F8) {
-            ok = ok && warp_wait_all(&bars.sc_full[k % C::kScaleStages], (k / C::kScaleStages) & 1);
-            ck[hf] = c * ssc[(k % C::kScaleStages) * 2 * kFewTile + key];
-            vs[hf] = ssc[(k % C::kScaleStages) * 2 * kFewTile + kFewTile + key];
-            warp_arrive(&bars.sc_empty[k % C::kScaleStages]);
-          }
-          ok = ok && warp_wait_all(&bars.s_full[s][(n + hf) % C::kSBufs], ((n + hf) / C::kSBufs) & 1);
-          seen[hf] = ~0ull;
-          if (SEL) {
-            const uint32_t *const w = bars.keys_ok[k & 31];
-            special[hf] = (w[0] & w[1] & w[2] & w[3]) != ~0u;
-            if (hf == 0) open = w[0] & 1u;
-            if (!((w[w4] >> lane) & 1u)) seen[hf] = 0ull;
-          } else {
-            const uint32_t pages = bars.pages_ok[k & 31];
-            special[hf] = key0 + kFewTile > ctx || pages != 3u;
-            if (hf == 0) open = key0 < ctx && (pages & 1u);
-            if (special[hf]) {
-              const int pos = key0 + key;
-              if (pos >= walk.q.keys || !((pages >> (key >> 6)) & 1u)) {
-                seen[hf] = 0ull;
-              } else if (pos >= ctx) {
-                const int u = pos - ctx;
-                seen[hf] = 0ull;
+      for (int j = (s ^ tiles) & 1; j < walk.count; j += 2, ++n) {   // the CTA's even or odd tiles
+        const int k = tiles + j;
+        const int key0 = (walk.tile0 + j) * kFewTile;
+        float ck = c, vs = 1.0f;
+        if (F8) {
+          ok = ok && warp_wait_all(&bars.sc_full[k % C::kScaleStages], (k / C::kScaleStages) & 1);
+          ck = c * ssc[(k % C::kScaleStages) * 2 * kFewTile + key];
+          vs = ssc[(k % C::kScaleStages) * 2 * kFewTile + kFewTile + key];
+          warp_arrive(&bars.sc_empty[k % C::kScaleStages]);
+        }
+        ok = ok && warp_wait_all(&bars.s_full[s][n & 1], (n >> 1) & 1);
+        uint64_t seen = ~0ull;         // rows that see the key
+        bool special, open;            // open: every row sees the tile's first key
+        if (SEL) {
+          const uint32_t *const w = bars.keys_ok[k & 31];
+          special = (w[0] & w[1] & w[2] & w[3]) != ~0u;
+          open = w[0] & 1u;
+          if (!((w[w4] >> lane) & 1u)) seen = 0ull;
+        } else {
+          const uint32_t pages = bars.pages_ok[k & 31];
+          special = key0 + kFewTile > ctx || pages != 3u;
+          open = key0 < ctx && (pages & 1u);
+          if (special) {
+            const int pos = key0 + key;
+            if (pos >= walk.q.keys || !((pages >> (key >> 6)) & 1u)) {
+              seen = 0ull;
+            } else if (pos >= ctx) {
+              const int u = pos - ctx;
+              seen = 0ull;
 #pragma unroll 4
-                for (int t = 0; t < walk.tokens; ++t) {
-                  const bool sees = p.mask != nullptr ? (p.mask[row0 + t] >> u) & 1ull : u <= walk.tok0 + t;
-                  if (sees) seen[hf] |= (G == 64 ? ~0ull : (1ull << G) - 1ull) << (t * G);
-                }
+              for (int t = 0; t < walk.tokens; ++t) {
+                const bool sees = p.mask != nullptr ? (p.mask[row0 + t] >> u) & 1ull : u <= walk.tok0 + t;
+                if (sees) seen |= (G == 64 ? ~0ull : (1ull << G) - 1ull) << (t * G);
               }
             }
           }
@@ -343,32 +325,27 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
         // Scores relative to the references, in units of log2.  Pass 0 finds whether any
         // passes its reference by too much; if so pass 1 takes the scores themselves, for
         // the rows' maxima, and pass 2 the scores relative to the raised references.
-        float e[kH][N];
+        float e[N];
 #pragma unroll 1
         for (int pass = 0;; ++pass) {
-          uint32_t x[kH][N];
+          uint32_t x[N];
           __syncwarp();
+          const uint32_t ts = tmem + (2 * s + (n & 1)) * N + lanes;
+          if constexpr (N == 16) {
+            tmem_ld16(ts, x);
+          } else {
 #pragma unroll
-          for (int hf = 0; hf < kH; ++hf) {
-            const uint32_t ts = tmem + (C::kSBufs * s + (n + hf) % C::kSBufs) * N + lanes;
-            if constexpr (N == 16) {
-              tmem_ld16(ts, x[hf]);
-            } else {
-#pragma unroll
-              for (int g = 0; g < N; g += 32) tmem_ld32(ts + g, *reinterpret_cast<uint32_t(*)[32]>(&x[hf][g]));
-            }
+            for (int g = 0; g < N; g += 32) tmem_ld32(ts + g, *reinterpret_cast<uint32_t(*)[32]>(&x[g]));
           }
           tmem_wait_ld();
 #pragma unroll
-          for (int hf = 0; hf < kH; ++hf)
-#pragma unroll
-            for (int r = 0; r < N; ++r) asm volatile("" : "+r"(x[hf][r]));
+          for (int r = 0; r < N; ++r) asm volatile("" : "+r"(x[r]));
           if (pass == 0 && h == h0 && open) {
             // the first tile: the references are its first key's scores
             if (key == 0) {
 #pragma unroll
               for (int r = 0; r < N; ++r) {
-                const float m = __uint_as_float(x[0][r]) * ck[0] * (F8 ? qs[r] : 1.0f);
+                const float m = __uint_as_float(x[r]) * ck * (F8 ? qs[r] : 1.0f);
                 const bool fine = m - m == 0.0f;    // else the row's maximum is taken below (+INFINITY asks for it)
                 bars.ref[s][r] = fine ? m : -INFINITY;
                 neg[r] = fine ? -m : INFINITY;
@@ -380,42 +357,34 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
 #pragma unroll
           for (int r = 0; r < N; r += 4) {
             const float4 m = *reinterpret_cast<const float4 *>(neg + r);
-            float4 q = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-            if (F8) q = *reinterpret_cast<const float4 *>(qs + r);
-#pragma unroll
-            for (int hf = 0; hf < kH; ++hf) {
-              float2 e0, e1;
-              const float2 x0 = make_float2(__uint_as_float(x[hf][r]), __uint_as_float(x[hf][r + 1]));
-              const float2 x1 = make_float2(__uint_as_float(x[hf][r + 2]), __uint_as_float(x[hf][r + 3]));
-              const float2 cc = make_float2(ck[hf], ck[hf]);
-              if (F8) {
-                e0 = __ffma2_rn(__fmul2_rn(x0, cc), make_float2(q.x, q.y), make_float2(m.x, m.y));
-                e1 = __ffma2_rn(__fmul2_rn(x1, cc), make_float2(q.z, q.w), make_float2(m.z, m.w));
-              } else {
-                e0 = __ffma2_rn(x0, cc, make_float2(m.x, m.y));
-                e1 = __ffma2_rn(x1, cc, make_float2(m.z, m.w));
-              }
-              e[hf][r] = e0.x;
-              e[hf][r + 1] = e0.y;
-              e[hf][r + 2] = e1.x;
-              e[hf][r + 3] = e1.y;
+            float2 e0, e1;
+            const float2 x0 = make_float2(__uint_as_float(x[r]), __uint_as_float(x[r + 1]));
+            const float2 x1 = make_float2(__uint_as_float(x[r + 2]), __uint_as_float(x[r + 3]));
+            const float2 cc = make_float2(ck, ck);
+            if (F8) {
+              const float4 q = *reinterpret_cast<const float4 *>(qs + r);
+              e0 = __ffma2_rn(__fmul2_rn(x0, cc), make_float2(q.x, q.y), make_float2(m.x, m.y));
+              e1 = __ffma2_rn(__fmul2_rn(x1, cc), make_float2(q.z, q.w), make_float2(m.z, m.w));
+            } else {
+              e0 = __ffma2_rn(x0, cc, make_float2(m.x, m.y));
+              e1 = __ffma2_rn(x1, cc, make_float2(m.z, m.w));
             }
+            e[r] = e0.x;
+            e[r + 1] = e0.y;
+            e[r + 2] = e1.x;
+            e[r + 3] = e1.y;
           }
+          if (special) {
 #pragma unroll
-          for (int hf = 0; hf < kH; ++hf)
-            if (special[hf]) {
-#pragma unroll
-              for (int r = 0; r < N; ++r)
-                if (!((static_cast<uint32_t>(seen[hf] >> (r & 32)) >> (r & 31)) & 1u)) e[hf][r] = -INFINITY;
-            }
+            for (int r = 0; r < N; ++r)
+              if (!((static_cast<uint32_t>(seen >> (r & 32)) >> (r & 31)) & 1u)) e[r] = -INFINITY;
+          }
           if (pass == 2) break;
           if (pass == 0) {
 #pragma unroll
-            for (int hf = 0; hf < kH; ++hf)
+            for (int r = 0; r < N; r += 8)
 #pragma unroll
-              for (int r = 0; r < N; r += 8)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], e[hf][r + 2 * z], e[hf][r + 2 * z + 1]);
+              for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], e[r + 2 * z], e[r + 2 * z + 1]);
             const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
             if (!team_any(s, !ok || top > kLazy)) break;
             if (team_any(s, !ok)) {
@@ -430,7 +399,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
           float mine[(N + 31) / 32] = {};
 #pragma unroll
           for (int r = 0; r < N; ++r) {
-            const float m = warp_max_all(kH == 1 ? e[0][r] : fmaxf(e[0][r], e[kH - 1][r]));
+            const float m = warp_max_all(e[r]);
             if (lane == (r & 31)) mine[r >> 5] = m;
           }
 #pragma unroll
@@ -479,11 +448,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
         // V of tokens that some rows do not see has to be finite (0 x NaN is NaN): zero
         // what no row sees, and what is not finite among the drafted tokens (rows that
         // see it get it back at the end)
-        if (!SEL && !F8) {
-#pragma unroll 1
-          for (int hf = 0; hf < nhalf; ++hf) {
-            if (!(hf == 0 ? special[0] : special[kH - 1])) continue;
-            const int k = tiles + j + 2 * hf, key0 = (walk.tile0 + j + 2 * hf) * kFewTile;
+        if (!SEL && !F8 && special) {
           const int sl = k % C::kVStages;
           ok = ok && warp_wait_all(&bars.v_full[sl], (k / C::kVStages) & 1);
           const int pos = key0 + key;
@@ -526,60 +491,51 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
             }
           }
           __syncwarp();
-          }
         }
         // P.  It is rounded to bf16 for the product with V.  Over the 128 or more keys of
         // a full tile the roundings average out below the output's own; the few keys of a
         // special tile do not, so there a second hand-over brings what the rounding left.
 #pragma unroll
-        for (int hf = 0; hf < kH; ++hf) {
-#pragma unroll
-          for (int r = 0; r < N; r += 2) {
-            const float2 y = make_float2(ex2(e[hf][r]), ex2(e[hf][r + 1]));
-            const float2 sum = __fadd2_rn(make_float2(l[r], l[r + 1]), y);
-            l[r] = sum.x;
-            l[r + 1] = sum.y;
-            const float2 z = F8 ? __fmul2_rn(y, make_float2(vs[hf], vs[hf])) : y;
-            e[hf][r] = z.x;
-            e[hf][r + 1] = z.y;
-          }
-          if (F8 && special[hf]) {   // a stale scale may be NaN
-#pragma unroll
-            for (int r = 0; r < N; ++r)
-              if (!((static_cast<uint32_t>(seen[hf] >> (r & 32)) >> (r & 31)) & 1u)) e[hf][r] = 0.0f;
-          }
+        for (int r = 0; r < N; r += 2) {
+          const float2 y = make_float2(ex2(e[r]), ex2(e[r + 1]));
+          const float2 sum = __fadd2_rn(make_float2(l[r], l[r + 1]), y);
+          l[r] = sum.x;
+          l[r + 1] = sum.y;
+          const float2 z = F8 ? __fmul2_rn(y, make_float2(vs, vs)) : y;
+          e[r] = z.x;
+          e[r + 1] = z.y;
         }
+        if (F8 && special) {   // a stale scale may be NaN
 #pragma unroll
-        for (int hf = 0; hf < kH; ++hf) {
-          if (hf >= nhalf) break;
+          for (int r = 0; r < N; ++r)
+            if (!((static_cast<uint32_t>(seen >> (r & 32)) >> (r & 31)) & 1u)) e[r] = 0.0f;
+        }
 #pragma unroll 1
-          for (int more = special[hf]; more >= 0; --more) {
-            // the buffer's product before has to have completed
-            if (h - h0 >= C::kPBufs) ok = ok && settled(h - C::kPBufs);
-            uint8_t *const row = sp + (s * C::kPBufs + h % C::kPBufs) * C::kPBytes + key * (2 * N);
+        for (int more = special; more >= 0; --more) {
+          // the buffer's product before has to have completed
+          if (h - h0 >= C::kPBufs) ok = ok && settled(h - C::kPBufs);
+          uint8_t *const row = sp + (s * C::kPBufs + h % C::kPBufs) * C::kPBytes + key * (2 * N);
 #pragma unroll
-            for (int r = 0; r < N; r += 8) {
-              uint32_t w[4];
+          for (int r = 0; r < N; r += 8) {
+            uint32_t w[4];
 #pragma unroll
-              for (int z = 0; z < 4; ++z) w[z] = pack_bf16(e[hf][r + 2 * z], e[hf][r + 2 * z + 1]);
-              const int sw = N == 64 ? key & 7 : N == 32 ? (key >> 1) & 3 : (key >> 2) & 1;
-              *reinterpret_cast<uint4 *>(row + (((r >> 3) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            if (key == 0) bars.two_terms[s][h % C::kPBufs] = more;
-            fence_proxy_async_shared();
-            tc_fence_before();
-            warp_arrive(&bars.p_ready[s][h % C::kPBufs]);
-            ++h;
-            if (more) {   // what the rounding left (an infinity, of a scale, leaves nothing)
+            for (int z = 0; z < 4; ++z) w[z] = pack_bf16(e[r + 2 * z], e[r + 2 * z + 1]);
+            const int sw = N == 64 ? key & 7 : N == 32 ? (key >> 1) & 3 : (key >> 2) & 1;
+            *reinterpret_cast<uint4 *>(row + (((r >> 3) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (key == 0) bars.two_terms[s][h % C::kPBufs] = more;
+          fence_proxy_async_shared();
+          tc_fence_before();
+          warp_arrive(&bars.p_ready[s][h % C::kPBufs]);
+          ++h;
+          if (more) {   // what the rounding left (an infinity, of a scale, leaves nothing)
 #pragma unroll
-              for (int r = 0; r < N; ++r) {
-                const float rest = e[hf][r] - __bfloat162float(__float2bfloat16_rn(e[hf][r]));
-                e[hf][r] = rest == rest ? rest : 0.0f;
-              }
+            for (int r = 0; r < N; ++r) {
+              const float rest = e[r] - __bfloat162float(__float2bfloat16_rn(e[r]));
+              e[r] = rest == rest ? rest : 0.0f;
             }
           }
         }
-        n += nhalf;
       }
       if (left) break;
 
@@ -811,8 +767,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       }
     } else if (warp != kFewVWarp && lane == 0) {
       // -------------------------------------------------------------- MMA issuers
-      // Per stream: S of as many tiles as there are buffers; then, tile by tile, O += P V for
-      // each term of its P, and the next S in its buffer (which has been read: its P is there).
+      // Per stream: S of two tiles; then, tile by tile, O += P V for each term of its P, and
+      // S of the second next tile (the S it replaces has been read: its P is there).
       const int s = warp - kFewIssuerWarp;
       const uint32_t to = tmem + kColO + s * N;
       constexpr uint32_t kAMn = 1u << 15;
@@ -837,7 +793,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
           if (!mbar_wait(&bars.k_full[sl], (k / C::kKStages) & 1, limit, abort)) return false;
           if (SEL) fence_proxy_async_shared();   // the gatherers' copies
           tc_fence_after();
-          const uint32_t d = tmem + (C::kSBufs * s + ns % C::kSBufs) * N;
+          const uint32_t d = tmem + (2 * s + (ns & 1)) * N;
           const uint32_t kaddr = smem_u32(sk + sl * C::kKBytes);
           if constexpr (F8) {
             // both terms of Q over the same keys: D = 128: 128-byte rows, the terms a block
@@ -857,14 +813,14 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
               umma_f16(d, kdesc + (((kk >> 2) * kBlockBytes + (kk & 3) * 32) >> 4),
                        qdesc + (((kk >> 2) * kQBlockBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
           }
-          umma_commit(&bars.s_full[s][ns % C::kSBufs]);
+          umma_commit(&bars.s_full[s][ns & 1]);
           umma_commit(&bars.k_empty[sl]);
           if (j + 2 >= walk.count) umma_commit(&bars.q_empty[qb]);
           any = true;
           ++ns;
           return true;
         };
-        for (int j = j0; ok && j < walk.count && j < j0 + 2 * C::kSBufs; j += 2) ok = scores(j);
+        for (int j = j0; ok && j < walk.count && j < j0 + 4; j += 2) ok = scores(j);
         for (int j = j0; ok && j < walk.count; j += 2) {
           const int k = tiles + j, sl = k % C::kVStages;
           bool more = true;
@@ -897,7 +853,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
           }
           if (!ok) break;
           umma_commit(&bars.v_empty[sl]);
-          if (j + 2 * C::kSBufs < walk.count) ok = scores(j + 2 * C::kSBufs);
+          if (j + 4 < walk.count) ok = scores(j + 4);
         }
         tiles += walk.count;
       }
