@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from sys import modules as _modules
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libidx.so")
@@ -161,6 +162,15 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _current(stream):
+    """The stream's handle as an integer; the current device's current stream for None.
+    (Calls of a few microseconds: no Stream object is made.)"""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _modules["torch"]   # the caller's tensors come from it
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 def make_problem(q, w, k_cache, k_scale, page_table, row_req, row_bound, max_bound: int,
                  kv_dtype: int, P: int | None = None, rows_hint: int = 0) -> Problem:
     """idx_problem from tensors (device tensors for the device calls, host tensors
@@ -298,7 +308,7 @@ def tree_tables_state_size() -> int:
 def idx_tree_tables(tables: TreeTables, state, stream=None):
     """Page tables, slots and masks of a step (see idx.h); `state` from
     alloc_state(tree_tables_state_size())."""
-    _check(lib.idx_tree_tables(ctypes.byref(tables), state.data_ptr(), state.nbytes, _stream(stream)),
+    _check(lib.idx_tree_tables(ctypes.byref(tables), state.data_ptr(), state.nbytes, _current(stream)),
            "idx_tree_tables")
 
 
@@ -327,19 +337,22 @@ def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
 def idx_write_kv(cache: KvCache, k_new, v_new, slot, stream=None):
     """Writes k_new and v_new (bf16 [R][Hkv][D], rows of equal stride) into the cache
     at slot [R] (see idx.h)."""
-    import torch
-    R, shape = slot.shape[0], (slot.shape[0], cache.Hkv, cache.D)
-    for x in (k_new, v_new):
-        st = x.stride()
-        if x.dtype != torch.bfloat16 or x.shape != shape or st[2] != 1 or (st[1] != cache.D and cache.Hkv > 1):
-            raise ValueError("k_new, v_new: bf16 [R][Hkv][D] with contiguous heads is wanted")
-    if slot.dtype != torch.int32 or not slot.is_contiguous():
-        raise ValueError("slot: a contiguous int32 tensor is wanted")
-    stride = k_new.stride(0) if R > 1 else cache.Hkv * cache.D
-    if R > 1 and v_new.stride(0) != stride:
+    torch = _modules["torch"]
+    R, Hkv, D = slot.numel(), cache.Hkv, cache.D
+    st, sv = k_new.stride(), v_new.stride()
+    for dtype, shape in ((k_new.dtype, k_new.shape), (v_new.dtype, v_new.shape)):
+        if dtype is not torch.bfloat16 or shape != (R, Hkv, D):
+            raise ValueError("k_new, v_new: bf16 [R][Hkv][D] is wanted")
+    # a dimension of one element is never stepped over: any stride will do
+    if st[2] != 1 or sv[2] != 1 or (Hkv > 1 and (st[1] != D or sv[1] != D)):
+        raise ValueError("k_new, v_new: bf16 [R][Hkv][D] with contiguous heads is wanted")
+    if R > 1 and st[0] != sv[0]:
         raise ValueError("k_new, v_new: equal row strides are wanted")
+    if slot.dtype is not torch.int32 or not slot.is_contiguous():
+        raise ValueError("slot: a contiguous int32 tensor is wanted")
+    stride = st[0] if R > 1 else Hkv * D
     _check(lib.idx_write_kv(ctypes.byref(cache), k_new.data_ptr(), v_new.data_ptr(), stride, slot.data_ptr(), R,
-                            _stream(stream)), "idx_write_kv")
+                            _current(stream)), "idx_write_kv")
 
 
 def make_tree_problem(q, cache: KvCache, page_table, ctx_len, row_start, mask, max_ctx: int, max_new: int,
@@ -368,11 +381,11 @@ def tree_state_size(problem: TreeProblem, sel_k: int = 0) -> int:
 
 
 def _attn_outputs(problem, out, lse):
-    import torch
+    torch = _modules["torch"]
     rows, heads = problem.R, problem.Hq
-    if out.dtype != torch.bfloat16 or out.shape != (rows, heads, problem.cache.D) or not out.is_contiguous():
+    if out.dtype is not torch.bfloat16 or out.shape != (rows, heads, problem.cache.D) or not out.is_contiguous():
         raise ValueError("out: contiguous bf16 [R][Hq][D] is wanted")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (rows, heads) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (rows, heads) or not lse.is_contiguous()):
         raise ValueError("lse: contiguous fp32 [R][Hq] is wanted")
 
 
@@ -382,19 +395,19 @@ def idx_tree_attention(problem: TreeProblem, out, state, lse=None, stream=None):
     alloc_state(tree_state_size(problem))."""
     _attn_outputs(problem, out, lse)
     _check(lib.idx_tree_attention(ctypes.byref(problem), out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                  state.data_ptr(), state.nbytes, _stream(stream)), "idx_tree_attention")
+                                  state.data_ptr(), state.nbytes, _current(stream)), "idx_tree_attention")
 
 
 def idx_tree_attention_selected(problem: TreeProblem, sel, out, state, lse=None, stream=None):
     """The same over the cached positions sel (int32 [R][K], as idx_launch writes
     them); `state` from alloc_state(tree_state_size(problem, K))."""
-    import torch
+    torch = _modules["torch"]
     _attn_outputs(problem, out, lse)
     if sel.dtype != torch.int32 or sel.dim() != 2 or sel.shape[0] != problem.R or not sel.is_contiguous():
         raise ValueError("sel: a contiguous int32 [R][K] tensor is wanted")
     _check(lib.idx_tree_attention_selected(ctypes.byref(problem), sel.data_ptr(), sel.shape[1], out.data_ptr(),
                                            None if lse is None else lse.data_ptr(), state.data_ptr(), state.nbytes,
-                                           _stream(stream)), "idx_tree_attention_selected")
+                                           _current(stream)), "idx_tree_attention_selected")
 
 
 def last_device_status(ws, stream=None) -> int:

@@ -61,14 +61,14 @@ struct FewCfg {
   static constexpr int kTeams = !F8 ? 0 : N < 64 && !SEL ? 2 : 1;
   static constexpr int kLookupWarp = kFewConvertWarp + 4 * kTeams;
   static constexpr int kScaleStages = F8 && D == 64 ? 8 : 4;
-  static constexpr int kScaleBytes = F8 ? kScaleStages * 2 * kFewTile * 4 : 0;
+  static constexpr int kScaleBytes = F8 && SEL ? kScaleStages * 2 * kFewTile * 4 : 0;
   static constexpr int kThreads = 32 * (kLookupWarp + (SEL ? 4 : 0));
   // Registers per thread after the roles part, where a softmax thread holds a key's scores
   // and row sums; the shares add up to no more than the launch's threads x registers.
   static constexpr bool kShareRegs = kThreads > 384 || N == 64;
   static constexpr int kRegsLaunch = kThreads == 384 ? 168 : kThreads == 512 ? 128 : 96;
-  static constexpr int kRegsSoftmax = kThreads == 384 ? 208 : kThreads == 512 ? 176 : N == 64 ? 144 : 128;
-  static constexpr int kRegsOther = kThreads == 384 ? 88 : kThreads == 512 ? 80 : N == 64 ? 64 : 72;
+  static constexpr int kRegsSoftmax = kThreads == 384 ? 208 : kThreads == 512 ? 176 : N == 16 ? 120 : N == 64 ? 144 : SEL ? 128 : 136;
+  static constexpr int kRegsOther = kThreads == 384 ? 88 : kThreads == 512 ? 80 : N == 16 ? 80 : N == 32 && SEL ? 72 : 64;
   static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch, "register shares");
   static constexpr int kDynamic = 1024 + kFixed + kKStages * kKBytes + kVStages * kTileBytes + kRawStages * kRawBytes +
                                   kScaleBytes;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
     mbar_init(&bars.v_empty[s], 1);
     mbar_init(&bars.raw_full[s], loaders);
     mbar_init(&bars.raw_empty[s], F8 ? 4 * C::kTeams : 1);
-    mbar_init(&bars.sc_full[s], SEL ? 128 : 2);   // dense: K's and V's scales
+    mbar_init(&bars.sc_full[s], 128);
     mbar_init(&bars.sc_empty[s], 4);
     if (s < 2) {
       mbar_init(&bars.q_full[s], F8 ? 4 * C::kTeams : 1);
@@ -284,11 +284,34 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       for (int r = 0; r < N; ++r) l[r] = 0.0f;
       const uint32_t h0 = h;
       bool left = false;
+      // Dense E4M3: a thread reads its key's two scales itself, a tile of its stream ahead,
+      // and the page's id another one ahead.
+      const int32_t *const table = p.page_table + static_cast<int64_t>(walk.i) * p.pt_stride + walk.tile0 * 2 + (key >> 6);
+      const int table_left = (walk.q.keys + kPage - 1) / kPage - walk.tile0 * 2 - (key >> 6);
+      float next_k = 0.0f, next_v = 0.0f;
+      int32_t next_page = -1;
+      auto page_of = [&](int j) -> int32_t { return j < walk.count && 2 * j < table_left ? table[2 * j] : -1; };
+      auto bring_scales = [&](int32_t page) {
+        const bool good = page >= 0 && page < p.cache.P;
+        const int64_t at = good ? (static_cast<int64_t>(page) * Hkv + walk.head) * kPage + (key & 63) : 0;
+        next_k = good ? p.cache.k_scale[at] : 0.0f;
+        next_v = good ? p.cache.v_scale[at] : 0.0f;
+      };
+      if (F8 && !SEL) {
+        const int j = (s ^ tiles) & 1;
+        bring_scales(page_of(j));
+        next_page = page_of(j + 2);
+      }
       for (int j = (s ^ tiles) & 1; j < walk.count; j += 2, ++n) {   // the CTA's even or odd tiles
         const int k = tiles + j;
         const int key0 = (walk.tile0 + j) * kFewTile;
         float ck = c, vs = 1.0f;
-        if (F8) {
+        if (F8 && !SEL) {
+          ck = c * next_k;
+          vs = next_v;
+          bring_scales(next_page);
+          next_page = page_of(j + 4);
+        } else if (F8) {
           ok = ok && warp_wait_all(&bars.sc_full[k % C::kScaleStages], (k / C::kScaleStages) & 1);
           ck = c * ssc[(k % C::kScaleStages) * 2 * kFewTile + key];
           vs = ssc[(k % C::kScaleStages) * 2 * kFewTile + kFewTile + key];
@@ -665,7 +688,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
     if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kFewKWarp || (!SEL && warp == kFewVWarp)) {
       // -------------------------------------------------------------- loads
-      // K's warp also brings a bf16 Q; each brings its own scales.  Selected positions are
+      // K's warp also brings a bf16 Q.  Selected positions are
       // brought by a team of their own.
       const bool is_v = warp == kFewVWarp;
       const int stages = is_v ? (F8 ? C::kRawStages : C::kVStages) : C::kKStages;
@@ -673,8 +696,6 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       uint64_t *const full = is_v ? (F8 ? bars.raw_full : bars.v_full) : bars.k_full;
       uint64_t *const empty = is_v ? (F8 ? bars.raw_empty : bars.v_empty) : bars.k_empty;
       uint8_t *const ring = is_v ? (F8 ? sraw : sv) : sk;
-      const float *const scales = is_v ? p.cache.v_scale : p.cache.k_scale;
-      float *const sscale = ssc + (is_v ? kFewTile : 0);
       int stage = 0;          // of the next load
       uint32_t phase = 1;     // its empty barrier's
       int nload = 0;          // loads (tiles) so far
@@ -725,9 +746,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
               uint32_t good = 0;
 #pragma unroll
               for (int x = 0; x < 2; ++x) good |= static_cast<uint32_t>(pg[x] >= 0 && pg[x] < p.cache.P) << x;
-              const int ss = nload % C::kScaleStages;
-              if (!mbar_wait(&empty[stage], phase, limit, abort) ||
-                  (F8 && !mbar_wait(&bars.sc_empty[ss], ((nload / C::kScaleStages) & 1) ^ 1, limit, abort))) {
+              if (!mbar_wait(&empty[stage], phase, limit, abort)) {
                 ok = false;
                 break;
               }
@@ -735,14 +754,11 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
               oks[nload & 31] = good;
               if ((!(good & 1u) && pg[0] != -2) || (!(good & 2u) && pg[1] != -2)) flag_status(a.status, kStatusBadPage);
               mbar_arrive_expect_tx(&full[stage], __popc(good) * static_cast<uint32_t>(kBytes / 2));
-              if (F8) mbar_arrive_expect_tx(&bars.sc_full[ss], __popc(good) * 256u);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 if (!((good >> x) & 1u)) continue;
                 if constexpr (F8) {
                   tma_load_4d(dst + x * (kPage * D), map, 0, 0, walk.head, pg[x], &full[stage]);
-                  bulk_load(sscale + ss * 2 * kFewTile + x * kPage,
-                            scales + (static_cast<int64_t>(pg[x]) * Hkv + walk.head) * kPage, 256u, &bars.sc_full[ss]);
                 } else {
 #pragma unroll
                   for (int b = 0; b < kBlocks; ++b)
@@ -763,7 +779,6 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       if (lane == 0) {
         land(bars.q_full, C::kQBufs, nq);
         land(full, stages, nload);
-        if (F8) land(bars.sc_full, C::kScaleStages, nload);
       }
     } else if (warp != kFewVWarp && lane == 0) {
       // -------------------------------------------------------------- MMA issuers
