@@ -1,4 +1,5 @@
-// Attention of drafted tokens over a paged cache, whole or at selected positions.
+// Attention of drafted tokens over a paged cache, whole or at selected positions, for more
+// than 64 query vectors per key/value head and item.
 //
 // For a key/value head the query vectors that read it (tokens x query heads per
 // key/value head) are the M = 128 rows of a tensor-core tile, and the 64 positions of
@@ -20,22 +21,14 @@
 // Work: an item is (request, key/value head, block of tokens) with its tiles in
 // position order; the launch's tiles, in item order, are dealt out as one even,
 // contiguous share per CTA (one CTA per SM).  A CTA that holds a whole item writes
-// its output; shares of an item go to the state as (O, m, l) and the combine kernel
-// joins them in CTA order, so equal calls give equal bits.
+// its output; shares of an item go to the state as (O, m, l), and the CTAs that hold them
+// join them in a fixed order, so equal calls give equal bits.
 //
 // Two streams fill the tensor core: the even and odd tiles of one row block (up to 128
-// rows, joined in TMEM at the end of the item: more bytes in flight for the few-row,
-// memory-bound calls) or two row blocks over the same tiles (more rows: each K and V
+// rows, joined in TMEM at the end of the item) or two row blocks over the same tiles (more rows: each K and V
 // tile is read from shared memory for 256 rows).  Each has O and two S buffers of 64
 // columns in TMEM, so that the scores of a tile are computed while its four softmax
 // warps, one thread per row, work on the tile before; P takes its S's place.
-//
-// A block of at most 32 (64) rows fills the 128 of the tile four (two) times over: Q
-// is loaded that often, and each copy of the rows takes a quarter (half) of a tile's
-// keys, with zeros in its P for the others.  All four softmax warps then work on
-// every tile, 16 (32) keys each, and the copies' O are summed at the end of the item.
-// The tensor core computes nothing that it would not have computed for the empty
-// rows.
 #pragma once
 
 #include "tree_attention_common.cuh"
@@ -50,12 +43,13 @@ constexpr uint32_t kColS = 0, kColO = 256;   // + 128 * stream (S: + 64 * buffer
 // ---------------------------------------------------------------------------- roles
 // warps 0-3 and 4-7: softmax of streams 0 and 1; 8 and 11: loads of K and of V (by TMA,
 // or gathering selected positions); 9 and 10: MMA issuers of streams 0 and 1; 12-19 with
-// an E4M3 cache: the split of Q, and V to bf16, two teams of four on alternate loads.
-constexpr int kKWarp = 8, kIssuerWarp = 9, kVWarp = 11, kConvertWarp = 12;
+// an E4M3 cache: the split of Q, and V to bf16, two teams of four on alternate loads; 13
+// and 14 with two bf16 row blocks: issuers of the streams' scores.
+constexpr int kKWarp = 8, kIssuerWarp = 9, kVWarp = 11, kConvertWarp = 12, kScoreWarp = 13;
 constexpr int kMaxStages = 8;
 
-// COPIES: copies of the row block in the tile's rows (4, 2 or 1); PAIR: two row blocks.
-template <int D, bool F8, int COPIES, bool PAIR, bool SEL>
+// PAIR: two row blocks.
+template <int D, bool F8, bool PAIR, bool SEL>
 struct Cfg {
   static constexpr int kLoad = 128 / D;                  // pages per load of K or V
   static constexpr int kLoadBytes = kLoad * kTile * D * 2;   // as bf16
@@ -69,21 +63,24 @@ struct Cfg {
   // stage then always has the same waiter.  Were they odd, a waiter could come to a stage
   // again before the other's load in between, and the parity of the barrier would pass for
   // the one that it waits for.
-  static constexpr int kKStages = F8 ? (D == 128 && COPIES > 1 ? 4 : 6) : 4;
+  static constexpr int kKStages = F8 ? 6 : 4;
   static constexpr int kVStages = F8 ? 4 : D == 128 ? 4 : 6;      // as bf16
   static constexpr int kRawStages = F8 ? (D == 128 ? 4 : 6) : 0;  // V as E4M3
   static_assert(kKStages % 2 == 0 && kVStages % 2 == 0 && kRawStages % 2 == 0, "one waiter per stage");
   static constexpr int kScaleStages = F8 ? 8 : 0;
   static constexpr int kScaleFloats = 2 * kLoad * kTile;   // of a load: K's, then V's
-  static constexpr int kRedBytes = COPIES > 1 ? 2 * kRows * 16 * 4 : 0;   // the copies' sum: 16 columns a stream
-  static constexpr int kThreads = 32 * (F8 ? kConvertWarp + 8 : kConvertWarp);
+  // Two row blocks keep an issuing thread busier than their softmax (a tcgen05.mma takes
+  // it some 70 cycles): the scores' products then have threads of their own, in four more
+  // warps (beside an E4M3 cache there are no registers for them).
+  static constexpr bool kSplitIssue = PAIR && !F8;
+  static constexpr int kThreads = 32 * (F8 ? kConvertWarp + 8 : kSplitIssue ? kConvertWarp + 4 : kConvertWarp);
   // Registers per thread after the roles part, where a softmax thread holds up to 64
   // scores.  The shares add up to no more than the launch's threads x registers.
-  static constexpr bool kShareRegs = F8;
-  static constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsOther = 64;
-  static_assert(!F8 || 256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch, "register shares");
+  static constexpr bool kShareRegs = kThreads > 384;
+  static constexpr int kRegsLaunch = F8 ? 96 : 128, kRegsSoftmax = F8 ? 144 : 176, kRegsOther = F8 ? 64 : 80;
+  static_assert(!kShareRegs || 256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch, "register shares");
   static constexpr int kDynamic = 1024 + kQTotal + kKStages * kKBytes + kVStages * kLoadBytes + kRawStages * kRawBytes +
-                                  kScaleStages * kScaleFloats * 4 + kRedBytes;
+                                  kScaleStages * kScaleFloats * 4;
 };
 
 template <bool PAIR>
@@ -94,7 +91,7 @@ struct Barriers {
   uint64_t sc_full[kMaxStages], sc_empty[kMaxStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];   // [stream][buffer]
-  uint64_t o_free[2], drain[2], stats[2], red_full[2], red_free[2], scrubbed[2];
+  uint64_t o_free[2], drain[2], drain_s[2], stats[2], scrubbed[2];
   uint32_t tmem_base;
   int abort;
   int32_t two_terms[2][2];         // P of [stream][buffer] has a low term
@@ -139,36 +136,29 @@ __device__ __forceinline__ bool raise_maximum(uint32_t to, float top, bool has_o
   return true;
 }
 
-// One row's keys of a tile (N of the 64, from column n0): S (columns at ts) to P in the
-// same columns, the row's maximum m and sum l, and O (D columns at to) when the maximum
-// moves.  special: only the keys of ok (a bit per key) are visible.  ks: the tile's K
-// scales; vs: its V scales.
+// One row's keys of a tile: S (64 columns at ts) to P in the same columns, the row's maximum
+// m and sum l, and O (D columns at to) when the maximum moves.  special: only the keys of ok
+// (a bit per key) are visible.  sk: the tile's K scales; sv: its V scales.
 //
 // P is rounded to bf16 for the product with V.  Over the 64 or more keys of a full tile
 // the roundings average out below the output's own; the few keys of a special tile do
 // not, so there P is kept in two bf16 terms, high in columns 0-31 and low in 32-63, and
 // the product runs over both.
-template <int D, bool F8, int N, typename F>
-__device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const float *sk, const float *sv, float c, int n0, bool special,
+template <int D, bool F8, typename F>
+__device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const float *sk, const float *sv, float c, bool special,
                                              uint64_t ok, bool has_o, float &m, float &l, F settled) {
-  constexpr int kW = N < 32 ? N : 32;        // columns per register group
-  uint32_t x[N / kW][kW];
+  constexpr int kW = 32;        // columns per register group
+  uint32_t x[2][kW];
 #pragma unroll
-  for (int w = 0; w < N / kW; ++w) {
-    if constexpr (kW == 32) tmem_ld32(ts + n0 + 32 * w, x[w]);
-    else tmem_ld16(ts + n0, x[w]);
-  }
-  const float4 *const ks = reinterpret_cast<const float4 *>(sk + n0);
-  const float2 *const vs = reinterpret_cast<const float2 *>(sv + n0);
+  for (int w = 0; w < 2; ++w) tmem_ld32(ts + 32 * w, x[w]);
+  const float4 *const ks = reinterpret_cast<const float4 *>(sk);
+  const float2 *const vs = reinterpret_cast<const float2 *>(sv);
   tmem_wait_ld();
 #pragma unroll
-  for (int w = 0; w < N / kW; ++w) {
-    if constexpr (kW == 32) reg_fence32(x[w]);
-    else reg_fence16(x[w]);
-  }
+  for (int w = 0; w < 2; ++w) reg_fence32(x[w]);
   if (F8) {
 #pragma unroll
-    for (int w = 0; w < N / kW; ++w)
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
       for (int y = 0; y < kW; y += 4) {
         if (y % 16 == 0) asm volatile("" ::: "memory");   // at most four of the loads ahead
@@ -181,14 +171,14 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const flo
   }
   if (special) {
 #pragma unroll
-    for (int w = 0; w < N / kW; ++w)
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
       for (int y = 0; y < kW; ++y)
         x[w][y] = (static_cast<uint32_t>(ok >> (32 * w)) >> y) & 1u ? x[w][y] : 0xFF800000u;   // -infinity
   }
   float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int w = 0; w < N / kW; ++w)
+  for (int w = 0; w < 2; ++w)
 #pragma unroll
     for (int y = 0; y < kW; y += 8)
 #pragma unroll
@@ -201,7 +191,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const flo
   const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
   float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-  for (int w = 0; w < N / kW; ++w) {
+  for (int w = 0; w < 2; ++w) {
     uint32_t hi[kW / 2];
 #pragma unroll
     for (int y = 0; y < kW; y += 2) {
@@ -224,8 +214,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const flo
       x[w][y] = __float_as_uint(e.x);
       x[w][y + 1] = __float_as_uint(e.y);
     }
-    if constexpr (kW == 32) tmem_st16(ts + n0 / 2 + 16 * w, hi);
-    else tmem_st8(ts + n0 / 2, hi);
+    tmem_st16(ts + 16 * w, hi);
     if (special) {
       uint32_t lo[kW / 2];
 #pragma unroll
@@ -235,17 +224,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const flo
         const float r1 = __uint_as_float(x[w][2 * y + 1]) - __uint_as_float(hi[y] & 0xFFFF0000u);
         lo[y] = pack_bf16(r0 == r0 ? r0 : 0.0f, r1 == r1 ? r1 : 0.0f);
       }
-      if constexpr (kW == 32) tmem_st16(ts + 32 + n0 / 2 + 16 * w, lo);
-      else tmem_st8(ts + 32 + n0 / 2, lo);
-    }
-  }
-  if constexpr (N < kTile) {   // the other copies' keys
-    uint32_t zero[8] = {};
-#pragma unroll
-    for (int w = 0; w < kTile / 2; w += 8) {
-      if (w >= n0 / 2 && w < (n0 + N) / 2) continue;
-      tmem_st8(ts + w, zero);
-      if (special) tmem_st8(ts + 32 + w, zero);
+      tmem_st16(ts + 32 + 16 * w, lo);
     }
   }
   l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
@@ -254,11 +233,11 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const flo
 }
 
 // ---------------------------------------------------------------------------- kernel
-template <int D, bool F8, int COPIES, bool PAIR, bool SEL>
-__global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
+template <int D, bool F8, bool PAIR, bool SEL>
+__global__ void __launch_bounds__(Cfg<D, F8, PAIR, SEL>::kThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap vmap, const TreeAttnArgs a) {
-  using C = Cfg<D, F8, COPIES, PAIR, SEL>;
+  using C = Cfg<D, F8, PAIR, SEL>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Barriers<PAIR> bars;
   uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
@@ -267,7 +246,6 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
   uint8_t *const sv = sk + C::kKStages * C::kKBytes;
   uint8_t *const sraw = sv + C::kVStages * C::kLoadBytes;
   float *const ssc = reinterpret_cast<float *>(sraw + C::kRawStages * C::kRawBytes);   // [stage][K, V]
-  float *const sred = ssc + C::kScaleStages * C::kScaleFloats;                          // [stream][row][16]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const idx_tree_problem &p = a.p;
   const int Hkv = p.cache.Hkv;
@@ -298,9 +276,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       }
       mbar_init(&bars.o_free[s], PAIR ? 4 : 8);
       mbar_init(&bars.drain[s], 1);
+      mbar_init(&bars.drain_s[s], 1);
       mbar_init(&bars.stats[s], 4);
-      mbar_init(&bars.red_full[s], 4);
-      mbar_init(&bars.red_free[s], 4);
       mbar_init(&bars.scrubbed[s], 4);
     }
     bars.abort = 0;
@@ -351,12 +328,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
     if constexpr (C::kShareRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
-    constexpr int kBlockRows = kRows / COPIES;   // rows of a copy
-    constexpr int kKeys = kTile / COPIES;        // keys of a tile that a copy takes
     const int s = warp >> 2;               // stream
-    const int lrow = tid & 127;            // row of the stream's tile, and its TMEM lane
-    const int row = lrow % kBlockRows;     // row of the block
-    const int copy = lrow / kBlockRows;    // the same for a whole warp
+    const int row = tid & 127;             // row of the stream's tile, and its TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // first TMEM lane of the warp << 16
     const uint32_t to = tmem + kColO + 128 * s + lanes;
     const float c = p.scale * kLog2e;
@@ -364,7 +337,6 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
     int tiles = 0;      // tiles of earlier segments
     int loads = 0;      // loads of earlier segments
     uint32_t n = 0;     // this stream's tiles so far
-    uint32_t nred = 0;  // sums of copies so far
     bool ok = true;
     while (ok && walk.next()) {
       const int stok0 = walk.tok0 + (PAIR ? s * tb : 0);                       // first token of the stream
@@ -392,12 +364,12 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
         }
         tc_fence_after();
         if (F8 && mine == 0) cs = c * bars.q_scale[walk.seg & 3][PAIR ? s : 0][row];
-        uint64_t okbits = ~0ull;   // the copy's keys of the tile that the row sees
+        uint64_t okbits = ~0ull;   // keys of the tile that the row sees
         bool special;
         if (SEL) {
           const uint32_t k0 = bars.keys_ok[k & 63][0], k1 = bars.keys_ok[k & 63][1];
           special = (k0 & k1) != ~0u;
-          if (special) okbits = (static_cast<uint64_t>(k1) << 32 | k0) >> (copy * kKeys);
+          if (special) okbits = static_cast<uint64_t>(k1) << 32 | k0;
         } else {
           const uint32_t page = bars.page_ok[k & 63];
           special = key0 + kTile > ctx || page == 0u;
@@ -409,7 +381,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
               if (before > 0) okbits = ((1ull << before) - 1ull) | (vm << before);
               else okbits = before > -64 ? vm >> -before : 0ull;
             }
-            okbits = page != 0u ? okbits >> (copy * kKeys) : 0ull;
+            if (page == 0u) okbits = 0ull;
           }
         }
         if (!SEL && !F8 && special) {
@@ -421,11 +393,11 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
             ok = false;
             break;
           }
-          const int key = lrow & 63, pos = key0 + key;
+          const int key = row & 63, pos = key0 + key;
           const bool dead = pos >= walk.q.keys || bars.page_ok[k & 63] == 0u;
           if (dead || pos >= ctx) {
 #pragma unroll 4
-            for (int x = (lrow >> 6) * kBlocks * 4; x < (lrow >> 6) * kBlocks * 4 + kBlocks * 4; ++x) {
+            for (int x = (row >> 6) * kBlocks * 4; x < (row >> 6) * kBlocks * 4 + kBlocks * 4; ++x) {
               uint4 *const at = reinterpret_cast<uint4 *>(sv + sl * C::kLoadBytes + (x >> 3) * kBlockBytes +
                                                           (sub * kTile + key) * 128 + ((x + key) & 7) * 16);
               uint4 v = dead ? make_uint4(0, 0, 0, 0) : *at;
@@ -457,13 +429,13 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           // O may be touched once the product of the tile before has completed
           auto settled = [&]() { return warp_wait_all(&bars.pv_done[s][buf ^ 1], ((n - 1) >> 1) & 1); };
           const float *const ks = ssc + (ld % 8) * C::kScaleFloats + sub * kTile;
-          if (!softmax_tile<D, F8, kKeys>(tmem + kColS + 128 * s + 64 * buf + lanes, to, ks, ks + kLoad * kTile, cs,
-                                          copy * kKeys, special, okbits, mine > 0, m, l, settled)) {
+          if (!softmax_tile<D, F8>(tmem + kColS + 128 * s + 64 * buf + lanes, to, ks, ks + kLoad * kTile, cs,
+                                   special, okbits, mine > 0, m, l, settled)) {
             ok = false;
             break;
           }
         }
-        if (lrow == 0) bars.two_terms[s][buf] = special;
+        if (row == 0) bars.two_terms[s][buf] = special;
         tc_fence_before();
         warp_arrive(&bars.p_ready[s][buf]);
         if (F8 && lane == 0 && (sub == kLoad - 1 || j + 1 == walk.count)) mbar_arrive(&bars.sc_empty[ld % 8]);
@@ -495,11 +467,10 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       if (l != l) m = INFINITY;   // a NaN among the visible scores takes the whole row, in every join
       float f0 = 1.0f, f1 = 0.0f;
       if constexpr (!PAIR) {
-        // the row's maximum and sum over both streams and all copies; this thread's O
-        // (of stream 0 and of stream 1) scales by f0 and f1
+        // the row's maximum and sum over both streams, whose O scale by f0 and f1
         const int sp = walk.seg & 1;
-        bars.row_m[sp][s][lrow] = m;
-        bars.row_l[sp][s][lrow] = l;
+        bars.row_m[sp][s][row] = m;
+        bars.row_l[sp][s][row] = l;
         tc_fence_before();
         warp_arrive(&bars.stats[s]);
         if (!warp_wait_all(&bars.stats[s], walk.seg & 1) || !warp_wait_all(&bars.stats[s ^ 1], walk.seg & 1)) {
@@ -507,18 +478,10 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           break;
         }
         tc_fence_after();
-        float mm = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < 2 * COPIES; ++x) mm = fmaxf(mm, bars.row_m[sp][x & 1][(x >> 1) * kBlockRows + row]);
-        l = 0.0f;
-#pragma unroll
-        for (int x = 0; x < 2 * COPIES; ++x) {
-          const int at = (x >> 1) * kBlockRows + row;
-          const float mx = bars.row_m[sp][x & 1][at];
-          const float f = mx == -INFINITY ? 0.0f : ex2(mx - mm);
-          l += bars.row_l[sp][x & 1][at] * f;
-          if ((x >> 1) == copy) (x & 1 ? f1 : f0) = f;
-        }
+        const float m0 = bars.row_m[sp][0][row], m1 = bars.row_m[sp][1][row], mm = fmaxf(m0, m1);
+        f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - mm);
+        f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - mm);
+        l = bars.row_l[sp][0][row] * f0 + bars.row_l[sp][1][row] * f1;
         m = mm;
       }
       const bool poison = *reinterpret_cast<volatile int32_t *>(&bars.nonfinite[walk.seg & 31]) == walk.seg + 1;
@@ -557,7 +520,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           *reinterpret_cast<float4 *>(a.part_o + (static_cast<int64_t>(slot) * kSlotRows + prow) * D + d) = o;
         }
       };
-      if (row < nrow && copy == 0 && (PAIR || s == 0)) {
+      if (row < nrow && (PAIR || s == 0)) {
         if (!walk.whole) a.part_ml[static_cast<int64_t>(slot) * kSlotRows + prow] = make_float2(m, l);
         else if (a.lse != nullptr)
           a.lse[static_cast<int64_t>(r) * p.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -581,48 +544,10 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
             if (has1) o[y] += f1 == 0.0f ? 0.0f : __uint_as_float(x1[y]) * f1;
           }
         }
-        if constexpr (COPIES == 1) {
-          if (row < nrow)
+        if (row < nrow)
 #pragma unroll
-            for (int y = 0; y < 16; y += 4) put(d + y, make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]));
-        } else {
-          // the copies' sum: thread (copy, row) takes 16 / COPIES of the columns
-          float4 *const red = reinterpret_cast<float4 *>(sred) + s * kRows * 4;
-          if (active)
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              red[lrow * 4 + (y ^ ((lrow >> 1) & 3))] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-          warp_arrive(&bars.red_full[s]);
-          if (!warp_wait_all(&bars.red_full[s], nred & 1)) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int z = 0; z < 4 / COPIES; ++z) {
-            const int y = copy * (4 / COPIES) + z;
-            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (row < nrow) {
-#pragma unroll
-              for (int x = 0; x < COPIES; ++x) {
-                const int at = x * kBlockRows + row;
-                const float4 v = red[at * 4 + (y ^ ((at >> 1) & 3))];
-                sum.x += v.x;
-                sum.y += v.y;
-                sum.z += v.z;
-                sum.w += v.w;
-              }
-              put(d + 4 * y, sum);
-            }
-          }
-          warp_arrive(&bars.red_free[s]);
-          if (!warp_wait_all(&bars.red_free[s], nred & 1)) {
-            ok = false;
-            break;
-          }
-          ++nred;
-        }
+          for (int y = 0; y < 16; y += 4) put(d + y, make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]));
       }
-      if (!ok) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -633,7 +558,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
     }
     if (!ok) give_up();
     join_items<D>(a, bars.shares, &bars.nshare, ok);
-  } else if (warp < kConvertWarp) {
+  } else if (warp < kConvertWarp || C::kSplitIssue) {
     if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kKWarp || warp == kVWarp) {
       // -------------------------------------------------------------- loads
@@ -684,7 +609,6 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       while (ok && walk.next()) {
         const int nloads = (walk.count + kLoad - 1) / kLoad;
         if (!F8 && !is_v) {
-          // Q of the segment, once for every copy
           const int qb = walk.seg % C::kQBufs;
           if (!wait_flushed(&bars.q_empty[qb], ((walk.seg / C::kQBufs) & 1) ^ 1)) {
             ok = false;
@@ -692,12 +616,11 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           }
           if (lane == 0) {
             const int nhalf = PAIR && walk.tokens > tb ? 2 : 1;
-            mbar_arrive_expect_tx(&bars.q_full[qb], static_cast<uint32_t>(nhalf * COPIES * kBlocks * G * tb * 128));
+            mbar_arrive_expect_tx(&bars.q_full[qb], static_cast<uint32_t>(nhalf * kBlocks * G * tb * 128));
             for (int s = 0; s < nhalf; ++s)
               for (int b = 0; b < kBlocks; ++b)
-                for (int x = 0; x < COPIES; ++x)
-                  tma_load_3d(sq + (PAIR ? s : qb) * C::kQBytes + b * kQBlockBytes + x * (kQBlockBytes / COPIES), &qmap,
-                              b * 64, walk.head * G, walk.q.row0 + walk.tok0 + s * tb, &bars.q_full[qb]);
+                tma_load_3d(sq + (PAIR ? s : qb) * C::kQBytes + b * kQBlockBytes, &qmap, b * 64, walk.head * G,
+                            walk.q.row0 + walk.tok0 + s * tb, &bars.q_full[qb]);
           }
           ++nq;
         }
@@ -894,12 +817,15 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           if (F8) land(bars.sc_full, 8, nload);
         }
       }
-    } else if (warp == kIssuerWarp || warp == kIssuerWarp + 1) {
+    } else if (warp == kIssuerWarp || warp == kIssuerWarp + 1 || warp == kScoreWarp || warp == kScoreWarp + 1) {
       // -------------------------------------------------------------- MMA issuers
       // Per stream: S of two tiles; then, tile by tile, O += P V once its P is ready, and S
-      // of the second next tile once that has completed, since it takes P's columns.
+      // of the second next tile once that has completed, since it takes P's columns.  One
+      // thread does both, or one each (the kScoreWarps S).
       if (lane == 0) {
-        const int s = warp - kIssuerWarp;
+        const int s = (warp - kIssuerWarp) & 1;
+        static_assert((kScoreWarp - kIssuerWarp) % 2 == 0);
+        const bool do_s = !C::kSplitIssue || warp >= kScoreWarp, do_pv = !C::kSplitIssue || warp < kScoreWarp;
         const uint32_t ts = tmem + kColS + 128 * s, to = tmem + kColO + 128 * s;
         const uint32_t idesc_s = umma_idesc(F8 ? 0u : 1u, kTile), idesc_o = umma_idesc(1u, D) | kIdescBMn;
         int kstage = 0, vstage = 0;          // of the next load of K and of V
@@ -920,27 +846,27 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
           const int qb = walk.seg % C::kQBufs;
           const int nloads = (walk.count + kLoad - 1) / kLoad;
           const bool live = !PAIR || s == 0 || walk.tokens > tb;   // this stream has rows
-          if (!mbar_wait(&bars.q_full[qb], (walk.seg / C::kQBufs) & 1, limit, abort)) {
+          if (do_s && !mbar_wait(&bars.q_full[qb], (walk.seg / C::kQBufs) & 1, limit, abort)) {
             ok = false;
             break;
           }
           const int j0 = PAIR ? 0 : (s ^ loads) & 1;   // the stream's first load
           loads += nloads;
-          if (j0 >= nloads) mbar_arrive(&bars.q_empty[qb]);
+          if (do_s && j0 >= nloads) mbar_arrive(&bars.q_empty[qb]);
           // the stream's first load, and what lies before the next segment's
           skip(kstage, kphase, C::kKStages, j0);
           skip(vstage, vphase, C::kVStages, j0);
           if (!live) {   // no rows: only pass the loads on
             for (int jj = 0; ok && jj < nloads; ++jj) {
-              ok = mbar_wait(&bars.k_full[kstage], kphase, limit, abort) &&
-                   mbar_wait(&bars.v_full[vstage], vphase, limit, abort);
+              ok = (!do_s || mbar_wait(&bars.k_full[kstage], kphase, limit, abort)) &&
+                   (!do_pv || mbar_wait(&bars.v_full[vstage], vphase, limit, abort));
               if (!ok) break;
-              mbar_arrive(&bars.k_empty[kstage]);
-              mbar_arrive(&bars.v_empty[vstage]);
+              if (do_s) mbar_arrive(&bars.k_empty[kstage]);
+              if (do_pv) mbar_arrive(&bars.v_empty[vstage]);
               skip(kstage, kphase, C::kKStages, 1);
               skip(vstage, vphase, C::kVStages, 1);
             }
-            if (ok) mbar_arrive(&bars.q_empty[qb]);
+            if (ok && do_s) mbar_arrive(&bars.q_empty[qb]);
             continue;
           }
           const uint32_t qaddr = smem_u32(sq + (PAIR ? s : qb) * C::kQBytes);
@@ -980,8 +906,15 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
             }
             return true;
           };
-          if (jk < nloads) ok = scores();
-          if (ok && jk < nloads) ok = scores();
+          if (!do_pv) {
+            // the product of the tile before the last has to have left the buffer
+            while (ok && jk < nloads)
+              ok = (ns < 2 || mbar_wait(&bars.pv_done[s][ns & 1], ((ns - 2) >> 1) & 1, limit, abort)) && scores();
+            skip(kstage, kphase, C::kKStages, 1);   // to the next segment's first load
+            continue;
+          }
+          if (do_s && jk < nloads) ok = scores();
+          if (do_s && ok && jk < nloads) ok = scores();
           for (int jj = j0; ok && jj < nloads; jj += step) {
             const int end = min(walk.count, (jj + 1) * kLoad);
             for (int j = jj * kLoad; j < end; ++j, ++n) {
@@ -1004,11 +937,12 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
                   umma_f16_ta(to, ta + 32 + kk * 8, vdesc + ((kk * 2048) >> 4), idesc_o, 1u);
               }
               umma_commit(&bars.pv_done[s][buf]);
+              any = true;
               if (j + 1 == end) {
                 umma_commit(&bars.v_empty[vstage]);
                 skip(vstage, vphase, C::kVStages, jj + step < nloads ? step : 0);
               }
-              ok = mbar_wait(&bars.pv_done[s][buf], (n >> 1) & 1, limit, abort) && (jk >= nloads || scores());
+              if (do_s) ok = mbar_wait(&bars.pv_done[s][buf], (n >> 1) & 1, limit, abort) && (jk >= nloads || scores());
               if (!ok) break;
             }
           }
@@ -1020,8 +954,9 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
         if (!ok) {
           give_up();
           if (any) {   // MMAs in flight read shared memory and TMEM: wait for them
-            umma_commit(&bars.drain[s]);
-            if (!mbar_wait(&bars.drain[s], 0, limit, &never)) flag_status(a.status, kStatusTimeout);
+            uint64_t *const drain = do_pv ? &bars.drain[s] : &bars.drain_s[s];
+            umma_commit(drain);
+            if (!mbar_wait(drain, 0, limit, &never)) flag_status(a.status, kStatusTimeout);
           }
         }
       }
@@ -1033,16 +968,14 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
       const int team = (warp - kConvertWarp) >> 2, t = (tid - kConvertWarp * 32) & 127;
       Walk qwalk(a, t0, t1, first.req, first.base, first.q);     // the segment whose Q is next
       // Q of qwalk's segment: two threads per row (of every row block), each with half of
-      // its dimensions.  The copies and both terms go to shared memory, rows without a
-      // token as zeros.
+      // its dimensions.  Both terms go to shared memory, rows without a token as
+      // zeros.
       auto split_q = [&]() -> bool {
-        constexpr int kBlockRows = kRows / COPIES;
         const int qb = qwalk.seg % C::kQBufs;
         if (!warp_wait_all(&bars.q_empty[qb], ((qwalk.seg / C::kQBufs) & 1) ^ 1)) return false;
         const int id = tid - kConvertWarp * 32, row = id >> 1, half = id & 1;
 #pragma unroll 1
         for (int blk = 0; blk < (PAIR && qwalk.tokens > tb ? 2 : 1); ++blk) {
-          if (row >= kBlockRows) break;
           const int nrow = min(tb, qwalk.tokens - blk * tb) * G;
           uint4 v[D / 16];
           const uint16_t *const src = static_cast<const uint16_t *>(p.q) +
@@ -1063,15 +996,12 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
               if (hi < 0x7F80u) top = max(top, hi);
             }
           }
-          top = max(top, __shfl_xor_sync(__activemask(), top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           // 2^e takes it to (224, 448]; rows below 2^-112 stop at 2^120
           const int e = min(((top & 0x7Fu) <= 0x60u ? 8 : 7) - (static_cast<int>(top >> 7) - 127), 120);
           const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
           if (half == 0)
-#pragma unroll
-            for (int x = 0; x < COPIES; ++x)
-              bars.q_scale[qwalk.seg & 3][PAIR ? blk : 0][row + x * kBlockRows] =
-                  __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            bars.q_scale[qwalk.seg & 3][PAIR ? blk : 0][row] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
           uint8_t *const dst = sq + (PAIR ? blk : qb) * C::kQBytes;
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) {       // 16 elements: 16 bytes of each term
@@ -1090,18 +1020,12 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
                       e4m3x2(fmaf(f2, 0.0f, f2 - g1.x), fmaf(f3, 0.0f, f3 - g1.y)) << 16;
             }
             const int ch = half * (D / 32) + x;    // 16-byte chunk of the term's row
-#pragma unroll
-            for (int z = 0; z < COPIES; ++z) {
-              const int rr = row + z * kBlockRows;
-              uint8_t *const at = dst + rr * 128;
-              if constexpr (D == 128) {
-                *reinterpret_cast<uint4 *>(at + ((ch ^ (rr & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(at + kQBlockBytes + ((ch ^ (rr & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              } else {
-                *reinterpret_cast<uint4 *>(at + ((ch ^ (rr & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(at + (((ch + 4) ^ (rr & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              }
-            }
+            uint8_t *const at = dst + row * 128;
+            *reinterpret_cast<uint4 *>(at + ((ch ^ (row & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (D == 128)
+              *reinterpret_cast<uint4 *>(at + kQBlockBytes + ((ch ^ (row & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            else
+              *reinterpret_cast<uint4 *>(at + (((ch + 4) ^ (row & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
         fence_proxy_async_shared();
@@ -1210,25 +1134,25 @@ __global__ void __launch_bounds__(Cfg<D, F8, COPIES, PAIR, SEL>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------- launch
-template <int D, bool F8, int COPIES, bool PAIR, bool SEL>
+template <int D, bool F8, bool PAIR, bool SEL>
 cudaError_t launch(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm,
                    int num_ctas, cudaStream_t stream) {
-  using C = Cfg<D, F8, COPIES, PAIR, SEL>;
+  using C = Cfg<D, F8, PAIR, SEL>;
   static std::mutex mu;
   static bool done[128] = {};
   const cudaError_t e = once_per_device(mu, done, [] {
     if (C::kShareRegs) {
       // the register shares come out of what the launch gets: a smaller launch would wait forever
       cudaFuncAttributes f;
-      const cudaError_t got = cudaFuncGetAttributes(&f, tree_attention_kernel<D, F8, COPIES, PAIR, SEL>);
+      const cudaError_t got = cudaFuncGetAttributes(&f, tree_attention_kernel<D, F8, PAIR, SEL>);
       if (got != cudaSuccess) return got;
       if (f.numRegs != C::kRegsLaunch) return cudaErrorInvalidConfiguration;
     }
-    return cudaFuncSetAttribute(tree_attention_kernel<D, F8, COPIES, PAIR, SEL>,
+    return cudaFuncSetAttribute(tree_attention_kernel<D, F8, PAIR, SEL>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kDynamic);
   });
   if (e != cudaSuccess) return e;
-  return launch_cooperative(tree_attention_kernel<D, F8, COPIES, PAIR, SEL>, num_ctas, C::kThreads, C::kDynamic, stream,
+  return launch_cooperative(tree_attention_kernel<D, F8, PAIR, SEL>, num_ctas, C::kThreads, C::kDynamic, stream,
                             qm, km, vm, a);
 }
 

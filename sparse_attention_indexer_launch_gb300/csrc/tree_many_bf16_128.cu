@@ -5,9 +5,9 @@ namespace idx {
 
 cudaError_t launch_tree_many_bf16_128(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km,
                                   const CUtensorMap &vm, int num_ctas, cudaStream_t stream) {
-  if (a.sel != nullptr) return launch<128, false, 1, false, true>(a, qm, km, vm, num_ctas, stream);
-  return a.pair ? launch<128, false, 1, true, false>(a, qm, km, vm, num_ctas, stream)
-                : launch<128, false, 1, false, false>(a, qm, km, vm, num_ctas, stream);
+  if (a.sel != nullptr) return launch<128, false, false, true>(a, qm, km, vm, num_ctas, stream);
+  return a.pair ? launch<128, false, true, false>(a, qm, km, vm, num_ctas, stream)
+                : launch<128, false, false, false>(a, qm, km, vm, num_ctas, stream);
 }
 
 }  // namespace idx
