@@ -352,8 +352,16 @@ __device__ __forceinline__ Share share_of(const Walk &w, const Shares &sh, int G
   return s;
 }
 
+// A share's O: rows of D values, as the few-row kernel's threads (one per dimension) hold
+// them, or (BY_FOURS) groups of four dimensions of all rows, as the many-row kernel's (one per
+// row) do; either way a warp's stores and the join's loads are contiguous.
+template <int D, bool BY_FOURS>
+__device__ __forceinline__ int64_t share_at(int64_t slot, int slot_rows, int row, int d) {
+  return BY_FOURS ? ((slot * (D / 4) + d / 4) * slot_rows + row) * 4 : (slot * slot_rows + row) * D + d;
+}
+
 // Called by the 256 softmax threads of a CTA once its shares are written (thread 0's list).
-template <int D>
+template <int D, bool BY_FOURS>
 __device__ __forceinline__ void join_items(const TreeAttnArgs &a, const Share *shares, const int *count, bool ok) {
   const idx_tree_problem &p = a.p;
   constexpr int kBatch = 8;   // shares whose loads are in flight together
@@ -393,7 +401,15 @@ __device__ __forceinline__ void join_items(const TreeAttnArgs &a, const Share *s
     for (int u0 = begin; u0 < end; u0 += 256 / lanes) {
       const int u = u0 + static_cast<int>(threadIdx.x) / lanes;
       const bool live = u < end;
-      const int row = live ? u / (D / 4) : 0, d = live ? (u - row * (D / 4)) * 4 : 0;
+      int row = 0, d = 0;
+      if (live && BY_FOURS) {
+        d = u / s.nrow;
+        row = u - d * s.nrow;
+        d *= 4;
+      } else if (live) {
+        row = u / (D / 4);
+        d = (u - row * (D / 4)) * 4;
+      }
       const int tok = row / G;
       const int prow = a.pair && tok >= tb ? 128 + row - tb * G : row;
       float m = -INFINITY, l = 0.0f;
@@ -407,9 +423,9 @@ __device__ __forceinline__ void join_items(const TreeAttnArgs &a, const Share *s
           ml[y] = make_float2(-INFINITY, 0.0f);
           o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if (c >= s.count) continue;
-          const int64_t at = static_cast<int64_t>(c == 0 ? s.slot0 : 2 * (s.c0 + c)) * slot_rows + prow;
-          ml[y] = __ldcg(&a.part_ml[at]);
-          o[y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D + d));
+          const int64_t slot = c == 0 ? s.slot0 : 2 * (s.c0 + c);
+          ml[y] = __ldcg(&a.part_ml[slot * slot_rows + prow]);
+          o[y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + share_at<D, BY_FOURS>(slot, slot_rows, prow, d)));
         }
 #pragma unroll
         for (int y = 0; y < kBatch; ++y) {

@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       const bool has0 = odd < walk.count, has1 = (odd ^ 1) < walk.count;   // the streams that had tiles
       // an item's rows are G heads of consecutive tokens
       uint16_t *const out = a.out + (static_cast<int64_t>(row0) * p.Hq + walk.head * G) * D + d;
-      float *const part = a.part_o + static_cast<int64_t>(slot) * 128 * D + d;
+      float *const part = a.part_o + share_at<D, false>(slot, 128, 0, d);
       auto put = [&](int row, float o) {
         if (!walk.whole) {
           part[row * D] = o;
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       if (!walk.whole && tid == 0) bars.shares[bars.nshare++] = share_of(walk, share, G);
     }
     if (!ok) give_up();
-    join_items<D>(a, bars.shares, &bars.nshare, ok);
+    join_items<D, false>(a, bars.shares, &bars.nshare, ok);
   } else if (warp < kFewConvertWarp) {
     if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kFewKWarp || (!SEL && warp == kFewVWarp)) {

@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, PAIR, SEL>::kThreads, 1)
           *reinterpret_cast<uint2 *>(a.out + (static_cast<int64_t>(r) * p.Hq + hq) * D + d) =
               make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         } else {
-          *reinterpret_cast<float4 *>(a.part_o + (static_cast<int64_t>(slot) * kSlotRows + prow) * D + d) = o;
+          *reinterpret_cast<float4 *>(a.part_o + share_at<D, true>(slot, kSlotRows, prow, d)) = o;
         }
       };
       if (row < nrow && (PAIR || s == 0)) {
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, PAIR, SEL>::kThreads, 1)
       if (!walk.whole && tid == 0) bars.shares[bars.nshare++] = share_of(walk, share, G);
     }
     if (!ok) give_up();
-    join_items<D>(a, bars.shares, &bars.nshare, ok);
+    join_items<D, true>(a, bars.shares, &bars.nshare, ok);
   } else if (warp < kConvertWarp || C::kSplitIssue) {
     if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kKWarp || warp == kVWarp) {
