@@ -360,12 +360,103 @@ __device__ __forceinline__ int64_t share_at(int64_t slot, int slot_rows, int row
   return BY_FOURS ? ((slot * (D / 4) + d / 4) * slot_rows + row) * 4 : (slot * slot_rows + row) * D + d;
 }
 
+// Units [begin, end) of a split item: U per thread at a time, each by `lanes` lanes over the
+// shares, whose loads are issued BATCH at a time.
+template <int D, bool BY_FOURS, int U, int BATCH>
+__device__ __forceinline__ void join_units(const TreeAttnArgs &a, const Share &s, int begin, int end, int lanes,
+                                           int slot_rows, int tb) {
+  const idx_tree_problem &p = a.p;
+  const int G = p.Hq / p.cache.Hkv;
+  const int sub = (threadIdx.x & 31) & (lanes - 1);
+  const int step = 256 / lanes;
+  for (int u0 = begin; u0 < end; u0 += U * step) {
+    int row[U], d[U], prow[U];
+    bool live[U];
+    float m[U], l[U];
+    float4 acc[U];
+#pragma unroll
+    for (int z = 0; z < U; ++z) {
+      const int u = u0 + z * step + static_cast<int>(threadIdx.x) / lanes;
+      live[z] = u < end;
+      row[z] = d[z] = 0;
+      if (live[z] && BY_FOURS) {
+        d[z] = u / s.nrow;
+        row[z] = u - d[z] * s.nrow;
+        d[z] *= 4;
+      } else if (live[z]) {
+        row[z] = u / (D / 4);
+        d[z] = (u - row[z] * (D / 4)) * 4;
+      }
+      prow[z] = a.pair && row[z] >= tb * G ? 128 + row[z] - tb * G : row[z];
+      m[z] = -INFINITY;
+      l[z] = 0.0f;
+      acc[z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    for (int c0 = sub; c0 < s.count; c0 += BATCH * lanes) {
+      float2 ml[U][BATCH];
+      float4 o[U][BATCH];
+#pragma unroll
+      for (int z = 0; z < U; ++z)
+#pragma unroll
+        for (int y = 0; y < BATCH; ++y) {
+          const int c = c0 + y * lanes;
+          ml[z][y] = make_float2(-INFINITY, 0.0f);
+          o[z][y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (!live[z] || c >= s.count) continue;
+          const int64_t slot = c == 0 ? s.slot0 : 2 * (s.c0 + c);
+          ml[z][y] = __ldcg(&a.part_ml[slot * slot_rows + prow[z]]);
+          o[z][y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + share_at<D, BY_FOURS>(slot, slot_rows, prow[z], d[z])));
+        }
+#pragma unroll
+      for (int z = 0; z < U; ++z)
+#pragma unroll
+        for (int y = 0; y < BATCH; ++y) {
+          const float nm = fmaxf(m[z], ml[z][y].x);
+          const float f = ml[z][y].x == -INFINITY ? 0.0f : ex2(ml[z][y].x - nm), keep = m[z] == -INFINITY ? 0.0f : ex2(m[z] - nm);
+          m[z] = nm;
+          if (keep != 1.0f) {
+            l[z] = keep == 0.0f ? 0.0f : l[z] * keep;
+            acc[z].x = keep == 0.0f ? 0.0f : acc[z].x * keep;
+            acc[z].y = keep == 0.0f ? 0.0f : acc[z].y * keep;
+            acc[z].z = keep == 0.0f ? 0.0f : acc[z].z * keep;
+            acc[z].w = keep == 0.0f ? 0.0f : acc[z].w * keep;
+          }
+          if (f != 0.0f) {
+            l[z] += f * ml[z][y].y;
+            acc[z].x += f * o[z][y].x;
+            acc[z].y += f * o[z][y].y;
+            acc[z].z += f * o[z][y].z;
+            acc[z].w += f * o[z][y].w;
+          }
+        }
+    }
+#pragma unroll
+    for (int z = 0; z < U; ++z) {
+      float top = m[z];
+      for (int o = lanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float f = m[z] == -INFINITY ? 0.0f : ex2(m[z] - top);
+      float v[5] = {l[z], acc[z].x, acc[z].y, acc[z].z, acc[z].w};
+#pragma unroll
+      for (int y = 0; y < 5; ++y) v[y] = f == 0.0f ? 0.0f : v[y] * f;
+      for (int o = lanes / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int y = 0; y < 5; ++y) v[y] += __shfl_xor_sync(0xffffffffu, v[y], o);
+      if (!live[z] || sub != 0) continue;
+      const float inv = v[0] == 0.0f ? 0.0f : 1.0f / v[0];
+      const int tok = row[z] / G;
+      const int64_t at = static_cast<int64_t>(s.row0 + tok) * p.Hq + s.head * G + row[z] - tok * G;
+      *reinterpret_cast<uint2 *>(a.out + at * D + d[z]) =
+          make_uint2(pack_bf16(v[1] * inv, v[2] * inv), pack_bf16(v[3] * inv, v[4] * inv));
+      if (d[z] == 0 && a.lse != nullptr) a.lse[at] = v[0] == 0.0f ? -INFINITY : (top + log2f(v[0])) * kLn2;
+    }
+  }
+}
+
 // Called by the 256 softmax threads of a CTA once its shares are written (thread 0's list).
 template <int D, bool BY_FOURS>
 __device__ __forceinline__ void join_items(const TreeAttnArgs &a, const Share *shares, const int *count, bool ok) {
   const idx_tree_problem &p = a.p;
   constexpr int kBatch = 8;   // shares whose loads are in flight together
-  const int lane = threadIdx.x & 31;
   const int G = p.Hq / p.cache.Hkv;
   const int slot_rows = a.pair ? 256 : 128;
   const int tb = a.pair ? a.item_tokens / 2 : a.item_tokens;
@@ -397,74 +488,10 @@ __device__ __forceinline__ void join_items(const TreeAttnArgs &a, const Share *s
     // lanes per unit, over the shares: as many as the units leave of the 256 threads
     int lanes = 1;
     while (lanes < 32 && 2 * lanes * (end - begin) <= 256) lanes *= 2;
-    const int sub = lane & (lanes - 1);
-    for (int u0 = begin; u0 < end; u0 += 256 / lanes) {
-      const int u = u0 + static_cast<int>(threadIdx.x) / lanes;
-      const bool live = u < end;
-      int row = 0, d = 0;
-      if (live && BY_FOURS) {
-        d = u / s.nrow;
-        row = u - d * s.nrow;
-        d *= 4;
-      } else if (live) {
-        row = u / (D / 4);
-        d = (u - row * (D / 4)) * 4;
-      }
-      const int tok = row / G;
-      const int prow = a.pair && tok >= tb ? 128 + row - tb * G : row;
-      float m = -INFINITY, l = 0.0f;
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int c0 = live ? sub : s.count; c0 < s.count; c0 += kBatch * lanes) {
-        float2 ml[kBatch];
-        float4 o[kBatch];
-#pragma unroll
-        for (int y = 0; y < kBatch; ++y) {
-          const int c = c0 + y * lanes;
-          ml[y] = make_float2(-INFINITY, 0.0f);
-          o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (c >= s.count) continue;
-          const int64_t slot = c == 0 ? s.slot0 : 2 * (s.c0 + c);
-          ml[y] = __ldcg(&a.part_ml[slot * slot_rows + prow]);
-          o[y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + share_at<D, BY_FOURS>(slot, slot_rows, prow, d)));
-        }
-#pragma unroll
-        for (int y = 0; y < kBatch; ++y) {
-          const float nm = fmaxf(m, ml[y].x);
-          const float f = ml[y].x == -INFINITY ? 0.0f : ex2(ml[y].x - nm), keep = m == -INFINITY ? 0.0f : ex2(m - nm);
-          m = nm;
-          if (keep != 1.0f) {
-            l = keep == 0.0f ? 0.0f : l * keep;
-            acc.x = keep == 0.0f ? 0.0f : acc.x * keep;
-            acc.y = keep == 0.0f ? 0.0f : acc.y * keep;
-            acc.z = keep == 0.0f ? 0.0f : acc.z * keep;
-            acc.w = keep == 0.0f ? 0.0f : acc.w * keep;
-          }
-          if (f != 0.0f) {
-            l += f * ml[y].y;
-            acc.x += f * o[y].x;
-            acc.y += f * o[y].y;
-            acc.z += f * o[y].z;
-            acc.w += f * o[y].w;
-          }
-        }
-      }
-      float top = m;
-      for (int o = lanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float f = m == -INFINITY ? 0.0f : ex2(m - top);
-      float v[5] = {l, acc.x, acc.y, acc.z, acc.w};
-#pragma unroll
-      for (int y = 0; y < 5; ++y) v[y] = f == 0.0f ? 0.0f : v[y] * f;
-      for (int o = lanes / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int y = 0; y < 5; ++y) v[y] += __shfl_xor_sync(0xffffffffu, v[y], o);
-      if (live && sub == 0) {
-        const float inv = v[0] == 0.0f ? 0.0f : 1.0f / v[0];
-        const int64_t at = static_cast<int64_t>(s.row0 + tok) * p.Hq + s.head * G + row - tok * G;
-        *reinterpret_cast<uint2 *>(a.out + at * D + d) =
-            make_uint2(pack_bf16(v[1] * inv, v[2] * inv), pack_bf16(v[3] * inv, v[4] * inv));
-        if (d == 0 && a.lse != nullptr) a.lse[at] = v[0] == 0.0f ? -INFINITY : (top + log2f(v[0])) * kLn2;
-      }
-    }
+    if (BY_FOURS && s.count <= kBatch / 2)   // few shares of many rows: two units at a time keep as many loads in flight
+      join_units<D, BY_FOURS, 2, kBatch / 2>(a, s, begin, end, 1, slot_rows, tb);
+    else
+      join_units<D, BY_FOURS, 1, kBatch>(a, s, begin, end, lanes, slot_rows, tb);
   }
   // the last CTA out leaves the counters at zero for the next launch
   if (threadIdx.x == 0)
