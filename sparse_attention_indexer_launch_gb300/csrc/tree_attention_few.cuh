@@ -80,7 +80,9 @@ struct FewBarriers {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2][2];                    // [stream][S buffer]
   uint64_t p_ready[2][2], pv_done[2][2];    // [stream][P buffer]
-  uint64_t o_free[2], drain[2], stats[2], scrubbed[2];
+  uint64_t o_free[2], drain[2], scrubbed[2];
+  // [stream][segment parity]: a stream without tiles in a segment may be one segment ahead
+  uint64_t stats[2][2];
   uint32_t tmem_base;
   int abort;
   int32_t two_terms[2][2];         // [stream][P buffer]: a low term follows
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       }
       mbar_init(&bars.o_free[s], 8);
       mbar_init(&bars.drain[s], 1);
-      mbar_init(&bars.stats[s], 4);
+      for (int b = 0; b < 2; ++b) mbar_init(&bars.stats[s][b], 4);
       mbar_init(&bars.scrubbed[s], 4);
     }
     fence_barrier_init();
@@ -473,6 +475,9 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
         // see it get it back at the end)
         if (!SEL && !F8 && special) {
           const int sl = k % C::kVStages;
+          // (the stream's product before first: with two stages its V stood in the same one, and
+          // while that had not come this wait's parity would pass for it)
+          if (h != h0) ok = ok && settled(h - 1);
           ok = ok && warp_wait_all(&bars.v_full[sl], (k / C::kVStages) & 1);
           const int pos = key0 + key;
           const bool dead = pos >= walk.q.keys || !((bars.pages_ok[k & 31] >> (key >> 6)) & 1u);
@@ -576,8 +581,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       }
       if (key < N) bars.row_ref[sp2][s][key] = bars.ref[s][key];
       tc_fence_before();
-      warp_arrive(&bars.stats[s]);
-      ok = ok && warp_wait_all(&bars.stats[0], walk.seg & 1) && warp_wait_all(&bars.stats[1], walk.seg & 1);
+      warp_arrive(&bars.stats[s][sp2]);
+      ok = ok && warp_wait_all(&bars.stats[0][sp2], (walk.seg >> 1) & 1) && warp_wait_all(&bars.stats[1][sp2], (walk.seg >> 1) & 1);
       tc_fence_after();
       const int slot = (walk.first ? 0 : 1) + 2 * static_cast<int>(blockIdx.x);
       if (key < N) {

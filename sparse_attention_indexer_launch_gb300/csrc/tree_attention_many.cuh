@@ -91,7 +91,9 @@ struct Barriers {
   uint64_t sc_full[kMaxStages], sc_empty[kMaxStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];   // [stream][buffer]
-  uint64_t o_free[2], drain[2], drain_s[2], stats[2], scrubbed[2];
+  uint64_t o_free[2], drain[2], drain_s[2], scrubbed[2];
+  // [stream][segment parity]: a stream without tiles in a segment may be one segment ahead
+  uint64_t stats[2][2];
   uint32_t tmem_base;
   int abort;
   int32_t two_terms[2][2];         // P of [stream][buffer] has a low term
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, PAIR, SEL>::kThreads, 1)
       mbar_init(&bars.o_free[s], PAIR ? 4 : 8);
       mbar_init(&bars.drain[s], 1);
       mbar_init(&bars.drain_s[s], 1);
-      mbar_init(&bars.stats[s], 4);
+      for (int b = 0; b < 2; ++b) mbar_init(&bars.stats[s][b], 4);
       mbar_init(&bars.scrubbed[s], 4);
     }
     bars.abort = 0;
@@ -472,8 +474,9 @@ __global__ void __launch_bounds__(Cfg<D, F8, PAIR, SEL>::kThreads, 1)
         bars.row_m[sp][s][row] = m;
         bars.row_l[sp][s][row] = l;
         tc_fence_before();
-        warp_arrive(&bars.stats[s]);
-        if (!warp_wait_all(&bars.stats[s], walk.seg & 1) || !warp_wait_all(&bars.stats[s ^ 1], walk.seg & 1)) {
+        warp_arrive(&bars.stats[s][sp]);
+        if (!warp_wait_all(&bars.stats[s][sp], (walk.seg >> 1) & 1) ||
+            !warp_wait_all(&bars.stats[s ^ 1][sp], (walk.seg >> 1) & 1)) {
           ok = false;
           break;
         }
