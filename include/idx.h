@@ -300,7 +300,7 @@ idx_status idx_topk_noalloc(const float *scores, int64_t ld, const int32_t *row_
  * The state buffer of these calls is device memory, 1024-byte aligned, all zero
  * before its first use.  Its first word is a status word that errors found on the
  * device are or-ed into; idx_last_device_status reads and clears it.  Calls that
- * overlap in time need a state each. */
+ * overlap in time need a state each, and after IDX_ETIMEOUT a state is zeroed anew. */
 #define IDX_MAX_REQS 4096     /* requests of a step */
 #define IDX_MAX_TREE 64       /* drafted tokens of one request (bits of a mask) */
 
@@ -310,7 +310,8 @@ idx_status idx_topk_noalloc(const float *scores, int64_t ld, const int32_t *row_
  * free_pages[free_count - 1], free_pages[free_count - 2], ...  A prompt is a
  * request with ctx_len 0. */
 typedef struct {
-    const int32_t *ctx_len;    /* device int32 [Q]: tokens each request has cached (< 0 reads as 0) */
+    const int32_t *ctx_len;    /* device int32 [Q]: tokens each request has cached (< 0 reads as 0,
+                                  lengths above 2^30 - 64 as that) */
     const int32_t *new_len;    /* device int32 [Q]: new tokens of each request (< 0 reads as 0) */
     const int32_t *parent;     /* device int32 [cap] or NULL (a chain): the parent of row r as a token number
                                   of its request, below the row's own number; -1 for a root */
@@ -407,9 +408,11 @@ size_t idx_tree_state_size(const idx_tree_problem *problem, int32_t sel_k);
  *   out  device bf16 [R][Hq][D], 16-byte aligned.
  *   lse  device fp32 [R][Hq] or NULL.
  * Rows outside every request are not written.  Sums and softmax statistics are fp32;
- * the probabilities are rounded to bf16 for the product with V (to two bf16 terms where
- * fewer than 64 keys of a 64-key tile are visible to all).  The result does not
- * depend on how the work was split in a way that changes between equal calls.
+ * the probabilities are rounded to bf16 for the product with V (to two bf16 terms in
+ * tiles of 64 or 128 positions that are not visible as a whole to every row); beside an
+ * E4M3 cache q is used as the sum of two E4M3 terms, exact for elements down to 2^-9 of
+ * its row's largest and to 2^-17 of that below.  Equal calls give equal bits.
+ * The launch is cooperative: its CTAs, at most one per SM, run at the same time.
  * Device-detected (IDX_EDEVICE): a page id outside [0, P) (its tokens are left out),
  * ctx_len outside 0 .. max_ctx, more rows than max_new or positions past the page
  * table (clamped), row_start outside 0 .. R.  IDX_ETIMEOUT: a wait ran out.
