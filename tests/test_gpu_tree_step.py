@@ -122,3 +122,18 @@ def test_a_state_serves_call_after_call(lib, Hq, new):
     o, z = t.attend(state=s.state)
     fresh, zf = t.attend()
     assert torch.equal(o, fresh) and torch.equal(z, zf)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [4, 32, 64, 128])
+def test_selected_shares_of_many_tiles(lib, kv, D, G):
+    """Enough rows for every CTA to walk several tiles and items: each ring of stages turns over."""
+    ctx, new = [3579, 700, 2100, 64], [30, 40, 13, 25]
+    s = tu.Step(ctx, new, G, 1, D, kv, masks=_trees(47, new), seed=48)
+    sel = _select(s, 2048, 49, False)
+    out, lse = s.attend(sel)
+    assert s.status() == lib.IDX_OK
+    tu.check(s, out, lse, sel)
+    again, _ = s.attend(sel, state=s.state)
+    assert torch.equal(out, again)
