@@ -952,15 +952,11 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
             ok = false;
             break;
           }
-          const int64_t off = slot < 0 ? -1
-                                       : (slot / kPage * p.cache.page_stride + slot % kPage * p.cache.token_stride +
-                                          walk.head * p.cache.head_stride) *
-                                             (F8 ? 1 : 2);
           const int32_t row = slot < 0 ? static_cast<int32_t>(a.cache_rows)
                                        : slot / kPage * a.row_page + slot % kPage * a.row_token + walk.head * a.row_head;
-#pragma unroll
-          for (int part = 0; part < 2 && ok; ++part) {
-            if (part == 0) k_loads = k + 1;
+          k_loads = k + 1;
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
             if (part == 1 && !kTogether && !v_free()) {
               ok = false;
               break;
@@ -989,6 +985,10 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
               // 16 bytes per thread: D / 16 or D / 8 lanes bring one key
               constexpr int kLanes = F8 ? D / 16 : D / 8, kKeysAtOnce = 32 / kLanes;
               const int ch = lane % kLanes;
+              const int64_t off = slot < 0 ? -1
+                                           : (slot / kPage * p.cache.page_stride + slot % kPage * p.cache.token_stride +
+                                              walk.head * p.cache.head_stride) *
+                                                 (F8 ? 1 : 2);
 #pragma unroll 4
               for (int y = 0; y < kLanes; ++y) {
                 const int from = y * kKeysAtOnce + lane / kLanes, at_key = w4 * 32 + from;
