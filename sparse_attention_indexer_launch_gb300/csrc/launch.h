@@ -143,11 +143,6 @@ struct TreeAttnArgs {
   int32_t pair;            // its rows are two blocks of item_tokens / 2 tokens
   int32_t tile;            // keys per tile
   int32_t rows;            // rows that the few-row kernel provides for, 0: the many-row kernel
-  // selected: the cache as rows of equal pitch, for loads of four rows at a time.  A slot's
-  // row is page * row_page + token * row_token + head * row_head, its first dimension at
-  // head * row_x; rows: how many there are, 0 for a layout without a common pitch.
-  int64_t cache_rows, row_pitch;
-  int32_t row_page, row_token, row_head, row_x;
 };
 constexpr int kTreeMaxCtas = 160;   // shares of an attention launch, at most
 

@@ -2,7 +2,6 @@
 #include <cuda.h>
 
 #include <cmath>
-#include <numeric>
 
 #include "idx.h"
 #include "idx_device.cuh"
@@ -45,9 +44,11 @@ idx_status check_cache(const idx_kv_cache *c) {
   return IDX_OK;
 }
 
-// The launch's shape: up to 64 rows of a request and key/value head (selected: of a token)
-// go to the few-row kernel, up to 128 to the many-row kernel in one block, more in pairs of
-// blocks that share every K and V tile.
+// The launch's shape.  Up to 64 rows of a request and key/value head (selected: of a token)
+// go to the few-row kernel, over a bf16 cache up to 32 (64 rows of 4 tokens at 131,072 keys:
+// 110 us there, 102 us in the many-row kernel; E4M3 130 against 174); up to 128 rows to the
+// many-row kernel in one block, more in pairs of blocks that share every K and V tile (4
+// requests of 64 x 64 rows: 186 us, one block at a time 204).
 struct Shape {
   int rows;           // the few-row kernel's N, or 0
   int tile;           // keys
@@ -58,7 +59,7 @@ Shape shape_of(const idx_tree_problem *p, int32_t sel_k) {
   Shape s{};
   const int G = p->Hq / p->cache.Hkv;
   const int rows = (sel_k > 0 ? 1 : p->max_new) * G;
-  if (rows <= 64) {
+  if (rows <= (sel_k > 0 || p->cache.kv_dtype == IDX_KV_E4M3 ? 64 : 32)) {
     s.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     s.tile = 128;
     s.block_tokens = sel_k > 0 ? 1 : s.rows / G;
@@ -145,48 +146,6 @@ idx_status cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const idx_kv_cach
   return r == CUDA_SUCCESS ? IDX_OK : IDX_ECUDA;
 }
 
-// The cache as rows of equal pitch, where its strides allow: a slot's row, or its row of one
-// head, then is one row of a 2-D tensor, and four of them come with one load.  Measured with
-// 64 requests, 2,048 selected positions, E4M3: @@ us by rows, @@ us by threads' copies.
-void row_layout(const idx_kv_cache *c, idx::TreeAttnArgs *a) {
-  int64_t pitch = std::gcd(c->page_stride, c->token_stride), rows = 0;
-  int64_t row_head = 0, row_x = c->head_stride;
-  if ((c->Hkv - 1) * c->head_stride + c->D > pitch) {   // heads are rows of their own
-    pitch = std::gcd(pitch, c->head_stride);
-    row_head = c->head_stride / pitch;
-    row_x = 0;
-  }
-  const int64_t row_page = c->page_stride / pitch, row_token = c->token_stride / pitch;
-  constexpr int64_t kMost = INT32_MAX;
-  if (pitch >= c->D && row_page <= kMost / c->P && row_token <= kMost / IDX_PAGE && row_head <= kMost / c->Hkv &&
-      row_x <= kMost / c->Hkv)
-    rows = (c->P - 1) * row_page + (IDX_PAGE - 1) * row_token + (c->Hkv - 1) * row_head + 1;
-  if (rows < 1 || rows >= kMost) return;
-  a->cache_rows = rows;
-  a->row_page = static_cast<int32_t>(row_page);
-  a->row_token = static_cast<int32_t>(row_token);
-  a->row_head = static_cast<int32_t>(row_head);
-  a->row_x = static_cast<int32_t>(row_x);
-  a->row_pitch = pitch;
-}
-idx_status row_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const idx_kv_cache *c, const idx::TreeAttnArgs &a, bool is_v,
-                   CUtensorMap *map) {
-  const bool f8 = c->kv_dtype == IDX_KV_E4M3;
-  const cuuint64_t e = f8 ? 1 : 2;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>((c->Hkv - 1) * static_cast<int64_t>(a.row_x) + c->D),
-                              static_cast<cuuint64_t>(a.cache_rows)};
-  const cuuint64_t strides[1] = {a.row_pitch * e};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(f8 ? c->D : 64), 1}, one[2] = {1, 1};
-  const CUtensorMapL2promotion promote = c->D * e >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-                                         : c->D * e >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
-                                                           : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
-  return encode(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, is_v ? c->v : c->k, dims,
-                strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, cache_swizzle(c, is_v), promote,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? IDX_OK
-             : IDX_ECUDA;
-}
-
 idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, void *out, float *lse, void *state,
                   size_t state_bytes, void *stream) {
   idx_status st = check_problem(p, sel_k);
@@ -217,11 +176,7 @@ idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, 
   if (sel == nullptr) {
     st = cache_map(encode, &p->cache, false, &km);
     if (st == IDX_OK) st = cache_map(encode, &p->cache, true, &vm);
-  } else if (s.rows > 0) {
-    row_layout(&p->cache, &a);
-    if (a.cache_rows > 0) st = row_map(encode, &p->cache, a, false, &km);
-    if (a.cache_rows > 0 && st == IDX_OK) st = row_map(encode, &p->cache, a, true, &vm);
-  }
+  }   // selected positions are gathered by plain loads
   if (st != IDX_OK) return st;
   a.p = *p;
   a.sel = sel;

@@ -169,8 +169,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
 
   if (tid < 8) {
     const int s = tid;
-    // selected: four warps bring a tile, with bulk loads or each thread with its copies
-    const int loaders = !SEL ? 1 : a.cache_rows > 0 ? 4 : 128;
+    constexpr int loaders = SEL ? 128 : 1;    // selected: each thread of a team with its copies
     mbar_init(&bars.k_full[s], loaders);
     mbar_init(&bars.k_empty[s], 1);
     mbar_init(&bars.v_full[s], F8 ? 4 * C::kTeams : loaders);
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
     for (int x = tid; x < C::kQBufs * C::kQBytes / 16; x += C::kThreads) reinterpret_cast<uint4 *>(sq)[x] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_shared();
   }
-  if ((!SEL || a.cache_rows > 0) && tid == kFewKWarp * 32) {
+  if (!SEL && tid == kFewKWarp * 32) {
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
   }
@@ -894,10 +893,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       if constexpr (C::kShareRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
       const int key = tid - C::kLookupWarp * 32, w4 = key >> 5;
       constexpr int kVRing = F8 ? C::kRawStages : C::kVStages;
-      constexpr bool kTogether = kVRing >= 4;
       uint64_t *const vfull = F8 ? bars.raw_full : bars.v_full;
       int k = 0;     // tiles so far
-      int k_loads = 0;   // and loads of K
       bool ok = true;
       while (ok && walk.next()) {
         const int32_t *const table = p.page_table + static_cast<int64_t>(walk.i) * p.pt_stride;
@@ -926,9 +923,6 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
           e = entry(n + 2 * kFewTile);
           const uint32_t bits = __ballot_sync(0xffffffffu, slot >= 0);
           const int ks = k % C::kKStages, vs = k % kVRing, ss = k % C::kScaleStages;
-          auto v_free = [&]() -> bool {
-            return warp_wait_all(&(F8 ? bars.raw_empty : bars.v_empty)[vs], ((k / kVRing) & 1) ^ 1);
-          };
           if (!warp_wait_all(&bars.k_empty[ks], ((k / C::kKStages) & 1) ^ 1) ||
               (F8 && !warp_wait_all(&bars.sc_empty[ss], ((k / C::kScaleStages) & 1) ^ 1))) {
             ok = false;
@@ -945,75 +939,42 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
                          : "memory");
             cp_async_arrive(&bars.sc_full[ss]);
           }
-          // S runs up to four tiles ahead of the products that free V's stages.  With four
-          // stages of V a tile's K and V are issued together; with two, K first, then V
-          // once its stage is free.
-          if (kTogether && !v_free()) {
-            ok = false;
-            break;
-          }
-          const int32_t row = slot < 0 ? static_cast<int32_t>(a.cache_rows)
-                                       : slot / kPage * a.row_page + slot % kPage * a.row_token + walk.head * a.row_head;
-          k_loads = k + 1;
+          // K first, then V once its stage is free: S runs up to four tiles ahead of the
+          // products that free V's stages, and must not wait for them.
+          const int64_t off = slot < 0 ? -1
+                                       : (slot / kPage * p.cache.page_stride + slot % kPage * p.cache.token_stride +
+                                          walk.head * p.cache.head_stride) *
+                                             (F8 ? 1 : 2);
 #pragma unroll 1
-          for (int part = 0; part < 2; ++part) {
-            if (part == 1 && !kTogether && !v_free()) {
+          for (int is_v = 0; is_v < 2; ++is_v) {
+            if (is_v && !warp_wait_all(&(F8 ? bars.raw_empty : bars.v_empty)[vs], ((k / kVRing) & 1) ^ 1)) {
               ok = false;
               break;
             }
-            constexpr int kBoxes = F8 ? 1 : kBlocks, kBoxBytes = F8 ? D : 128;   // of a row
-            const bool rows_together = kTogether && a.cache_rows > 0;
-            if (rows_together && part == 1) break;
-            // the first lanes bring K, with kTogether the next ones V
-            const bool is_v = rows_together ? lane >= 8 * kBoxes : part == 1;
             uint8_t *const dst = is_v ? (F8 ? sraw : sv) + vs * C::kKBytes : sk + ks * C::kKBytes;
-            uint64_t *const full = is_v ? &vfull[vs] : &bars.k_full[ks];
-            if (a.cache_rows > 0) {
-              // Four rows at a time (bf16: twice, for both blocks of 64 dimensions).  A row
-              // outside the cache reads as zero.
-              if (lane == 0) mbar_arrive_expect_tx(full, C::kKBytes / 4);
-              if (rows_together && lane == 0) mbar_arrive_expect_tx(&vfull[vs], C::kKBytes / 4);
-              int32_t rows[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x) rows[x] = __shfl_sync(0xffffffffu, row, (lane & 7) * 4 + x);
-              const int b = (lane >> 3) % kBoxes;
-              if (lane < 8 * kBoxes * (rows_together ? 2 : 1))
-                tma_gather4(dst + b * kBlockBytes + (w4 * 32 + (lane & 7) * 4) * kBoxBytes, is_v ? &vmap : &kmap,
-                            walk.head * a.row_x + b * 64, rows[0], rows[1], rows[2], rows[3], full);
-              __syncwarp();
-            } else {
-              // 16 bytes per thread: D / 16 or D / 8 lanes bring one key
-              constexpr int kLanes = F8 ? D / 16 : D / 8, kKeysAtOnce = 32 / kLanes;
-              const int ch = lane % kLanes;
-              const int64_t off = slot < 0 ? -1
-                                           : (slot / kPage * p.cache.page_stride + slot % kPage * p.cache.token_stride +
-                                              walk.head * p.cache.head_stride) *
-                                                 (F8 ? 1 : 2);
+            // 16 bytes per thread: D / 16 or D / 8 lanes bring one key
+            constexpr int kLanes = F8 ? D / 16 : D / 8, kKeysAtOnce = 32 / kLanes;
+            const int ch = lane % kLanes;
 #pragma unroll 4
-              for (int y = 0; y < kLanes; ++y) {
-                const int from = y * kKeysAtOnce + lane / kLanes, at_key = w4 * 32 + from;
-                const int64_t o = __shfl_sync(0xffffffffu, off, from);
-                uint32_t at;   // bf16: blocks of 128-byte rows, swizzled; E4M3 K: rows of D, swizzled; V: rows of D
-                if (!F8) at = (ch >> 3) * kBlockBytes + at_key * 128 + (((ch & 7) ^ (at_key & 7)) << 4);
-                else if (is_v) at = at_key * D + ch * 16;
-                else at = at_key * D + ((D == 128 ? ch ^ (at_key & 7) : ch ^ ((at_key >> 1) & 3)) << 4);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + at)),
-                             "l"(static_cast<const uint8_t *>(is_v ? p.cache.v : p.cache.k) + (o < 0 ? 0 : o) + ch * 16),
-                             "r"(o < 0 ? 0 : 16)
-                             : "memory");
-              }
-              cp_async_arrive(full);
+            for (int y = 0; y < kLanes; ++y) {
+              const int from = y * kKeysAtOnce + lane / kLanes, at_key = w4 * 32 + from;
+              const int64_t o = __shfl_sync(0xffffffffu, off, from);
+              uint32_t at;   // bf16: blocks of 128-byte rows, swizzled; E4M3 K: rows of D, swizzled; V: rows of D
+              if (!F8) at = (ch >> 3) * kBlockBytes + at_key * 128 + (((ch & 7) ^ (at_key & 7)) << 4);
+              else if (is_v) at = at_key * D + ch * 16;
+              else at = at_key * D + ((D == 128 ? ch ^ (at_key & 7) : ch ^ ((at_key >> 1) & 3)) << 4);
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + at)),
+                           "l"(static_cast<const uint8_t *>(is_v ? p.cache.v : p.cache.k) + (o < 0 ? 0 : o) + ch * 16),
+                           "r"(o < 0 ? 0 : 16)
+                           : "memory");
             }
+            cp_async_arrive(is_v ? &vfull[vs] : &bars.k_full[ks]);
           }
           if (!ok) break;
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (!ok && lane == 0) give_up();
-      if (lane == 0 && a.cache_rows > 0) {
-        land(bars.k_full, C::kKStages, k_loads);
-        land(vfull, kVRing, k);
-      }
     }
   } else {
     if constexpr (F8) {

@@ -12,8 +12,7 @@ cudaError_t launch_tree_few_bf16_128(const TreeAttnArgs &a, const CUtensorMap &q
   if (a.rows == 32)
     return sel ? launch_few_rows<128, false, 32, true>(a, qm, km, vm, num_ctas, stream)
                : launch_few_rows<128, false, 32, false>(a, qm, km, vm, num_ctas, stream);
-  return sel ? launch_few_rows<128, false, 64, true>(a, qm, km, vm, num_ctas, stream)
-             : launch_few_rows<128, false, 64, false>(a, qm, km, vm, num_ctas, stream);
+  return launch_few_rows<128, false, 64, true>(a, qm, km, vm, num_ctas, stream);   // 64 rows: selected only
 }
 
 }  // namespace idx
