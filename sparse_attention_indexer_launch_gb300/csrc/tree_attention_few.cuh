@@ -945,7 +945,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
                                        : (slot / kPage * p.cache.page_stride + slot % kPage * p.cache.token_stride +
                                           walk.head * p.cache.head_stride) *
                                              (F8 ? 1 : 2);
-#pragma unroll 1
+#pragma unroll
           for (int is_v = 0; is_v < 2; ++is_v) {
             if (is_v && !warp_wait_all(&(F8 ? bars.raw_empty : bars.v_empty)[vs], ((k / kVRing) & 1) ^ 1)) {
               ok = false;
@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
             // 16 bytes per thread: D / 16 or D / 8 lanes bring one key
             constexpr int kLanes = F8 ? D / 16 : D / 8, kKeysAtOnce = 32 / kLanes;
             const int ch = lane % kLanes;
-#pragma unroll 4
+#pragma unroll 8
             for (int y = 0; y < kLanes; ++y) {
               const int from = y * kKeysAtOnce + lane / kLanes, at_key = w4 * 32 + from;
               const int64_t o = __shfl_sync(0xffffffffu, off, from);
