@@ -321,8 +321,8 @@ __device__ __forceinline__ Start find_share(const TreeAttnArgs &a, Start *found,
 // ---------------------------------------------------------------------------- join
 // A split item is joined by the CTAs that share it.  Each leaves its share (O before the
 // division, the rows' references and sums) in its slot of the state and counts itself in;
-// once all are in, each joins its part of the item's outputs, four values at a time.  The launch is cooperative: the CTAs that wait for each other run at
-// the same time.
+// once all are in, each joins its part of the item's outputs, four values at a time, in CTA
+// order.  The launch is cooperative: the CTAs that wait for each other run at the same time.
 struct Share {
   int row0, head, nrow;   // the item's first row of q, key/value head, rows
   int c0, count;          // its first CTA, and how many there are

@@ -16,9 +16,14 @@
 // tells the four warps, and only then are the row maxima taken.  Row sums stay with the
 // threads until the item ends.  K's scale is one factor per thread, V's another.
 //
-// Two streams take the even and odd tiles of the CTA's share, each with two S buffers, its own O,
-// an MMA-issuing thread and four softmax warps; they are joined in TMEM at the item's
-// end.  Work is dealt out as tree_attention_many.cuh says.
+// Two streams take the even and odd tiles of the CTA's share, each with two S buffers, its
+// own O, an MMA-issuing thread and four softmax warps; they are joined in TMEM at the item's
+// end.  An item is (request, key/value head, block of tokens) with its tiles in position
+// order; the launch's tiles, in item order, are dealt out as one even, contiguous share per
+// CTA, and a split item is joined by the CTAs that hold it.
+//
+// Selected positions: the tiles are 128 entries of a row's selection (then its ancestors),
+// and a team of four warps looks them up and copies K, V and scales, 16 bytes a thread.
 //
 // E4M3 keys feed the tensor core as they are: a row of Q, scaled by a power of two to
 // at most 448, is split into two E4M3 terms whose sum it is (exactly, for elements down
@@ -26,6 +31,14 @@
 // terms' products.  P needs bf16's range (two E4M3 terms would drop what lies below
 // 2^-18 of the largest, which adds up over a long cache), so V is converted to bf16 in
 // shared memory, exactly.
+//
+// What bounds it.  bf16: memory (4 tokens of 64 heads over 131,072 keys of 8 heads 98 us, 5.5
+// TB/s).  E4M3: the chain of a tile's steps in the softmax warps, with the conversion of V
+// taking issue slots beside it (the same 84.5 us, 3.3 TB/s; 64 requests of D = 64 287 us, 2.4
+// TB/s): two tiles per step, the tiles' waits hidden behind the TMEM reads and sleeping
+// waits were all no faster.  Selected: the copies, at 16 bytes a thread (150 rows over 2,048
+// positions of 2 E4M3 heads 102 us).  Small calls: the chain launch, lookups, one tile, join
+// (one token over 4,096 keys 16.4 us; 8 rows over 2,048 selected positions 23 us).
 #pragma once
 
 #include "tree_attention_common.cuh"
@@ -33,9 +46,10 @@
 namespace idx {
 namespace {
 
-// Warps 0-3 and 4-7: softmax of streams 0 and 1; 8 and 11: loads of K and of V (by TMA,
-// or gathering selected positions); 9 and 10: MMA issuers of streams 0 and 1; 12-19 with
-// an E4M3 cache: the split of Q, and V to bf16, in teams of four on a part of every tile.
+// Warps 0-3 and 4-7: softmax of streams 0 and 1; 8 and 11: loads of K (and a bf16 Q) and of
+// V by TMA; 9 and 10: MMA issuers of streams 0 and 1; from 12 on with an E4M3 cache: the
+// split of Q, and V to bf16, in teams of four on a part of every tile; then, for selected
+// positions, the team that gathers.
 constexpr int kFewKWarp = 8, kFewIssuerWarp = 9, kFewVWarp = 11, kFewConvertWarp = 12;
 constexpr int kFewTile = 128;
 
@@ -49,9 +63,10 @@ struct FewCfg {
   static constexpr int kPBufs = N == 64 ? 1 : 2;           // per stream
   static constexpr int kQBufs = F8 && N == 64 ? 1 : 2;
   static constexpr int kFixed = kQBufs * kQBytes + 2 * kPBufs * kPBytes;
-  // Tiles in flight, as shared memory allows.  The streams take alternate tiles, so the counts are even: a stage then always has the same waiter.  Were
-  // they odd, a waiter could come to a stage again before the other's tile in between, and
-  // the parity of the barrier would pass for the one that it waits for.
+  // Tiles in flight, as shared memory allows.  The streams take alternate tiles, so the counts
+  // are even: a stage then always has the same waiter.  Were they odd, a waiter could come to
+  // a stage again before the other's tile in between, and the parity of the barrier would
+  // pass for the one that it waits for.
   static constexpr int kKStages = F8 ? (D == 64 ? 6 : N == 16 ? 4 : 2) : D == 64 ? (N == 16 ? 6 : 4) : 2;
   static constexpr int kVStages = F8 ? (D == 64 ? 4 : 2) : D == 64 ? 6 : N == 16 ? 4 : 2;   // as bf16
   static constexpr int kRawStages = F8 ? 4 : 0;                                             // V as E4M3
