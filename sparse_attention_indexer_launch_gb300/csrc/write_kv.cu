@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) write_kv_kernel(const Wr
   float *const scale = F8 ? (is_v ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(h) * kPage : nullptr;
   const uint32_t limit = static_cast<uint32_t>(min(a.c.P * kPage, static_cast<int64_t>(INT32_MAX)));   // slots
 
-  // the warp stays together: its first row decides
+  // the warp stays together while any of its groups has rows left
   while (__any_sync(0xffffffffu, row < a.R)) {
     uint4 x[kVectors];
     uint32_t slot[kVectors];
