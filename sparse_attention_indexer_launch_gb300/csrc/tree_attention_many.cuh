@@ -130,6 +130,7 @@ __device__ __forceinline__ bool raise_maximum(uint32_t to, float top, bool has_o
   l *= f;
   if (!has_o) return true;
   if (!settled()) return false;
+  tc_fence_after();   // the product's O, before it is read
 #pragma unroll 1
   for (int w = 0; w < D / 16; ++w) {
     uint32_t x[16];

@@ -1,0 +1,46 @@
+"""Attention where its paths meet their edges: references that rise over a whole cache."""
+import numpy as np
+import pytest
+import torch
+
+from tests import tree_util as tu
+from tests.test_gpu_tree_attention import _trees
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.fail("no CUDA device")
+    import sparse_attention_indexer_launch_gb300 as lib
+    return lib
+
+
+def _rising(step, i, h, rise):
+    """Keys of request i, head h grow by `rise` a page: scores of spread 1 become ones of spread
+    rise, 2 rise, 3 rise ..., whose maxima over a page's 64 keys lie some 2.4 rise apart."""
+    ctx = step.ctx[i]
+    j = np.arange(ctx)
+    page = torch.from_numpy(step.table[i, j // 64].astype(np.int64)).cuda()
+    off = torch.from_numpy(j % 64).cuda()
+    grow = torch.from_numpy(rise * (1.0 + j // 64)).cuda()[:, None]
+    if step.kv == "bf16":
+        step.k[page, off, h] = (step.k[page, off, h].double() * grow).bfloat16()
+    else:
+        step.k_scale[page, h, off] = (step.k_scale[page, h, off].double() * grow[:, 0]).float()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,new", [(128, [1]), (64, [64]), (96, [5]), (16, [3])])
+def test_references_that_rise_page_after_page(lib, kv, D, Hq, new):
+    """Scores that pass their row's reference by 2^30 (21 in natural units) in one page after
+    another: O is scaled again and again, each time after the product that wrote it."""
+    s = tu.Step([700], new, Hq, 1, D, kv, masks=_trees(50, new), seed=51)
+    _rising(s, 0, 0, 12.0)
+    out, lse = s.attend()
+    assert s.status() == lib.IDX_OK
+    tu.check(s, out, lse)
+    again, _ = s.attend(state=s.state)
+    assert torch.equal(out, again)
