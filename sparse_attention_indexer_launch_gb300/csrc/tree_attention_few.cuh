@@ -379,8 +379,10 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int r = 0; r < N; ++r) asm volatile("" : "+r"(x[r]));
-          if (pass == 0 && h == h0 && open) {
-            // the first tile: the references are its first key's scores
+          // the first tile, where every row sees its first key: the references are that key's
+          // scores.  The four warps decide it together: one whose wait ran out may have read
+          // `open` from a tile that never came, and none may meet the barrier below alone.
+          if (pass == 0 && h == h0 && !team_any(s, !ok || !open)) {
             if (key == 0) {
 #pragma unroll
               for (int r = 0; r < N; ++r) {

@@ -44,3 +44,17 @@ def test_references_that_rise_page_after_page(lib, kv, D, Hq, new):
     tu.check(s, out, lse)
     again, _ = s.attend(state=s.state)
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,new", [((8, 2), 3), ((32, 1), 1), ((64, 1), 1), ((16, 2), 16)])
+def test_many_items_whose_first_key_some_rows_do_not_see(lib, kv, heads, new):
+    """Items that begin with a tile every row sees the first key of, and items that do not (no
+    cached token), in turn within one CTA's share."""
+    ctx = [0, 40, 130, 0, 300, 0, 128, 1] * 25
+    rng = np.random.default_rng(52)
+    counts = rng.integers(1, new + 1, len(ctx)).tolist()
+    s = tu.Step(ctx, counts, *heads, 128, kv, masks=_trees(53, counts), seed=54)
+    out, lse = s.attend()
+    assert s.status() == lib.IDX_OK
+    tu.check(s, out, lse)
