@@ -329,7 +329,8 @@ typedef struct {
     int64_t P;                 /* pages of the cache, 1 .. INT32_MAX / 64 */
     int32_t Q;                 /* requests, 1 .. IDX_MAX_REQS */
     int32_t pt_stride;         /* page-table row length, >= 1 */
-    int32_t cap;               /* rows that the per-row arrays hold, >= 0 (0: only tables and row_start) */
+    int32_t cap;               /* rows that the per-row arrays hold, 0 .. INT32_MAX - 3 (0: only tables and
+                                  row_start) */
 } idx_tree_tables_args;
 
 /* Bytes of state that idx_tree_tables needs. */
@@ -342,7 +343,7 @@ size_t idx_tree_tables_state_size(void);
  * row), a page id outside [0, P) (slot -1), a parent that is not an earlier token
  * (read as a root), a request of more than IDX_MAX_TREE new tokens with parents or
  * masks asked for (those past the 64th: mask 0, depth counted as in a chain).  IDX_EINVAL for a NULL or bad
- * argument, IDX_EUNSUPPORTED for Q or P above the limits; launches nothing then. */
+ * argument, IDX_EUNSUPPORTED for Q, P or cap above the limits; launches nothing then. */
 idx_status idx_tree_tables(const idx_tree_tables_args *args, void *state, size_t state_bytes, void *stream);
 
 /* A paged key/value cache.  Element (page p, token s, head h, dim d) of K and of V

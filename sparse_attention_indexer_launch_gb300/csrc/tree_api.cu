@@ -217,6 +217,7 @@ idx_status idx_tree_tables(const idx_tree_tables_args *t, void *state, size_t st
     return IDX_EINVAL;
   if (t->free_left == t->free_count || !aligned(t->mask, 8)) return IDX_EINVAL;
   if (t->Q > IDX_MAX_REQS || t->P > INT32_MAX / IDX_PAGE) return IDX_EUNSUPPORTED;
+  if (t->cap > INT32_MAX - 3) return IDX_EUNSUPPORTED;   // a thread's four rows end within 31 bits
   if (!state_ok(state, state_bytes, kStatusBytes)) return IDX_EINVAL;
   int sms = 0;
   const idx_status st = idx::device_sms(&sms);

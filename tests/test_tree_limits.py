@@ -1,0 +1,26 @@
+"""Sizes and addresses that the verify step's kernels could not follow are refused on the host,
+before any GPU call."""
+import ctypes
+
+import pytest
+
+from tests.test_tree_abi import FAKE, _attend, _cache, _problem, _tables, _write
+
+INT32_MAX = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    import sparse_attention_indexer_launch_gb300 as lib
+    return lib
+
+
+def test_rows_are_counted_in_31_bits(lib):
+    """A thread stores four rows from r on, r < cap a multiple of four: r + 4 has to fit."""
+    for cap in (INT32_MAX - 2, INT32_MAX - 1, INT32_MAX):
+        assert (cap - 1) // 4 * 4 + 4 > INT32_MAX
+        t = _tables(lib, cap=cap)
+        assert lib.lib.idx_tree_tables(ctypes.byref(t), FAKE, 1024, None) == lib.IDX_EUNSUPPORTED, cap
+    assert (INT32_MAX - 3 - 1) // 4 * 4 + 4 <= INT32_MAX
