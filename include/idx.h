@@ -385,7 +385,7 @@ typedef struct {
     int32_t R;                 /* rows that q and the outputs hold, 1 .. IDX_MAX_ROWS */
     int32_t Q;                 /* requests, 1 .. IDX_MAX_REQS */
     int32_t pt_stride;
-    int32_t max_ctx;           /* host upper bound on every ctx_len, 0 .. pt_stride * 64 */
+    int32_t max_ctx;           /* host upper bound on every ctx_len, 0 .. pt_stride * 64, at most 2^30 */
     int32_t max_new;           /* host upper bound on every request's rows, 1 .. IDX_MAX_TREE */
     int32_t Hq;                /* query heads, a multiple of cache.Hkv; head h reads key/value head h / (Hq / Hkv);
                                   Hq / Hkv at most 128 */

@@ -12,6 +12,7 @@ namespace {
 constexpr size_t kStateAlign = 1024;
 constexpr int kMaxGroup = 128;          // query heads per key/value head: the rows of a tensor-core tile
 constexpr size_t kStatusBytes = 1024;   // the status word's block at the start of every state
+constexpr int32_t kMaxCtx = 1 << 30;    // cached tokens of a request: its keys, up to the end of a tile, fit 31 bits
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -94,6 +95,7 @@ idx_status check_problem(const idx_tree_problem *p, int32_t sel_k) {
   if (p->q_row_stride < static_cast<int64_t>(p->Hq) * p->cache.D || p->q_row_stride % 8 != 0) return IDX_EINVAL;
   if (p->R > IDX_MAX_ROWS || p->Q > IDX_MAX_REQS || p->max_new > IDX_MAX_TREE || p->Hq > 1024) return IDX_EUNSUPPORTED;
   if (sel_k < 0 || sel_k > IDX_MAX_K) return IDX_EINVAL;
+  if (p->max_ctx > kMaxCtx) return IDX_EUNSUPPORTED;
   if (p->Hq / p->cache.Hkv > kMaxGroup) return IDX_EUNSUPPORTED;
   if (!tiles_fit(p, sel_k)) return IDX_EUNSUPPORTED;
   if (p->q_row_stride >= int64_t{1} << 39) return IDX_EUNSUPPORTED;   // a tensor map's strides have 40 bits

@@ -168,7 +168,7 @@ __device__ __forceinline__ Req load_req(const TreeAttnArgs &a, int i) {
   if (ctx < 0 || ctx > p.max_ctx) q.bad = kStatusBadBound;
   ctx = max(0, min(ctx, p.max_ctx));
   q.ctx = ctx;
-  q.keys = ctx + q.tokens;       // both far below 2^30
+  q.keys = ctx + q.tokens;       // at most 2^30 + 64
   const int64_t room = static_cast<int64_t>(p.pt_stride) * kPage;
   if (q.keys > room) {
     q.bad = kStatusBadBound;

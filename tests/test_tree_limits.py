@@ -24,3 +24,14 @@ def test_rows_are_counted_in_31_bits(lib):
         t = _tables(lib, cap=cap)
         assert lib.lib.idx_tree_tables(ctypes.byref(t), FAKE, 1024, None) == lib.IDX_EUNSUPPORTED, cap
     assert (INT32_MAX - 3 - 1) // 4 * 4 + 4 <= INT32_MAX
+
+
+def test_positions_are_counted_in_31_bits(lib):
+    """A request's keys, and the keys of its last tile, are ctx_len + up to 64 tokens + 127."""
+    for max_ctx in ((1 << 30) + 1, INT32_MAX - 128, INT32_MAX):
+        p = _problem(lib, cache=_cache(lib, Hkv=1), Hq=8, pt_stride=1 << 25, max_ctx=max_ctx)
+        for sel_k in (0, 64):
+            assert _attend(lib, p, sel=FAKE, sel_k=sel_k) == lib.IDX_EUNSUPPORTED, max_ctx
+            assert lib.tree_state_size(p, sel_k) == 0
+    p = _problem(lib, cache=_cache(lib, Hkv=1), Hq=8, pt_stride=1 << 25, max_ctx=1 << 30)
+    assert lib.tree_state_size(p) > 0 and lib.tree_state_size(p, 64) > 0
