@@ -300,7 +300,8 @@ idx_status idx_topk_noalloc(const float *scores, int64_t ld, const int32_t *row_
  * The state buffer of these calls is device memory, 1024-byte aligned, all zero
  * before its first use.  Its first word is a status word that errors found on the
  * device are or-ed into; idx_last_device_status reads and clears it.  Calls that
- * overlap in time need a state each, and after IDX_ETIMEOUT a state is zeroed anew. */
+ * overlap in time need a state each, and after IDX_ETIMEOUT a state is zeroed anew.
+ * Arrays are aligned to their elements at least (IDX_EINVAL otherwise). */
 #define IDX_MAX_REQS 4096     /* requests of a step */
 #define IDX_MAX_TREE 64       /* drafted tokens of one request (bits of a mask) */
 

@@ -2,6 +2,7 @@
 #include <cuda.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include "idx.h"
 #include "idx_device.cuh"
@@ -15,6 +16,11 @@ constexpr size_t kStatusBytes = 1024;   // the status word's block at the start 
 constexpr int32_t kMaxCtx = 1 << 30;    // cached tokens of a request: its keys, up to the end of a tile, fit 31 bits
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool words(std::initializer_list<const void *> arrays) {   // 4-byte elements at 4-byte addresses (or null)
+  for (const void *p : arrays)
+    if (!aligned(p, 4)) return false;
+  return true;
+}
 
 idx_status cuda_ok(cudaError_t e) { return e == cudaSuccess ? IDX_OK : IDX_ECUDA; }
 
@@ -87,6 +93,7 @@ idx_status check_problem(const idx_tree_problem *p, int32_t sel_k) {
   if (p->q == nullptr || !aligned(p->q, 16) || p->page_table == nullptr || p->ctx_len == nullptr ||
       p->row_start == nullptr)
     return IDX_EINVAL;
+  if (!words({p->page_table, p->ctx_len, p->row_start}) || !aligned(p->mask, 8)) return IDX_EINVAL;
   const idx_status st = check_cache(&p->cache);
   if (st != IDX_OK) return st;
   if (p->R < 1 || p->Q < 1 || p->pt_stride < 1 || p->max_ctx < 0 || p->max_new < 1 || p->Hq < 1) return IDX_EINVAL;
@@ -153,7 +160,7 @@ idx_status attend(const idx_tree_problem *p, const int32_t *sel, int32_t sel_k, 
   idx_status st = check_problem(p, sel_k);
   if (st != IDX_OK) return st;
   const StateLayout L = state_layout(p, sel_k);
-  if (out == nullptr || !aligned(out, 16) || !state_ok(state, state_bytes, L.total)) return IDX_EINVAL;
+  if (out == nullptr || !aligned(out, 16) || !words({sel, lse}) || !state_ok(state, state_bytes, L.total)) return IDX_EINVAL;
   int sms = 0;
   st = idx::device_sms(&sms);
   if (st != IDX_OK) return st;
@@ -218,6 +225,9 @@ idx_status idx_tree_tables(const idx_tree_tables_args *t, void *state, size_t st
   if (t->cap > 0 && (t->row_req == nullptr || t->row_bound == nullptr || t->row_pos == nullptr || t->slot == nullptr))
     return IDX_EINVAL;
   if (t->free_left == t->free_count || !aligned(t->mask, 8)) return IDX_EINVAL;
+  if (!words({t->ctx_len, t->new_len, t->parent, t->free_pages, t->free_count, t->page_table, t->row_start, t->free_left,
+              t->row_req, t->row_bound, t->row_pos, t->slot}))
+    return IDX_EINVAL;
   if (t->Q > IDX_MAX_REQS || t->P > INT32_MAX / IDX_PAGE) return IDX_EUNSUPPORTED;
   if (t->cap > INT32_MAX - 3) return IDX_EUNSUPPORTED;   // a thread's four rows end within 31 bits
   if (!state_ok(state, state_bytes, kStatusBytes)) return IDX_EINVAL;
@@ -238,7 +248,7 @@ idx_status idx_write_kv(const idx_kv_cache *cache, const void *k_new, const void
   idx_status st = check_cache(cache);
   if (st != IDX_OK) return st;
   if (R == 0) return IDX_OK;
-  if (k_new == nullptr || v_new == nullptr || slot == nullptr || !aligned(k_new, 16) || !aligned(v_new, 16))
+  if (k_new == nullptr || v_new == nullptr || slot == nullptr || !aligned(k_new, 16) || !aligned(v_new, 16) || !words({slot}))
     return IDX_EINVAL;
   if (row_stride < static_cast<int64_t>(cache->Hkv) * cache->D || row_stride % 8 != 0) return IDX_EINVAL;
   if (R > INT32_MAX) return IDX_EUNSUPPORTED;   // the grid: a row is at most 128 CTAs of vectors

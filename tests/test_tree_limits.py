@@ -35,3 +35,25 @@ def test_positions_are_counted_in_31_bits(lib):
             assert lib.tree_state_size(p, sel_k) == 0
     p = _problem(lib, cache=_cache(lib, Hkv=1), Hq=8, pt_stride=1 << 25, max_ctx=1 << 30)
     assert lib.tree_state_size(p) > 0 and lib.tree_state_size(p, 64) > 0
+
+
+@pytest.mark.parametrize("name", ["ctx_len", "new_len", "free_pages", "free_count", "page_table", "row_start", "free_left",
+                                  "row_req", "row_bound", "row_pos", "slot", "parent"])
+def test_tables_want_aligned_arrays(lib, name):
+    t = _tables(lib, **{name: FAKE + 130})
+    assert lib.lib.idx_tree_tables(ctypes.byref(t), FAKE, 1024, None) == lib.IDX_EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(page_table=FAKE + 2), dict(ctx_len=FAKE + 1), dict(row_start=FAKE + 2), dict(mask=FAKE + 4)])
+def test_attention_wants_aligned_arrays(lib, kw):
+    p = _problem(lib, **kw)
+    assert _attend(lib, p) == lib.IDX_EINVAL
+    assert _attend(lib, p, sel=FAKE, sel_k=64) == lib.IDX_EINVAL
+    assert lib.tree_state_size(p) == 0
+
+
+def test_other_arrays_are_aligned_too(lib):
+    p = _problem(lib)
+    assert _attend(lib, p, sel=FAKE + 2, sel_k=64) == lib.IDX_EINVAL
+    assert lib.lib.idx_tree_attention(ctypes.byref(p), FAKE, FAKE + 2, FAKE, 1 << 40, None) == lib.IDX_EINVAL
+    assert _write(lib, _cache(lib), slot=FAKE + 2) == lib.IDX_EINVAL
