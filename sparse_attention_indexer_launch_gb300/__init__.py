@@ -56,6 +56,7 @@ class Problem(ctypes.Structure):
 
 class TreeTables(ctypes.Structure):
     """Mirror of idx_tree_tables_args."""
+    device = None   # the GPU of its tensors, where they are known
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "ctx_len", "new_len", "parent", "free_pages", "free_count", "page_table", "row_start", "free_left",
         "row_req", "row_bound", "row_pos", "slot", "mask")] + [
@@ -64,6 +65,7 @@ class TreeTables(ctypes.Structure):
 
 class KvCache(ctypes.Structure):
     """Mirror of idx_kv_cache."""
+    device = None   # the GPU of its tensors, where they are known
     _fields_ = [
         ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
         ("P", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
@@ -73,6 +75,7 @@ class KvCache(ctypes.Structure):
 
 class TreeProblem(ctypes.Structure):
     """Mirror of idx_tree_problem."""
+    device = None   # the GPU of its tensors, where they are known
     _fields_ = [
         ("q", ctypes.c_void_p), ("q_row_stride", ctypes.c_int64), ("cache", KvCache), ("page_table", ctypes.c_void_p),
         ("ctx_len", ctypes.c_void_p), ("row_start", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("R", ctypes.c_int32),
@@ -162,13 +165,27 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _current(stream):
+def _one_device(*tensors):
+    """The index of the GPU that all the tensors (None: not given) are on."""
+    got = {t.get_device() for t in tensors if t is not None}
+    if len(got) != 1 or min(got) < 0:
+        raise ValueError("tensors of one GPU are wanted")
+    return got.pop()
+
+
+def _current(stream, plan, *tensors):
     """The stream's handle as an integer; the current device's current stream for None.
+    The tensors (None: not given) and the plan's have to be on the current device.
     (Calls of a few microseconds: no Stream object is made.)"""
-    if stream is not None:
-        return stream.cuda_stream
-    torch = _modules["torch"]   # the caller's tensors come from it
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    cuda = _modules["torch"]._C   # the caller's tensors come from it
+    here = cuda._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError("tensors on the current device are wanted")
+    planned = plan.device
+    if planned != here and planned is not None:
+        raise ValueError("a plan of tensors on the current device is wanted")
+    return stream.cuda_stream if stream is not None else cuda._cuda_getCurrentRawStream(here)
 
 
 def make_problem(q, w, k_cache, k_scale, page_table, row_req, row_bound, max_bound: int,
@@ -294,11 +311,15 @@ def make_tree_tables(ctx_len, new_len, page_table, free_pages, free_count, *, P:
     _need(page_table.dim() == 2 and page_table.shape[0] == Q, "page_table: [Q][stride] is wanted")
     _need(mask is None or (mask.dtype == torch.int64 and mask.is_contiguous() and mask.numel() >= cap),
           "mask: a contiguous int64 tensor of a value per row is wanted")
-    return TreeTables(ctx_len=_ptr(ctx_len), new_len=_ptr(new_len), parent=_ptr(parent), free_pages=_ptr(free_pages),
-                      free_count=_ptr(free_count), page_table=_ptr(page_table), row_start=_ptr(row_start),
-                      free_left=_ptr(free_left), row_req=_ptr(row_req), row_bound=_ptr(row_bound),
-                      row_pos=_ptr(row_pos), slot=_ptr(slot), mask=_ptr(mask), P=int(P), Q=Q,
-                      pt_stride=int(page_table.shape[1]), cap=cap)
+    device = _one_device(ctx_len, new_len, parent, free_pages, free_count, page_table, row_start, free_left, row_req,
+                         row_bound, row_pos, slot, mask)
+    t = TreeTables(ctx_len=_ptr(ctx_len), new_len=_ptr(new_len), parent=_ptr(parent), free_pages=_ptr(free_pages),
+                   free_count=_ptr(free_count), page_table=_ptr(page_table), row_start=_ptr(row_start),
+                   free_left=_ptr(free_left), row_req=_ptr(row_req), row_bound=_ptr(row_bound),
+                   row_pos=_ptr(row_pos), slot=_ptr(slot), mask=_ptr(mask), P=int(P), Q=Q,
+                   pt_stride=int(page_table.shape[1]), cap=cap)
+    t.device = device
+    return t
 
 
 def tree_tables_state_size() -> int:
@@ -308,7 +329,7 @@ def tree_tables_state_size() -> int:
 def idx_tree_tables(tables: TreeTables, state, stream=None):
     """Page tables, slots and masks of a step (see idx.h); `state` from
     alloc_state(tree_tables_state_size())."""
-    _check(lib.idx_tree_tables(ctypes.byref(tables), state.data_ptr(), state.nbytes, _current(stream)),
+    _check(lib.idx_tree_tables(ctypes.byref(tables), state.data_ptr(), state.nbytes, _current(stream, tables, state)),
            "idx_tree_tables")
 
 
@@ -329,20 +350,22 @@ def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
         _need((s is not None) == f8, "k_scale, v_scale: wanted for an E4M3 cache only")
         _need(s is None or (s.dtype == torch.float32 and s.is_contiguous() and tuple(s.shape) == (P, Hkv, page)),
               "k_scale, v_scale: contiguous fp32 [P][Hkv][64] is wanted")
-    return KvCache(k=_ptr(k), v=_ptr(v), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale), P=P, page_stride=st[0][0],
-                   token_stride=st[0][1], head_stride=st[0][2], Hkv=Hkv, D=D,
-                   kv_dtype=IDX_KV_E4M3 if f8 else IDX_KV_BF16)
+    device = _one_device(k, v, k_scale, v_scale)
+    c = KvCache(k=_ptr(k), v=_ptr(v), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale), P=P, page_stride=st[0][0],
+                token_stride=st[0][1], head_stride=st[0][2], Hkv=Hkv, D=D,
+                kv_dtype=IDX_KV_E4M3 if f8 else IDX_KV_BF16)
+    c.device = device
+    return c
 
 
 def idx_write_kv(cache: KvCache, k_new, v_new, slot, stream=None):
     """Writes k_new and v_new (bf16 [R][Hkv][D], rows of equal stride) into the cache
     at slot [R] (see idx.h)."""
     torch = _modules["torch"]
-    R, Hkv, D = slot.numel(), cache.Hkv, cache.D
-    st, sv = k_new.stride(), v_new.stride()
-    for dtype, shape in ((k_new.dtype, k_new.shape), (v_new.dtype, v_new.shape)):
-        if dtype is not torch.bfloat16 or shape != (R, Hkv, D):
-            raise ValueError("k_new, v_new: bf16 [R][Hkv][D] is wanted")
+    wanted = R, Hkv, D = slot.numel(), cache.Hkv, cache.D
+    st, sv, bf16 = k_new.stride(), v_new.stride(), torch.bfloat16
+    if k_new.dtype is not bf16 or v_new.dtype is not bf16 or k_new.shape != wanted or v_new.shape != wanted:
+        raise ValueError("k_new, v_new: bf16 [R][Hkv][D] is wanted")
     # a dimension of one element is never stepped over: any stride will do
     if st[2] != 1 or sv[2] != 1 or (Hkv > 1 and (st[1] != D or sv[1] != D)):
         raise ValueError("k_new, v_new: bf16 [R][Hkv][D] with contiguous heads is wanted")
@@ -352,7 +375,7 @@ def idx_write_kv(cache: KvCache, k_new, v_new, slot, stream=None):
         raise ValueError("slot: a contiguous int32 tensor is wanted")
     stride = st[0] if R > 1 else Hkv * D
     _check(lib.idx_write_kv(ctypes.byref(cache), k_new.data_ptr(), v_new.data_ptr(), stride, slot.data_ptr(), R,
-                            _current(stream)), "idx_write_kv")
+                            _current(stream, cache, k_new, v_new, slot)), "idx_write_kv")
 
 
 def make_tree_problem(q, cache: KvCache, page_table, ctx_len, row_start, mask, max_ctx: int, max_new: int,
@@ -370,10 +393,14 @@ def make_tree_problem(q, cache: KvCache, page_table, ctx_len, row_start, mask, m
     _need(page_table.dim() == 2 and page_table.shape[0] == Q, "page_table: [Q][stride] is wanted")
     _need(mask is None or (mask.dtype == torch.int64 and mask.is_contiguous() and mask.numel() >= R),
           "mask: a contiguous int64 tensor of a value per row is wanted")
-    return TreeProblem(q=_ptr(q), q_row_stride=int(q.stride(0)) if R > 1 else Hq * D, cache=cache,
-                       page_table=_ptr(page_table), ctx_len=_ptr(ctx_len), row_start=_ptr(row_start), mask=_ptr(mask),
-                       R=R, Q=Q, pt_stride=int(page_table.shape[1]), max_ctx=int(max_ctx), max_new=int(max_new), Hq=Hq,
-                       scale=float(scale))
+    device = _one_device(q, page_table, ctx_len, row_start, mask)
+    _need(cache.device is None or cache.device == device, "a cache on the GPU of the other tensors is wanted")
+    p = TreeProblem(q=_ptr(q), q_row_stride=int(q.stride(0)) if R > 1 else Hq * D, cache=cache,
+                    page_table=_ptr(page_table), ctx_len=_ptr(ctx_len), row_start=_ptr(row_start), mask=_ptr(mask),
+                    R=R, Q=Q, pt_stride=int(page_table.shape[1]), max_ctx=int(max_ctx), max_new=int(max_new), Hq=Hq,
+                    scale=float(scale))
+    p.device = device
+    return p
 
 
 def tree_state_size(problem: TreeProblem, sel_k: int = 0) -> int:
@@ -395,7 +422,8 @@ def idx_tree_attention(problem: TreeProblem, out, state, lse=None, stream=None):
     alloc_state(tree_state_size(problem))."""
     _attn_outputs(problem, out, lse)
     _check(lib.idx_tree_attention(ctypes.byref(problem), out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                  state.data_ptr(), state.nbytes, _current(stream)), "idx_tree_attention")
+                                  state.data_ptr(), state.nbytes, _current(stream, problem, out, state, lse)),
+           "idx_tree_attention")
 
 
 def idx_tree_attention_selected(problem: TreeProblem, sel, out, state, lse=None, stream=None):
@@ -407,7 +435,8 @@ def idx_tree_attention_selected(problem: TreeProblem, sel, out, state, lse=None,
         raise ValueError("sel: a contiguous int32 [R][K] tensor is wanted")
     _check(lib.idx_tree_attention_selected(ctypes.byref(problem), sel.data_ptr(), sel.shape[1], out.data_ptr(),
                                            None if lse is None else lse.data_ptr(), state.data_ptr(), state.nbytes,
-                                           _current(stream)), "idx_tree_attention_selected")
+                                           _current(stream, problem, sel, out, state, lse)),
+           "idx_tree_attention_selected")
 
 
 def last_device_status(ws, stream=None) -> int:
