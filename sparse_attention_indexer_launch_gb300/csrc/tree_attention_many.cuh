@@ -178,6 +178,13 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const flo
       }
   }
   if (special) {
+    if (c == 0.0f) {   // scores of 0 (or NaN): multiplied here, so that what is masked below stays -infinity
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int y = 0; y < kW; ++y) x[w][y] = __float_as_uint(__uint_as_float(x[w][y]) * c);
+      c = 1.0f;
+    }
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
@@ -192,8 +199,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const flo
 #pragma unroll
       for (int z = 0; z < 4; ++z)
         t4[z] = max3(t4[z], __uint_as_float(x[w][y + 2 * z]), __uint_as_float(x[w][y + 2 * z + 1]));
-  float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c;   // in units of log2
-  if (top != top) top = 0.0f;   // scale 0: 0 x -inf moves no maximum
+  const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c;   // in units of log2
   if (!raise_maximum<D>(to, top, has_o, m, l, settled)) return false;
   const float base = m == -INFINITY ? 0.0f : m;
   const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import tree_util as tu
-from tests.test_gpu_tree_attention import _trees
+from tests.test_gpu_tree_attention import _select, _trees
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,19 @@ def test_many_items_whose_first_key_some_rows_do_not_see(lib, kv, heads, new):
     out, lse = s.attend()
     assert s.status() == lib.IDX_OK
     tu.check(s, out, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,new", [(16, [3, 2, 4]), (128, [1, 1, 1]), (64, [64, 20, 5])])
+def test_a_scale_of_zero_takes_the_mean(lib, kv, D, Hq, new):
+    """Scores of 0 for every visible key, whatever the masked ones hold (stale slots are NaN)."""
+    s = tu.Step([100, 300, 0], new, Hq, 1, D, kv, masks=_trees(55, new), seed=56)
+    s.scale = 0.0
+    out, lse = s.attend()
+    assert s.status() == lib.IDX_OK
+    tu.check(s, out, lse)
+    sel = _select(s, 150, 57)
+    out, lse = s.attend(sel)
+    assert s.status() == lib.IDX_OK
+    tu.check(s, out, lse, sel)
