@@ -319,7 +319,8 @@ typedef struct {
     const int32_t *free_pages; /* device int32 [free_count]: page ids in [0, P) */
     const int32_t *free_count; /* device int32 [1] */
     int32_t *page_table;       /* device int32 [Q][pt_stride]: held pages are read, new entries written */
-    int32_t *row_start;        /* out, device int32 [Q + 1]: exclusive prefix sums of new_len, at most cap */
+    int32_t *row_start;        /* out, device int32 [Q + 1]: exclusive prefix sums of new_len, at most cap
+                                  (INT32_MAX where cap is 0) */
     int32_t *free_left;        /* out, device int32 [1]: pages left on the free stack (not free_count itself) */
     int32_t *row_req;          /* out, device int32 [cap]: the row's request */
     int32_t *row_bound;        /* out, device int32 [cap]: its storage position + 1 (idx_patch_new_keys's bound) */
@@ -341,10 +342,11 @@ size_t idx_tree_tables_state_size(void);
  * position 0, slot -1, mask 0.  Found on the device and recorded as IDX_EDEVICE:
  * fewer free pages than needed or a table row too short (the rows without a page
  * get slot -1, their table entries -1), more new tokens than cap (the rest have no
- * row), a page id outside [0, P) (slot -1), a parent that is not an earlier token
- * (read as a root), a request of more than IDX_MAX_TREE new tokens with parents or
- * masks asked for (those past the 64th: mask 0, depth counted as in a chain).  IDX_EINVAL for a NULL or bad
- * argument, IDX_EUNSUPPORTED for Q, P or cap above the limits; launches nothing then. */
+ * row; for cap 0: more than INT32_MAX), a page id outside [0, P) (slot -1), a parent
+ * that is not an earlier token (read as a root), a request of more than IDX_MAX_TREE
+ * new tokens with parents or masks asked for (those past the 64th: mask 0, depth
+ * counted as in a chain).  IDX_EINVAL for a NULL or bad argument, IDX_EUNSUPPORTED for
+ * Q, P or cap above the limits; launches nothing then. */
 idx_status idx_tree_tables(const idx_tree_tables_args *args, void *state, size_t state_bytes, void *stream);
 
 /* A paged key/value cache.  Element (page p, token s, head h, dim d) of K and of V

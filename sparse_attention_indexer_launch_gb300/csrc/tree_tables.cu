@@ -53,7 +53,8 @@ __global__ void __launch_bounds__(kThreads) tree_tables_kernel(const TreeTablesA
   uint32_t bad = 0;
 
   // Prefix sums in 64 bits (lengths are the caller's data), stored clamped: rows to
-  // cap, pages to INT32_MAX, which no free stack reaches.
+  // cap (without rows, cap 0, to INT32_MAX), pages to INT32_MAX, which no free stack reaches.
+  const int64_t most_rows = a.t.cap > 0 ? a.t.cap : INT32_MAX;
   int64_t base_rows = 0, base_pages = 0;
   for (int i0 = 0; i0 < Q; i0 += kThreads) {
     const int i = i0 + tid;
@@ -89,15 +90,15 @@ __global__ void __launch_bounds__(kThreads) tree_tables_kernel(const TreeTablesA
       base_pages += warp_pages[w];
     }
     if (i < Q) {
-      start[i] = static_cast<int32_t>(min(before_r + sr - rows, static_cast<int64_t>(a.t.cap)));
+      start[i] = static_cast<int32_t>(min(before_r + sr - rows, most_rows));
       taken[i] = static_cast<int32_t>(min(before_p + sp - pages, static_cast<int64_t>(INT32_MAX)));
     }
     __syncthreads();   // the warp sums are rewritten by the next chunk
   }
   if (tid == 0) {
-    start[Q] = static_cast<int32_t>(min(base_rows, static_cast<int64_t>(a.t.cap)));
+    start[Q] = static_cast<int32_t>(min(base_rows, most_rows));
     taken[Q] = static_cast<int32_t>(min(base_pages, static_cast<int64_t>(INT32_MAX)));
-    if (base_rows > a.t.cap) bad |= kStatusBadBound;
+    if (base_rows > most_rows) bad |= kStatusBadBound;
   }
   __syncthreads();
   const int32_t rows = start[Q], pages = taken[Q];
