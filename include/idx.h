@@ -407,8 +407,9 @@ size_t idx_tree_state_size(const idx_tree_problem *problem, int32_t sel_k);
  *     V(r)  = { j < ctx_len[i] } + { ctx_len[i] + u : u < rows of i, bit u of mask[r] }
  *     s_j   = scale * <q[r][h], k_j>
  *     out   = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)   over j in V(r);
- * a row that sees nothing gets zeros and lse -inf.  Masked positions contribute
- * nothing, whatever the cache holds there (NaN and infinities included).
+ * a row that sees nothing, or only scores of -inf, gets zeros and lse -inf.  Masked
+ * positions contribute nothing, whatever the cache holds there (NaN and infinities
+ * included).
  *   out  device bf16 [R][Hq][D], 16-byte aligned.
  *   lse  device fp32 [R][Hq] or NULL.
  * Rows outside every request are not written.  Sums and softmax statistics are fp32;

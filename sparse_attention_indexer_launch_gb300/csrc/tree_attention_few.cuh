@@ -52,6 +52,9 @@ namespace {
 // positions, the team that gathers.
 constexpr int kFewKWarp = 8, kFewIssuerWarp = 9, kFewVWarp = 11, kFewConvertWarp = 12;
 constexpr int kFewTile = 128;
+// Added to the scores of a row without a reference: what any finite score becomes passes kLazy
+// and asks for one, and a score of -infinity stays that (added to +infinity it would be NaN).
+constexpr float kNoRef = 0x1p127f;
 
 template <int D, bool F8, int N, bool SEL>
 struct FewCfg {
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
       const float *const qs = bars.q_scale[walk.seg & 3];
       if (key < N) {
         bars.ref[s][key] = -INFINITY;
-        neg[key] = INFINITY;
+        neg[key] = kNoRef;
       }
       team_sync(s);
       float l[N];
@@ -387,9 +390,9 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
 #pragma unroll
               for (int r = 0; r < N; ++r) {
                 const float m = __uint_as_float(x[r]) * ck * (F8 ? qs[r] : 1.0f);
-                const bool fine = m - m == 0.0f;    // else the row's maximum is taken below (+INFINITY asks for it)
+                const bool fine = m - m == 0.0f;    // else the row's maximum is taken below (kNoRef asks for it)
                 bars.ref[s][r] = fine ? m : -INFINITY;
-                neg[r] = fine ? -m : INFINITY;
+                neg[r] = fine ? -m : kNoRef;
               }
             }
             team_sync(s);
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
             const float old = bars.ref[s][key];
             const float now = m > old + kLazy || old == -INFINITY ? fmaxf(m, old) : old;
             bars.ref[s][key] = now;
-            neg[key] = now == -INFINITY ? INFINITY : -now;
+            neg[key] = now == -INFINITY ? kNoRef : -now;
             bars.keep[s][key] = old == -INFINITY ? 0.0f : ex2(old - now);
           }
           team_sync(s);

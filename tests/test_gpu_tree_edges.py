@@ -74,3 +74,27 @@ def test_a_scale_of_zero_takes_the_mean(lib, kv, D, Hq, new):
     out, lse = s.attend(sel)
     assert s.status() == lib.IDX_OK
     tu.check(s, out, lse, sel)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads,new", [((8, 1), 3), ((32, 1), 1), ((16, 2), 2), ((64, 1), 1), ((128, 1), 2)])
+def test_scores_of_minus_infinity_add_nothing(lib, D, heads, new):
+    """Whole tiles of visible keys with scores of -infinity, in front of others: exp(-inf) = 0."""
+    s = tu.Step([400], [new], *heads, D, seed=60)
+    s.q[:, :, 0].abs_().clamp_(min=0.5)
+    j = np.arange(256)
+    page, off = torch.from_numpy(s.table[0, j // 64].astype(np.int64)).cuda(), torch.from_numpy(j % 64).cuda()
+    s.k[page, off, :, 0] = float("-inf")
+    rest = torch.arange(256, 400, dtype=torch.int32, device="cuda").expand(new, 144).contiguous()
+    ro, rl, to, tl = s.reference(rest)       # the same keys but those
+    every = torch.arange(400, dtype=torch.int32, device="cuda").expand(new, 400).contiguous()
+    for sel in (None, every):
+        out, lse = s.attend(sel)
+        assert s.status() == lib.IDX_OK
+        assert bool(((out.double() - ro).abs() <= to).all())
+        assert bool(((lse.double() - rl).abs() <= tl).all())
+    # rows whose every score is -infinity have nothing to weigh
+    s.k[:, :, :, 0] = float("-inf")
+    for sel in (None, every):
+        out, lse = s.attend(sel)
+        assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
