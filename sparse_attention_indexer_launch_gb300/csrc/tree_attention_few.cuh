@@ -382,11 +382,11 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int r = 0; r < N; ++r) asm volatile("" : "+r"(x[r]));
-          // the first tile, where every row sees its first key: the references are that key's
-          // scores.  The four warps decide it together: one whose wait ran out may have read
-          // `open` from a tile that never came, and none may meet the barrier below alone.
-          if (pass == 0 && h == h0 && !team_any(s, !ok || !open)) {
-            if (key == 0) {
+          if (pass == 0 && h == h0) {
+            // the first tile: the references are its first key's scores, where every row sees it.
+            // All four warps meet here whether or not: one whose wait ran out may have read `open`
+            // from a tile that never came, and none may be left at a barrier alone.
+            if (open && key == 0) {
 #pragma unroll
               for (int r = 0; r < N; ++r) {
                 const float m = __uint_as_float(x[r]) * ck * (F8 ? qs[r] : 1.0f);
