@@ -370,7 +370,10 @@ typedef struct {
  *                 slot outside [0, P * 64) writes nothing.  Slots >= 0 must differ.
  * bf16 cache: the values as given.  E4M3 cache: per token and head scale = amax / 448
  * in fp32 (1 for an all-zero vector), each value divided by it in fp32 and rounded to
- * the nearest E4M3 code (ties to even), saturating at +-448.  R = 0 does nothing.
+ * the nearest E4M3 code (ties to even), saturating at +-448.  A NaN is left out of
+ * amax and becomes a NaN code (a vector of NaN only: scale 1); an infinity makes the
+ * scale infinite, itself a NaN code and the vector's other codes zeros.  R = 0 does
+ * nothing.
  * Asynchronous on `stream`; allocates nothing. */
 idx_status idx_write_kv(const idx_kv_cache *cache, const void *k_new, const void *v_new, int64_t row_stride,
                         const int32_t *slot, int64_t R, void *stream);

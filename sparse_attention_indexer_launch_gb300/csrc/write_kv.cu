@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) write_kv_kernel(const Wr
         if (live) *reinterpret_cast<uint4 *>(to) = x[u];
       } else {
         const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        // exact in bf16: a maximum rounds nothing (NaN is passed over)
+        // exact in bf16: a maximum rounds nothing (NaN is passed over, as the indexer's new keys do)
         __nv_bfloat162 m = __habs2(reinterpret_cast<const __nv_bfloat162 &>(w[0]));
 #pragma unroll
         for (int i = 1; i < 4; ++i) m = __hmax2(m, __habs2(reinterpret_cast<const __nv_bfloat162 &>(w[i])));
