@@ -1,4 +1,5 @@
-"""Attention where its paths meet their edges: references that rise over a whole cache."""
+"""Attention where its paths meet their edges: references that rise over a whole cache, scales and
+scores at their limits, more requests than a warp or a CTA sums at once."""
 import numpy as np
 import pytest
 import torch
@@ -98,3 +99,27 @@ def test_scores_of_minus_infinity_add_nothing(lib, D, heads, new):
     for sel in (None, every):
         out, lse = s.attend(sel)
         assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("Q", [33, 64, 384, 400, 641, 1000, 4096])
+@pytest.mark.parametrize("kv,heads", [("bf16", (8, 1)), ("e4m3", (16, 2)), ("bf16", (128, 1)), ("e4m3", (96, 1))])
+def test_many_requests(lib, kv, heads, Q):
+    """More requests than a warp sums (32), than a CTA does in one go (384 to 640), and the most
+    there may be; empty ones among them."""
+    rng = np.random.default_rng(Q)
+    ctx = rng.integers(0, 150, Q)
+    new = rng.integers(0, 3, Q)
+    for i in (31, 32, 383, 384, 639, 640, Q - 1):      # where a scan's chunks end
+        if i < Q:
+            ctx[i], new[i] = 130 + i % 7, 1 + i % 2
+    if Q > 1000:
+        new[rng.random(Q) < 0.7] = 0
+    ctx, new = ctx.tolist(), new.tolist()
+    s = tu.Step(ctx, new, *heads, 64, kv, masks=_trees(61, new), seed=62)
+    out, lse = s.attend()
+    assert s.status() == lib.IDX_OK
+    tu.check(s, out, lse)
+    sel = _select(s, 70, 63)
+    out, lse = s.attend(sel)
+    assert s.status() == lib.IDX_OK
+    tu.check(s, out, lse, sel)
