@@ -404,20 +404,13 @@ __device__ __forceinline__ void join_units(const TreeAttnArgs &a, const Share &s
           const float nm = fmaxf(m[z], ml[z][y].x);
           const float f = ml[z][y].x == -INFINITY ? 0.0f : ex2(ml[z][y].x - nm), keep = m[z] == -INFINITY ? 0.0f : ex2(m[z] - nm);
           m[z] = nm;
-          if (keep != 1.0f) {
-            l[z] = keep == 0.0f ? 0.0f : l[z] * keep;
-            acc[z].x = keep == 0.0f ? 0.0f : acc[z].x * keep;
-            acc[z].y = keep == 0.0f ? 0.0f : acc[z].y * keep;
-            acc[z].z = keep == 0.0f ? 0.0f : acc[z].z * keep;
-            acc[z].w = keep == 0.0f ? 0.0f : acc[z].w * keep;
-          }
-          if (f != 0.0f) {
-            l[z] += f * ml[z][y].y;
-            acc[z].x += f * o[z][y].x;
-            acc[z].y += f * o[z][y].y;
-            acc[z].z += f * o[z][y].z;
-            acc[z].w += f * o[z][y].w;
-          }
+          // a share that a row sees nothing of is 0; one whose weight vanishes is not left out: its
+          // O may be NaN
+          l[z] = l[z] * keep + f * ml[z][y].y;
+          acc[z].x = acc[z].x * keep + f * o[z][y].x;
+          acc[z].y = acc[z].y * keep + f * o[z][y].y;
+          acc[z].z = acc[z].z * keep + f * o[z][y].z;
+          acc[z].w = acc[z].w * keep + f * o[z][y].w;
         }
     }
 #pragma unroll
@@ -427,7 +420,7 @@ __device__ __forceinline__ void join_units(const TreeAttnArgs &a, const Share &s
       const float f = m[z] == -INFINITY ? 0.0f : ex2(m[z] - top);
       float v[5] = {l[z], acc[z].x, acc[z].y, acc[z].z, acc[z].w};
 #pragma unroll
-      for (int y = 0; y < 5; ++y) v[y] = f == 0.0f ? 0.0f : v[y] * f;
+      for (int y = 0; y < 5; ++y) v[y] *= f;
       for (int o = lanes / 2; o > 0; o >>= 1)
 #pragma unroll
         for (int y = 0; y < 5; ++y) v[y] += __shfl_xor_sync(0xffffffffu, v[y], o);

@@ -477,10 +477,7 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
 #pragma unroll
                 for (int r = 0; r < 8; ++r) asm volatile("" : "+r"(o[r]));
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                  const float f = bars.keep[s][g + r];
-                  o[r] = f == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[r]) * f);
-                }
+                for (int r = 0; r < 8; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * bars.keep[s][g + r]);
                 tmem_st8(to + g, o);
               }
               tmem_wait_st();
@@ -668,8 +665,8 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
           const int row = g + r;
           if (row >= nrow || !ok) continue;
           const float f0 = bars.join[s][0][row], f1 = bars.join[s][1][row];
-          float o = f0 == 0.0f || !has0 ? 0.0f : __uint_as_float(x0[r]) * f0;
-          if (has1) o += f1 == 0.0f ? 0.0f : __uint_as_float(x1[r]) * f1;
+          float o = has0 ? __uint_as_float(x0[r]) * f0 : 0.0f;
+          if (has1) o += __uint_as_float(x1[r]) * f1;
           if (bars.join[s][2][row] == 0.0f) o = 0.0f;
           if (!poison) {
             put(row, o);

@@ -555,8 +555,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, PAIR, SEL>::kThreads, 1)
           reg_fence16(x1);
 #pragma unroll
           for (int y = 0; y < 16; ++y) {
-            o[y] = PAIR ? __uint_as_float(x[y]) : f0 == 0.0f || !has0 ? 0.0f : __uint_as_float(x[y]) * f0;
-            if (has1) o[y] += f1 == 0.0f ? 0.0f : __uint_as_float(x1[y]) * f1;
+            o[y] = PAIR ? __uint_as_float(x[y]) : has0 ? __uint_as_float(x[y]) * f0 : 0.0f;
+            if (has1) o[y] += __uint_as_float(x1[y]) * f1;
           }
         }
         if (row < nrow)

@@ -123,3 +123,28 @@ def test_many_requests(lib, kv, heads, Q):
     out, lse = s.attend(sel)
     assert s.status() == lib.IDX_OK
     tu.check(s, out, lse, sel)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Q,ctx,heads,new", [(1, 3000, (8, 1), 2), (16, 600, (16, 16), 2), (1, 3000, (128, 1), 1), (16, 600, (512, 8), 1),
+                                             (1, 3000, (64, 1), 4), (8, 600, (512, 8), 5)])
+def test_a_cached_nan_reaches_rows_that_hardly_weigh_it(lib, kv, D, Q, ctx, heads, new):
+    """A visible V that is NaN, under a probability that vanishes beside a later key's: the
+    weight is not zero, so the output is NaN, in whichever share, stream or order they meet."""
+    s = tu.Step([ctx] * Q, [new] * Q, *heads, D, kv, seed=64)
+    u = torch.randint(0, 2, (D,), device="cuda").double() * 2 - 1
+    s.q[:] = u.bfloat16()
+    for i in range(Q):
+        page, off = int(s.table[i, 0]), 5
+        s.v[page, off, :, 7] = 0x7F if kv == "e4m3" else float("nan")
+        page, off = int(s.table[i, 300 // 64]), 300 % 64
+        if kv == "e4m3":      # scores of 20 sqrt(D) there, against some 2 elsewhere
+            s.k[page, off] = u.to(torch.float8_e4m3fn).view(torch.uint8)
+            s.k_scale[page, :, off] = 20.0
+        else:
+            s.k[page, off] = (20.0 * u).bfloat16()
+    out, lse = s.attend()
+    assert s.status() == lib.IDX_OK
+    tu.check(s, out, lse)
+    assert bool(torch.isnan(out[:, :, 7].float()).all())
