@@ -417,7 +417,8 @@ size_t idx_tree_state_size(const idx_tree_problem *problem, int32_t sel_k);
  *   lse  device fp32 [R][Hq] or NULL.
  * Rows outside every request are not written.  Sums and softmax statistics are fp32;
  * the probabilities are rounded to bf16 for the product with V (to two bf16 terms in
- * tiles of 64 or 128 positions that are not visible as a whole to every row); beside an
+ * tiles of 64 or 128 positions that are not visible as a whole to every row), which
+ * leaves an error nearly as large as the rounding of out to bf16; beside an
  * E4M3 cache q is used as the sum of two E4M3 terms, exact for elements down to 2^-9 of
  * its row's largest and to 2^-17 of that below.  Equal calls give equal bits.
  * The launch is cooperative: its CTAs, at most one per SM, run at the same time.

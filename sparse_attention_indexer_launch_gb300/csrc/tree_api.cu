@@ -52,10 +52,21 @@ idx_status check_cache(const idx_kv_cache *c) {
 }
 
 // The launch's shape.  Up to 64 rows of a request and key/value head (selected: of a token)
-// go to the few-row kernel, over a bf16 cache up to 32 (64 rows of 4 tokens at 131,072 keys:
-// 110 us there, 102 us in the many-row kernel; E4M3 130 against 174); up to 128 rows to the
-// many-row kernel in one block, more in pairs of blocks that share every K and V tile (4
-// requests of 64 x 64 rows: 186 us, one block at a time 204).
+// go to the few-row kernel, over a bf16 cache up to 32; up to 128 rows to the many-row kernel in
+// one block, more in pairs of blocks that share every K and V tile (4 requests of 64 x 64 rows:
+// 184 us, one block at a time 206; E4M3, 2 x 64 x 64 rows on 2 heads: 223, 294).  Few-row
+// against many-row kernel, us, 4 tokens, 8 key/value heads:
+//                          1 request, 131,072 keys   32 requests, 1,024 to 16,384 keys
+//   bf16 D =  64, 32 rows         62    76                   99   116
+//   bf16 D = 128, 32 rows         96    99                  156   154
+//   bf16 D =  64, 64 rows         71    80                  143   121
+//   bf16 D = 128, 64 rows        107   100                  205   164
+//   E4M3 D =  64, 32 rows         73   136                  127   238
+//   E4M3 D = 128, 32 rows         85   154                  167   282
+//   E4M3 D =  64, 64 rows        111   138                  220   259
+//   E4M3 D = 128, 64 rows        130   160                  274   317
+// One long request of 64 rows at D = 64 would be served faster by the few-row kernel, batches
+// lose more there.
 struct Shape {
   int rows;           // the few-row kernel's N, or 0
   int tile;           // keys

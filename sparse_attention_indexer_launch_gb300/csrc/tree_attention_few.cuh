@@ -34,11 +34,12 @@
 //
 // What bounds it.  bf16: memory (4 tokens of 64 heads over 131,072 keys of 8 heads 98 us, 5.5
 // TB/s).  E4M3: the chain of a tile's steps in the softmax warps, with the conversion of V
-// taking issue slots beside it (the same 84.5 us, 3.3 TB/s; 64 requests of D = 64 287 us, 2.4
+// taking issue slots beside it (the same 84 us, 3.3 TB/s; 64 requests of D = 64 285 us, 2.4
 // TB/s): two tiles per step, the tiles' waits hidden behind the TMEM reads and sleeping
 // waits were all no faster.  Selected: the copies, at 16 bytes a thread (150 rows over 2,048
-// positions of 2 E4M3 heads 102 us).  Small calls: the chain launch, lookups, one tile, join
-// (one token over 4,096 keys 16.4 us; 8 rows over 2,048 selected positions 23 us).
+// positions of 2 E4M3 heads 103 us); a tile without a single valid entry takes every step all
+// the same.  Small calls: the chain launch, lookups, one tile, join (one token over 4,096 keys
+// 16.4 us; 8 rows over 2,048 selected positions 22.7 us).
 #pragma once
 
 #include "tree_attention_common.cuh"
@@ -536,9 +537,11 @@ __global__ void __launch_bounds__(FewCfg<D, F8, N, SEL>::kThreads, 1)
           }
           __syncwarp();
         }
-        // P.  It is rounded to bf16 for the product with V.  Over the 128 or more keys of
-        // a full tile the roundings average out below the output's own; the few keys of a
-        // special tile do not, so there a second hand-over brings what the rounding left.
+        // P.  It is rounded to bf16 for the product with V.  That leaves an error nearly as
+        // large as the output's own rounding (relative to the output 0.9e-3 over 128 keys to
+        // 1.5e-3 over 65,536, beside 1.7e-3), for half the products that two terms would take.
+        // The few visible keys of a special tile average out less (up to 2^-8 of one value):
+        // there a second hand-over brings what the rounding left.
 #pragma unroll
         for (int r = 0; r < N; r += 2) {
           const float2 y = make_float2(ex2(e[r]), ex2(e[r + 1]));

@@ -31,9 +31,10 @@
 // warps, one thread per row, work on the tile before; P takes its S's place.
 //
 // What bounds it.  One row block: memory (8 requests' 16-node trees, 128 rows, over up to
-// 256K bf16 keys 370 us, 6.2 TB/s).  Two: the softmax, at about 1,300 cycles for a tile of 64
+// 256K bf16 keys 373 us, 6.2 TB/s).  Two: the softmax, at about 1,300 cycles for a tile of 64
 // keys whose products take the tensor core as long, and the ends of items split over CTAs
-// (4 requests' 64-node trees, 4,096 rows per request, 187 us, 1.0 PFLOP/s).
+// (4 requests' 64-node trees, 4,096 rows per request, 184.5 us, 1.0 PFLOP/s; 2 requests of
+// 64 x 64 rows over 30,000 E4M3 keys of 2 heads 223 us).
 #pragma once
 
 #include "tree_attention_common.cuh"
@@ -148,10 +149,11 @@ __device__ __forceinline__ bool raise_maximum(uint32_t to, float top, bool has_o
 // m and sum l, and O (D columns at to) when the maximum moves.  special: only the keys of ok
 // (a bit per key) are visible.  sk: the tile's K scales; sv: its V scales.
 //
-// P is rounded to bf16 for the product with V.  Over the 64 or more keys of a full tile
-// the roundings average out below the output's own; the few keys of a special tile do
-// not, so there P is kept in two bf16 terms, high in columns 0-31 and low in 32-63, and
-// the product runs over both.
+// P is rounded to bf16 for the product with V.  That leaves an error nearly as large as the
+// output's own rounding (relative to the output 0.9e-3 over 128 keys to 1.5e-3 over 65,536,
+// beside 1.7e-3), for half the products that two terms would take.  The few visible keys of a
+// special tile average out less (up to 2^-8 of one value): there P is kept in two bf16 terms,
+// high in columns 0-31 and low in 32-63, and the product runs over both.
 template <int D, bool F8, typename F>
 __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, const float *sk, const float *sv, float c, bool special,
                                              uint64_t ok, bool has_o, float &m, float &l, F settled) {

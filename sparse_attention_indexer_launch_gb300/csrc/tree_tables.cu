@@ -12,7 +12,7 @@
 //
 // Long runs of rows are bound by instructions: four consecutive rows per thread take one
 // lookup of the request (none while the last one's goes on) and one or two of a page.
-// Measured: 4.0 million rows of 64 prompts 16.7 us, 3.9 TB/s of stores; 64 trees of up to 64
+// Measured: 4.0 million rows of 64 prompts 16.6 us, 3.9 TB/s of stores; 64 trees of up to 64
 // tokens 8.2 us (the prefix sums and the walks up the trees); 2 x 4 rows 4.1 us, which is
 // what the host needs for a call.
 #include "idx_device.cuh"

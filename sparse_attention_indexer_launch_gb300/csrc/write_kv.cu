@@ -8,7 +8,7 @@
 // token; kVectors loads are in flight before the first is needed.  In E4M3 the call
 // is bound by instructions as much as by memory: what a vector costs beyond its loads
 // is kept small (amax in packed bf16, quotients by a two-term reciprocal).  Measured: 61,084
-// tokens x 8 heads of 128 dimensions into E4M3 73.5 us, 5.2 TB/s; into bf16 82.5 us, 6.1
+// tokens x 8 heads of 128 dimensions into E4M3 73.6 us, 5.2 TB/s; into bf16 82.5 us, 6.1
 // TB/s; 32 tokens 5.4 us, what the host needs for a call.
 #include <algorithm>
 
