@@ -424,7 +424,8 @@ size_t idx_tree_state_size(const idx_tree_problem *problem, int32_t sel_k);
  * The launch is cooperative: its CTAs, at most one per SM, run at the same time.
  * Device-detected (IDX_EDEVICE): a page id outside [0, P) (its tokens are left out),
  * ctx_len outside 0 .. max_ctx, more rows than max_new or positions past the page
- * table (clamped), row_start outside 0 .. R.  IDX_ETIMEOUT: a wait ran out.
+ * table (clamped), row_start outside 0 .. R or descending, so many keys over requests that
+ * share rows that tiles pass 31 bits (nothing is written).  IDX_ETIMEOUT: a wait ran out.
  * Asynchronous on `stream`; allocates nothing. */
 idx_status idx_tree_attention(const idx_tree_problem *problem, void *out, float *lse, void *state,
                               size_t state_bytes, void *stream);

@@ -54,7 +54,7 @@ idx_status check_cache(const idx_kv_cache *c) {
 // The launch's shape.  Up to 64 rows of a request and key/value head (selected: of a token)
 // go to the few-row kernel, over a bf16 cache up to 32; up to 128 rows to the many-row kernel in
 // one block, more in pairs of blocks that share every K and V tile (4 requests of 64 x 64 rows:
-// 184 us, one block at a time 206; E4M3, 2 x 64 x 64 rows on 2 heads: 223, 294).  Few-row
+// 184 us, one block at a time 206; E4M3, 2 x 64 x 64 rows on 2 heads: 225, 294).  Few-row
 // against many-row kernel, us, 4 tokens, 8 key/value heads:
 //                          1 request, 131,072 keys   32 requests, 1,024 to 16,384 keys
 //   bf16 D =  64, 32 rows         62    76                   99   116
@@ -89,14 +89,14 @@ Shape shape_of(const idx_tree_problem *p, int32_t sel_k) {
   return s;
 }
 
-// Tiles of the launch, at most: the kernels count them in 31 bits.
+// Tiles of the launch, at most: the kernels count them in 31 bits, and take INT32_MAX for more.
 bool tiles_fit(const idx_tree_problem *p, int32_t sel_k) {
   const Shape s = shape_of(p, sel_k);
   const int64_t item = s.pair ? 2 * s.block_tokens : s.block_tokens;
   const int64_t tiles = ((sel_k > 0 ? sel_k : p->max_ctx) + static_cast<int64_t>(p->max_new) + s.tile - 1) / s.tile;
   const int64_t blocks = (p->max_new + item - 1) / item;
   const int64_t items = (static_cast<int64_t>(p->Q) * blocks < p->R ? static_cast<int64_t>(p->Q) * blocks : p->R) * p->cache.Hkv;
-  return items * tiles <= INT32_MAX;
+  return items * tiles < INT32_MAX;
 }
 
 idx_status check_problem(const idx_tree_problem *p, int32_t sel_k) {

@@ -179,8 +179,12 @@ __device__ __forceinline__ Req load_req(const TreeAttnArgs &a, int i) {
   q.blocks = (q.tokens + a.item_tokens - 1) / a.item_tokens;
   return q;
 }
-// Tiles of a request: with the host's bounds the launch's sum fits 31 bits.
+// Tiles of a request.  With the host's bounds the launch's sum is below INT32_MAX, unless
+// requests share rows (row_start does not ascend): sums stop there, and such a launch does nothing.
 __device__ __forceinline__ int req_tiles(const Req &q, int hkv) { return q.tiles * q.blocks * hkv; }
+__device__ __forceinline__ int add_tiles(int a, int b) {
+  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), static_cast<uint32_t>(INT32_MAX)));
+}
 
 constexpr int kMinKeys = 256;   // keys of a CTA's share, at least (fewer CTAs otherwise)
 
@@ -267,13 +271,17 @@ __device__ __forceinline__ Start find_share(const TreeAttnArgs &a, Start *found,
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
+      if (lane >= o) incl = add_tiles(incl, up);
     }
     return make_int2(mine, incl);
   };
   if (p.Q <= 32) {
     const int2 s = scan32(lane);
     st.W = __shfl_sync(0xffffffffu, s.y, 31);
+    if (st.W == INT32_MAX) {
+      st.W = 0;
+      bad |= kStatusBadBound;
+    }
     const Shares sh(st.W, a.tile, gridDim.x);
     const int t0 = sh.begin(min(static_cast<int>(blockIdx.x), sh.n));
     const uint32_t at = __ballot_sync(0xffffffffu, t0 >= s.y - s.x && t0 < s.y);
@@ -293,22 +301,27 @@ __device__ __forceinline__ Start find_share(const TreeAttnArgs &a, Start *found,
     if (lane == 31) warp_sums[warp] = s.y;
     __syncthreads();
     int total = 0;
-    s.y += before;
+    s.y = add_tiles(s.y, before);
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) s.y += warp_sums[w];
-      total += warp_sums[w];
+      if (w < warp) s.y = add_tiles(s.y, warp_sums[w]);
+      total = add_tiles(total, warp_sums[w]);
     }
     __syncthreads();
     return total;
   };
   int2 s = make_int2(0, 0);
-  for (int i0 = 0; i0 < p.Q; i0 += kThreads) st.W += scan(i0, st.W, s);
+  for (int i0 = 0; i0 < p.Q; i0 += kThreads) st.W = add_tiles(st.W, scan(i0, st.W, s));
+  if (st.W == INT32_MAX) {
+    if (blockIdx.x == 0 && tid == 0) flag_status(a.status, kStatusBadBound);
+    st.W = 0;
+    return st;
+  }
   if (blockIdx.x == 0 && bad) flag_status(a.status, bad);
   const Shares sh(st.W, a.tile, gridDim.x);
   const int t0 = sh.begin(min(static_cast<int>(blockIdx.x), sh.n));
   int before = 0;
   for (int i0 = 0; i0 < p.Q; i0 += kThreads) {
-    if (p.Q > kThreads) before += scan(i0, before, s);   // one chunk: the sums are still in registers
+    if (p.Q > kThreads) before = add_tiles(before, scan(i0, before, s));   // one chunk: the sums are still in registers
     if (i0 + tid < p.Q && t0 >= s.y - s.x && t0 < s.y) {
       found->req = i0 + tid;
       found->base = s.y - s.x;

@@ -34,7 +34,7 @@
 // 256K bf16 keys 373 us, 6.2 TB/s).  Two: the softmax, at about 1,300 cycles for a tile of 64
 // keys whose products take the tensor core as long, and the ends of items split over CTAs
 // (4 requests' 64-node trees, 4,096 rows per request, 184.5 us, 1.0 PFLOP/s; 2 requests of
-// 64 x 64 rows over 30,000 E4M3 keys of 2 heads 223 us).
+// 64 x 64 rows over 30,000 E4M3 keys of 2 heads 225 us).
 #pragma once
 
 #include "tree_attention_common.cuh"

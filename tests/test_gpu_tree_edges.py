@@ -148,3 +148,22 @@ def test_a_cached_nan_reaches_rows_that_hardly_weigh_it(lib, kv, D, Q, ctx, head
     assert s.status() == lib.IDX_OK
     tu.check(s, out, lse)
     assert bool(torch.isnan(out[:, :, 7].float()).all())
+
+
+@pytest.mark.parametrize("Q,Hkv,G,ctx", [(32, 1024, 1, 2 ** 25), (4096, 16, 1, 2 ** 24), (4096, 8, 64, 2 ** 24)])
+def test_tiles_past_32_bits_are_reported(lib, Q, Hkv, G, ctx):
+    """Requests that share their rows (row_start does not ascend) pass the host's bounds; a launch
+    of so many tiles that their count would wrap does nothing."""
+    new, tile = 4, 128 if 4 * G <= 32 else 64
+    assert 2 ** 32 < Q // 2 * Hkv * ((ctx + new + tile - 1) // tile) < 2 ** 32 + 2 ** 20
+    k, v = (torch.zeros(1, 64, Hkv, 64, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    q = torch.zeros(new, Hkv * G, 64, dtype=torch.bfloat16, device="cuda")
+    row_start = torch.tensor([0, new] * (Q // 2) + [0], dtype=torch.int32, device="cuda")
+    table = torch.zeros(Q, ctx // 64 + 1, dtype=torch.int32, device="cuda")
+    lens = torch.full((Q,), ctx, dtype=torch.int32, device="cuda")
+    p = lib.make_tree_problem(q, lib.make_kv_cache(k, v), table, lens, row_start, None, ctx, new, 0.125)
+    out = torch.full((new, Hkv * G, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    state = lib.alloc_state(lib.tree_state_size(p))
+    lib.idx_tree_attention(p, out, state)
+    assert lib.last_device_status(state) == lib.IDX_EDEVICE
+    assert bool((out == 7).all())
