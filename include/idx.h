@@ -440,6 +440,60 @@ idx_status idx_tree_attention(const idx_tree_problem *problem, void *out, float 
 idx_status idx_tree_attention_selected(const idx_tree_problem *problem, const int32_t *sel, int32_t sel_k, void *out,
                                        float *lse, void *state, size_t state_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The two ends of the verify step: from a projection's output to q and the cache
+ * (idx_norm_rope), and from the logits to the next step's lengths (idx_sample,
+ * idx_tree_accept, idx_tree_commit). */
+typedef enum {
+    IDX_NORM_NONE = 0,    /* y = x */
+    IDX_NORM_RMS = 1,     /* y = x / sqrt(mean(x^2) + eps) * weight */
+    IDX_NORM_LAYER = 2    /* y = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * weight + bias */
+} idx_norm;
+
+#define IDX_MAX_AXES 4
+
+/* Queries, keys and values of R rows as a fused projection leaves them. */
+typedef struct {
+    const void *q, *k, *v;     /* device bf16: row r's head h at r * stride + h * D elements, 16-byte aligned; q NULL for
+                                  Hq = 0, k NULL for Hkv = 0, v given with a cache that has values, else NULL */
+    int64_t q_stride, k_stride, v_stride;     /* elements, at least the row's heads, multiples of 8 */
+    void *q_out, *k_out;       /* device bf16, laid out as q and k; each may be its input itself (with its stride), else
+                                  they overlap no input.  k_out NULL: the keys go to the cache alone */
+    int64_t q_out_stride, k_out_stride;
+    const float *q_weight, *q_bias, *k_weight, *k_bias;   /* device fp32 [D], 16-byte aligned, or NULL (1 and 0).
+                                  Weights with a norm only, biases with IDX_NORM_LAYER only */
+    const int32_t *pos;        /* device int32: row r's position on axis a at a * pos_stride + r (any int32 value) */
+    int64_t pos_stride;        /* >= R (>= 0 for one axis) */
+    const float *inv_freq;     /* device fp32 [rot / 2]: radians per position (not finite: NaN) */
+    const int32_t *slot;       /* device int32 [R] with a cache (as idx_write_kv's), else NULL */
+    const int32_t *rows;       /* device int32 [1] or NULL: rows from *rows on are left as they were */
+    int64_t R;
+    int32_t Hq, Hkv;           /* heads, 0 .. 1024, not both 0 */
+    int32_t D;                 /* 64, 128 or 256 (64 or 128 with a cache) */
+    int32_t rot;               /* rotated dimensions 0 .. rot - 1: a multiple of 16 within 0 .. D */
+    int32_t interleaved;       /* 0: dimension i turns with i + rot / 2; 1: 2 i turns with 2 i + 1 */
+    int32_t q_norm, k_norm;    /* idx_norm */
+    float eps;                 /* 2^-60 .. 1 */
+    int32_t axes;              /* 1 .. IDX_MAX_AXES */
+    uint8_t axis[128];         /* HOST: frequency i turns by the position on axis axis[i], i < rot / 2 */
+} idx_norm_rope_args;
+
+/* Norm of every head of q and k, then its rotation: with y the normed head and
+ * angle_i = pos[axis[i]][r] * inv_freq[i] in real numbers, for any position (off by 2^-24 of
+ * itself or 2^-32 of a turn while |inv_freq| <= 1), for the pair (a, b) of frequency i
+ *     z_a = y_a cos angle_i - y_b sin angle_i,   z_b = y_b cos angle_i + y_a sin angle_i.
+ * All of it in fp32, rounded once: q to q_out; k to k_out (bf16) where given, and to the
+ * cache where given, at its rows' slots: bf16, or E4M3 with scale = amax / 448 of the fp32
+ * values (1 where they are all zero), saturating; v to the cache exactly as idx_write_kv.
+ * NaN and infinity in a normed or quantised head act as idx_write_kv and the formulas say;
+ * a head whose squares pass fp32's range is normed all the same.  A slot outside
+ * [0, P * 64) writes nothing to the cache; slots >= 0 must differ.
+ * cache  NULL, or a cache of Hkv heads of D dimensions; one without values (v and v_scale
+ *        NULL, the indexer's key cache among them: Hkv = 1, D = 128, token_stride 128)
+ *        takes the keys alone.
+ * R = 0 does nothing.  Asynchronous on `stream`; allocates nothing. */
+idx_status idx_norm_rope(const idx_norm_rope_args *args, const idx_kv_cache *cache, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

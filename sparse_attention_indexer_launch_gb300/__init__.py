@@ -13,6 +13,8 @@ not been built, importing this package raises; there is no other code path.
     idx_tree_tables, idx_write_kv, idx_tree_attention,
     idx_tree_attention_selected  the tree-verify step around the indexer: page
                      tables and slots, K/V writes, attention over the paged cache
+    idx_norm_rope    head norms and rotation of q and k, K/V into the cache in the
+                     same pass
 """
 from __future__ import annotations
 
@@ -27,6 +29,8 @@ IDX_OK, IDX_EINVAL, IDX_EUNSUPPORTED, IDX_ECUDA, IDX_ETIMEOUT, IDX_EDEVICE = ran
 IDX_KV_E4M3, IDX_KV_BF16 = 0, 1
 IDX_HEADS, IDX_DIM, IDX_PAGE, IDX_MAX_K = 64, 128, 64, 2048
 IDX_MAX_REQS, IDX_MAX_TREE = 4096, 64
+IDX_NORM_NONE, IDX_NORM_RMS, IDX_NORM_LAYER = 0, 1, 2
+IDX_MAX_AXES = 4
 IDX_DEBUG_WAIT_LIMIT_NS, IDX_DEBUG_STALL_SCORE_MMA = 1, 2
 
 EXPORTS = ["idx_workspace_size", "idx_score", "idx_topk", "idx_launch", "idx_host_arena_size",
@@ -34,7 +38,7 @@ EXPORTS = ["idx_workspace_size", "idx_score", "idx_topk", "idx_launch", "idx_hos
            "idx_debug_set", "idx_profile_events", "idx_top1_state_size", "idx_top1", "idx_topk_noalloc",
            "idx_patch_new_keys", "idx_launch_scored", "idx_merge_topk", "idx_launch_new_keys",
            "idx_tree_tables_state_size", "idx_tree_tables", "idx_write_kv", "idx_tree_state_size",
-           "idx_tree_attention", "idx_tree_attention_selected"]
+           "idx_tree_attention", "idx_tree_attention_selected", "idx_norm_rope"]
 
 
 class IdxError(RuntimeError):
@@ -82,6 +86,21 @@ class TreeProblem(ctypes.Structure):
         ("Q", ctypes.c_int32), ("pt_stride", ctypes.c_int32), ("max_ctx", ctypes.c_int32), ("max_new", ctypes.c_int32),
         ("Hq", ctypes.c_int32), ("scale", ctypes.c_float),
     ]
+
+
+class NormRope(ctypes.Structure):
+    """Mirror of idx_norm_rope_args, with its cache."""
+    device = None   # the GPU of its tensors, where they are known
+    cache = None    # KvCache or None
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v")] + [
+        (n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")] + [
+        (n, ctypes.c_void_p) for n in ("q_out", "k_out")] + [
+        (n, ctypes.c_int64) for n in ("q_out_stride", "k_out_stride")] + [
+        (n, ctypes.c_void_p) for n in ("q_weight", "q_bias", "k_weight", "k_bias", "pos")] + [
+        ("pos_stride", ctypes.c_int64)] + [(n, ctypes.c_void_p) for n in ("inv_freq", "slot", "rows")] + [
+        ("R", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
+            "Hq", "Hkv", "D", "rot", "interleaved", "q_norm", "k_norm")] + [
+        ("eps", ctypes.c_float), ("axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 128)]
 
 
 def _load():
@@ -140,6 +159,8 @@ def _load():
     lib.idx_tree_attention.restype = ctypes.c_int
     lib.idx_tree_attention_selected.argtypes = [A, vp, i32, vp, vp, vp, sz, vp]
     lib.idx_tree_attention_selected.restype = ctypes.c_int
+    lib.idx_norm_rope.argtypes = [ctypes.POINTER(NormRope), C, vp]
+    lib.idx_norm_rope.restype = ctypes.c_int
     return lib
 
 
@@ -336,18 +357,21 @@ def idx_tree_tables(tables: TreeTables, state, stream=None):
 def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
     """idx_kv_cache from device tensors: k and v [P][64][Hkv][D] (any strides but a
     contiguous last dimension, the same for both), bf16, or E4M3 (float8_e4m3fn or
-    uint8) with contiguous fp32 scales [P][Hkv][64]."""
+    uint8) with contiguous fp32 scales [P][Hkv][64].  v None (and v_scale): keys alone,
+    for the calls that take such a cache."""
     import torch
     P, page, Hkv, D = (int(x) for x in k.shape)
-    _need(page == IDX_PAGE and v.shape == k.shape and v.dtype == k.dtype, "k, v: two [P][64][Hkv][D] tensors are wanted")
+    both = (k,) if v is None else (k, v)
+    _need(page == IDX_PAGE and all(x.shape == k.shape and x.dtype == k.dtype for x in both),
+          "k, v: two [P][64][Hkv][D] tensors are wanted")
     _need(k.dtype in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8), "k, v: bf16 or E4M3 is wanted")
     f8 = k.dtype != torch.bfloat16
     # a dimension of one element is never stepped over: any stride will do
-    st = [[s if n > 1 else page * Hkv * D for n, s in zip(x.shape, x.stride())] for x in (k, v)]
-    _need(st[0] == st[1] and k.stride(3) == 1 and v.stride(3) == 1,
+    st = [[s if n > 1 else page * Hkv * D for n, s in zip(x.shape, x.stride())] for x in both]
+    _need(st[0] == st[-1] and all(x.stride(3) == 1 for x in both),
           "k, v: equal strides and contiguous dimensions are wanted")
-    for s in (k_scale, v_scale):
-        _need((s is not None) == f8, "k_scale, v_scale: wanted for an E4M3 cache only")
+    for s, x in ((k_scale, k), (v_scale, v)):
+        _need((s is not None) == (f8 and x is not None), "k_scale, v_scale: wanted for an E4M3 cache only")
         _need(s is None or (s.dtype == torch.float32 and s.is_contiguous() and tuple(s.shape) == (P, Hkv, page)),
               "k_scale, v_scale: contiguous fp32 [P][Hkv][64] is wanted")
     device = _one_device(k, v, k_scale, v_scale)
@@ -437,6 +461,63 @@ def idx_tree_attention_selected(problem: TreeProblem, sel, out, state, lse=None,
                                            None if lse is None else lse.data_ptr(), state.data_ptr(), state.nbytes,
                                            _current(stream, problem, sel, out, state, lse)),
            "idx_tree_attention_selected")
+
+
+def _heads(name, t, R, H, D):
+    """The row stride of a bf16 [R][H][D] tensor with contiguous heads."""
+    import torch
+    _need(t.dtype == torch.bfloat16 and tuple(t.shape) == (R, H, D) and t.stride(2) == 1 and (H == 1 or t.stride(1) == D),
+          f"{name}: bf16 {[R, H, D]} with contiguous heads is wanted")
+    return int(t.stride(0)) if R > 1 else H * D
+
+
+def make_norm_rope(q, k=None, v=None, *, q_out=None, k_out=None, pos, inv_freq, cache: KvCache | None = None, slot=None,
+                   axis=None, interleaved: bool = False, q_norm: int = IDX_NORM_RMS, k_norm: int = IDX_NORM_RMS,
+                   q_weight=None, q_bias=None, k_weight=None, k_bias=None, eps: float = 1e-6, rows=None) -> NormRope:
+    """idx_norm_rope_args from device tensors (see idx.h): q bf16 [R][Hq][D], k and v bf16
+    [R][Hkv][D] (rows of any stride, each None where there is none); q_out and k_out laid
+    out as q and k, or q and k themselves; pos int32 [R] or [axes][R]; inv_freq fp32
+    [rot / 2]; weights and biases fp32 [D]; cache and slot [R] int32 together; axis: the
+    axis of every frequency (rot / 2 integers; None: axis 0); rows int32 [1] or None."""
+    import torch
+    first = q if q is not None else k
+    _need(first is not None and first.dim() == 3, "q, k: one [R][H][D] tensor at least is wanted")
+    R, _, D = (int(x) for x in first.shape)
+    Hq, Hkv = (int(x.shape[1]) if x is not None else 0 for x in (q, k))
+    strides = [_heads(n, t, R, h, D) if t is not None else 0 for n, t, h in (
+        ("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv), ("q_out", q_out, Hq), ("k_out", k_out, Hkv))]
+    pos2 = pos if pos.dim() == 2 else pos.unsqueeze(0)
+    axes, pairs = int(pos2.shape[0]), int(inv_freq.numel())
+    _need(pos2.dtype == torch.int32 and pos2.shape[1] == R and (R <= 1 or pos2.stride(1) == 1),
+          "pos: int32 [R] or [axes][R] with contiguous rows is wanted")
+    _need(inv_freq.dtype == torch.float32 and inv_freq.is_contiguous() and pairs <= 128,
+          "inv_freq: contiguous fp32 of a value per pair is wanted")
+    for name, t in (("q_weight", q_weight), ("q_bias", q_bias), ("k_weight", k_weight), ("k_bias", k_bias)):
+        _need(t is None or (t.dtype == torch.float32 and t.is_contiguous() and t.numel() == D),
+              f"{name}: contiguous fp32 [D] is wanted")
+    axis = [0] * pairs if axis is None else [int(a) for a in axis]
+    _need(len(axis) == pairs and all(0 <= a < axes for a in axis), "axis: an axis of pos for every frequency is wanted")
+    if slot is not None:
+        _int32("slot", slot, R)
+    if rows is not None:
+        _int32("rows", rows, 1)
+    device = _one_device(q, k, v, q_out, k_out, pos, inv_freq, slot, q_weight, q_bias, k_weight, k_bias, rows)
+    _need(cache is None or cache.device is None or cache.device == device, "a cache on the GPU of the other tensors is wanted")
+    a = NormRope(q=_ptr(q), k=_ptr(k), v=_ptr(v), q_stride=strides[0], k_stride=strides[1], v_stride=strides[2],
+                 q_out=_ptr(q_out), k_out=_ptr(k_out), q_out_stride=strides[3], k_out_stride=strides[4],
+                 q_weight=_ptr(q_weight), q_bias=_ptr(q_bias), k_weight=_ptr(k_weight), k_bias=_ptr(k_bias), pos=_ptr(pos),
+                 pos_stride=int(pos2.stride(0)) if axes > 1 else R, inv_freq=_ptr(inv_freq), slot=_ptr(slot),
+                 rows=_ptr(rows), R=R, Hq=Hq, Hkv=Hkv, D=D, rot=2 * pairs, interleaved=int(bool(interleaved)),
+                 q_norm=int(q_norm), k_norm=int(k_norm), eps=float(eps), axes=axes,
+                 axis=(ctypes.c_uint8 * 128)(*axis))
+    a.device, a.cache = device, cache
+    return a
+
+
+def idx_norm_rope(plan: NormRope, stream=None):
+    """Norms and rotates q and k of the plan's rows, with K and V into its cache (see idx.h)."""
+    _check(lib.idx_norm_rope(ctypes.byref(plan), None if plan.cache is None else ctypes.byref(plan.cache),
+                             _current(stream, plan)), "idx_norm_rope")
 
 
 def last_device_status(ws, stream=None) -> int:

@@ -128,6 +128,14 @@ struct WriteKvArgs {
   const int32_t *slot;
 };
 
+struct NormRopeArgs {
+  idx_norm_rope_args p;
+  idx_kv_cache c;          // k null: no cache
+  int32_t heads;           // heads of a warp; set by the launcher, like the counts below
+  int32_t q_jobs, k_jobs;  // warps of a row for its q heads, and for its k heads
+  int32_t jobs;            // with those for v
+};
+
 struct TreeAttnArgs {
   idx_tree_problem p;
   const int32_t *sel;      // [R][sel_k] or null: every cached position
@@ -148,6 +156,7 @@ constexpr int kTreeMaxCtas = 160;   // shares of an attention launch, at most
 
 cudaError_t launch_tree_tables(TreeTablesArgs a, int num_sms, cudaStream_t stream);
 cudaError_t launch_write_kv(const WriteKvArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t stream);
 // qm: q as [R][Hq][D], box 64 x heads per key/value head x tokens of a row block; km, vm:
 // the cache as [P][Hkv][64][D], box one head's page (64 dimensions of it for bf16).
 using TreeAttnLaunch = cudaError_t(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km,

@@ -1,0 +1,89 @@
+// The C ABI of the verify step's two ends (include/idx.h): argument checks and launches.
+#include <cmath>
+
+#include "api_checks.h"
+#include "idx.h"
+#include "idx_device.cuh"
+#include "launch.h"
+
+namespace {
+
+using idx::aligned;
+using idx::check_cache;
+using idx::cuda_ok;
+using idx::words;
+
+// One of q, k, v or an output: rows of `heads` heads.
+bool rows_ok(const void *p, int64_t stride, int64_t heads, int64_t D) {
+  return p != nullptr && aligned(p, 16) && stride >= heads * D && stride % 8 == 0;
+}
+constexpr int64_t kMaxStride = int64_t{1} << 39;   // elements: a row's offset stays within 64 bits
+
+idx_status check_norm_rope(const idx_norm_rope_args *p, const idx_kv_cache *c) {
+  if (p == nullptr || p->R < 0) return IDX_EINVAL;
+  if (c != nullptr) {
+    const idx_status st = check_cache(c, true);
+    if (st != IDX_OK) return st;
+    if (c->Hkv != p->Hkv || c->D != p->D) return IDX_EINVAL;
+  }
+  const bool has_v = c != nullptr && c->v != nullptr;
+  if (p->Hq < 0 || p->Hkv < 0 || p->Hq + static_cast<int64_t>(p->Hkv) < 1) return IDX_EINVAL;
+  if (p->Hq > 1024 || p->Hkv > 1024) return IDX_EUNSUPPORTED;
+  if (p->D != 64 && p->D != 128 && p->D != 256) return IDX_EUNSUPPORTED;
+  if (p->rot < 0 || p->rot > p->D) return IDX_EINVAL;
+  if (p->rot % 16 != 0) return IDX_EUNSUPPORTED;   // pairs of whole lanes
+  if (p->axes < 1 || p->axes > IDX_MAX_AXES) return IDX_EINVAL;
+  for (int i = 0; i < p->rot / 2; ++i)
+    if (p->axis[i] >= p->axes) return IDX_EINVAL;
+  for (const int n : {p->q_norm, p->k_norm})
+    if (n != IDX_NORM_NONE && n != IDX_NORM_RMS && n != IDX_NORM_LAYER) return IDX_EINVAL;
+  if ((p->q_weight != nullptr && p->q_norm == IDX_NORM_NONE) || (p->k_weight != nullptr && p->k_norm == IDX_NORM_NONE) ||
+      (p->q_bias != nullptr && p->q_norm != IDX_NORM_LAYER) || (p->k_bias != nullptr && p->k_norm != IDX_NORM_LAYER))
+    return IDX_EINVAL;
+  if (!(p->eps >= 0x1p-60f && p->eps <= 1.0f)) return IDX_EINVAL;
+  if (p->R == 0) return IDX_OK;
+  for (const float *w : {p->q_weight, p->q_bias, p->k_weight, p->k_bias})
+    if (!aligned(w, 16)) return IDX_EINVAL;
+  if (!words({p->pos, p->inv_freq, p->slot, p->rows})) return IDX_EINVAL;
+  if (p->Hq > 0) {
+    if (!rows_ok(p->q, p->q_stride, p->Hq, p->D) || !rows_ok(p->q_out, p->q_out_stride, p->Hq, p->D)) return IDX_EINVAL;
+    if (p->q == p->q_out && p->q_stride != p->q_out_stride) return IDX_EINVAL;
+  } else if (p->q != nullptr || p->q_out != nullptr) {
+    return IDX_EINVAL;
+  }
+  if (p->Hkv > 0) {
+    if (!rows_ok(p->k, p->k_stride, p->Hkv, p->D)) return IDX_EINVAL;
+    if (p->k_out != nullptr && !rows_ok(p->k_out, p->k_out_stride, p->Hkv, p->D)) return IDX_EINVAL;
+    if (p->k == p->k_out && p->k_stride != p->k_out_stride) return IDX_EINVAL;
+    if (p->k_out == nullptr && c == nullptr) return IDX_EINVAL;   // keys that go nowhere
+  } else if (p->k != nullptr || p->k_out != nullptr) {
+    return IDX_EINVAL;
+  }
+  if (has_v ? !rows_ok(p->v, p->v_stride, p->Hkv, p->D) : p->v != nullptr) return IDX_EINVAL;
+  if ((c != nullptr) != (p->slot != nullptr)) return IDX_EINVAL;
+  if (p->rot > 0 && (p->pos == nullptr || p->inv_freq == nullptr)) return IDX_EINVAL;
+  if (p->pos_stride < 0 || (p->axes > 1 && p->pos_stride < p->R)) return IDX_EINVAL;
+  // the grid holds a warp per vector at most, eight to a CTA
+  if (p->R > INT32_MAX / (p->Hq + 2 * static_cast<int64_t>(p->Hkv))) return IDX_EUNSUPPORTED;
+  for (const int64_t s : {p->q_stride, p->k_stride, p->v_stride, p->q_out_stride, p->k_out_stride, p->pos_stride})
+    if (s >= kMaxStride) return IDX_EUNSUPPORTED;
+  return IDX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+idx_status idx_norm_rope(const idx_norm_rope_args *args, const idx_kv_cache *cache, void *stream) {
+  idx_status st = check_norm_rope(args, cache);
+  if (st != IDX_OK || args->R == 0) return st;
+  int sms = 0;
+  st = idx::device_sms(&sms);
+  if (st != IDX_OK) return st;
+  idx::NormRopeArgs a{};
+  a.p = *args;
+  if (cache != nullptr) a.c = *cache;
+  return cuda_ok(idx::launch_norm_rope(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

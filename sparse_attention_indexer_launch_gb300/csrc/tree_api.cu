@@ -2,54 +2,24 @@
 #include <cuda.h>
 
 #include <cmath>
-#include <initializer_list>
 
+#include "api_checks.h"
 #include "idx.h"
 #include "idx_device.cuh"
 #include "launch.h"
 
 namespace {
 
-constexpr size_t kStateAlign = 1024;
+using idx::aligned;
+using idx::check_cache;
+using idx::cuda_ok;
+using idx::kStateAlign;
+using idx::kStatusBytes;
+using idx::state_ok;
+using idx::words;
+
 constexpr int kMaxGroup = 128;          // query heads per key/value head: the rows of a tensor-core tile
-constexpr size_t kStatusBytes = 1024;   // the status word's block at the start of every state
 constexpr int32_t kMaxCtx = 1 << 30;    // cached tokens of a request: its keys, up to the end of a tile, fit 31 bits
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-bool words(std::initializer_list<const void *> arrays) {   // 4-byte elements at 4-byte addresses (or null)
-  for (const void *p : arrays)
-    if (!aligned(p, 4)) return false;
-  return true;
-}
-
-idx_status cuda_ok(cudaError_t e) { return e == cudaSuccess ? IDX_OK : IDX_ECUDA; }
-
-bool state_ok(const void *state, size_t bytes, size_t need) {
-  return state != nullptr && aligned(state, kStateAlign) && bytes >= need;
-}
-
-idx_status check_cache(const idx_kv_cache *c) {
-  if (c->k == nullptr || c->v == nullptr || !aligned(c->k, 16) || !aligned(c->v, 16)) return IDX_EINVAL;
-  if (c->P < 1 || c->Hkv < 1) return IDX_EINVAL;
-  if (c->P > INT32_MAX / IDX_PAGE || c->Hkv > 1024) return IDX_EUNSUPPORTED;
-  if (c->D != 64 && c->D != 128) return IDX_EUNSUPPORTED;
-  int64_t bytes;
-  if (c->kv_dtype == IDX_KV_E4M3) {
-    bytes = 1;
-    if (c->k_scale == nullptr || c->v_scale == nullptr || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
-      return IDX_EINVAL;
-  } else if (c->kv_dtype == IDX_KV_BF16) {
-    bytes = 2;
-    if (c->k_scale != nullptr || c->v_scale != nullptr) return IDX_EINVAL;
-  } else {
-    return IDX_EINVAL;
-  }
-  for (const int64_t s : {c->page_stride, c->token_stride, c->head_stride}) {
-    if (s < 1 || s % (16 / bytes) != 0) return IDX_EINVAL;
-    if (s >= (int64_t{1} << 40) / bytes) return IDX_EUNSUPPORTED;   // a tensor map's strides have 40 bits
-  }
-  return IDX_OK;
-}
 
 // The launch's shape.  Up to 64 rows of a request and key/value head (selected: of a token)
 // go to the few-row kernel, over a bf16 cache up to 32; up to 128 rows to the many-row kernel in
