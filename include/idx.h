@@ -494,6 +494,46 @@ typedef struct {
  * R = 0 does nothing.  Asynchronous on `stream`; allocates nothing. */
 idx_status idx_norm_rope(const idx_norm_rope_args *args, const idx_kv_cache *cache, void *stream);
 
+typedef enum {
+    IDX_LOGITS_F32 = 0,
+    IDX_LOGITS_BF16 = 1
+} idx_logits_dtype;
+
+#define IDX_MAX_VOCAB 360448   /* logits of a row that the sampler takes */
+
+/* Logits of R rows and how a token of each is drawn.  Every parameter is a value per row. */
+typedef struct {
+    const void *logits;        /* device fp32 or bf16 [R][ld], aligned to its elements; columns 0 .. V-1 are read */
+    const float *u;            /* device fp32 [R]: a random number in [0, 1) (below it or NaN: 0, above it: the last
+                                  number below 1) */
+    const float *temperature;  /* device fp32 [R] or NULL (1): 0 or less, or NaN: the largest logit's token; else used
+                                  within 2^-60 .. 2^60 */
+    const int32_t *top_k;      /* device int32 [R] or NULL: 0 or less, or V or more: off */
+    const float *top_p;        /* device fp32 [R] or NULL: 1 or more, or NaN: off; 0 or less: the largest logit's token */
+    const float *min_p;        /* device fp32 [R] or NULL: 0 or less, or NaN: off; used as at most 1 */
+    const int32_t *rows;       /* device int32 [1] or NULL: rows from *rows on are left as they were */
+    int64_t ld;                /* elements, >= V */
+    int32_t R;                 /* 1 .. IDX_MAX_ROWS */
+    int32_t V;                 /* 1 .. IDX_MAX_VOCAB */
+    int32_t logits_dtype;      /* idx_logits_dtype */
+} idx_sample_args;
+
+/* Draws a token of every row, in one launch.  With w_i = exp((l_i - max l) / T) and the
+ * tokens ordered by logit descending, then index ascending:
+ *   top-k keeps the first k; top-p of those the ones before which there is less than
+ *   p times their weight; min-p of those the ones with w_i >= min_p.
+ * The token is the first kept one, in order of index, up to and with which there is more
+ * than u times the kept weight: its probability is w_i over that weight.
+ *   token    device int32 [R]; -1 for a row without a logit above -inf.
+ *   logprob  device fp32 [R] or NULL: the log of the token's probability among the kept
+ *            (-inf beside token -1).
+ * A NaN counts as -inf; with logits of +inf those alone have weight.  Weights are held to
+ * about 2^-39 of themselves as integers of 2^-43 (below half of that: 0) and summed
+ * exactly: where 64-bit sums put a token, so does this, but for numbers u that close to a
+ * border.  Equal calls give equal results.
+ * Asynchronous on `stream`; allocates nothing and needs no workspace. */
+idx_status idx_sample(const idx_sample_args *args, int32_t *token, float *logprob, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,6 +15,7 @@ not been built, importing this package raises; there is no other code path.
                      tables and slots, K/V writes, attention over the paged cache
     idx_norm_rope    head norms and rotation of q and k, K/V into the cache in the
                      same pass
+    idx_sample       a token of every row: temperature, top-k, top-p, min-p
 """
 from __future__ import annotations
 
@@ -31,6 +32,8 @@ IDX_HEADS, IDX_DIM, IDX_PAGE, IDX_MAX_K = 64, 128, 64, 2048
 IDX_MAX_REQS, IDX_MAX_TREE = 4096, 64
 IDX_NORM_NONE, IDX_NORM_RMS, IDX_NORM_LAYER = 0, 1, 2
 IDX_MAX_AXES = 4
+IDX_LOGITS_F32, IDX_LOGITS_BF16 = 0, 1
+IDX_MAX_VOCAB = 360448
 IDX_DEBUG_WAIT_LIMIT_NS, IDX_DEBUG_STALL_SCORE_MMA = 1, 2
 
 EXPORTS = ["idx_workspace_size", "idx_score", "idx_topk", "idx_launch", "idx_host_arena_size",
@@ -38,7 +41,7 @@ EXPORTS = ["idx_workspace_size", "idx_score", "idx_topk", "idx_launch", "idx_hos
            "idx_debug_set", "idx_profile_events", "idx_top1_state_size", "idx_top1", "idx_topk_noalloc",
            "idx_patch_new_keys", "idx_launch_scored", "idx_merge_topk", "idx_launch_new_keys",
            "idx_tree_tables_state_size", "idx_tree_tables", "idx_write_kv", "idx_tree_state_size",
-           "idx_tree_attention", "idx_tree_attention_selected", "idx_norm_rope"]
+           "idx_tree_attention", "idx_tree_attention_selected", "idx_norm_rope", "idx_sample"]
 
 
 class IdxError(RuntimeError):
@@ -103,6 +106,14 @@ class NormRope(ctypes.Structure):
         ("eps", ctypes.c_float), ("axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 128)]
 
 
+class Sample(ctypes.Structure):
+    """Mirror of idx_sample_args, with its outputs."""
+    device = None   # the GPU of its tensors, where they are known
+    token = logprob = None
+    _fields_ = [(n, ctypes.c_void_p) for n in ("logits", "u", "temperature", "top_k", "top_p", "min_p", "rows")] + [
+        ("ld", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("R", "V", "logits_dtype")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libidx.so is not built ({LIB_PATH}); run "
@@ -161,6 +172,8 @@ def _load():
     lib.idx_tree_attention_selected.restype = ctypes.c_int
     lib.idx_norm_rope.argtypes = [ctypes.POINTER(NormRope), C, vp]
     lib.idx_norm_rope.restype = ctypes.c_int
+    lib.idx_sample.argtypes = [ctypes.POINTER(Sample), vp, vp, vp]
+    lib.idx_sample.restype = ctypes.c_int
     return lib
 
 
@@ -518,6 +531,35 @@ def idx_norm_rope(plan: NormRope, stream=None):
     """Norms and rotates q and k of the plan's rows, with K and V into its cache (see idx.h)."""
     _check(lib.idx_norm_rope(ctypes.byref(plan), None if plan.cache is None else ctypes.byref(plan.cache),
                              _current(stream, plan)), "idx_norm_rope")
+
+
+def make_sample(logits, u, token, *, logprob=None, temperature=None, top_k=None, top_p=None, min_p=None,
+                rows=None) -> Sample:
+    """idx_sample_args from device tensors (see idx.h), with its outputs: logits fp32 or bf16
+    [R][V] (rows of any stride), u [R] fp32; token [R] int32 and logprob [R] fp32 or None are
+    written; temperature, top_p and min_p [R] fp32, top_k [R] int32, each None where it is
+    off; rows int32 [1] or None."""
+    import torch
+    _need(logits.dim() == 2 and logits.dtype in (torch.float32, torch.bfloat16) and (logits.shape[1] <= 1 or logits.stride(1) == 1),
+          "logits: fp32 or bf16 [R][V] with contiguous rows is wanted")
+    R, V = (int(x) for x in logits.shape)
+    for name, t in (("u", u), ("logprob", logprob), ("temperature", temperature), ("top_p", top_p), ("min_p", min_p)):
+        _need(t is None or (t.dtype == torch.float32 and t.is_contiguous() and t.numel() >= R),
+              f"{name}: a contiguous fp32 tensor of a value per row is wanted")
+    for name, t, n in (("token", token, R), ("top_k", top_k, R), ("rows", rows, 1)):
+        if t is not None:
+            _int32(name, t, n)
+    device = _one_device(logits, u, token, logprob, temperature, top_k, top_p, min_p, rows)
+    a = Sample(logits=_ptr(logits), u=_ptr(u), temperature=_ptr(temperature), top_k=_ptr(top_k), top_p=_ptr(top_p),
+               min_p=_ptr(min_p), rows=_ptr(rows), ld=int(logits.stride(0)) if R > 1 else V, R=R, V=V,
+               logits_dtype=IDX_LOGITS_BF16 if logits.dtype == torch.bfloat16 else IDX_LOGITS_F32)
+    a.device, a.token, a.logprob = device, token.data_ptr(), None if logprob is None else logprob.data_ptr()
+    return a
+
+
+def idx_sample(plan: Sample, stream=None):
+    """Draws a token of every row of the plan's logits into its outputs (see idx.h)."""
+    _check(lib.idx_sample(ctypes.byref(plan), plan.token, plan.logprob, _current(stream, plan)), "idx_sample")
 
 
 def last_device_status(ws, stream=None) -> int:

@@ -136,6 +136,14 @@ struct NormRopeArgs {
   int32_t jobs;            // with those for v
 };
 
+struct SampleArgs {
+  idx_sample_args p;
+  int32_t *token;
+  float *logprob;          // or null
+  int32_t vec;             // rows allow loads of four logits
+  int32_t warp_len;        // logits of a warp (set by launch_sample)
+};
+
 struct TreeAttnArgs {
   idx_tree_problem p;
   const int32_t *sel;      // [R][sel_k] or null: every cached position
@@ -157,6 +165,7 @@ constexpr int kTreeMaxCtas = 160;   // shares of an attention launch, at most
 cudaError_t launch_tree_tables(TreeTablesArgs a, int num_sms, cudaStream_t stream);
 cudaError_t launch_write_kv(const WriteKvArgs &a, int num_sms, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
 // qm: q as [R][Hq][D], box 64 x heads per key/value head x tokens of a row block; km, vm:
 // the cache as [P][Hkv][64][D], box one head's page (64 dimensions of it for bf16).
 using TreeAttnLaunch = cudaError_t(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km,

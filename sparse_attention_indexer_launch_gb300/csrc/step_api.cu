@@ -70,6 +70,16 @@ idx_status check_norm_rope(const idx_norm_rope_args *p, const idx_kv_cache *c) {
   return IDX_OK;
 }
 
+idx_status check_sample(const idx_sample_args *p, const int32_t *token, const float *logprob) {
+  if (p == nullptr || p->logits == nullptr || p->u == nullptr || token == nullptr) return IDX_EINVAL;
+  if (p->logits_dtype != IDX_LOGITS_F32 && p->logits_dtype != IDX_LOGITS_BF16) return IDX_EINVAL;
+  if (p->R < 1 || p->V < 1 || p->ld < p->V) return IDX_EINVAL;
+  if (!aligned(p->logits, p->logits_dtype == IDX_LOGITS_F32 ? 4 : 2)) return IDX_EINVAL;
+  if (!words({p->u, p->temperature, p->top_p, p->min_p, p->top_k, p->rows, token, logprob})) return IDX_EINVAL;
+  if (p->R > IDX_MAX_ROWS || p->V > IDX_MAX_VOCAB || p->ld >= kMaxStride) return IDX_EUNSUPPORTED;
+  return IDX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -84,6 +94,20 @@ idx_status idx_norm_rope(const idx_norm_rope_args *args, const idx_kv_cache *cac
   a.p = *args;
   if (cache != nullptr) a.c = *cache;
   return cuda_ok(idx::launch_norm_rope(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+idx_status idx_sample(const idx_sample_args *args, int32_t *token, float *logprob, void *stream) {
+  idx_status st = check_sample(args, token, logprob);
+  if (st != IDX_OK) return st;
+  int sms = 0;
+  st = idx::device_sms(&sms);   // the device check
+  if (st != IDX_OK) return st;
+  idx::SampleArgs a{};
+  a.p = *args;
+  a.token = token;
+  a.logprob = logprob;
+  a.vec = args->ld % 4 == 0 && aligned(args->logits, args->logits_dtype == IDX_LOGITS_F32 ? 16 : 8);
+  return cuda_ok(idx::launch_sample(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

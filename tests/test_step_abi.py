@@ -97,3 +97,36 @@ def test_norm_rope_binding(lib):
             lib.make_norm_rope(*args, **good)
     with pytest.raises(ValueError, match="one GPU"):      # all of it on the CPU
         lib.make_norm_rope(q, k, **good)
+
+
+def _sample(lib, token=2 * FAKE, logprob=None, **kw):
+    a = dict(logits=FAKE, u=FAKE, temperature=FAKE, top_k=FAKE, top_p=FAKE, min_p=FAKE, rows=FAKE, ld=1000, R=4, V=1000,
+             logits_dtype=lib.IDX_LOGITS_F32)
+    a.update(kw)
+    return lib.lib.idx_sample(ctypes.byref(lib.Sample(**a)), token, logprob, None)
+
+
+@pytest.mark.parametrize("kw", [dict(logits=None), dict(u=None), dict(token=None), dict(logits=FAKE + 2), dict(u=FAKE + 2),
+                                dict(logits=FAKE + 1, logits_dtype=1), dict(temperature=FAKE + 1), dict(top_k=FAKE + 1),
+                                dict(top_p=FAKE + 2), dict(min_p=FAKE + 3), dict(rows=FAKE + 2), dict(token=FAKE + 2),
+                                dict(logprob=FAKE + 2), dict(ld=999), dict(R=0), dict(R=-1), dict(V=0), dict(logits_dtype=2)])
+def test_sample(lib, kw):
+    assert _sample(lib, **kw) == lib.IDX_EINVAL
+
+
+def test_sample_limits(lib):
+    for kw in (dict(R=65536), dict(V=lib.IDX_MAX_VOCAB + 1, ld=1 << 20), dict(ld=1 << 39)):
+        assert _sample(lib, **kw) == lib.IDX_EUNSUPPORTED, kw
+    assert lib.lib.idx_sample(None, FAKE, None, None) == lib.IDX_EINVAL
+
+
+def test_sample_binding(lib):
+    x, u, token = torch.zeros(3, 10), torch.zeros(3), torch.zeros(3, dtype=torch.int32)
+    for args, kw in (((x.double(), u, token), {}), ((x[0], u, token), {}), ((x.t(), u, token), {}), ((x, u.double(), token), {}),
+                     ((x, u[:2], token), {}), ((x, u, token.long()), {}), ((x, u, token[:2]), {}), ((x, u, token), dict(top_k=u)),
+                     ((x, u, token), dict(top_p=token)), ((x, u, token), dict(temperature=u[:1])), ((x, u, token), dict(logprob=token)),
+                     ((x, u, token), dict(rows=u))):
+        with pytest.raises(ValueError):
+            lib.make_sample(*args, **kw)
+    with pytest.raises(ValueError, match="one GPU"):
+        lib.make_sample(x, u, token)
