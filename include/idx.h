@@ -534,6 +534,62 @@ typedef struct {
  * Asynchronous on `stream`; allocates nothing and needs no workspace. */
 idx_status idx_sample(const idx_sample_args *args, int32_t *token, float *logprob, void *stream);
 
+/* The drafted trees of a step and the token sampled (or ranked first) at every row. */
+typedef struct {
+    const int32_t *row_start;  /* device int32 [Q + 1]: ascending, within 0 .. cap (idx_tree_tables writes it) */
+    const int32_t *parent;     /* device int32 [cap] or NULL (a chain), as idx_tree_tables reads it */
+    const int32_t *draft;      /* device int32 [cap]: every row's own token; a request's token 0 is the one that was
+                                  known before the step */
+    const int32_t *target;     /* device int32 [cap]: the token drawn from every row's logits */
+    const int32_t *ctx_len;    /* device int32 [Q]: tokens cached before the step (as idx_tree_tables reads them) */
+    const int32_t *page_table; /* device int32 [Q][pt_stride], with the step's pages */
+    int32_t *free_pages;       /* device int32 [free_cap]: the free stack; pages given back are written from free_count on */
+    const int32_t *free_count; /* device int32 [1]: its height (idx_tree_tables's free_left) */
+    int32_t *free_left;        /* out, device int32 [1]: its height afterwards; may be free_count itself */
+    int32_t *new_ctx;          /* out, device int32 [Q]: ctx_len + accept_len; may be ctx_len itself */
+    int32_t *accept_len;       /* out, device int32 [Q]: accepted tokens, token 0 among them; 0 for a request without rows */
+    int32_t *last;             /* out, device int32 [Q]: the sampled token behind the last accepted one: the next step's
+                                  token 0 (-1 for a request without rows) */
+    int32_t *path;             /* out, device int32 [cap]: path[row_start[i] + a] is the token number of request i's a-th
+                                  accepted token, -1 from accept_len[i] on */
+    int32_t *token;            /* out, device int32 [cap]: the request's new tokens, token[row_start[i] + a] =
+                                  target[row_start[i] + path[row_start[i] + a]], -1 from accept_len[i] on */
+    int64_t P;                 /* pages of the cache, 1 .. INT32_MAX / 64 */
+    int32_t Q;                 /* requests, 1 .. IDX_MAX_REQS */
+    int32_t pt_stride;         /* page-table row length, >= 1 */
+    int32_t cap;               /* rows that the per-row arrays hold, 1 .. INT32_MAX - 3 */
+    int32_t free_cap;          /* entries of free_pages, >= 0 */
+} idx_tree_accept_args;
+
+/* Bytes of state that idx_tree_accept needs. */
+size_t idx_tree_accept_state_size(void);
+
+/* One launch.  A request's token 0 is accepted; behind an accepted token n the first child c
+ * (parent[c] == n) with draft[c] == target[n] is, and so on.  Where target is drawn by
+ * idx_sample, the accepted tokens and `last` are distributed as the model alone would draw
+ * them, whatever was drafted.  Pages of the step's tokens that hold none of the first
+ * ctx_len + accept_len positions go back to the stack, in order of requests and positions;
+ * their table entries are left as they were, behind the request's length.  The accepted
+ * tokens' keys and values still lie at their slots in the tree: idx_tree_commit moves them.
+ * Rows from row_start[Q] on are not written.
+ * Outputs may not overlap inputs or each other, but for the two that say so.
+ * Found on the device and recorded as IDX_EDEVICE: row_start outside 0 .. cap or descending
+ * (cut), a request of more than IDX_MAX_TREE rows (those past the 64th are not accepted), a
+ * parent that is not an earlier token (nobody's child), a page to give back without an id in
+ * [0, P) or without room on the stack (left out). */
+idx_status idx_tree_accept(const idx_tree_accept_args *args, void *state, size_t state_bytes, void *stream);
+
+/* Moves the accepted tokens' keys and values, scales with them, to consecutive positions:
+ * for a = 1 .. accept_len[i] - 1 from the slot of row row_start[i] + path[row_start[i] + a] to
+ * that of row row_start[i] + a, bit for bit, as if all were read before any is written.
+ *   cache       any; one without values moves keys alone (see idx_norm_rope).
+ *   row_start, accept_len, path   as idx_tree_accept reads and writes them.
+ *   slot        device int32 [cap], as idx_tree_tables writes it: page * 64 + token.
+ * Rows with path <= a or outside the request, and slots outside [0, P * 64), move nothing;
+ * slots >= 0 must differ.  Asynchronous on `stream`; allocates nothing. */
+idx_status idx_tree_commit(const idx_kv_cache *cache, const int32_t *row_start, const int32_t *accept_len,
+                           const int32_t *path, const int32_t *slot, int32_t Q, int32_t cap, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,6 +16,8 @@ not been built, importing this package raises; there is no other code path.
     idx_norm_rope    head norms and rotation of q and k, K/V into the cache in the
                      same pass
     idx_sample       a token of every row: temperature, top-k, top-p, min-p
+    idx_tree_accept, idx_tree_commit  the drafted tokens that the sampled ones
+                     confirm, pages back on the stack, accepted K/V moved up
 """
 from __future__ import annotations
 
@@ -41,7 +43,8 @@ EXPORTS = ["idx_workspace_size", "idx_score", "idx_topk", "idx_launch", "idx_hos
            "idx_debug_set", "idx_profile_events", "idx_top1_state_size", "idx_top1", "idx_topk_noalloc",
            "idx_patch_new_keys", "idx_launch_scored", "idx_merge_topk", "idx_launch_new_keys",
            "idx_tree_tables_state_size", "idx_tree_tables", "idx_write_kv", "idx_tree_state_size",
-           "idx_tree_attention", "idx_tree_attention_selected", "idx_norm_rope", "idx_sample"]
+           "idx_tree_attention", "idx_tree_attention_selected", "idx_norm_rope", "idx_sample",
+           "idx_tree_accept_state_size", "idx_tree_accept", "idx_tree_commit"]
 
 
 class IdxError(RuntimeError):
@@ -114,6 +117,15 @@ class Sample(ctypes.Structure):
         ("ld", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("R", "V", "logits_dtype")]
 
 
+class TreeAccept(ctypes.Structure):
+    """Mirror of idx_tree_accept_args."""
+    device = None   # the GPU of its tensors, where they are known
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "row_start", "parent", "draft", "target", "ctx_len", "page_table", "free_pages", "free_count", "free_left",
+        "new_ctx", "accept_len", "last", "path", "token")] + [
+        ("P", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("Q", "pt_stride", "cap", "free_cap")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libidx.so is not built ({LIB_PATH}); run "
@@ -174,6 +186,12 @@ def _load():
     lib.idx_norm_rope.restype = ctypes.c_int
     lib.idx_sample.argtypes = [ctypes.POINTER(Sample), vp, vp, vp]
     lib.idx_sample.restype = ctypes.c_int
+    lib.idx_tree_accept_state_size.argtypes = []
+    lib.idx_tree_accept_state_size.restype = sz
+    lib.idx_tree_accept.argtypes = [ctypes.POINTER(TreeAccept), vp, sz, vp]
+    lib.idx_tree_accept.restype = ctypes.c_int
+    lib.idx_tree_commit.argtypes = [C, vp, vp, vp, vp, i32, i32, vp]
+    lib.idx_tree_commit.restype = ctypes.c_int
     return lib
 
 
@@ -560,6 +578,54 @@ def make_sample(logits, u, token, *, logprob=None, temperature=None, top_k=None,
 def idx_sample(plan: Sample, stream=None):
     """Draws a token of every row of the plan's logits into its outputs (see idx.h)."""
     _check(lib.idx_sample(ctypes.byref(plan), plan.token, plan.logprob, _current(stream, plan)), "idx_sample")
+
+
+def make_tree_accept(row_start, draft, target, ctx_len, page_table, free_pages, free_count, *, P: int, new_ctx, accept_len,
+                     last, path, token, free_left, parent=None) -> TreeAccept:
+    """idx_tree_accept_args from int32 device tensors (see idx.h): row_start [Q + 1], draft,
+    target and parent (None: chains) [cap], ctx_len [Q], page_table [Q][stride], free_pages [F]
+    with free_count [1] of them free, P the cache's pages; outputs new_ctx (may be ctx_len),
+    accept_len and last [Q], path and token [cap], free_left [1] (may be free_count)."""
+    Q, cap = int(ctx_len.shape[0]), int(draft.shape[0])
+    for name, t, n in (("row_start", row_start, Q + 1), ("draft", draft, cap), ("target", target, cap), ("ctx_len", ctx_len, Q),
+                       ("page_table", page_table, None), ("free_pages", free_pages, None), ("free_count", free_count, 1),
+                       ("free_left", free_left, 1), ("new_ctx", new_ctx, Q), ("accept_len", accept_len, Q), ("last", last, Q),
+                       ("path", path, cap), ("token", token, cap)):
+        _int32(name, t, n)
+    if parent is not None:
+        _int32("parent", parent, cap)
+    _need(page_table.dim() == 2 and page_table.shape[0] == Q, "page_table: [Q][stride] is wanted")
+    device = _one_device(row_start, draft, target, ctx_len, page_table, free_pages, free_count, free_left, new_ctx, accept_len,
+                         last, path, token, parent)
+    a = TreeAccept(row_start=_ptr(row_start), parent=_ptr(parent), draft=_ptr(draft), target=_ptr(target), ctx_len=_ptr(ctx_len),
+                   page_table=_ptr(page_table), free_pages=_ptr(free_pages), free_count=_ptr(free_count), free_left=_ptr(free_left),
+                   new_ctx=_ptr(new_ctx), accept_len=_ptr(accept_len), last=_ptr(last), path=_ptr(path), token=_ptr(token),
+                   P=int(P), Q=Q, pt_stride=int(page_table.shape[1]), cap=cap, free_cap=int(free_pages.numel()))
+    a.device = device
+    return a
+
+
+def tree_accept_state_size() -> int:
+    return int(lib.idx_tree_accept_state_size())
+
+
+def idx_tree_accept(plan: TreeAccept, state, stream=None):
+    """The drafted tokens that the sampled ones confirm, and their pages (see idx.h); `state`
+    from alloc_state(tree_accept_state_size())."""
+    _check(lib.idx_tree_accept(ctypes.byref(plan), state.data_ptr(), state.nbytes, _current(stream, plan, state)),
+           "idx_tree_accept")
+
+
+def idx_tree_commit(cache: KvCache, row_start, accept_len, path, slot, stream=None):
+    """Moves the accepted tokens' keys and values to consecutive positions (see idx.h):
+    accept_len [Q] and path [cap] as idx_tree_accept wrote them, slot [cap]; all int32."""
+    int32 = _modules["torch"].int32
+    Q, cap = accept_len.numel(), path.numel()
+    for t, n in ((row_start, Q + 1), (accept_len, Q), (path, cap), (slot, cap)):
+        if t.dtype is not int32 or not t.is_contiguous() or t.numel() < n:
+            raise ValueError("row_start [Q + 1], accept_len [Q], path and slot [cap]: contiguous int32 tensors are wanted")
+    _check(lib.idx_tree_commit(ctypes.byref(cache), row_start.data_ptr(), accept_len.data_ptr(), path.data_ptr(), slot.data_ptr(),
+                               Q, cap, _current(stream, cache, row_start, accept_len, path, slot)), "idx_tree_commit")
 
 
 def last_device_status(ws, stream=None) -> int:

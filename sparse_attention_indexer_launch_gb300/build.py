@@ -20,7 +20,7 @@ SOURCES = ["api.cu", "prep.cu", "score.cu", "select.cu", "top1.cu", "patch.cu", 
            "tree_tables.cu", "write_kv.cu", "tree_few_bf16_64.cu", "tree_few_bf16_128.cu", "tree_few_e4m3_64.cu",
            "tree_few_e4m3_128.cu", "tree_many_bf16_64.cu", "tree_many_bf16_128.cu", "tree_many_e4m3_64.cu",
            "tree_many_e4m3_128.cu", "step_api.cu", "norm_rope.cu",
-           "sample.cu"]
+           "sample.cu", "tree_accept.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", INCLUDE, "-I", CSRC]

@@ -144,6 +144,18 @@ struct SampleArgs {
   int32_t warp_len;        // logits of a warp (set by launch_sample)
 };
 
+struct TreeAcceptArgs {
+  idx_tree_accept_args t;
+  uint32_t *status;
+  uint32_t *arrived;       // CTAs that have walked their requests, zero between calls
+};
+
+struct TreeCommitArgs {
+  idx_kv_cache c;          // v null: keys alone
+  const int32_t *row_start, *accept_len, *path, *slot;
+  int32_t Q, cap;
+};
+
 struct TreeAttnArgs {
   idx_tree_problem p;
   const int32_t *sel;      // [R][sel_k] or null: every cached position
@@ -166,6 +178,8 @@ cudaError_t launch_tree_tables(TreeTablesArgs a, int num_sms, cudaStream_t strea
 cudaError_t launch_write_kv(const WriteKvArgs &a, int num_sms, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t stream);
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
+cudaError_t launch_tree_accept(const TreeAcceptArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_tree_commit(const TreeCommitArgs &a, cudaStream_t stream);
 // qm: q as [R][Hq][D], box 64 x heads per key/value head x tokens of a row block; km, vm:
 // the cache as [P][Hkv][64][D], box one head's page (64 dimensions of it for bf16).
 using TreeAttnLaunch = cudaError_t(const TreeAttnArgs &a, const CUtensorMap &qm, const CUtensorMap &km,

@@ -11,6 +11,8 @@ namespace {
 using idx::aligned;
 using idx::check_cache;
 using idx::cuda_ok;
+using idx::kStatusBytes;
+using idx::state_ok;
 using idx::words;
 
 // One of q, k, v or an output: rows of `heads` heads.
@@ -108,6 +110,53 @@ idx_status idx_sample(const idx_sample_args *args, int32_t *token, float *logpro
   a.logprob = logprob;
   a.vec = args->ld % 4 == 0 && aligned(args->logits, args->logits_dtype == IDX_LOGITS_F32 ? 16 : 8);
   return cuda_ok(idx::launch_sample(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t idx_tree_accept_state_size(void) { return kStatusBytes; }
+
+idx_status idx_tree_accept(const idx_tree_accept_args *t, void *state, size_t state_bytes, void *stream) {
+  if (t == nullptr || t->row_start == nullptr || t->draft == nullptr || t->target == nullptr || t->ctx_len == nullptr ||
+      t->page_table == nullptr || t->free_pages == nullptr || t->free_count == nullptr || t->new_ctx == nullptr ||
+      t->free_left == nullptr || t->accept_len == nullptr || t->last == nullptr || t->path == nullptr || t->token == nullptr)
+    return IDX_EINVAL;
+  if (!words({t->row_start, t->parent, t->draft, t->target, t->ctx_len, t->page_table, t->free_pages, t->free_count, t->new_ctx,
+              t->free_left, t->accept_len, t->last, t->path, t->token}))
+    return IDX_EINVAL;
+  if (t->Q < 1 || t->P < 1 || t->pt_stride < 1 || t->cap < 1 || t->free_cap < 0) return IDX_EINVAL;
+  // the walk of one request reads what another's would overwrite
+  if (t->path == t->draft || t->path == t->target || t->token == t->draft || t->token == t->target || t->path == t->token)
+    return IDX_EINVAL;
+  if (t->Q > IDX_MAX_REQS || t->P > INT32_MAX / IDX_PAGE || t->cap > INT32_MAX - 3) return IDX_EUNSUPPORTED;
+  if (!state_ok(state, state_bytes, kStatusBytes)) return IDX_EINVAL;
+  int sms = 0;
+  const idx_status st = idx::device_sms(&sms);
+  if (st != IDX_OK) return st;
+  idx::TreeAcceptArgs a{};
+  a.t = *t;
+  a.status = static_cast<uint32_t *>(state);
+  a.arrived = a.status + 1;
+  return cuda_ok(idx::launch_tree_accept(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+idx_status idx_tree_commit(const idx_kv_cache *cache, const int32_t *row_start, const int32_t *accept_len, const int32_t *path,
+                           const int32_t *slot, int32_t Q, int32_t cap, void *stream) {
+  if (cache == nullptr || row_start == nullptr || accept_len == nullptr || path == nullptr || slot == nullptr) return IDX_EINVAL;
+  idx_status st = check_cache(cache, true);
+  if (st != IDX_OK) return st;
+  if (!words({row_start, accept_len, path, slot}) || Q < 1 || cap < 1) return IDX_EINVAL;
+  if (Q > IDX_MAX_REQS || cap > INT32_MAX - 3) return IDX_EUNSUPPORTED;
+  int sms = 0;
+  st = idx::device_sms(&sms);   // the device check
+  if (st != IDX_OK) return st;
+  idx::TreeCommitArgs a{};
+  a.c = *cache;
+  a.row_start = row_start;
+  a.accept_len = accept_len;
+  a.path = path;
+  a.slot = slot;
+  a.Q = Q;
+  a.cap = cap;
+  return cuda_ok(idx::launch_tree_commit(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -130,3 +130,55 @@ def test_sample_binding(lib):
             lib.make_sample(*args, **kw)
     with pytest.raises(ValueError, match="one GPU"):
         lib.make_sample(x, u, token)
+
+
+OUTS = ("free_left", "new_ctx", "accept_len", "last", "path", "token")
+
+
+def _accept(lib, state=FAKE, size=1024, **kw):
+    a = {f: FAKE for f in ("row_start", "parent", "draft", "target", "ctx_len", "page_table", "free_pages", "free_count")}
+    a.update({n: (2 + i) * FAKE for i, n in enumerate(OUTS)}, P=8, Q=2, pt_stride=4, cap=8, free_cap=8)
+    a.update(kw)
+    return lib.lib.idx_tree_accept(ctypes.byref(lib.TreeAccept(**a)), state, size, None)
+
+
+def test_tree_accept(lib):
+    for n in ("row_start", "draft", "target", "ctx_len", "page_table", "free_pages", "free_count") + OUTS:
+        assert _accept(lib, **{n: None}) == lib.IDX_EINVAL, n
+        assert _accept(lib, **{n: FAKE + 2}) == lib.IDX_EINVAL, n
+    for kw in (dict(parent=FAKE + 1), dict(Q=0), dict(P=0), dict(pt_stride=0), dict(cap=0), dict(free_cap=-1), dict(path=FAKE),
+               dict(token=FAKE), dict(path=FAKE * 9, token=FAKE * 9), dict(state=None), dict(state=FAKE + 512),
+               dict(size=lib.tree_accept_state_size() - 1)):
+        assert _accept(lib, **kw) == lib.IDX_EINVAL, kw
+    for kw in (dict(Q=4097), dict(P=2 ** 31 // 64 + 1), dict(cap=2 ** 31 - 3)):
+        assert _accept(lib, **kw) == lib.IDX_EUNSUPPORTED, kw
+    assert lib.lib.idx_tree_accept(None, FAKE, 1024, None) == lib.IDX_EINVAL
+
+
+def test_tree_commit(lib):
+    def call(c=None, starts=FAKE, length=FAKE, path=FAKE, slot=FAKE, Q=2, cap=8):
+        return lib.lib.idx_tree_commit(ctypes.byref(c or _cache(lib)), starts, length, path, slot, Q, cap, None)
+
+    for kw in (dict(starts=None), dict(length=None), dict(path=None), dict(slot=None), dict(starts=FAKE + 2), dict(length=FAKE + 1),
+               dict(path=FAKE + 3), dict(slot=FAKE + 2), dict(Q=0), dict(cap=0), dict(c=_cache(lib, k=None)),
+               dict(c=_cache(lib, kv_dtype=0)), dict(c=_cache(lib, head_stride=4)), dict(c=_cache(lib, v=None, v_scale=FAKE))):
+        assert call(**kw) == lib.IDX_EINVAL, kw
+    for kw in (dict(Q=4097), dict(cap=2 ** 31 - 3), dict(c=_cache(lib, D=256))):
+        assert call(**kw) == lib.IDX_EUNSUPPORTED, kw
+    assert lib.lib.idx_tree_commit(None, FAKE, FAKE, FAKE, FAKE, 2, 8, None) == lib.IDX_EINVAL
+
+
+def test_tree_accept_and_commit_binding(lib):
+    i = lambda *n: torch.zeros(*n, dtype=torch.int32)  # noqa: E731
+    good = dict(row_start=i(3), draft=i(8), target=i(8), ctx_len=i(2), page_table=i(2, 4), free_pages=i(6), free_count=i(1), P=8,
+                new_ctx=i(2), accept_len=i(2), last=i(2), path=i(8), token=i(8), free_left=i(1))
+    for kw in (dict(row_start=i(2)), dict(target=i(7)), dict(page_table=i(3, 4)), dict(page_table=i(8)), dict(path=i(7)),
+               dict(token=torch.zeros(8)), dict(last=i(1)), dict(parent=i(7)), dict(free_count=i(0)), dict(draft=i(16)[::2])):
+        with pytest.raises(ValueError):
+            lib.make_tree_accept(**dict(good, **kw))
+    with pytest.raises(ValueError, match="one GPU"):
+        lib.make_tree_accept(**good)
+    c = _cache(lib)
+    for args in ((i(2), i(2), i(8), i(8)), (i(3), i(2), i(8), i(7)), (i(3), i(2).long(), i(8), i(8)), (i(3), i(2), i(16)[::2], i(8))):
+        with pytest.raises(ValueError):
+            lib.idx_tree_commit(c, *args)
