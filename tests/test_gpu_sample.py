@@ -4,8 +4,8 @@ A token has to be the reference's: the library's sums are off by about 2^-38 of 
 weight, so a random u lies that close to a border once in millions of rows.  Where the
 inputs put u or p on a border exactly (equal logits), both sides are exact.  logprob is
 the sum of -(max l - l) / T and -log1p(Z - 1), both <= 0 and each rounded to fp32 (with log1p
-2^-22 of itself), but Z is a sum of at most V weights that are each rounded to a multiple of
-2^-43, off by half of that: 2^-21 of itself and V 2^-44 at most."""
+2^-22 of itself), but Z is a sum of at most V weights that are each rounded to an odd multiple of
+2^-44 of the largest, off by that at most: 2^-21 of itself and V 2^-44."""
 import numpy as np
 import pytest
 import torch
