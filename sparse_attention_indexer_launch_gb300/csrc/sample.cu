@@ -16,9 +16,9 @@
 // so one number is enough, the composite (key, ~index) of the last kept one.  A first pass
 // sorts the weights' exponents into bins of 1 / 32 octave, counts for top-k and leading bits
 // of the weights for top-p; the elements of the bin that holds the border (for top-k those
-// above as well) go into a list that every CTA gathers, and a radix descent over that list
-// finds the composite.  Where the list is too long (many equal logits, a large k) the descent
-// runs over the whole row, with the histograms of all CTAs.
+// above as well, where they are few) go into a list that every CTA gathers and searches.  A
+// bin with too many is cut into 256 finer ones first; where even those hold too many (equal
+// logits), a radix descent runs over the whole row.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -39,116 +39,121 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRanges = kCtas * kWarps;   // a warp's part of the row
 constexpr int kTile = 128;       // a warp's step: four elements a lane
 constexpr uint32_t kKeyMasked = 0x007FFFFFu;   // radix_key(-inf)
+constexpr int kFine = 256;       // parts of such a bin
 constexpr int kOctaves = 44;     // below 2^-44 of the largest: no weight
-constexpr int kCut = kOctaves * 256;
-constexpr int kYBins = 1536;     // (D + 255) / 8 for D < kCut, three to a thread
-constexpr int kDigit = 10;       // bits of a descent's level
+constexpr int kCut = kOctaves * 64;
+constexpr int kYBins = 48 * 32;   // (d + 63) / 2 for d < kCut, 32 to an octave
+constexpr int kDigit = 9;        // bits of a descent's level
 constexpr int kBins = 1 << kDigit;
+constexpr int kSmallList = 256;  // searched by a thread per element
 constexpr int kIndexBits = 19;
 constexpr int kCompositeBits = 32 + kIndexBits;
 static_assert(IDX_MAX_VOCAB <= 1 << kIndexBits, "an index in a composite");
 
-// 2^(j / 256) in units of 2^-44: powers of 2^(1 / 256), multiplied up with 62 bits after the point.
+// 2^(j / 64) = t 2^-25 2^-off: 26 bits that a product with them loses nothing of, and what
+// they miss by.  Powers of 2^(1 / 64), multiplied up with 62 bits after the point.
+struct Exp2 {
+  int32_t t;
+  float off;
+};
 struct Exp2Table {
-  uint64_t v[256];
+  Exp2 v[64];
 };
 constexpr Exp2Table make_exp2_table() {
-  Exp2Table t{};
+  Exp2Table table{};
   unsigned __int128 x = static_cast<unsigned __int128>(1) << 62;
-  for (int j = 0; j < 256; ++j) {
-    t.v[j] = static_cast<uint64_t>((x + (1ull << 17)) >> 18);
-    x = (x * 0x402C6BE96AF2FB58ull + (1ull << 61)) >> 62;   // 2^(1 / 256)
+  for (int j = 0; j < 64; ++j) {
+    const uint64_t v = static_cast<uint64_t>(x), t = (v + (1ull << 36)) >> 37;
+    const double miss = static_cast<double>(static_cast<int64_t>((t << 37) - v)) / static_cast<double>(v);
+    table.v[j] = {static_cast<int32_t>(t), static_cast<float>(miss * 1.4426950408889634)};
+    x = (x * 0x40B268F9DE0183BAull + (1ull << 61)) >> 62;   // 2^(1 / 64)
   }
-  return t;
+  return table;
 }
 __device__ const Exp2Table kExp2 = make_exp2_table();
+constexpr int kColumns = 16;   // the table stands in 16 columns of two banks: a lane reads its own
 
-constexpr float kMagic = 49152.0f;   // 1.5 * 2^15: a sum's last bit is 1 / 256
+constexpr float kMagic = 196608.0f;   // 1.5 * 2^17: a sum's last bit is 1 / 64
 
-// How a row's logits become weights: exp(l / T) = 2^p with p = l c, c = log2(e) / T.
+// How a row's logits become weights: exp(l / T) = 2^p up to a factor of the row, with
+// p = (l - ref) c, c = log2(e) / T.  ref is 0 while p stays small enough for the second term
+// that its product has, else the largest logit: then every logit with a weight lies within
+// a factor of two of it, and the difference is exact.
 struct Row {
-  float top;          // the largest logit
-  float temperature;  // within 2^-60 .. 2^60
-  float c_hi, c_lo;   // c in two terms
-  float floor;        // of p: below it there is no weight
-  int32_t top_bits;   // p + kMagic of the largest
-  bool far;           // p would lose bits: differences to the largest are taken first
+  float top;            // the largest logit
+  float ref;
+  float temperature;    // within 2^-60 .. 2^60
+  float c_hi, c_lo;     // c in two terms
+  float floor;          // of p: below it there is no weight
+  int32_t top_bits;     // p + kMagic of the largest
+  uint64_t top_weight;
+  uint64_t least;       // of the weights that min-p keeps
 };
 
 // p in two terms for two logits; the first is cut at r.floor (NaN and -inf as well).
 __device__ __forceinline__ void exponents(float x0, float x1, const Row &r, uint64_t &p, uint64_t &lo) {
-  float p0, p1;
-  if (!r.far) {
-    const uint64_t x = pack2(x0, x1), c = pack2(r.c_hi, r.c_hi);
-    const uint64_t minus = mul2(x, pack2(-r.c_hi, -r.c_hi));
-    lo = fma2(x, pack2(r.c_lo, r.c_lo), fma2(x, c, minus));
-    p0 = fmaxf(-__uint_as_float(static_cast<uint32_t>(minus)), r.floor);
-    p1 = fmaxf(-__uint_as_float(static_cast<uint32_t>(minus >> 32)), r.floor);
-  } else {
-    float l[2], q[2];
-    const float v[2] = {x0, x1};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      // top - x = s + e exactly (Knuth's sum of two terms); an infinite top is no distance from itself
-      const bool same = v[i] == r.top;
-      const float s = same ? 0.0f : r.top - v[i], b = s - r.top, e = same ? 0.0f : (r.top - (s - b)) - (v[i] + b);
-      const float m = s * r.c_hi;
-      l[i] = -fmaf(e, r.c_hi, fmaf(s, r.c_lo, fmaf(s, r.c_hi, -m)));
-      q[i] = fmaxf(-m, r.floor);
-    }
-    p0 = q[0];
-    p1 = q[1];
-    lo = pack2(l[0], l[1]);
-  }
-  p = pack2(p0, p1);
+  const uint64_t x = fma2(pack2(x0, x1), pack2(1.0f, 1.0f), pack2(-r.ref, -r.ref)), c = pack2(r.c_hi, r.c_hi);
+  const uint64_t minus = mul2(x, pack2(-r.c_hi, -r.c_hi));
+  lo = fma2(x, pack2(r.c_lo, r.c_lo), fma2(x, c, minus));
+  p = pack2(fmaxf(-__uint_as_float(static_cast<uint32_t>(minus)), r.floor),
+            fmaxf(-__uint_as_float(static_cast<uint32_t>(minus >> 32)), r.floor));
 }
-// p in steps of 1 / 256 below the largest's, >= 0.
+// p in steps of 1 / 64 below the largest's, >= 0.
 __device__ __forceinline__ void steps(uint64_t p, const Row &r, uint64_t &t, int32_t (&d)[2]) {
   t = fma2(p, pack2(1.0f, 1.0f), pack2(kMagic, kMagic));
   d[0] = r.top_bits - static_cast<int32_t>(static_cast<uint32_t>(t));
   d[1] = r.top_bits - static_cast<int32_t>(static_cast<uint32_t>(t >> 32));
 }
 
-// Weights of two logits: 2^p is a power of two, a table entry of 8 bits and exp(g) - 1 of
-// the rest g, |g| <= 2^-9.5, whose leading bits are kept apart so that integers hold it to
-// 2^-40.  m: the weight before its shift by the power of two, 2^44 .. 2^45.  The last bit of
-// a weight stands for all below it (it is always set), so roundings have no direction.
+// The part of its bin that element i of a pair lies in, behind the bin: smaller above.
+__device__ __forceinline__ int32_t fine_code(uint64_t p, uint64_t t, int32_t d, int i) {
+  const float v = __uint_as_float(static_cast<uint32_t>(p >> (32 * i))), c = __uint_as_float(static_cast<uint32_t>(t >> (32 * i)));
+  const float f = v - (c - kMagic);   // exact, within 2^-7: 128 parts of a 64th
+  const int32_t part = min(max(static_cast<int32_t>((f + 0x1p-7f) * 0x1p13f), 0), kFine / 2 - 1);
+  return (d + 63) * (kFine / 2) + (kFine / 2 - 1 - part);
+}
+
+// Weights of two logits: 2^p is a power of two, a table entry of 6 bits and exp(g) - 1 of
+// the rest g, |g| <= 2^-7.5, whose leading term is kept apart so that integers hold it to
+// 2^-37.  m: 16 leading bits of a weight before its shift by the power of two.  The last bit
+// of a weight stands for all below it (it is always set), so roundings have no direction.
+// Measured against 64 bits: off by 2^-38.2 in the mean square, 2^-36.2 at most.
 struct Weights {
-  uint64_t w[2], m[2];
+  uint64_t w[2];
+  uint32_t m[2];
   int32_t d[2];
 };
-__device__ __forceinline__ void weights(float x0, float x1, const Row &r, const uint64_t *exp2_table, Weights &out) {
+__device__ __forceinline__ void weights(float x0, float x1, const Row &r, const Exp2 *table, Weights &out) {
   constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;
-  constexpr float kHead = 0x1.8p-3f;    // 1.5 * 2^-3: a sum's last bit is 2^-26
-  constexpr float kTail = 0x1.8p-17f;   // ... 2^-40
+  constexpr float kTail = 0x1.8p-14f;   // 1.5 * 2^-14: a sum's last bit is 2^-37
   uint64_t p, lo, t;
   exponents(x0, x1, r, p, lo);
   steps(p, r, t, out.d);
+  const Exp2 *const column = table + (threadIdx.x & (kColumns - 1));
+  const Exp2 e0 = column[(-out.d[0] & 63) * kColumns], e1 = column[(-out.d[1] & 63) * kColumns];
   const uint64_t one = pack2(1.0f, 1.0f), minus = pack2(-1.0f, -1.0f), ln2 = pack2(kLn2Hi, kLn2Hi);
-  // p less its 256ths and its second term, again in two terms
-  const uint64_t f0 = fma2(fma2(t, one, pack2(-kMagic, -kMagic)), minus, p), f = fma2(f0, one, lo);
-  const uint64_t fl = fma2(fma2(f, minus, f0), one, lo);
+  lo = pack2(__uint_as_float(static_cast<uint32_t>(lo)) - e0.off, __uint_as_float(static_cast<uint32_t>(lo >> 32)) - e1.off);
+  const uint64_t f = fma2(fma2(t, one, pack2(-kMagic, -kMagic)), minus, p);   // p less its 64ths
+  // exp((f + lo) ln 2) - 1 = h + q, with h + b = (f + lo) ln 2
   const uint64_t h = mul2(f, ln2);
-  const uint64_t hl = fma2(fl, ln2, fma2(f, pack2(kLn2Lo, kLn2Lo), fma2(f, ln2, mul2(h, minus))));
-  // exp(h + hl) - 1 = h + q
-  const uint64_t q = fma2(mul2(h, h), fma2(h, pack2(1.0f / 6.0f, 1.0f / 6.0f), pack2(0.5f, 0.5f)), hl);
-  const uint64_t head = fma2(h, one, pack2(kHead, kHead));
-  const uint64_t rest = fma2(fma2(head, one, pack2(-kHead, -kHead)), minus, h);
-  const uint64_t tail = fma2(fma2(q, one, rest), one, pack2(kTail, kTail));
+  const uint64_t b = fma2(lo, ln2, fma2(f, pack2(kLn2Lo, kLn2Lo), fma2(f, ln2, mul2(h, minus))));
+  const uint64_t g = fma2(h, one, b);
+  const uint64_t a = fma2(g, fma2(g, pack2(1.0f / 24.0f, 1.0f / 24.0f), pack2(1.0f / 6.0f, 1.0f / 6.0f)), pack2(0.5f, 0.5f));
+  const uint64_t tail = fma2(fma2(mul2(g, g), a, b), one, pack2(kTail, kTail));
+  const uint64_t head = mul2(h, pack2(0x1p37f, 0x1p37f));
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int32_t hb = static_cast<int32_t>(static_cast<uint32_t>(head >> (32 * i))) - __float_as_int(kHead);
-    const int32_t tb = static_cast<int32_t>(static_cast<uint32_t>(tail >> (32 * i))) - __float_as_int(kTail);
-    const int32_t g = (hb << 14) + tb;   // units of 2^-40
-    const uint64_t b = exp2_table[-out.d[i] & 255];
-    const uint64_t m = b + static_cast<uint64_t>((static_cast<int64_t>(static_cast<int32_t>(b >> 14)) * g) >> 26);
-    out.m[i] = m;
-    out.w[i] = out.d[i] < kCut ? m >> ((out.d[i] + 255) >> 8) | 1ull : 0ull;
+    const int32_t gi = __float2int_rn(__uint_as_float(static_cast<uint32_t>(head >> (32 * i)))) +
+                       (static_cast<int32_t>(static_cast<uint32_t>(tail >> (32 * i))) - __float_as_int(kTail));
+    const int32_t e = i == 0 ? e0.t : e1.t;
+    const uint64_t w = (static_cast<uint64_t>(static_cast<uint32_t>(e) << 5) << 32) + static_cast<uint64_t>(static_cast<int64_t>(e) * gi);
+    out.m[i] = static_cast<uint32_t>(w >> 47);
+    out.w[i] = out.d[i] < kCut ? w >> (((out.d[i] + 63) >> 6) + 18) | 1ull : 0ull;
   }
 }
-__device__ __forceinline__ uint64_t weight(float x, const Row &r, const uint64_t *exp2_table) {
+__device__ __noinline__ uint64_t weight(float x, const Row &r, const Exp2 *table) {   // one, where they are few
   Weights v;
-  weights(x, x, r, exp2_table, v);
+  weights(x, x, r, table, v);
   return v.w[0];
 }
 
@@ -162,6 +167,7 @@ struct Quad;
 template <>
 struct Quad<float> {
   using Vec = float4;
+  static __device__ __forceinline__ float one(float v) { return v; }
   static constexpr int kListMost = 1024;   // a list that lies beside the row
   static __device__ __forceinline__ void get(const Vec &v, float (&x)[4]) {
     x[0] = v.x;
@@ -169,12 +175,12 @@ struct Quad<float> {
     x[2] = v.z;
     x[3] = v.w;
   }
-  static __device__ __forceinline__ float one(float v) { return v; }
   static __device__ __forceinline__ float masked() { return -INFINITY; }
 };
 template <>
 struct Quad<uint16_t> {
   using Vec = uint2;
+  static __device__ __forceinline__ float one(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
   static constexpr int kListMost = 4096;   // bf16 rows are half as long, and their bins hold more equals
   static __device__ __forceinline__ void get(const Vec &v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x << 16);
@@ -182,7 +188,6 @@ struct Quad<uint16_t> {
     x[2] = __uint_as_float(v.y << 16);
     x[3] = __uint_as_float(v.y & 0xFFFF0000u);
   }
-  static __device__ __forceinline__ float one(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
   static __device__ __forceinline__ uint16_t masked() { return 0xFF80u; }
 };
 
@@ -191,14 +196,16 @@ template <typename T>
 struct Shared {
   static constexpr int kSegment = Quad<T>::kListMost / 16;   // candidates of a warp
   // the first CTA's: the row's parameters
-  float temperature, top_p, min_p, u;
+  float temperature, c_hi, c_lo, top_p, min_p, u;
   int32_t top_k, live;
   unsigned long long best;   // (key << 32) | ~index of the CTA's largest
   uint64_t all;              // its weights
-  uint64_t above, kept;      // its weights above the border's bin, those that min-p keeps of them
+  uint64_t above, kept;      // its weights (or elements) above the border's bin, the weights that min-p keeps of them
   uint64_t sum;              // its kept weights, where no list gave them
+  uint32_t octave[kYBins / 32];   // sums of the exponents' bins
   uint16_t count[kWarps];    // candidates
-  uint16_t segment[kWarps][kSegment];   // their places in the warp's range, ascending
+  T logit[kWarps][kSegment];           // they, and their places in the warp's range, by place
+  uint16_t place[kWarps][kSegment];
 };
 
 struct Found {
@@ -208,13 +215,14 @@ struct Found {
 // What a CTA uses alone.
 struct Scratch {
   uint64_t warp_sum[kWarps];
+  uint64_t octave[kYBins / 32], bin[32];
   Found found;
   uint32_t overflow;
   uint64_t composite;
 };
 
 // The sum over the threads before this one, and over all.
-__device__ __forceinline__ uint64_t exclusive_sum(uint64_t sum, Scratch &s, uint64_t &total) {
+__device__ __noinline__ uint64_t exclusive_sum(uint64_t sum, Scratch &s, uint64_t &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint64_t upto = sum;
 #pragma unroll
@@ -234,69 +242,86 @@ __device__ __forceinline__ uint64_t exclusive_sum(uint64_t sum, Scratch &s, uint
   return before + upto - sum;
 }
 
+__device__ __forceinline__ uint64_t warp_total(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// The sum of a value per warp, for one warp to call.
+__device__ __forceinline__ uint64_t warps_total(const uint64_t *v) {
+  return warp_total((threadIdx.x & 31) < kWarps ? v[threadIdx.x & 31] : 0);
+}
+
 // A row's outputs.  log(w / Z) from the logit itself, whose weight may be a few units, and
 // log1p of what the others weigh beside the largest.
-__device__ void finish(const SampleArgs &a, int64_t row, int token, float x, uint64_t total, uint64_t top_weight, const Row &r) {
+__device__ __noinline__ void finish(const SampleArgs &a, int64_t row, int token, float x, uint64_t total, const Row &r) {
   a.token[row] = token;
   if (a.logprob == nullptr) return;
-  const double y = x == r.top ? 0.0 : (static_cast<double>(r.top) - static_cast<double>(x)) / r.temperature;
-  const double z = static_cast<double>(total - top_weight) / static_cast<double>(top_weight);
-  a.logprob[row] = 0.0f - static_cast<float>(y) - log1pf(static_cast<float>(z));
+  const float y = x == r.top ? 0.0f : (r.top - x) / r.temperature;
+  const float z = static_cast<float>(total - r.top_weight) / static_cast<float>(r.top_weight);
+  a.logprob[row] = 0.0f - y - log1pf(z);
 }
 
 // The element of this CTA's part of the row at which the kept weights pass `at`: the range,
 // its step of a warp, the lane.  reach: the weights before the CTA's.  All its threads call.
 template <typename T>
-__device__ void pick(const SampleArgs &a, int64_t row, const T *data, int len, int rank, const uint64_t *warp_kept, uint64_t reach,
-                     uint64_t at, uint64_t threshold, uint64_t least, uint64_t total, uint64_t top_weight, const Row &r,
-                     const uint64_t *table, uint64_t *tile_sum) {
+__device__ __noinline__ void pick(const SampleArgs &a, int64_t row, const T *data, int rank, const uint64_t *warp_kept, uint64_t reach,
+                                  uint64_t at, uint64_t threshold, uint64_t total, const Row &r, const Exp2 *table, uint64_t *tile_sum) {
   using Q = Quad<T>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, len = a.warp_len, tiles = len / kTile;
   int range = 0;
   while (range < kWarps - 1 && at >= reach + warp_kept[range]) reach += warp_kept[range++];
   const int base = (rank * kWarps + range) * len;
-  const auto tile = [&](int t, float (&x)[4], uint64_t (&w)[4]) {
-    Q::get(*reinterpret_cast<const typename Q::Vec *>(data + range * len + t * kTile + 4 * lane), x);
-    uint64_t sum = 0;
+  int chosen = -1;
+  // first the sums of all steps, then again the one that has it
+#pragma unroll 1
+  for (int t = warp;;) {
+    float x[4];
+    uint64_t w[4], sum = 0;
+    if (t < tiles) {
+      Q::get(*reinterpret_cast<const typename Q::Vec *>(data + range * len + t * kTile + 4 * lane), x);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      Weights v;
-      weights(x[2 * h], x[2 * h + 1], r, table, v);
+      for (int h = 0; h < 2; ++h) {
+        Weights v;
+        weights(x[2 * h], x[2 * h + 1], r, table, v);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int k = 2 * h + i;
-        w[k] = v.w[i] >= least && composite(x[k], base + t * kTile + 4 * lane + k) >= threshold ? v.w[i] : 0;
-        sum += w[k];
+        for (int i = 0; i < 2; ++i) {
+          const int k = 2 * h + i;
+          w[k] = v.w[i] >= r.least && composite(x[k], base + t * kTile + 4 * lane + k) >= threshold ? v.w[i] : 0;
+          sum += w[k];
+        }
       }
     }
-    return sum;
-  };
-  const int tiles = len / kTile;
-  for (int t = warp; t < tiles; t += kWarps) {
-    float x[4];
-    uint64_t w[4], sum = tile(t, x, w);
+    if (chosen < 0 && t < tiles) {
+      sum = warp_total(sum);
+      if (lane == 0) tile_sum[t] = sum;
+      t += kWarps;
+      continue;
+    }
+    if (chosen < 0) {
+      __syncthreads();
+      chosen = 0;
+      while (chosen < tiles - 1 && at >= reach + tile_sum[chosen]) reach += tile_sum[chosen++];
+      if (chosen % kWarps != warp) return;
+      t = chosen;
+      continue;
+    }
+    uint64_t upto = sum;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) tile_sum[t] = sum;
-  }
-  __syncthreads();
-  int t = 0;
-  while (t < tiles - 1 && at >= reach + tile_sum[t]) reach += tile_sum[t++];
-  if (t % kWarps != warp) return;
-  float x[4];
-  uint64_t w[4];
-  const uint64_t sum = tile(t, x, w);
-  uint64_t upto = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += up;
+    }
+    uint64_t from = reach + upto - sum;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += up;
-  }
-  uint64_t from = reach + upto - sum;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (at >= from && at < from + w[k]) finish(a, row, base + t * kTile + 4 * lane + k, x[k], total, top_weight, r);
-    from += w[k];
+    for (int k = 0; k < 4; ++k) {
+      if (at >= from && at < from + w[k]) {
+        finish(a, row, base + t * kTile + 4 * lane + k, x[k], total, r);
+        return;
+      }
+      from += w[k];
+    }
+    return;
   }
 }
 
@@ -315,72 +340,102 @@ __device__ __forceinline__ void add_to_hist(uint32_t *hist, uint32_t bin, uint64
   if (hi != 0) atomicAdd(&hist[kBins + bin], hi);
 }
 
-// The bin of a descent's level, from the top, at which the running sum reaches want(total)
-// (1 .. total).  One histogram, or those of all CTAs.  kMass: 64-bit sums in two words.
-template <bool kMass, bool kAll, typename F>
-__device__ __forceinline__ Found find_bin(uint32_t *hist, Scratch &s, F want) {
-  constexpr int kPer = kBins / kThreads;
-  static_assert(kPer == 2, "a thread's bins are one vector");
-  const int first = kBins - kPer * (static_cast<int>(threadIdx.x) + 1);
-  uint64_t own[kPer] = {}, total;
-#pragma unroll
-  for (int c = 0; c < (kAll ? kCtas : 1); ++c) {
-    const uint32_t *const h = kAll ? cg::this_cluster().map_shared_rank(hist, c) : hist;
-    const uint2 lo = *reinterpret_cast<const uint2 *>(h + first);
-    own[0] += lo.x;
-    own[1] += lo.y;
-    if constexpr (kMass) {
-      const uint2 hi = *reinterpret_cast<const uint2 *>(h + kBins + first);
-      own[0] += static_cast<uint64_t>(hi.x) << 32;
-      own[1] += static_cast<uint64_t>(hi.y) << 32;
-    }
+// The bin of a descent's level, from the top, at which the running sum reaches `want`
+// (1 .. the sum of all; bin kBins where none does).  One histogram, or those of all CTAs;
+// mass: 64-bit sums in two words.
+__device__ __noinline__ Found find_bin(bool mass, int ctas, uint32_t *hist, Scratch &s, uint64_t want) {
+  static_assert(kBins == kThreads, "a bin a thread");
+  const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
+  uint64_t own = 0, total;
+  if (threadIdx.x == 0) s.found = {kBins, 0, 0};
+#pragma unroll 1
+  for (int c = 0; c < ctas; ++c) {
+    const uint32_t *const h = ctas > 1 ? cg::this_cluster().map_shared_rank(hist, c) : hist;
+    own += h[bin];
+    if (mass) own += static_cast<uint64_t>(h[kBins + bin]) << 32;
   }
-  uint64_t above = exclusive_sum(own[0] + own[1], s, total);
-  const uint64_t w = want(total);
-#pragma unroll
-  for (int i = kPer - 1; i >= 0; --i) {
-    if (above < w && w <= above + own[i]) s.found = {static_cast<uint32_t>(first + i), above, own[i]};
-    above += own[i];
-  }
+  const uint64_t above = exclusive_sum(own, s, total);
+  if (above < want && want <= above + own) s.found = {static_cast<uint32_t>(bin), above, own};
   __syncthreads();
   return s.found;
 }
 
+// The octaves' sums of this CTA's bins of exponents, before find_exponent's barrier.
+__device__ __forceinline__ void sum_octaves(const uint32_t *hist, uint32_t *octave) {
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = warp; o < kYBins / 32; o += kWarps) {
+    const uint32_t v = __reduce_add_sync(0xffffffffu, hist[o * 32 + lane]);
+    if (lane == 0) octave[o] = v;
+  }
+}
+
+// Of 32 values, one a lane, the first at which the running sum reaches `want` (the last that
+// is not 0 if none does), the sum before it and its own; `all`: of all.
+struct Reached {
+  int at;
+  uint64_t before, own, all;
+};
+__device__ __forceinline__ Reached reach_in_warp(uint64_t v, uint64_t want) {
+  const int lane = threadIdx.x & 31;
+  uint64_t upto = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += up;
+  }
+  const uint32_t there = __ballot_sync(0xffffffffu, upto >= want), some = __ballot_sync(0xffffffffu, v != 0);
+  Reached r;
+  r.at = there != 0 ? __ffs(there) - 1 : some != 0 ? 31 - __clz(some) : 31;
+  r.before = __shfl_sync(0xffffffffu, upto - v, r.at);
+  r.own = __shfl_sync(0xffffffffu, v, r.at);
+  r.all = __shfl_sync(0xffffffffu, upto, 31);
+  return r;
+}
+
 // The bin of exponents, from the largest, at which the running sum over all CTAs reaches
-// want(total); bin kYBins where none does.  kMass: sums of weights' 16 leading bits.
-template <bool kMass, typename F>
-__device__ __forceinline__ Found find_exponent(uint32_t *hist, Scratch &s, F want) {
-  constexpr int kPer = kYBins / kThreads;
-  const int first = kPer * static_cast<int>(threadIdx.x);
-  uint64_t own[kPer] = {}, sum = 0, total;
+// `want`, and the sum of all: first the octave, then its bin, so that a thread reads two words
+// of another CTA.  mass: sums of weights' 16 leading bits, which may end a little short.
+__device__ __noinline__ int find_exponent(bool mass, const uint32_t *hist, const uint32_t *octave, Scratch &s, uint64_t want, uint64_t &total) {
+  constexpr int kOct = kYBins / 32;
+  static_assert(kOct * kCtas <= kThreads && kOct <= 64, "a word a thread");
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < kOct * kCtas) {
+    const int o = tid / kCtas;
+    uint64_t v = cg::this_cluster().map_shared_rank(octave, tid % kCtas)[o];
 #pragma unroll
-  for (int c = 0; c < kCtas; ++c) {
-    const uint32_t *const h = cg::this_cluster().map_shared_rank(hist, c);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) own[i] += h[first + i];
-  }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (kMass) own[i] = own[i] << 29 >> ((first + i) >> 5);
-    sum += own[i];
-  }
-  if (threadIdx.x == 0) s.found = {kYBins, 0, 0};
-  uint64_t above = exclusive_sum(sum, s, total);
-  const uint64_t w = want(total);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (above < w && w <= above + own[i]) s.found = {static_cast<uint32_t>(first + i), above, own[i]};
-    above += own[i];
+    for (int k = kCtas / 2; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+    if (tid % kCtas == 0) s.octave[o] = mass ? v << 29 >> o : v;
   }
   __syncthreads();
-  return s.found;
+  Reached r = reach_in_warp(s.octave[lane], want);
+  total = r.all;
+  int o = r.at;
+  {
+    const uint64_t v = lane < kOct - 32 ? s.octave[32 + lane] : 0;
+    Reached far = reach_in_warp(v, want > r.all ? want - r.all : 0);
+    total += far.all;
+    if (r.all < want && far.all != 0) {
+      o = 32 + far.at;
+      far.before += r.all;
+      r = far;
+    }
+  }
+  if (tid < 32 * kCtas) {
+    uint64_t v = cg::this_cluster().map_shared_rank(hist, tid % kCtas)[o * 32 + tid / kCtas];
+#pragma unroll
+    for (int k = kCtas / 2; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+    if (tid % kCtas == 0) s.bin[tid / kCtas] = mass ? v << 29 >> o : v;
+  }
+  __syncthreads();
+  return o * 32 + reach_in_warp(s.bin[lane], want > r.before ? want - r.before : 0).at;
 }
 
 // The composite in list[0 .. n) at which the running sum, from the largest, over those >= low
 // reaches want: of ones, or of weights.  The CTA alone.
-template <bool kMass>
-__device__ uint64_t descend_list(const uint64_t *list, int n, uint64_t low, uint64_t want, const Row &r,
-                                 const uint64_t *table, uint32_t *hist, Scratch &s) {
+__device__ __noinline__ uint64_t descend_list(bool mass, const uint64_t *list, int n, uint64_t low, uint64_t want, const Row &r,
+                                 const Exp2 *table, uint32_t *hist, Scratch &s) {
   // the bits in which they differ
   if (threadIdx.x == 0) s.composite = 0;
   __syncthreads();
@@ -403,10 +458,10 @@ __device__ uint64_t descend_list(const uint64_t *list, int n, uint64_t low, uint
       if (c < low || c >> known != prefix) continue;
       const uint32_t bin = static_cast<uint32_t>(c >> shift) & ((1u << bits) - 1);
       atomicAdd(&hist[2 * kBins + bin], 1u);
-      if constexpr (kMass) add_to_hist(hist, bin, weight(radix_key_value(static_cast<uint32_t>(c >> kIndexBits)), r, table));
+      if (mass) add_to_hist(hist, bin, weight(radix_key_value(static_cast<uint32_t>(c >> kIndexBits)), r, table));
     }
     __syncthreads();
-    const Found f = find_bin<kMass, false>(kMass ? hist : hist + 2 * kBins, s, [&](uint64_t) { return want; });
+    const Found f = find_bin(mass, 1, mass ? hist : hist + 2 * kBins, s, want);
     prefix = prefix << bits | f.bin;
     want -= f.above;
     if (shift > 0 && hist[2 * kBins + f.bin] == 1) {   // one left: its other bits from the list
@@ -421,7 +476,7 @@ __device__ uint64_t descend_list(const uint64_t *list, int n, uint64_t low, uint
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
   using Q = Quad<T>;
   using Vec = typename Q::Vec;
   using Pub = Shared<T>;
@@ -432,13 +487,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   T *const data = reinterpret_cast<T *>(list + kListMost);
   __shared__ Pub mine;
   __shared__ Scratch s;
-  __shared__ uint64_t table[256];
+  __shared__ Row r;
+  __shared__ __align__(8) Exp2 table[64 * kColumns];
   __shared__ unsigned long long warp_best[kWarps];
   __shared__ uint64_t warp_kept[kWarps], warp_above[kWarps];
   __shared__ uint64_t range_at[kRanges + 1], cta_above[kCtas], cta_kept[kCtas];
   __shared__ int32_t list_at[kRanges + 1];
   __shared__ uint64_t tile_sum[2 * kWarps];
-  static_assert(kYBins <= 3 * kBins && kThreads * sizeof(uint64_t) <= 3 * kBins * sizeof(uint32_t), "what hist holds by turns");
+  static_assert(kYBins <= 3 * kBins && kThreads * sizeof(uint64_t) <= 3 * kBins * sizeof(uint32_t) && kFine <= kBins, "what hist holds by turns");
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
@@ -450,11 +506,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   T *const own = data + warp * len;
   const T *const src = static_cast<const T *>(a.p.logits) + row * a.p.ld;
 
-  for (int i = tid; i < 256; i += kThreads) table[i] = kExp2.v[i];
+  for (int i = tid; i < 64 * kColumns; i += kThreads) table[i] = kExp2.v[i / kColumns];
   clear_hist(hist);
   if (rank == 0 && tid == 0) {
     mine.live = a.p.rows == nullptr || row < *a.p.rows;
     mine.temperature = a.p.temperature != nullptr ? a.p.temperature[row] : 1.0f;
+    const double c = 1.4426950408889634 / static_cast<double>(fminf(fmaxf(mine.temperature, 0x1p-60f), 0x1p60f));
+    mine.c_hi = static_cast<float>(c);
+    mine.c_lo = static_cast<float>(c - static_cast<double>(mine.c_hi));
     mine.top_k = a.p.top_k != nullptr ? a.p.top_k[row] : 0;
     mine.top_p = a.p.top_p != nullptr ? a.p.top_p[row] : 1.0f;
     mine.min_p = a.p.min_p != nullptr ? a.p.min_p[row] : 0.0f;
@@ -502,9 +561,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
   if (lane == 0) warp_best[warp] = best;
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) best = warp_best[w] > best ? warp_best[w] : best;
-    mine.best = best;
+  if (warp == 0) {
+    best = warp_best[lane & (kWarps - 1)];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
+      const unsigned long long b = __shfl_xor_sync(0xffffffffu, best, o);
+      best = b > best ? b : best;
+    }
+    if (lane == 0) mine.best = best;
   }
   cluster.sync();
   best = 0;
@@ -531,296 +595,377 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     return;
   }
 
-  Row r;
-  r.top = radix_key_value(top_key);
-  r.temperature = fminf(fmaxf(temperature, 0x1p-60f), 0x1p60f);
-  {
-    const double c = 1.4426950408889634 / static_cast<double>(r.temperature);
-    r.c_hi = static_cast<float>(c);
-    r.c_lo = static_cast<float>(c - static_cast<double>(r.c_hi));
-    // p keeps 2^-39 up to 2^10: the rounding of its second term is 2^-48 of it
-    r.far = !(fabsf(r.top * r.c_hi) <= 1024.0f);
-    r.floor = -INFINITY;
+  if (warp == 0) {   // every lane the same
+    Row v;
+    v.top = radix_key_value(top_key);
+    if (v.top == INFINITY) v.top = 0.0f;   // see below
+    v.temperature = fminf(fmaxf(temperature, 0x1p-60f), 0x1p60f);
+    v.c_hi = params->c_hi;
+    v.c_lo = params->c_lo;
+    v.ref = fabsf(v.top * v.c_hi) <= 128.0f ? 0.0f : v.top;
+    v.floor = -INFINITY;
+    v.top_bits = 0;
     uint64_t p, lo, t;
     int32_t d[2];
-    exponents(r.top, r.top, r, p, lo);
-    r.top_bits = 0;
-    steps(p, r, t, d);
-    r.top_bits = -d[0];
-    r.floor = __uint_as_float(static_cast<uint32_t>(p)) - 64.0f;
+    exponents(v.top, v.top, v, p, lo);
+    steps(p, v, t, d);
+    v.top_bits = -d[0];
+    v.floor = __uint_as_float(static_cast<uint32_t>(p)) - 64.0f;
+    v.least = 1;
+    r = v;
+    __syncwarp();
+    v.top_weight = weight(v.top, r, table);
+    if (min_p > 0.0f) {
+      const uint64_t f = static_cast<uint64_t>(fminf(min_p, 1.0f) * 0x1p63f);
+      const uint64_t hi = __umul64hi(f, v.top_weight), lw = f * v.top_weight;
+      v.least = (hi << 1 | lw >> 63) + (lw << 1 != 0 || f == 0 ? 1 : 0);
+    }
+    __syncwarp();
+    r = v;
   }
-  const uint64_t top_weight = weight(r.top, r, table);
-  uint64_t least = 1;   // of the weights that min-p keeps
-  if (min_p > 0.0f) {
-    const uint64_t f = static_cast<uint64_t>(fminf(min_p, 1.0f) * 0x1p63f);
-    const uint64_t hi = __umul64hi(f, top_weight), lo = f * top_weight;
-    least = (hi << 1 | lo >> 63) + (lo << 1 != 0 || f == 0 ? 1 : 0);
+  if (radix_key_value(top_key) == INFINITY) {   // those at +inf alone have a weight, the same
+    for (int t = lane; t < len; t += 32) {
+      const bool is = Q::one(own[t]) == INFINITY;
+      own[t] = is ? static_cast<T>(0) : Q::masked();
+    }
   }
+  __syncthreads();
 
+  const Row local = r;   // in registers, for the loops over the row
   // f(tile, x[4]) over this warp's elements
   const auto each_tile = [&](auto f) {
+#pragma unroll 1
     for (int t = 0; t < len; t += kTile) {
       float x[4];
       Q::get(*reinterpret_cast<const Vec *>(own + t + 4 * lane), x);
       f(t, x);
     }
   };
-
+  const uint64_t f_u = u > 0.0f ? (u < 1.0f ? static_cast<uint64_t>(u * 0x1p64f) : ~0ull) : 0ull;
   uint64_t threshold = 0;   // composite of the last kept element
-  uint64_t mass = 0;        // what top-p's border lies at
-  bool count = top_k > 0 && top_k < a.p.V, whole = false;
-  bool filter = count || top_p < 1.0f;
-  Found y{kYBins, 0, 0};
-  if (count) {
-    each_tile([&](int, const float (&x)[4]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint64_t p, lo, t;
-        int32_t d[2];
-        exponents(x[2 * h], x[2 * h + 1], r, p, lo);
-        steps(p, r, t, d);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (d[i] < kCut) atomicAdd(&hist[(d[i] + 255) >> 3], 1u);
-      }
-    });
-    cluster.sync();
-    y = find_exponent<false>(hist, s, [&](uint64_t total) {
-      if (total <= static_cast<uint64_t>(top_k)) count = false;   // all that have a weight
-      return static_cast<uint64_t>(top_k);
-    });
-    if (!count) {
-      filter = top_p < 1.0f;
-      cluster.sync();   // nobody reads the histogram any more
-      clear_hist(hist);
-      __syncthreads();
-    }
-  }
-  if (filter && !count) {
-    uint64_t sum = 0;
-    each_tile([&](int, const float (&x)[4]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        Weights v;
-        weights(x[2 * h], x[2 * h + 1], r, table, v);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          sum += v.w[i];
-          if (v.d[i] < kCut) atomicAdd(&hist[(v.d[i] + 255) >> 3], static_cast<uint32_t>(v.m[i] >> 29) | 1u);
-        }
-      }
-    });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) warp_above[warp] = sum;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kWarps; ++w) sum += warp_above[w];
-      mine.all = sum;
-    }
-    cluster.sync();
-    uint64_t z = 0;
-#pragma unroll
-    for (int c = 0; c < kCtas; ++c) z += cluster.map_shared_rank(&mine, c)->all;
-    mass = ceil_product(top_p, z);
-    y = find_exponent<true>(hist, s, [&](uint64_t) { return mass; });
-  }
 
-  if (filter) {
-    // candidates of the border in order of their index; the exact weights above its bin
-    const int32_t bin = static_cast<int32_t>(y.bin);
-    uint64_t above = 0, kept = 0;
-    int32_t n = 0;
-    each_tile([&](int t, const float (&x)[4]) {
-      int32_t d[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint64_t p, lo, b;
-        int32_t e[2];
-        exponents(x[2 * h], x[2 * h + 1], r, p, lo);
-        steps(p, r, b, e);
-        d[2 * h] = (e[0] + 255) >> 3;
-        d[2 * h + 1] = (e[1] + 255) >> 3;
-      }
-      uint32_t take = 0;
-      bool over = false;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (d[k] == bin || (count && d[k] < bin)) take |= 1u << k;
-        over = over || d[k] < bin;
-      }
-      if (!count && __any_sync(0xffffffffu, over)) {
+  // top-k's border, then top-p's among what top-k keeps
+  for (int kind = top_k > 0 && top_k < a.p.V ? 0 : 1; kind < (top_p < 1.0f ? 2 : 1); ++kind) {
+    const bool mass = kind == 1;
+    const uint64_t low = threshold;
+    uint64_t sum = 0;
+    if (mass) {
+      each_tile([&](int t, const float (&x)[4]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           Weights v;
-          weights(x[2 * h], x[2 * h + 1], r, table, v);
+          weights(x[2 * h], x[2 * h + 1], local, table, v);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (d[2 * h + i] < bin) {
-              above += v.w[i];
-              kept += v.w[i] >= least ? v.w[i] : 0;
+            if (v.d[i] < kCut && (low == 0 || composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) >= low)) {
+              sum += v.w[i];
+              atomicAdd(&hist[(v.d[i] + 63) >> 1], v.m[i] | 1u);
             }
           }
         }
-      }
-      if (__any_sync(0xffffffffu, take != 0)) {
-        const int32_t here = __popc(take);
-        int32_t upto = here;
+      });
+      sum = warp_total(sum);
+      if (lane == 0) warp_above[warp] = sum;
+    } else {
+      each_tile([&](int, const float (&x)[4]) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int32_t up = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += up;
+        for (int h = 0; h < 2; ++h) {
+          uint64_t p, lo, t;
+          int32_t d[2];
+          exponents(x[2 * h], x[2 * h + 1], local, p, lo);
+          steps(p, local, t, d);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (d[i] < kCut) atomicAdd(&hist[(d[i] + 63) >> 1], 1u);
         }
-        int32_t at = n + upto - here;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (take >> k & 1) {
-            if (at < Pub::kSegment) mine.segment[warp][at] = static_cast<uint16_t>(t + 4 * lane + k);
-            ++at;
-          }
-        }
-        n += __shfl_sync(0xffffffffu, upto, 31);
-      }
-    });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      above += __shfl_xor_sync(0xffffffffu, above, o);
-      kept += __shfl_xor_sync(0xffffffffu, kept, o);
+      });
     }
-    if (lane == 0) {
-      warp_above[warp] = above;
-      warp_kept[warp] = kept;
-      mine.count[warp] = static_cast<uint16_t>(n);   // at most the warp's range
-    }
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kWarps; ++w) {
-        above += warp_above[w];
-        kept += warp_kept[w];
-      }
-      mine.above = above;
-      mine.kept = kept;
+    sum_octaves(hist, mine.octave);
+    if (mass && warp == 0) {
+      sum = warps_total(warp_above);
+      if (lane == 0) mine.all = sum;
     }
     cluster.sync();
+    uint64_t want = static_cast<uint64_t>(top_k), total;
+    if (mass) {
+      uint64_t z = 0;
+#pragma unroll
+      for (int c = 0; c < kCtas; ++c) z += cluster.map_shared_rank(&mine, c)->all;
+      want = ceil_product(top_p, z);
+    }
+    const int32_t border = find_exponent(mass, hist, mine.octave, s, want, total);
+    if (!mass && total <= want) {   // all that have a weight are kept
+      cluster.sync();               // nobody reads the histogram any more
+      clear_hist(hist);
+      __syncthreads();
+      continue;
+    }
 
-    // the list: places of the ranges, then the elements
-    if (tid < kCtas) {
-      cta_above[tid] = cluster.map_shared_rank(&mine, tid)->above;
-      cta_kept[tid] = cluster.map_shared_rank(&mine, tid)->kept;
+    // Candidates in order of their index, and exactly what lies above them: of the border's
+    // bin, or of its part `fine`; in the first round for top-k all from the top.
+    int32_t fine = -1, n = 0;
+    bool listed = false, from_top = false;
+    uint64_t over = 0;   // what lies above the candidates in all CTAs
+    for (int round = 0; round < 2; ++round) {
+      from_top = !mass && round == 0;
+      uint64_t above = 0, kept = 0;
+      n = 0;
+      each_tile([&](int t, const float (&x)[4]) {
+        int32_t code[4];   // the bin, and its part in the second round: smaller above
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint64_t p, lo, b;
+          int32_t d[2];
+          exponents(x[2 * h], x[2 * h + 1], local, p, lo);
+          steps(p, local, b, d);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            code[2 * h + i] = (d[i] + 63) >> 1;
+            if (round == 1) code[2 * h + i] = fine_code(p, b, d[i], i);
+          }
+        }
+        const int32_t at_border = round == 0 ? border : border * kFine + fine;
+        uint32_t take = 0, higher = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          take |= static_cast<uint32_t>(code[k] == at_border) << k;
+          higher |= static_cast<uint32_t>(code[k] < at_border) << k;
+        }
+        if (!mass) {
+          above += __popc(higher);
+          if (from_top) take |= higher;
+        } else if (__any_sync(0xffffffffu, higher != 0)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            Weights v;
+            weights(x[2 * h], x[2 * h + 1], local, table, v);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (higher >> (2 * h + i) & 1) {
+                above += v.w[i];
+                kept += v.w[i] >= local.least ? v.w[i] : 0;
+              }
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, take != 0)) {
+          const int32_t here = __popc(take);
+          int32_t upto = here;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int32_t up = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += up;
+          }
+          int32_t at = n + upto - here;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (take >> k & 1) {
+              if (at < Pub::kSegment) {
+                mine.logit[warp][at] = own[t + 4 * lane + k];
+                mine.place[warp][at] = static_cast<uint16_t>(t + 4 * lane + k);
+              }
+              ++at;
+            }
+          }
+          n += __shfl_sync(0xffffffffu, upto, 31);
+        }
+      });
+      above = warp_total(above);
+      kept = warp_total(kept);
+      if (lane == 0) {
+        warp_above[warp] = above;
+        warp_kept[warp] = kept;
+        mine.count[warp] = static_cast<uint16_t>(n);   // at most the warp's range
+      }
+      __syncthreads();
+      if (warp == 0) {
+        above = warps_total(warp_above);
+        kept = warps_total(warp_kept);
+        if (lane == 0) {
+          mine.above = above;
+          mine.kept = kept;
+          s.overflow = 0;
+        }
+      }
+      cluster.sync();
+
+      // the list's length, the places of the ranges in it, the sums of all
+      if (tid < kCtas) {
+        cta_above[tid] = cluster.map_shared_rank(&mine, tid)->above;
+        cta_kept[tid] = cluster.map_shared_rank(&mine, tid)->kept;
+      }
+      {
+        const int32_t c = tid < kRanges ? cluster.map_shared_rank(&mine, tid / kWarps)->count[tid % kWarps] : 0;
+        if (c > Pub::kSegment) s.overflow = 1;
+        uint64_t all;
+        const uint64_t before = exclusive_sum(static_cast<uint64_t>(c), s, all);
+        if (tid <= kRanges) list_at[tid] = static_cast<int32_t>(before);
+        n = static_cast<int32_t>(all);
+      }
+      __syncthreads();
+      over = 0;
+#pragma unroll
+      for (int c = 0; c < kCtas; ++c) over += cta_above[c];
+      listed = n > 0 && n <= kListMost && s.overflow == 0;
+      if (from_top && listed) over = 0;   // they are in the list themselves
+      if (listed || round == 1 || over >= want) break;
+
+      // too many: the bin's parts
+      clear_hist(hist);
+      __syncthreads();
+      each_tile([&](int t, const float (&x)[4]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint64_t p, lo, b;
+          int32_t d[2];
+          exponents(x[2 * h], x[2 * h + 1], local, p, lo);
+          steps(p, local, b, d);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if ((d[i] + 63) >> 1 != border) continue;
+            if (low != 0 && composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) < low) continue;
+            const uint32_t bin = kBins - 1 - fine_code(p, b, d[i], i) % kFine;
+            if (mass) add_to_hist(hist, bin, weight(x[2 * h + i], r, table));
+            else atomicAdd(&hist[bin], 1u);
+          }
+        }
+      });
+      cluster.sync();
+      const Found f = find_bin(mass, kCtas, hist, s, want - over);
+      if (f.bin == kBins) break;   // the leading bits had missed the bin
+      fine = kBins - 1 - static_cast<int32_t>(f.bin);
     }
-    if (tid == 0) s.overflow = 0;
-    __syncthreads();
-    uint64_t listed;
-    {
-      const int32_t c = tid < kRanges ? cluster.map_shared_rank(&mine, tid / kWarps)->count[tid % kWarps] : 0;
-      if (c > Pub::kSegment) s.overflow = 1;
-      const uint64_t before = exclusive_sum(static_cast<uint64_t>(c), s, listed);
-      if (tid <= kRanges) list_at[tid] = static_cast<int32_t>(before);
-    }
-    __syncthreads();
-    n = static_cast<int32_t>(listed);
-    whole = n == 0 || n > kListMost || s.overflow != 0;
-    bool reading = false;   // the end of the barrier behind the last remote read is still to come
-    if (!whole) {
+
+    bool reading = false;   // a barrier behind the last read from other CTAs has begun
+    if (listed) {
       for (int i = tid; i < n; i += kThreads) {
         int w = 0;
 #pragma unroll
         for (int step = kRanges / 2; step > 0; step >>= 1)
           if (list_at[w + step] <= i) w += step;
-        const int c = w / kWarps, at = cluster.map_shared_rank(&mine, c)->segment[w % kWarps][i - list_at[w]];
-        const float x = Q::one(cluster.map_shared_rank(data, c)[(w % kWarps) * len + at]);
-        list[i] = composite(x, w * len + at);
+        const Pub *const from = cluster.map_shared_rank(&mine, w / kWarps);
+        const int k = i - list_at[w];
+        list[i] = composite(Q::one(from->logit[w % kWarps][k]), w * len + from->place[w % kWarps][k]);
       }
-      cluster.barrier_arrive();
-      reading = true;
+      if (mass || from_top) {   // what follows needs no other CTA
+        cluster.barrier_arrive();
+        reading = true;
+        if (from_top && rank != 0) {   // everything that is kept is in the first CTA's list as well
+          cluster.barrier_wait();
+          return;
+        }
+      }
       __syncthreads();
       const auto list_weight = [&](int i) { return weight(radix_key_value(static_cast<uint32_t>(list[i] >> kIndexBits)), r, table); };
-      const auto list_mass = [&](uint64_t low) {
-        uint64_t sum = 0, total;
-        for (int i = tid; i < n; i += kThreads) sum += list[i] >= low ? list_weight(i) : 0;
-        exclusive_sum(sum, s, total);
-        __syncthreads();
-        return total;
+      const auto kept_weight = [&](int i) {   // behind the search
+        const uint64_t v = list[i] >= threshold ? list_weight(i) : 0;
+        return v >= local.least ? v : 0;
       };
-      if (count) {
-        if (rank != 0) {   // everything that is kept is in the first CTA's list as well
-          cluster.barrier_wait();
-          return;
-        }
-        threshold = descend_list<false>(list, n, 0, static_cast<uint64_t>(top_k), r, table, hist, s);
-        if (top_p < 1.0f) {
-          const uint64_t z = list_mass(threshold);
-          threshold = descend_list<true>(list, n, threshold, ceil_product(top_p, z), r, table, hist, s);
-        }
-      } else {
-        uint64_t over = 0;
-#pragma unroll
-        for (int c = 0; c < kCtas; ++c) over += cta_above[c];
-        // the leading bits of the weights may have missed the bin
-        if (over < mass && mass <= over + list_mass(0)) threshold = descend_list<true>(list, n, 0, mass - over, r, table, hist, s);
-        else whole = true;
-      }
-      if (!whole) {
-        // kept weights of the list: each thread's part of it, and up to each range
-        uint64_t sum = 0, total, w[kChunk];
-#pragma unroll
-        for (int k = 0; k < kChunk; ++k) {
-          const int i = tid * kChunk + k;
-          w[k] = 0;
-          if (i < n && list[i] >= threshold) w[k] = list_weight(i);
-          if (w[k] < least) w[k] = 0;
-          sum += w[k];
-        }
-        uint64_t before = exclusive_sum(sum, s, total);
-        const uint64_t f = u > 0.0f ? (u < 1.0f ? static_cast<uint64_t>(u * 0x1p64f) : ~0ull) : 0ull;
-        if (count) {
-          const uint64_t at = __umul64hi(f, total);
-#pragma unroll
-          for (int k = 0; k < kChunk; ++k) {
-            if (at >= before && at < before + w[k]) {
-              const uint64_t c = list[tid * kChunk + k];
-              finish(a, row, (1 << kIndexBits) - 1 - static_cast<int>(c & ((1u << kIndexBits) - 1)),
-                     radix_key_value(static_cast<uint32_t>(c >> kIndexBits)), total, top_weight, r);
-            }
-            before += w[k];
-          }
-          cluster.barrier_wait();
-          return;
-        }
-        uint64_t *const part = reinterpret_cast<uint64_t *>(hist);   // the list's weights before each thread's
-        part[tid] = before;
+      uint64_t *const part = reinterpret_cast<uint64_t *>(hist);   // [kThreads]
+      bool found = true;
+      uint64_t before = 0, list_total = 0, own_kept = 0;   // kept weights: before this thread's, all, its own
+      if (n <= kSmallList) {
+        // a thread per element; the rank and the weight of what lies above it by looking at all
+        const uint64_t mine_c = tid < n ? list[tid] : 0, mine_w = tid < n && mine_c >= low ? list_weight(tid) : 0;
+        if (tid < n) part[tid] = mine_w;
         __syncthreads();
-        if (tid <= kRanges) {
-          const int i = list_at[tid];
-          uint64_t at = i / kChunk < kThreads ? part[i / kChunk] : total;
-          for (int j = i / kChunk * kChunk; j < i && j < n; ++j) {
-            if (list[j] < threshold) continue;
-            const uint64_t v = list_weight(j);
-            at += v >= least ? v : 0;
+        uint64_t higher = 0;
+        uint32_t higher_n = 0;
+        if (warp * 32 < n) {
+#pragma unroll 4
+          for (int j = 0; j < n; ++j) {
+            const bool is = list[j] > mine_c;
+            higher_n += is;
+            higher += is ? part[j] : 0;
           }
-          range_at[tid] = at;
         }
-        __syncthreads();
-        for (int c = 0; c < kCtas; ++c) total += cta_kept[c];
-        const uint64_t at = __umul64hi(f, total);
-        uint64_t reach = 0;
-        for (int c = 0; c < rank; ++c) reach += cta_kept[c];
-        reach += range_at[rank * kWarps];
-        const uint64_t here = cta_kept[rank] + range_at[(rank + 1) * kWarps] - range_at[rank * kWarps];
-        if (at >= reach && at < reach + here) {
-          if (tid < kWarps) warp_kept[tid] += range_at[rank * kWarps + tid + 1] - range_at[rank * kWarps + tid];
+        bool keep = tid < n && mine_c >= low;
+        if (!mass) keep = keep && over + higher_n < want;
+        uint64_t mass_want = want, all;
+        if (mass || (from_top && top_p < 1.0f)) {
+          exclusive_sum(keep ? mine_w : 0, s, all);
           __syncthreads();
-          pick<T>(a, row, data, len, rank, warp_kept, reach, at, threshold, least, total, top_weight, r, table, tile_sum);
+          if (!mass) mass_want = ceil_product(top_p, all);
+          else found = over < want && want <= over + all;
+          keep = keep && (mass ? over : 0) + higher < mass_want;
+        }
+        const int kept_n = __syncthreads_count(keep);
+        if (keep && higher_n == static_cast<uint32_t>(kept_n) - 1) s.composite = mine_c;
+        own_kept = keep && mine_w >= local.least ? mine_w : 0;
+        before = exclusive_sum(own_kept, s, list_total);
+        threshold = s.composite;
+        __syncthreads();
+        part[tid] = before;
+      } else {
+        const auto list_mass = [&](uint64_t from) {
+          uint64_t v = 0, all;
+          for (int i = tid; i < n; i += kThreads) v += list[i] >= from ? list_weight(i) : 0;
+          exclusive_sum(v, s, all);
+          __syncthreads();
+          return all;
+        };
+        if (!mass) {
+          threshold = descend_list(false, list, n, 0, want - over, r, table, hist, s);
+          if (from_top && top_p < 1.0f) {
+            const uint64_t z = list_mass(threshold);
+            threshold = descend_list(true, list, n, threshold, ceil_product(top_p, z), r, table, hist, s);
+          }
+        } else {
+          // the leading bits of the weights may have missed the bin
+          found = over < want && want <= over + list_mass(low);
+          if (found) threshold = descend_list(true, list, n, low, want - over, r, table, hist, s);
+        }
+        if (found && (mass || from_top)) {
+#pragma unroll 1
+          for (int i = tid * kChunk; i < min((tid + 1) * kChunk, n); ++i) own_kept += kept_weight(i);
+          before = exclusive_sum(own_kept, s, list_total);
+          part[tid] = before;
+        }
+      }
+      const int chunk = n <= kSmallList ? 1 : kChunk;   // elements of a thread
+      if (from_top) {
+        const uint64_t at = __umul64hi(f_u, list_total);
+        if (at >= before && at < before + own_kept) {
+          int i = tid * chunk;
+          for (uint64_t v; at >= before + (v = kept_weight(i)); ++i) before += v;
+          finish(a, row, (1 << kIndexBits) - 1 - static_cast<int>(list[i] & ((1u << kIndexBits) - 1)),
+                 radix_key_value(static_cast<uint32_t>(list[i] >> kIndexBits)), list_total, r);
         }
         cluster.barrier_wait();
         return;
       }
+      if (mass && found) {
+        // up to each range: the list's kept weights before it
+        __syncthreads();
+        if (tid <= kRanges) {
+          const int i = list_at[tid], t = i / chunk;
+          uint64_t at = t < kThreads ? part[t] : list_total;
+#pragma unroll 1
+          for (int j = t * chunk; j < i; ++j) at += kept_weight(j);
+          range_at[tid] = at;
+        }
+        __syncthreads();
+        uint64_t all = list_total, reach = range_at[rank * kWarps];
+        for (int c = 0; c < kCtas; ++c) {
+          all += cta_kept[c];
+          if (c < rank) reach += cta_kept[c];
+        }
+        const uint64_t at = __umul64hi(f_u, all);
+        const uint64_t here = cta_kept[rank] + range_at[(rank + 1) * kWarps] - range_at[rank * kWarps];
+        if (at >= reach && at < reach + here) {
+          if (tid < kWarps) warp_kept[tid] += range_at[rank * kWarps + tid + 1] - range_at[rank * kWarps + tid];
+          __syncthreads();
+          pick<T>(a, row, data, rank, warp_kept, reach, at, threshold, all, r, table, tile_sum);
+        }
+        cluster.barrier_wait();
+        return;
+      }
+      listed = found;
     }
-    // long lists: the whole row, all CTAs
     if (reading) cluster.barrier_wait();
-    uint64_t left = static_cast<uint64_t>(top_k), low = static_cast<uint64_t>(kKeyMasked + 1) << kIndexBits;
-    for (int kind = count ? 0 : 1; kind < (top_p < 1.0f ? 2 : 1); ++kind) {   // top-k's border, top-p's
-      uint64_t prefix = 0;
+    if (!listed) {
+      // long lists: a descent over the row
+      uint64_t left = want, prefix = 0;
       for (int shift = kCompositeBits; shift > 0;) {
         const int known = shift, bits = min(kDigit, shift);
         shift -= bits;
@@ -831,28 +976,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint64_t c = composite(x[k], begin + t + 4 * lane + k);
-            if (c < low || c >> known != prefix) continue;
+            if (key_of(x[k]) <= kKeyMasked || c < low || c >> known != prefix) continue;
             const uint32_t at = static_cast<uint32_t>(c >> shift) & ((1u << bits) - 1);
-            if (kind == 0) {
-              atomicAdd(&hist[at], 1u);
-            } else {
-              const uint64_t w = weight(x[k], r, table);
-              if (w != 0) add_to_hist(hist, at, w);
-            }
+            if (!mass) atomicAdd(&hist[at], 1u);
+            else if (const uint64_t v = weight(x[k], r, table); v != 0) add_to_hist(hist, at, v);
           }
         });
         cluster.sync();
-        const Found f = kind == 0 ? find_bin<false, true>(hist, s, [&](uint64_t) { return left; })
-                                  : find_bin<true, true>(hist, s, [&](uint64_t z) {
-                                      if (known == kCompositeBits) left = ceil_product(top_p, z);
-                                      return left;
-                                    });
+        const Found f = find_bin(mass, kCtas, hist, s, left);
         prefix = prefix << bits | f.bin;
         left -= f.above;
       }
-      threshold = low = prefix;
+      threshold = prefix;
     }
-    cluster.sync();
+    cluster.sync();   // nobody reads what is written next
+    clear_hist(hist);
+    __syncthreads();
   }
 
   // the kept weights of the row
@@ -861,19 +1000,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       Weights v;
-      weights(x[2 * h], x[2 * h + 1], r, table, v);
+      weights(x[2 * h], x[2 * h + 1], local, table, v);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (v.w[i] >= least && (threshold == 0 || composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) >= threshold)) sum += v.w[i];
+        if (v.w[i] >= local.least && (threshold == 0 || composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) >= threshold)) sum += v.w[i];
     }
   });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  sum = warp_total(sum);
   if (lane == 0) warp_kept[warp] = sum;
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) sum += warp_kept[w];
-    mine.sum = sum;
+  if (warp == 0) {
+    sum = warps_total(warp_kept);
+    if (lane == 0) mine.sum = sum;
   }
   cluster.sync();
   uint64_t total = 0, reach = 0, here = 0;
@@ -885,9 +1023,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     total += v;
   }
   cluster.barrier_arrive();
-  const uint64_t at = __umul64hi(u > 0.0f ? (u < 1.0f ? static_cast<uint64_t>(u * 0x1p64f) : ~0ull) : 0ull, total);
+  const uint64_t at = __umul64hi(f_u, total);
   if (at >= reach && at < reach + here)
-    pick<T>(a, row, data, len, rank, warp_kept, reach, at, threshold, least, total, top_weight, r, table, tile_sum);
+    pick<T>(a, row, data, rank, warp_kept, reach, at, threshold, total, r, table, tile_sum);
   cluster.barrier_wait();
 }
 

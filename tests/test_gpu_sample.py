@@ -109,6 +109,21 @@ def test_equal_logits(lib, dtype):
         check(lib, x, u, top_k=k, top_p=rng.uniform(0.5, 0.999, 40))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_flat_rows_and_many_kept(lib, dtype):
+    """Borders in bins of thousands of elements: cut finer, or found over the whole row."""
+    rng = np.random.default_rng(13)
+    V = 150001
+    for scale in (0.02, 0.3, 1.0):
+        x = torch.from_numpy((rng.standard_normal((6, V)) * scale).astype(np.float32)).cuda().to(dtype)
+        u = rng.random(6)
+        k = [400, 1500, 5000, 20000, 100000, V - 1]
+        p = [0.01, 0.3, 0.6, 0.9, 0.99, 0.9999]
+        check(lib, x, u, top_k=k)
+        check(lib, x, u, top_p=p)
+        check(lib, x, u, top_k=k, top_p=p[::-1], min_p=[0.0, 0.1, 0.5, 0.9, 0.0, 0.99])
+
+
 def test_exact_borders(lib):
     """u Z and p Z on a border: equal weights, quotients that fp32 holds."""
     x = torch.zeros(64, 64, device="cuda")
