@@ -42,7 +42,8 @@ constexpr uint32_t kKeyMasked = 0x007FFFFFu;   // radix_key(-inf)
 constexpr int kFine = 256;       // parts of such a bin
 constexpr int kOctaves = 44;     // below 2^-44 of the largest: no weight
 constexpr int kCut = kOctaves * 64;
-constexpr int kYBins = 48 * 32;   // (d + 63) / 2 for d < kCut, 32 to an octave
+constexpr int kOctaveBins = 48;  // octaves, with room
+constexpr int kYBins = kOctaveBins * 32;   // (d + 63) / 2 for d < kCut, 32 to an octave
 constexpr int kDigit = 9;        // bits of a descent's level
 constexpr int kBins = 1 << kDigit;
 constexpr int kSmallList = 256;  // searched by a thread per element
@@ -86,7 +87,6 @@ struct Row {
   float c_hi, c_lo;     // c in two terms
   float floor;          // of p: below it there is no weight
   int32_t top_bits;     // p + kMagic of the largest
-  uint64_t top_weight;
   uint64_t least;       // of the weights that min-p keeps
 };
 
@@ -191,20 +191,26 @@ struct Quad<uint16_t> {
   static __device__ __forceinline__ uint16_t masked() { return 0xFF80u; }
 };
 
-// What the CTAs of a row publish; every field is written before one barrier and read behind it.
-template <typename T>
-struct Shared {
-  static constexpr int kSegment = Quad<T>::kListMost / 16;   // candidates of a warp
-  // the first CTA's: the row's parameters
-  float temperature, c_hi, c_lo, top_p, min_p, u;
-  int32_t top_k, live;
+// What the CTAs of a row tell each other: each writes its own entry into every CTA, before a
+// barrier that all read behind, so that nobody waits for another SM's shared memory.
+struct Told {
   unsigned long long best;   // (key << 32) | ~index of the CTA's largest
   uint64_t all;              // its weights
   uint64_t above, kept;      // its weights (or elements) above the border's bin, the weights that min-p keeps of them
   uint64_t sum;              // its kept weights, where no list gave them
-  uint32_t octave[kYBins / 32];   // sums of the exponents' bins
-  uint16_t count[kWarps];    // candidates
-  T logit[kWarps][kSegment];           // they, and their places in the warp's range, by place
+};
+struct Params {              // of the row, from the first CTA
+  float temperature, c_hi, c_lo, top_p, min_p, u;
+  int32_t top_k, live;
+};
+template <typename T>
+struct Shared {
+  static constexpr int kSegment = Quad<T>::kListMost / 16;   // candidates of a warp
+  Told told[kCtas];
+  Params params;
+  uint32_t octave[kCtas][kOctaveBins];   // sums of the exponents' bins
+  uint16_t count[kRanges];               // candidates of every warp
+  T logit[kWarps][kSegment];             // this CTA's, and their places in the warp's range, by place
   uint16_t place[kWarps][kSegment];
 };
 
@@ -215,31 +221,38 @@ struct Found {
 // What a CTA uses alone.
 struct Scratch {
   uint64_t warp_sum[kWarps];
-  uint64_t octave[kYBins / 32], bin[32];
+  float bin[32];
   Found found;
   uint32_t overflow;
   uint64_t composite;
 };
 
 // The sum over the threads before this one, and over all.
-__device__ __noinline__ uint64_t exclusive_sum(uint64_t sum, Scratch &s, uint64_t &total) {
+struct Sums {
+  uint64_t before, all;
+};
+__device__ __noinline__ Sums exclusive_sum(uint64_t v, uint64_t *warp_sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t upto = sum;
+  uint64_t upto = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += up;
   }
-  if (lane == 31) s.warp_sum[warp] = upto;
+  if (lane == 31) warp_sum[warp] = upto;
   __syncthreads();
-  uint64_t before = 0;
-  total = 0;
+  // every warp sums the warps' sums, one a lane
+  uint64_t w = lane < kWarps ? warp_sum[lane] : 0;
+  const uint64_t own = w;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s.warp_sum[w];
-    total += s.warp_sum[w];
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const uint64_t up = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += up;
   }
-  return before + upto - sum;
+  Sums r;
+  r.before = __shfl_sync(0xffffffffu, w - own, warp) + upto - v;
+  r.all = __shfl_sync(0xffffffffu, w, kWarps - 1);
+  return r;
 }
 
 __device__ __forceinline__ uint64_t warp_total(uint64_t v) {
@@ -254,11 +267,12 @@ __device__ __forceinline__ uint64_t warps_total(const uint64_t *v) {
 
 // A row's outputs.  log(w / Z) from the logit itself, whose weight may be a few units, and
 // log1p of what the others weigh beside the largest.
-__device__ __noinline__ void finish(const SampleArgs &a, int64_t row, int token, float x, uint64_t total, const Row &r) {
+__device__ __noinline__ void finish(const SampleArgs &a, int64_t row, int token, float x, uint64_t total, const Row &r, const Exp2 *table) {
   a.token[row] = token;
   if (a.logprob == nullptr) return;
   const float y = x == r.top ? 0.0f : (r.top - x) / r.temperature;
-  const float z = static_cast<float>(total - r.top_weight) / static_cast<float>(r.top_weight);
+  const uint64_t top = weight(r.top, r, table);
+  const float z = static_cast<float>(total - top) / static_cast<float>(top);
   a.logprob[row] = 0.0f - y - log1pf(z);
 }
 
@@ -316,7 +330,7 @@ __device__ __noinline__ void pick(const SampleArgs &a, int64_t row, const T *dat
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (at >= from && at < from + w[k]) {
-        finish(a, row, base + t * kTile + 4 * lane + k, x[k], total, r);
+        finish(a, row, base + t * kTile + 4 * lane + k, x[k], total, r, table);
         return;
       }
       from += w[k];
@@ -346,7 +360,7 @@ __device__ __forceinline__ void add_to_hist(uint32_t *hist, uint32_t bin, uint64
 __device__ __noinline__ Found find_bin(bool mass, int ctas, uint32_t *hist, Scratch &s, uint64_t want) {
   static_assert(kBins == kThreads, "a bin a thread");
   const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
-  uint64_t own = 0, total;
+  uint64_t own = 0;
   if (threadIdx.x == 0) s.found = {kBins, 0, 0};
 #pragma unroll 1
   for (int c = 0; c < ctas; ++c) {
@@ -354,82 +368,83 @@ __device__ __noinline__ Found find_bin(bool mass, int ctas, uint32_t *hist, Scra
     own += h[bin];
     if (mass) own += static_cast<uint64_t>(h[kBins + bin]) << 32;
   }
-  const uint64_t above = exclusive_sum(own, s, total);
+  const uint64_t above = exclusive_sum(own, s.warp_sum).before;
   if (above < want && want <= above + own) s.found = {static_cast<uint32_t>(bin), above, own};
   __syncthreads();
   return s.found;
 }
 
-// The octaves' sums of this CTA's bins of exponents, before find_exponent's barrier.
-__device__ __forceinline__ void sum_octaves(const uint32_t *hist, uint32_t *octave) {
+// The octaves' sums of this CTA's bins of exponents, to all CTAs: octave[rank] there.
+__device__ __noinline__ void push_octaves(const uint32_t *hist, uint32_t (*octave)[kOctaveBins]) {
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int o = warp; o < kYBins / 32; o += kWarps) {
+  for (int o = warp; o < kOctaveBins; o += kWarps) {
     const uint32_t v = __reduce_add_sync(0xffffffffu, hist[o * 32 + lane]);
-    if (lane == 0) octave[o] = v;
+    if (lane < kCtas) cg::this_cluster().map_shared_rank(octave, lane)[cg::this_cluster().block_rank()][o] = v;
   }
 }
 
 // Of 32 values, one a lane, the first at which the running sum reaches `want` (the last that
-// is not 0 if none does), the sum before it and its own; `all`: of all.
+// is not 0 if none does), and the sum before it; `all`: of all.
 struct Reached {
   int at;
-  uint64_t before, own, all;
+  float before, all;
 };
-__device__ __forceinline__ Reached reach_in_warp(uint64_t v, uint64_t want) {
+__device__ __forceinline__ Reached reach_in_warp(float v, float want) {
   const int lane = threadIdx.x & 31;
-  uint64_t upto = v;
+  float upto = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+    const float up = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += up;
   }
-  const uint32_t there = __ballot_sync(0xffffffffu, upto >= want), some = __ballot_sync(0xffffffffu, v != 0);
+  const uint32_t there = __ballot_sync(0xffffffffu, upto >= want && v != 0.0f), some = __ballot_sync(0xffffffffu, v != 0.0f);
   Reached r;
   r.at = there != 0 ? __ffs(there) - 1 : some != 0 ? 31 - __clz(some) : 31;
   r.before = __shfl_sync(0xffffffffu, upto - v, r.at);
-  r.own = __shfl_sync(0xffffffffu, v, r.at);
   r.all = __shfl_sync(0xffffffffu, upto, 31);
   return r;
 }
 
 // The bin of exponents, from the largest, at which the running sum over all CTAs reaches
-// `want`, and the sum of all: first the octave, then its bin, so that a thread reads two words
-// of another CTA.  mass: sums of weights' 16 leading bits, which may end a little short.
-__device__ __noinline__ int find_exponent(bool mass, const uint32_t *hist, const uint32_t *octave, Scratch &s, uint64_t want, uint64_t &total) {
-  constexpr int kOct = kYBins / 32;
-  static_assert(kOct * kCtas <= kThreads && kOct <= 64, "a word a thread");
+// `want`, and the sum of all: first the octave, then its bin, so that a thread reads one word
+// of another CTA.  In fp32: counts below 2^24 are exact; sums of weights' leading bits
+// (mass, in units of 2^-16 of the largest) may miss a border that lies close to an end of
+// its bin, which the exact sums behind it find out.
+struct Exponent {
+  int32_t bin;
+  float all;
+};
+__device__ __noinline__ Exponent find_exponent(bool mass, const uint32_t *hist, const uint32_t (*octave)[kOctaveBins], float *sum, float want) {
+  static_assert(kOctaveBins > 32 && kOctaveBins <= 64, "one or two octaves a lane");
   const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < kOct * kCtas) {
-    const int o = tid / kCtas;
-    uint64_t v = cg::this_cluster().map_shared_rank(octave, tid % kCtas)[o];
+  const auto scaled = [&](float v, int o) { return mass ? v * __uint_as_float(static_cast<uint32_t>(127 - o) << 23) : v; };
+  float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-    for (int k = kCtas / 2; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-    if (tid % kCtas == 0) s.octave[o] = mass ? v << 29 >> o : v;
+  for (int c = 0; c < kCtas; ++c) {
+    v0 += static_cast<float>(octave[c][lane]);
+    if (lane + 32 < kOctaveBins) v1 += static_cast<float>(octave[c][lane + 32]);
   }
-  __syncthreads();
-  Reached r = reach_in_warp(s.octave[lane], want);
-  total = r.all;
+  Reached r = reach_in_warp(scaled(v0, lane), want);
+  const Reached far = reach_in_warp(scaled(v1, lane + 32), want - r.all);
+  Exponent e;
+  e.all = r.all + far.all;
   int o = r.at;
-  {
-    const uint64_t v = lane < kOct - 32 ? s.octave[32 + lane] : 0;
-    Reached far = reach_in_warp(v, want > r.all ? want - r.all : 0);
-    total += far.all;
-    if (r.all < want && far.all != 0) {
-      o = 32 + far.at;
-      far.before += r.all;
-      r = far;
-    }
+  float before = r.before;
+  if (r.all < want && far.all != 0.0f) {
+    o = 32 + far.at;
+    before = r.all + far.before;
   }
   if (tid < 32 * kCtas) {
-    uint64_t v = cg::this_cluster().map_shared_rank(hist, tid % kCtas)[o * 32 + tid / kCtas];
+    float v = static_cast<float>(cg::this_cluster().map_shared_rank(hist, tid % kCtas)[o * 32 + tid / kCtas]);
 #pragma unroll
     for (int k = kCtas / 2; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-    if (tid % kCtas == 0) s.bin[tid / kCtas] = mass ? v << 29 >> o : v;
+    if (tid % kCtas == 0) sum[tid / kCtas] = scaled(v, o);
   }
   __syncthreads();
-  return o * 32 + reach_in_warp(s.bin[lane], want > r.before ? want - r.before : 0).at;
+  e.bin = o * 32 + reach_in_warp(sum[lane], want - before).at;
+  return e;
 }
 
 // The composite in list[0 .. n) at which the running sum, from the largest, over those >= low
@@ -475,7 +490,8 @@ __device__ __noinline__ uint64_t descend_list(bool mass, const uint64_t *list, i
   return prefix;
 }
 
-template <typename T>
+// kTopK, kTopP: the rows may have these filters.
+template <typename T, bool kTopK, bool kTopP>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
   using Q = Quad<T>;
   using Vec = typename Q::Vec;
@@ -491,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   __shared__ __align__(8) Exp2 table[64 * kColumns];
   __shared__ unsigned long long warp_best[kWarps];
   __shared__ uint64_t warp_kept[kWarps], warp_above[kWarps];
-  __shared__ uint64_t range_at[kRanges + 1], cta_above[kCtas], cta_kept[kCtas];
+  __shared__ uint64_t range_at[kRanges + 1];
   __shared__ int32_t list_at[kRanges + 1];
   __shared__ uint64_t tile_sum[2 * kWarps];
   static_assert(kYBins <= 3 * kBins && kThreads * sizeof(uint64_t) <= 3 * kBins * sizeof(uint32_t) && kFine <= kBins, "what hist holds by turns");
@@ -506,18 +522,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   T *const own = data + warp * len;
   const T *const src = static_cast<const T *>(a.p.logits) + row * a.p.ld;
 
+  cluster.barrier_arrive();
   for (int i = tid; i < 64 * kColumns; i += kThreads) table[i] = kExp2.v[i / kColumns];
   clear_hist(hist);
-  if (rank == 0 && tid == 0) {
-    mine.live = a.p.rows == nullptr || row < *a.p.rows;
-    mine.temperature = a.p.temperature != nullptr ? a.p.temperature[row] : 1.0f;
-    const double c = 1.4426950408889634 / static_cast<double>(fminf(fmaxf(mine.temperature, 0x1p-60f), 0x1p60f));
-    mine.c_hi = static_cast<float>(c);
-    mine.c_lo = static_cast<float>(c - static_cast<double>(mine.c_hi));
-    mine.top_k = a.p.top_k != nullptr ? a.p.top_k[row] : 0;
-    mine.top_p = a.p.top_p != nullptr ? a.p.top_p[row] : 1.0f;
-    mine.min_p = a.p.min_p != nullptr ? a.p.min_p[row] : 0.0f;
-    mine.u = a.p.u[row];
+  if (rank == 0 && warp == 0) {
+    Params v;
+    v.live = a.p.rows == nullptr || row < *a.p.rows;
+    v.temperature = a.p.temperature != nullptr ? a.p.temperature[row] : 1.0f;
+    const double c = 1.4426950408889634 / static_cast<double>(fminf(fmaxf(v.temperature, 0x1p-60f), 0x1p60f));
+    v.c_hi = static_cast<float>(c);
+    v.c_lo = static_cast<float>(c - static_cast<double>(v.c_hi));
+    v.top_k = kTopK ? a.p.top_k[row] : 0;
+    v.top_p = kTopP ? a.p.top_p[row] : 1.0f;
+    v.min_p = a.p.min_p != nullptr ? a.p.min_p[row] : 0.0f;
+    v.u = a.p.u[row];
+    mine.params = v;
   }
 
   // the row, once, and its largest element (the first of several)
@@ -568,70 +587,64 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const unsigned long long b = __shfl_xor_sync(0xffffffffu, best, o);
       best = b > best ? b : best;
     }
-    if (lane == 0) mine.best = best;
+  }
+  cluster.barrier_wait();   // all CTAs run: their memory can be written
+  if (warp == 0 && lane < kCtas) {
+    Pub *const to = cluster.map_shared_rank(&mine, lane);
+    to->told[rank].best = best;
+    if (rank == 0 && lane != 0) to->params = mine.params;
   }
   cluster.sync();
   best = 0;
 #pragma unroll
-  for (int c = 0; c < kCtas; ++c) {
-    const unsigned long long b = cluster.map_shared_rank(&mine, c)->best;
-    best = b > best ? b : best;
-  }
-  const Pub *const params = cluster.map_shared_rank(&mine, 0);
-  const float temperature = params->temperature, min_p = params->min_p, u = params->u;
-  const float top_p = params->top_p < 1.0f ? params->top_p : 1.0f;   // NaN: off
-  const int32_t top_k = params->top_k;
-  const bool live = params->live != 0;
+  for (int c = 0; c < kCtas; ++c) best = mine.told[c].best > best ? mine.told[c].best : best;
+  const float temperature = mine.params.temperature, min_p = mine.params.min_p, u = mine.params.u;
+  const float top_p = kTopP && mine.params.top_p < 1.0f ? mine.params.top_p : 1.0f;   // NaN: off
+  const int32_t top_k = mine.params.top_k;
   const uint32_t top_key = static_cast<uint32_t>(best >> 32);
 
   // rows without a choice
+  const bool live = mine.params.live != 0;
   if (!live || top_key <= kKeyMasked || !(temperature > 0.0f) || top_k == 1 || top_p <= 0.0f) {
     if (live && rank == 0 && tid == 0) {
       const bool empty = top_key <= kKeyMasked;
       a.token[row] = empty ? -1 : static_cast<int32_t>(~static_cast<uint32_t>(best));
       if (a.logprob != nullptr) a.logprob[row] = empty ? -INFINITY : 0.0f;
     }
-    cluster.sync();   // the others may still read this CTA's maximum
-    return;
+    return;   // nobody reads or writes another CTA's memory any more
   }
 
-  if (warp == 0) {   // every lane the same
-    Row v;
-    v.top = radix_key_value(top_key);
-    if (v.top == INFINITY) v.top = 0.0f;   // see below
-    v.temperature = fminf(fmaxf(temperature, 0x1p-60f), 0x1p60f);
-    v.c_hi = params->c_hi;
-    v.c_lo = params->c_lo;
-    v.ref = fabsf(v.top * v.c_hi) <= 128.0f ? 0.0f : v.top;
-    v.floor = -INFINITY;
-    v.top_bits = 0;
+  Row local;   // in registers, for the loops over the row
+  local.top = radix_key_value(top_key);
+  if (local.top == INFINITY) {   // those at +inf alone have a weight, the same
+    local.top = 0.0f;
+    for (int t = lane; t < len; t += 32) own[t] = Q::one(own[t]) == INFINITY ? static_cast<T>(0) : Q::masked();
+    __syncwarp();
+  }
+  local.temperature = fminf(fmaxf(temperature, 0x1p-60f), 0x1p60f);
+  local.c_hi = mine.params.c_hi;
+  local.c_lo = mine.params.c_lo;
+  local.ref = fabsf(local.top * local.c_hi) <= 128.0f ? 0.0f : local.top;
+  local.floor = -INFINITY;
+  local.top_bits = 0;
+  {
     uint64_t p, lo, t;
     int32_t d[2];
-    exponents(v.top, v.top, v, p, lo);
-    steps(p, v, t, d);
-    v.top_bits = -d[0];
-    v.floor = __uint_as_float(static_cast<uint32_t>(p)) - 64.0f;
-    v.least = 1;
-    r = v;
-    __syncwarp();
-    v.top_weight = weight(v.top, r, table);
-    if (min_p > 0.0f) {
-      const uint64_t f = static_cast<uint64_t>(fminf(min_p, 1.0f) * 0x1p63f);
-      const uint64_t hi = __umul64hi(f, v.top_weight), lw = f * v.top_weight;
-      v.least = (hi << 1 | lw >> 63) + (lw << 1 != 0 || f == 0 ? 1 : 0);
-    }
-    __syncwarp();
-    r = v;
+    exponents(local.top, local.top, local, p, lo);
+    steps(p, local, t, d);
+    local.top_bits = -d[0];
+    local.floor = __uint_as_float(static_cast<uint32_t>(p)) - 64.0f;
   }
-  if (radix_key_value(top_key) == INFINITY) {   // those at +inf alone have a weight, the same
-    for (int t = lane; t < len; t += 32) {
-      const bool is = Q::one(own[t]) == INFINITY;
-      own[t] = is ? static_cast<T>(0) : Q::masked();
-    }
-  }
+  local.least = 1;
+  if (tid == 0) r = local;   // for what is not inlined
   __syncthreads();
+  if (min_p > 0.0f) {
+    const uint64_t f = static_cast<uint64_t>(fminf(min_p, 1.0f) * 0x1p63f), w = weight(r.top, r, table);
+    const uint64_t hi = __umul64hi(f, w), lo = f * w;
+    local.least = (hi << 1 | lo >> 63) + (lo << 1 != 0 || f == 0 ? 1 : 0);
+    if (tid == 0) r.least = local.least;
+  }
 
-  const Row local = r;   // in registers, for the loops over the row
   // f(tile, x[4]) over this warp's elements
   const auto each_tile = [&](auto f) {
 #pragma unroll 1
@@ -645,9 +658,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   uint64_t threshold = 0;   // composite of the last kept element
 
   // top-k's border, then top-p's among what top-k keeps
-  for (int kind = top_k > 0 && top_k < a.p.V ? 0 : 1; kind < (top_p < 1.0f ? 2 : 1); ++kind) {
-    const bool mass = kind == 1;
-    const uint64_t low = threshold;
+  if constexpr (kTopK || kTopP)
+  for (int kind = kTopK && top_k > 0 && top_k < a.p.V ? 0 : 1; kind < (kTopP && top_p < 1.0f ? 2 : 1); ++kind) {
+    const bool mass = kTopP && (!kTopK || kind == 1);
+    const uint64_t low = kTopK ? threshold : 0;   // top-p's elements are those >= low
+    const auto among = [&](uint64_t c) { return !kTopK || c >= low; };
     uint64_t sum = 0;
     if (mass) {
       each_tile([&](int t, const float (&x)[4]) {
@@ -657,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           weights(x[2 * h], x[2 * h + 1], local, table, v);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (v.d[i] < kCut && (low == 0 || composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) >= low)) {
+            if (v.d[i] < kCut && (!kTopK || low == 0 || among(composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i)))) {
               sum += v.w[i];
               atomicAdd(&hist[(v.d[i] + 63) >> 1], v.m[i] | 1u);
             }
@@ -680,21 +695,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
       });
     }
-    sum_octaves(hist, mine.octave);
+    push_octaves(hist, mine.octave);
     if (mass && warp == 0) {
       sum = warps_total(warp_above);
-      if (lane == 0) mine.all = sum;
+      if (lane < kCtas) cluster.map_shared_rank(&mine, lane)->told[rank].all = sum;
     }
     cluster.sync();
-    uint64_t want = static_cast<uint64_t>(top_k), total;
+    uint64_t want = static_cast<uint64_t>(top_k);
     if (mass) {
       uint64_t z = 0;
 #pragma unroll
-      for (int c = 0; c < kCtas; ++c) z += cluster.map_shared_rank(&mine, c)->all;
+      for (int c = 0; c < kCtas; ++c) z += mine.told[c].all;
       want = ceil_product(top_p, z);
     }
-    const int32_t border = find_exponent(mass, hist, mine.octave, s, want, total);
-    if (!mass && total <= want) {   // all that have a weight are kept
+    const Exponent ex = find_exponent(mass, hist, mine.octave, s.bin, mass ? static_cast<float>(want) * 0x1p-29f : static_cast<float>(want));
+    const int32_t border = ex.bin;
+    if (!mass && ex.all <= static_cast<float>(want)) {   // all that have a weight are kept
       cluster.sync();               // nobody reads the histogram any more
       clear_hist(hist);
       __syncthreads();
@@ -775,37 +791,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (lane == 0) {
         warp_above[warp] = above;
         warp_kept[warp] = kept;
-        mine.count[warp] = static_cast<uint16_t>(n);   // at most the warp's range
       }
+      if (lane < kCtas) cluster.map_shared_rank(&mine, lane)->count[rank * kWarps + warp] = static_cast<uint16_t>(n);   // at most the range
       __syncthreads();
       if (warp == 0) {
         above = warps_total(warp_above);
         kept = warps_total(warp_kept);
-        if (lane == 0) {
-          mine.above = above;
-          mine.kept = kept;
-          s.overflow = 0;
+        if (lane < kCtas) {
+          Pub *const to = cluster.map_shared_rank(&mine, lane);
+          to->told[rank].above = above;
+          to->told[rank].kept = kept;
         }
+        if (lane == 0) s.overflow = 0;
       }
       cluster.sync();
 
       // the list's length, the places of the ranges in it, the sums of all
-      if (tid < kCtas) {
-        cta_above[tid] = cluster.map_shared_rank(&mine, tid)->above;
-        cta_kept[tid] = cluster.map_shared_rank(&mine, tid)->kept;
-      }
       {
-        const int32_t c = tid < kRanges ? cluster.map_shared_rank(&mine, tid / kWarps)->count[tid % kWarps] : 0;
+        const int32_t c = tid < kRanges ? mine.count[tid] : 0;
         if (c > Pub::kSegment) s.overflow = 1;
-        uint64_t all;
-        const uint64_t before = exclusive_sum(static_cast<uint64_t>(c), s, all);
-        if (tid <= kRanges) list_at[tid] = static_cast<int32_t>(before);
-        n = static_cast<int32_t>(all);
+        const Sums all = exclusive_sum(static_cast<uint64_t>(c), s.warp_sum);
+        if (tid <= kRanges) list_at[tid] = static_cast<int32_t>(all.before);
+        n = static_cast<int32_t>(all.all);
       }
       __syncthreads();
       over = 0;
 #pragma unroll
-      for (int c = 0; c < kCtas; ++c) over += cta_above[c];
+      for (int c = 0; c < kCtas; ++c) over += mine.told[c].above;
       listed = n > 0 && n <= kListMost && s.overflow == 0;
       if (from_top && listed) over = 0;   // they are in the list themselves
       if (listed || round == 1 || over >= want) break;
@@ -823,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if ((d[i] + 63) >> 1 != border) continue;
-            if (low != 0 && composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) < low) continue;
+            if (kTopK && low != 0 && !among(composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i))) continue;
             const uint32_t bin = kBins - 1 - fine_code(p, b, d[i], i) % kFine;
             if (mass) add_to_hist(hist, bin, weight(x[2 * h + i], r, table));
             else atomicAdd(&hist[bin], 1u);
@@ -866,41 +878,44 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       uint64_t before = 0, list_total = 0, own_kept = 0;   // kept weights: before this thread's, all, its own
       if (n <= kSmallList) {
         // a thread per element; the rank and the weight of what lies above it by looking at all
-        const uint64_t mine_c = tid < n ? list[tid] : 0, mine_w = tid < n && mine_c >= low ? list_weight(tid) : 0;
-        if (tid < n) part[tid] = mine_w;
+        ulonglong2 *const both = reinterpret_cast<ulonglong2 *>(hist);
+        const uint64_t mine_c = tid < n ? list[tid] : 0, mine_w = tid < n && among(mine_c) ? list_weight(tid) : 0;
+        if (tid < n) both[tid] = make_ulonglong2(mine_c, mine_w);
         __syncthreads();
         uint64_t higher = 0;
         uint32_t higher_n = 0;
         if (warp * 32 < n) {
 #pragma unroll 4
           for (int j = 0; j < n; ++j) {
-            const bool is = list[j] > mine_c;
-            higher_n += is;
-            higher += is ? part[j] : 0;
+            const ulonglong2 e = both[j];
+            if (e.x > mine_c) {
+              ++higher_n;
+              higher += e.y;
+            }
           }
         }
-        bool keep = tid < n && mine_c >= low;
+        bool keep = tid < n && among(mine_c);
         if (!mass) keep = keep && over + higher_n < want;
-        uint64_t mass_want = want, all;
-        if (mass || (from_top && top_p < 1.0f)) {
-          exclusive_sum(keep ? mine_w : 0, s, all);
+        if (mass || (kTopP && from_top && top_p < 1.0f)) {
+          const uint64_t all = exclusive_sum(keep ? mine_w : 0, s.warp_sum).all;
           __syncthreads();
-          if (!mass) mass_want = ceil_product(top_p, all);
-          else found = over < want && want <= over + all;
-          keep = keep && (mass ? over : 0) + higher < mass_want;
+          if (mass) found = over < want && want <= over + all;
+          keep = keep && (mass ? over + higher < want : higher < ceil_product(top_p, all));
         }
         const int kept_n = __syncthreads_count(keep);
         if (keep && higher_n == static_cast<uint32_t>(kept_n) - 1) s.composite = mine_c;
         own_kept = keep && mine_w >= local.least ? mine_w : 0;
-        before = exclusive_sum(own_kept, s, list_total);
+        const Sums kept_sums = exclusive_sum(own_kept, s.warp_sum);
+        before = kept_sums.before;
+        list_total = kept_sums.all;
         threshold = s.composite;
         __syncthreads();
         part[tid] = before;
       } else {
         const auto list_mass = [&](uint64_t from) {
-          uint64_t v = 0, all;
+          uint64_t v = 0;
           for (int i = tid; i < n; i += kThreads) v += list[i] >= from ? list_weight(i) : 0;
-          exclusive_sum(v, s, all);
+          const uint64_t all = exclusive_sum(v, s.warp_sum).all;
           __syncthreads();
           return all;
         };
@@ -918,7 +933,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (found && (mass || from_top)) {
 #pragma unroll 1
           for (int i = tid * kChunk; i < min((tid + 1) * kChunk, n); ++i) own_kept += kept_weight(i);
-          before = exclusive_sum(own_kept, s, list_total);
+          const Sums kept_sums = exclusive_sum(own_kept, s.warp_sum);
+          before = kept_sums.before;
+          list_total = kept_sums.all;
           part[tid] = before;
         }
       }
@@ -929,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           int i = tid * chunk;
           for (uint64_t v; at >= before + (v = kept_weight(i)); ++i) before += v;
           finish(a, row, (1 << kIndexBits) - 1 - static_cast<int>(list[i] & ((1u << kIndexBits) - 1)),
-                 radix_key_value(static_cast<uint32_t>(list[i] >> kIndexBits)), list_total, r);
+                 radix_key_value(static_cast<uint32_t>(list[i] >> kIndexBits)), list_total, r, table);
         }
         cluster.barrier_wait();
         return;
@@ -947,11 +964,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         __syncthreads();
         uint64_t all = list_total, reach = range_at[rank * kWarps];
         for (int c = 0; c < kCtas; ++c) {
-          all += cta_kept[c];
-          if (c < rank) reach += cta_kept[c];
+          all += mine.told[c].kept;
+          if (c < rank) reach += mine.told[c].kept;
         }
         const uint64_t at = __umul64hi(f_u, all);
-        const uint64_t here = cta_kept[rank] + range_at[(rank + 1) * kWarps] - range_at[rank * kWarps];
+        const uint64_t here = mine.told[rank].kept + range_at[(rank + 1) * kWarps] - range_at[rank * kWarps];
         if (at >= reach && at < reach + here) {
           if (tid < kWarps) warp_kept[tid] += range_at[rank * kWarps + tid + 1] - range_at[rank * kWarps + tid];
           __syncthreads();
@@ -976,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint64_t c = composite(x[k], begin + t + 4 * lane + k);
-            if (key_of(x[k]) <= kKeyMasked || c < low || c >> known != prefix) continue;
+            if (key_of(x[k]) <= kKeyMasked || !among(c) || c >> known != prefix) continue;
             const uint32_t at = static_cast<uint32_t>(c >> shift) & ((1u << bits) - 1);
             if (!mass) atomicAdd(&hist[at], 1u);
             else if (const uint64_t v = weight(x[k], r, table); v != 0) add_to_hist(hist, at, v);
@@ -1003,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       weights(x[2 * h], x[2 * h + 1], local, table, v);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (v.w[i] >= local.least && (threshold == 0 || composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) >= threshold)) sum += v.w[i];
+        if (v.w[i] >= local.least && (!(kTopK || kTopP) || threshold == 0 || composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) >= threshold)) sum += v.w[i];
     }
   });
   sum = warp_total(sum);
@@ -1011,22 +1028,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   __syncthreads();
   if (warp == 0) {
     sum = warps_total(warp_kept);
-    if (lane == 0) mine.sum = sum;
+    if (lane < kCtas) cluster.map_shared_rank(&mine, lane)->told[rank].sum = sum;
   }
   cluster.sync();
   uint64_t total = 0, reach = 0, here = 0;
 #pragma unroll
   for (int c = 0; c < kCtas; ++c) {
-    const uint64_t v = cluster.map_shared_rank(&mine, c)->sum;
+    const uint64_t v = mine.told[c].sum;
     if (c < rank) reach += v;
     if (c == rank) here = v;
     total += v;
   }
-  cluster.barrier_arrive();
   const uint64_t at = __umul64hi(f_u, total);
   if (at >= reach && at < reach + here)
     pick<T>(a, row, data, rank, warp_kept, reach, at, threshold, total, r, table, tile_sum);
-  cluster.barrier_wait();
 }
 
 template <typename T>
@@ -1034,18 +1049,15 @@ constexpr size_t fixed_smem() {
   return 3 * kBins * sizeof(uint32_t) + Quad<T>::kListMost * sizeof(uint64_t);
 }
 
-template <typename T>
-cudaError_t launch(SampleArgs a, cudaStream_t stream) {
-  constexpr int kSpan = kCtas * kWarps * kTile;
+template <typename T, bool kTopK, bool kTopP>
+cudaError_t launch(const SampleArgs &a, cudaStream_t stream) {
   constexpr int kMost = static_cast<int>(fixed_smem<T>()) + IDX_MAX_VOCAB / kCtas * static_cast<int>(sizeof(T));
-  static_assert(IDX_MAX_VOCAB % kSpan == 0 && IDX_MAX_VOCAB / kRanges / kTile <= 2 * kWarps, "whole steps of every warp");
   static std::mutex mu;
   static bool done[128];
   cudaError_t e = once_per_device(mu, done, [] {
-    return cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    return cudaFuncSetAttribute(sample_kernel<T, kTopK, kTopP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   });
   if (e != cudaSuccess) return e;
-  a.warp_len = static_cast<int32_t>((a.p.V + kSpan - 1) / kSpan) * kTile;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim = {kCtas, 1, 1};
@@ -1056,7 +1068,16 @@ cudaError_t launch(SampleArgs a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T, kTopK, kTopP>, a);
+}
+
+template <typename T>
+cudaError_t launch(SampleArgs a, cudaStream_t stream) {
+  constexpr int kSpan = kCtas * kWarps * kTile;
+  static_assert(IDX_MAX_VOCAB % kSpan == 0 && IDX_MAX_VOCAB / kRanges / kTile <= 2 * kWarps, "whole steps of every warp");
+  a.warp_len = static_cast<int32_t>((a.p.V + kSpan - 1) / kSpan) * kTile;
+  if (a.p.top_k != nullptr) return a.p.top_p != nullptr ? launch<T, true, true>(a, stream) : launch<T, true, false>(a, stream);
+  return a.p.top_p != nullptr ? launch<T, false, true>(a, stream) : launch<T, false, false>(a, stream);
 }
 
 }  // namespace
