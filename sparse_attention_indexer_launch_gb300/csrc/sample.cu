@@ -85,43 +85,44 @@ struct Row {
   float ref;
   float temperature;    // within 2^-60 .. 2^60
   float c_hi, c_lo;     // c in two terms
-  float floor;          // of p: below it there is no weight
-  int32_t top_bits;     // p + kMagic of the largest
+  uint32_t top_bits;    // p + kMagic of the largest
   uint64_t least;       // of the weights that min-p keeps
 };
 
-// p in two terms for two logits; the first is cut at r.floor (NaN and -inf as well).
+// p in two terms for two logits.
 __device__ __forceinline__ void exponents(float x0, float x1, const Row &r, uint64_t &p, uint64_t &lo) {
-  const uint64_t x = fma2(pack2(x0, x1), pack2(1.0f, 1.0f), pack2(-r.ref, -r.ref)), c = pack2(r.c_hi, r.c_hi);
-  const uint64_t minus = mul2(x, pack2(-r.c_hi, -r.c_hi));
-  lo = fma2(x, pack2(r.c_lo, r.c_lo), fma2(x, c, minus));
-  p = pack2(fmaxf(-__uint_as_float(static_cast<uint32_t>(minus)), r.floor),
-            fmaxf(-__uint_as_float(static_cast<uint32_t>(minus >> 32)), r.floor));
+  const uint64_t x = fma2(pack2(x0, x1), pack2(1.0f, 1.0f), pack2(-r.ref, -r.ref));
+  p = mul2(x, pack2(r.c_hi, r.c_hi));
+  lo = fma2(x, pack2(r.c_lo, r.c_lo), fma2(x, pack2(r.c_hi, r.c_hi), mul2(p, pack2(-1.0f, -1.0f))));
 }
-// p in steps of 1 / 64 below the largest's, >= 0.
-__device__ __forceinline__ void steps(uint64_t p, const Row &r, uint64_t &t, int32_t (&d)[2]) {
+// p in steps of 1 / 64 below the largest's.  Unsigned: floats' bits ascend with their values,
+// and those of negative ones and of NaN end up far behind kCut as well.
+__device__ __forceinline__ void steps(uint64_t p, const Row &r, uint64_t &t, uint32_t (&d)[2]) {
   t = fma2(p, pack2(1.0f, 1.0f), pack2(kMagic, kMagic));
-  d[0] = r.top_bits - static_cast<int32_t>(static_cast<uint32_t>(t));
-  d[1] = r.top_bits - static_cast<int32_t>(static_cast<uint32_t>(t >> 32));
+  d[0] = r.top_bits - static_cast<uint32_t>(t);
+  d[1] = r.top_bits - static_cast<uint32_t>(t >> 32);
 }
 
+// A bin of exponents for d steps, kFar for what has no weight.
+constexpr int32_t kFar = 1 << 20;
+__device__ __forceinline__ int32_t exponent_bin(uint32_t d) { return d < kCut ? static_cast<int32_t>((d + 63) >> 1) : kFar; }
 // The part of its bin that element i of a pair lies in, behind the bin: smaller above.
-__device__ __forceinline__ int32_t fine_code(uint64_t p, uint64_t t, int32_t d, int i) {
+__device__ __forceinline__ int32_t fine_code(uint64_t p, uint64_t t, uint32_t d, int i) {
+  if (d >= kCut) return kFar * kFine;
   const float v = __uint_as_float(static_cast<uint32_t>(p >> (32 * i))), c = __uint_as_float(static_cast<uint32_t>(t >> (32 * i)));
   const float f = v - (c - kMagic);   // exact, within 2^-7: 128 parts of a 64th
   const int32_t part = min(max(static_cast<int32_t>((f + 0x1p-7f) * 0x1p13f), 0), kFine / 2 - 1);
-  return (d + 63) * (kFine / 2) + (kFine / 2 - 1 - part);
+  return static_cast<int32_t>(d + 63) * (kFine / 2) + (kFine / 2 - 1 - part);
 }
 
 // Weights of two logits: 2^p is a power of two, a table entry of 6 bits and exp(g) - 1 of
 // the rest g, |g| <= 2^-7.5, whose leading term is kept apart so that integers hold it to
-// 2^-37.  m: 16 leading bits of a weight before its shift by the power of two.  The last bit
+// 2^-37.  m: the weight before its shift by the power of two, 2^62 .. 2^63.  The last bit
 // of a weight stands for all below it (it is always set), so roundings have no direction.
 // Measured against 64 bits: off by 2^-38.2 in the mean square, 2^-36.2 at most.
 struct Weights {
-  uint64_t w[2];
-  uint32_t m[2];
-  int32_t d[2];
+  uint64_t w[2], m[2];
+  uint32_t d[2];
 };
 __device__ __forceinline__ void weights(float x0, float x1, const Row &r, const Exp2 *table, Weights &out) {
   constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;
@@ -130,7 +131,7 @@ __device__ __forceinline__ void weights(float x0, float x1, const Row &r, const 
   exponents(x0, x1, r, p, lo);
   steps(p, r, t, out.d);
   const Exp2 *const column = table + (threadIdx.x & (kColumns - 1));
-  const Exp2 e0 = column[(-out.d[0] & 63) * kColumns], e1 = column[(-out.d[1] & 63) * kColumns];
+  const Exp2 e0 = column[(0u - out.d[0] & 63u) * kColumns], e1 = column[(0u - out.d[1] & 63u) * kColumns];
   const uint64_t one = pack2(1.0f, 1.0f), minus = pack2(-1.0f, -1.0f), ln2 = pack2(kLn2Hi, kLn2Hi);
   lo = pack2(__uint_as_float(static_cast<uint32_t>(lo)) - e0.off, __uint_as_float(static_cast<uint32_t>(lo >> 32)) - e1.off);
   const uint64_t f = fma2(fma2(t, one, pack2(-kMagic, -kMagic)), minus, p);   // p less its 64ths
@@ -147,8 +148,8 @@ __device__ __forceinline__ void weights(float x0, float x1, const Row &r, const 
                        (static_cast<int32_t>(static_cast<uint32_t>(tail >> (32 * i))) - __float_as_int(kTail));
     const int32_t e = i == 0 ? e0.t : e1.t;
     const uint64_t w = (static_cast<uint64_t>(static_cast<uint32_t>(e) << 5) << 32) + static_cast<uint64_t>(static_cast<int64_t>(e) * gi);
-    out.m[i] = static_cast<uint32_t>(w >> 47);
-    out.w[i] = out.d[i] < kCut ? w >> (((out.d[i] + 63) >> 6) + 18) | 1ull : 0ull;
+    out.m[i] = w;
+    out.w[i] = out.d[i] < kCut ? w >> ((out.d[i] + 63 + 18 * 64) >> 6) | 1ull : 0ull;
   }
 }
 __device__ __noinline__ uint64_t weight(float x, const Row &r, const Exp2 *table) {   // one, where they are few
@@ -168,7 +169,7 @@ template <>
 struct Quad<float> {
   using Vec = float4;
   static __device__ __forceinline__ float one(float v) { return v; }
-  static constexpr int kListMost = 1024;   // a list that lies beside the row
+  static constexpr int kListMost = 768;    // a list within the histogram's second half
   static __device__ __forceinline__ void get(const Vec &v, float (&x)[4]) {
     x[0] = v.x;
     x[1] = v.y;
@@ -208,7 +209,7 @@ struct Shared {
   static constexpr int kSegment = Quad<T>::kListMost / 16;   // candidates of a warp
   Told told[kCtas];
   Params params;
-  uint32_t octave[kCtas][kOctaveBins];   // sums of the exponents' bins
+  float octave[kCtas][kOctaveBins];      // sums of the exponents' bins
   uint16_t count[kRanges];               // candidates of every warp
   T logit[kWarps][kSegment];             // this CTA's, and their places in the warp's range, by place
   uint16_t place[kWarps][kSegment];
@@ -345,8 +346,8 @@ __device__ __forceinline__ uint64_t ceil_product(float p, uint64_t z) {
   return __umul64hi(f, z) + (f == 0 || f * z != 0 ? 1 : 0);
 }
 
-__device__ __forceinline__ void clear_hist(uint32_t *hist) {
-  for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) hist[i] = 0;
+__device__ __forceinline__ void clear_hist(uint32_t *hist, int n) {
+  for (int i = threadIdx.x; i < n; i += kThreads) hist[i] = 0;
 }
 __device__ __forceinline__ void add_to_hist(uint32_t *hist, uint32_t bin, uint64_t w) {   // 64 bits from two words
   const uint32_t lo = static_cast<uint32_t>(w), was = atomicAdd(&hist[bin], lo);
@@ -374,13 +375,15 @@ __device__ __noinline__ Found find_bin(bool mass, int ctas, uint32_t *hist, Scra
   return s.found;
 }
 
-// The octaves' sums of this CTA's bins of exponents, to all CTAs: octave[rank] there.
-__device__ __noinline__ void push_octaves(const uint32_t *hist, uint32_t (*octave)[kOctaveBins]) {
+// The octaves' sums of this CTA's bins of exponents, to all CTAs: octave[rank] there.  Bins in
+// units of the first words; `low`: what a unit of the second words is (0: there are none).
+__device__ __noinline__ void push_octaves(const uint32_t *hist, float low, float (*octave)[kOctaveBins]) {
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = warp; o < kOctaveBins; o += kWarps) {
-    const uint32_t v = __reduce_add_sync(0xffffffffu, hist[o * 32 + lane]);
+    float v = static_cast<float>(__reduce_add_sync(0xffffffffu, hist[o * 32 + lane]));
+    if (low != 0.0f) v = fmaf(static_cast<float>(__reduce_add_sync(0xffffffffu, hist[kYBins + o * 32 + lane])), low, v);
     if (lane < kCtas) cg::this_cluster().map_shared_rank(octave, lane)[cg::this_cluster().block_rank()][o] = v;
   }
 }
@@ -408,23 +411,22 @@ __device__ __forceinline__ Reached reach_in_warp(float v, float want) {
 }
 
 // The bin of exponents, from the largest, at which the running sum over all CTAs reaches
-// `want`, and the sum of all: first the octave, then its bin, so that a thread reads one word
-// of another CTA.  In fp32: counts below 2^24 are exact; sums of weights' leading bits
-// (mass, in units of 2^-16 of the largest) may miss a border that lies close to an end of
-// its bin, which the exact sums behind it find out.
+// `want`, and the sum of all: first the octave, then its bin, so that a thread reads one bin
+// of another CTA.  In fp32: counts below 2^24 are exact; masses (low != 0) may miss a border
+// that lies within 2^-23 of an end of its bin, which the exact sums behind it find out.
 struct Exponent {
   int32_t bin;
   float all;
 };
-__device__ __noinline__ Exponent find_exponent(bool mass, const uint32_t *hist, const uint32_t (*octave)[kOctaveBins], float *sum, float want) {
+__device__ __noinline__ Exponent find_exponent(float low, const uint32_t *hist, const float (*octave)[kOctaveBins], float *sum, float want) {
   static_assert(kOctaveBins > 32 && kOctaveBins <= 64, "one or two octaves a lane");
   const int tid = threadIdx.x, lane = tid & 31;
-  const auto scaled = [&](float v, int o) { return mass ? v * __uint_as_float(static_cast<uint32_t>(127 - o) << 23) : v; };
+  const auto scaled = [&](float v, int o) { return low != 0.0f ? v * __uint_as_float(static_cast<uint32_t>(127 - o) << 23) : v; };
   float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
   for (int c = 0; c < kCtas; ++c) {
-    v0 += static_cast<float>(octave[c][lane]);
-    if (lane + 32 < kOctaveBins) v1 += static_cast<float>(octave[c][lane + 32]);
+    v0 += octave[c][lane];
+    if (lane + 32 < kOctaveBins) v1 += octave[c][lane + 32];
   }
   Reached r = reach_in_warp(scaled(v0, lane), want);
   const Reached far = reach_in_warp(scaled(v1, lane + 32), want - r.all);
@@ -437,7 +439,9 @@ __device__ __noinline__ Exponent find_exponent(bool mass, const uint32_t *hist, 
     before = r.all + far.before;
   }
   if (tid < 32 * kCtas) {
-    float v = static_cast<float>(cg::this_cluster().map_shared_rank(hist, tid % kCtas)[o * 32 + tid / kCtas]);
+    const uint32_t *const h = cg::this_cluster().map_shared_rank(hist, tid % kCtas) + o * 32 + tid / kCtas;
+    float v = static_cast<float>(*h);
+    if (low != 0.0f) v = fmaf(static_cast<float>(h[kYBins]), low, v);
 #pragma unroll
     for (int k = kCtas / 2; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
     if (tid % kCtas == 0) sum[tid / kCtas] = scaled(v, o);
@@ -466,7 +470,7 @@ __device__ __noinline__ uint64_t descend_list(bool mass, const uint64_t *list, i
   while (shift > 0) {
     const int known = shift, bits = min(kDigit, shift);
     shift -= bits;
-    clear_hist(hist);
+    clear_hist(hist, 3 * kBins);
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const uint64_t c = list[i];
@@ -490,27 +494,38 @@ __device__ __noinline__ uint64_t descend_list(bool mass, const uint64_t *list, i
   return prefix;
 }
 
+// The histograms, the list (in the second half of them where it fits), the row.
+template <typename T>
+__host__ __device__ constexpr size_t list_offset() {
+  return Quad<T>::kListMost * sizeof(uint64_t) <= kYBins * sizeof(uint32_t) ? kYBins * sizeof(uint32_t) : 2 * kYBins * sizeof(uint32_t);
+}
+template <typename T>
+__host__ __device__ constexpr size_t fixed_smem() {
+  const size_t list = list_offset<T>() + Quad<T>::kListMost * sizeof(uint64_t), hist = 2 * kYBins * sizeof(uint32_t);
+  return list > hist ? list : hist;
+}
+
 // kTopK, kTopP: the rows may have these filters.
 template <typename T, bool kTopK, bool kTopP>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
   using Q = Quad<T>;
   using Vec = typename Q::Vec;
   using Pub = Shared<T>;
-  constexpr int kListMost = Q::kListMost, kChunk = kListMost / kThreads;
+  constexpr int kListMost = Q::kListMost, kChunk = (kListMost + kThreads - 1) / kThreads;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  uint32_t *const hist = reinterpret_cast<uint32_t *>(smem_raw);                     // [3][kBins]
-  uint64_t *const list = reinterpret_cast<uint64_t *>(hist + 3 * kBins);             // [kListMost] composites, by index
-  T *const data = reinterpret_cast<T *>(list + kListMost);
+  uint32_t *const hist = reinterpret_cast<uint32_t *>(smem_raw);                     // [2][kYBins], [3][kBins] in descents
+  uint64_t *const list = reinterpret_cast<uint64_t *>(smem_raw + list_offset<T>());  // [kListMost] composites, by index
+  T *const data = reinterpret_cast<T *>(smem_raw + fixed_smem<T>());
   __shared__ Pub mine;
   __shared__ Scratch s;
   __shared__ Row r;
   __shared__ __align__(8) Exp2 table[64 * kColumns];
   __shared__ unsigned long long warp_best[kWarps];
   __shared__ uint64_t warp_kept[kWarps], warp_above[kWarps];
-  __shared__ uint64_t range_at[kRanges + 1];
+  __shared__ uint64_t cta_at[kCtas + 1];
   __shared__ int32_t list_at[kRanges + 1];
   __shared__ uint64_t tile_sum[2 * kWarps];
-  static_assert(kYBins <= 3 * kBins && kThreads * sizeof(uint64_t) <= 3 * kBins * sizeof(uint32_t) && kFine <= kBins, "what hist holds by turns");
+  static_assert(kYBins == 3 * kBins && kThreads * sizeof(uint64_t) <= 3 * kBins * sizeof(uint32_t) && kFine <= kBins, "what hist holds by turns");
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
@@ -524,19 +539,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   cluster.barrier_arrive();
   for (int i = tid; i < 64 * kColumns; i += kThreads) table[i] = kExp2.v[i / kColumns];
-  clear_hist(hist);
-  if (rank == 0 && warp == 0) {
-    Params v;
-    v.live = a.p.rows == nullptr || row < *a.p.rows;
-    v.temperature = a.p.temperature != nullptr ? a.p.temperature[row] : 1.0f;
-    const double c = 1.4426950408889634 / static_cast<double>(fminf(fmaxf(v.temperature, 0x1p-60f), 0x1p60f));
-    v.c_hi = static_cast<float>(c);
-    v.c_lo = static_cast<float>(c - static_cast<double>(v.c_hi));
-    v.top_k = kTopK ? a.p.top_k[row] : 0;
-    v.top_p = kTopP ? a.p.top_p[row] : 1.0f;
-    v.min_p = a.p.min_p != nullptr ? a.p.min_p[row] : 0.0f;
-    v.u = a.p.u[row];
-    mine.params = v;
+  clear_hist(hist, 2 * kYBins);
+  Params par{};
+  if (rank == 0 && warp == 0) {   // every lane the same; used behind the row's loads
+    par.live = a.p.rows == nullptr || row < *a.p.rows;
+    par.temperature = a.p.temperature != nullptr ? a.p.temperature[row] : 1.0f;
+    par.top_k = kTopK ? a.p.top_k[row] : 0;
+    par.top_p = kTopP ? a.p.top_p[row] : 1.0f;
+    par.min_p = a.p.min_p != nullptr ? a.p.min_p[row] : 0.0f;
+    par.u = a.p.u[row];
   }
 
   // the row, once, and its largest element (the first of several)
@@ -579,6 +590,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     best = b > best ? b : best;
   }
   if (lane == 0) warp_best[warp] = best;
+  if (rank == 0 && warp == 0) {
+    // c = log2(e) / T in two terms
+    constexpr float kHi = 0x1.715476p+0f, kLo = 0x1.4ae0cp-26f;
+    const float T_used = fminf(fmaxf(par.temperature, 0x1p-60f), 0x1p60f);
+    par.c_hi = kHi / T_used;
+    par.c_lo = (fmaf(-par.c_hi, T_used, kHi) + kLo) / T_used;
+  }
   __syncthreads();
   if (warp == 0) {
     best = warp_best[lane & (kWarps - 1)];
@@ -592,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (warp == 0 && lane < kCtas) {
     Pub *const to = cluster.map_shared_rank(&mine, lane);
     to->told[rank].best = best;
-    if (rank == 0 && lane != 0) to->params = mine.params;
+    if (rank == 0) to->params = par;
   }
   cluster.sync();
   best = 0;
@@ -625,15 +643,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   local.c_hi = mine.params.c_hi;
   local.c_lo = mine.params.c_lo;
   local.ref = fabsf(local.top * local.c_hi) <= 128.0f ? 0.0f : local.top;
-  local.floor = -INFINITY;
   local.top_bits = 0;
   {
     uint64_t p, lo, t;
-    int32_t d[2];
+    uint32_t d[2];
     exponents(local.top, local.top, local, p, lo);
     steps(p, local, t, d);
-    local.top_bits = -d[0];
-    local.floor = __uint_as_float(static_cast<uint32_t>(p)) - 64.0f;
+    local.top_bits = 0u - d[0];
   }
   local.least = 1;
   if (tid == 0) r = local;   // for what is not inlined
@@ -654,6 +670,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       f(t, x);
     }
   };
+  // the warp's kept weights
+  const auto kept_sums = [&](const Row &q, uint64_t threshold) {
+    uint64_t sum = 0;
+    each_tile([&](int t, const float (&x)[4]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        Weights v;
+        weights(x[2 * h], x[2 * h + 1], q, table, v);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (v.w[i] >= q.least && (!(kTopK || kTopP) || threshold == 0 || composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) >= threshold)) sum += v.w[i];
+      }
+    });
+    return warp_total(sum);
+  };
   const uint64_t f_u = u > 0.0f ? (u < 1.0f ? static_cast<uint64_t>(u * 0x1p64f) : ~0ull) : 0ull;
   uint64_t threshold = 0;   // composite of the last kept element
 
@@ -664,6 +695,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const uint64_t low = kTopK ? threshold : 0;   // top-p's elements are those >= low
     const auto among = [&](uint64_t c) { return !kTopK || c >= low; };
     uint64_t sum = 0;
+    // leading bits of a weight in two words of the histogram, as many as this CTA's elements leave room for
+    const int lead = __clz(kWarps * len);
     if (mass) {
       each_tile([&](int t, const float (&x)[4]) {
 #pragma unroll
@@ -674,7 +707,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           for (int i = 0; i < 2; ++i) {
             if (v.d[i] < kCut && (!kTopK || low == 0 || among(composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i)))) {
               sum += v.w[i];
-              atomicAdd(&hist[(v.d[i] + 63) >> 1], v.m[i] | 1u);
+              uint32_t *const bin = hist + ((v.d[i] + 63) >> 1);
+              const uint64_t m = v.m[i] << 1;   // the leading bit on top
+              atomicAdd(bin, static_cast<uint32_t>(m >> 32) >> (32 - lead));
+              atomicAdd(bin + kYBins, (static_cast<uint32_t>(m >> (64 - 2 * lead)) & ((1u << lead) - 1)) | 1u);
             }
           }
         }
@@ -686,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint64_t p, lo, t;
-          int32_t d[2];
+          uint32_t d[2];
           exponents(x[2 * h], x[2 * h + 1], local, p, lo);
           steps(p, local, t, d);
 #pragma unroll
@@ -695,7 +731,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
       });
     }
-    push_octaves(hist, mine.octave);
+    const float low_unit = mass ? __uint_as_float(static_cast<uint32_t>(127 - lead) << 23) : 0.0f;
+    push_octaves(hist, low_unit, mine.octave);
     if (mass && warp == 0) {
       sum = warps_total(warp_above);
       if (lane < kCtas) cluster.map_shared_rank(&mine, lane)->told[rank].all = sum;
@@ -708,11 +745,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       for (int c = 0; c < kCtas; ++c) z += mine.told[c].all;
       want = ceil_product(top_p, z);
     }
-    const Exponent ex = find_exponent(mass, hist, mine.octave, s.bin, mass ? static_cast<float>(want) * 0x1p-29f : static_cast<float>(want));
+    const Exponent ex = find_exponent(low_unit, hist, mine.octave, s.bin,
+                                      mass ? static_cast<float>(want) * __uint_as_float(static_cast<uint32_t>(127 + lead - 45) << 23) : static_cast<float>(want));
     const int32_t border = ex.bin;
     if (!mass && ex.all <= static_cast<float>(want)) {   // all that have a weight are kept
       cluster.sync();               // nobody reads the histogram any more
-      clear_hist(hist);
+      clear_hist(hist, 2 * kYBins);
       __syncthreads();
       continue;
     }
@@ -725,18 +763,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     for (int round = 0; round < 2; ++round) {
       from_top = !mass && round == 0;
       uint64_t above = 0, kept = 0;
+      if (mass && local.least == 1) {   // this CTA's weights above: from its histogram
+        if (round == 0) {
+#pragma unroll
+          for (int k = 0; k < kYBins / kThreads; ++k) {
+            const int b = tid + k * kThreads, o = b >> 5;
+            if (b >= border) continue;
+            const uint64_t m = (static_cast<uint64_t>(hist[b]) << lead) + hist[kYBins + b];   // units of 2^(o + 1 - 2 lead)
+            const int down = o + 2 * lead - 45;   // to 2^-44
+            above += down > 0 ? (m + (1ull << down >> 1)) >> down : m << -down;
+          }
+        } else {
+          const int b = kBins - 1 - tid;
+          if (b > kBins - 1 - fine) above = (static_cast<uint64_t>(hist[kBins + b]) << 32) + hist[b];
+          if (tid == 0) above += mine.told[rank].above;
+        }
+        kept = above;
+      }
       n = 0;
       each_tile([&](int t, const float (&x)[4]) {
         int32_t code[4];   // the bin, and its part in the second round: smaller above
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint64_t p, lo, b;
-          int32_t d[2];
+          uint32_t d[2];
           exponents(x[2 * h], x[2 * h + 1], local, p, lo);
           steps(p, local, b, d);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            code[2 * h + i] = (d[i] + 63) >> 1;
+            code[2 * h + i] = exponent_bin(d[i]);
             if (round == 1) code[2 * h + i] = fine_code(p, b, d[i], i);
           }
         }
@@ -750,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (!mass) {
           above += __popc(higher);
           if (from_top) take |= higher;
-        } else if (__any_sync(0xffffffffu, higher != 0)) {
+        } else if (local.least > 1 && __any_sync(0xffffffffu, higher != 0)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             Weights v;
@@ -823,18 +878,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (listed || round == 1 || over >= want) break;
 
       // too many: the bin's parts
-      clear_hist(hist);
+      clear_hist(hist, 3 * kBins);
       __syncthreads();
       each_tile([&](int t, const float (&x)[4]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint64_t p, lo, b;
-          int32_t d[2];
+          uint32_t d[2];
           exponents(x[2 * h], x[2 * h + 1], local, p, lo);
           steps(p, local, b, d);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if ((d[i] + 63) >> 1 != border) continue;
+            if (exponent_bin(d[i]) != border) continue;
             if (kTopK && low != 0 && !among(composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i))) continue;
             const uint32_t bin = kBins - 1 - fine_code(p, b, d[i], i) % kFine;
             if (mass) add_to_hist(hist, bin, weight(x[2 * h + i], r, table));
@@ -952,27 +1007,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         return;
       }
       if (mass && found) {
-        // up to each range: the list's kept weights before it
+        // up to each CTA's part: the list's kept weights before it
         __syncthreads();
-        if (tid <= kRanges) {
-          const int i = list_at[tid], t = i / chunk;
+        if (tid <= kCtas) {
+          const int i = list_at[tid * kWarps], t = i / chunk;
           uint64_t at = t < kThreads ? part[t] : list_total;
 #pragma unroll 1
           for (int j = t * chunk; j < i; ++j) at += kept_weight(j);
-          range_at[tid] = at;
+          cta_at[tid] = at;
         }
         __syncthreads();
-        uint64_t all = list_total, reach = range_at[rank * kWarps];
+        uint64_t all = list_total, reach = cta_at[rank];
         for (int c = 0; c < kCtas; ++c) {
           all += mine.told[c].kept;
           if (c < rank) reach += mine.told[c].kept;
         }
-        const uint64_t at = __umul64hi(f_u, all);
-        const uint64_t here = mine.told[rank].kept + range_at[(rank + 1) * kWarps] - range_at[rank * kWarps];
+        const uint64_t at = __umul64hi(f_u, all), here = mine.told[rank].kept + cta_at[rank + 1] - cta_at[rank];
         if (at >= reach && at < reach + here) {
-          if (tid < kWarps) warp_kept[tid] += range_at[rank * kWarps + tid + 1] - range_at[rank * kWarps + tid];
+          // this CTA's kept weights exactly (the histogram's may differ in the last units)
+          const uint64_t kept = kept_sums(local, threshold);
+          if (lane == 0) warp_kept[warp] = kept;
           __syncthreads();
-          pick<T>(a, row, data, rank, warp_kept, reach, at, threshold, all, r, table, tile_sum);
+          uint64_t exact = 0;
+          for (int v = 0; v < kWarps; ++v) exact += warp_kept[v];
+          pick<T>(a, row, data, rank, warp_kept, 0, min(at - reach, exact - 1), threshold, all, r, table, tile_sum);
         }
         cluster.barrier_wait();
         return;
@@ -987,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const int known = shift, bits = min(kDigit, shift);
         shift -= bits;
         cluster.sync();   // nobody reads the histogram any more
-        clear_hist(hist);
+        clear_hist(hist, 3 * kBins);
         __syncthreads();
         each_tile([&](int t, const float (&x)[4]) {
 #pragma unroll
@@ -1007,23 +1065,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       threshold = prefix;
     }
     cluster.sync();   // nobody reads what is written next
-    clear_hist(hist);
+    clear_hist(hist, 2 * kYBins);
     __syncthreads();
   }
 
   // the kept weights of the row
-  uint64_t sum = 0;
-  each_tile([&](int t, const float (&x)[4]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      Weights v;
-      weights(x[2 * h], x[2 * h + 1], local, table, v);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (v.w[i] >= local.least && (!(kTopK || kTopP) || threshold == 0 || composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) >= threshold)) sum += v.w[i];
-    }
-  });
-  sum = warp_total(sum);
+  uint64_t sum = kept_sums(local, threshold);
   if (lane == 0) warp_kept[warp] = sum;
   __syncthreads();
   if (warp == 0) {
@@ -1042,11 +1089,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const uint64_t at = __umul64hi(f_u, total);
   if (at >= reach && at < reach + here)
     pick<T>(a, row, data, rank, warp_kept, reach, at, threshold, total, r, table, tile_sum);
-}
-
-template <typename T>
-constexpr size_t fixed_smem() {
-  return 3 * kBins * sizeof(uint32_t) + Quad<T>::kListMost * sizeof(uint64_t);
 }
 
 template <typename T, bool kTopK, bool kTopP>
