@@ -131,9 +131,10 @@ struct WriteKvArgs {
 struct NormRopeArgs {
   idx_norm_rope_args p;
   idx_kv_cache c;          // k null: no cache
-  int32_t heads;           // heads of a warp; set by the launcher, like the counts below
-  int32_t q_jobs, k_jobs;  // warps of a row for its q heads, and for its k heads
-  int32_t jobs;            // with those for v
+  // set by the launcher
+  int32_t heads;                    // of a unit: a warp's work at a time, of one row and kind
+  int32_t q_units, k_units, units;  // of a row: its q heads, its k heads, with those for v
+  int32_t group_rows, splits;       // rows of a group, CTAs that share it
 };
 
 struct SampleArgs {
