@@ -153,86 +153,108 @@ __device__ __forceinline__ void store(uint16_t *head, const Place &at, const uin
 struct Factors {
   uint64_t aa[2], ab[2], bb[2], ba[2], ca[2], cb[2];
 };
+// Four values of a lane's pairs from an array by dimension: halves, runs of four at a and b;
+// interleaved, eight from a on.
+template <bool kInterleaved>
+__device__ __forceinline__ Pairs by_pairs(const Place &at, const float *v) {
+  const float4 x = *reinterpret_cast<const float4 *>(v + at.a), y = *reinterpret_cast<const float4 *>(v + (kInterleaved ? at.a + 4 : at.b));
+  Pairs p;
+  if constexpr (kInterleaved) {
+    p.a[0] = pack2(x.x, x.z);
+    p.b[0] = pack2(x.y, x.w);
+    p.a[1] = pack2(y.x, y.z);
+    p.b[1] = pack2(y.y, y.w);
+  } else {
+    p.a[0] = pack2(x.x, x.y);
+    p.a[1] = pack2(x.z, x.w);
+    p.b[0] = pack2(y.x, y.y);
+    p.b[1] = pack2(y.z, y.w);
+  }
+  return p;
+}
 // cs: the row's (cos, sin) per frequency; w, b: the head's weights and biases in shared memory.
 template <bool kInterleaved, bool kBias>
 __device__ __forceinline__ void make_factors(const Place &at, const float2 *cs, const float *w, const float *b, Factors &f) {
-  constexpr int kStep = kInterleaved ? 2 : 1;
-  const int first = kInterleaved ? at.a / 2 : at.a;   // of the lane's frequencies
+  float4 t[2] = {make_float4(1.0f, 0.0f, 1.0f, 0.0f), make_float4(1.0f, 0.0f, 1.0f, 0.0f)};
+  if (at.turns) {
+    const float4 *const from = reinterpret_cast<const float4 *>(cs + (kInterleaved ? at.a / 2 : at.a));   // four frequencies
+    t[0] = from[0];
+    t[1] = from[1];
+  }
+  const Pairs v = by_pairs<kInterleaved>(at, w);
+  Pairs u{};
+  if constexpr (kBias) u = by_pairs<kInterleaved>(at, b);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float2 t[2] = {make_float2(1.0f, 0.0f), make_float2(1.0f, 0.0f)};
-    if (at.turns) {
-      t[0] = cs[first + 2 * h];
-      t[1] = cs[first + 2 * h + 1];
-    }
-    const uint64_t c = pack2(t[0].x, t[1].x), s = pack2(t[0].y, t[1].y), m = pack2(-t[0].y, -t[1].y);
-    const uint64_t wa = pack2(w[at.a + kStep * 2 * h], w[at.a + kStep * (2 * h + 1)]);
-    const uint64_t wb = pack2(w[at.b + kStep * 2 * h], w[at.b + kStep * (2 * h + 1)]);
-    f.aa[h] = mul2(wa, c);
-    f.ab[h] = mul2(wb, m);
-    f.bb[h] = mul2(wb, c);
-    f.ba[h] = mul2(wa, s);
+    const uint64_t c = pack2(t[h].x, t[h].z), s = pack2(t[h].y, t[h].w), m = pack2(-t[h].y, -t[h].w);
+    f.aa[h] = mul2(v.a[h], c);
+    f.ab[h] = mul2(v.b[h], m);
+    f.bb[h] = mul2(v.b[h], c);
+    f.ba[h] = mul2(v.a[h], s);
     if (!at.turns) f.ab[h] = f.ba[h] = both(-0.0f);   // times 0: adds nothing, a zero's sign included
     if constexpr (kBias) {
-      const uint64_t va = pack2(b[at.a + kStep * 2 * h], b[at.a + kStep * (2 * h + 1)]);
-      const uint64_t vb = pack2(b[at.b + kStep * 2 * h], b[at.b + kStep * (2 * h + 1)]);
-      f.ca[h] = at.turns ? fma2(vb, m, mul2(va, c)) : va;
-      f.cb[h] = at.turns ? fma2(va, s, mul2(vb, c)) : vb;
+      f.ca[h] = at.turns ? fma2(u.b[h], m, mul2(u.a[h], c)) : u.a[h];
+      f.cb[h] = at.turns ? fma2(u.a[h], s, mul2(u.b[h], c)) : u.b[h];
     }
   }
 }
 
-// The normed and rotated head of a lane's eight values.  The whole warp calls.
-template <int D, bool kInterleaved, bool kBias>
-__device__ __forceinline__ Pairs turn(const uint4 &raw, const Factors &f, int norm, float eps, bool all_turn, bool turns) {
+// Deviations from the mean (kMean) and the mean of their squares.
+template <int D, bool kMean>
+__device__ __forceinline__ float spread(Pairs &x) {
   constexpr int kLanes = D / 8;
-  Pairs x = unpack<kInterleaved>(raw);
-  float inv = 1.0f;
-  if (norm != IDX_NORM_NONE) {
-    float scale = 1.0f;
-    for (;;) {
-      float mean = 0.0f;
-      Pairs d = x;
-      if (kBias && norm == IDX_NORM_LAYER) {
-        float s = 0.0f;
+  if constexpr (kMean) {
+    const uint64_t one = both(1.0f), t = fma2(fma2(x.a[0], one, x.a[1]), one, fma2(x.b[0], one, x.b[1]));
+    const uint64_t minus = both(group_sum<kLanes>(low(t) + high(t)) * (-1.0f / D));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) s += low(x.a[h]) + high(x.a[h]) + (low(x.b[h]) + high(x.b[h]));
-        mean = group_sum<kLanes>(s) * (1.0f / D);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          d.a[h] = fma2(both(-mean), both(1.0f), x.a[h]);
-          d.b[h] = fma2(both(-mean), both(1.0f), x.b[h]);
-        }
-      }
-      uint64_t q = mul2(d.a[0], d.a[0]);
-      q = fma2(d.a[1], d.a[1], q);
-      q = fma2(d.b[0], d.b[0], q);
-      q = fma2(d.b[1], d.b[1], q);
-      const float s = group_sum<kLanes>(low(q) + high(q)) * (1.0f / D);
-      // squares past fp32's range: once more with the head scaled down by 2^80, beside which
-      // eps is nothing.  (A true infinity or NaN comes out the same way the second time.)
-      const bool again = scale == 1.0f && !(s <= 3.402823466e38f);
-      if (__any_sync(0xffffffffu, again)) {
-        if (again) {
-          scale = 0x1p-80f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            x.a[h] = mul2(x.a[h], both(scale));
-            x.b[h] = mul2(x.b[h], both(scale));
-          }
-        }
-        continue;
-      }
-      inv = rsqrtf(scale == 1.0f ? s + eps : s);
-      x = d;
-      break;
+    for (int h = 0; h < 2; ++h) {
+      x.a[h] = fma2(x.a[h], one, minus);
+      x.b[h] = fma2(x.b[h], one, minus);
     }
   }
+  const uint64_t q = fma2(x.b[1], x.b[1], fma2(x.b[0], x.b[0], fma2(x.a[1], x.a[1], mul2(x.a[0], x.a[0]))));
+  return group_sum<kLanes>(low(q) + high(q)) * (1.0f / D);
+}
+
+// x of kAtATime heads to their normed values but for weights and biases.  The whole warp calls.
+template <int D, bool kMean, int kAtATime>
+__device__ __forceinline__ void normed(Pairs (&x)[kAtATime], const uint4 (&raw)[kAtATime], bool interleaved, float eps, float (&inv)[kAtATime]) {
+  float s[kAtATime];
+  bool again = false;
+#pragma unroll
+  for (int k = 0; k < kAtATime; ++k) {
+    s[k] = spread<D, kMean>(x[k]);
+    again = again || !(s[k] <= 3.402823466e38f);
+    inv[k] = rsqrtf(s[k] + eps);
+  }
+  // Squares past fp32's range: once more with the head scaled down by 2^80, beside which eps is
+  // nothing.  (A true infinity or NaN comes out the same way the second time.)
+  if (__any_sync(0xffffffffu, again)) {
+#pragma unroll
+    for (int k = 0; k < kAtATime; ++k) {
+      Pairs y = interleaved ? unpack<true>(raw[k]) : unpack<false>(raw[k]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        y.a[h] = mul2(y.a[h], both(0x1p-80f));
+        y.b[h] = mul2(y.b[h], both(0x1p-80f));
+      }
+      const float t = spread<D, kMean>(y);
+      if (!(s[k] <= 3.402823466e38f)) {
+        x[k] = y;
+        inv[k] = rsqrtf(t);
+      }
+    }
+  }
+}
+
+// A head's values turned by their factors.
+template <bool kBias>
+__device__ __forceinline__ Pairs turned(const Pairs &x, const Factors &f, float inv, bool crosses) {
   Pairs z;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     // where nothing turns, the other's factor is 0: an infinite other must not make it NaN
-    const uint64_t oa = all_turn || turns ? x.b[h] : 0, ob = all_turn || turns ? x.a[h] : 0;
+    const uint64_t oa = crosses ? x.b[h] : 0, ob = crosses ? x.a[h] : 0;
     const uint64_t ta = fma2(x.a[h], f.aa[h], mul2(oa, f.ab[h])), tb = fma2(x.b[h], f.bb[h], mul2(ob, f.ba[h]));
     if constexpr (kBias) {
       z.a[h] = fma2(both(inv), ta, f.ca[h]);
@@ -249,8 +271,9 @@ __device__ __forceinline__ Pairs turn(const uint4 &raw, const Factors &f, int no
 template <int D, bool kInterleaved, bool kBias>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
-  __shared__ float2 cs[kMostRows][D / 2];
-  __shared__ __align__(16) float weights[2][D], biases[kBias ? 2 : 1][kBias ? D : 1];   // of q and of k
+  constexpr int kPair = kBias ? 1 : 2;   // heads normed at a time, so that one's sums run beside the other's
+  __shared__ __align__(16) float2 cs[kMostRows][D / 2];
+  __shared__ __align__(16) float weights[2][D], biases[kBias ? 2 : 1][kBias ? D : 4];   // of q and of k
   const idx_norm_rope_args &p = a.p;
   const int tid = threadIdx.x, lane = tid % kLanes, sub = tid % 32 / kLanes, warp = tid / 32;
   const int64_t group = blockIdx.x / a.splits;
@@ -276,102 +299,110 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const _
   __syncthreads();
 
   const Place at = place_of<kInterleaved>(lane, p.rot);
-  const bool f8 = a.c.kv_dtype == IDX_KV_E4M3, all_turn = p.rot == D;
-  for (int unit = part * kWarps + warp; unit < rows * a.units; unit += a.splits * kWarps) {
-    const int r = unit / a.units;
-    int u = unit % a.units;
+  const bool f8 = a.c.kv_dtype == IDX_KV_E4M3, crosses = p.rot == D || at.turns;
+  constexpr int kStep = kAtOnce * D;   // elements from one of a lane's heads to the next
+  int r = 0, u = part * kWarps + warp;
+  for (; u >= a.units; u -= a.units) ++r;
+  while (r < rows) {
     const int64_t row = row0 + r;
-    // the unit's kind and heads
+    // the unit's kind and heads: this lane's are h, h + kAtOnce, ..., `mine` of them
     const int kind = u < a.q_units ? 0 : u < a.q_units + a.k_units ? 1 : 2;
-    u -= kind == 0 ? 0 : kind == 1 ? a.q_units : a.q_units + a.k_units;
-    const int h0 = u * a.heads, h_end = min(h0 + a.heads, kind == 0 ? p.Hq : p.Hkv);
+    const int first = (u - (kind == 0 ? 0 : kind == 1 ? a.q_units : a.q_units + a.k_units)) * a.heads, h = first + sub;
+    const int heads = min(a.heads, (kind == 0 ? p.Hq : p.Hkv) - first), mine = (heads - sub + kAtOnce - 1) / kAtOnce;
+    const uint16_t *const src = static_cast<const uint16_t *>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
+                                row * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride) + h * D;
+    uint4 raw[kVectors];
+#pragma unroll
+    for (int k = 0; k < kVectors; ++k) {
+      raw[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (k < mine) raw[k] = kind == 2 ? __ldcs(reinterpret_cast<const uint4 *>(src + k * kStep + 8 * lane)) : load<kInterleaved>(src + k * kStep, at);
+    }
 
-    // the row's place in the cache
-    bool live = false;
+    // the row's place in the cache, at head h
     char *to = nullptr;
     float *scale = nullptr;
+    bool live = false;
     if (kind != 0 && p.slot != nullptr) {
       const uint32_t slot = static_cast<uint32_t>(p.slot[row]);   // negative slots are large ones
       live = slot < static_cast<uint64_t>(a.c.P) * kPage;
       const int64_t page = slot / kPage, tok = slot % kPage;
-      to = static_cast<char *>(kind == 1 ? a.c.k : a.c.v) + (page * a.c.page_stride + tok * a.c.token_stride) * (f8 ? 1 : 2);
-      scale = f8 ? (kind == 1 ? a.c.k_scale : a.c.v_scale) + page * p.Hkv * kPage + tok : nullptr;
+      to = static_cast<char *>(kind == 1 ? a.c.k : a.c.v) +
+           (page * a.c.page_stride + tok * a.c.token_stride + h * a.c.head_stride) * (f8 ? 1 : 2);
+      scale = f8 ? (kind == 1 ? a.c.k_scale : a.c.v_scale) + (page * p.Hkv + h) * kPage + tok : nullptr;
     }
+    const int64_t to_step = kAtOnce * a.c.head_stride * (f8 ? 1 : 2);
 
     if (kind == 2) {
-      const uint16_t *const src = static_cast<const uint16_t *>(p.v) + row * p.v_stride + 8 * lane;
-      uint4 raw[kVectors];
 #pragma unroll
       for (int k = 0; k < kVectors; ++k) {
-        const int h = h0 + k * kAtOnce + sub;
-        raw[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < h_end) raw[k] = __ldcs(reinterpret_cast<const uint4 *>(src + h * D));
-      }
-#pragma unroll
-      for (int k = 0; k < kVectors; ++k) {
-        const int h = h0 + k * kAtOnce + sub;
-        if (h0 + k * kAtOnce >= h_end) break;   // the warp's lanes together
+        if (k * kAtOnce >= heads) break;   // the warp's lanes together
         if (f8) {
           const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
           uint32_t lo, hi;
           const float sc = quantize(w, vector_amax<kLanes>(w), lo, hi);
-          if (live && h < h_end) {
-            *reinterpret_cast<uint2 *>(to + h * a.c.head_stride + 8 * lane) = make_uint2(lo, hi);
-            if (lane == 0) scale[static_cast<int64_t>(h) * kPage] = sc;
+          if (live && k < mine) {
+            *reinterpret_cast<uint2 *>(to + k * to_step + 8 * lane) = make_uint2(lo, hi);
+            if (lane == 0) scale[k * kAtOnce * kPage] = sc;
           }
-        } else if (live && h < h_end) {
-          *reinterpret_cast<uint4 *>(to + (h * a.c.head_stride + 8 * lane) * 2) = raw[k];
+        } else if (live && k < mine) {
+          *reinterpret_cast<uint4 *>(to + k * to_step + 16 * lane) = raw[k];
         }
       }
-      continue;
-    }
-
-    const uint16_t *const src = static_cast<const uint16_t *>(kind == 0 ? p.q : p.k) + row * (kind == 0 ? p.q_stride : p.k_stride);
-    uint16_t *dst = static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out);
-    if (dst != nullptr) dst += row * (kind == 0 ? p.q_out_stride : p.k_out_stride);
-    uint4 raw[kVectors];
+    } else {
+      uint16_t *dst = static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out);
+      const bool out = dst != nullptr;
+      if (out) dst += row * (kind == 0 ? p.q_out_stride : p.k_out_stride) + h * D;
+      Factors f;
+      make_factors<kInterleaved, kBias>(at, cs[r], weights[kind], kBias ? biases[kind] : nullptr, f);
+      const int norm = kind == 0 ? p.q_norm : p.k_norm;
 #pragma unroll
-    for (int k = 0; k < kVectors; ++k) {
-      const int h = h0 + k * kAtOnce + sub;
-      raw[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < h_end) raw[k] = load<kInterleaved>(src + h * D, at);
-    }
-    Factors f;
-    make_factors<kInterleaved, kBias>(at, cs[r], weights[kind], kBias ? biases[kind] : nullptr, f);
-    const int norm = kind == 0 ? p.q_norm : p.k_norm;
+      for (int k0 = 0; k0 < kVectors; k0 += kPair) {
+        if (k0 * kAtOnce >= heads) break;   // the warp's lanes together
+        Pairs x[kPair];
+        uint4 v[kPair];
+        float inv[kPair];
 #pragma unroll
-    for (int k = 0; k < kVectors; ++k) {
-      const int h = h0 + k * kAtOnce + sub;
-      if (h0 + k * kAtOnce >= h_end) break;   // the warp's lanes together
-      const bool here = h < h_end;
-      const Pairs z = turn<D, kInterleaved, kBias>(raw[k], f, norm, p.eps, all_turn, at.turns);
-      const uint4 out = pack<kInterleaved>(z);
-      if (dst != nullptr && here) store<kInterleaved>(dst + h * D, at, out);
-      if (to == nullptr) continue;
-      if (!f8) {
-        if (live && here) store<kInterleaved>(reinterpret_cast<uint16_t *>(to) + h * a.c.head_stride, at, out);
-        continue;
-      }
-      // eight values in the order of their bytes
-      const float v[8] = {low(z.a[0]), kInterleaved ? low(z.b[0]) : high(z.a[0]), kInterleaved ? high(z.a[0]) : low(z.a[1]),
-                          kInterleaved ? high(z.b[0]) : high(z.a[1]), kInterleaved ? low(z.a[1]) : low(z.b[0]),
-                          kInterleaved ? low(z.b[1]) : high(z.b[0]), kInterleaved ? high(z.a[1]) : low(z.b[1]), high(z.b[1])};
-      float m = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-      uint32_t lo, hi;
-      const float sc = quantize_f32(v, group_max<kLanes>(m), lo, hi);
-      if (live && here) {
-        char *const head = to + h * a.c.head_stride;
-        if (kInterleaved) {
-          *reinterpret_cast<uint2 *>(head + at.a) = make_uint2(lo, hi);
-        } else {
-          *reinterpret_cast<uint32_t *>(head + at.a) = lo;
-          *reinterpret_cast<uint32_t *>(head + at.b) = hi;
+        for (int k = 0; k < kPair; ++k) {
+          v[k] = raw[k0 + k];
+          x[k] = unpack<kInterleaved>(v[k]);
+          inv[k] = 1.0f;
         }
-        if (lane == 0) scale[static_cast<int64_t>(h) * kPage] = sc;
+        if (kBias && norm == IDX_NORM_LAYER) normed<D, true>(x, v, kInterleaved, p.eps, inv);
+        else if (norm != IDX_NORM_NONE) normed<D, false>(x, v, kInterleaved, p.eps, inv);
+#pragma unroll
+        for (int k = 0; k < kPair; ++k) {
+          const Pairs z = turned<kBias>(x[k], f, inv[k], crosses);
+          const uint4 packed = pack<kInterleaved>(z);
+          const bool here = k0 + k < mine;
+          if (out && here) store<kInterleaved>(dst + (k0 + k) * kStep, at, packed);
+          if (to == nullptr) continue;
+          char *const head = to + (k0 + k) * to_step;
+          if (!f8) {
+            if (live && here) store<kInterleaved>(reinterpret_cast<uint16_t *>(head), at, packed);
+            continue;
+          }
+          // eight values in the order of their bytes
+          const float e[8] = {low(z.a[0]), kInterleaved ? low(z.b[0]) : high(z.a[0]), kInterleaved ? high(z.a[0]) : low(z.a[1]),
+                              kInterleaved ? high(z.b[0]) : high(z.a[1]), kInterleaved ? low(z.a[1]) : low(z.b[0]),
+                              kInterleaved ? low(z.b[1]) : high(z.b[0]), kInterleaved ? high(z.a[1]) : low(z.b[1]), high(z.b[1])};
+          float m = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(e[j]));
+          uint32_t lo, hi;
+          const float sc = quantize_f32(e, group_max<kLanes>(m), lo, hi);
+          if (live && here) {
+            if (kInterleaved) {
+              *reinterpret_cast<uint2 *>(head + at.a) = make_uint2(lo, hi);
+            } else {
+              *reinterpret_cast<uint32_t *>(head + at.a) = lo;
+              *reinterpret_cast<uint32_t *>(head + at.b) = hi;
+            }
+            if (lane == 0) scale[(k0 + k) * kAtOnce * kPage] = sc;
+          }
+        }
       }
     }
+    for (u += a.splits * kWarps; u >= a.units; u -= a.units) ++r;
   }
 }
 
