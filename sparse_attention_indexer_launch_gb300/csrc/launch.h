@@ -132,9 +132,9 @@ struct NormRopeArgs {
   idx_norm_rope_args p;
   idx_kv_cache c;          // k null: no cache
   // set by the launcher
-  int32_t heads;                    // of a unit: a warp's work at a time, of one row and kind
-  int32_t q_units, k_units, units;  // of a row: its q heads, its k heads, with those for v
-  int32_t group_rows, splits;       // rows of a group, CTAs that share it
+  int32_t heads;                // of a batch: a warp's loads at a time, of one row and kind
+  int32_t q_units, k_units;     // batches of a row: of its q heads, its k heads
+  int32_t group_rows, splits;   // rows of a group, CTAs that share it
 };
 
 struct SampleArgs {

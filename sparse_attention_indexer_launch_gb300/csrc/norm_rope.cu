@@ -4,12 +4,10 @@
 // A vector of D values (one head of a row) is a group of D / 8 lanes with eight values each,
 // four pairs that turn together, so that the rotation stays within a lane: two runs of four
 // for halves, one of eight for interleaved pairs.  It is read once and written once.  A CTA
-// takes a group of rows, works their angles out once into shared memory, and its warps walk
-// over units of a few heads of a row of one kind (q, k or v).  The rotation is linear in the
-// normed head, y = inv * (x - mean) * w + b, so weight, bias, cosine and sine fold into a
-// unit's factors: for a pair (a, b)
-//     z_a = inv * ((a - mean) w_a c - (b - mean) w_b s) + (b_a c - b_b s),
-// and z_b alike.
+// takes a group of rows, works their angles out once into shared memory, and its warps take
+// batches of a few heads of one row, first of q, then of k, then of v, each in a loop of its
+// own that keeps the head's weights in registers.  Beside memory the call is bound by
+// instructions: everything is done for two values at a time.
 //
 // Angles: positions reach 2^31, where pos * inv_freq in fp32 is off by whole turns.  The
 // frequency in turns, inv_freq / (2 pi), is a fixed-point fraction of 64 bits, and a
@@ -25,9 +23,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kVectors = 4;     // loads of a lane in flight
+constexpr int kVectors = 4;     // heads of a lane in a batch
 constexpr int kMostRows = 8;    // of a CTA's group
-constexpr int kCtasPerSm = 3;
 
 // inv_freq / (2 pi) in units of 2^-64 turn, modulo one turn: the 24-bit significand times
 // 2^64 / (2 pi), shifted by the exponent.
@@ -132,12 +129,17 @@ __device__ __forceinline__ uint4 pack(const Pairs &z) {
     return make_uint4(bf16x2(low(z.a[0]), high(z.a[0])), bf16x2(low(z.a[1]), high(z.a[1])), bf16x2(low(z.b[0]), high(z.b[0])),
                       bf16x2(low(z.b[1]), high(z.b[1])));
 }
-// A lane's eight bf16 values of a head: one load for interleaved pairs, two for halves.
+// Copies a lane's eight bf16 values of a head to its own place in shared memory, asynchronously:
+// one copy, or two for halves.
 template <bool kInterleaved>
-__device__ __forceinline__ uint4 load(const uint16_t *head, const Place &at) {
-  if constexpr (kInterleaved) return __ldcs(reinterpret_cast<const uint4 *>(head + at.a));
-  const uint2 a = __ldcs(reinterpret_cast<const uint2 *>(head + at.a)), b = __ldcs(reinterpret_cast<const uint2 *>(head + at.b));
-  return make_uint4(a.x, a.y, b.x, b.y);
+__device__ __forceinline__ void copy_async(uint4 *to, const uint16_t *head, const Place &at) {
+  const uint32_t dst = smem_u32(to);
+  if constexpr (kInterleaved) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(head + at.a) : "memory");
+  } else {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(head + at.a) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + 8), "l"(head + at.b) : "memory");
+  }
 }
 template <bool kInterleaved>
 __device__ __forceinline__ void store(uint16_t *head, const Place &at, const uint4 &v) {
@@ -149,10 +151,6 @@ __device__ __forceinline__ void store(uint16_t *head, const Place &at, const uin
   }
 }
 
-// A unit's factors for a lane: z_a = inv (x_a aa + x_b ab) + ca, z_b = inv (x_b bb + x_a ba) + cb.
-struct Factors {
-  uint64_t aa[2], ab[2], bb[2], ba[2], ca[2], cb[2];
-};
 // Four values of a lane's pairs from an array by dimension: halves, runs of four at a and b;
 // interleaved, eight from a on.
 template <bool kInterleaved>
@@ -172,33 +170,6 @@ __device__ __forceinline__ Pairs by_pairs(const Place &at, const float *v) {
   }
   return p;
 }
-// cs: the row's (cos, sin) per frequency; w, b: the head's weights and biases in shared memory.
-template <bool kInterleaved, bool kBias>
-__device__ __forceinline__ void make_factors(const Place &at, const float2 *cs, const float *w, const float *b, Factors &f) {
-  float4 t[2] = {make_float4(1.0f, 0.0f, 1.0f, 0.0f), make_float4(1.0f, 0.0f, 1.0f, 0.0f)};
-  if (at.turns) {
-    const float4 *const from = reinterpret_cast<const float4 *>(cs + (kInterleaved ? at.a / 2 : at.a));   // four frequencies
-    t[0] = from[0];
-    t[1] = from[1];
-  }
-  const Pairs v = by_pairs<kInterleaved>(at, w);
-  Pairs u{};
-  if constexpr (kBias) u = by_pairs<kInterleaved>(at, b);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint64_t c = pack2(t[h].x, t[h].z), s = pack2(t[h].y, t[h].w), m = pack2(-t[h].y, -t[h].w);
-    f.aa[h] = mul2(v.a[h], c);
-    f.ab[h] = mul2(v.b[h], m);
-    f.bb[h] = mul2(v.b[h], c);
-    f.ba[h] = mul2(v.a[h], s);
-    if (!at.turns) f.ab[h] = f.ba[h] = both(-0.0f);   // times 0: adds nothing, a zero's sign included
-    if constexpr (kBias) {
-      f.ca[h] = at.turns ? fma2(u.b[h], m, mul2(u.a[h], c)) : u.a[h];
-      f.cb[h] = at.turns ? fma2(u.a[h], s, mul2(u.b[h], c)) : u.b[h];
-    }
-  }
-}
-
 // Deviations from the mean (kMean) and the mean of their squares.
 template <int D, bool kMean>
 __device__ __forceinline__ float spread(Pairs &x) {
@@ -216,66 +187,241 @@ __device__ __forceinline__ float spread(Pairs &x) {
   return group_sum<kLanes>(low(q) + high(q)) * (1.0f / D);
 }
 
+// 1 / sqrt of a normal number, to two units of the last place.
+__device__ __forceinline__ float rsqrt_normal(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A head whose squares pass fp32's range: normed once more, scaled down by 2^80, beside which
+// eps is nothing.  (A true infinity or NaN comes out as it would have.)  The whole warp calls.
+struct Rescued {
+  Pairs x;
+  float inv;
+};
+template <int D, bool kInterleaved, bool kMean>
+__device__ __noinline__ Rescued rescue(uint4 raw) {
+  Rescued r;
+  r.x = unpack<kInterleaved>(raw);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    r.x.a[h] = mul2(r.x.a[h], both(0x1p-80f));
+    r.x.b[h] = mul2(r.x.b[h], both(0x1p-80f));
+  }
+  r.inv = rsqrtf(spread<D, kMean>(r.x));
+  return r;
+}
+
 // x of kAtATime heads to their normed values but for weights and biases.  The whole warp calls.
-template <int D, bool kMean, int kAtATime>
-__device__ __forceinline__ void normed(Pairs (&x)[kAtATime], const uint4 (&raw)[kAtATime], bool interleaved, float eps, float (&inv)[kAtATime]) {
+template <int D, bool kInterleaved, bool kMean, int kAtATime>
+__device__ __forceinline__ void normed(Pairs (&x)[kAtATime], const uint4 (&raw)[kAtATime], float eps, float (&inv)[kAtATime]) {
   float s[kAtATime];
-  bool again = false;
+  bool past = false;
 #pragma unroll
   for (int k = 0; k < kAtATime; ++k) {
     s[k] = spread<D, kMean>(x[k]);
-    again = again || !(s[k] <= 3.402823466e38f);
-    inv[k] = rsqrtf(s[k] + eps);
+    past = past || !(s[k] <= 3.402823466e38f);
+    inv[k] = rsqrt_normal(s[k] + eps);
   }
-  // Squares past fp32's range: once more with the head scaled down by 2^80, beside which eps is
-  // nothing.  (A true infinity or NaN comes out the same way the second time.)
-  if (__any_sync(0xffffffffu, again)) {
+  if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
     for (int k = 0; k < kAtATime; ++k) {
-      Pairs y = interleaved ? unpack<true>(raw[k]) : unpack<false>(raw[k]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        y.a[h] = mul2(y.a[h], both(0x1p-80f));
-        y.b[h] = mul2(y.b[h], both(0x1p-80f));
-      }
-      const float t = spread<D, kMean>(y);
+      const Rescued r = rescue<D, kInterleaved, kMean>(raw[k]);
       if (!(s[k] <= 3.402823466e38f)) {
-        x[k] = y;
-        inv[k] = rsqrtf(t);
+        x[k] = r.x;
+        inv[k] = r.inv;
       }
     }
   }
 }
 
-// A head's values turned by their factors.
-template <bool kBias>
-__device__ __forceinline__ Pairs turned(const Pairs &x, const Factors &f, float inv, bool crosses) {
+// Cosines, sines and negated sines of a row's frequencies, each in a run.
+template <int D>
+struct Turns {
+  float c[D / 2], s[D / 2], m[D / 2];
+};
+// A head's normed values, y, turned, times inv.
+template <int D, bool kInterleaved>
+__device__ __forceinline__ Pairs turned(const Pairs &y, const Turns<D> &t, const Place &at) {
+  if (!at.turns) return y;
+  const int f = kInterleaved ? at.a / 2 : at.a;   // four frequencies
+  const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(t.c + f), s = *reinterpret_cast<const ulonglong2 *>(t.s + f),
+                   m = *reinterpret_cast<const ulonglong2 *>(t.m + f);
   Pairs z;
+  z.a[0] = fma2(y.b[0], m.x, mul2(y.a[0], c.x));
+  z.a[1] = fma2(y.b[1], m.y, mul2(y.a[1], c.y));
+  z.b[0] = fma2(y.a[0], s.x, mul2(y.b[0], c.x));
+  z.b[1] = fma2(y.a[1], s.y, mul2(y.b[1], c.y));
+  return z;
+}
+
+constexpr int ctas_per_sm(bool bias) { return bias ? 2 : 3; }   // 128 or 80 registers a thread
+
+// A row's place in the cache for keys or values, at head h.
+struct Spot {
+  char *to;
+  float *scale;
+  bool live;
+};
+__device__ __forceinline__ Spot spot_of(const NormRopeArgs &a, bool values, bool f8, int64_t row, int h) {
+  const uint32_t slot = static_cast<uint32_t>(a.p.slot[row]);   // negative slots are large ones
+  const int64_t page = slot / kPage, tok = slot % kPage;
+  Spot s;
+  s.live = slot < static_cast<uint64_t>(a.c.P) * kPage;
+  s.to = static_cast<char *>(values ? a.c.v : a.c.k) + (page * a.c.page_stride + tok * a.c.token_stride + h * a.c.head_stride) * (f8 ? 1 : 2);
+  s.scale = f8 ? (values ? a.c.v_scale : a.c.k_scale) + (page * a.p.Hkv + h) * kPage + tok : nullptr;
+  return s;
+}
+
+// A warp's batches of one kind (0 q, 1 k, 2 v) in a group of rows: item i is batch i % units of
+// row i / units, a step from one to the next; and the copies that run one batch ahead.
+template <int D, bool kInterleaved, int kKind>
+struct Walk {
+  static constexpr int kAtOnce = 32 / (D / 8);
+  const NormRopeArgs &a;
+  const int units, heads, step;
+  const uint16_t *const in;   // the group's first row, this lane's first head
+  const int64_t stride;
+  const Place at;
+  int r, u, r_next, u_next;
+
+  __device__ __forceinline__ Walk(const NormRopeArgs &args, int64_t row0, int item, int step_)
+      : a(args), units(kKind == 0 ? args.q_units : args.k_units), heads(kKind == 0 ? args.p.Hq : args.p.Hkv), step(step_),
+        in(static_cast<const uint16_t *>(kKind == 0 ? args.p.q : kKind == 1 ? args.p.k : args.p.v) +
+           row0 * (kKind == 0 ? args.p.q_stride : kKind == 1 ? args.p.k_stride : args.p.v_stride) + sub() * D),
+        stride(kKind == 0 ? args.p.q_stride : kKind == 1 ? args.p.k_stride : args.p.v_stride),
+        at(kKind == 2 ? Place{8 * lane(), 0, false} : place_of<kInterleaved>(lane(), args.p.rot)) {
+    r = r_next = item / units;
+    u = u_next = item % units;
+  }
+  static __device__ __forceinline__ int lane() { return threadIdx.x % (D / 8); }
+  static __device__ __forceinline__ int sub() { return threadIdx.x % 32 / (D / 8); }
+  __device__ __forceinline__ int first() const { return u * a.heads; }
+  // This lane's heads of the batch: 0, kAtOnce, .. below this.
+  __device__ __forceinline__ int mine(int batch) const { return min(heads - batch * a.heads - sub(), a.heads - sub()); }
+  __device__ __forceinline__ void copy_next(uint4 (&to)[kVectors][32]) {
+    const int n = mine(u_next);
+    const uint16_t *const src = in + r_next * stride + u_next * a.heads * D;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    // where nothing turns, the other's factor is 0: an infinite other must not make it NaN
-    const uint64_t oa = crosses ? x.b[h] : 0, ob = crosses ? x.a[h] : 0;
-    const uint64_t ta = fma2(x.a[h], f.aa[h], mul2(oa, f.ab[h])), tb = fma2(x.b[h], f.bb[h], mul2(ob, f.ba[h]));
-    if constexpr (kBias) {
-      z.a[h] = fma2(both(inv), ta, f.ca[h]);
-      z.b[h] = fma2(both(inv), tb, f.cb[h]);
-    } else {
-      z.a[h] = mul2(both(inv), ta);
-      z.b[h] = mul2(both(inv), tb);
+    for (int k = 0; k < kVectors; ++k)
+      if (k * kAtOnce < n) copy_async<kInterleaved || kKind == 2>(&to[k][threadIdx.x % 32], src + k * kAtOnce * D, at);
+    for (u_next += step; u_next >= units; u_next -= units) ++r_next;
+  }
+  __device__ __forceinline__ void next() {
+    for (u += step; u >= units; u -= units) ++r;
+  }
+};
+
+// Norm and rotation of a kind's items from `item` on.  Returns the first item past them.
+// copied: the first batch's copies are on their way.
+template <int D, bool kInterleaved, bool kBias, bool kKeys>
+__device__ __forceinline__ int turn_items(const NormRopeArgs &a, int item, int step, int rows, int64_t row0, const Turns<D> *turns,
+                                          const float *weight, const float *bias, uint4 (*ring)[kVectors][32], bool copied) {
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kStep = kAtOnce * D;
+  constexpr int kPair = kBias ? 1 : 2;   // heads normed at a time, so that one's sums run beside the other's
+  const idx_norm_rope_args &p = a.p;
+  const int lane = threadIdx.x % kLanes, sub = threadIdx.x % 32 / kLanes, slot = threadIdx.x % 32;
+  const int items = rows * (kKeys ? a.k_units : a.q_units), norm = kKeys ? p.k_norm : p.q_norm;
+  if (item >= items) return item - items;
+  Walk<D, kInterleaved, kKeys ? 1 : 0> walk(a, row0, item, step);
+  const Place &at = walk.at;
+  const Pairs w = by_pairs<kInterleaved>(at, weight);
+  const bool f8 = a.c.kv_dtype == IDX_KV_E4M3;
+  uint16_t *const out = static_cast<uint16_t *>(kKeys ? p.k_out : p.q_out);
+  uint16_t *const out0 = out + row0 * (kKeys ? p.k_out_stride : p.q_out_stride) + sub * D;
+  // the next batch is on its way while one is worked on; a lane reads what it copied itself
+  int stage = 0;
+  if (copied) {
+    for (walk.u_next += step; walk.u_next >= walk.units; walk.u_next -= walk.units) ++walk.r_next;
+  } else {
+    walk.copy_next(ring[0]);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+#pragma unroll 1
+  for (; item < items; item += step, stage ^= 1, walk.next()) {
+    if (item + step < items) walk.copy_next(ring[stage ^ 1]);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const int r = walk.r, first = walk.first(), mine = walk.mine(walk.u);
+    uint16_t *const dst = out0 + r * (kKeys ? p.k_out_stride : p.q_out_stride) + first * D;
+    Spot spot{};
+    if (kKeys && p.slot != nullptr) spot = spot_of(a, false, f8, row0 + r, first + sub);
+    const int64_t to_step = kAtOnce * a.c.head_stride * (f8 ? 1 : 2);
+#pragma unroll
+    for (int k0 = 0; k0 < kVectors; k0 += kPair) {
+      if (k0 * kAtOnce >= mine + sub) break;   // the warp's lanes together
+      Pairs x[kPair];
+      uint4 v[kPair];
+      float inv[kPair];
+#pragma unroll
+      for (int k = 0; k < kPair; ++k) {
+        v[k] = ring[stage][k0 + k][slot];   // past the last head: whatever is there, and not stored
+        x[k] = unpack<kInterleaved>(v[k]);
+        inv[k] = 1.0f;
+      }
+      if (kBias && norm == IDX_NORM_LAYER) normed<D, kInterleaved, true>(x, v, p.eps, inv);
+      else if (norm != IDX_NORM_NONE) normed<D, kInterleaved, false>(x, v, p.eps, inv);
+#pragma unroll
+      for (int k = 0; k < kPair; ++k) {
+        Pairs y;
+        if constexpr (kBias) {
+          const Pairs b = by_pairs<kInterleaved>(at, bias);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            y.a[h] = fma2(mul2(x[k].a[h], both(inv[k])), w.a[h], b.a[h]);
+            y.b[h] = fma2(mul2(x[k].b[h], both(inv[k])), w.b[h], b.b[h]);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            y.a[h] = mul2(mul2(x[k].a[h], both(inv[k])), w.a[h]);
+            y.b[h] = mul2(mul2(x[k].b[h], both(inv[k])), w.b[h]);
+          }
+        }
+        const Pairs z = turned<D, kInterleaved>(y, turns[r], at);
+        const uint4 packed = pack<kInterleaved>(z);
+        const bool here = (k0 + k) * kAtOnce < mine;
+        if ((!kKeys || out != nullptr) && here) store<kInterleaved>(dst + (k0 + k) * kStep, at, packed);
+        if (!kKeys || spot.to == nullptr) continue;
+        char *const head = spot.to + (k0 + k) * to_step;
+        if (!f8) {
+          if (spot.live && here) store<kInterleaved>(reinterpret_cast<uint16_t *>(head), at, packed);
+          continue;
+        }
+        // eight values in the order of their bytes
+        const float e[8] = {low(z.a[0]), kInterleaved ? low(z.b[0]) : high(z.a[0]), kInterleaved ? high(z.a[0]) : low(z.a[1]),
+                            kInterleaved ? high(z.b[0]) : high(z.a[1]), kInterleaved ? low(z.a[1]) : low(z.b[0]),
+                            kInterleaved ? low(z.b[1]) : high(z.b[0]), kInterleaved ? high(z.a[1]) : low(z.b[1]), high(z.b[1])};
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(e[j]));
+        uint32_t lo, hi;
+        const float sc = quantize_f32(e, group_max<kLanes>(m), lo, hi);
+        if (spot.live && here) {
+          if (kInterleaved) {
+            *reinterpret_cast<uint2 *>(head + at.a) = make_uint2(lo, hi);
+          } else {
+            *reinterpret_cast<uint32_t *>(head + at.a) = lo;
+            *reinterpret_cast<uint32_t *>(head + at.b) = hi;
+          }
+          if (lane == 0) spot.scale[(k0 + k) * kAtOnce * kPage] = sc;
+        }
+      }
     }
   }
-  return z;
+  return item - items;
 }
 
 // kBias: a LayerNorm is among the norms.
 template <int D, bool kInterleaved, bool kBias>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kBias)) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
-  constexpr int kPair = kBias ? 1 : 2;   // heads normed at a time, so that one's sums run beside the other's
-  __shared__ __align__(16) float2 cs[kMostRows][D / 2];
+  __shared__ __align__(16) Turns<D> turns[kMostRows];
+  __shared__ uint4 rings[kWarps][2][kVectors][32];
   __shared__ __align__(16) float weights[2][D], biases[kBias ? 2 : 1][kBias ? D : 4];   // of q and of k
   const idx_norm_rope_args &p = a.p;
-  const int tid = threadIdx.x, lane = tid % kLanes, sub = tid % 32 / kLanes, warp = tid / 32;
+  const int tid = threadIdx.x;
   const int64_t group = blockIdx.x / a.splits;
   const int part = static_cast<int>(blockIdx.x % a.splits);
   const int64_t row0 = group * a.group_rows;
@@ -283,10 +429,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const _
   const int rows = static_cast<int>(min(static_cast<int64_t>(a.group_rows), limit - row0));
   if (rows <= 0) return;
 
+  // the warp's first copies, before the angles
+  const int step = a.splits * kWarps;
+  int item = part * kWarps + tid / 32;
+  uint4(*const ring)[kVectors][32] = rings[tid / 32];
+  const int kind = item < rows * a.q_units ? 0 : item < rows * (a.q_units + a.k_units) ? 1 : 2;
+  if (kind == 0) Walk<D, kInterleaved, 0>(a, row0, item, step).copy_next(ring[0]);
+  if (kind == 1) Walk<D, kInterleaved, 1>(a, row0, item - rows * a.q_units, step).copy_next(ring[0]);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+
   const int pairs = p.rot >> 1;
   for (int i = tid; i < rows * pairs; i += kThreads) {
     const int r = i / pairs, k = i % pairs;
-    cs[r][k] = cos_sin(p.pos[p.axis[k] * p.pos_stride + row0 + r], p.inv_freq[k]);
+    const float2 t = cos_sin(p.pos[p.axis[k] * p.pos_stride + row0 + r], p.inv_freq[k]);
+    turns[r].c[k] = t.x;
+    turns[r].s[k] = t.y;
+    turns[r].m[k] = -t.y;
   }
   for (int i = tid; i < D; i += kThreads) {
     weights[0][i] = p.q_weight != nullptr ? p.q_weight[i] : 1.0f;
@@ -298,111 +456,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const _
   }
   __syncthreads();
 
-  const Place at = place_of<kInterleaved>(lane, p.rot);
-  const bool f8 = a.c.kv_dtype == IDX_KV_E4M3, crosses = p.rot == D || at.turns;
-  constexpr int kStep = kAtOnce * D;   // elements from one of a lane's heads to the next
-  int r = 0, u = part * kWarps + warp;
-  for (; u >= a.units; u -= a.units) ++r;
-  while (r < rows) {
-    const int64_t row = row0 + r;
-    // the unit's kind and heads: this lane's are h, h + kAtOnce, ..., `mine` of them
-    const int kind = u < a.q_units ? 0 : u < a.q_units + a.k_units ? 1 : 2;
-    const int first = (u - (kind == 0 ? 0 : kind == 1 ? a.q_units : a.q_units + a.k_units)) * a.heads, h = first + sub;
-    const int heads = min(a.heads, (kind == 0 ? p.Hq : p.Hkv) - first), mine = (heads - sub + kAtOnce - 1) / kAtOnce;
-    const uint16_t *const src = static_cast<const uint16_t *>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
-                                row * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride) + h * D;
-    uint4 raw[kVectors];
+  item = turn_items<D, kInterleaved, kBias, false>(a, item, step, rows, row0, turns, weights[0], biases[0], ring, kind == 0);
+  item = turn_items<D, kInterleaved, kBias, true>(a, item, step, rows, row0, turns, weights[1], biases[kBias ? 1 : 0], ring, kind == 1);
+  if (a.c.v == nullptr || item >= rows * a.k_units) return;
+  Walk<D, kInterleaved, 2> walk(a, row0, item, step);
+  const int lane = tid % kLanes, sub = tid % 32 / kLanes, slot = tid % 32;
+  const bool f8 = a.c.kv_dtype == IDX_KV_E4M3;
+  const int64_t to_step = kAtOnce * a.c.head_stride * (f8 ? 1 : 2);
+  int stage = 0;
+  walk.copy_next(ring[0]);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll 1
+  for (; item < rows * a.k_units; item += step, stage ^= 1, walk.next()) {
+    if (item + step < rows * a.k_units) walk.copy_next(ring[stage ^ 1]);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const int first = walk.first(), mine = walk.mine(walk.u);
+    const Spot spot = spot_of(a, true, f8, row0 + walk.r, first + sub);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll
     for (int k = 0; k < kVectors; ++k) {
-      raw[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (k < mine) raw[k] = kind == 2 ? __ldcs(reinterpret_cast<const uint4 *>(src + k * kStep + 8 * lane)) : load<kInterleaved>(src + k * kStep, at);
-    }
-
-    // the row's place in the cache, at head h
-    char *to = nullptr;
-    float *scale = nullptr;
-    bool live = false;
-    if (kind != 0 && p.slot != nullptr) {
-      const uint32_t slot = static_cast<uint32_t>(p.slot[row]);   // negative slots are large ones
-      live = slot < static_cast<uint64_t>(a.c.P) * kPage;
-      const int64_t page = slot / kPage, tok = slot % kPage;
-      to = static_cast<char *>(kind == 1 ? a.c.k : a.c.v) +
-           (page * a.c.page_stride + tok * a.c.token_stride + h * a.c.head_stride) * (f8 ? 1 : 2);
-      scale = f8 ? (kind == 1 ? a.c.k_scale : a.c.v_scale) + (page * p.Hkv + h) * kPage + tok : nullptr;
-    }
-    const int64_t to_step = kAtOnce * a.c.head_stride * (f8 ? 1 : 2);
-
-    if (kind == 2) {
-#pragma unroll
-      for (int k = 0; k < kVectors; ++k) {
-        if (k * kAtOnce >= heads) break;   // the warp's lanes together
-        if (f8) {
-          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-          uint32_t lo, hi;
-          const float sc = quantize(w, vector_amax<kLanes>(w), lo, hi);
-          if (live && k < mine) {
-            *reinterpret_cast<uint2 *>(to + k * to_step + 8 * lane) = make_uint2(lo, hi);
-            if (lane == 0) scale[k * kAtOnce * kPage] = sc;
-          }
-        } else if (live && k < mine) {
-          *reinterpret_cast<uint4 *>(to + k * to_step + 16 * lane) = raw[k];
+      if (k * kAtOnce >= mine + sub) break;   // the warp's lanes together
+      const bool here = spot.live && k * kAtOnce < mine;
+      char *const head = spot.to + k * to_step;
+      const uint4 v = ring[stage][k][slot];
+      if (f8) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t lo, hi;
+        const float sc = quantize(w, vector_amax<kLanes>(w), lo, hi);
+        if (here) {
+          *reinterpret_cast<uint2 *>(head + 8 * lane) = make_uint2(lo, hi);
+          if (lane == 0) spot.scale[k * kAtOnce * kPage] = sc;
         }
-      }
-    } else {
-      uint16_t *dst = static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out);
-      const bool out = dst != nullptr;
-      if (out) dst += row * (kind == 0 ? p.q_out_stride : p.k_out_stride) + h * D;
-      Factors f;
-      make_factors<kInterleaved, kBias>(at, cs[r], weights[kind], kBias ? biases[kind] : nullptr, f);
-      const int norm = kind == 0 ? p.q_norm : p.k_norm;
-#pragma unroll
-      for (int k0 = 0; k0 < kVectors; k0 += kPair) {
-        if (k0 * kAtOnce >= heads) break;   // the warp's lanes together
-        Pairs x[kPair];
-        uint4 v[kPair];
-        float inv[kPair];
-#pragma unroll
-        for (int k = 0; k < kPair; ++k) {
-          v[k] = raw[k0 + k];
-          x[k] = unpack<kInterleaved>(v[k]);
-          inv[k] = 1.0f;
-        }
-        if (kBias && norm == IDX_NORM_LAYER) normed<D, true>(x, v, kInterleaved, p.eps, inv);
-        else if (norm != IDX_NORM_NONE) normed<D, false>(x, v, kInterleaved, p.eps, inv);
-#pragma unroll
-        for (int k = 0; k < kPair; ++k) {
-          const Pairs z = turned<kBias>(x[k], f, inv[k], crosses);
-          const uint4 packed = pack<kInterleaved>(z);
-          const bool here = k0 + k < mine;
-          if (out && here) store<kInterleaved>(dst + (k0 + k) * kStep, at, packed);
-          if (to == nullptr) continue;
-          char *const head = to + (k0 + k) * to_step;
-          if (!f8) {
-            if (live && here) store<kInterleaved>(reinterpret_cast<uint16_t *>(head), at, packed);
-            continue;
-          }
-          // eight values in the order of their bytes
-          const float e[8] = {low(z.a[0]), kInterleaved ? low(z.b[0]) : high(z.a[0]), kInterleaved ? high(z.a[0]) : low(z.a[1]),
-                              kInterleaved ? high(z.b[0]) : high(z.a[1]), kInterleaved ? low(z.a[1]) : low(z.b[0]),
-                              kInterleaved ? low(z.b[1]) : high(z.b[0]), kInterleaved ? high(z.a[1]) : low(z.b[1]), high(z.b[1])};
-          float m = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(e[j]));
-          uint32_t lo, hi;
-          const float sc = quantize_f32(e, group_max<kLanes>(m), lo, hi);
-          if (live && here) {
-            if (kInterleaved) {
-              *reinterpret_cast<uint2 *>(head + at.a) = make_uint2(lo, hi);
-            } else {
-              *reinterpret_cast<uint32_t *>(head + at.a) = lo;
-              *reinterpret_cast<uint32_t *>(head + at.b) = hi;
-            }
-            if (lane == 0) scale[(k0 + k) * kAtOnce * kPage] = sc;
-          }
-        }
+      } else if (here) {
+        *reinterpret_cast<uint4 *>(head + 16 * lane) = v;
       }
     }
-    for (u += a.splits * kWarps; u >= a.units; u -= a.units) ++r;
   }
 }
 
@@ -410,20 +498,18 @@ template <int D, bool kInterleaved, bool kBias>
 cudaError_t launch(NormRopeArgs a, int num_sms, cudaStream_t stream) {
   constexpr int kAtOnce = 32 / (D / 8);
   const int kinds = a.c.v != nullptr ? 2 : 1;
-  // Units of kVectors loads a lane and groups of kMostRows rows where that leaves every SM its
-  // CTAs; else single loads, single rows and as many CTAs to a row as it has warps of work.
-  const int64_t vectors = a.p.R * (a.p.Hq + static_cast<int64_t>(a.p.Hkv) * kinds);
-  const int64_t full = static_cast<int64_t>(num_sms) * kCtasPerSm * kWarps * kAtOnce;   // vectors that the GPU holds
+  // Batches of kVectors heads a lane and groups of kMostRows rows where that leaves every SM its
+  // CTAs; else single heads, single rows and as many CTAs to a row as it has batches for.
+  const int64_t ctas = static_cast<int64_t>(num_sms) * ctas_per_sm(kBias);
+  const int64_t vectors = a.p.R * (a.p.Hq + static_cast<int64_t>(a.p.Hkv) * kinds), full = ctas * kWarps * kAtOnce;   // at a time
   int per = 1;
   while (per < kVectors && vectors >= 2 * per * full) per *= 2;
   a.heads = per * kAtOnce;
   a.q_units = (a.p.Hq + a.heads - 1) / a.heads;
   a.k_units = (a.p.Hkv + a.heads - 1) / a.heads;
-  a.units = a.q_units + a.k_units * kinds;
   a.group_rows = 1;
-  while (a.group_rows < kMostRows && a.p.R >= 2 * a.group_rows * static_cast<int64_t>(num_sms) * kCtasPerSm) a.group_rows *= 2;
-  a.splits = 1;
-  if (a.group_rows == 1) a.splits = (a.units + kWarps - 1) / kWarps;
+  while (a.group_rows < kMostRows && a.p.R >= 2 * a.group_rows * ctas) a.group_rows *= 2;
+  a.splits = a.group_rows > 1 ? 1 : (a.q_units + a.k_units * kinds + kWarps - 1) / kWarps;
   const int64_t grid = (a.p.R + a.group_rows - 1) / a.group_rows * a.splits;
   norm_rope_kernel<D, kInterleaved, kBias><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a);
   return cudaGetLastError();
