@@ -27,6 +27,27 @@ inline cudaError_t once_per_device(std::mutex &mu, bool (&done)[128], F setup) {
   return e;
 }
 
+// Launches a kernel that begins with grid_dependency_wait(): it may be set up while the stream's
+// previous kernel ends, and waits there for that one's memory.  cluster: CTAs of a cluster.
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                                cudaStream_t stream, const A &...args) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // SMs of the current device (IDX_EUNSUPPORTED unless it is compute capability 10.3).
 idx_status device_sms(int *out);
 // The time limit of device-side waits (idx_debug_set).

@@ -422,6 +422,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBias)) norm_rope_kernel
   __shared__ __align__(16) float weights[2][D], biases[kBias ? 2 : 1][kBias ? D : 4];   // of q and of k
   const idx_norm_rope_args &p = a.p;
   const int tid = threadIdx.x;
+  grid_dependency_trigger();
+  grid_dependency_wait();
   const int64_t group = blockIdx.x / a.splits;
   const int part = static_cast<int>(blockIdx.x % a.splits);
   const int64_t row0 = group * a.group_rows;
@@ -498,21 +500,23 @@ template <int D, bool kInterleaved, bool kBias>
 cudaError_t launch(NormRopeArgs a, int num_sms, cudaStream_t stream) {
   constexpr int kAtOnce = 32 / (D / 8);
   const int kinds = a.c.v != nullptr ? 2 : 1;
-  // Batches of kVectors heads a lane and groups of kMostRows rows where that leaves every SM its
-  // CTAs; else single heads, single rows and as many CTAs to a row as it has batches for.
+  // Groups of kMostRows rows where that leaves every SM its CTAs, else of fewer; below that as
+  // many CTAs to a row as run at a time, and batches as large as leaves each of their warps one.
   const int64_t ctas = static_cast<int64_t>(num_sms) * ctas_per_sm(kBias);
-  const int64_t vectors = a.p.R * (a.p.Hq + static_cast<int64_t>(a.p.Hkv) * kinds), full = ctas * kWarps * kAtOnce;   // at a time
-  int per = 1;
-  while (per < kVectors && vectors >= 2 * per * full) per *= 2;
-  a.heads = per * kAtOnce;
-  a.q_units = (a.p.Hq + a.heads - 1) / a.heads;
-  a.k_units = (a.p.Hkv + a.heads - 1) / a.heads;
   a.group_rows = 1;
   while (a.group_rows < kMostRows && a.p.R >= 2 * a.group_rows * ctas) a.group_rows *= 2;
-  a.splits = a.group_rows > 1 ? 1 : (a.q_units + a.k_units * kinds + kWarps - 1) / kWarps;
+  const int most = static_cast<int>(std::max<int64_t>(1, ctas / a.p.R));
+  int per = 1;
+  for (;; per *= 2) {
+    a.heads = per * kAtOnce;
+    a.q_units = (a.p.Hq + a.heads - 1) / a.heads;
+    a.k_units = (a.p.Hkv + a.heads - 1) / a.heads;
+    a.splits = (a.q_units + a.k_units * kinds + kWarps - 1) / kWarps;
+    if (per == kVectors || (a.group_rows == 1 && a.splits <= most)) break;
+  }
+  a.splits = a.group_rows > 1 ? 1 : std::min(a.splits, most);
   const int64_t grid = (a.p.R + a.group_rows - 1) / a.group_rows * a.splits;
-  norm_rope_kernel<D, kInterleaved, kBias><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(norm_rope_kernel<D, kInterleaved, kBias>, static_cast<unsigned>(grid), kThreads, 0, 1, stream, a);
 }
 
 template <int D>

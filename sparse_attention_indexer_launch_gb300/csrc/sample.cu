@@ -538,8 +538,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const T *const src = static_cast<const T *>(a.p.logits) + row * a.p.ld;
 
   cluster.barrier_arrive();
+  grid_dependency_trigger();
   for (int i = tid; i < 64 * kColumns; i += kThreads) table[i] = kExp2.v[i / kColumns];
   clear_hist(hist, 2 * kYBins);
+  grid_dependency_wait();
   Params par{};
   if (rank == 0 && warp == 0) {   // every lane the same; used behind the row's loads
     par.live = a.p.rows == nullptr || row < *a.p.rows;
@@ -1100,17 +1102,8 @@ cudaError_t launch(const SampleArgs &a, cudaStream_t stream) {
     return cudaFuncSetAttribute(sample_kernel<T, kTopK, kTopP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   });
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {kCtas, 1, 1};
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.p.R) * kCtas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = fixed_smem<T>() + static_cast<size_t>(kWarps) * a.warp_len * sizeof(T);
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T, kTopK, kTopP>, a);
+  return launch_early(sample_kernel<T, kTopK, kTopP>, static_cast<unsigned>(a.p.R) * kCtas, kThreads,
+                      fixed_smem<T>() + static_cast<size_t>(kWarps) * a.warp_len * sizeof(T), kCtas, stream, a);
 }
 
 template <typename T>

@@ -41,6 +41,8 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeAcceptA
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const idx_tree_accept_args &t = a.t;
   uint32_t bad = 0;
+  grid_dependency_trigger();
+  grid_dependency_wait();
 
   for (int i = blockIdx.x * kWarps + warp; i < t.Q; i += gridDim.x * kWarps) {
     int32_t first, n;
@@ -152,6 +154,7 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeAcceptA
 template <int kLanes>
 __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const TreeCommitArgs a) {
   const int lane = threadIdx.x % kLanes;
+  grid_dependency_trigger();
   const int64_t group = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
   const int per_req = a.c.Hkv * (a.c.v != nullptr ? 2 : 1);
   const int64_t i = group / per_req;
@@ -161,6 +164,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const TreeCommitA
   if (is_v) h -= a.c.Hkv;
   uint32_t bad = 0;
   int32_t first, n;
+  grid_dependency_wait();
   rows_of(a.row_start, static_cast<int>(i), a.cap, first, n, bad);
   const int32_t length = min(a.accept_len[i], min(n, IDX_MAX_TREE));
   const int bytes = a.c.kv_dtype == IDX_KV_E4M3 ? 1 : 2;
@@ -199,16 +203,14 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const TreeCommitA
 template <int kLanes>
 cudaError_t launch_commit(const TreeCommitArgs &a, cudaStream_t stream) {
   const int64_t threads = static_cast<int64_t>(a.Q) * a.c.Hkv * (a.c.v != nullptr ? 2 : 1) * kLanes;
-  tree_commit_kernel<kLanes><<<static_cast<unsigned>((threads + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(tree_commit_kernel<kLanes>, static_cast<unsigned>((threads + kThreads - 1) / kThreads), kThreads, 0, 1, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_accept(const TreeAcceptArgs &a, int num_sms, cudaStream_t stream) {
   const int grid = std::min((a.t.Q + kWarps - 1) / kWarps, 2 * num_sms);
-  tree_accept_kernel<<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(tree_accept_kernel, static_cast<unsigned>(grid), kThreads, 0, 1, stream, a);
 }
 
 cudaError_t launch_tree_commit(const TreeCommitArgs &a, cudaStream_t stream) {
