@@ -621,9 +621,10 @@ def idx_tree_commit(cache: KvCache, row_start, accept_len, path, slot, stream=No
     accept_len [Q] and path [cap] as idx_tree_accept wrote them, slot [cap]; all int32."""
     int32 = _modules["torch"].int32
     Q, cap = accept_len.numel(), path.numel()
-    for t, n in ((row_start, Q + 1), (accept_len, Q), (path, cap), (slot, cap)):
-        if t.dtype is not int32 or not t.is_contiguous() or t.numel() < n:
-            raise ValueError("row_start [Q + 1], accept_len [Q], path and slot [cap]: contiguous int32 tensors are wanted")
+    if not (row_start.dtype is accept_len.dtype is path.dtype is slot.dtype is int32 and row_start.numel() > Q
+            and slot.numel() >= cap and row_start.is_contiguous() and accept_len.is_contiguous() and path.is_contiguous()
+            and slot.is_contiguous()):
+        raise ValueError("row_start [Q + 1], accept_len [Q], path and slot [cap]: contiguous int32 tensors are wanted")
     _check(lib.idx_tree_commit(ctypes.byref(cache), row_start.data_ptr(), accept_len.data_ptr(), path.data_ptr(), slot.data_ptr(),
                                Q, cap, _current(stream, cache, row_start, accept_len, path, slot)), "idx_tree_commit")
 

@@ -5,7 +5,8 @@
 // Acceptance walks down from token 0: the next token is the first child whose draft is the
 // sampled token.  A warp holds a request's tree, two tokens a lane, so a step of the walk is
 // two comparisons and a ballot.  Giving pages back needs a prefix sum over all requests'
-// results: the CTA that finishes last does it, so nobody waits.
+// results: the CTA that finishes last does it, so nobody waits.  A single CTA, of a warp per
+// request, has them in shared memory.
 //
 // Moving is in place: the a-th accepted token goes from the slot of row path[a] to that of row
 // a, path[a] >= a and ascending.  Row a's slot is read by no later move (path[b] = a only for
@@ -19,8 +20,9 @@
 namespace idx {
 namespace {
 
+constexpr int kWalkThreads = 1024;   // at most: a request per warp, and per thread where pages go back
+constexpr int kWalkWarps = kWalkThreads / 32;
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMoves = 4;   // loads of a lane in flight
 
 __device__ __forceinline__ int32_t pages_of(int64_t tokens) {
@@ -35,16 +37,34 @@ __device__ __forceinline__ void rows_of(const int32_t *row_start, int i, int32_t
   if (first != a || static_cast<int64_t>(first) + n != b) bad |= kStatusBadBound;
 }
 
-__global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeAcceptArgs a) {
-  __shared__ int32_t warp_pages[kWarps];
+// A request's cached tokens, its pages [first, end) of which the last may go back, two of them read.
+struct Held {
+  int32_t ctx, first, end, page[2];
+};
+__device__ __forceinline__ Held held_by(const idx_tree_accept_args &t, int i) {
+  uint32_t bad = 0;   // recorded where the request is walked
+  int32_t row, n;
+  rows_of(t.row_start, i, t.cap, row, n, bad);
+  Held h;
+  h.ctx = min(max(t.ctx_len[i], 0), (1 << 30) - kPage);
+  h.first = pages_of(static_cast<int64_t>(h.ctx) + min(n, 1));   // token 0 stays
+  h.end = min(pages_of(static_cast<int64_t>(h.ctx) + n), t.pt_stride);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    h.page[k] = h.first + k < h.end ? t.page_table[static_cast<int64_t>(i) * t.pt_stride + h.first + k] : -1;
+  return h;
+}
+
+__global__ void __launch_bounds__(kWalkThreads, 1) tree_accept_kernel(const TreeAcceptArgs a) {
+  __shared__ int32_t warp_pages[kWalkWarps], lengths[kWalkWarps];
   __shared__ bool last;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
   const idx_tree_accept_args &t = a.t;
   uint32_t bad = 0;
   grid_dependency_trigger();
   grid_dependency_wait();
 
-  for (int i = blockIdx.x * kWarps + warp; i < t.Q; i += gridDim.x * kWarps) {
+  for (int i = blockIdx.x * warps + warp; i < t.Q; i += gridDim.x * warps) {
     int32_t first, n;
     rows_of(t.row_start, i, t.cap, first, n, bad);
     if (n > IDX_MAX_TREE) bad |= kStatusBadBound;
@@ -76,9 +96,12 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeAcceptA
       if ((lo | hi) == 0) break;
       node = lo != 0 ? __ffs(lo) - 1 : 31 + __ffs(hi);
       next = __shfl_sync(0xffffffffu, lo != 0 ? target[0] : target[1], node & 31);
-      if ((length & 31) == lane) {
-        mine[length >> 5] = node;
-        token[length >> 5] = next;
+      if (length == lane) {
+        mine[0] = node;
+        token[0] = next;
+      } else if (length == lane + 32) {
+        mine[1] = node;
+        token[1] = next;
       }
       ++length;
     }
@@ -92,37 +115,50 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeAcceptA
     for (int u = IDX_MAX_TREE + lane; u < n; u += 32) t.path[first + u] = t.token[first + u] = -1;
     if (lane == 0) {
       t.accept_len[i] = length;
+      lengths[warp] = length;
       t.last[i] = next;
     }
   }
   if (bad) flag_status(a.status, bad);
 
+  // What giving pages back needs beside the lengths is read by every CTA before it is known which
+  // one comes last: a request's rows and cached tokens, and its pages from the first that may go.
+  Held held{};
+  if (tid < t.Q) held = held_by(t, tid);
+
   // the CTA that comes last sees every request's length
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) last = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  if (tid == 0) *a.arrived = 0;
+  const bool alone = gridDim.x == 1 && t.Q <= warps;
+  if (!alone) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) last = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    if (tid == 0) *a.arrived = 0;
+  } else {
+    __syncthreads();
+  }
   bad = 0;
   const int32_t had = max(*t.free_count, 0);
   int64_t base = had;
-  for (int i0 = 0; i0 < t.Q; i0 += kThreads) {
+  for (int i0 = 0; i0 < t.Q; i0 += threads) {
     const int i = i0 + tid;
-    int32_t keep = 0, n_pages = 0, have = 0;   // pages behind the new length, those among them with an id
+    int32_t keep = 0, have = 0;   // the first page behind the new length, those from there on with an id
+    if (i0 > 0 && i < t.Q) held = held_by(t, i);
+    const auto page_at = [&](int32_t p) {
+      const int32_t k = p - held.first;
+      return k == 0 ? held.page[0] : k == 1 ? held.page[1] : t.page_table[static_cast<int64_t>(i) * t.pt_stride + p];
+    };
     if (i < t.Q) {
-      int32_t first, n;
-      rows_of(t.row_start, i, t.cap, first, n, bad);
-      const int32_t ctx = min(max(t.ctx_len[i], 0), (1 << 30) - kPage), length = __ldcg(t.accept_len + i);
-      keep = pages_of(static_cast<int64_t>(ctx) + length);
-      n_pages = max(min(pages_of(static_cast<int64_t>(ctx) + n), t.pt_stride) - keep, 0);
-      for (int j = 0; j < n_pages; ++j) {
-        const int32_t page = t.page_table[static_cast<int64_t>(i) * t.pt_stride + keep + j];
-        have += page >= 0 && page < t.P;
+      const int32_t length = alone ? lengths[i] : __ldcg(t.accept_len + i);
+      keep = pages_of(static_cast<int64_t>(held.ctx) + length);
+      for (int32_t p = keep; p < held.end; ++p) {
+        const int32_t page = page_at(p);
+        if (page >= 0 && page < t.P) ++have;
+        else bad |= kStatusBadPage;
       }
-      if (have != n_pages) bad |= kStatusBadPage;
-      t.new_ctx[i] = ctx + length;
+      t.new_ctx[i] = held.ctx + length;
     }
     int32_t upto = have;   // places on the stack: a prefix sum
 #pragma unroll
@@ -133,12 +169,12 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeAcceptA
     if (lane == 31) warp_pages[warp] = upto;
     __syncthreads();
     int64_t before = base + upto - have;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < warps; ++w) {
       if (w < warp) before += warp_pages[w];
       base += warp_pages[w];
     }
-    for (int j = 0; j < n_pages; ++j) {
-      const int32_t page = t.page_table[static_cast<int64_t>(i) * t.pt_stride + keep + j];
+    for (int32_t p = keep; i < t.Q && p < held.end; ++p) {
+      const int32_t page = page_at(p);
       if (page < 0 || page >= t.P) continue;
       if (before < t.free_cap) t.free_pages[before] = page;
       else bad |= kStatusBadPage;
@@ -209,8 +245,8 @@ cudaError_t launch_commit(const TreeCommitArgs &a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_tree_accept(const TreeAcceptArgs &a, int num_sms, cudaStream_t stream) {
-  const int grid = std::min((a.t.Q + kWarps - 1) / kWarps, 2 * num_sms);
-  return launch_early(tree_accept_kernel, static_cast<unsigned>(grid), kThreads, 0, 1, stream, a);
+  const int warps = std::min(a.t.Q, kWalkWarps), grid = std::min((a.t.Q + warps - 1) / warps, 2 * num_sms);
+  return launch_early(tree_accept_kernel, static_cast<unsigned>(grid), 32 * static_cast<unsigned>(warps), 0, 1, stream, a);
 }
 
 cudaError_t launch_tree_commit(const TreeCommitArgs &a, cudaStream_t stream) {
