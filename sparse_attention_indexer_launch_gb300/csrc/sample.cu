@@ -16,7 +16,7 @@
 // so one number is enough, the composite (key, ~index) of the last kept one.  A first pass
 // sorts the weights' exponents into bins of 1 / 32 octave, counts for top-k and leading bits
 // of the weights for top-p; the elements of the bin that holds the border (for top-k those
-// above as well, where they are few) go into a list that every CTA gathers and searches.  A
+// above as well, where they are few) go into a list that the first CTA gathers and searches.  A
 // bin with too many is cut into 256 finer ones first; where even those hold too many (equal
 // logits), a radix descent runs over the whole row.
 #include <cooperative_groups.h>
@@ -204,11 +204,17 @@ struct Params {              // of the row, from the first CTA
   float temperature, c_hi, c_lo, top_p, min_p, u;
   int32_t top_k, live;
 };
+struct Verdict {             // on a list, from the first CTA
+  uint64_t threshold;        // composite of the last kept element
+  uint64_t total, at;        // kept weights of the row; of the CTA `owner`, what the drawn token's pass
+  int32_t owner;             // -1: the border was not in the list
+};
 template <typename T>
 struct Shared {
   static constexpr int kSegment = Quad<T>::kListMost / 16;   // candidates of a warp
   Told told[kCtas];
   Params params;
+  Verdict verdict;
   float octave[kCtas][kOctaveBins];      // sums of the exponents' bins
   uint16_t count[kRanges];               // candidates of every warp
   T logit[kWarps][kSegment];             // this CTA's, and their places in the warp's range, by place
@@ -224,7 +230,6 @@ struct Scratch {
   uint64_t warp_sum[kWarps];
   float bin[32];
   Found found;
-  uint32_t overflow;
   uint64_t composite;
 };
 
@@ -765,7 +770,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     for (int round = 0; round < 2; ++round) {
       from_top = !mass && round == 0;
       uint64_t above = 0, kept = 0;
-      if (mass && local.least == 1) {   // this CTA's weights above: from its histogram
+      const bool by_weight = mass && local.least > 1;   // min-p: what is kept above is summed element by element
+      if (!by_weight) {   // what this CTA has above: from its histogram
         if (round == 0) {
 #pragma unroll
           for (int k = 0; k < kYBins / kThreads; ++k) {
@@ -773,17 +779,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             if (b >= border) continue;
             const uint64_t m = (static_cast<uint64_t>(hist[b]) << lead) + hist[kYBins + b];   // units of 2^(o + 1 - 2 lead)
             const int down = o + 2 * lead - 45;   // to 2^-44
-            above += down > 0 ? (m + (1ull << down >> 1)) >> down : m << -down;
+            above += !mass ? hist[b] : down > 0 ? (m + (1ull << down >> 1)) >> down : m << -down;
           }
         } else {
           const int b = kBins - 1 - tid;
-          if (b > kBins - 1 - fine) above = (static_cast<uint64_t>(hist[kBins + b]) << 32) + hist[b];
+          if (b > kBins - 1 - fine) above = (mass ? static_cast<uint64_t>(hist[kBins + b]) << 32 : 0) + hist[b];
           if (tid == 0) above += mine.told[rank].above;
         }
         kept = above;
       }
       n = 0;
+      // the border's bin as a range of logits less ref, a little wide: most steps of a warp hold none of it
+      const float p_low = __uint_as_float(r.top_bits - static_cast<uint32_t>(2 * border - 62)) - kMagic - 0x1p-6f;
+      const float p_high = __uint_as_float(r.top_bits - static_cast<uint32_t>(max(2 * border - 63, 0))) - kMagic + 0x1p-6f;
+      const float x_low = p_low / r.c_hi, x_high = from_top ? INFINITY : p_high / r.c_hi;
       each_tile([&](int t, const float (&x)[4]) {
+        bool near = by_weight;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) near = near || (x[k] - local.ref >= x_low && x[k] - local.ref <= x_high);
+        if (!__any_sync(0xffffffffu, near)) return;
         int32_t code[4];   // the bin, and its part in the second round: smaller above
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -804,10 +818,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           take |= static_cast<uint32_t>(code[k] == at_border) << k;
           higher |= static_cast<uint32_t>(code[k] < at_border) << k;
         }
-        if (!mass) {
-          above += __popc(higher);
-          if (from_top) take |= higher;
-        } else if (local.least > 1 && __any_sync(0xffffffffu, higher != 0)) {
+        if (from_top) take |= higher;
+        if (by_weight && __any_sync(0xffffffffu, higher != 0)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             Weights v;
@@ -859,23 +871,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           to->told[rank].above = above;
           to->told[rank].kept = kept;
         }
-        if (lane == 0) s.overflow = 0;
       }
       cluster.sync();
 
-      // the list's length, the places of the ranges in it, the sums of all
-      {
-        const int32_t c = tid < kRanges ? mine.count[tid] : 0;
-        if (c > Pub::kSegment) s.overflow = 1;
-        const Sums all = exclusive_sum(static_cast<uint64_t>(c), s.warp_sum);
-        if (tid <= kRanges) list_at[tid] = static_cast<int32_t>(all.before);
-        n = static_cast<int32_t>(all.all);
-      }
-      __syncthreads();
+      // the list's length (every warp by itself), and what lies above it
+      static_assert(kRanges == 128, "four counts a lane");
+      const ushort4 counts = reinterpret_cast<const ushort4 *>(mine.count)[lane];
+      n = __reduce_add_sync(0xffffffffu, counts.x + counts.y + counts.z + counts.w);
+      const bool fits = __all_sync(0xffffffffu, max(max(counts.x, counts.y), max(counts.z, counts.w)) <= Pub::kSegment);
       over = 0;
 #pragma unroll
       for (int c = 0; c < kCtas; ++c) over += mine.told[c].above;
-      listed = n > 0 && n <= kListMost && s.overflow == 0;
+      listed = n > 0 && n <= kListMost && fits;
       if (from_top && listed) over = 0;   // they are in the list themselves
       if (listed || round == 1 || over >= want) break;
 
@@ -905,8 +912,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       fine = kBins - 1 - static_cast<int32_t>(f.bin);
     }
 
-    bool reading = false;   // a barrier behind the last read from other CTAs has begun
-    if (listed) {
+    // the list: gathered and searched by the first CTA
+    Verdict verdict{0, 0, 0, -1};
+    if (listed && rank == 0) {
+      {
+        const Sums all = exclusive_sum(tid < kRanges ? mine.count[tid] : 0, s.warp_sum);
+        if (tid <= kRanges) list_at[tid] = static_cast<int32_t>(all.before);
+        __syncthreads();
+      }
       for (int i = tid; i < n; i += kThreads) {
         int w = 0;
 #pragma unroll
@@ -916,14 +929,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const int k = i - list_at[w];
         list[i] = composite(Q::one(from->logit[w % kWarps][k]), w * len + from->place[w % kWarps][k]);
       }
-      if (mass || from_top) {   // what follows needs no other CTA
-        cluster.barrier_arrive();
-        reading = true;
-        if (from_top && rank != 0) {   // everything that is kept is in the first CTA's list as well
-          cluster.barrier_wait();
-          return;
-        }
-      }
+      if (from_top) cluster.barrier_arrive();   // everything that is kept is in the list: the other CTAs may go
       __syncthreads();
       const auto list_weight = [&](int i) { return weight(radix_key_value(static_cast<uint32_t>(list[i] >> kIndexBits)), r, table); };
       const auto kept_weight = [&](int i) {   // behind the search
@@ -1008,6 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         cluster.barrier_wait();
         return;
       }
+      verdict.threshold = threshold;
       if (mass && found) {
         // up to each CTA's part: the list's kept weights before it
         __syncthreads();
@@ -1019,27 +1026,45 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           cta_at[tid] = at;
         }
         __syncthreads();
-        uint64_t all = list_total, reach = cta_at[rank];
-        for (int c = 0; c < kCtas; ++c) {
-          all += mine.told[c].kept;
-          if (c < rank) reach += mine.told[c].kept;
+        // the CTA in which the sums pass u Z
+        const int c = lane & (kCtas - 1);
+        const uint64_t here = mine.told[c].kept + cta_at[c + 1] - cta_at[c];
+        uint64_t upto = here;
+#pragma unroll
+        for (int o = 1; o < kCtas; o <<= 1) {
+          const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o, kCtas);
+          if (c >= o) upto += up;
         }
-        const uint64_t at = __umul64hi(f_u, all), here = mine.told[rank].kept + cta_at[rank + 1] - cta_at[rank];
-        if (at >= reach && at < reach + here) {
+        verdict.total = __shfl_sync(0xffffffffu, upto, kCtas - 1);
+        const uint64_t at = __umul64hi(f_u, verdict.total);
+        verdict.owner = __ffs(__ballot_sync(0xffffffffu, at < upto)) - 1;
+        verdict.at = at - __shfl_sync(0xffffffffu, upto - here, verdict.owner);
+      } else if (!mass) {
+        verdict.owner = 0;
+      }
+      if (warp == 0 && lane < kCtas) cluster.map_shared_rank(&mine, lane)->verdict = verdict;
+    } else if (listed && from_top) {
+      cluster.sync();
+      return;
+    }
+    if (listed) {
+      cluster.sync();
+      verdict = mine.verdict;
+      threshold = verdict.threshold;
+      listed = verdict.owner >= 0;
+      if (mass && listed) {
+        if (rank == verdict.owner) {
           // this CTA's kept weights exactly (the histogram's may differ in the last units)
           const uint64_t kept = kept_sums(local, threshold);
           if (lane == 0) warp_kept[warp] = kept;
           __syncthreads();
           uint64_t exact = 0;
           for (int v = 0; v < kWarps; ++v) exact += warp_kept[v];
-          pick<T>(a, row, data, rank, warp_kept, 0, min(at - reach, exact - 1), threshold, all, r, table, tile_sum);
+          pick<T>(a, row, data, rank, warp_kept, 0, min(verdict.at, exact - 1), threshold, verdict.total, r, table, tile_sum);
         }
-        cluster.barrier_wait();
         return;
       }
-      listed = found;
     }
-    if (reading) cluster.barrier_wait();
     if (!listed) {
       // long lists: a descent over the row
       uint64_t left = want, prefix = 0;
