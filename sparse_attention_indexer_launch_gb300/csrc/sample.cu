@@ -9,7 +9,7 @@
 //
 // A token may not depend on how sums are rounded, and a border (u Z between two tokens' sums,
 // p Z between two masses) lies within 2^-24 of some sum in a percent of the rows.  So weights
-// are integers, 2^44 exp((l - l_ref) / T) to about 2^-39 of itself or one unit; their sums are
+// are integers, 2^44 exp((l - l_ref) / T) to about 2^-38 of itself or one unit; their sums are
 // exact in 64 bits whatever the order, and the comparisons with p Z and u Z exact in 128.
 //
 // Thresholds: the kept tokens are a prefix of the order (logit descending, index ascending),
@@ -46,7 +46,7 @@ constexpr int kOctaveBins = 48;  // octaves, with room
 constexpr int kYBins = kOctaveBins * 32;   // (d + 63) / 2 for d < kCut, 32 to an octave
 constexpr int kDigit = 9;        // bits of a descent's level
 constexpr int kBins = 1 << kDigit;
-constexpr int kSmallList = 256;  // searched by a thread per element
+constexpr int kSmallList = 256;  // searched by two or four threads per element
 constexpr int kIndexBits = 19;
 constexpr int kCompositeBits = 32 + kIndexBits;
 static_assert(IDX_MAX_VOCAB <= 1 << kIndexBits, "an index in a composite");
@@ -85,32 +85,33 @@ struct Row {
   float ref;
   float temperature;    // within 2^-60 .. 2^60
   float c_hi, c_lo;     // c in two terms
-  uint32_t top_bits;    // p + kMagic of the largest
+  uint32_t whole_bits;  // p + kMagic of the largest, up to a whole octave: weights are relative to that
   uint64_t least;       // of the weights that min-p keeps
 };
 
-// p in two terms for two logits.
-__device__ __forceinline__ void exponents(float x0, float x1, const Row &r, uint64_t &p, uint64_t &lo) {
+// -p for two logits, in two terms (p = -(minus) + lo).
+__device__ __forceinline__ void exponents(float x0, float x1, const Row &r, uint64_t &minus, uint64_t &lo) {
   const uint64_t x = fma2(pack2(x0, x1), pack2(1.0f, 1.0f), pack2(-r.ref, -r.ref));
-  p = mul2(x, pack2(r.c_hi, r.c_hi));
-  lo = fma2(x, pack2(r.c_lo, r.c_lo), fma2(x, pack2(r.c_hi, r.c_hi), mul2(p, pack2(-1.0f, -1.0f))));
+  minus = mul2(x, pack2(-r.c_hi, -r.c_hi));
+  lo = fma2(x, pack2(r.c_lo, r.c_lo), fma2(x, pack2(r.c_hi, r.c_hi), minus));
 }
-// p in steps of 1 / 64 below the largest's.  Unsigned: floats' bits ascend with their values,
-// and those of negative ones and of NaN end up far behind kCut as well.
-__device__ __forceinline__ void steps(uint64_t p, const Row &r, uint64_t &t, uint32_t (&d)[2]) {
-  t = fma2(p, pack2(1.0f, 1.0f), pack2(kMagic, kMagic));
-  d[0] = r.top_bits - static_cast<uint32_t>(t);
-  d[1] = r.top_bits - static_cast<uint32_t>(t >> 32);
+// p to 64ths, as the bits of a float: they ascend with p, from kMagic's for 0 by one a 64th.
+__device__ __forceinline__ uint64_t to_64ths(uint64_t minus) { return fma2(minus, pack2(-1.0f, -1.0f), pack2(kMagic, kMagic)); }
+// 64ths below the largest's octave for each.  Unsigned: negative floats and NaN end up far behind
+// kCut as well.
+__device__ __forceinline__ void steps(uint64_t t, const Row &r, uint32_t (&d)[2]) {
+  d[0] = r.whole_bits - static_cast<uint32_t>(t);
+  d[1] = r.whole_bits - static_cast<uint32_t>(t >> 32);
 }
 
-// A bin of exponents for d steps, kFar for what has no weight.
+// A bin of exponents for d 64ths, kFar for what has no weight.
 constexpr int32_t kFar = 1 << 20;
 __device__ __forceinline__ int32_t exponent_bin(uint32_t d) { return d < kCut ? static_cast<int32_t>((d + 63) >> 1) : kFar; }
 // The part of its bin that element i of a pair lies in, behind the bin: smaller above.
-__device__ __forceinline__ int32_t fine_code(uint64_t p, uint64_t t, uint32_t d, int i) {
+__device__ __forceinline__ int32_t fine_code(uint64_t minus, uint64_t t, uint32_t d, int i) {
   if (d >= kCut) return kFar * kFine;
-  const float v = __uint_as_float(static_cast<uint32_t>(p >> (32 * i))), c = __uint_as_float(static_cast<uint32_t>(t >> (32 * i)));
-  const float f = v - (c - kMagic);   // exact, within 2^-7: 128 parts of a 64th
+  const float v = __uint_as_float(static_cast<uint32_t>(minus >> (32 * i))), c = __uint_as_float(static_cast<uint32_t>(t >> (32 * i)));
+  const float f = (kMagic - c) - v;   // exact, within 2^-7: 128 parts of a 64th
   const int32_t part = min(max(static_cast<int32_t>((f + 0x1p-7f) * 0x1p13f), 0), kFine / 2 - 1);
   return static_cast<int32_t>(d + 63) * (kFine / 2) + (kFine / 2 - 1 - part);
 }
@@ -121,27 +122,28 @@ __device__ __forceinline__ int32_t fine_code(uint64_t p, uint64_t t, uint32_t d,
 // of a weight stands for all below it (it is always set), so roundings have no direction.
 // Measured against 64 bits: off by 2^-38.2 in the mean square, 2^-36.2 at most.
 struct Weights {
-  uint64_t w[2], m[2];
+  uint64_t w[2], m[2];   // w: of no meaning from kCut on
   uint32_t d[2];
 };
 __device__ __forceinline__ void weights(float x0, float x1, const Row &r, const Exp2 *table, Weights &out) {
-  constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;
-  constexpr float kTail = 0x1.8p-14f;   // 1.5 * 2^-14: a sum's last bit is 2^-37
-  uint64_t p, lo, t;
-  exponents(x0, x1, r, p, lo);
-  steps(p, r, t, out.d);
-  const Exp2 *const column = table + (threadIdx.x & (kColumns - 1));
-  const Exp2 e0 = column[(0u - out.d[0] & 63u) * kColumns], e1 = column[(0u - out.d[1] & 63u) * kColumns];
-  const uint64_t one = pack2(1.0f, 1.0f), minus = pack2(-1.0f, -1.0f), ln2 = pack2(kLn2Hi, kLn2Hi);
+  constexpr float kLn2 = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;
+  constexpr float kTail = 0x1.8p-14f;     // 1.5 * 2^-14: a sum's last bit is 2^-37
+  uint64_t minus, lo;
+  exponents(x0, x1, r, minus, lo);
+  const uint64_t t = to_64ths(minus), one = pack2(1.0f, 1.0f), negative = pack2(-1.0f, -1.0f), ln2 = pack2(kLn2, kLn2);
+  steps(t, r, out.d);
+  // (kMagic's last six bits are 0, and so are the octave's)
+  const uint32_t column = threadIdx.x & (kColumns - 1);
+  const Exp2 e0 = table[(static_cast<uint32_t>(t) & 63u) * kColumns | column], e1 = table[(static_cast<uint32_t>(t >> 32) & 63u) * kColumns | column];
   lo = pack2(__uint_as_float(static_cast<uint32_t>(lo)) - e0.off, __uint_as_float(static_cast<uint32_t>(lo >> 32)) - e1.off);
-  const uint64_t f = fma2(fma2(t, one, pack2(-kMagic, -kMagic)), minus, p);   // p less its 64ths
+  const uint64_t f = fma2(minus, negative, fma2(t, negative, pack2(kMagic, kMagic)));   // p less its 64ths
   // exp((f + lo) ln 2) - 1 = h + q, with h + b = (f + lo) ln 2
-  const uint64_t h = mul2(f, ln2);
-  const uint64_t b = fma2(lo, ln2, fma2(f, pack2(kLn2Lo, kLn2Lo), fma2(f, ln2, mul2(h, minus))));
-  const uint64_t g = fma2(h, one, b);
+  const uint64_t mh = mul2(f, pack2(-kLn2, -kLn2));   // -h
+  const uint64_t b = fma2(lo, ln2, fma2(f, pack2(kLn2Lo, kLn2Lo), fma2(f, ln2, mh)));
+  const uint64_t g = fma2(mh, negative, b);
   const uint64_t a = fma2(g, fma2(g, pack2(1.0f / 24.0f, 1.0f / 24.0f), pack2(1.0f / 6.0f, 1.0f / 6.0f)), pack2(0.5f, 0.5f));
   const uint64_t tail = fma2(fma2(mul2(g, g), a, b), one, pack2(kTail, kTail));
-  const uint64_t head = mul2(h, pack2(0x1p37f, 0x1p37f));
+  const uint64_t head = mul2(mh, pack2(-0x1p37f, -0x1p37f));
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int32_t gi = __float2int_rn(__uint_as_float(static_cast<uint32_t>(head >> (32 * i)))) +
@@ -149,13 +151,13 @@ __device__ __forceinline__ void weights(float x0, float x1, const Row &r, const 
     const int32_t e = i == 0 ? e0.t : e1.t;
     const uint64_t w = (static_cast<uint64_t>(static_cast<uint32_t>(e) << 5) << 32) + static_cast<uint64_t>(static_cast<int64_t>(e) * gi);
     out.m[i] = w;
-    out.w[i] = out.d[i] < kCut ? w >> ((out.d[i] + 63 + 18 * 64) >> 6) | 1ull : 0ull;
+    out.w[i] = w >> ((out.d[i] + 63 + 18 * 64) >> 6) | 1ull;
   }
 }
 __device__ __noinline__ uint64_t weight(float x, const Row &r, const Exp2 *table) {   // one, where they are few
   Weights v;
   weights(x, x, r, table, v);
-  return v.w[0];
+  return v.d[0] < kCut ? v.w[0] : 0;
 }
 
 __device__ __forceinline__ uint32_t key_of(float x) { return x != x ? kKeyMasked : radix_key(x); }
@@ -307,7 +309,7 @@ __device__ __noinline__ void pick(const SampleArgs &a, int64_t row, const T *dat
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int k = 2 * h + i;
-          w[k] = v.w[i] >= r.least && composite(x[k], base + t * kTile + 4 * lane + k) >= threshold ? v.w[i] : 0;
+          w[k] = v.d[i] < kCut && v.w[i] >= r.least && composite(x[k], base + t * kTile + 4 * lane + k) >= threshold ? v.w[i] : 0;
           sum += w[k];
         }
       }
@@ -650,13 +652,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   local.c_hi = mine.params.c_hi;
   local.c_lo = mine.params.c_lo;
   local.ref = fabsf(local.top * local.c_hi) <= 128.0f ? 0.0f : local.top;
-  local.top_bits = 0;
   {
-    uint64_t p, lo, t;
-    uint32_t d[2];
-    exponents(local.top, local.top, local, p, lo);
-    steps(p, local, t, d);
-    local.top_bits = 0u - d[0];
+    uint64_t minus, lo;
+    exponents(local.top, local.top, local, minus, lo);
+    local.whole_bits = (static_cast<uint32_t>(to_64ths(minus)) + 63u) & ~63u;
   }
   local.least = 1;
   if (tid == 0) r = local;   // for what is not inlined
@@ -677,6 +676,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       f(t, x);
     }
   };
+  // the same, two steps at a time
+  const auto each_two_tiles = [&](auto f) {
+    int t = 0;
+#pragma unroll 1
+    for (; t + kTile < len; t += 2 * kTile) {
+      float x[4], y[4];
+      Q::get(*reinterpret_cast<const Vec *>(own + t + 4 * lane), x);
+      Q::get(*reinterpret_cast<const Vec *>(own + t + kTile + 4 * lane), y);
+      f(t, x);
+      f(t + kTile, y);
+    }
+    if (t < len) {
+      float x[4];
+      Q::get(*reinterpret_cast<const Vec *>(own + t + 4 * lane), x);
+      f(t, x);
+    }
+  };
   // the warp's kept weights
   const auto kept_sums = [&](const Row &q, uint64_t threshold) {
     uint64_t sum = 0;
@@ -687,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         weights(x[2 * h], x[2 * h + 1], q, table, v);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (v.w[i] >= q.least && (!(kTopK || kTopP) || threshold == 0 || composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) >= threshold)) sum += v.w[i];
+          if (v.d[i] < kCut && v.w[i] >= q.least && (!(kTopK || kTopP) || threshold == 0 || composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) >= threshold)) sum += v.w[i];
       }
     });
     return warp_total(sum);
@@ -715,9 +731,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             if (v.d[i] < kCut && (!kTopK || low == 0 || among(composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i)))) {
               sum += v.w[i];
               uint32_t *const bin = hist + ((v.d[i] + 63) >> 1);
-              const uint64_t m = v.m[i] << 1;   // the leading bit on top
-              atomicAdd(bin, static_cast<uint32_t>(m >> 32) >> (32 - lead));
-              atomicAdd(bin + kYBins, (static_cast<uint32_t>(m >> (64 - 2 * lead)) & ((1u << lead) - 1)) | 1u);
+              atomicAdd(bin, static_cast<uint32_t>(v.m[i] >> 32) >> (31 - lead));
+              atomicAdd(bin + kYBins, (static_cast<uint32_t>(v.m[i] >> (63 - 2 * lead)) & ((1u << lead) - 1)) | 1u);
             }
           }
         }
@@ -725,13 +740,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       sum = warp_total(sum);
       if (lane == 0) warp_above[warp] = sum;
     } else {
-      each_tile([&](int, const float (&x)[4]) {
+      each_two_tiles([&](int, const float (&x)[4]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint64_t p, lo, t;
+          uint64_t minus, lo;
           uint32_t d[2];
-          exponents(x[2 * h], x[2 * h + 1], local, p, lo);
-          steps(p, local, t, d);
+          exponents(x[2 * h], x[2 * h + 1], local, minus, lo);
+          steps(to_64ths(minus), local, d);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             if (d[i] < kCut) atomicAdd(&hist[(d[i] + 63) >> 1], 1u);
@@ -790,8 +805,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       n = 0;
       // the border's bin as a range of logits less ref, a little wide: most steps of a warp hold none of it
-      const float p_low = __uint_as_float(r.top_bits - static_cast<uint32_t>(2 * border - 62)) - kMagic - 0x1p-6f;
-      const float p_high = __uint_as_float(r.top_bits - static_cast<uint32_t>(max(2 * border - 63, 0))) - kMagic + 0x1p-6f;
+      const float p_low = __uint_as_float(r.whole_bits - static_cast<uint32_t>(2 * border - 62)) - kMagic - 0x1p-6f;
+      const float p_high = __uint_as_float(r.whole_bits - static_cast<uint32_t>(max(2 * border - 63, 0))) - kMagic + 0x1p-6f;
       const float x_low = p_low / r.c_hi, x_high = from_top ? INFINITY : p_high / r.c_hi;
       each_tile([&](int t, const float (&x)[4]) {
         bool near = by_weight;
@@ -801,14 +816,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         int32_t code[4];   // the bin, and its part in the second round: smaller above
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint64_t p, lo, b;
+          uint64_t minus, lo;
           uint32_t d[2];
-          exponents(x[2 * h], x[2 * h + 1], local, p, lo);
-          steps(p, local, b, d);
+          exponents(x[2 * h], x[2 * h + 1], local, minus, lo);
+          const uint64_t t64 = to_64ths(minus);
+          steps(t64, local, d);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             code[2 * h + i] = exponent_bin(d[i]);
-            if (round == 1) code[2 * h + i] = fine_code(p, b, d[i], i);
+            if (round == 1) code[2 * h + i] = fine_code(minus, t64, d[i], i);
           }
         }
         const int32_t at_border = round == 0 ? border : border * kFine + fine;
@@ -892,15 +908,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       each_tile([&](int t, const float (&x)[4]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint64_t p, lo, b;
+          uint64_t minus, lo;
           uint32_t d[2];
-          exponents(x[2 * h], x[2 * h + 1], local, p, lo);
-          steps(p, local, b, d);
+          exponents(x[2 * h], x[2 * h + 1], local, minus, lo);
+          const uint64_t t64 = to_64ths(minus);
+          steps(t64, local, d);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (exponent_bin(d[i]) != border) continue;
             if (kTopK && low != 0 && !among(composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i))) continue;
-            const uint32_t bin = kBins - 1 - fine_code(p, b, d[i], i) % kFine;
+            const uint32_t bin = kBins - 1 - fine_code(minus, t64, d[i], i) % kFine;
             if (mass) add_to_hist(hist, bin, weight(x[2 * h + i], r, table));
             else atomicAdd(&hist[bin], 1u);
           }
@@ -938,26 +955,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       };
       uint64_t *const part = reinterpret_cast<uint64_t *>(hist);   // [kThreads]
       bool found = true;
+      // threads of an element of a small list; of others a thread has kChunk
+      const int split = n <= 128 ? 4 : n <= kSmallList ? 2 : 0;
       uint64_t before = 0, list_total = 0, own_kept = 0;   // kept weights: before this thread's, all, its own
       if (n <= kSmallList) {
-        // a thread per element; the rank and the weight of what lies above it by looking at all
+        // threads e * split .. for element e: its rank and the weight of what lies above it by looking at all
         ulonglong2 *const both = reinterpret_cast<ulonglong2 *>(hist);
-        const uint64_t mine_c = tid < n ? list[tid] : 0, mine_w = tid < n && among(mine_c) ? list_weight(tid) : 0;
-        if (tid < n) both[tid] = make_ulonglong2(mine_c, mine_w);
+        const int e = tid / split, part_of = tid % split;
+        const bool here = e < n;
+        const uint64_t mine_c = here ? list[e] : 0;
+        if (tid < n) both[tid] = make_ulonglong2(list[tid], among(list[tid]) ? list_weight(tid) : 0);
         __syncthreads();
+        const uint64_t mine_w = here ? both[e].y : 0;
         uint64_t higher = 0;
         uint32_t higher_n = 0;
-        if (warp * 32 < n) {
+        if (__any_sync(0xffffffffu, here)) {
 #pragma unroll 4
-          for (int j = 0; j < n; ++j) {
-            const ulonglong2 e = both[j];
-            if (e.x > mine_c) {
-              ++higher_n;
-              higher += e.y;
-            }
+          for (int j = part_of; j < n; j += split) {
+            const ulonglong2 o = both[j];
+            const bool above = o.x > mine_c;
+            higher_n += above;
+            higher += above ? o.y : 0;
+          }
+          for (int o = 1; o < split; o <<= 1) {
+            higher_n += __shfl_xor_sync(0xffffffffu, higher_n, o);
+            higher += __shfl_xor_sync(0xffffffffu, higher, o);
           }
         }
-        bool keep = tid < n && among(mine_c);
+        bool keep = here && part_of == 0 && among(mine_c);
         if (!mass) keep = keep && over + higher_n < want;
         if (mass || (kTopP && from_top && top_p < 1.0f)) {
           const uint64_t all = exclusive_sum(keep ? mine_w : 0, s.warp_sum).all;
@@ -1002,11 +1027,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           part[tid] = before;
         }
       }
-      const int chunk = n <= kSmallList ? 1 : kChunk;   // elements of a thread
       if (from_top) {
         const uint64_t at = __umul64hi(f_u, list_total);
         if (at >= before && at < before + own_kept) {
-          int i = tid * chunk;
+          int i = split > 0 ? tid / split : tid * kChunk;
           for (uint64_t v; at >= before + (v = kept_weight(i)); ++i) before += v;
           finish(a, row, (1 << kIndexBits) - 1 - static_cast<int>(list[i] & ((1u << kIndexBits) - 1)),
                  radix_key_value(static_cast<uint32_t>(list[i] >> kIndexBits)), list_total, r, table);
@@ -1019,10 +1043,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         // up to each CTA's part: the list's kept weights before it
         __syncthreads();
         if (tid <= kCtas) {
-          const int i = list_at[tid * kWarps], t = i / chunk;
+          const int i = list_at[tid * kWarps], t = split > 0 ? i * split : i / kChunk;   // the thread that has it
           uint64_t at = t < kThreads ? part[t] : list_total;
 #pragma unroll 1
-          for (int j = t * chunk; j < i; ++j) at += kept_weight(j);
+          for (int j = split > 0 ? i : t * kChunk; j < i; ++j) at += kept_weight(j);
           cta_at[tid] = at;
         }
         __syncthreads();
