@@ -528,8 +528,8 @@ typedef struct {
  *   logprob  device fp32 [R] or NULL: the log of the token's probability among the kept
  *            (-inf beside token -1).
  * A NaN counts as -inf; with logits of +inf those alone have weight.  Weights are held to
- * about 2^-38 of themselves as integers of 2^-44 of the largest (0 below it) and summed
- * exactly: where 64-bit sums put a token, so does this, but for numbers u that close to a
+ * about 2^-38 of themselves as integers, one unit 2^-44 of the power of two at or above the
+ * largest (0 below a unit), and summed exactly: where 64-bit sums put a token, so does this, but for numbers u that close to a
  * border.  Equal calls give equal results.
  * Asynchronous on `stream`; allocates nothing and needs no workspace. */
 idx_status idx_sample(const idx_sample_args *args, int32_t *token, float *logprob, void *stream);

@@ -1,7 +1,7 @@
 // A token of every row of logits: temperature, top-k, top-p and min-p, drawn with given
 // random numbers.
 //
-// Eight CTAs, a cluster, hold one row in shared memory: the logits are read once, and what
+// A cluster of up to eight CTAs holds one row in shared memory: the logits are read once, and what
 // the CTAs need of each other (maxima, histograms, sums, candidates) they read from each
 // other's shared memory between cluster barriers.  Every CTA then finds the same thresholds
 // from the same numbers; parameters come from the first CTA's copy, so that no barrier
@@ -9,7 +9,8 @@
 //
 // A token may not depend on how sums are rounded, and a border (u Z between two tokens' sums,
 // p Z between two masses) lies within 2^-24 of some sum in a percent of the rows.  So weights
-// are integers, 2^44 exp((l - l_ref) / T) to about 2^-38 of itself or one unit; their sums are
+// are integers, 2^44 exp(l / T) over the power of two at or above the largest exp(l / T), to
+// about 2^-38 of itself or one unit; their sums are
 // exact in 64 bits whatever the order, and the comparisons with p Z and u Z exact in 128.
 //
 // Thresholds: the kept tokens are a prefix of the order (logit descending, index ascending),
@@ -33,14 +34,14 @@ namespace cg = cooperative_groups;
 namespace idx {
 namespace {
 
-constexpr int kCtas = 8;         // of a cluster: a row
+constexpr int kCtas = 8;         // of a cluster, a row, at most
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRanges = kCtas * kWarps;   // a warp's part of the row
+constexpr int kRanges = kCtas * kWarps;   // warps' parts of the row
 constexpr int kTile = 128;       // a warp's step: four elements a lane
 constexpr uint32_t kKeyMasked = 0x007FFFFFu;   // radix_key(-inf)
 constexpr int kFine = 256;       // parts of such a bin
-constexpr int kOctaves = 44;     // below 2^-44 of the largest: no weight
+constexpr int kOctaves = 44;     // below 2^-44 of the largest's octave: no weight
 constexpr int kCut = kOctaves * 64;
 constexpr int kOctaveBins = 48;  // octaves, with room
 constexpr int kYBins = kOctaveBins * 32;   // (d + 63) / 2 for d < kCut, 32 to an octave
@@ -211,9 +212,9 @@ struct Verdict {             // on a list, from the first CTA
   uint64_t total, at;        // kept weights of the row; of the CTA `owner`, what the drawn token's pass
   int32_t owner;             // -1: the border was not in the list
 };
-template <typename T>
+template <typename T, bool kList>
 struct Shared {
-  static constexpr int kSegment = Quad<T>::kListMost / 16;   // candidates of a warp
+  static constexpr int kSegment = kList ? Quad<T>::kListMost / 16 : 1;   // candidates of a warp
   Told told[kCtas];
   Params params;
   Verdict verdict;
@@ -391,7 +392,7 @@ __device__ __noinline__ void push_octaves(const uint32_t *hist, float low, float
   for (int o = warp; o < kOctaveBins; o += kWarps) {
     float v = static_cast<float>(__reduce_add_sync(0xffffffffu, hist[o * 32 + lane]));
     if (low != 0.0f) v = fmaf(static_cast<float>(__reduce_add_sync(0xffffffffu, hist[kYBins + o * 32 + lane])), low, v);
-    if (lane < kCtas) cg::this_cluster().map_shared_rank(octave, lane)[cg::this_cluster().block_rank()][o] = v;
+    if (lane < cg::this_cluster().num_blocks()) cg::this_cluster().map_shared_rank(octave, lane)[cg::this_cluster().block_rank()][o] = v;
   }
 }
 
@@ -427,7 +428,7 @@ struct Exponent {
 };
 __device__ __noinline__ Exponent find_exponent(float low, const uint32_t *hist, const float (*octave)[kOctaveBins], float *sum, float want) {
   static_assert(kOctaveBins > 32 && kOctaveBins <= 64, "one or two octaves a lane");
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, ctas = static_cast<int>(cg::this_cluster().num_blocks());
   const auto scaled = [&](float v, int o) { return low != 0.0f ? v * __uint_as_float(static_cast<uint32_t>(127 - o) << 23) : v; };
   float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
@@ -446,12 +447,16 @@ __device__ __noinline__ Exponent find_exponent(float low, const uint32_t *hist, 
     before = r.all + far.before;
   }
   if (tid < 32 * kCtas) {
-    const uint32_t *const h = cg::this_cluster().map_shared_rank(hist, tid % kCtas) + o * 32 + tid / kCtas;
-    float v = static_cast<float>(*h);
-    if (low != 0.0f) v = fmaf(static_cast<float>(h[kYBins]), low, v);
+    const int c = tid & (kCtas - 1), b = tid / kCtas;
+    float v = 0.0f;
+    if (c < ctas) {
+      const uint32_t *const h = cg::this_cluster().map_shared_rank(hist, c) + o * 32 + b;
+      v = static_cast<float>(*h);
+      if (low != 0.0f) v = fmaf(static_cast<float>(h[kYBins]), low, v);
+    }
 #pragma unroll
     for (int k = kCtas / 2; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-    if (tid % kCtas == 0) sum[tid / kCtas] = scaled(v, o);
+    if (c == 0) sum[b] = scaled(v, o);
   }
   __syncthreads();
   e.bin = o * 32 + reach_in_warp(sum[lane], want - before).at;
@@ -501,15 +506,16 @@ __device__ __noinline__ uint64_t descend_list(bool mass, const uint64_t *list, i
   return prefix;
 }
 
-// The histograms, the list (in the second half of them where it fits), the row.
+// The histograms, the list (in the second half of them where it fits), the row; without filters
+// the row alone.
 template <typename T>
 __host__ __device__ constexpr size_t list_offset() {
   return Quad<T>::kListMost * sizeof(uint64_t) <= kYBins * sizeof(uint32_t) ? kYBins * sizeof(uint32_t) : 2 * kYBins * sizeof(uint32_t);
 }
-template <typename T>
+template <typename T, bool kList>
 __host__ __device__ constexpr size_t fixed_smem() {
   const size_t list = list_offset<T>() + Quad<T>::kListMost * sizeof(uint64_t), hist = 2 * kYBins * sizeof(uint32_t);
-  return list > hist ? list : hist;
+  return !kList ? 0 : list > hist ? list : hist;
 }
 
 // kTopK, kTopP: the rows may have these filters.
@@ -517,12 +523,12 @@ template <typename T, bool kTopK, bool kTopP>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
   using Q = Quad<T>;
   using Vec = typename Q::Vec;
-  using Pub = Shared<T>;
+  using Pub = Shared<T, kTopK || kTopP>;
   constexpr int kListMost = Q::kListMost, kChunk = (kListMost + kThreads - 1) / kThreads;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint32_t *const hist = reinterpret_cast<uint32_t *>(smem_raw);                     // [2][kYBins], [3][kBins] in descents
   uint64_t *const list = reinterpret_cast<uint64_t *>(smem_raw + list_offset<T>());  // [kListMost] composites, by index
-  T *const data = reinterpret_cast<T *>(smem_raw + fixed_smem<T>());
+  T *const data = reinterpret_cast<T *>(smem_raw + fixed_smem<T, kTopK || kTopP>());
   __shared__ Pub mine;
   __shared__ Scratch s;
   __shared__ Row r;
@@ -537,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x / kCtas;
+  const int ctas = a.ctas;   // a power of two
+  const int64_t row = blockIdx.x >> (__ffs(ctas) - 1);
   // this warp's range: [begin, begin + len) of the row, what lies past V masked
   const int len = a.warp_len;
   const int begin = (rank * kWarps + warp) * len;
@@ -547,7 +554,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   cluster.barrier_arrive();
   grid_dependency_trigger();
   for (int i = tid; i < 64 * kColumns; i += kThreads) table[i] = kExp2.v[i / kColumns];
-  clear_hist(hist, 2 * kYBins);
+  // what CTAs that are not there would tell
+  if (tid >= ctas && tid < kCtas) mine.told[tid] = Told{};
+  if constexpr (kTopK || kTopP) {
+    for (int i = ctas * kOctaveBins + tid; i < kCtas * kOctaveBins; i += kThreads) (&mine.octave[0][0])[i] = 0.0f;
+    if (tid >= ctas * kWarps && tid < kRanges) mine.count[tid] = 0;
+    clear_hist(hist, 2 * kYBins);
+  }
   grid_dependency_wait();
   Params par{};
   if (rank == 0 && warp == 0) {   // every lane the same; used behind the row's loads
@@ -616,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
   }
   cluster.barrier_wait();   // all CTAs run: their memory can be written
-  if (warp == 0 && lane < kCtas) {
+  if (warp == 0 && lane < ctas) {
     Pub *const to = cluster.map_shared_rank(&mine, lane);
     to->told[rank].best = best;
     if (rank == 0) to->params = par;
@@ -757,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     push_octaves(hist, low_unit, mine.octave);
     if (mass && warp == 0) {
       sum = warps_total(warp_above);
-      if (lane < kCtas) cluster.map_shared_rank(&mine, lane)->told[rank].all = sum;
+      if (lane < ctas) cluster.map_shared_rank(&mine, lane)->told[rank].all = sum;
     }
     cluster.sync();
     uint64_t want = static_cast<uint64_t>(top_k);
@@ -877,12 +890,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         warp_above[warp] = above;
         warp_kept[warp] = kept;
       }
-      if (lane < kCtas) cluster.map_shared_rank(&mine, lane)->count[rank * kWarps + warp] = static_cast<uint16_t>(n);   // at most the range
+      if (lane < ctas) cluster.map_shared_rank(&mine, lane)->count[rank * kWarps + warp] = static_cast<uint16_t>(n);   // at most the range
       __syncthreads();
       if (warp == 0) {
         above = warps_total(warp_above);
         kept = warps_total(warp_kept);
-        if (lane < kCtas) {
+        if (lane < ctas) {
           Pub *const to = cluster.map_shared_rank(&mine, lane);
           to->told[rank].above = above;
           to->told[rank].kept = kept;
@@ -924,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
       });
       cluster.sync();
-      const Found f = find_bin(mass, kCtas, hist, s, want - over);
+      const Found f = find_bin(mass, ctas, hist, s, want - over);
       if (f.bin == kBins) break;   // the leading bits had missed the bin
       fine = kBins - 1 - static_cast<int32_t>(f.bin);
     }
@@ -1042,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (mass && found) {
         // up to each CTA's part: the list's kept weights before it
         __syncthreads();
-        if (tid <= kCtas) {
+        if (tid <= ctas) {
           const int i = list_at[tid * kWarps], t = split > 0 ? i * split : i / kChunk;   // the thread that has it
           uint64_t at = t < kThreads ? part[t] : list_total;
 #pragma unroll 1
@@ -1052,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         __syncthreads();
         // the CTA in which the sums pass u Z
         const int c = lane & (kCtas - 1);
-        const uint64_t here = mine.told[c].kept + cta_at[c + 1] - cta_at[c];
+        const uint64_t here = c < ctas ? mine.told[c].kept + cta_at[c + 1] - cta_at[c] : 0;
         uint64_t upto = here;
 #pragma unroll
         for (int o = 1; o < kCtas; o <<= 1) {
@@ -1066,7 +1079,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       } else if (!mass) {
         verdict.owner = 0;
       }
-      if (warp == 0 && lane < kCtas) cluster.map_shared_rank(&mine, lane)->verdict = verdict;
+      if (warp == 0 && lane < ctas) cluster.map_shared_rank(&mine, lane)->verdict = verdict;
     } else if (listed && from_top) {
       cluster.sync();
       return;
@@ -1109,7 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           }
         });
         cluster.sync();
-        const Found f = find_bin(mass, kCtas, hist, s, left);
+        const Found f = find_bin(mass, ctas, hist, s, left);
         prefix = prefix << bits | f.bin;
         left -= f.above;
       }
@@ -1126,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   __syncthreads();
   if (warp == 0) {
     sum = warps_total(warp_kept);
-    if (lane < kCtas) cluster.map_shared_rank(&mine, lane)->told[rank].sum = sum;
+    if (lane < ctas) cluster.map_shared_rank(&mine, lane)->told[rank].sum = sum;
   }
   cluster.sync();
   uint64_t total = 0, reach = 0, here = 0;
@@ -1143,31 +1156,49 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 }
 
 template <typename T, bool kTopK, bool kTopP>
-cudaError_t launch(const SampleArgs &a, cudaStream_t stream) {
-  constexpr int kMost = static_cast<int>(fixed_smem<T>()) + IDX_MAX_VOCAB / kCtas * static_cast<int>(sizeof(T));
+cudaError_t launch(SampleArgs a, int num_sms, cudaStream_t stream) {
+  constexpr bool kList = kTopK || kTopP;
+  constexpr int kFixed = static_cast<int>(fixed_smem<T, kList>());
+  constexpr int kMost = kFixed + IDX_MAX_VOCAB / kCtas * static_cast<int>(sizeof(T));
+  constexpr int kHalf = 112 * 1024 - static_cast<int>(sizeof(Shared<T, kList>)) - 11 * 1024;   // dynamic shared memory with two CTAs to an SM
   static std::mutex mu;
   static bool done[128];
   cudaError_t e = once_per_device(mu, done, [] {
     return cudaFuncSetAttribute(sample_kernel<T, kTopK, kTopP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   });
   if (e != cudaSuccess) return e;
-  return launch_early(sample_kernel<T, kTopK, kTopP>, static_cast<unsigned>(a.p.R) * kCtas, kThreads,
-                      fixed_smem<T>() + static_cast<size_t>(kWarps) * a.warp_len * sizeof(T), kCtas, stream, a);
+  // CTAs of a row: by the cycles that all rows take, at a CTA's 15,000 and one a logit, two CTAs to
+  // an SM (64 x 128,000 bf16: four 22.9 us, eight 27.7; 8 x 151,552: eight).
+  const auto len_of = [&](int ctas) { return (a.p.V + ctas * kWarps * kTile - 1) / (ctas * kWarps * kTile) * kTile; };
+  int64_t best = 0;
+  a.ctas = 0;
+  for (int ctas = kCtas; ctas > 0; ctas /= 2) {
+    const int len = len_of(ctas);
+    if (ctas < kCtas && (len > 2 * kWarps * kTile || kFixed + kWarps * len * static_cast<int>(sizeof(T)) > kHalf)) break;
+    const int64_t slots = 2 * static_cast<int64_t>(num_sms) * 19 / 20, waves = (static_cast<int64_t>(a.p.R) * ctas + slots - 1) / slots;
+    const int64_t cycles = waves * (15000 + a.p.V / ctas);
+    if (a.ctas == 0 || cycles < best) {
+      best = cycles;
+      a.ctas = ctas;
+      a.warp_len = len;
+    }
+  }
+  return launch_early(sample_kernel<T, kTopK, kTopP>, static_cast<unsigned>(a.p.R) * static_cast<unsigned>(a.ctas), kThreads,
+                      kFixed + static_cast<size_t>(kWarps) * a.warp_len * sizeof(T), static_cast<unsigned>(a.ctas), stream, a);
 }
 
 template <typename T>
-cudaError_t launch(SampleArgs a, cudaStream_t stream) {
+cudaError_t launch(const SampleArgs &a, int num_sms, cudaStream_t stream) {
   constexpr int kSpan = kCtas * kWarps * kTile;
   static_assert(IDX_MAX_VOCAB % kSpan == 0 && IDX_MAX_VOCAB / kRanges / kTile <= 2 * kWarps, "whole steps of every warp");
-  a.warp_len = static_cast<int32_t>((a.p.V + kSpan - 1) / kSpan) * kTile;
-  if (a.p.top_k != nullptr) return a.p.top_p != nullptr ? launch<T, true, true>(a, stream) : launch<T, true, false>(a, stream);
-  return a.p.top_p != nullptr ? launch<T, false, true>(a, stream) : launch<T, false, false>(a, stream);
+  if (a.p.top_k != nullptr) return a.p.top_p != nullptr ? launch<T, true, true>(a, num_sms, stream) : launch<T, true, false>(a, num_sms, stream);
+  return a.p.top_p != nullptr ? launch<T, false, true>(a, num_sms, stream) : launch<T, false, false>(a, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
-  return a.p.logits_dtype == IDX_LOGITS_F32 ? launch<float>(a, stream) : launch<uint16_t>(a, stream);
+cudaError_t launch_sample(const SampleArgs &a, int num_sms, cudaStream_t stream) {
+  return a.p.logits_dtype == IDX_LOGITS_F32 ? launch<float>(a, num_sms, stream) : launch<uint16_t>(a, num_sms, stream);
 }
 
 }  // namespace idx
