@@ -529,8 +529,9 @@ typedef struct {
  *            (-inf beside token -1).
  * A NaN counts as -inf; with logits of +inf those alone have weight.  Weights are held to
  * about 2^-38 of themselves as integers, one unit 2^-44 of the power of two at or above the
- * largest (0 below a unit), and summed exactly: where 64-bit sums put a token, so does this, but for numbers u that close to a
- * border.  Equal calls give equal results.
+ * largest (0 below a unit), and summed exactly: where 64-bit sums put a token, so does this,
+ * but for numbers u that close to a border.  Equal calls give equal results, and a row the
+ * same in any batch.
  * Asynchronous on `stream`; allocates nothing and needs no workspace. */
 idx_status idx_sample(const idx_sample_args *args, int32_t *token, float *logprob, void *stream);
 
