@@ -292,59 +292,65 @@ __device__ __noinline__ void pick(const SampleArgs &a, int64_t row, const T *dat
                                   uint64_t at, uint64_t threshold, uint64_t total, const Row &r, const Exp2 *table, uint64_t *tile_sum) {
   using Q = Quad<T>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, len = a.warp_len, tiles = len / kTile;
-  int range = 0;
-  while (range < kWarps - 1 && at >= reach + warp_kept[range]) reach += warp_kept[range++];
-  const int base = (rank * kWarps + range) * len;
-  int chosen = -1;
-  // first the sums of all steps, then again the one that has it
-#pragma unroll 1
-  for (int t = warp;;) {
-    float x[4];
-    uint64_t w[4], sum = 0;
-    if (t < tiles) {
-      Q::get(*reinterpret_cast<const typename Q::Vec *>(data + range * len + t * kTile + 4 * lane), x);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        Weights v;
-        weights(x[2 * h], x[2 * h + 1], r, table, v);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int k = 2 * h + i;
-          w[k] = v.d[i] < kCut && v.w[i] >= r.least && composite(x[k], base + t * kTile + 4 * lane + k) >= threshold ? v.w[i] : 0;
-          sum += w[k];
-        }
-      }
-    }
-    if (chosen < 0 && t < tiles) {
-      sum = warp_total(sum);
-      if (lane == 0) tile_sum[t] = sum;
-      t += kWarps;
-      continue;
-    }
-    if (chosen < 0) {
-      __syncthreads();
-      chosen = 0;
-      while (chosen < tiles - 1 && at >= reach + tile_sum[chosen]) reach += tile_sum[chosen++];
-      if (chosen % kWarps != warp) return;
-      t = chosen;
-      continue;
-    }
-    uint64_t upto = sum;
+  // the last entry v[i], i < n <= 32, before which there is no more than `at` (and what is before it): for every warp by itself
+  const auto reached = [&](const uint64_t *v, int n) {
+    const uint64_t own = lane < n ? v[lane] : 0;
+    uint64_t upto = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += up;
     }
-    uint64_t from = reach + upto - sum;
+    const uint32_t past = __ballot_sync(0xffffffffu, at < reach + upto);
+    const int i = min(past != 0 ? __ffs(past) - 1 : 31, n - 1);
+    reach += __shfl_sync(0xffffffffu, upto - own, i);
+    return i;
+  };
+  const int range = reached(warp_kept, kWarps), base = (rank * kWarps + range) * len;
+  float x[4];
+  uint64_t w[4], sum = 0;
+  const auto step = [&](int t) {
+    Q::get(*reinterpret_cast<const typename Q::Vec *>(data + range * len + t * kTile + 4 * lane), x);
+    sum = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (at >= from && at < from + w[k]) {
-        finish(a, row, base + t * kTile + 4 * lane + k, x[k], total, r, table);
-        return;
+    for (int h = 0; h < 2; ++h) {
+      Weights v;
+      weights(x[2 * h], x[2 * h + 1], r, table, v);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = 2 * h + i;
+        w[k] = v.d[i] < kCut && v.w[i] >= r.least && composite(x[k], base + t * kTile + 4 * lane + k) >= threshold ? v.w[i] : 0;
+        sum += w[k];
       }
-      from += w[k];
     }
-    return;
+  };
+  // the sums of all steps, a warp a step, then within the one that has it
+  int t = warp;
+#pragma unroll 1
+  for (int n = warp; n < tiles; n += kWarps) {
+    t = n;
+    step(t);
+    const uint64_t all = warp_total(sum);
+    if (lane == 0) tile_sum[t] = all;
+  }
+  __syncthreads();
+  const int chosen = reached(tile_sum, tiles);
+  if (chosen % kWarps != warp) return;
+  if (chosen != t) step(chosen);   // the last step's are still there
+  uint64_t upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += up;
+  }
+  uint64_t from = reach + upto - sum;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (at >= from && at < from + w[k]) {
+      finish(a, row, base + chosen * kTile + 4 * lane + k, x[k], total, r, table);
+      return;
+    }
+    from += w[k];
   }
 }
 
@@ -706,20 +712,64 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       f(t, x);
     }
   };
-  // the warp's kept weights
-  const auto kept_sums = [&](const Row &q, uint64_t threshold) {
+  // The sum of f(x, w, d) over the warp's elements with near(x, place).  Steps of a warp hold a few
+  // of them, so a lane marks its own of eight steps and then takes them two at a time: as many
+  // weights as the lane with the most has, not as many as there are elements.
+  const auto sum_of_some = [&](auto near, auto f) {
     uint64_t sum = 0;
-    each_tile([&](int t, const float (&x)[4]) {
+#pragma unroll 1
+    for (int t0 = 0; t0 < len; t0 += 8 * kTile) {
+      uint32_t mask = 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int j = 0; j < 8; ++j) {
+        const int t = t0 + j * kTile;
+        if (t >= len) break;
+        float x[4];
+        Q::get(*reinterpret_cast<const Vec *>(own + t + 4 * lane), x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mask |= static_cast<uint32_t>(near(x[k], t + 4 * lane + k)) << (4 * j + k);
+      }
+#pragma unroll 1
+      while (__any_sync(0xffffffffu, mask != 0)) {
+        float x[2];
+        bool here[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int b = __ffs(mask) - 1;
+          here[i] = b >= 0;
+          x[i] = Q::one(own[t0 + (max(b, 0) >> 2) * kTile + 4 * lane + (b & 3)]);
+          mask &= mask - 1;
+        }
         Weights v;
-        weights(x[2 * h], x[2 * h + 1], q, table, v);
+        weights(x[0], x[1], local, table, v);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (v.d[i] < kCut && v.w[i] >= q.least && (!(kTopK || kTopP) || threshold == 0 || composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i) >= threshold)) sum += v.w[i];
+          if (here[i] && v.d[i] < kCut) sum += f(x[i], v.w[i], v.d[i]);
       }
-    });
+    }
     return warp_total(sum);
+  };
+  // the warp's kept weights
+  const auto kept_sums = [&](uint64_t threshold) {
+    const auto kept = [&](uint64_t w) { return w >= local.least ? w : 0; };
+    if (!(kTopK || kTopP) || threshold == 0) {
+      uint64_t sum = 0;
+      each_tile([&](int, const float (&x)[4]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          Weights v;
+          weights(x[2 * h], x[2 * h + 1], local, table, v);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (v.d[i] < kCut) sum += kept(v.w[i]);
+        }
+      });
+      return warp_total(sum);
+    }
+    const float least_x = radix_key_value(static_cast<uint32_t>(threshold >> kIndexBits));
+    const int last = (1 << kIndexBits) - 1 - static_cast<int>(threshold & ((1u << kIndexBits) - 1)) - begin;   // of its equals
+    return sum_of_some([&](float x, int place) { return x > least_x || (x == least_x && place <= last); },
+                       [&](float, uint64_t w, uint32_t) { return kept(w); });
   };
   const uint64_t f_u = u > 0.0f ? (u < 1.0f ? static_cast<uint64_t>(u * 0x1p64f) : ~0ull) : 0ull;
   uint64_t threshold = 0;   // composite of the last kept element
@@ -798,8 +848,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     for (int round = 0; round < 2; ++round) {
       from_top = !mass && round == 0;
       uint64_t above = 0, kept = 0;
-      const bool by_weight = mass && local.least > 1;   // min-p: what is kept above is summed element by element
-      if (!by_weight) {   // what this CTA has above: from its histogram
+      {   // what this CTA has above: from its histogram
         if (round == 0) {
 #pragma unroll
           for (int k = 0; k < kYBins / kThreads; ++k) {
@@ -816,13 +865,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         kept = above;
       }
+      const int32_t at_border = round == 0 ? border : border * kFine + fine;
       n = 0;
       // the border's bin as a range of logits less ref, a little wide: most steps of a warp hold none of it
       const float p_low = __uint_as_float(r.whole_bits - static_cast<uint32_t>(2 * border - 62)) - kMagic - 0x1p-6f;
       const float p_high = __uint_as_float(r.whole_bits - static_cast<uint32_t>(max(2 * border - 63, 0))) - kMagic + 0x1p-6f;
       const float x_low = p_low / r.c_hi, x_high = from_top ? INFINITY : p_high / r.c_hi;
       each_tile([&](int t, const float (&x)[4]) {
-        bool near = by_weight;
+        bool near = false;
 #pragma unroll
         for (int k = 0; k < 4; ++k) near = near || (x[k] - local.ref >= x_low && x[k] - local.ref <= x_high);
         if (!__any_sync(0xffffffffu, near)) return;
@@ -840,52 +890,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             if (round == 1) code[2 * h + i] = fine_code(minus, t64, d[i], i);
           }
         }
-        const int32_t at_border = round == 0 ? border : border * kFine + fine;
-        uint32_t take = 0, higher = 0;
+        uint32_t take = 0;   // places among those taken: four ballots, a lane's elements side by side
+        int32_t at = n;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          take |= static_cast<uint32_t>(code[k] == at_border) << k;
-          higher |= static_cast<uint32_t>(code[k] < at_border) << k;
+          const bool in = from_top ? code[k] <= at_border : code[k] == at_border;
+          const uint32_t lanes = __ballot_sync(0xffffffffu, in);
+          take |= static_cast<uint32_t>(in) << k;
+          at += __popc(lanes & ((1u << lane) - 1));
+          n += __popc(lanes);
         }
-        if (from_top) take |= higher;
-        if (by_weight && __any_sync(0xffffffffu, higher != 0)) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            Weights v;
-            weights(x[2 * h], x[2 * h + 1], local, table, v);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (higher >> (2 * h + i) & 1) {
-                above += v.w[i];
-                kept += v.w[i] >= local.least ? v.w[i] : 0;
-              }
+        for (int k = 0; k < 4; ++k) {
+          if (take >> k & 1) {
+            if (at < Pub::kSegment) {
+              mine.logit[warp][at] = own[t + 4 * lane + k];
+              mine.place[warp][at] = static_cast<uint16_t>(t + 4 * lane + k);
             }
+            ++at;
           }
-        }
-        if (__any_sync(0xffffffffu, take != 0)) {
-          const int32_t here = __popc(take);
-          int32_t upto = here;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int32_t up = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += up;
-          }
-          int32_t at = n + upto - here;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (take >> k & 1) {
-              if (at < Pub::kSegment) {
-                mine.logit[warp][at] = own[t + 4 * lane + k];
-                mine.place[warp][at] = static_cast<uint16_t>(t + 4 * lane + k);
-              }
-              ++at;
-            }
-          }
-          n += __shfl_sync(0xffffffffu, upto, 31);
         }
       });
+      if (mass && local.least > 1) {   // min-p: of what lies above, what it keeps
+        kept = sum_of_some([&](float x, int) { return x - local.ref >= x_low; },
+                           [&](float x, uint64_t w, uint32_t d) {
+                             int32_t code = exponent_bin(d);
+                             if (round == 1) {
+                               uint64_t minus, lo;
+                               exponents(x, x, local, minus, lo);
+                               code = fine_code(minus, to_64ths(minus), d, 0);
+                             }
+                             return code < at_border && w >= local.least ? w : 0;
+                           });
+      } else {
+        kept = warp_total(kept);
+      }
       above = warp_total(above);
-      kept = warp_total(kept);
       if (lane == 0) {
         warp_above[warp] = above;
         warp_kept[warp] = kept;
@@ -1092,7 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (mass && listed) {
         if (rank == verdict.owner) {
           // this CTA's kept weights exactly (the histogram's may differ in the last units)
-          const uint64_t kept = kept_sums(local, threshold);
+          const uint64_t kept = kept_sums(threshold);
           if (lane == 0) warp_kept[warp] = kept;
           __syncthreads();
           uint64_t exact = 0;
@@ -1134,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
 
   // the kept weights of the row
-  uint64_t sum = kept_sums(local, threshold);
+  uint64_t sum = kept_sums(threshold);
   if (lane == 0) warp_kept[warp] = sum;
   __syncthreads();
   if (warp == 0) {
