@@ -199,7 +199,7 @@ constexpr int kTreeMaxCtas = 160;   // shares of an attention launch, at most
 cudaError_t launch_tree_tables(TreeTablesArgs a, int num_sms, cudaStream_t stream);
 cudaError_t launch_write_kv(const WriteKvArgs &a, int num_sms, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t stream);
-cudaError_t launch_sample(const SampleArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
 cudaError_t launch_tree_accept(const TreeAcceptArgs &a, int num_sms, cudaStream_t stream);
 cudaError_t launch_tree_commit(const TreeCommitArgs &a, cudaStream_t stream);
 // qm: q as [R][Hq][D], box 64 x heads per key/value head x tokens of a row block; km, vm:

@@ -23,6 +23,7 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "idx_device.cuh"
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const auto kept = [&](uint64_t w) { return w >= local.least ? w : 0; };
     if (!(kTopK || kTopP) || threshold == 0) {
       uint64_t sum = 0;
-      each_tile([&](int, const float (&x)[4]) {
+      each_two_tiles([&](int, const float (&x)[4]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           Weights v;
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // leading bits of a weight in two words of the histogram, as many as this CTA's elements leave room for
     const int lead = __clz(kWarps * len);
     if (mass) {
-      each_tile([&](int t, const float (&x)[4]) {
+      each_two_tiles([&](int t, const float (&x)[4]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           Weights v;
@@ -868,8 +869,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const int32_t at_border = round == 0 ? border : border * kFine + fine;
       n = 0;
       // the border's bin as a range of logits less ref, a little wide: most steps of a warp hold none of it
-      const float p_low = __uint_as_float(r.whole_bits - static_cast<uint32_t>(2 * border - 62)) - kMagic - 0x1p-6f;
-      const float p_high = __uint_as_float(r.whole_bits - static_cast<uint32_t>(max(2 * border - 63, 0))) - kMagic + 0x1p-6f;
+      const float p_low = __uint_as_float(r.whole_bits - static_cast<uint32_t>(2 * border - 62)) - kMagic - 0x1.2p-7f;
+      const float p_high = __uint_as_float(r.whole_bits - static_cast<uint32_t>(max(2 * border - 63, 0))) - kMagic + 0x1.2p-7f;
       const float x_low = p_low / r.c_hi, x_high = from_top ? INFINITY : p_high / r.c_hi;
       each_tile([&](int t, const float (&x)[4]) {
         bool near = false;
@@ -1195,50 +1196,84 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     pick<T>(a, row, data, rank, warp_kept, reach, at, threshold, total, r, table, tile_sum);
 }
 
+// Clusters of 1, 2, 4 and 8 CTAs that run at a time: two CTAs to an SM, and one.
+struct Room {
+  int clusters[2][4];
+};
 template <typename T, bool kTopK, bool kTopP>
-cudaError_t launch(SampleArgs a, int num_sms, cudaStream_t stream) {
+cudaError_t launch(SampleArgs a, cudaStream_t stream) {
   constexpr bool kList = kTopK || kTopP;
   constexpr int kFixed = static_cast<int>(fixed_smem<T, kList>());
-  constexpr int kMost = kFixed + IDX_MAX_VOCAB / kCtas * static_cast<int>(sizeof(T));
   constexpr int kHalf = 112 * 1024 - static_cast<int>(sizeof(Shared<T, kList>)) - 11 * 1024;   // dynamic shared memory with two CTAs to an SM
+  constexpr int kAlone = 120 * 1024;                                                           // that leaves room for one
+  constexpr int kMost = std::max(kAlone, kFixed + IDX_MAX_VOCAB / kCtas * static_cast<int>(sizeof(T)));
   static std::mutex mu;
   static bool done[128];
-  cudaError_t e = once_per_device(mu, done, [] {
-    return cudaFuncSetAttribute(sample_kernel<T, kTopK, kTopP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  static Room rooms[128];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once_per_device(mu, done, [dev] {
+    cudaError_t got = cudaFuncSetAttribute(sample_kernel<T, kTopK, kTopP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    for (int alone = 0; alone < 2; ++alone) {
+      for (int k = 0; k < 4 && got == cudaSuccess; ++k) {
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 1u << k;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(1u << k);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = static_cast<size_t>(alone ? kAlone : kHalf);
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        got = cudaOccupancyMaxActiveClusters(&rooms[dev].clusters[alone][k], sample_kernel<T, kTopK, kTopP>, &cfg);
+      }
+    }
+    return got;
   });
   if (e != cudaSuccess) return e;
-  // CTAs of a row: by the cycles that all rows take, at a CTA's 15,000 and one a logit, two CTAs to
-  // an SM (64 x 128,000 bf16: four 22.9 us, eight 27.7; 8 x 151,552: eight).
-  const auto len_of = [&](int ctas) { return (a.p.V + ctas * kWarps * kTile - 1) / (ctas * kWarps * kTile) * kTile; };
+
+  // CTAs of a row, and whether an SM has one or two of them: by the cycles that all rows take in
+  // waves of the clusters that fit.  A CTA takes about 15,000 and one a logit beside another one,
+  // seven tenths of that alone (64 x 128,000 bf16: four in pairs 21.7 us, eight 27.7; 8 x 151,552 fp32:
+  // eight alone 14.9 us, in pairs, which the hardware takes where they fit, 16.9).
   int64_t best = 0;
+  int smem = 0;
   a.ctas = 0;
-  for (int ctas = kCtas; ctas > 0; ctas /= 2) {
-    const int len = len_of(ctas);
-    if (ctas < kCtas && (len > 2 * kWarps * kTile || kFixed + kWarps * len * static_cast<int>(sizeof(T)) > kHalf)) break;
-    const int64_t slots = 2 * static_cast<int64_t>(num_sms) * 19 / 20, waves = (static_cast<int64_t>(a.p.R) * ctas + slots - 1) / slots;
-    const int64_t cycles = waves * (15000 + a.p.V / ctas);
-    if (a.ctas == 0 || cycles < best) {
-      best = cycles;
-      a.ctas = ctas;
-      a.warp_len = len;
+  for (int k = 3; k >= 0; --k) {
+    const int ctas = 1 << k, len = (a.p.V + ctas * kWarps * kTile - 1) / (ctas * kWarps * kTile) * kTile;
+    const int need = kFixed + kWarps * len * static_cast<int>(sizeof(T));
+    if (len > 2 * kWarps * kTile || need > kMost) break;
+    for (int alone = 0; alone < 2; ++alone) {
+      const int64_t fit = rooms[dev].clusters[alone][k];
+      if (fit < 1 || (alone == 0 && need > kHalf)) continue;
+      const int64_t cycles = (a.p.R + fit - 1) / fit * (15000 + a.p.V / ctas) * (alone ? 7 : 10);
+      if (a.ctas == 0 || cycles < best) {
+        best = cycles;
+        a.ctas = ctas;
+        a.warp_len = len;
+        smem = alone ? std::max(need, kAlone) : need;
+      }
     }
   }
+  if (a.ctas == 0) return cudaErrorInvalidConfiguration;
   return launch_early(sample_kernel<T, kTopK, kTopP>, static_cast<unsigned>(a.p.R) * static_cast<unsigned>(a.ctas), kThreads,
-                      kFixed + static_cast<size_t>(kWarps) * a.warp_len * sizeof(T), static_cast<unsigned>(a.ctas), stream, a);
+                      static_cast<size_t>(smem), static_cast<unsigned>(a.ctas), stream, a);
 }
 
 template <typename T>
-cudaError_t launch(const SampleArgs &a, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const SampleArgs &a, cudaStream_t stream) {
   constexpr int kSpan = kCtas * kWarps * kTile;
   static_assert(IDX_MAX_VOCAB % kSpan == 0 && IDX_MAX_VOCAB / kRanges / kTile <= 2 * kWarps, "whole steps of every warp");
-  if (a.p.top_k != nullptr) return a.p.top_p != nullptr ? launch<T, true, true>(a, num_sms, stream) : launch<T, true, false>(a, num_sms, stream);
-  return a.p.top_p != nullptr ? launch<T, false, true>(a, num_sms, stream) : launch<T, false, false>(a, num_sms, stream);
+  if (a.p.top_k != nullptr) return a.p.top_p != nullptr ? launch<T, true, true>(a, stream) : launch<T, true, false>(a, stream);
+  return a.p.top_p != nullptr ? launch<T, false, true>(a, stream) : launch<T, false, false>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_sample(const SampleArgs &a, int num_sms, cudaStream_t stream) {
-  return a.p.logits_dtype == IDX_LOGITS_F32 ? launch<float>(a, num_sms, stream) : launch<uint16_t>(a, num_sms, stream);
+cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream) {
+  return a.p.logits_dtype == IDX_LOGITS_F32 ? launch<float>(a, stream) : launch<uint16_t>(a, stream);
 }
 
 }  // namespace idx

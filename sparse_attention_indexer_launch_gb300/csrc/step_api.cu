@@ -102,14 +102,14 @@ idx_status idx_sample(const idx_sample_args *args, int32_t *token, float *logpro
   idx_status st = check_sample(args, token, logprob);
   if (st != IDX_OK) return st;
   int sms = 0;
-  st = idx::device_sms(&sms);
+  st = idx::device_sms(&sms);   // the device check
   if (st != IDX_OK) return st;
   idx::SampleArgs a{};
   a.p = *args;
   a.token = token;
   a.logprob = logprob;
   a.vec = args->ld % 4 == 0 && aligned(args->logits, args->logits_dtype == IDX_LOGITS_F32 ? 16 : 8);
-  return cuda_ok(idx::launch_sample(a, sms, static_cast<cudaStream_t>(stream)));
+  return cuda_ok(idx::launch_sample(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t idx_tree_accept_state_size(void) { return kStatusBytes; }
