@@ -714,32 +714,38 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
   };
   // The sum of f(x, w, d) over the warp's elements with near(x, place).  Steps of a warp hold a few
-  // of them, so a lane marks its own of eight steps and then takes them two at a time: as many
+  // of them, so a lane marks its own of 16 steps and then takes them two at a time: as many
   // weights as the lane with the most has, not as many as there are elements.
   const auto sum_of_some = [&](auto near, auto f) {
     uint64_t sum = 0;
 #pragma unroll 1
-    for (int t0 = 0; t0 < len; t0 += 8 * kTile) {
-      uint32_t mask = 0;
+    for (int t0 = 0; t0 < len; t0 += 16 * kTile) {
+      uint32_t mask[2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int t = t0 + j * kTile;
-        if (t >= len) break;
-        float x[4];
-        Q::get(*reinterpret_cast<const Vec *>(own + t + 4 * lane), x);
+      for (int half = 0; half < 2; ++half) {
+        mask[half] = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mask |= static_cast<uint32_t>(near(x[k], t + 4 * lane + k)) << (4 * j + k);
+        for (int j = 0; j < 8; ++j) {
+          const int t = t0 + (8 * half + j) * kTile;
+          if (t >= len) break;
+          float x[4];
+          Q::get(*reinterpret_cast<const Vec *>(own + t + 4 * lane), x);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mask[half] |= static_cast<uint32_t>(near(x[k], t + 4 * lane + k)) << (4 * j + k);
+        }
       }
 #pragma unroll 1
-      while (__any_sync(0xffffffffu, mask != 0)) {
+      while (__any_sync(0xffffffffu, (mask[0] | mask[1]) != 0)) {
         float x[2];
         bool here[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int b = __ffs(mask) - 1;
-          here[i] = b >= 0;
-          x[i] = Q::one(own[t0 + (max(b, 0) >> 2) * kTile + 4 * lane + (b & 3)]);
-          mask &= mask - 1;
+          here[i] = (mask[0] | mask[1]) != 0;
+          const bool second = mask[0] == 0;
+          const int b = max(__ffs(second ? mask[1] : mask[0]) - 1, 0);
+          x[i] = Q::one(own[t0 + (b >> 2) * kTile + 4 * lane + (b & 3) + (second && here[i] ? 8 * kTile : 0)]);
+          if (second) mask[1] &= mask[1] - 1;
+          mask[0] &= mask[0] - 1;
         }
         Weights v;
         weights(x[0], x[1], local, table, v);
@@ -771,6 +777,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const int last = (1 << kIndexBits) - 1 - static_cast<int>(threshold & ((1u << kIndexBits) - 1)) - begin;   // of its equals
     return sum_of_some([&](float x, int place) { return x > least_x || (x == least_x && place <= last); },
                        [&](float, uint64_t w, uint32_t) { return kept(w); });
+  };
+  // Those of the elements above a bin of exponents, or above part `fine` of it.
+  const auto low_edge = [&](int32_t border) {   // less ref, a little lower
+    return (__uint_as_float(local.whole_bits - static_cast<uint32_t>(2 * border - 62)) - kMagic - 0x1.2p-7f) / local.c_hi;
+  };
+  const auto sum_above = [&](int32_t border, int32_t fine) {
+    const float least_x = low_edge(border);
+    return sum_of_some([&](float x, int) { return x - local.ref >= least_x; },
+                       [&](float x, uint64_t w, uint32_t d) {
+                         int32_t code = exponent_bin(d), at = border;
+                         if (fine >= 0) {
+                           uint64_t minus, lo;
+                           exponents(x, x, local, minus, lo);
+                           code = fine_code(minus, to_64ths(minus), d, 0);
+                           at = border * kFine + fine;
+                         }
+                         return code < at && w >= local.least ? w : 0;
+                       });
   };
   const uint64_t f_u = u > 0.0f ? (u < 1.0f ? static_cast<uint64_t>(u * 0x1p64f) : ~0ull) : 0ull;
   uint64_t threshold = 0;   // composite of the last kept element
@@ -845,7 +869,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // bin, or of its part `fine`; in the first round for top-k all from the top.
     int32_t fine = -1, n = 0;
     bool listed = false, from_top = false;
+    int32_t candidates = 0;   // of this warp
     uint64_t over = 0;   // what lies above the candidates in all CTAs
+    ushort4 counts{};    // candidates of warps 4 * lane to 4 * lane + 3
     for (int round = 0; round < 2; ++round) {
       from_top = !mass && round == 0;
       uint64_t above = 0, kept = 0;
@@ -869,9 +895,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const int32_t at_border = round == 0 ? border : border * kFine + fine;
       n = 0;
       // the border's bin as a range of logits less ref, a little wide: most steps of a warp hold none of it
-      const float p_low = __uint_as_float(r.whole_bits - static_cast<uint32_t>(2 * border - 62)) - kMagic - 0x1.2p-7f;
       const float p_high = __uint_as_float(r.whole_bits - static_cast<uint32_t>(max(2 * border - 63, 0))) - kMagic + 0x1.2p-7f;
-      const float x_low = p_low / r.c_hi, x_high = from_top ? INFINITY : p_high / r.c_hi;
+      const float x_low = low_edge(border), x_high = from_top ? INFINITY : p_high / r.c_hi;
       each_tile([&](int t, const float (&x)[4]) {
         bool near = false;
 #pragma unroll
@@ -912,20 +937,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           }
         }
       });
-      if (mass && local.least > 1) {   // min-p: of what lies above, what it keeps
-        kept = sum_of_some([&](float x, int) { return x - local.ref >= x_low; },
-                           [&](float x, uint64_t w, uint32_t d) {
-                             int32_t code = exponent_bin(d);
-                             if (round == 1) {
-                               uint64_t minus, lo;
-                               exponents(x, x, local, minus, lo);
-                               code = fine_code(minus, to_64ths(minus), d, 0);
-                             }
-                             return code < at_border && w >= local.least ? w : 0;
-                           });
-      } else {
-        kept = warp_total(kept);
-      }
+      if (mass && local.least > 1) kept = sum_above(border, fine);   // min-p: of what lies above, what it keeps
+      else kept = warp_total(kept);
+      candidates = n;
       above = warp_total(above);
       if (lane == 0) {
         warp_above[warp] = above;
@@ -946,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
       // the list's length (every warp by itself), and what lies above it
       static_assert(kRanges == 128, "four counts a lane");
-      const ushort4 counts = reinterpret_cast<const ushort4 *>(mine.count)[lane];
+      counts = reinterpret_cast<const ushort4 *>(mine.count)[lane];
       n = __reduce_add_sync(0xffffffffu, counts.x + counts.y + counts.z + counts.w);
       const bool fits = __all_sync(0xffffffffu, max(max(counts.x, counts.y), max(counts.z, counts.w)) <= Pub::kSegment);
       over = 0;
@@ -986,11 +1000,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // the list: gathered and searched by the first CTA
     Verdict verdict{0, 0, 0, -1};
     if (listed && rank == 0) {
-      {
-        const Sums all = exclusive_sum(tid < kRanges ? mine.count[tid] : 0, s.warp_sum);
-        if (tid <= kRanges) list_at[tid] = static_cast<int32_t>(all.before);
-        __syncthreads();
+      if (warp == 0) {
+        const int32_t four = counts.x + counts.y + counts.z + counts.w;
+        int32_t at = four;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int32_t up = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += up;
+        }
+        at -= four;
+        list_at[4 * lane] = at;
+        list_at[4 * lane + 1] = at += counts.x;
+        list_at[4 * lane + 2] = at += counts.y;
+        list_at[4 * lane + 3] = at += counts.z;
+        if (lane == 31) list_at[kRanges] = at + counts.w;
       }
+      __syncthreads();
       for (int i = tid; i < n; i += kThreads) {
         int w = 0;
 #pragma unroll
@@ -1039,7 +1064,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         bool keep = here && part_of == 0 && among(mine_c);
         if (!mass) keep = keep && over + higher_n < want;
         if (mass || (kTopP && from_top && top_p < 1.0f)) {
-          const uint64_t all = exclusive_sum(keep ? mine_w : 0, s.warp_sum).all;
+          const uint64_t some = warp_total(keep ? mine_w : 0);
+          if (lane == 0) s.warp_sum[warp] = some;
+          __syncthreads();
+          const uint64_t all = warps_total(s.warp_sum);
           __syncthreads();
           if (mass) found = over < want && want <= over + all;
           keep = keep && (mass ? over + higher < want : higher < ceil_product(top_p, all));
@@ -1126,14 +1154,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       return;
     }
     if (listed) {
-      cluster.sync();
+      // While the first CTA searches, the others sum what lies above the border in each of their
+      // warps, for the one in which the token will be.
+      const bool early = a.alone && mass && rank != 0;
+      cluster.barrier_arrive();
+      if (early && local.least == 1) {
+        const uint64_t above = sum_above(border, fine);
+        if (lane == 0) warp_kept[warp] = above;
+      }
+      cluster.barrier_wait();
       verdict = mine.verdict;
       threshold = verdict.threshold;
       listed = verdict.owner >= 0;
       if (mass && listed) {
         if (rank == verdict.owner) {
           // this CTA's kept weights exactly (the histogram's may differ in the last units)
-          const uint64_t kept = kept_sums(threshold);
+          uint64_t kept = 0;
+          if (early) {
+            for (int i = lane; i < candidates; i += 32) {
+              const float x = Q::one(mine.logit[warp][i]);
+              if (composite(x, begin + mine.place[warp][i]) < threshold) continue;
+              const uint64_t w = weight(x, r, table);
+              if (w >= local.least) kept += w;
+            }
+            kept = warp_total(kept) + warp_kept[warp];
+            __syncwarp();
+          } else {
+            kept = kept_sums(threshold);
+          }
           if (lane == 0) warp_kept[warp] = kept;
           __syncthreads();
           uint64_t exact = 0;
@@ -1253,6 +1301,7 @@ cudaError_t launch(SampleArgs a, cudaStream_t stream) {
         best = cycles;
         a.ctas = ctas;
         a.warp_len = len;
+        a.alone = alone;
         smem = alone ? std::max(need, kAlone) : need;
       }
     }
