@@ -1,17 +1,18 @@
 // A token of every row of logits: temperature, top-k, top-p and min-p, drawn with given
 // random numbers.
 //
-// A cluster of up to eight CTAs holds one row in shared memory: the logits are read once, and what
-// the CTAs need of each other (maxima, histograms, sums, candidates) they read from each
-// other's shared memory between cluster barriers.  Every CTA then finds the same thresholds
-// from the same numbers; parameters come from the first CTA's copy, so that no barrier
-// depends on memory that could change in between.
+// A cluster of up to eight CTAs holds one row in shared memory: the logits are read once.  What
+// the CTAs need of each other (maxima, sums, histograms by octave, counts) each writes into
+// all of them before a cluster barrier, so that behind it nobody waits for another SM; only
+// one octave's bins and the candidates are read from afar.  Every CTA then finds the same
+// border from the same numbers; parameters come from the first CTA's copy, so that no
+// barrier depends on memory that could change in between.
 //
 // A token may not depend on how sums are rounded, and a border (u Z between two tokens' sums,
 // p Z between two masses) lies within 2^-24 of some sum in a percent of the rows.  So weights
 // are integers, 2^44 exp(l / T) over the power of two at or above the largest exp(l / T), to
-// about 2^-38 of itself or one unit; their sums are
-// exact in 64 bits whatever the order, and the comparisons with p Z and u Z exact in 128.
+// about 2^-38 of itself or one unit; their sums are exact in 64 bits whatever the order, and
+// the comparisons with p Z and u Z exact in 128.
 //
 // Thresholds: the kept tokens are a prefix of the order (logit descending, index ascending),
 // so one number is enough, the composite (key, ~index) of the last kept one.  A first pass
@@ -19,7 +20,16 @@
 // of the weights for top-p; the elements of the bin that holds the border (for top-k those
 // above as well, where they are few) go into a list that the first CTA gathers and searches.  A
 // bin with too many is cut into 256 finer ones first; where even those hold too many (equal
-// logits), a radix descent runs over the whole row.
+// logits), a radix descent runs over the whole row.  (Descents over the whole row for every
+// border took 953 us for 256 rows of 151,552 fp32 logits with mixed filters; this 211.)
+//
+// What bounds it: reading those rows would take 22.9 us at the measured copy bandwidth.  Their
+// weights to 2^-38 are some 30 instructions a logit, 27 us if every slot were used.  The rest is the
+// chain of a row's steps, 25 to 30 us with two rows to an SM, in which warps wait for the slowest
+// one of the cluster (issue slots 42% busy, a third of the stalls at barriers).  A single row is that
+// chain alone: with top-p of 151,552 logits some 45,000 cycles, of which reading and the largest
+// logit are 7,000, weights and histograms 12,000, border and candidates 9,000, the list 8,000 and the
+// token among the kept ones 9,000 (less where the first CTA's neighbours have summed meanwhile).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -399,7 +409,8 @@ __device__ __noinline__ void push_octaves(const uint32_t *hist, float low, float
   for (int o = warp; o < kOctaveBins; o += kWarps) {
     float v = static_cast<float>(__reduce_add_sync(0xffffffffu, hist[o * 32 + lane]));
     if (low != 0.0f) v = fmaf(static_cast<float>(__reduce_add_sync(0xffffffffu, hist[kYBins + o * 32 + lane])), low, v);
-    if (lane < cg::this_cluster().num_blocks()) cg::this_cluster().map_shared_rank(octave, lane)[cg::this_cluster().block_rank()][o] = v;
+    const cg::cluster_group cluster = cg::this_cluster();
+    if (lane < cluster.num_blocks()) cluster.map_shared_rank(octave, lane)[cluster.block_rank()][o] = v;
   }
 }
 
@@ -433,7 +444,8 @@ struct Exponent {
   int32_t bin;
   float all;
 };
-__device__ __noinline__ Exponent find_exponent(float low, const uint32_t *hist, const float (*octave)[kOctaveBins], float *sum, float want) {
+__device__ __noinline__ Exponent find_exponent(float low, const uint32_t *hist, const float (*octave)[kOctaveBins], float *sum,
+                                               float want) {
   static_assert(kOctaveBins > 32 && kOctaveBins <= 64, "one or two octaves a lane");
   const int tid = threadIdx.x, lane = tid & 31, ctas = static_cast<int>(cg::this_cluster().num_blocks());
   const auto scaled = [&](float v, int o) { return low != 0.0f ? v * __uint_as_float(static_cast<uint32_t>(127 - o) << 23) : v; };
@@ -482,7 +494,8 @@ __device__ __noinline__ uint64_t descend_list(bool mass, const uint64_t *list, i
   for (int i = threadIdx.x; i < n; i += kThreads) diff |= list[i] ^ any;
   const uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(diff >> 32));
   const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(diff));
-  if ((threadIdx.x & 31) == 0 && (hi | lo) != 0) atomicOr(reinterpret_cast<unsigned long long *>(&s.composite), static_cast<unsigned long long>(hi) << 32 | lo);
+  if ((threadIdx.x & 31) == 0 && (hi | lo) != 0)
+    atomicOr(reinterpret_cast<unsigned long long *>(&s.composite), static_cast<unsigned long long>(hi) << 32 | lo);
   __syncthreads();
   int shift = 64 - __clzll(static_cast<long long>(s.composite));
   uint64_t prefix = any >> shift;
@@ -855,8 +868,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       for (int c = 0; c < kCtas; ++c) z += mine.told[c].all;
       want = ceil_product(top_p, z);
     }
-    const Exponent ex = find_exponent(low_unit, hist, mine.octave, s.bin,
-                                      mass ? static_cast<float>(want) * __uint_as_float(static_cast<uint32_t>(127 + lead - 45) << 23) : static_cast<float>(want));
+    const float want_units = mass ? static_cast<float>(want) * __uint_as_float(static_cast<uint32_t>(127 + lead - 45) << 23) : static_cast<float>(want);
+    const Exponent ex = find_exponent(low_unit, hist, mine.octave, s.bin, want_units);
     const int32_t border = ex.bin;
     if (!mass && ex.all <= static_cast<float>(want)) {   // all that have a weight are kept
       cluster.sync();               // nobody reads the histogram any more
@@ -1252,8 +1265,8 @@ template <typename T, bool kTopK, bool kTopP>
 cudaError_t launch(SampleArgs a, cudaStream_t stream) {
   constexpr bool kList = kTopK || kTopP;
   constexpr int kFixed = static_cast<int>(fixed_smem<T, kList>());
-  constexpr int kHalf = 112 * 1024 - static_cast<int>(sizeof(Shared<T, kList>)) - 11 * 1024;   // dynamic shared memory with two CTAs to an SM
-  constexpr int kAlone = 120 * 1024;                                                           // that leaves room for one
+  // dynamic shared memory with two CTAs to an SM, and that leaves room for one
+  constexpr int kHalf = 112 * 1024 - static_cast<int>(sizeof(Shared<T, kList>)) - 11 * 1024, kAlone = 120 * 1024;
   constexpr int kMost = std::max(kAlone, kFixed + IDX_MAX_VOCAB / kCtas * static_cast<int>(sizeof(T)));
   static std::mutex mu;
   static bool done[128];

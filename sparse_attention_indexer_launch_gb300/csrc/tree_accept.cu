@@ -6,12 +6,16 @@
 // sampled token.  A warp holds a request's tree, two tokens a lane, so a step of the walk is
 // two comparisons and a ballot.  Giving pages back needs a prefix sum over all requests'
 // results: the CTA that finishes last does it, so nobody waits.  A single CTA, of a warp per
-// request, has them in shared memory.
+// request, has them in shared memory.  It is latency from end to end: 2.2 us in a graph for two
+// requests, 6.5 for 1,024 trees (32 CTAs, the counter, then one CTA that sums 1,024 results, a
+// request a thread, with the pages read before it is known to be the last one).  CTAs are as large as
+// the batch, up to 1,024 threads, because a few requests in one of 1,024 were slower.
 //
 // Moving is in place: the a-th accepted token goes from the slot of row path[a] to that of row
 // a, path[a] >= a and ascending.  Row a's slot is read by no later move (path[b] = a only for
 // b <= a), so one group of lanes that takes a head's moves in order, loads ahead of stores,
-// needs no copy.
+// needs no copy.  Four loads a lane in flight: 512 requests of an E4M3 cache 3.7 us in a graph
+// where the bytes take 1.0; 8 requests 2.1, all launch.
 #include <algorithm>
 
 #include "idx_device.cuh"
