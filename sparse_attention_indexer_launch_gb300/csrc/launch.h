@@ -155,7 +155,7 @@ struct NormRopeArgs {
   // set by the launcher
   int32_t heads;                // of a batch: a warp's loads at a time, of one row and kind
   int32_t q_units, k_units;     // batches of a row: of its q heads, its k heads
-  int32_t group_rows, splits;   // rows of a group, CTAs that share it
+  int32_t parts;                // warps that share a row
 };
 
 struct SampleArgs {

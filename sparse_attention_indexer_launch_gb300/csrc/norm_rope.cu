@@ -3,18 +3,19 @@
 //
 // A vector of D values (one head of a row) is a group of D / 8 lanes with eight values each,
 // four pairs that turn together, so that the rotation stays within a lane: two runs of four
-// for halves, one of eight for interleaved pairs.  It is read once and written once.  A CTA
-// takes a group of rows, works their angles out once into shared memory, and its warps take
-// batches of a few heads of one row, first of q, then of k, then of v, each in a loop of its
-// own that keeps the head's weights in registers (one walk over all kinds, with its branches and
-// reloads, took 152 us for the prompts below; loops by kind with the next batch's copies on
-// their way 114).  A warp takes every `step`-th batch: runs of consecutive batches left warps with
-// uneven ends and were slower.
+// for halves, one of eight for interleaved pairs.  It is read once and written once.  A warp
+// takes a row, or a part of one where there are few: its lanes keep the cosines and sines of
+// their four pairs in registers, and go through batches of a few heads, first of q, then of
+// k, then of v, with the next batch's copies on their way to a lane's own place in shared
+// memory.  Warps share nothing, so no barrier holds them up; two values ride in an instruction.
 //
-// What bounds it: 16,209 prompt rows of 64 + 2 x 8 heads of 128 into an E4M3 cache take 113.6 us,
-// 5.6 TB/s or 82% of the measured copy bandwidth, with 60% of the issue slots busy, so everything is
-// done for two values at a time.  8,855 rows of 16 + 2 x 16 heads turned by three axes, bf16: 42.9 us, 75%.
-// A few rows: 3.4 us in a graph, which is launch, one read and one write.
+// What bounds it: memory.  16,209 rows of 64 + 2 x 8 heads of 128 into an E4M3 cache take 103 us,
+// 6.1 TB/s or 91% of the measured copy bandwidth; 8,855 rows of 16 + 2 x 16 heads turned by three axes,
+// bf16, 37.3 us, 86%; 40,000 rows reach 98 to 100%, so what is missing is start and end.  28 warps to
+// an SM with one head at a time: 24 with 80 registers took 115 us and 40.7, 32 with 64 spill (127; one
+// head at a time 103.5).  Groups of rows to a CTA, angles in shared memory behind a barrier, took 113
+// and 42.2, two heads at a time 107 and 37.7.  A few rows: 2.7 us in a graph, which is launch, one read
+// and one write.
 //
 // Angles: positions reach 2^31, where pos * inv_freq in fp32 is off by whole turns.  The
 // frequency in turns, inv_freq / (2 pi), is a fixed-point fraction of 64 bits, and a
@@ -28,10 +29,9 @@
 namespace idx {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVectors = 4;     // heads of a lane in a batch
-constexpr int kMostRows = 8;    // of a CTA's group
 
 // inv_freq / (2 pi) in units of 2^-64 turn, modulo one turn: the 24-bit significand times
 // 2^64 / (2 pi), shifted by the exponent.
@@ -220,50 +220,68 @@ __device__ __noinline__ Rescued rescue(uint4 raw) {
   return r;
 }
 
-// x of kAtATime heads to their normed values but for weights and biases.  The whole warp calls.
-template <int D, bool kInterleaved, bool kMean, int kAtATime>
-__device__ __forceinline__ void normed(Pairs (&x)[kAtATime], const uint4 (&raw)[kAtATime], float eps, float (&inv)[kAtATime]) {
-  float s[kAtATime];
-  bool past = false;
-#pragma unroll
-  for (int k = 0; k < kAtATime; ++k) {
-    s[k] = spread<D, kMean>(x[k]);
-    past = past || !(s[k] <= 3.402823466e38f);
-    inv[k] = rsqrt_normal(s[k] + eps);
-  }
+// x to its normed values but for weights and biases and the factor `inv`.  The whole warp calls.
+template <int D, bool kInterleaved, bool kMean>
+__device__ __forceinline__ void normed(Pairs &x, const uint4 &raw, float eps, float &inv) {
+  const float s = spread<D, kMean>(x);
+  const bool past = !(s <= 3.402823466e38f);
+  inv = rsqrt_normal(s + eps);
   if (__any_sync(0xffffffffu, past)) {
-#pragma unroll
-    for (int k = 0; k < kAtATime; ++k) {
-      const Rescued r = rescue<D, kInterleaved, kMean>(raw[k]);
-      if (!(s[k] <= 3.402823466e38f)) {
-        x[k] = r.x;
-        inv[k] = r.inv;
-      }
+    const Rescued r = rescue<D, kInterleaved, kMean>(raw);
+    if (past) {
+      x = r.x;
+      inv = r.inv;
     }
   }
 }
 
-// Cosines, sines and negated sines of a row's frequencies, each in a run.
-template <int D>
+// Cosines, sines and negated sines of a lane's four pairs, two in a word.
 struct Turns {
-  float c[D / 2], s[D / 2], m[D / 2];
+  uint64_t c[2], s[2], m[2];
 };
-// A head's normed values, y, turned, times inv.
+// Lanes of a warp with the same pairs, one in each head, work out a part of them each.
 template <int D, bool kInterleaved>
-__device__ __forceinline__ Pairs turned(const Pairs &y, const Turns<D> &t, const Place &at) {
+__device__ __forceinline__ Turns turns_of(const idx_norm_rope_args &p, int64_t row, const Place &at) {
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+  const int lane = threadIdx.x % kLanes, sub = threadIdx.x % 32 / kLanes;
+  float2 mine[4 / kAtOnce];
+#pragma unroll
+  for (int j = 0; j < 4 / kAtOnce; ++j) {
+    mine[j] = make_float2(1.0f, 0.0f);
+    if (at.turns) {
+      const int f = (kInterleaved ? at.a / 2 : at.a) + j * kAtOnce + sub;
+      mine[j] = cos_sin(p.pos[p.axis[f] * p.pos_stride + row], p.inv_freq[f]);
+    }
+  }
+  float c[4], s[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int from = k % kAtOnce * kLanes + lane;
+    c[k] = __shfl_sync(0xffffffffu, mine[k / kAtOnce].x, from);
+    s[k] = __shfl_sync(0xffffffffu, mine[k / kAtOnce].y, from);
+  }
+  Turns t;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    t.c[h] = pack2(c[2 * h], c[2 * h + 1]);
+    t.s[h] = pack2(s[2 * h], s[2 * h + 1]);
+    t.m[h] = pack2(-s[2 * h], -s[2 * h + 1]);
+  }
+  return t;
+}
+// A head's normed values, y, turned.
+__device__ __forceinline__ Pairs turned(const Pairs &y, const Turns &t, const Place &at) {
   if (!at.turns) return y;
-  const int f = kInterleaved ? at.a / 2 : at.a;   // four frequencies
-  const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(t.c + f), s = *reinterpret_cast<const ulonglong2 *>(t.s + f),
-                   m = *reinterpret_cast<const ulonglong2 *>(t.m + f);
   Pairs z;
-  z.a[0] = fma2(y.b[0], m.x, mul2(y.a[0], c.x));
-  z.a[1] = fma2(y.b[1], m.y, mul2(y.a[1], c.y));
-  z.b[0] = fma2(y.a[0], s.x, mul2(y.b[0], c.x));
-  z.b[1] = fma2(y.a[1], s.y, mul2(y.b[1], c.y));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    z.a[h] = fma2(y.b[h], t.m[h], mul2(y.a[h], t.c[h]));
+    z.b[h] = fma2(y.a[h], t.s[h], mul2(y.b[h], t.c[h]));
+  }
   return z;
 }
 
-constexpr int ctas_per_sm(bool bias) { return bias ? 2 : 3; }   // 128 or 80 registers a thread
+constexpr int ctas_per_sm(bool bias) { return bias ? 5 : 7; }   // 96 or 72 registers a thread
 
 // A row's place in the cache for keys or values, at head h.
 struct Spot {
@@ -281,212 +299,155 @@ __device__ __forceinline__ Spot spot_of(const NormRopeArgs &a, bool values, bool
   return s;
 }
 
-// A warp's batches of one kind (0 q, 1 k, 2 v) in a group of rows: item i is batch i % units of
-// row i / units, a step from one to the next; and the copies that run one batch ahead.
-template <int D, bool kInterleaved, int kKind>
-struct Walk {
-  static constexpr int kAtOnce = 32 / (D / 8);
-  const NormRopeArgs &a;
-  const int units, heads, step;
-  const uint16_t *const in;   // the group's first row, this lane's first head
-  const int64_t stride;
-  const Place at;
-  int r, u, r_next, u_next;
-
-  __device__ __forceinline__ Walk(const NormRopeArgs &args, int64_t row0, int item, int step_)
-      : a(args), units(kKind == 0 ? args.q_units : args.k_units), heads(kKind == 0 ? args.p.Hq : args.p.Hkv), step(step_),
-        in(static_cast<const uint16_t *>(kKind == 0 ? args.p.q : kKind == 1 ? args.p.k : args.p.v) +
-           row0 * (kKind == 0 ? args.p.q_stride : kKind == 1 ? args.p.k_stride : args.p.v_stride) + sub() * D),
-        stride(kKind == 0 ? args.p.q_stride : kKind == 1 ? args.p.k_stride : args.p.v_stride),
-        at(kKind == 2 ? Place{8 * lane(), 0, false} : place_of<kInterleaved>(lane(), args.p.rot)) {
-    r = r_next = item / units;
-    u = u_next = item % units;
-  }
-  static __device__ __forceinline__ int lane() { return threadIdx.x % (D / 8); }
-  static __device__ __forceinline__ int sub() { return threadIdx.x % 32 / (D / 8); }
-  __device__ __forceinline__ int first() const { return u * a.heads; }
-  // This lane's heads of the batch: 0, kAtOnce, .. below this.
-  __device__ __forceinline__ int mine(int batch) const { return min(heads - batch * a.heads - sub(), a.heads - sub()); }
-  __device__ __forceinline__ void copy_next(uint4 (&to)[kVectors][32]) {
-    const int n = mine(u_next);
-    const uint16_t *const src = in + r_next * stride + u_next * a.heads * D;
+// Copies of batch `item` of a row, counted over all kinds (q's, then k's, then v's; none past the last).
+template <int D, bool kInterleaved>
+__device__ __forceinline__ void copy_item(const NormRopeArgs &a, int64_t row, int item, uint4 (&to)[kVectors][32]) {
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+  const int lane = threadIdx.x % kLanes, sub = threadIdx.x % 32 / kLanes, slot = threadIdx.x % 32;
+  const bool is_q = item < a.q_units, is_v = item >= a.q_units + a.k_units;
+  if (is_v && (a.c.v == nullptr || item >= a.q_units + 2 * a.k_units)) return;
+  const int u = is_q ? item : item - a.q_units - (is_v ? a.k_units : 0), first = u * a.heads;
+  const int n = min((is_q ? a.p.Hq : a.p.Hkv) - first, a.heads) - sub;   // this lane's heads: 0, kAtOnce, .. below this
+  const uint16_t *const src = static_cast<const uint16_t *>(is_q ? a.p.q : is_v ? a.p.v : a.p.k) +
+                              row * (is_q ? a.p.q_stride : is_v ? a.p.v_stride : a.p.k_stride) + (first + sub) * D;
+  const Place at = place_of<kInterleaved>(lane, a.p.rot);
 #pragma unroll
-    for (int k = 0; k < kVectors; ++k)
-      if (k * kAtOnce < n) copy_async<kInterleaved || kKind == 2>(&to[k][threadIdx.x % 32], src + k * kAtOnce * D, at);
-    for (u_next += step; u_next >= units; u_next -= units) ++r_next;
+  for (int k = 0; k < kVectors; ++k) {
+    if (k * kAtOnce >= n) break;
+    if (kInterleaved || !is_v) copy_async<kInterleaved>(&to[k][slot], src + k * kAtOnce * D, at);
+    else copy_async<true>(&to[k][slot], src + k * kAtOnce * D, Place{8 * lane, 0, false});
   }
-  __device__ __forceinline__ void next() {
-    for (u += step; u >= units; u -= units) ++r;
-  }
-};
+}
 
-// Norm and rotation of a kind's items from `item` on.  Returns the first item past them.
-// copied: the first batch's copies are on their way.
+// Norm and rotation of a row's batches of one kind from `item` (over all kinds) on, whose copies to
+// ring[stage] are on their way.  The first batch past them is on its way to the new ring[stage] then.
 template <int D, bool kInterleaved, bool kBias, bool kKeys>
-__device__ __forceinline__ int turn_items(const NormRopeArgs &a, int item, int step, int rows, int64_t row0, const Turns<D> *turns,
-                                          const float *weight, const float *bias, uint4 (*ring)[kVectors][32], bool copied) {
+__device__ __forceinline__ void turn_items(const NormRopeArgs &a, int64_t row, int &item, int step, const Turns &turns, const Place &at,
+                                           uint4 (*ring)[kVectors][32], int &stage) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kStep = kAtOnce * D;
-  constexpr int kPair = kBias ? 1 : 2;   // heads normed at a time, so that one's sums run beside the other's
   const idx_norm_rope_args &p = a.p;
   const int lane = threadIdx.x % kLanes, sub = threadIdx.x % 32 / kLanes, slot = threadIdx.x % 32;
-  const int items = rows * (kKeys ? a.k_units : a.q_units), norm = kKeys ? p.k_norm : p.q_norm;
-  if (item >= items) return item - items;
-  Walk<D, kInterleaved, kKeys ? 1 : 0> walk(a, row0, item, step);
-  const Place &at = walk.at;
-  const Pairs w = by_pairs<kInterleaved>(at, weight);
+  const int begin = kKeys ? a.q_units : 0, end = kKeys ? a.q_units + a.k_units : a.q_units;
+  const int norm = kKeys ? p.k_norm : p.q_norm, heads = kKeys ? p.Hkv : p.Hq;
+  if (item >= end) return;
+  const float *const weight = kKeys ? p.k_weight : p.q_weight, *const bias = kKeys ? p.k_bias : p.q_bias;
+  Pairs w, b;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    w.a[h] = w.b[h] = both(1.0f);
+    b.a[h] = b.b[h] = both(-0.0f);   // adds nothing to any value, a zero's sign included
+  }
+  if (weight != nullptr) w = by_pairs<kInterleaved>(at, weight);
+  if (kBias && bias != nullptr) b = by_pairs<kInterleaved>(at, bias);
   const bool f8 = a.c.kv_dtype == IDX_KV_E4M3;
   uint16_t *const out = static_cast<uint16_t *>(kKeys ? p.k_out : p.q_out);
-  uint16_t *const out0 = out + row0 * (kKeys ? p.k_out_stride : p.q_out_stride) + sub * D;
+  uint16_t *const out0 = out + row * (kKeys ? p.k_out_stride : p.q_out_stride) + sub * D;
+  Spot spot{};
+  if (kKeys && p.slot != nullptr) spot = spot_of(a, false, f8, row, sub);
   // the next batch is on its way while one is worked on; a lane reads what it copied itself
-  int stage = 0;
-  if (copied) {
-    for (walk.u_next += step; walk.u_next >= walk.units; walk.u_next -= walk.units) ++walk.r_next;
-  } else {
-    walk.copy_next(ring[0]);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
 #pragma unroll 1
-  for (; item < items; item += step, stage ^= 1, walk.next()) {
-    if (item + step < items) walk.copy_next(ring[stage ^ 1]);
+  for (; item < end; item += step, stage ^= 1) {
+    copy_item<D, kInterleaved>(a, row, item + step, ring[stage ^ 1]);
     asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 1;" ::: "memory");
-    const int r = walk.r, first = walk.first(), mine = walk.mine(walk.u);
-    uint16_t *const dst = out0 + r * (kKeys ? p.k_out_stride : p.q_out_stride) + first * D;
-    Spot spot{};
-    if (kKeys && p.slot != nullptr) spot = spot_of(a, false, f8, row0 + r, first + sub);
+    const int first = (item - begin) * a.heads, mine = min(heads - first, a.heads) - sub;
+    uint16_t *const dst = out0 + first * D;
+    char *const to = spot.to + first * a.c.head_stride * (f8 ? 1 : 2);
     const int64_t to_step = kAtOnce * a.c.head_stride * (f8 ? 1 : 2);
 #pragma unroll
-    for (int k0 = 0; k0 < kVectors; k0 += kPair) {
-      if (k0 * kAtOnce >= mine + sub) break;   // the warp's lanes together
-      Pairs x[kPair];
-      uint4 v[kPair];
-      float inv[kPair];
-#pragma unroll
-      for (int k = 0; k < kPair; ++k) {
-        v[k] = ring[stage][k0 + k][slot];   // past the last head: whatever is there, and not stored
-        x[k] = unpack<kInterleaved>(v[k]);
-        inv[k] = 1.0f;
-      }
+    for (int k = 0; k < kVectors; ++k) {
+      if (k * kAtOnce >= mine + sub) break;   // the warp's lanes together
+      const uint4 v = ring[stage][k][slot];   // past the last head: whatever is there, and not stored
+      Pairs x = unpack<kInterleaved>(v);
+      float inv = 1.0f;
       if (kBias && norm == IDX_NORM_LAYER) normed<D, kInterleaved, true>(x, v, p.eps, inv);
       else if (norm != IDX_NORM_NONE) normed<D, kInterleaved, false>(x, v, p.eps, inv);
 #pragma unroll
-      for (int k = 0; k < kPair; ++k) {
-        Pairs y;
+      for (int h = 0; h < 2; ++h) {
+        x.a[h] = mul2(x.a[h], both(inv));
+        x.b[h] = mul2(x.b[h], both(inv));
         if constexpr (kBias) {
-          const Pairs b = by_pairs<kInterleaved>(at, bias);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            y.a[h] = fma2(mul2(x[k].a[h], both(inv[k])), w.a[h], b.a[h]);
-            y.b[h] = fma2(mul2(x[k].b[h], both(inv[k])), w.b[h], b.b[h]);
-          }
+          x.a[h] = fma2(x.a[h], w.a[h], b.a[h]);
+          x.b[h] = fma2(x.b[h], w.b[h], b.b[h]);
         } else {
+          x.a[h] = mul2(x.a[h], w.a[h]);
+          x.b[h] = mul2(x.b[h], w.b[h]);
+        }
+      }
+      const Pairs z = turned(x, turns, at);
+      const uint4 packed = pack<kInterleaved>(z);
+      const bool here = k * kAtOnce < mine;
+      if ((!kKeys || out != nullptr) && here) store<kInterleaved>(dst + k * kStep, at, packed);
+      if (!kKeys || spot.to == nullptr) continue;
+      char *const head = to + k * to_step;
+      if (!f8) {
+        if (spot.live && here) store<kInterleaved>(reinterpret_cast<uint16_t *>(head), at, packed);
+        continue;
+      }
+      // eight values in the order of their bytes
+      const float e[8] = {low(z.a[0]), kInterleaved ? low(z.b[0]) : high(z.a[0]), kInterleaved ? high(z.a[0]) : low(z.a[1]),
+                          kInterleaved ? high(z.b[0]) : high(z.a[1]), kInterleaved ? low(z.a[1]) : low(z.b[0]),
+                          kInterleaved ? low(z.b[1]) : high(z.b[0]), kInterleaved ? high(z.a[1]) : low(z.b[1]), high(z.b[1])};
+      float m = 0.0f;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            y.a[h] = mul2(mul2(x[k].a[h], both(inv[k])), w.a[h]);
-            y.b[h] = mul2(mul2(x[k].b[h], both(inv[k])), w.b[h]);
-          }
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(e[j]));
+      uint32_t lo, hi;
+      const float sc = quantize_f32(e, group_max<kLanes>(m), lo, hi);
+      if (spot.live && here) {
+        if (kInterleaved) {
+          *reinterpret_cast<uint2 *>(head + at.a) = make_uint2(lo, hi);
+        } else {
+          *reinterpret_cast<uint32_t *>(head + at.a) = lo;
+          *reinterpret_cast<uint32_t *>(head + at.b) = hi;
         }
-        const Pairs z = turned<D, kInterleaved>(y, turns[r], at);
-        const uint4 packed = pack<kInterleaved>(z);
-        const bool here = (k0 + k) * kAtOnce < mine;
-        if ((!kKeys || out != nullptr) && here) store<kInterleaved>(dst + (k0 + k) * kStep, at, packed);
-        if (!kKeys || spot.to == nullptr) continue;
-        char *const head = spot.to + (k0 + k) * to_step;
-        if (!f8) {
-          if (spot.live && here) store<kInterleaved>(reinterpret_cast<uint16_t *>(head), at, packed);
-          continue;
-        }
-        // eight values in the order of their bytes
-        const float e[8] = {low(z.a[0]), kInterleaved ? low(z.b[0]) : high(z.a[0]), kInterleaved ? high(z.a[0]) : low(z.a[1]),
-                            kInterleaved ? high(z.b[0]) : high(z.a[1]), kInterleaved ? low(z.a[1]) : low(z.b[0]),
-                            kInterleaved ? low(z.b[1]) : high(z.b[0]), kInterleaved ? high(z.a[1]) : low(z.b[1]), high(z.b[1])};
-        float m = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(e[j]));
-        uint32_t lo, hi;
-        const float sc = quantize_f32(e, group_max<kLanes>(m), lo, hi);
-        if (spot.live && here) {
-          if (kInterleaved) {
-            *reinterpret_cast<uint2 *>(head + at.a) = make_uint2(lo, hi);
-          } else {
-            *reinterpret_cast<uint32_t *>(head + at.a) = lo;
-            *reinterpret_cast<uint32_t *>(head + at.b) = hi;
-          }
-          if (lane == 0) spot.scale[(k0 + k) * kAtOnce * kPage] = sc;
-        }
+        if (lane == 0) spot.scale[(first + k * kAtOnce) * kPage] = sc;
       }
     }
   }
-  return item - items;
 }
 
 // kBias: a LayerNorm is among the norms.
 template <int D, bool kInterleaved, bool kBias>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBias)) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
-  __shared__ __align__(16) Turns<D> turns[kMostRows];
   __shared__ uint4 rings[kWarps][2][kVectors][32];
-  __shared__ __align__(16) float weights[2][D], biases[kBias ? 2 : 1][kBias ? D : 4];   // of q and of k
   const idx_norm_rope_args &p = a.p;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid % kLanes, sub = tid % 32 / kLanes, slot = tid % 32;
+  const uint32_t index = blockIdx.x * kWarps + tid / 32;   // R * parts is below 2^31
+  const int64_t row = index / static_cast<uint32_t>(a.parts);
+  const int step = a.parts;
+  int item = static_cast<int>(index % static_cast<uint32_t>(a.parts)), stage = 0;
+  uint4(*const ring)[kVectors][32] = rings[tid / 32];
   grid_dependency_trigger();
   grid_dependency_wait();
-  const int64_t group = blockIdx.x / a.splits;
-  const int part = static_cast<int>(blockIdx.x % a.splits);
-  const int64_t row0 = group * a.group_rows;
-  const int64_t limit = p.rows != nullptr ? min(p.R, static_cast<int64_t>(*p.rows)) : p.R;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(a.group_rows), limit - row0));
-  if (rows <= 0) return;
+  if (row >= p.R || (p.rows != nullptr && row >= *p.rows)) return;
 
   // the warp's first copies, before the angles
-  const int step = a.splits * kWarps;
-  int item = part * kWarps + tid / 32;
-  uint4(*const ring)[kVectors][32] = rings[tid / 32];
-  const int kind = item < rows * a.q_units ? 0 : item < rows * (a.q_units + a.k_units) ? 1 : 2;
-  if (kind == 0) Walk<D, kInterleaved, 0>(a, row0, item, step).copy_next(ring[0]);
-  if (kind == 1) Walk<D, kInterleaved, 1>(a, row0, item - rows * a.q_units, step).copy_next(ring[0]);
+  copy_item<D, kInterleaved>(a, row, item, ring[0]);
   asm volatile("cp.async.commit_group;" ::: "memory");
-
-  const int pairs = p.rot >> 1;
-  for (int i = tid; i < rows * pairs; i += kThreads) {
-    const int r = i / pairs, k = i % pairs;
-    const float2 t = cos_sin(p.pos[p.axis[k] * p.pos_stride + row0 + r], p.inv_freq[k]);
-    turns[r].c[k] = t.x;
-    turns[r].s[k] = t.y;
-    turns[r].m[k] = -t.y;
+  const Place at = place_of<kInterleaved>(lane, p.rot);
+  if (item < a.q_units + a.k_units) {
+    const Turns turns = turns_of<D, kInterleaved>(p, row, at);
+    turn_items<D, kInterleaved, kBias, false>(a, row, item, step, turns, at, ring, stage);
+    turn_items<D, kInterleaved, kBias, true>(a, row, item, step, turns, at, ring, stage);
   }
-  for (int i = tid; i < D; i += kThreads) {
-    weights[0][i] = p.q_weight != nullptr ? p.q_weight[i] : 1.0f;
-    weights[1][i] = p.k_weight != nullptr ? p.k_weight[i] : 1.0f;
-    if constexpr (kBias) {   // -0 adds nothing to any value, a zero's sign included
-      biases[0][i] = p.q_bias != nullptr ? p.q_bias[i] : -0.0f;
-      biases[1][i] = p.k_bias != nullptr ? p.k_bias[i] : -0.0f;
-    }
-  }
-  __syncthreads();
-
-  item = turn_items<D, kInterleaved, kBias, false>(a, item, step, rows, row0, turns, weights[0], biases[0], ring, kind == 0);
-  item = turn_items<D, kInterleaved, kBias, true>(a, item, step, rows, row0, turns, weights[1], biases[kBias ? 1 : 0], ring, kind == 1);
-  if (a.c.v == nullptr || item >= rows * a.k_units) return;
-  Walk<D, kInterleaved, 2> walk(a, row0, item, step);
-  const int lane = tid % kLanes, sub = tid % 32 / kLanes, slot = tid % 32;
+  const int end = a.q_units + 2 * a.k_units;
+  if (a.c.v == nullptr || item >= end) return;
   const bool f8 = a.c.kv_dtype == IDX_KV_E4M3;
+  const Spot spot = spot_of(a, true, f8, row, sub);
   const int64_t to_step = kAtOnce * a.c.head_stride * (f8 ? 1 : 2);
-  int stage = 0;
-  walk.copy_next(ring[0]);
-  asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll 1
-  for (; item < rows * a.k_units; item += step, stage ^= 1, walk.next()) {
-    if (item + step < rows * a.k_units) walk.copy_next(ring[stage ^ 1]);
+  for (; item < end; item += step, stage ^= 1) {
+    copy_item<D, kInterleaved>(a, row, item + step, ring[stage ^ 1]);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    const int first = walk.first(), mine = walk.mine(walk.u);
-    const Spot spot = spot_of(a, true, f8, row0 + walk.r, first + sub);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const int first = (item - a.q_units - a.k_units) * a.heads, mine = min(p.Hkv - first, a.heads) - sub;
+    char *const to = spot.to + first * a.c.head_stride * (f8 ? 1 : 2);
 #pragma unroll
     for (int k = 0; k < kVectors; ++k) {
       if (k * kAtOnce >= mine + sub) break;   // the warp's lanes together
       const bool here = spot.live && k * kAtOnce < mine;
-      char *const head = spot.to + k * to_step;
+      char *const head = to + k * to_step;
       const uint4 v = ring[stage][k][slot];
       if (f8) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -494,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kBias)) norm_rope_kernel
         const float sc = quantize(w, vector_amax<kLanes>(w), lo, hi);
         if (here) {
           *reinterpret_cast<uint2 *>(head + 8 * lane) = make_uint2(lo, hi);
-          if (lane == 0) spot.scale[k * kAtOnce * kPage] = sc;
+          if (lane == 0) spot.scale[(first + k * kAtOnce) * kPage] = sc;
         }
       } else if (here) {
         *reinterpret_cast<uint4 *>(head + 16 * lane) = v;
@@ -507,22 +468,18 @@ template <int D, bool kInterleaved, bool kBias>
 cudaError_t launch(NormRopeArgs a, int num_sms, cudaStream_t stream) {
   constexpr int kAtOnce = 32 / (D / 8);
   const int kinds = a.c.v != nullptr ? 2 : 1;
-  // Groups of kMostRows rows where that leaves every SM its CTAs, else of fewer; below that as
-  // many CTAs to a row as run at a time, and batches as large as leaves each of their warps one.
-  const int64_t ctas = static_cast<int64_t>(num_sms) * ctas_per_sm(kBias);
-  a.group_rows = 1;
-  while (a.group_rows < kMostRows && a.p.R >= 2 * a.group_rows * ctas) a.group_rows *= 2;
-  const int most = static_cast<int>(std::max<int64_t>(1, ctas / a.p.R));
-  int per = 1;
-  for (;; per *= 2) {
+  // Batches as large as leaves each of the warps that run at a time one, and a row to a warp where there
+  // are as many rows.
+  const int64_t warps = static_cast<int64_t>(num_sms) * ctas_per_sm(kBias) * kWarps;
+  for (int per = 1;; per *= 2) {
     a.heads = per * kAtOnce;
     a.q_units = (a.p.Hq + a.heads - 1) / a.heads;
     a.k_units = (a.p.Hkv + a.heads - 1) / a.heads;
-    a.splits = (a.q_units + a.k_units * kinds + kWarps - 1) / kWarps;
-    if (per == kVectors || (a.group_rows == 1 && a.splits <= most)) break;
+    a.parts = a.q_units + a.k_units * kinds;
+    if (per == kVectors || 2 * a.p.R * a.parts <= warps) break;
   }
-  a.splits = a.group_rows > 1 ? 1 : std::min(a.splits, most);
-  const int64_t grid = (a.p.R + a.group_rows - 1) / a.group_rows * a.splits;
+  a.parts = static_cast<int>(std::min<int64_t>(a.parts, (warps + a.p.R - 1) / a.p.R));
+  const int64_t grid = (a.p.R * a.parts + kWarps - 1) / kWarps;
   return launch_early(norm_rope_kernel<D, kInterleaved, kBias>, static_cast<unsigned>(grid), kThreads, 0, 1, stream, a);
 }
 
