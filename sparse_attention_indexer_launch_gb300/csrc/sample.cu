@@ -774,16 +774,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const auto kept = [&](uint64_t w) { return w >= local.least ? w : 0; };
     if (!(kTopK || kTopP) || threshold == 0) {
       uint64_t sum = 0;
-      each_two_tiles([&](int, const float (&x)[4]) {
+      const auto all = [&](auto keep) {
+        each_two_tiles([&](int, const float (&x)[4]) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          Weights v;
-          weights(x[2 * h], x[2 * h + 1], local, table, v);
+          for (int h = 0; h < 2; ++h) {
+            Weights v;
+            weights(x[2 * h], x[2 * h + 1], local, table, v);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (v.d[i] < kCut) sum += kept(v.w[i]);
-        }
-      });
+            for (int i = 0; i < 2; ++i)
+              if (v.d[i] < kCut) sum += keep(v.w[i]);
+          }
+        });
+      };
+      if (local.least == 1) all([](uint64_t w) { return w; });
+      else all(kept);
       return warp_total(sum);
     }
     const float least_x = radix_key_value(static_cast<uint32_t>(threshold >> kIndexBits));

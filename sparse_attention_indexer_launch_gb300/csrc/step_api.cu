@@ -65,7 +65,7 @@ idx_status check_norm_rope(const idx_norm_rope_args *p, const idx_kv_cache *c) {
   if ((c != nullptr) != (p->slot != nullptr)) return IDX_EINVAL;
   if (p->rot > 0 && (p->pos == nullptr || p->inv_freq == nullptr)) return IDX_EINVAL;
   if (p->pos_stride < 0 || (p->axes > 1 && p->pos_stride < p->R)) return IDX_EINVAL;
-  // the grid holds a warp per vector at most, eight to a CTA
+  // a warp per vector at most: their number stays below 2^31
   if (p->R > INT32_MAX / (p->Hq + 2 * static_cast<int64_t>(p->Hkv))) return IDX_EUNSUPPORTED;
   for (const int64_t s : {p->q_stride, p->k_stride, p->v_stride, p->q_out_stride, p->k_out_stride, p->pos_stride})
     if (s >= kMaxStride) return IDX_EUNSUPPORTED;
