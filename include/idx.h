@@ -562,7 +562,8 @@ typedef struct {
     int32_t free_cap;          /* entries of free_pages, >= 0 */
 } idx_tree_accept_args;
 
-/* Bytes of state that idx_tree_accept needs. */
+/* Bytes of state that idx_tree_accept needs: as for idx_tree_tables, all zero before its
+ * first use; calls that overlap in time need one each. */
 size_t idx_tree_accept_state_size(void);
 
 /* One launch.  A request's token 0 is accepted; behind an accepted token n the first child c

@@ -542,6 +542,7 @@ def make_norm_rope(q, k=None, v=None, *, q_out=None, k_out=None, pos, inv_freq, 
                  q_norm=int(q_norm), k_norm=int(k_norm), eps=float(eps), axes=axes,
                  axis=(ctypes.c_uint8 * 128)(*axis))
     a.device, a.cache = device, cache
+    a.held = (q, k, v, q_out, k_out, pos, inv_freq, slot, q_weight, q_bias, k_weight, k_bias, rows)   # as long as the plan
     return a
 
 
@@ -572,6 +573,7 @@ def make_sample(logits, u, token, *, logprob=None, temperature=None, top_k=None,
                min_p=_ptr(min_p), rows=_ptr(rows), ld=int(logits.stride(0)) if R > 1 else V, R=R, V=V,
                logits_dtype=IDX_LOGITS_BF16 if logits.dtype == torch.bfloat16 else IDX_LOGITS_F32)
     a.device, a.token, a.logprob = device, token.data_ptr(), None if logprob is None else logprob.data_ptr()
+    a.held = (logits, u, token, logprob, temperature, top_k, top_p, min_p, rows)   # as long as the plan
     return a
 
 
@@ -602,6 +604,8 @@ def make_tree_accept(row_start, draft, target, ctx_len, page_table, free_pages, 
                    new_ctx=_ptr(new_ctx), accept_len=_ptr(accept_len), last=_ptr(last), path=_ptr(path), token=_ptr(token),
                    P=int(P), Q=Q, pt_stride=int(page_table.shape[1]), cap=cap, free_cap=int(free_pages.numel()))
     a.device = device
+    a.held = (row_start, draft, target, ctx_len, page_table, free_pages, free_count, free_left, new_ctx, accept_len, last, path,
+              token, parent)   # as long as the plan
     return a
 
 

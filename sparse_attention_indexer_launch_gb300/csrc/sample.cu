@@ -1301,7 +1301,7 @@ cudaError_t launch(SampleArgs a, cudaStream_t stream) {
 
   // CTAs of a row, and whether an SM has one or two of them: by the cycles that all rows take in
   // waves of the clusters that fit.  A CTA takes about 15,000 and one a logit beside another one,
-  // seven tenths of that alone (64 x 128,000 bf16: four in pairs 21.7 us, eight 27.7; 8 x 151,552 fp32:
+  // seven tenths of that alone (64 x 128,000 bf16: four in pairs 20.8 us, eight 27.7; 8 x 151,552 fp32:
   // eight alone 14.9 us, in pairs, which the hardware takes where they fit, 16.9).
   int64_t best = 0;
   int smem = 0;

@@ -268,3 +268,27 @@ def test_the_indexers_own_cache(lib):
     lib.idx_norm_rope(c.plan())
     c.check()
     assert keys.data_ptr() == c.cache.k
+
+
+@pytest.mark.parametrize("Hq,Hkv,norm", [(64, 8, "rms"), (5, 3, "rms"), (64, 1, "layer"), (0, 2, "rms"), (3, 0, "none")])
+def test_rows_do_not_depend_on_their_batch(lib, Hq, Hkv, norm):
+    """A row's warps and their shares follow from the batch; its values do not, to the bit."""
+    gen = torch.Generator(device="cuda").manual_seed(Hq)
+    R, D = 9001, 128
+    kind = dict(rms=lib.IDX_NORM_RMS, layer=lib.IDX_NORM_LAYER, none=lib.IDX_NORM_NONE)[norm]
+    x = torch.randn(R, Hq + Hkv, D, device="cuda", generator=gen).bfloat16()
+    pos = torch.randint(-2 ** 31, 2 ** 31, (R,), device="cuda", generator=gen).int()
+    inv_freq = 10000.0 ** (-torch.arange(0, D, 2, device="cuda").float() / D)
+    weight = None if norm == "none" else torch.rand(D, device="cuda", generator=gen)
+
+    def rows(a, b):
+        out = torch.full((b - a, Hq + Hkv, D), -7.0, device="cuda").bfloat16()
+        part = lambda t, lo, hi: t[:, lo:hi] if hi > lo else None  # noqa: E731
+        lib.idx_norm_rope(lib.make_norm_rope(part(x[a:b], 0, Hq), part(x[a:b], Hq, Hq + Hkv), q_out=part(out, 0, Hq), k_out=part(out, Hq, Hq + Hkv),
+                                             pos=pos[a:b], inv_freq=inv_freq, q_norm=kind, k_norm=kind, q_weight=weight if Hq else None,
+                                             k_weight=weight if Hkv else None))
+        return out
+
+    every = rows(0, R)
+    for a, b in ((0, 1), (77, 84), (100, 400), (500, 1500), (2000, 5000), (R - 4300, R)):
+        assert torch.equal(rows(a, b), every[a:b])

@@ -82,3 +82,48 @@ def test_a_serving_loop(example, prompts):
     for t, want in zip((again.k, again.v, again.k_scale, again.v_scale, again.idx_k, again.idx_scale), mine):
         pick = (lambda t: t[page, at]) if t.dtype == torch.uint8 else (lambda t: t[page, :, at])
         assert torch.equal(pick(t), pick(want))
+
+
+CAPTURED_FIRST = """
+import torch, sparse_attention_indexer_launch_gb300 as lib
+torch.manual_seed(0)
+i32 = dict(dtype=torch.int32, device="cuda")
+x = torch.randn(5, 6, 128, device="cuda").bfloat16()
+q, cache = torch.zeros(5, 4, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 64, 1, 128, dtype=torch.bfloat16, device="cuda")
+values = cache.clone()
+norm = lib.make_norm_rope(x[:, :4], x[:, 4:5], x[:, 5:], q_out=q, pos=torch.arange(5, **i32), inv_freq=torch.rand(64, device="cuda"),
+                          cache=lib.make_kv_cache(cache, values), slot=torch.arange(5, **i32))
+logits, token = torch.randn(5, 5000, device="cuda"), torch.zeros(5, **i32)
+sample = lib.make_sample(logits, torch.rand(5, device="cuda"), token, top_p=torch.full((5,), 0.9, device="cuda"))
+row_start, table, stack = torch.tensor([0, 5], **i32), torch.tensor([[0, 1]], **i32), torch.zeros(2, **i32)
+n = {k: torch.zeros(s, **i32) for k, s in dict(new_ctx=1, accept_len=1, last=1, path=5, token=5, free_left=1).items()}
+state = lib.alloc_state(lib.tree_accept_state_size())
+accept = lib.make_tree_accept(row_start, token.clone(), token, torch.zeros(1, **i32), table, stack, torch.zeros(1, **i32), P=2, **n)
+def calls():
+    lib.idx_norm_rope(norm)
+    lib.idx_sample(sample)
+    lib.idx_tree_accept(accept, state)
+    lib.idx_tree_commit(norm.cache, row_start, n["accept_len"], n["path"], slots)
+slots = torch.arange(5, **i32)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (q, cache, token, *n.values())]
+calls()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (q, cache, token, *n.values())))
+print("the same")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose very first calls are captured: what they set up once works there as well."""
+    import subprocess
+    import sys
+    if not torch.cuda.is_available():
+        pytest.fail("no CUDA device")
+    done = subprocess.run([sys.executable, "-c", CAPTURED_FIRST], cwd=ROOT, capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0 and "the same" in done.stdout, done.stderr[-2000:]
