@@ -163,7 +163,7 @@ struct SampleArgs {
   int32_t *token;
   float *logprob;          // or null
   int32_t vec;             // rows allow loads of four logits
-  int32_t ctas, warp_len, alone;   // CTAs of a row, logits of a warp, whether an SM has one CTA (set by launch_sample)
+  int32_t ctas, warp_len;  // CTAs of a row, logits of a warp (set by launch_sample)
 };
 
 struct TreeAcceptArgs {

@@ -1173,7 +1173,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (listed) {
       // While the first CTA searches, the others sum what lies above the border in each of their
       // warps, for the one in which the token will be.
-      const bool early = a.alone && mass && rank != 0;
+      const bool early = mass && rank != 0;
       cluster.barrier_arrive();
       if (early && local.least == 1) {
         const uint64_t above = sum_above(border, fine);
@@ -1318,7 +1318,6 @@ cudaError_t launch(SampleArgs a, cudaStream_t stream) {
         best = cycles;
         a.ctas = ctas;
         a.warp_len = len;
-        a.alone = alone;
         smem = alone ? std::max(need, kAlone) : need;
       }
     }
