@@ -1049,6 +1049,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const uint64_t v = list[i] >= threshold ? list_weight(i) : 0;
         return v >= local.least ? v : 0;
       };
+      const auto finish_listed = [&](uint64_t c, uint64_t total) {
+        finish(a, row, (1 << kIndexBits) - 1 - static_cast<int>(c & ((1u << kIndexBits) - 1)), radix_key_value(static_cast<uint32_t>(c >> kIndexBits)),
+               total, r, table);
+      };
       uint64_t *const part = reinterpret_cast<uint64_t *>(hist);   // [kThreads]
       bool found = true;
       // threads of an element of a small list; of others a thread has kChunk
@@ -1089,15 +1093,45 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           if (mass) found = over < want && want <= over + all;
           keep = keep && (mass ? over + higher < want : higher < ceil_product(top_p, all));
         }
+        // kept weights by place, behind `both`
+        static_assert(kSmallList * (sizeof(ulonglong2) + sizeof(uint64_t)) <= kYBins * sizeof(uint32_t), "beside the list");
+        uint64_t *const kept = reinterpret_cast<uint64_t *>(both + kSmallList);
+        if (here && part_of == 0) kept[e] = keep && mine_w >= local.least ? mine_w : 0;
         const int kept_n = __syncthreads_count(keep);
         if (keep && higher_n == static_cast<uint32_t>(kept_n) - 1) s.composite = mine_c;
-        own_kept = keep && mine_w >= local.least ? mine_w : 0;
-        const Sums kept_sums = exclusive_sum(own_kept, s.warp_sum);
-        before = kept_sums.before;
-        list_total = kept_sums.all;
-        threshold = s.composite;
         __syncthreads();
-        part[tid] = before;
+        threshold = s.composite;
+        if (warp == 0) {   // the rest is one warp's, which waits for nobody: up to eight a lane
+          const int each = (n + 31) / 32, first = min(lane * each, n), last = min(first + each, n);
+          for (int i = first; i < last; ++i) own_kept += kept[i];
+          before = own_kept;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t up = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += up;
+          }
+          list_total = __shfl_sync(0xffffffffu, before, 31);
+          before -= own_kept;
+          if (from_top) {
+            const uint64_t at = __umul64hi(f_u, list_total);
+            if (at >= before && at < before + own_kept) {
+              int i = first;
+              for (; at >= before + kept[i]; ++i) before += kept[i];
+              finish_listed(list[i], list_total);
+            }
+          } else {   // sums before each
+            for (int i = first; i < last; ++i) {
+              const uint64_t w = kept[i];
+              kept[i] = before;
+              before += w;
+            }
+            __syncwarp();
+            if (lane <= ctas) {
+              const int i = list_at[lane * kWarps];
+              cta_at[lane] = i < n ? kept[i] : list_total;
+            }
+          }
+        }
       } else {
         const auto list_mass = [&](uint64_t from) {
           uint64_t v = 0;
@@ -1128,27 +1162,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       if (from_top) {
         const uint64_t at = __umul64hi(f_u, list_total);
-        if (at >= before && at < before + own_kept) {
-          int i = split > 0 ? tid / split : tid * kChunk;
+        if (n > kSmallList && at >= before && at < before + own_kept) {
+          int i = tid * kChunk;
           for (uint64_t v; at >= before + (v = kept_weight(i)); ++i) before += v;
-          finish(a, row, (1 << kIndexBits) - 1 - static_cast<int>(list[i] & ((1u << kIndexBits) - 1)),
-                 radix_key_value(static_cast<uint32_t>(list[i] >> kIndexBits)), list_total, r, table);
+          finish_listed(list[i], list_total);
         }
         cluster.barrier_wait();
         return;
       }
       verdict.threshold = threshold;
-      if (mass && found) {
+      if (mass && found && n > kSmallList) {
         // up to each CTA's part: the list's kept weights before it
         __syncthreads();
         if (tid <= ctas) {
-          const int i = list_at[tid * kWarps], t = split > 0 ? i * split : i / kChunk;   // the thread that has it
+          const int i = list_at[tid * kWarps], t = i / kChunk;   // the thread that has it
           uint64_t at = t < kThreads ? part[t] : list_total;
 #pragma unroll 1
-          for (int j = split > 0 ? i : t * kChunk; j < i; ++j) at += kept_weight(j);
+          for (int j = t * kChunk; j < i; ++j) at += kept_weight(j);
           cta_at[tid] = at;
         }
-        __syncthreads();
+      }
+      if (mass && found && warp == 0) {
+        __syncwarp();
         // the CTA in which the sums pass u Z
         const int c = lane & (kCtas - 1);
         const uint64_t here = c < ctas ? mine.told[c].kept + cta_at[c + 1] - cta_at[c] : 0;
