@@ -21,15 +21,15 @@
 // above as well, where they are few) go into a list that the first CTA gathers and searches.  A
 // bin with too many is cut into 256 finer ones first; where even those hold too many (equal
 // logits), a radix descent runs over the whole row.  (Descents over the whole row for every
-// border took 953 us for 256 rows of 151,552 fp32 logits with mixed filters; this 211.)
+// border took 953 us for 256 rows of 151,552 fp32 logits with mixed filters; this 208.)
 //
 // What bounds it: reading those rows would take 22.9 us at the measured copy bandwidth.  Their
 // weights to 2^-38 are some 30 instructions a logit, 27 us if every slot were used.  The rest is the
 // chain of a row's steps, 25 to 30 us with two rows to an SM, in which warps wait for the slowest
-// one of the cluster (issue slots 42% busy, a third of the stalls at barriers).  A single row is that
+// one of the cluster (issue slots 48% busy, a quarter of the stalls at barriers).  A single row is that
 // chain alone: with top-p of 151,552 logits some 45,000 cycles, of which reading and the largest
-// logit are 7,000, weights and histograms 12,000, border and candidates 9,000, the list 8,000 and the
-// token among the kept ones 9,000 (less where the first CTA's neighbours have summed meanwhile).
+// logit are 6,500, weights and histograms 12,500, border and candidates 8,700, the list 6,900 and the
+// token among the kept ones 9,800 (5,000 in other CTAs than the first, which sum during the search).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -1336,8 +1336,8 @@ cudaError_t launch(SampleArgs a, cudaStream_t stream) {
 
   // CTAs of a row, and whether an SM has one or two of them: by the cycles that all rows take in
   // waves of the clusters that fit.  A CTA takes about 15,000 and one a logit beside another one,
-  // seven tenths of that alone (64 x 128,000 bf16: four in pairs 20.8 us, eight 27.7; 8 x 151,552 fp32:
-  // eight alone 14.9 us, in pairs, which the hardware takes where they fit, 16.9).
+  // seven tenths of that alone (64 x 128,000 bf16: four in pairs 22.9 us where eight took 27.7; 8 x 151,552
+  // fp32: eight alone 14.9 us, in pairs, which the hardware takes where they fit, 16.9).
   int64_t best = 0;
   int smem = 0;
   a.ctas = 0;
