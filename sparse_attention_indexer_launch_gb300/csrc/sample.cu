@@ -18,18 +18,20 @@
 // so one number is enough, the composite (key, ~index) of the last kept one.  A first pass
 // sorts the weights' exponents into bins of 1 / 32 octave, counts for top-k and leading bits
 // of the weights for top-p; the elements of the bin that holds the border (for top-k those
-// above as well, where they are few) go into a list that the first CTA gathers and searches.  A
-// bin with too many is cut into 256 finer ones first; where even those hold too many (equal
+// above as well, where they are few) go into a list that the first CTA gathers and searches, and
+// what lies above it is summed exactly.  (Leading bits can point at the neighbour of a bin whose edge
+// is next to the border; the exact sum tells, and the neighbour is taken.)  A bin with too many is cut into 256 finer ones first; where even those hold too many (equal
 // logits), a radix descent runs over the whole row.  (Descents over the whole row for every
-// border took 953 us for 256 rows of 151,552 fp32 logits with mixed filters; this 208.)
+// border took 953 us for 256 rows of 151,552 fp32 logits with mixed filters; this 222.)
 //
 // What bounds it: reading those rows would take 22.9 us at the measured copy bandwidth.  Their
 // weights to 2^-38 are some 30 instructions a logit, 27 us if every slot were used.  The rest is the
 // chain of a row's steps, 25 to 30 us with two rows to an SM, in which warps wait for the slowest
-// one of the cluster (issue slots 48% busy, a quarter of the stalls at barriers).  A single row is that
-// chain alone: with top-p of 151,552 logits some 45,000 cycles, of which reading and the largest
-// logit are 6,500, weights and histograms 12,500, border and candidates 8,700, the list 6,900 and the
-// token among the kept ones 9,800 (5,000 in other CTAs than the first, which sum during the search).
+// one of the cluster (issue slots half busy, a quarter of the stalls at barriers).  A single row is that
+// chain alone: with top-p of 151,552 logits some 40,000 cycles, of which reading and the largest
+// logit are 6,500, weights and histogram 11,500, border, candidates and what lies above 11,000, the
+// list 7,000 and the token among the kept ones 4,500.  (Sums above from a histogram of two words to a
+// bin, off by 2^-30, took 208 us instead of 222: but a row's last bits then depend on its CTAs.)
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -183,7 +185,7 @@ template <>
 struct Quad<float> {
   using Vec = float4;
   static __device__ __forceinline__ float one(float v) { return v; }
-  static constexpr int kListMost = 768;    // a list within the histogram's second half
+  static constexpr int kListMost = 768;    // candidates of a row in the list
   static __device__ __forceinline__ void get(const Vec &v, float (&x)[4]) {
     x[0] = v.x;
     x[1] = v.y;
@@ -400,15 +402,13 @@ __device__ __noinline__ Found find_bin(bool mass, int ctas, uint32_t *hist, Scra
   return s.found;
 }
 
-// The octaves' sums of this CTA's bins of exponents, to all CTAs: octave[rank] there.  Bins in
-// units of the first words; `low`: what a unit of the second words is (0: there are none).
-__device__ __noinline__ void push_octaves(const uint32_t *hist, float low, float (*octave)[kOctaveBins]) {
+// The octaves' sums of this CTA's bins of exponents, to all CTAs: octave[rank] there.
+__device__ __noinline__ void push_octaves(const uint32_t *hist, float (*octave)[kOctaveBins]) {
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = warp; o < kOctaveBins; o += kWarps) {
-    float v = static_cast<float>(__reduce_add_sync(0xffffffffu, hist[o * 32 + lane]));
-    if (low != 0.0f) v = fmaf(static_cast<float>(__reduce_add_sync(0xffffffffu, hist[kYBins + o * 32 + lane])), low, v);
+    const float v = static_cast<float>(__reduce_add_sync(0xffffffffu, hist[o * 32 + lane]));
     const cg::cluster_group cluster = cg::this_cluster();
     if (lane < cluster.num_blocks()) cluster.map_shared_rank(octave, lane)[cluster.block_rank()][o] = v;
   }
@@ -444,11 +444,11 @@ struct Exponent {
   int32_t bin;
   float all;
 };
-__device__ __noinline__ Exponent find_exponent(float low, const uint32_t *hist, const float (*octave)[kOctaveBins], float *sum,
+__device__ __noinline__ Exponent find_exponent(bool mass, const uint32_t *hist, const float (*octave)[kOctaveBins], float *sum,
                                                float want) {
   static_assert(kOctaveBins > 32 && kOctaveBins <= 64, "one or two octaves a lane");
   const int tid = threadIdx.x, lane = tid & 31, ctas = static_cast<int>(cg::this_cluster().num_blocks());
-  const auto scaled = [&](float v, int o) { return low != 0.0f ? v * __uint_as_float(static_cast<uint32_t>(127 - o) << 23) : v; };
+  const auto scaled = [&](float v, int o) { return mass ? v * __uint_as_float(static_cast<uint32_t>(127 - o) << 23) : v; };
   float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
   for (int c = 0; c < kCtas; ++c) {
@@ -469,9 +469,7 @@ __device__ __noinline__ Exponent find_exponent(float low, const uint32_t *hist, 
     const int c = tid & (kCtas - 1), b = tid / kCtas;
     float v = 0.0f;
     if (c < ctas) {
-      const uint32_t *const h = cg::this_cluster().map_shared_rank(hist, c) + o * 32 + b;
-      v = static_cast<float>(*h);
-      if (low != 0.0f) v = fmaf(static_cast<float>(h[kYBins]), low, v);
+      v = static_cast<float>(cg::this_cluster().map_shared_rank(hist, c)[o * 32 + b]);
     }
 #pragma unroll
     for (int k = kCtas / 2; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
@@ -526,16 +524,11 @@ __device__ __noinline__ uint64_t descend_list(bool mass, const uint64_t *list, i
   return prefix;
 }
 
-// The histograms, the list (in the second half of them where it fits), the row; without filters
-// the row alone.
-template <typename T>
-__host__ __device__ constexpr size_t list_offset() {
-  return Quad<T>::kListMost * sizeof(uint64_t) <= kYBins * sizeof(uint32_t) ? kYBins * sizeof(uint32_t) : 2 * kYBins * sizeof(uint32_t);
-}
+// The histogram, the list, the row; without filters the row alone.
+constexpr size_t kListOffset = kYBins * sizeof(uint32_t);
 template <typename T, bool kList>
 __host__ __device__ constexpr size_t fixed_smem() {
-  const size_t list = list_offset<T>() + Quad<T>::kListMost * sizeof(uint64_t), hist = 2 * kYBins * sizeof(uint32_t);
-  return !kList ? 0 : list > hist ? list : hist;
+  return kList ? kListOffset + Quad<T>::kListMost * sizeof(uint64_t) : 0;
 }
 
 // kTopK, kTopP: the rows may have these filters.
@@ -546,8 +539,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   using Pub = Shared<T, kTopK || kTopP>;
   constexpr int kListMost = Q::kListMost, kChunk = (kListMost + kThreads - 1) / kThreads;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  uint32_t *const hist = reinterpret_cast<uint32_t *>(smem_raw);                     // [2][kYBins], [3][kBins] in descents
-  uint64_t *const list = reinterpret_cast<uint64_t *>(smem_raw + list_offset<T>());  // [kListMost] composites, by index
+  uint32_t *const hist = reinterpret_cast<uint32_t *>(smem_raw);                     // [kYBins], [3][kBins] in descents
+  uint64_t *const list = reinterpret_cast<uint64_t *>(smem_raw + kListOffset);  // [kListMost] composites, by index
   T *const data = reinterpret_cast<T *>(smem_raw + fixed_smem<T, kTopK || kTopP>());
   __shared__ Pub mine;
   __shared__ Scratch s;
@@ -579,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if constexpr (kTopK || kTopP) {
     for (int i = ctas * kOctaveBins + tid; i < kCtas * kOctaveBins; i += kThreads) (&mine.octave[0][0])[i] = 0.0f;
     if (tid >= ctas * kWarps && tid < kRanges) mine.count[tid] = 0;
-    clear_hist(hist, 2 * kYBins);
+    clear_hist(hist, kYBins);
   }
   grid_dependency_wait();
   Params par{};
@@ -799,19 +792,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const auto low_edge = [&](int32_t border) {   // less ref, a little lower
     return (__uint_as_float(local.whole_bits - static_cast<uint32_t>(2 * border - 62)) - kMagic - 0x1.2p-7f) / local.c_hi;
   };
-  const auto sum_above = [&](int32_t border, int32_t fine) {
+  const auto sum_above = [&](int32_t border, int32_t fine, uint64_t &all, uint64_t &kept) {   // and what min-p keeps of them
     const float least_x = low_edge(border);
-    return sum_of_some([&](float x, int) { return x - local.ref >= least_x; },
-                       [&](float x, uint64_t w, uint32_t d) {
-                         int32_t code = exponent_bin(d), at = border;
-                         if (fine >= 0) {
-                           uint64_t minus, lo;
-                           exponents(x, x, local, minus, lo);
-                           code = fine_code(minus, to_64ths(minus), d, 0);
-                           at = border * kFine + fine;
-                         }
-                         return code < at && w >= local.least ? w : 0;
-                       });
+    uint64_t small = 0;
+    all = sum_of_some([&](float x, int) { return x - local.ref >= least_x; },
+                      [&](float x, uint64_t w, uint32_t d) {
+                        int32_t code = exponent_bin(d), at = border;
+                        if (fine >= 0) {
+                          uint64_t minus, lo;
+                          exponents(x, x, local, minus, lo);
+                          code = fine_code(minus, to_64ths(minus), d, 0);
+                          at = border * kFine + fine;
+                        }
+                        if (code >= at) return static_cast<uint64_t>(0);
+                        if (w < local.least) small += w;
+                        return w;
+                      });
+    kept = all - (local.least > 1 ? warp_total(small) : 0);
   };
   const uint64_t f_u = u > 0.0f ? (u < 1.0f ? static_cast<uint64_t>(u * 0x1p64f) : ~0ull) : 0ull;
   uint64_t threshold = 0;   // composite of the last kept element
@@ -823,7 +820,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const uint64_t low = kTopK ? threshold : 0;   // top-p's elements are those >= low
     const auto among = [&](uint64_t c) { return !kTopK || c >= low; };
     uint64_t sum = 0;
-    // leading bits of a weight in two words of the histogram, as many as this CTA's elements leave room for
+    // leading bits of a weight in a word of the histogram, as many as this CTA's elements leave room for;
+    // the last one always set, so that what is cut off has no direction
     const int lead = __clz(kWarps * len);
     if (mass) {
       each_two_tiles([&](int t, const float (&x)[4]) {
@@ -835,9 +833,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           for (int i = 0; i < 2; ++i) {
             if (v.d[i] < kCut && (!kTopK || low == 0 || among(composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i)))) {
               sum += v.w[i];
-              uint32_t *const bin = hist + ((v.d[i] + 63) >> 1);
-              atomicAdd(bin, static_cast<uint32_t>(v.m[i] >> 32) >> (31 - lead));
-              atomicAdd(bin + kYBins, (static_cast<uint32_t>(v.m[i] >> (63 - 2 * lead)) & ((1u << lead) - 1)) | 1u);
+              atomicAdd(&hist[(v.d[i] + 63) >> 1], static_cast<uint32_t>(v.m[i] >> 32) >> (31 - lead) | 1u);
             }
           }
         }
@@ -858,8 +854,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
       });
     }
-    const float low_unit = mass ? __uint_as_float(static_cast<uint32_t>(127 - lead) << 23) : 0.0f;
-    push_octaves(hist, low_unit, mine.octave);
+    push_octaves(hist, mine.octave);
     if (mass && warp == 0) {
       sum = warps_total(warp_above);
       if (lane < ctas) cluster.map_shared_rank(&mine, lane)->told[rank].all = sum;
@@ -873,375 +868,369 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       want = ceil_product(top_p, z);
     }
     const float want_units = mass ? static_cast<float>(want) * __uint_as_float(static_cast<uint32_t>(127 + lead - 45) << 23) : static_cast<float>(want);
-    const Exponent ex = find_exponent(low_unit, hist, mine.octave, s.bin, want_units);
-    const int32_t border = ex.bin;
+    const Exponent ex = find_exponent(mass, hist, mine.octave, s.bin, want_units);
+    int32_t border = ex.bin;
     if (!mass && ex.all <= static_cast<float>(want)) {   // all that have a weight are kept
       cluster.sync();               // nobody reads the histogram any more
-      clear_hist(hist, 2 * kYBins);
+      clear_hist(hist, kYBins);
       __syncthreads();
       continue;
     }
 
     // Candidates in order of their index, and exactly what lies above them: of the border's
-    // bin, or of its part `fine`; in the first round for top-k all from the top.
-    int32_t fine = -1, n = 0;
-    bool listed = false, from_top = false;
-    int32_t candidates = 0;   // of this warp
-    uint64_t over = 0;   // what lies above the candidates in all CTAs
-    ushort4 counts{};    // candidates of warps 4 * lane to 4 * lane + 3
-    for (int round = 0; round < 2; ++round) {
-      from_top = !mass && round == 0;
-      uint64_t above = 0, kept = 0;
-      {   // what this CTA has above: from its histogram
-        if (round == 0) {
-#pragma unroll
-          for (int k = 0; k < kYBins / kThreads; ++k) {
-            const int b = tid + k * kThreads, o = b >> 5;
-            if (b >= border) continue;
-            const uint64_t m = (static_cast<uint64_t>(hist[b]) << lead) + hist[kYBins + b];   // units of 2^(o + 1 - 2 lead)
-            const int down = o + 2 * lead - 45;   // to 2^-44
-            above += !mass ? hist[b] : down > 0 ? (m + (1ull << down >> 1)) >> down : m << -down;
-          }
-        } else {
+    // bin, or of its part `fine`; in the first round for top-k all from the top.  Where the leading
+    // bits of the weights had missed the bin (a border very near its edge), again with its neighbour.
+    bool listed = false;
+    for (int misses = 0;; ++misses) {
+      int32_t fine = -1, n = 0;
+      bool from_top = false, empty = false, by_warp = false;   // by_warp: warp_kept is each warp's
+      int32_t candidates = 0;   // of this warp
+      uint64_t over = 0;   // what lies above the candidates in all CTAs
+      ushort4 counts{};    // candidates of warps 4 * lane to 4 * lane + 3
+      for (int round = 0; round < 2; ++round) {
+        from_top = !mass && round == 0;
+        uint64_t above = 0, kept = 0;
+        // what this CTA has above, from its histogram: counts, and weights in the second round
+        if (round == 1) {
           const int b = kBins - 1 - tid;
           if (b > kBins - 1 - fine) above = (mass ? static_cast<uint64_t>(hist[kBins + b]) << 32 : 0) + hist[b];
           if (tid == 0) above += mine.told[rank].above;
+        } else if (!mass) {
+#pragma unroll
+          for (int k = 0; k < kYBins / kThreads; ++k) above += tid + k * kThreads < border ? hist[tid + k * kThreads] : 0;
         }
-        kept = above;
-      }
-      const int32_t at_border = round == 0 ? border : border * kFine + fine;
-      n = 0;
-      // the border's bin as a range of logits less ref, a little wide: most steps of a warp hold none of it
-      const float p_high = __uint_as_float(r.whole_bits - static_cast<uint32_t>(max(2 * border - 63, 0))) - kMagic + 0x1.2p-7f;
-      const float x_low = low_edge(border), x_high = from_top ? INFINITY : p_high / r.c_hi;
-      each_tile([&](int t, const float (&x)[4]) {
-        bool near = false;
+        const int32_t at_border = round == 0 ? border : border * kFine + fine;
+        n = 0;
+        // the border's bin as a range of logits less ref, a little wide: most steps of a warp hold none of it
+        const float p_high = __uint_as_float(r.whole_bits - static_cast<uint32_t>(max(2 * border - 63, 0))) - kMagic + 0x1.2p-7f;
+        const float x_low = low_edge(border), x_high = from_top ? INFINITY : p_high / r.c_hi;
+        each_tile([&](int t, const float (&x)[4]) {
+          bool near = false;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) near = near || (x[k] - local.ref >= x_low && x[k] - local.ref <= x_high);
-        if (!__any_sync(0xffffffffu, near)) return;
-        int32_t code[4];   // the bin, and its part in the second round: smaller above
+          for (int k = 0; k < 4; ++k) near = near || (x[k] - local.ref >= x_low && x[k] - local.ref <= x_high);
+          if (!__any_sync(0xffffffffu, near)) return;
+          int32_t code[4];   // the bin, and its part in the second round: smaller above
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint64_t minus, lo;
-          uint32_t d[2];
-          exponents(x[2 * h], x[2 * h + 1], local, minus, lo);
-          const uint64_t t64 = to_64ths(minus);
-          steps(t64, local, d);
+          for (int h = 0; h < 2; ++h) {
+            uint64_t minus, lo;
+            uint32_t d[2];
+            exponents(x[2 * h], x[2 * h + 1], local, minus, lo);
+            const uint64_t t64 = to_64ths(minus);
+            steps(t64, local, d);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            code[2 * h + i] = exponent_bin(d[i]);
-            if (round == 1) code[2 * h + i] = fine_code(minus, t64, d[i], i);
-          }
-        }
-        uint32_t take = 0;   // places among those taken: four ballots, a lane's elements side by side
-        int32_t at = n;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool in = from_top ? code[k] <= at_border : code[k] == at_border;
-          const uint32_t lanes = __ballot_sync(0xffffffffu, in);
-          take |= static_cast<uint32_t>(in) << k;
-          at += __popc(lanes & ((1u << lane) - 1));
-          n += __popc(lanes);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (take >> k & 1) {
-            if (at < Pub::kSegment) {
-              mine.logit[warp][at] = own[t + 4 * lane + k];
-              mine.place[warp][at] = static_cast<uint16_t>(t + 4 * lane + k);
+            for (int i = 0; i < 2; ++i) {
+              code[2 * h + i] = exponent_bin(d[i]);
+              if (round == 1) code[2 * h + i] = fine_code(minus, t64, d[i], i);
             }
-            ++at;
           }
-        }
-      });
-      if (mass && local.least > 1) kept = sum_above(border, fine);   // min-p: of what lies above, what it keeps
-      else kept = warp_total(kept);
-      candidates = n;
-      above = warp_total(above);
-      if (lane == 0) {
-        warp_above[warp] = above;
-        warp_kept[warp] = kept;
-      }
-      if (lane < ctas) cluster.map_shared_rank(&mine, lane)->count[rank * kWarps + warp] = static_cast<uint16_t>(n);   // at most the range
-      __syncthreads();
-      if (warp == 0) {
-        above = warps_total(warp_above);
-        kept = warps_total(warp_kept);
-        if (lane < ctas) {
-          Pub *const to = cluster.map_shared_rank(&mine, lane);
-          to->told[rank].above = above;
-          to->told[rank].kept = kept;
-        }
-      }
-      cluster.sync();
-
-      // the list's length (every warp by itself), and what lies above it
-      static_assert(kRanges == 128, "four counts a lane");
-      counts = reinterpret_cast<const ushort4 *>(mine.count)[lane];
-      n = __reduce_add_sync(0xffffffffu, counts.x + counts.y + counts.z + counts.w);
-      const bool fits = __all_sync(0xffffffffu, max(max(counts.x, counts.y), max(counts.z, counts.w)) <= Pub::kSegment);
-      over = 0;
+          uint32_t take = 0;   // places among those taken: four ballots, a lane's elements side by side
+          int32_t at = n;
 #pragma unroll
-      for (int c = 0; c < kCtas; ++c) over += mine.told[c].above;
-      listed = n > 0 && n <= kListMost && fits;
-      if (from_top && listed) over = 0;   // they are in the list themselves
-      if (listed || round == 1 || over >= want) break;
-
-      // too many: the bin's parts
-      clear_hist(hist, 3 * kBins);
-      __syncthreads();
-      each_tile([&](int t, const float (&x)[4]) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint64_t minus, lo;
-          uint32_t d[2];
-          exponents(x[2 * h], x[2 * h + 1], local, minus, lo);
-          const uint64_t t64 = to_64ths(minus);
-          steps(t64, local, d);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (exponent_bin(d[i]) != border) continue;
-            if (kTopK && low != 0 && !among(composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i))) continue;
-            const uint32_t bin = kBins - 1 - fine_code(minus, t64, d[i], i) % kFine;
-            if (mass) add_to_hist(hist, bin, weight(x[2 * h + i], r, table));
-            else atomicAdd(&hist[bin], 1u);
+          for (int k = 0; k < 4; ++k) {
+            const bool in = from_top ? code[k] <= at_border : code[k] == at_border;
+            const uint32_t lanes = __ballot_sync(0xffffffffu, in);
+            take |= static_cast<uint32_t>(in) << k;
+            at += __popc(lanes & ((1u << lane) - 1));
+            n += __popc(lanes);
           }
-        }
-      });
-      cluster.sync();
-      const Found f = find_bin(mass, ctas, hist, s, want - over);
-      if (f.bin == kBins) break;   // the leading bits had missed the bin
-      fine = kBins - 1 - static_cast<int32_t>(f.bin);
-    }
-
-    // the list: gathered and searched by the first CTA
-    Verdict verdict{0, 0, 0, -1};
-    if (listed && rank == 0) {
-      if (warp == 0) {
-        const int32_t four = counts.x + counts.y + counts.z + counts.w;
-        int32_t at = four;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int32_t up = __shfl_up_sync(0xffffffffu, at, o);
-          if (lane >= o) at += up;
+          for (int k = 0; k < 4; ++k) {
+            if (take >> k & 1) {
+              if (at < Pub::kSegment) {
+                mine.logit[warp][at] = own[t + 4 * lane + k];
+                mine.place[warp][at] = static_cast<uint16_t>(t + 4 * lane + k);
+              }
+              ++at;
+            }
+          }
+        });
+        candidates = n;
+        by_warp = mass && (round == 0 || local.least > 1);
+        if (by_warp) sum_above(border, fine, above, kept);
+        else above = kept = warp_total(above);
+        if (lane == 0) {
+          warp_above[warp] = above;
+          warp_kept[warp] = kept;
         }
-        at -= four;
-        list_at[4 * lane] = at;
-        list_at[4 * lane + 1] = at += counts.x;
-        list_at[4 * lane + 2] = at += counts.y;
-        list_at[4 * lane + 3] = at += counts.z;
-        if (lane == 31) list_at[kRanges] = at + counts.w;
-      }
-      __syncthreads();
-      for (int i = tid; i < n; i += kThreads) {
-        int w = 0;
-#pragma unroll
-        for (int step = kRanges / 2; step > 0; step >>= 1)
-          if (list_at[w + step] <= i) w += step;
-        const Pub *const from = cluster.map_shared_rank(&mine, w / kWarps);
-        const int k = i - list_at[w];
-        list[i] = composite(Q::one(from->logit[w % kWarps][k]), w * len + from->place[w % kWarps][k]);
-      }
-      if (from_top) cluster.barrier_arrive();   // everything that is kept is in the list: the other CTAs may go
-      __syncthreads();
-      const auto list_weight = [&](int i) { return weight(radix_key_value(static_cast<uint32_t>(list[i] >> kIndexBits)), r, table); };
-      const auto kept_weight = [&](int i) {   // behind the search
-        const uint64_t v = list[i] >= threshold ? list_weight(i) : 0;
-        return v >= local.least ? v : 0;
-      };
-      const auto finish_listed = [&](uint64_t c, uint64_t total) {
-        finish(a, row, (1 << kIndexBits) - 1 - static_cast<int>(c & ((1u << kIndexBits) - 1)), radix_key_value(static_cast<uint32_t>(c >> kIndexBits)),
-               total, r, table);
-      };
-      uint64_t *const part = reinterpret_cast<uint64_t *>(hist);   // [kThreads]
-      bool found = true;
-      // threads of an element of a small list; of others a thread has kChunk
-      const int split = n <= 128 ? 4 : n <= kSmallList ? 2 : 0;
-      uint64_t before = 0, list_total = 0, own_kept = 0;   // kept weights: before this thread's, all, its own
-      if (n <= kSmallList) {
-        // threads e * split .. for element e: its rank and the weight of what lies above it by looking at all
-        ulonglong2 *const both = reinterpret_cast<ulonglong2 *>(hist);
-        const int e = tid / split, part_of = tid % split;
-        const bool here = e < n;
-        const uint64_t mine_c = here ? list[e] : 0;
-        if (tid < n) both[tid] = make_ulonglong2(list[tid], among(list[tid]) ? list_weight(tid) : 0);
+        if (lane < ctas) cluster.map_shared_rank(&mine, lane)->count[rank * kWarps + warp] = static_cast<uint16_t>(n);   // at most the range
         __syncthreads();
-        const uint64_t mine_w = here ? both[e].y : 0;
-        uint64_t higher = 0;
-        uint32_t higher_n = 0;
-        if (__any_sync(0xffffffffu, here)) {
-#pragma unroll 4
-          for (int j = part_of; j < n; j += split) {
-            const ulonglong2 o = both[j];
-            const bool above = o.x > mine_c;
-            higher_n += above;
-            higher += above ? o.y : 0;
-          }
-          for (int o = 1; o < split; o <<= 1) {
-            higher_n += __shfl_xor_sync(0xffffffffu, higher_n, o);
-            higher += __shfl_xor_sync(0xffffffffu, higher, o);
+        if (warp == 0) {
+          above = warps_total(warp_above);
+          kept = warps_total(warp_kept);
+          if (lane < ctas) {
+            Pub *const to = cluster.map_shared_rank(&mine, lane);
+            to->told[rank].above = above;
+            to->told[rank].kept = kept;
           }
         }
-        bool keep = here && part_of == 0 && among(mine_c);
-        if (!mass) keep = keep && over + higher_n < want;
-        if (mass || (kTopP && from_top && top_p < 1.0f)) {
-          const uint64_t some = warp_total(keep ? mine_w : 0);
-          if (lane == 0) s.warp_sum[warp] = some;
-          __syncthreads();
-          const uint64_t all = warps_total(s.warp_sum);
-          __syncthreads();
-          if (mass) found = over < want && want <= over + all;
-          keep = keep && (mass ? over + higher < want : higher < ceil_product(top_p, all));
-        }
-        // kept weights by place, behind `both`
-        static_assert(kSmallList * (sizeof(ulonglong2) + sizeof(uint64_t)) <= kYBins * sizeof(uint32_t), "beside the list");
-        uint64_t *const kept = reinterpret_cast<uint64_t *>(both + kSmallList);
-        if (here && part_of == 0) kept[e] = keep && mine_w >= local.least ? mine_w : 0;
-        const int kept_n = __syncthreads_count(keep);
-        if (keep && higher_n == static_cast<uint32_t>(kept_n) - 1) s.composite = mine_c;
+        cluster.sync();
+
+        // the list's length (every warp by itself), and what lies above it
+        static_assert(kRanges == 128, "four counts a lane");
+        counts = reinterpret_cast<const ushort4 *>(mine.count)[lane];
+        n = __reduce_add_sync(0xffffffffu, counts.x + counts.y + counts.z + counts.w);
+        const bool fits = __all_sync(0xffffffffu, max(max(counts.x, counts.y), max(counts.z, counts.w)) <= Pub::kSegment);
+        over = 0;
+#pragma unroll
+        for (int c = 0; c < kCtas; ++c) over += mine.told[c].above;
+        listed = n > 0 && n <= kListMost && fits;
+        empty = n == 0;
+        if (from_top && listed) over = 0;   // they are in the list themselves
+        if (listed || round == 1 || over >= want || (mass && empty)) break;
+
+        // too many: the bin's parts
+        clear_hist(hist, 3 * kBins);
         __syncthreads();
-        threshold = s.composite;
-        if (warp == 0) {   // the rest is one warp's, which waits for nobody: up to eight a lane
-          const int each = (n + 31) / 32, first = min(lane * each, n), last = min(first + each, n);
-          for (int i = first; i < last; ++i) own_kept += kept[i];
-          before = own_kept;
+        each_tile([&](int t, const float (&x)[4]) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint64_t minus, lo;
+            uint32_t d[2];
+            exponents(x[2 * h], x[2 * h + 1], local, minus, lo);
+            const uint64_t t64 = to_64ths(minus);
+            steps(t64, local, d);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (exponent_bin(d[i]) != border) continue;
+              if (kTopK && low != 0 && !among(composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i))) continue;
+              const uint32_t bin = kBins - 1 - fine_code(minus, t64, d[i], i) % kFine;
+              if (mass) add_to_hist(hist, bin, weight(x[2 * h + i], r, table));
+              else atomicAdd(&hist[bin], 1u);
+            }
+          }
+        });
+        cluster.sync();
+        const Found f = find_bin(mass, ctas, hist, s, want - over);
+        if (f.bin == kBins) break;   // the leading bits had missed the bin
+        fine = kBins - 1 - static_cast<int32_t>(f.bin);
+      }
+
+      // the list: gathered and searched by the first CTA
+      Verdict verdict{0, 0, 0, -1};
+      if (listed && rank == 0) {
+        if (warp == 0) {
+          const int32_t four = counts.x + counts.y + counts.z + counts.w;
+          int32_t at = four;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t up = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane >= o) before += up;
+            const int32_t up = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += up;
           }
-          list_total = __shfl_sync(0xffffffffu, before, 31);
-          before -= own_kept;
-          if (from_top) {
-            const uint64_t at = __umul64hi(f_u, list_total);
-            if (at >= before && at < before + own_kept) {
-              int i = first;
-              for (; at >= before + kept[i]; ++i) before += kept[i];
-              finish_listed(list[i], list_total);
-            }
-          } else {   // sums before each
-            for (int i = first; i < last; ++i) {
-              const uint64_t w = kept[i];
-              kept[i] = before;
-              before += w;
-            }
-            __syncwarp();
-            if (lane <= ctas) {
-              const int i = list_at[lane * kWarps];
-              cta_at[lane] = i < n ? kept[i] : list_total;
-            }
-          }
+          at -= four;
+          list_at[4 * lane] = at;
+          list_at[4 * lane + 1] = at += counts.x;
+          list_at[4 * lane + 2] = at += counts.y;
+          list_at[4 * lane + 3] = at += counts.z;
+          if (lane == 31) list_at[kRanges] = at + counts.w;
         }
-      } else {
-        const auto list_mass = [&](uint64_t from) {
-          uint64_t v = 0;
-          for (int i = tid; i < n; i += kThreads) v += list[i] >= from ? list_weight(i) : 0;
-          const uint64_t all = exclusive_sum(v, s.warp_sum).all;
-          __syncthreads();
-          return all;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+          int w = 0;
+#pragma unroll
+          for (int step = kRanges / 2; step > 0; step >>= 1)
+            if (list_at[w + step] <= i) w += step;
+          const Pub *const from = cluster.map_shared_rank(&mine, w / kWarps);
+          const int k = i - list_at[w];
+          list[i] = composite(Q::one(from->logit[w % kWarps][k]), w * len + from->place[w % kWarps][k]);
+        }
+        if (from_top) cluster.barrier_arrive();   // everything that is kept is in the list: the other CTAs may go
+        __syncthreads();
+        const auto list_weight = [&](int i) { return weight(radix_key_value(static_cast<uint32_t>(list[i] >> kIndexBits)), r, table); };
+        const auto kept_weight = [&](int i) {   // behind the search
+          const uint64_t v = list[i] >= threshold ? list_weight(i) : 0;
+          return v >= local.least ? v : 0;
         };
-        if (!mass) {
-          threshold = descend_list(false, list, n, 0, want - over, r, table, hist, s);
-          if (from_top && top_p < 1.0f) {
-            const uint64_t z = list_mass(threshold);
-            threshold = descend_list(true, list, n, threshold, ceil_product(top_p, z), r, table, hist, s);
+        const auto finish_listed = [&](uint64_t c, uint64_t total) {
+          finish(a, row, (1 << kIndexBits) - 1 - static_cast<int>(c & ((1u << kIndexBits) - 1)), radix_key_value(static_cast<uint32_t>(c >> kIndexBits)),
+                 total, r, table);
+        };
+        uint64_t *const part = reinterpret_cast<uint64_t *>(hist);   // [kThreads]
+        bool found = true;
+        // threads of an element of a small list; of others a thread has kChunk
+        const int split = n <= 128 ? 4 : n <= kSmallList ? 2 : 0;
+        uint64_t before = 0, list_total = 0, own_kept = 0;   // kept weights: before this thread's, all, its own
+        if (n <= kSmallList) {
+          // threads e * split .. for element e: its rank and the weight of what lies above it by looking at all
+          ulonglong2 *const both = reinterpret_cast<ulonglong2 *>(hist);
+          const int e = tid / split, part_of = tid % split;
+          const bool here = e < n;
+          const uint64_t mine_c = here ? list[e] : 0;
+          if (tid < n) both[tid] = make_ulonglong2(list[tid], among(list[tid]) ? list_weight(tid) : 0);
+          __syncthreads();
+          const uint64_t mine_w = here ? both[e].y : 0;
+          uint64_t higher = 0;
+          uint32_t higher_n = 0;
+          if (__any_sync(0xffffffffu, here)) {
+#pragma unroll 4
+            for (int j = part_of; j < n; j += split) {
+              const ulonglong2 o = both[j];
+              const bool above = o.x > mine_c;
+              higher_n += above;
+              higher += above ? o.y : 0;
+            }
+            for (int o = 1; o < split; o <<= 1) {
+              higher_n += __shfl_xor_sync(0xffffffffu, higher_n, o);
+              higher += __shfl_xor_sync(0xffffffffu, higher, o);
+            }
+          }
+          bool keep = here && part_of == 0 && among(mine_c);
+          if (!mass) keep = keep && over + higher_n < want;
+          if (mass || (kTopP && from_top && top_p < 1.0f)) {
+            const uint64_t some = warp_total(keep ? mine_w : 0);
+            if (lane == 0) s.warp_sum[warp] = some;
+            __syncthreads();
+            const uint64_t all = warps_total(s.warp_sum);
+            __syncthreads();
+            if (mass) found = over < want && want <= over + all;
+            keep = keep && (mass ? over + higher < want : higher < ceil_product(top_p, all));
+          }
+          // kept weights by place, behind `both`
+          static_assert(kSmallList * (sizeof(ulonglong2) + sizeof(uint64_t)) <= kYBins * sizeof(uint32_t), "beside the list");
+          uint64_t *const kept = reinterpret_cast<uint64_t *>(both + kSmallList);
+          if (here && part_of == 0) kept[e] = keep && mine_w >= local.least ? mine_w : 0;
+          const int kept_n = __syncthreads_count(keep);
+          if (keep && higher_n == static_cast<uint32_t>(kept_n) - 1) s.composite = mine_c;
+          __syncthreads();
+          threshold = s.composite;
+          if (warp == 0) {   // the rest is one warp's, which waits for nobody: up to eight a lane
+            const int each = (n + 31) / 32, first = min(lane * each, n), last = min(first + each, n);
+            for (int i = first; i < last; ++i) own_kept += kept[i];
+            before = own_kept;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const uint64_t up = __shfl_up_sync(0xffffffffu, before, o);
+              if (lane >= o) before += up;
+            }
+            list_total = __shfl_sync(0xffffffffu, before, 31);
+            before -= own_kept;
+            if (from_top) {
+              const uint64_t at = __umul64hi(f_u, list_total);
+              if (at >= before && at < before + own_kept) {
+                int i = first;
+                for (; at >= before + kept[i]; ++i) before += kept[i];
+                finish_listed(list[i], list_total);
+              }
+            } else {   // sums before each
+              for (int i = first; i < last; ++i) {
+                const uint64_t w = kept[i];
+                kept[i] = before;
+                before += w;
+              }
+              __syncwarp();
+              if (lane <= ctas) {
+                const int i = list_at[lane * kWarps];
+                cta_at[lane] = i < n ? kept[i] : list_total;
+              }
+            }
           }
         } else {
-          // the leading bits of the weights may have missed the bin
-          found = over < want && want <= over + list_mass(low);
-          if (found) threshold = descend_list(true, list, n, low, want - over, r, table, hist, s);
-        }
-        if (found && (mass || from_top)) {
-#pragma unroll 1
-          for (int i = tid * kChunk; i < min((tid + 1) * kChunk, n); ++i) own_kept += kept_weight(i);
-          const Sums kept_sums = exclusive_sum(own_kept, s.warp_sum);
-          before = kept_sums.before;
-          list_total = kept_sums.all;
-          part[tid] = before;
-        }
-      }
-      if (from_top) {
-        const uint64_t at = __umul64hi(f_u, list_total);
-        if (n > kSmallList && at >= before && at < before + own_kept) {
-          int i = tid * kChunk;
-          for (uint64_t v; at >= before + (v = kept_weight(i)); ++i) before += v;
-          finish_listed(list[i], list_total);
-        }
-        cluster.barrier_wait();
-        return;
-      }
-      verdict.threshold = threshold;
-      if (mass && found && n > kSmallList) {
-        // up to each CTA's part: the list's kept weights before it
-        __syncthreads();
-        if (tid <= ctas) {
-          const int i = list_at[tid * kWarps], t = i / kChunk;   // the thread that has it
-          uint64_t at = t < kThreads ? part[t] : list_total;
-#pragma unroll 1
-          for (int j = t * kChunk; j < i; ++j) at += kept_weight(j);
-          cta_at[tid] = at;
-        }
-      }
-      if (mass && found && warp == 0) {
-        __syncwarp();
-        // the CTA in which the sums pass u Z
-        const int c = lane & (kCtas - 1);
-        const uint64_t here = c < ctas ? mine.told[c].kept + cta_at[c + 1] - cta_at[c] : 0;
-        uint64_t upto = here;
-#pragma unroll
-        for (int o = 1; o < kCtas; o <<= 1) {
-          const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o, kCtas);
-          if (c >= o) upto += up;
-        }
-        verdict.total = __shfl_sync(0xffffffffu, upto, kCtas - 1);
-        const uint64_t at = __umul64hi(f_u, verdict.total);
-        verdict.owner = __ffs(__ballot_sync(0xffffffffu, at < upto)) - 1;
-        verdict.at = at - __shfl_sync(0xffffffffu, upto - here, verdict.owner);
-      } else if (!mass) {
-        verdict.owner = 0;
-      }
-      if (warp == 0 && lane < ctas) cluster.map_shared_rank(&mine, lane)->verdict = verdict;
-    } else if (listed && from_top) {
-      cluster.sync();
-      return;
-    }
-    if (listed) {
-      // While the first CTA searches, the others sum what lies above the border in each of their
-      // warps, for the one in which the token will be.
-      const bool early = mass && rank != 0;
-      cluster.barrier_arrive();
-      if (early && local.least == 1) {
-        const uint64_t above = sum_above(border, fine);
-        if (lane == 0) warp_kept[warp] = above;
-      }
-      cluster.barrier_wait();
-      verdict = mine.verdict;
-      threshold = verdict.threshold;
-      listed = verdict.owner >= 0;
-      if (mass && listed) {
-        if (rank == verdict.owner) {
-          // this CTA's kept weights exactly (the histogram's may differ in the last units)
-          uint64_t kept = 0;
-          if (early) {
-            for (int i = lane; i < candidates; i += 32) {
-              const float x = Q::one(mine.logit[warp][i]);
-              if (composite(x, begin + mine.place[warp][i]) < threshold) continue;
-              const uint64_t w = weight(x, r, table);
-              if (w >= local.least) kept += w;
+          const auto list_mass = [&](uint64_t from) {
+            uint64_t v = 0;
+            for (int i = tid; i < n; i += kThreads) v += list[i] >= from ? list_weight(i) : 0;
+            const uint64_t all = exclusive_sum(v, s.warp_sum).all;
+            __syncthreads();
+            return all;
+          };
+          if (!mass) {
+            threshold = descend_list(false, list, n, 0, want - over, r, table, hist, s);
+            if (from_top && top_p < 1.0f) {
+              const uint64_t z = list_mass(threshold);
+              threshold = descend_list(true, list, n, threshold, ceil_product(top_p, z), r, table, hist, s);
             }
-            kept = warp_total(kept) + warp_kept[warp];
-            __syncwarp();
           } else {
-            kept = kept_sums(threshold);
+            // the leading bits of the weights may have missed the bin
+            found = over < want && want <= over + list_mass(low);
+            if (found) threshold = descend_list(true, list, n, low, want - over, r, table, hist, s);
           }
-          if (lane == 0) warp_kept[warp] = kept;
-          __syncthreads();
-          uint64_t exact = 0;
-          for (int v = 0; v < kWarps; ++v) exact += warp_kept[v];
-          pick<T>(a, row, data, rank, warp_kept, 0, min(verdict.at, exact - 1), threshold, verdict.total, r, table, tile_sum);
+          if (found && (mass || from_top)) {
+#pragma unroll 1
+            for (int i = tid * kChunk; i < min((tid + 1) * kChunk, n); ++i) own_kept += kept_weight(i);
+            const Sums kept_sums = exclusive_sum(own_kept, s.warp_sum);
+            before = kept_sums.before;
+            list_total = kept_sums.all;
+            part[tid] = before;
+          }
         }
+        if (from_top) {
+          const uint64_t at = __umul64hi(f_u, list_total);
+          if (n > kSmallList && at >= before && at < before + own_kept) {
+            int i = tid * kChunk;
+            for (uint64_t v; at >= before + (v = kept_weight(i)); ++i) before += v;
+            finish_listed(list[i], list_total);
+          }
+          cluster.barrier_wait();
+          return;
+        }
+        verdict.threshold = threshold;
+        if (mass && found && n > kSmallList) {
+          // up to each CTA's part: the list's kept weights before it
+          __syncthreads();
+          if (tid <= ctas) {
+            const int i = list_at[tid * kWarps], t = i / kChunk;   // the thread that has it
+            uint64_t at = t < kThreads ? part[t] : list_total;
+#pragma unroll 1
+            for (int j = t * kChunk; j < i; ++j) at += kept_weight(j);
+            cta_at[tid] = at;
+          }
+        }
+        if (mass && found && warp == 0) {
+          __syncwarp();
+          // the CTA in which the sums pass u Z
+          const int c = lane & (kCtas - 1);
+          const uint64_t here = c < ctas ? mine.told[c].kept + cta_at[c + 1] - cta_at[c] : 0;
+          uint64_t upto = here;
+#pragma unroll
+          for (int o = 1; o < kCtas; o <<= 1) {
+            const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o, kCtas);
+            if (c >= o) upto += up;
+          }
+          verdict.total = __shfl_sync(0xffffffffu, upto, kCtas - 1);
+          const uint64_t at = __umul64hi(f_u, verdict.total);
+          verdict.owner = __ffs(__ballot_sync(0xffffffffu, at < upto)) - 1;
+          verdict.at = at - __shfl_sync(0xffffffffu, upto - here, verdict.owner);
+        } else if (!mass) {
+          verdict.owner = 0;
+        }
+        if (warp == 0 && lane < ctas) cluster.map_shared_rank(&mine, lane)->verdict = verdict;
+      } else if (listed && from_top) {
+        cluster.sync();
         return;
       }
+      if (listed) {
+        cluster.sync();
+        verdict = mine.verdict;
+        threshold = verdict.threshold;
+        listed = verdict.owner >= 0;
+        if (mass && listed) {
+          if (rank == verdict.owner) {
+            // its warps' kept weights: what lies above the border, and of the candidates
+            uint64_t kept = 0;
+            if (by_warp) {
+              for (int i = lane; i < candidates; i += 32) {
+                const float x = Q::one(mine.logit[warp][i]);
+                if (composite(x, begin + mine.place[warp][i]) < threshold) continue;
+                const uint64_t w = weight(x, r, table);
+                if (w >= local.least) kept += w;
+              }
+              kept = warp_total(kept) + warp_kept[warp];
+              __syncwarp();
+            } else {
+              kept = kept_sums(threshold);
+            }
+            if (lane == 0) warp_kept[warp] = kept;
+            __syncthreads();
+            pick<T>(a, row, data, rank, warp_kept, 0, verdict.at, threshold, verdict.total, r, table, tile_sum);
+          }
+          return;
+        }
+      } else if (mass && (empty || over >= want)) {
+        cluster.sync();   // nobody reads these counts any more
+      } else {
+        break;
+      }
+      if (listed || !mass || misses == 2) break;
+      border += over >= want ? -1 : 1;
+      if (border < 0 || border >= kYBins) break;
     }
     if (!listed) {
       // long lists: a descent over the row
@@ -1270,7 +1259,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       threshold = prefix;
     }
     cluster.sync();   // nobody reads what is written next
-    clear_hist(hist, 2 * kYBins);
+    clear_hist(hist, kYBins);
     __syncthreads();
   }
 

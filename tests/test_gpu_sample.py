@@ -237,6 +237,29 @@ def test_rows_do_not_depend_on_their_batch(lib, dtype, V):
             t, lp = run(lib, x[a:a + 3], u[a:a + 3], **{n: v[a:a + 3] for n, v in args.items()})
             assert (t == token[a:a + 3]).all() and (lp == logprob[a:a + 3]).all()
         check(lib, x[:60], u[:60], **{n: v[:60] for n, v in args.items()})
+    parts = [run(lib, x[a:a + 14], u[a:a + 14], top_p=kw["top_p"][a:a + 14]) for a in range(0, R, 14)]
+    token, logprob = run(lib, x, u, top_p=kw["top_p"])
+    assert (np.concatenate([t for t, _ in parts]) == token).all() and (np.concatenate([lp for _, lp in parts]) == logprob).all()
+
+
+@pytest.mark.parametrize("V,sigma", [(20000, 1.5), (150000, 3.0), (1500, 4.0)])
+def test_borders_at_the_edges_of_bins(lib, V, sigma):
+    """p Z within an fp32 rounding of p of the mass above a 1/32 octave's edge, where the leading bits of
+    the weights may point at the bin's neighbour."""
+    rng = np.random.default_rng(V)
+    row = (rng.standard_normal(V) * sigma).astype(np.float32)
+    x = np.sort(row.astype(np.float64))[::-1]
+    w = np.exp(x - x[0])
+    below = np.ceil(x[0] * np.log2(np.e)) * 64 - np.rint(64 * x * np.log2(np.e))
+    cum = np.cumsum(w) / w.sum()
+    edges = np.flatnonzero(np.diff((below.astype(int) + 63) >> 1))
+    edges = edges[(cum[edges] > 0.01) & (cum[edges] < 0.995)]
+    p = cum[edges][rng.permutation(edges.size)[:120]].astype(np.float32)
+    p = np.concatenate([p, np.nextafter(p, np.float32(0)), np.nextafter(p, np.float32(1))])
+    many = torch.from_numpy(row).cuda().expand(p.size, V).contiguous()
+    check(lib, many, rng.random(p.size), top_p=p)
+    few = slice(0, p.size, 7)
+    check(lib, many[few].contiguous(), rng.random(p[few].size), top_p=p[few], min_p=np.full(p[few].size, 1e-3))
 
 
 def test_streams_graphs_and_equal_calls(lib):
