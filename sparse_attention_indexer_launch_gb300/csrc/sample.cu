@@ -27,7 +27,7 @@
 // What bounds it: reading those rows would take 22.9 us at the measured copy bandwidth.  Their
 // weights to 2^-38 are some 30 instructions a logit, 27 us if every slot were used.  The rest is the
 // chain of a row's steps, 25 to 30 us with two rows to an SM, in which warps wait for the slowest
-// one of the cluster (issue slots half busy, a quarter of the stalls at barriers).  A single row is that
+// one of the cluster (issue slots 44% busy, a third of the stalls at barriers).  A single row is that
 // chain alone: with top-p of 151,552 logits some 40,000 cycles, of which reading and the largest
 // logit are 6,500, weights and histogram 11,500, border, candidates and what lies above 11,000, the
 // list 7,000 and the token among the kept ones 4,500.  (Sums above from a histogram of two words to a
