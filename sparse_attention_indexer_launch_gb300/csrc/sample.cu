@@ -16,11 +16,11 @@
 //
 // Thresholds: the kept tokens are a prefix of the order (logit descending, index ascending),
 // so one number is enough, the composite (key, ~index) of the last kept one.  A first pass
-// sorts the weights' exponents into bins of 1 / 32 octave, counts for top-k and leading bits
+// sorts the weights' exponents into bins of 1 / 64 octave, counts for top-k and leading bits
 // of the weights for top-p; the elements of the bin that holds the border (for top-k those
 // above as well, where they are few) go into a list that the first CTA gathers and searches, and
 // what lies above it is summed exactly.  (Leading bits can point at the neighbour of a bin whose edge
-// is next to the border; the exact sum tells, and the neighbour is taken.)  A bin with too many is cut into 256 finer ones first; where even those hold too many (equal
+// is next to the border; the exact sum tells, and the neighbour is taken.)  A bin with too many is cut into 128 finer ones first; where even those hold too many (equal
 // logits), a radix descent runs over the whole row.  (Descents over the whole row for every
 // border took 953 us for 256 rows of 151,552 fp32 logits with mixed filters; this 222.)
 //
@@ -53,11 +53,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRanges = kCtas * kWarps;   // warps' parts of the row
 constexpr int kTile = 128;       // a warp's step: four elements a lane
 constexpr uint32_t kKeyMasked = 0x007FFFFFu;   // radix_key(-inf)
-constexpr int kFine = 256;       // parts of such a bin
+constexpr int kFine = 128;       // parts of a bin of exponents
 constexpr int kOctaves = 44;     // below 2^-44 of the largest's octave: no weight
 constexpr int kCut = kOctaves * 64;
 constexpr int kOctaveBins = 48;  // octaves, with room
-constexpr int kYBins = kOctaveBins * 32;   // (d + 63) / 2 for d < kCut, 32 to an octave
+constexpr int kYBins = kOctaveBins * 64;   // d + 63 for d < kCut, 64 to an octave
 constexpr int kDigit = 9;        // bits of a descent's level
 constexpr int kBins = 1 << kDigit;
 constexpr int kSmallList = 256;  // searched by two or four threads per element
@@ -120,14 +120,14 @@ __device__ __forceinline__ void steps(uint64_t t, const Row &r, uint32_t (&d)[2]
 
 // A bin of exponents for d 64ths, kFar for what has no weight.
 constexpr int32_t kFar = 1 << 20;
-__device__ __forceinline__ int32_t exponent_bin(uint32_t d) { return d < kCut ? static_cast<int32_t>((d + 63) >> 1) : kFar; }
+__device__ __forceinline__ int32_t exponent_bin(uint32_t d) { return d < kCut ? static_cast<int32_t>(d + 63) : kFar; }
 // The part of its bin that element i of a pair lies in, behind the bin: smaller above.
 __device__ __forceinline__ int32_t fine_code(uint64_t minus, uint64_t t, uint32_t d, int i) {
   if (d >= kCut) return kFar * kFine;
   const float v = __uint_as_float(static_cast<uint32_t>(minus >> (32 * i))), c = __uint_as_float(static_cast<uint32_t>(t >> (32 * i)));
   const float f = (kMagic - c) - v;   // exact, within 2^-7: 128 parts of a 64th
-  const int32_t part = min(max(static_cast<int32_t>((f + 0x1p-7f) * 0x1p13f), 0), kFine / 2 - 1);
-  return static_cast<int32_t>(d + 63) * (kFine / 2) + (kFine / 2 - 1 - part);
+  const int32_t part = min(max(static_cast<int32_t>((f + 0x1p-7f) * 0x1p13f), 0), kFine - 1);
+  return static_cast<int32_t>(d + 63) * kFine + (kFine - 1 - part);
 }
 
 // Weights of two logits: 2^p is a power of two, a table entry of 6 bits and exp(g) - 1 of
@@ -244,7 +244,7 @@ struct Found {
 // What a CTA uses alone.
 struct Scratch {
   uint64_t warp_sum[kWarps];
-  float bin[32];
+  float bin[64];
   Found found;
   uint64_t composite;
 };
@@ -408,7 +408,7 @@ __device__ __noinline__ void push_octaves(const uint32_t *hist, float (*octave)[
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = warp; o < kOctaveBins; o += kWarps) {
-    const float v = static_cast<float>(__reduce_add_sync(0xffffffffu, hist[o * 32 + lane]));
+    const float v = static_cast<float>(__reduce_add_sync(0xffffffffu, hist[o * 64 + lane] + hist[o * 64 + 32 + lane]));
     const cg::cluster_group cluster = cg::this_cluster();
     if (lane < cluster.num_blocks()) cluster.map_shared_rank(octave, lane)[cluster.block_rank()][o] = v;
   }
@@ -465,18 +465,15 @@ __device__ __noinline__ Exponent find_exponent(bool mass, const uint32_t *hist, 
     o = 32 + far.at;
     before = r.all + far.before;
   }
-  if (tid < 32 * kCtas) {
-    const int c = tid & (kCtas - 1), b = tid / kCtas;
-    float v = 0.0f;
-    if (c < ctas) {
-      v = static_cast<float>(cg::this_cluster().map_shared_rank(hist, c)[o * 32 + b]);
-    }
+  static_assert(64 * kCtas == kThreads, "a bin of a CTA a thread");
+  const int c = tid & (kCtas - 1), b = tid / kCtas;
+  float v = c < ctas ? static_cast<float>(cg::this_cluster().map_shared_rank(hist, c)[o * 64 + b]) : 0.0f;
 #pragma unroll
-    for (int k = kCtas / 2; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-    if (c == 0) sum[b] = scaled(v, o);
-  }
+  for (int k = kCtas / 2; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+  if (c == 0) sum[b] = scaled(v, o);
   __syncthreads();
-  e.bin = o * 32 + reach_in_warp(sum[lane], want - before).at;
+  const Reached first = reach_in_warp(sum[lane], want - before), second = reach_in_warp(sum[lane + 32], want - before - first.all);
+  e.bin = o * 64 + (first.all < want - before && second.all != 0.0f ? 32 + second.at : first.at);
   return e;
 }
 
@@ -524,11 +521,12 @@ __device__ __noinline__ uint64_t descend_list(bool mass, const uint64_t *list, i
   return prefix;
 }
 
-// The histogram, the list, the row; without filters the row alone.
-constexpr size_t kListOffset = kYBins * sizeof(uint32_t);
+// The histogram, in its second half the list, the row; without filters the row alone.
+constexpr size_t kListOffset = 3 * kBins * sizeof(uint32_t);
 template <typename T, bool kList>
 __host__ __device__ constexpr size_t fixed_smem() {
-  return kList ? kListOffset + Quad<T>::kListMost * sizeof(uint64_t) : 0;
+  constexpr size_t list = kListOffset + Quad<T>::kListMost * sizeof(uint64_t), hist = kYBins * sizeof(uint32_t);
+  return !kList ? 0 : list > hist ? list : hist;
 }
 
 // kTopK, kTopP: the rows may have these filters.
@@ -551,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   __shared__ uint64_t cta_at[kCtas + 1];
   __shared__ int32_t list_at[kRanges + 1];
   __shared__ uint64_t tile_sum[2 * kWarps];
-  static_assert(kYBins == 3 * kBins && kThreads * sizeof(uint64_t) <= 3 * kBins * sizeof(uint32_t) && kFine <= kBins, "what hist holds by turns");
+  static_assert(kYBins >= 3 * kBins && kThreads * sizeof(uint64_t) <= kListOffset && kFine <= kBins, "what hist holds by turns");
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
@@ -790,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   };
   // Those of the elements above a bin of exponents, or above part `fine` of it.
   const auto low_edge = [&](int32_t border) {   // less ref, a little lower
-    return (__uint_as_float(local.whole_bits - static_cast<uint32_t>(2 * border - 62)) - kMagic - 0x1.2p-7f) / local.c_hi;
+    return (__uint_as_float(local.whole_bits - static_cast<uint32_t>(border - 63)) - kMagic - 0x1.2p-7f) / local.c_hi;
   };
   const auto sum_above = [&](int32_t border, int32_t fine, uint64_t &all, uint64_t &kept) {   // and what min-p keeps of them
     const float least_x = low_edge(border);
@@ -833,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           for (int i = 0; i < 2; ++i) {
             if (v.d[i] < kCut && (!kTopK || low == 0 || among(composite(x[2 * h + i], begin + t + 4 * lane + 2 * h + i)))) {
               sum += v.w[i];
-              atomicAdd(&hist[(v.d[i] + 63) >> 1], static_cast<uint32_t>(v.m[i] >> 32) >> (31 - lead) | 1u);
+              atomicAdd(&hist[v.d[i] + 63], static_cast<uint32_t>(v.m[i] >> 32) >> (31 - lead) | 1u);
             }
           }
         }
@@ -850,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           steps(to_64ths(minus), local, d);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (d[i] < kCut) atomicAdd(&hist[(d[i] + 63) >> 1], 1u);
+            if (d[i] < kCut) atomicAdd(&hist[d[i] + 63], 1u);
         }
       });
     }
@@ -902,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const int32_t at_border = round == 0 ? border : border * kFine + fine;
         n = 0;
         // the border's bin as a range of logits less ref, a little wide: most steps of a warp hold none of it
-        const float p_high = __uint_as_float(r.whole_bits - static_cast<uint32_t>(max(2 * border - 63, 0))) - kMagic + 0x1.2p-7f;
+        const float p_high = __uint_as_float(r.whole_bits - static_cast<uint32_t>(max(border - 63, 0))) - kMagic + 0x1.2p-7f;
         const float x_low = low_edge(border), x_high = from_top ? INFINITY : p_high / r.c_hi;
         each_tile([&](int t, const float (&x)[4]) {
           bool near = false;
@@ -1085,7 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             keep = keep && (mass ? over + higher < want : higher < ceil_product(top_p, all));
           }
           // kept weights by place, behind `both`
-          static_assert(kSmallList * (sizeof(ulonglong2) + sizeof(uint64_t)) <= kYBins * sizeof(uint32_t), "beside the list");
+          static_assert(kSmallList * (sizeof(ulonglong2) + sizeof(uint64_t)) <= kListOffset, "beside the list");
           uint64_t *const kept = reinterpret_cast<uint64_t *>(both + kSmallList);
           if (here && part_of == 0) kept[e] = keep && mine_w >= local.least ? mine_w : 0;
           const int kept_n = __syncthreads_count(keep);
