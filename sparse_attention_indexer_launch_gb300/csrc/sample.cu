@@ -244,7 +244,7 @@ struct Found {
 // What a CTA uses alone.
 struct Scratch {
   uint64_t warp_sum[kWarps];
-  float bin[64];
+  alignas(8) float bin[64];
   Found found;
   uint64_t composite;
 };
@@ -472,8 +472,10 @@ __device__ __noinline__ Exponent find_exponent(bool mass, const uint32_t *hist, 
   for (int k = kCtas / 2; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
   if (c == 0) sum[b] = scaled(v, o);
   __syncthreads();
-  const Reached first = reach_in_warp(sum[lane], want - before), second = reach_in_warp(sum[lane + 32], want - before - first.all);
-  e.bin = o * 64 + (first.all < want - before && second.all != 0.0f ? 32 + second.at : first.at);
+  const float2 two = reinterpret_cast<const float2 *>(sum)[lane];   // two neighbours a lane
+  const Reached pair = reach_in_warp(two.x + two.y, want - before);
+  const float x = __shfl_sync(0xffffffffu, two.x, pair.at), y = __shfl_sync(0xffffffffu, two.y, pair.at);
+  e.bin = o * 64 + 2 * pair.at + (pair.before + x < want - before && y != 0.0f ? 1 : 0);
   return e;
 }
 
