@@ -22,16 +22,16 @@
 // what lies above it is summed exactly.  (Leading bits can point at the neighbour of a bin whose edge
 // is next to the border; the exact sum tells, and the neighbour is taken.)  A bin with too many is cut into 128 finer ones first; where even those hold too many (equal
 // logits), a radix descent runs over the whole row.  (Descents over the whole row for every
-// border took 953 us for 256 rows of 151,552 fp32 logits with mixed filters; this 222.)
+// border took 953 us for 256 rows of 151,552 fp32 logits with mixed filters; this 194.)
 //
 // What bounds it: reading those rows would take 22.9 us at the measured copy bandwidth.  Their
 // weights to 2^-38 are some 30 instructions a logit, 27 us if every slot were used.  The rest is the
 // chain of a row's steps, 25 to 30 us with two rows to an SM, in which warps wait for the slowest
 // one of the cluster (issue slots 44% busy, a third of the stalls at barriers).  A single row is that
 // chain alone: with top-p of 151,552 logits some 40,000 cycles, of which reading and the largest
-// logit are 6,500, weights and histogram 11,500, border, candidates and what lies above 11,000, the
-// list 7,000 and the token among the kept ones 4,500.  (Sums above from a histogram of two words to a
-// bin, off by 2^-30, took 208 us instead of 222: but a row's last bits then depend on its CTAs.)
+// logit are 6,400, weights and histogram 12,000, border, candidates and what lies above 10,800, the
+// list 6,200 and the token among the kept ones 4,400.  (Sums above from a histogram of two words to a
+// bin of 1 / 32 octave, off by 2^-33, took 208 us, and a row's last bits depended on its CTAs.)
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -438,8 +438,8 @@ __device__ __forceinline__ Reached reach_in_warp(float v, float want) {
 
 // The bin of exponents, from the largest, at which the running sum over all CTAs reaches
 // `want`, and the sum of all: first the octave, then its bin, so that a thread reads one bin
-// of another CTA.  In fp32: counts below 2^24 are exact; masses (low != 0) may miss a border
-// that lies within 2^-23 of an end of its bin, which the exact sums behind it find out.
+// of another CTA.  In fp32: counts below 2^24 are exact; masses may miss a border next to an end
+// of its bin, which the exact sums behind it find out.
 struct Exponent {
   int32_t bin;
   float all;
