@@ -504,8 +504,8 @@ typedef enum {
 /* Logits of R rows and how a token of each is drawn.  Every parameter is a value per row. */
 typedef struct {
     const void *logits;        /* device fp32 or bf16 [R][ld], aligned to its elements; columns 0 .. V-1 are read */
-    const float *u;            /* device fp32 [R]: a random number in [0, 1) (below it or NaN: 0, above it: the last
-                                  number below 1) */
+    const float *u;            /* device fp32 [R]: a random number in [0, 1) (below it or NaN: 0, above it, 1 among
+                                  that: fp32's last number below 1, 1 - 2^-24) */
     const float *temperature;  /* device fp32 [R] or NULL (1): 0 or less, or NaN: the largest logit's token; else used
                                   within 2^-60 .. 2^60 */
     const int32_t *top_k;      /* device int32 [R] or NULL: 0 or less, or V or more: off */

@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                       });
     kept = all - (local.least > 1 ? warp_total(small) : 0);
   };
-  const uint64_t f_u = u > 0.0f ? (u < 1.0f ? static_cast<uint64_t>(u * 0x1p64f) : ~0ull) : 0ull;
+  const uint64_t f_u = u > 0.0f ? static_cast<uint64_t>(fminf(u, 0x1.fffffep-1f) * 0x1p64f) : 0ull;   // (NaN: 0)
   uint64_t threshold = 0;   // composite of the last kept element
 
   // top-k's border, then top-p's among what top-k keeps
