@@ -216,7 +216,8 @@ __device__ __noinline__ Rescued rescue(uint4 raw) {
     r.x.a[h] = mul2(r.x.a[h], both(0x1p-80f));
     r.x.b[h] = mul2(r.x.b[h], both(0x1p-80f));
   }
-  r.inv = rsqrtf(spread<D, kMean>(r.x));
+  const float v = spread<D, kMean>(r.x);
+  r.inv = v == 0.0f ? 0.0f : rsqrtf(v);   // equal elements whose sum passes the range: they deviate by 0
   return r;
 }
 
