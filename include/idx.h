@@ -484,7 +484,8 @@ typedef struct {
  *     z_a = y_a cos angle_i - y_b sin angle_i,   z_b = y_b cos angle_i + y_a sin angle_i.
  * All of it in fp32, rounded once: q to q_out; k to k_out (bf16) where given, and to the
  * cache where given, at its rows' slots: bf16, or E4M3 with scale = amax / 448 of the fp32
- * values (1 where they are all zero), saturating; v to the cache exactly as idx_write_kv.
+ * values (1 where they are all zero, else 2^-149 at least), saturating; v to the cache exactly
+ * as idx_write_kv.
  * NaN and infinity in a normed or quantised head act as idx_write_kv and the formulas say;
  * a head whose squares pass fp32's range is normed all the same.  A slot outside
  * [0, P * 64) writes nothing to the cache; slots >= 0 must differ.

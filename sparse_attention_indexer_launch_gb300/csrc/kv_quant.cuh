@@ -84,7 +84,7 @@ __device__ __forceinline__ float quantize_f32(const float (&x)[8], float amax, u
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = e4m3x2(fmaf(x[2 * i], r, x[2 * i] * e), fmaf(x[2 * i + 1], r, x[2 * i + 1] * e));
   } else {
-    sc = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    sc = amax > 0.0f ? fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-149f) : 1.0f;   // 0 would leave 0 / 0
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = e4m3x2(__fdiv_rn(x[2 * i], sc), __fdiv_rn(x[2 * i + 1], sc));
   }
