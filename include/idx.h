@@ -479,8 +479,9 @@ typedef struct {
 } idx_norm_rope_args;
 
 /* Norm of every head of q and k, then its rotation: with y the normed head and
- * angle_i = pos[axis[i]][r] * inv_freq[i] in real numbers, for any position (off by 2^-24 of
- * itself or 2^-32 of a turn while |inv_freq| <= 1), for the pair (a, b) of frequency i
+ * angle_i = pos[axis[i]][r] * inv_freq[i] in real numbers, for any position (off by 2^-32 of a
+ * turn at most while |inv_freq| <= 1, and by an fp32 rounding of what is left of it beside the
+ * nearest quarter turn), for the pair (a, b) of frequency i
  *     z_a = y_a cos angle_i - y_b sin angle_i,   z_b = y_b cos angle_i + y_a sin angle_i.
  * All of it in fp32, rounded once: q to q_out; k to k_out (bf16) where given, and to the
  * cache where given, at its rows' slots: bf16, or E4M3 with scale = amax / 448 of the fp32

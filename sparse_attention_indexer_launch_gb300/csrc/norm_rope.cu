@@ -34,7 +34,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kVectors = 4;     // heads of a lane in a batch
 
 // inv_freq / (2 pi) in units of 2^-64 turn, modulo one turn: the 24-bit significand times
-// 2^64 / (2 pi), shifted by the exponent.
+// 2^64 / (2 pi), shifted by the exponent and rounded.  Off by half a unit and, as the constant is
+// off by 0.497, by 0.497 |inv_freq|.
 __device__ __forceinline__ uint64_t turns_per_position(float inv_freq) {
   constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull;   // 2^64 / (2 pi)
   const uint32_t u = __float_as_uint(inv_freq);
@@ -44,16 +45,17 @@ __device__ __forceinline__ uint64_t turns_per_position(float inv_freq) {
   const int down = 150 - static_cast<int>(ex ? ex : 1u);   // the value is m * 2^-down
   uint64_t f;
   if (down <= 0) f = -down < 64 ? lo << -down : 0ull;
-  else if (down < 64) f = lo >> down | hi << (64 - down);
-  else f = down < 128 ? hi >> (down - 64) : 0ull;
+  else if (down < 64) f = (lo >> down | hi << (64 - down)) + (lo >> (down - 1) & 1u);
+  else if (down == 64) f = hi + (lo >> 63);
+  else f = down < 128 ? ((hi >> (down - 65)) + 1u) >> 1 : 0ull;   // hi has 22 bits
   return u >> 31 ? 0ull - f : f;
 }
 
 __device__ __forceinline__ float2 cos_sin(int32_t pos, float inv_freq) {
   const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns_per_position(inv_freq);
-  // the nearest quarter turn, and what is left of it, within an eighth: 32 of the 64 bits,
-  // rounded to fp32 at that smaller size
-  const uint32_t turn = static_cast<uint32_t>(phase >> 32), quarter = (turn + 0x20000000u) >> 30;
+  // the nearest quarter turn, and what is left of it, within an eighth: 32 of the 64 bits, rounded
+  // (for 2^31 positions and |inv_freq| <= 1 off by 2^-32 of a turn in all), then fp32 at that smaller size
+  const uint32_t turn = static_cast<uint32_t>((phase + 0x80000000ull) >> 32), quarter = (turn + 0x20000000u) >> 30;
   float s, c;
   sincospif(static_cast<float>(static_cast<int32_t>(turn - (quarter << 30))) * 0x1p-31f, &s, &c);
   if (quarter & 1u) {

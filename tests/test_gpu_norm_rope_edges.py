@@ -39,3 +39,44 @@ def test_scales_below_the_smallest_number(lib):
     z, _ = c.exact(c.k, 1, c.kw, None)
     got = c.K.view(torch.float8_e4m3fn)[page, off].double().cpu().numpy() * 2.0 ** -149
     assert (got[:, :, ::2] == 0).all() and (np.abs(got - z) <= 2.0 ** -149 + 2.0 ** -4 * np.abs(z)).all() and np.abs(got).max() > 0
+
+
+# 2^256 / (2 pi), and inverse frequencies (bits) with positions that come within 2 units of 2^-32 turn
+# of a quarter turn: the small one of cosine and sine shows the angle's own error.
+INV_2PI = 0x28be60db9391054a7f09d5f47d4d377036d8a5664f10e4107f9458eaf7aef158
+NEAR_QUARTERS = [
+    (0x3f4347d4, 2122934198), (0x3f21d5e2, 2040872170), (0x3f7b7378, 2076569594), (0x3f5b0e24, 2045508788),
+    (0x3f41b950, 2039619361), (0x3f2e3b52, 2096071377), (0x3f71b182, 2131501801), (0x3f14470a, 2081693231),
+    (0x3f013e3b, 2092000254), (0x3f6dd34c, 2056101290), (0x3f5c0c2e, 2145003625), (0x3f7fe5c3, 2131542241),
+    (0x3f6e9700, 2117353440), (0x3f4f42f5, 2057640967), (0x3f59a57d, 2064191376), (0x3f765a8f, 2083182781),
+    (0x3f696ed8, 2038087938), (0x3f5c7fde, 2135341770), (0x3f599147, 2022093181), (0x3f702ca0, 2052251297),
+    (0x3f0f168a, 2116037525), (0x3f43a4bf, 2025415655), (0x3f4d1865, 2090526301), (0x3f5c0c2e, 2034278808),
+]
+
+
+def test_angles_to_a_2_32nd_of_a_turn(lib):
+    """Heads of ones and zeros give cosines and sines themselves, rounded once to bf16."""
+    n, pairs = len(NEAR_QUARTERS), 32
+    bits = [b for b, _ in NEAR_QUARTERS] + [0x3F800000] * (pairs - n)
+    pos = [p for _, p in NEAR_QUARTERS] + [-p for _, p in NEAR_QUARTERS] + [2 ** 31 - 1, -2 ** 31]
+    for il in (False, True):
+        q = torch.zeros(len(pos), 1, 2 * pairs, dtype=torch.bfloat16, device="cuda")
+        a, b = (slice(0, None, 2), slice(1, None, 2)) if il else (slice(0, pairs), slice(pairs, None))
+        q[:, :, a] = 1
+        out = torch.empty_like(q)
+        inv = torch.from_numpy(np.array(bits, np.uint32).view(np.float32).copy()).cuda()
+        lib.idx_norm_rope(lib.make_norm_rope(q, q_out=out, pos=torch.tensor(pos, dtype=torch.int32, device="cuda"), inv_freq=inv,
+                                             interleaved=il, q_norm=lib.IDX_NORM_NONE))
+        got = out[:, 0].double().cpu().numpy()
+        want = np.zeros((len(pos), 2, pairs))
+        for i, u in enumerate(bits):
+            m, down = (u & 0x7FFFFF) | 0x800000, 150 - (u >> 23)        # the frequency is m 2^-down
+            unit = 1 << (256 + down)
+            for r, p in enumerate(pos):
+                turn = m * INV_2PI * p % unit
+                quarter = (4 * turn + unit // 2) // unit
+                rest = float((4 * turn - quarter * unit) / unit) * np.pi / 2
+                c, s = np.cos(rest), np.sin(rest)
+                want[r, :, i] = [(c, s), (-s, c), (-c, -s), (s, -c)][quarter % 4]
+        got = np.stack([got[:, a], got[:, b]], 1)
+        assert (np.abs(got - want) <= 2 * np.pi * 2.0 ** -32 + (2.0 ** -8 + 2.0 ** -22) * np.abs(want)).all()
