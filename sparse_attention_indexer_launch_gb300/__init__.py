@@ -248,11 +248,13 @@ def make_problem(q, w, k_cache, k_scale, page_table, row_req, row_bound, max_bou
     page_table [Q][stride] int32, row_req and row_bound [R] int32.  rows_hint: the
     most rows any request has (0: unknown)."""
     R = int(row_bound.shape[0])
-    return Problem(q=_ptr(q), w=_ptr(w), k_cache=_ptr(k_cache), k_scale=_ptr(k_scale),
-                   page_table=_ptr(page_table), row_req=_ptr(row_req), row_bound=_ptr(row_bound),
-                   R=R, Q=int(page_table.shape[0]), P=int(P if P is not None else k_cache.shape[0]),
-                   pt_stride=int(page_table.shape[1]), max_bound=int(max_bound), kv_dtype=int(kv_dtype),
-                   rows_hint=int(rows_hint))
+    p = Problem(q=_ptr(q), w=_ptr(w), k_cache=_ptr(k_cache), k_scale=_ptr(k_scale),
+                page_table=_ptr(page_table), row_req=_ptr(row_req), row_bound=_ptr(row_bound),
+                R=R, Q=int(page_table.shape[0]), P=int(P if P is not None else k_cache.shape[0]),
+                pt_stride=int(page_table.shape[1]), max_bound=int(max_bound), kv_dtype=int(kv_dtype),
+                rows_hint=int(rows_hint))
+    p.held = (q, w, k_cache, k_scale, page_table, row_req, row_bound)   # as long as the problem
+    return p
 
 
 def workspace_size(problem: Problem, K: int) -> int:
@@ -371,6 +373,8 @@ def make_tree_tables(ctx_len, new_len, page_table, free_pages, free_count, *, P:
                    row_pos=_ptr(row_pos), slot=_ptr(slot), mask=_ptr(mask), P=int(P), Q=Q,
                    pt_stride=int(page_table.shape[1]), cap=cap)
     t.device = device
+    t.held = (ctx_len, new_len, parent, free_pages, free_count, page_table, row_start, free_left, row_req, row_bound, row_pos, slot,
+              mask)   # as long as the plan
     return t
 
 
@@ -410,6 +414,7 @@ def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
                 token_stride=st[0][1], head_stride=st[0][2], Hkv=Hkv, D=D,
                 kv_dtype=IDX_KV_E4M3 if f8 else IDX_KV_BF16)
     c.device = device
+    c.held = (k, v, k_scale, v_scale)   # as long as the cache
     return c
 
 
@@ -455,6 +460,7 @@ def make_tree_problem(q, cache: KvCache, page_table, ctx_len, row_start, mask, m
                     R=R, Q=Q, pt_stride=int(page_table.shape[1]), max_ctx=int(max_ctx), max_new=int(max_new), Hq=Hq,
                     scale=float(scale))
     p.device = device
+    p.held = (q, cache, page_table, ctx_len, row_start, mask)   # as long as the plan
     return p
 
 
