@@ -80,3 +80,26 @@ def test_angles_to_a_2_32nd_of_a_turn(lib):
                 want[r, :, i] = [(c, s), (-s, c), (-c, -s), (s, -c)][quarter % 4]
         got = np.stack([got[:, a], got[:, b]], 1)
         assert (np.abs(got - want) <= 2 * np.pi * 2.0 ** -32 + (2.0 ** -8 + 2.0 ** -22) * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "bf16 keys", "e4m3 keys"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("layout", ["token", "head"])
+def test_halves_into_the_cache(lib, kv, D, layout):
+    """Pairs by halves, heads that turn whole, in part and not at all, into every kind of cache."""
+    for R, Hq, Hkv, rot in ((1, 8, 1, D), (70, 5, 3, D // 2), (33, 2, 2, 16), (131, 0, 16, 0)):
+        c = Case(lib, R, Hq, Hkv, D, kv, 1, 2, rot, False, seed=R, layout=layout)
+        K0, V0 = c.K.clone(), None if c.V is None else c.V.clone()
+        ks0, vs0 = [None if s is None else s.clone() for s in (c.ks, c.vs)]
+        lib.idx_norm_rope(c.plan())
+        c.check()
+        page, off = c.slot.long() // PAGE, c.slot.long() % PAGE
+        if V0 is not None:
+            spare = [x.clone() if x is not None else None for x in (K0, V0, ks0, vs0)]
+            lib.idx_write_kv(lib.make_kv_cache(*spare), c.v, c.v, c.slot)
+            assert torch.equal(c.V, spare[1]) and (vs0 is None or torch.equal(c.vs, spare[3]))
+        K0[page, off] = c.K[page, off]          # nothing else is touched
+        assert torch.equal(K0, c.K)
+        if ks0 is not None:
+            ks0[page, :, off] = c.ks[page, :, off]
+            assert torch.equal(ks0, c.ks)
