@@ -22,16 +22,20 @@
 // what lies above it is summed exactly.  (Leading bits can point at the neighbour of a bin whose edge
 // is next to the border; the exact sum tells, and the neighbour is taken.)  A bin with too many is cut into 128 finer ones first; where even those hold too many (equal
 // logits), a radix descent runs over the whole row.  (Descents over the whole row for every
-// border took 953 us for 256 rows of 151,552 fp32 logits with mixed filters; this 194.)
+// border took 953 us for 256 rows of 151,552 fp32 logits of mixed width, most with top-p; this 194 to 212,
+// by the parameters that the rows draw.)
 //
 // What bounds it: reading those rows would take 22.9 us at the measured copy bandwidth.  Their
 // weights to 2^-38 are some 30 instructions a logit, 27 us if every slot were used.  The rest is the
 // chain of a row's steps, 25 to 30 us with two rows to an SM, in which warps wait for the slowest
-// one of the cluster (issue slots 44% busy, a third of the stalls at barriers).  A single row is that
-// chain alone: with top-p of 151,552 logits some 40,000 cycles, of which reading and the largest
-// logit are 6,400, weights and histogram 12,000, border, candidates and what lies above 10,800, the
-// list 6,200 and the token among the kept ones 4,400.  (Sums above from a histogram of two words to a
-// bin of 1 / 32 octave, off by 2^-33, took 208 us, and a row's last bits depended on its CTAs.)
+// one of the cluster (issue slots 44% busy, a third of the stalls at barriers).  A single row with
+// top-p of 151,552 logits takes some 40,000 cycles: reading and the largest logit 6,400, weights
+// and histogram 12,000, border, candidates and what lies above 10,800, the list 6,200 and the token
+// among the kept ones 4,400.  22,800 of them are passes over the 37 logits of a thread, not latency.
+// Without filters it takes 20,000: reading 6,000, weights 7,600, their sums over the cluster 1,200, the
+// token 5,100.  (Sums above from a histogram of two words to a bin of 1 / 32 octave, off by 2^-33, took
+// 203 to 225 us on the 256 rows' inputs, and a row's last bits depended on its CTAs; exact ones beside
+// that histogram 216 to 243.)
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
