@@ -10,7 +10,7 @@
 // memory.  Warps share nothing, so no barrier holds them up; two values ride in an instruction.
 //
 // What bounds it: memory.  16,209 rows of 64 + 2 x 8 heads of 128 into an E4M3 cache take 103 us,
-// 6.1 TB/s or 91% of the measured copy bandwidth; 8,855 rows of 16 + 2 x 16 heads turned by three axes,
+// 6.1 TB/s or 90% of the measured copy bandwidth; 8,855 rows of 16 + 2 x 16 heads turned by three axes,
 // bf16, 37.3 us, 86%; 40,000 rows reach 98 to 100%, so what is missing is start and end.  28 warps to
 // an SM with one head at a time: 24 with 80 registers took 115 us and 40.7, 32 with 64 spill (127; one
 // head at a time 103.5).  Groups of rows to a CTA, angles in shared memory behind a barrier, took 113
